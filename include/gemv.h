@@ -53,9 +53,11 @@ typedef enum {
     GEMV_ERR_LAUNCH = 4,        /* the CUDA launch failed */
     GEMV_ERR_TIMEOUT = 5,       /* a device-side wait gave up (see gemv_get_device_error) */
     GEMV_ERR_CUDA = 6,          /* another CUDA runtime call failed */
-    GEMV_ERR_TIMEOUT_UNDRAINED = 7 /* as GEMV_ERR_TIMEOUT, and the bounded wait for the block's own
+    GEMV_ERR_TIMEOUT_UNDRAINED = 7, /* as GEMV_ERR_TIMEOUT, and the bounded wait for the block's own
                                       copies still in flight gave up too (see
                                       gemv_get_device_error) */
+    GEMV_ERR_BAD_INDEX = 8 /* a page number, slot, length or axis read on the device lay outside
+                              its range (decode-step operators; see gemv_get_device_error) */
 } gemv_status_t;
 
 /* Storage types, used by the variant-introspection calls. */
@@ -369,6 +371,145 @@ gemv_status_t gemv_q8_rowscale_run_variant(int variant, const int8_t *A, const u
                                            void *stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Decode-step operators: what stands between the GEMVs of a step.
+ *
+ * Conventions as above, and: data is FP32, binary16 or bfloat16 as named by a
+ * gemv_elem_t; strides are in elements, the last dimension is contiguous;
+ * all arithmetic is FP32.  Lengths, slots and page numbers live on the device
+ * and are checked there: one out of range is skipped and reported as
+ * GEMV_ERR_BAD_INDEX by gemv_get_device_error, nothing is read or written
+ * outside the given buffers.  16-byte aligned rows of a multiple of eight
+ * elements take vector loads; any other layout gives the same results more
+ * slowly.  Every kernel waits for the one before it on the stream, and may be
+ * captured into a CUDA graph; grids do not depend on the lengths.  The pages
+ * stop at the GEMV and the softmax; these calls have no counterpart there.
+ */
+typedef enum { GEMV_ELEM_F32 = 0, GEMV_ELEM_F16 = 1, GEMV_ELEM_BF16 = 5 } gemv_elem_t;
+
+/*
+ * A paged key-value cache.  Sequence b's slot s is token s % page_size of page
+ * page_table[b * table_stride + s / page_size]; its key for cached head h is
+ * the head_dim elements at k + page * k_stride[0] + token * k_stride[1] + h *
+ * k_stride[2], its value likewise.  elem: GEMV_ELEM_F16 or GEMV_ELEM_BF16;
+ * head_dim 1..256.  A sequence has max_pages * page_size slots (below 2^31).
+ * scores (FP32) and stamps (int32), both [batch][kv_heads][max_pages *
+ * page_size], may be NULL: the attention weight each slot has gathered and
+ * the number of the token it holds, which eviction goes by.
+ */
+typedef struct {
+    void *k, *v;
+    int64_t k_stride[3], v_stride[3];
+    const int32_t *page_table;
+    int64_t table_stride;
+    int64_t num_pages;
+    float *scores;
+    int32_t *stamps;
+    int32_t elem;
+    int32_t page_size, max_pages, batch, kv_heads, head_dim;
+} gemv_kv_t;
+
+/*
+ * Attention of one new token per sequence:
+ *   s_t = scale * q . k_t,  p = softmax(s),  out = sum_t p_t v_t
+ * over the slots t in [max(0, n - window), n), n = lengths[b] (window 0: all).
+ * q and out: [batch][q_heads][head_dim] of the cache's type, strides (sequence,
+ * head) given; q_heads a multiple of kv_heads, query heads h * g .. h * g + g - 1
+ * read cached head h (g = q_heads / kv_heads).  A sequence of length 0, or
+ * whose scores are all -inf, gives zeros.  lse: NULL, or FP32 [batch][q_heads]
+ * log(sum exp(s)) (-inf for such a row).
+ * scores_out: NULL, or FP32 like kv->scores (may be the same): scores_out =
+ * kv->scores + the sum of p over the head's query heads, for the slots attended
+ * to; the others are left alone.
+ * workspace: device memory of gemv_attn_paged_workspace(...) bytes, 256-byte
+ * aligned, zero-filled before its first use; a call leaves it fit for the
+ * next on the same stream.  One workspace serves one call at a time.
+ */
+gemv_status_t gemv_attn_paged(const gemv_kv_t *kv, const void *q, const int64_t q_stride[2],
+                              const int32_t *lengths, void *out, const int64_t out_stride[2],
+                              int q_heads, float scale, int window, float *lse, float *scores_out,
+                              void *workspace, size_t workspace_bytes, void *stream);
+/* Bytes of workspace (0 where the arguments are not valid).  weights: whether
+ * scores_out will be given; capacity-sized scratch comes with it. */
+size_t gemv_attn_paged_workspace(const gemv_kv_t *kv, int q_heads, int weights);
+
+/*
+ * Eviction by accumulated attention weight, one plan per sequence and cached
+ * head.  Of the n = lengths[b] slots the first `keep` (>= 1) stay in this
+ * order: protected slots (stamp < sinks, or stamp > newest stamp - recent),
+ * then the larger score (NaN as -inf), then the lower slot.  Those that stay at
+ * or behind slot `keep` move into the holes before it, in ascending order on
+ * both sides: moves[row][i] = (from, to), counts[row] of them, row = b *
+ * kv_heads + h; entries behind the count are left alone.  moves: int32
+ * [batch][kv_heads][max_moves][2], 8-byte aligned; max_moves at least
+ * min(keep, capacity - keep).  n <= keep: no moves.  kv->scores and kv->stamps
+ * are required.
+ */
+gemv_status_t gemv_kv_evict_plan(const gemv_kv_t *kv, const int32_t *lengths, int keep, int sinks,
+                                 int recent, int32_t *moves, int64_t max_moves, int32_t *counts,
+                                 void *stream);
+/*
+ * Carries a plan out on k, v and (where kv has them) scores and stamps, and
+ * lowers lengths[b] (may be NULL) to keep.  No move's source is another's
+ * target, so a plan may be carried out again, or on other caches laid out by
+ * the same lengths.
+ */
+gemv_status_t gemv_kv_evict_apply(const gemv_kv_t *kv, const int32_t *moves, int64_t max_moves,
+                                  const int32_t *counts, int32_t *lengths, int keep, void *stream);
+
+/*
+ * Rotary positions with several axes, and the append to the cache.  For each
+ * of `tokens` tokens, q [tokens][q_heads][head_dim], k and v
+ * [tokens][kv_heads][head_dim] of type src_elem with strides (token, head):
+ * pair i < rot / 2 of every head of q and k is turned by the angle
+ *   positions[axis[i] * pos_stride + token] * 2 pi * turns[i] / 2^64
+ * (turns[i] = round(2^64 f_i / (2 pi)) for frequency f_i; the fraction of a
+ * turn is exact for any int32 position).  pairs 0: elements i and i + rot / 2
+ * form pair i; pairs 1: elements 2 i and 2 i + 1.  Elements from rot on are
+ * kept.  q_out [tokens][q_heads][head_dim] of the cache's type; k and v go to
+ * slot slots[token] of sequence seq[token] (seq NULL: the token's number); a
+ * negative slot is padding (q_out is written, the cache is not).  Where kv has
+ * scores and stamps the slot's become 0 and stamps[token] (stamps NULL: the
+ * slot).  No two tokens of a call may share a slot.  axis: uint8 [rot / 2],
+ * values below axes; rot even, at most head_dim.
+ */
+gemv_status_t gemv_rope_append(const gemv_kv_t *kv, int src_elem, const void *q,
+                               const int64_t q_stride[2], const void *k, const int64_t k_stride[2],
+                               const void *v, const int64_t v_stride[2], void *q_out,
+                               const int64_t q_out_stride[2], int tokens, int q_heads,
+                               const int32_t *positions, int64_t pos_stride, int axes,
+                               const int32_t *slots, const int32_t *seq, const int32_t *stamps,
+                               const uint64_t *turns, const uint8_t *axis, int rot, int pairs,
+                               void *stream);
+
+/*
+ * The norms around a block with its gate and the residual:
+ *   u = y;  post: u = norm(u) * post_weight;  u = u * gate
+ *   x' = x + alpha * u -> out;  h = norm(x') * pre_weight + pre_bias -> h
+ * norm: v / sqrt(mean(v^2) + eps), or with GEMV_NORM_LAYER (v - mean) /
+ * sqrt(var + eps).  GEMV_NORM_UNIT_OFFSET: pre_weight stands for 1 +
+ * pre_weight.  An operand with data NULL is left out (as 1, or 0 for the
+ * bias); h with data NULL: only out.  row_stride 0: one row for all.  out has
+ * x's type and may be x; h may be y.  rows x width elements; width 0 is a
+ * no-op.
+ */
+#define GEMV_NORM_LAYER 1u
+#define GEMV_NORM_POST 2u
+#define GEMV_NORM_UNIT_OFFSET 4u
+typedef struct {
+    void *data;
+    int64_t row_stride;
+    int32_t elem; /* gemv_elem_t */
+} gemv_rows_t;
+typedef struct {
+    gemv_rows_t y, x, gate, post_weight, pre_weight, pre_bias, out, h;
+    int64_t rows, width;
+    float alpha, eps;
+    uint32_t flags; /* GEMV_NORM_* */
+} gemv_norm_t;
+gemv_status_t gemv_norm_residual(const gemv_norm_t *args, void *stream);
+
+/*
  * Synchronises `stream`, reads and clears this device's status word.
  * Returns GEMV_ERR_TIMEOUT if any kernel gave up a bounded wait since the
  * last call, GEMV_OK otherwise (GEMV_ERR_CUDA if the CUDA calls fail).
@@ -376,6 +517,8 @@ gemv_status_t gemv_q8_rowscale_run_variant(int variant, const int8_t *A, const u
  * for a bulk copy it had issued, so that copy may have landed in shared
  * memory after the block exited; treat every result computed on this device
  * since the previous call as suspect.
+ * GEMV_ERR_BAD_INDEX: a decode-step operator met a page number, slot, length
+ * or axis outside its range since the last call; it skipped the access.
  */
 gemv_status_t gemv_get_device_error(void *stream);
 

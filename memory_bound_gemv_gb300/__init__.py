@@ -9,7 +9,8 @@ built or loaded, every call raises.
 Function names match the C entry points: ``gemv_f32``, ``gemv_f16``,
 ``gemv_q8``, ``gemv_q4``, ``gemv_f16_xf32``, ``gemv_q8_rowscale``, ``gemv_probe_read``, ``gemv_dequant_q8``,
 ``gemv_dequant_q4``, ``gemv_run_variant`` ...  ``lib()`` returns the raw
-ctypes handle for callers that want to pass pointers themselves.
+ctypes handle for callers that want to pass pointers themselves.  The
+decode-step operators (``PagedKV``, ``gemv_attn_paged`` ...) are in ``decode``.
 """
 
 from __future__ import annotations
@@ -25,9 +26,9 @@ GROUP = 128
 
 STATUS = {0: "GEMV_OK", 1: "GEMV_ERR_INVALID_VALUE", 2: "GEMV_ERR_MISALIGNED",
           3: "GEMV_ERR_UNSUPPORTED", 4: "GEMV_ERR_LAUNCH", 5: "GEMV_ERR_TIMEOUT",
-          6: "GEMV_ERR_CUDA", 7: "GEMV_ERR_TIMEOUT_UNDRAINED"}
+          6: "GEMV_ERR_CUDA", 7: "GEMV_ERR_TIMEOUT_UNDRAINED", 8: "GEMV_ERR_BAD_INDEX"}
 (OK, ERR_INVALID_VALUE, ERR_MISALIGNED, ERR_UNSUPPORTED, ERR_LAUNCH, ERR_TIMEOUT, ERR_CUDA,
- ERR_TIMEOUT_UNDRAINED) = range(8)
+ ERR_TIMEOUT_UNDRAINED, ERR_BAD_INDEX) = range(9)
 
 # test hooks (gemv_debug_skip_copies)
 SKIP_X, SKIP_STAGE, SKIP_SEGMENT, SKIP_PROBE = 1, 2, 4, 8
@@ -116,7 +117,7 @@ def _declare(L):
     L.gemv_last_cuda_error.restype = i32
     L.gemv_build_info.argtypes = []
     L.gemv_build_info.restype = ctypes.c_char_p
-    return L
+    return _declare_decode(L)
 
 
 def library_path() -> str:
@@ -521,7 +522,7 @@ def copy_probe_variants() -> List[str]:
 
 
 def gemv_get_device_error(stream=None) -> int:
-    """Synchronise the stream; return and clear the device status (OK or ERR_TIMEOUT)."""
+    """Synchronise the stream; return and clear the device status (OK, ERR_TIMEOUT, ERR_BAD_INDEX ...)."""
     return lib().gemv_get_device_error(_stream_ptr(stream))
 
 
@@ -552,3 +553,8 @@ def status_string(status: int) -> str:
 
 def build_info() -> str:
     return lib().gemv_build_info().decode()
+
+
+from .decode import _declare as _declare_decode  # noqa: E402
+from .decode import (PagedKV, RopeTable, gemv_attn_paged, gemv_kv_evict, gemv_kv_evict_apply,  # noqa: E402,F401
+                     gemv_kv_evict_plan, gemv_norm_residual, gemv_rope_append)

@@ -14,6 +14,7 @@
 #include <tuple>
 
 #include "../../include/gemv.h"
+#include "gemv_decode.h"
 #include "gemv_internal.h"
 
 #define MBG_STR2(v) #v
@@ -429,6 +430,18 @@ gemv_status_t run(int dtype, int vid, const void *A, const void *x, float *y, in
 }
 
 }  // namespace
+
+bool decode_device(DecodeDevice *out)
+{
+    DeviceState *d = current_device();
+    if (!d) return false;
+    out->status = d->status;
+    out->sm_count = d->sm_count;
+    return true;
+}
+
+gemv_status_t decode_cuda_fail(cudaError_t e, gemv_status_t code) { return cuda_fail(e, code); }
+
 }  // namespace mbg
 
 using namespace mbg;
@@ -754,7 +767,8 @@ gemv_status_t gemv_get_device_error(void *stream)
         if (e != cudaSuccess) return cuda_fail(e, GEMV_ERR_CUDA);
     }
     if (word & DEVERR_UNDRAINED) return GEMV_ERR_TIMEOUT_UNDRAINED;
-    return (word & DEVERR_TIMEOUT) ? GEMV_ERR_TIMEOUT : GEMV_OK;
+    if (word & DEVERR_TIMEOUT) return GEMV_ERR_TIMEOUT;
+    return (word & DEVERR_BAD_INDEX) ? GEMV_ERR_BAD_INDEX : GEMV_OK;
 }
 
 void gemv_debug_set_wait_limit_ns(uint64_t ns)
@@ -801,6 +815,7 @@ const char *gemv_status_string(gemv_status_t status)
     case GEMV_ERR_TIMEOUT: return "GEMV_ERR_TIMEOUT";
     case GEMV_ERR_CUDA: return "GEMV_ERR_CUDA";
     case GEMV_ERR_TIMEOUT_UNDRAINED: return "GEMV_ERR_TIMEOUT_UNDRAINED";
+    case GEMV_ERR_BAD_INDEX: return "GEMV_ERR_BAD_INDEX";
     default: return "GEMV_ERR_UNKNOWN";
     }
 }

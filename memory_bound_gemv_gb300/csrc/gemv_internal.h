@@ -29,8 +29,9 @@ enum { MATH_F32 = 0, MATH_MIXED = 1 };
 // Device status bits (the device status word).  DEVERR_UNDRAINED: after a
 // wait gave up, the bounded wait for the block's own copies still in flight
 // gave up too, so a copy may have landed in shared memory the block no
-// longer owned.
-enum : unsigned int { DEVERR_TIMEOUT = 1u, DEVERR_UNDRAINED = 2u };
+// longer owned.  DEVERR_BAD_INDEX: a page number, slot, length or axis read on
+// the device lay outside its range and was skipped.
+enum : unsigned int { DEVERR_TIMEOUT = 1u, DEVERR_UNDRAINED = 2u, DEVERR_BAD_INDEX = 4u };
 
 // Test hooks: copies that a launch arms its barrier for but does not issue,
 // so that the bounded wait on it runs out (nothing is copied, nothing

@@ -1,0 +1,463 @@
+"""Binding of the decode-step operators: what stands between the GEMVs of a step.
+
+``PagedKV`` describes a paged key-value cache once; the calls then take it with
+the step's tensors: ``gemv_rope_append`` (rotary positions with several axes,
+and the append), ``gemv_attn_paged`` (attention of one new token per
+sequence), ``gemv_kv_evict_plan`` / ``gemv_kv_evict_apply`` (eviction by
+accumulated attention weight; ``gemv_kv_evict`` does both) and
+``gemv_norm_residual`` (the norms around a block with its gate and the
+residual).  As in the rest of the package: argument checks and marshalling
+only, no CPU fallback, C errors raised as ``GemvError``.  Lengths, slots and
+page numbers stay on the device; one out of range is skipped and reported by
+``gemv_get_device_error``.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import math
+import struct
+from typing import List, Optional, Sequence
+
+import memory_bound_gemv_gb300 as _mbg
+
+ELEM_F32, ELEM_F16, ELEM_BF16 = 0, 1, 5
+NORM_LAYER, NORM_POST, NORM_UNIT_OFFSET = 1, 2, 4
+
+_elems = None
+
+
+def _elem(dtype) -> Optional[int]:
+    global _elems
+    if _elems is None:
+        torch = _mbg._torch()
+        _elems = {torch.float32: ELEM_F32, torch.float16: ELEM_F16, torch.bfloat16: ELEM_BF16}
+    return _elems.get(dtype)
+
+
+class _KvStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+                ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("num_pages", ctypes.c_int64), ("scores", ctypes.c_void_p), ("stamps", ctypes.c_void_p),
+                ("elem", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("batch", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+def _declare(L):
+    vp, i32, i64, st = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int
+    f32 = ctypes.c_float
+    sig = {
+        "gemv_attn_paged": [vp, vp, vp, vp, vp, vp, i32, f32, i32, vp, vp, vp, ctypes.c_size_t, vp],
+        "gemv_kv_evict_plan": [vp, vp, i32, i32, i32, vp, i64, vp, vp],
+        "gemv_kv_evict_apply": [vp, vp, i64, vp, vp, i32, vp],
+        "gemv_rope_append": [vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, vp, i64, i32, vp, vp, vp, vp, vp,
+                             i32, i32, vp],
+        "gemv_norm_residual": [vp, vp],
+    }
+    for name, args in sig.items():
+        f = getattr(L, name)
+        f.argtypes = args
+        f.restype = st
+    L.gemv_attn_paged_workspace.argtypes = [vp, i32, i32]
+    L.gemv_attn_paged_workspace.restype = ctypes.c_size_t
+    return L
+
+
+_pairs = {}
+
+
+def _pair(a: int, b: int):
+    """Two strides as a C array (kept: a program has few)."""
+    got = _pairs.get((a, b))
+    if got is None:
+        if len(_pairs) > 4096:
+            _pairs.clear()
+        got = _pairs[(a, b)] = (ctypes.c_int64 * 2)(a, b)
+    return got
+
+
+def _operand(t, name, dtype, shape, device):
+    """A CUDA tensor of this type and shape whose last dimension is contiguous."""
+    torch = _mbg._torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if shape and shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+
+
+def _dense(t, name, dtype, shape, device):
+    _operand(t, name, dtype, shape, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _on(stream):
+    """Context in which tensors belong to the stream that a call runs on."""
+    torch = _mbg._torch()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    return torch.cuda.stream(stream)  # None: no change
+
+
+class PagedKV:
+    """A paged key-value cache, described once.
+
+    k, v: [pages, page_size, kv_heads, head_dim], float16 or bfloat16, any
+    strides with a contiguous last dimension (a pool laid out [pages, kv_heads,
+    page_size, head_dim] is passed transposed).  page_table: int32 [batch,
+    max_pages], the pages of each sequence in order; entries behind a
+    sequence's last page are never read.  scores (float32) and stamps (int32),
+    [batch, kv_heads, max_pages * page_size]: the attention weight each slot
+    has gathered and the number of its token, for eviction.
+
+    The tensors are kept; their contents may change, their storage not.  The
+    handle keeps a workspace per stream for ``gemv_attn_paged``: calls on one
+    stream use it in turn, calls on different streams have one each, and a call
+    that is being captured into a CUDA graph gets its own.
+    """
+
+    def __init__(self, k, v, page_table, scores=None, stamps=None):
+        torch = _mbg._torch()
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("k must be a tensor [pages, page_size, kv_heads, head_dim]")
+        if k.dtype not in (torch.float16, torch.bfloat16):
+            raise TypeError(f"k has dtype {k.dtype}, expected float16 or bfloat16")
+        _operand(k, "k", k.dtype, k.shape, k.device)
+        _operand(v, "v", k.dtype, k.shape, k.device)
+        if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+            raise ValueError("page_table must be a tensor [batch, max_pages]")
+        _operand(page_table, "page_table", torch.int32, page_table.shape, k.device)
+        pages, self.page_size, self.kv_heads, self.head_dim = k.shape
+        self.batch, self.max_pages = page_table.shape
+        self.capacity = self.max_pages * self.page_size
+        self.device, self.dtype = k.device, k.dtype
+        per_slot = (self.batch, self.kv_heads, self.capacity)
+        if scores is not None:
+            _dense(scores, "scores", torch.float32, per_slot, k.device)
+        if stamps is not None:
+            _dense(stamps, "stamps", torch.int32, per_slot, k.device)
+        self.k, self.v, self.page_table, self.scores, self.stamps = k, v, page_table, scores, stamps
+        self._s = _KvStruct(
+            k.data_ptr(), v.data_ptr(), k.stride()[:3], v.stride()[:3], page_table.data_ptr(), page_table.stride(0),
+            pages, None if scores is None else scores.data_ptr(), None if stamps is None else stamps.data_ptr(),
+            _elem(k.dtype), self.page_size, self.max_pages, self.batch, self.kv_heads, self.head_dim)
+        self._at = ctypes.addressof(self._s)
+        self._workspaces = {}
+        self._captured: List = []
+        self._lib = _mbg.lib()
+
+    def _workspace(self, q_heads, weights, ptr, stream):
+        torch = _mbg._torch()
+        key = (ptr, q_heads, weights)
+        if not torch.cuda.is_current_stream_capturing():
+            got = self._workspaces.get(key)
+            if got is not None:
+                return got
+        with _on(stream):
+            capturing = torch.cuda.is_current_stream_capturing()
+            if not capturing and key in self._workspaces:
+                return self._workspaces[key]
+            n = self._lib.gemv_attn_paged_workspace(self._at, q_heads, 1 if weights else 0)
+            t = torch.empty(max(n, 256), dtype=torch.uint8, device=self.device)
+            t[:4 * self.batch * q_heads + 256].zero_()  # the counters of its first part
+            got = (t.data_ptr(), t.numel(), t)
+        if capturing:
+            self._captured.append(t)  # the graph's own, as long as the handle lives
+        else:
+            self._workspaces[key] = got
+        return got
+
+
+class RopeTable:
+    """Frequencies of rotary positions with one or more axes, kept on the device.
+
+    ``rot_dim`` leading elements of a head are turned, as rot_dim / 2 pairs:
+    elements i and i + rot_dim / 2, or with ``pairs`` elements 2 i and 2 i + 1.
+    ``sections``: how many consecutive pairs go by each axis (default: all by
+    one).  Pair i turns with frequency theta^(-2 i / rot_dim); with ``per_axis``
+    each axis has the whole ladder over its own pairs, theta^(-j / pairs of the
+    axis).  ``frequencies`` (radians per position, below 2 pi) replaces them,
+    for ladders stretched or scaled otherwise.
+    """
+
+    def __init__(self, rot_dim: int, sections: Optional[Sequence[int]] = None, theta: float = 10000.0,
+                 pairs: bool = False, per_axis: bool = False, frequencies: Optional[Sequence[float]] = None,
+                 device="cuda"):
+        torch = _mbg._torch()
+        half = rot_dim // 2
+        if rot_dim < 0 or rot_dim % 2:
+            raise ValueError("rot_dim must be even and not negative")
+        sections = [half] if sections is None else [int(n) for n in sections]
+        if not 1 <= len(sections) <= 255 or min(sections) < 0 or sum(sections) != half:
+            raise ValueError(f"sections must be 1 to 255 counts that add up to rot_dim / 2 = {half}")
+        if frequencies is None:
+            if not theta > 0:
+                raise ValueError("theta must be positive")
+            if per_axis:
+                frequencies = [theta ** (-j / n) for n in sections for j in range(n)]
+            else:
+                frequencies = [theta ** (-2.0 * i / rot_dim) for i in range(half)]
+        if len(frequencies) != half:
+            raise ValueError(f"frequencies must have rot_dim / 2 = {half} values")
+        turns = []
+        for f in frequencies:
+            if not 0 <= f < 2 * math.pi:
+                raise ValueError("frequencies must lie in [0, 2 pi)")
+            t = round(math.ldexp(f / (2 * math.pi), 64)) % (1 << 64)
+            turns.append(t - (1 << 64) if t >= 1 << 63 else t)
+        self.rot_dim, self.axes, self.pairs = rot_dim, len(sections), bool(pairs)
+        self.turns = torch.tensor(turns, dtype=torch.int64).to(device)
+        self.axis = torch.tensor([a for a, n in enumerate(sections) for _ in range(n)], dtype=torch.uint8).to(device)
+        self._turns_at, self._axis_at = self.turns.data_ptr(), self.axis.data_ptr()
+
+
+def gemv_attn_paged(cache: PagedKV, q, lengths, out=None, scale: Optional[float] = None, window: int = 0, lse=None,
+                    accumulate: bool = False, scores_out=None, stream=None):
+    """Attention of one new token per sequence over the cache; returns out.
+
+    q: [batch, q_heads, head_dim] of the cache's type, any strides with a
+    contiguous last dimension; lengths: int32 [batch], the slots in use (the
+    new token's among them).  ``window``: only the last so many slots (0: all).
+    ``lse``: float32 [batch, q_heads] that receives log(sum exp(score)).
+    ``accumulate``: adds the weights, summed over the query heads of a cached
+    head, to cache.scores, or with ``scores_out`` writes the sums there.  A
+    sequence of length 0 gives zeros (and lse -inf)."""
+    torch = _mbg._torch()
+    device = cache.device
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor [batch, q_heads, head_dim]")
+    heads = q.shape[1]
+    shape = (cache.batch, heads, cache.head_dim)
+    _operand(q, "q", cache.dtype, shape, device)
+    if heads < 1 or heads % cache.kv_heads:
+        raise ValueError(f"q has {heads} heads, expected a multiple of {cache.kv_heads}")
+    _dense(lengths, "lengths", torch.int32, (cache.batch,), device)
+    if window < 0:
+        raise ValueError("window must not be negative")
+    if out is None:
+        with _on(stream):
+            out = torch.empty(shape, dtype=cache.dtype, device=device)
+    else:
+        _operand(out, "out", cache.dtype, shape, device)
+    if lse is not None:
+        _dense(lse, "lse", torch.float32, (cache.batch, heads), device)
+    s_ptr = None
+    if accumulate:
+        if cache.scores is None:
+            raise ValueError("accumulate needs a cache with scores")
+        if scores_out is None:
+            scores_out = cache.scores
+        else:
+            _dense(scores_out, "scores_out", torch.float32, cache.scores.shape, device)
+        s_ptr = scores_out.data_ptr()
+    elif scores_out is not None:
+        raise ValueError("scores_out goes with accumulate=True")
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    ptr = _mbg._stream_ptr(stream)
+    ws = cache._workspace(heads, accumulate, ptr, stream)
+    qs, os = q.stride(), out.stride()
+    st = cache._lib.gemv_attn_paged(cache._at, q.data_ptr(), _pair(qs[0], qs[1]), lengths.data_ptr(), out.data_ptr(),
+                                    _pair(os[0], os[1]), heads, scale, window,
+                                    None if lse is None else lse.data_ptr(), s_ptr, ws[0], ws[1], ptr)
+    if st:
+        _mbg._raise(st, "gemv_attn_paged")
+    return out
+
+
+def gemv_rope_append(cache: PagedKV, q, k, v, positions, slots, rope: RopeTable, q_out=None, seq=None, stamps=None,
+                     stream=None):
+    """Turns q and k by their positions, writes k and v to the cache; returns q_out.
+
+    q: [tokens, q_heads, head_dim], k and v: [tokens, kv_heads, head_dim], all
+    float32 (a GEMV's output), float16 or bfloat16; any strides with a
+    contiguous last dimension, so parts of one QKV product will do.
+    positions: int32 [axes, tokens].  slots: int32 [tokens], each token's slot
+    in its sequence (negative: padding, not written).  seq: int32 [tokens], the
+    tokens' sequences (default: token t belongs to sequence t).  stamps: int32
+    [tokens], the tokens' numbers (default: the slots) for a cache with stamps.
+    q_out: [tokens, q_heads, head_dim] of the cache's type."""
+    torch = _mbg._torch()
+    device = cache.device
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor [tokens, q_heads, head_dim]")
+    elem = _elem(q.dtype)
+    if elem is None:
+        raise TypeError(f"q has dtype {q.dtype}, expected float32, float16 or bfloat16")
+    tokens, heads, dim = q.shape
+    _operand(q, "q", q.dtype, (tokens, heads, cache.head_dim), device)
+    kv_shape = (tokens, cache.kv_heads, dim)
+    _operand(k, "k", q.dtype, kv_shape, device)
+    _operand(v, "v", q.dtype, kv_shape, device)
+    if rope.rot_dim > dim:
+        raise ValueError(f"the rope turns {rope.rot_dim} elements, a head has {dim}")
+    if rope.turns.device != device:
+        raise ValueError(f"the rope table is on {rope.turns.device}, expected {device}")
+    _operand(positions, "positions", torch.int32, (rope.axes, tokens), device)
+    _dense(slots, "slots", torch.int32, (tokens,), device)
+    if seq is not None:
+        _dense(seq, "seq", torch.int32, (tokens,), device)
+    elif tokens > cache.batch:
+        raise ValueError(f"{tokens} tokens for {cache.batch} sequences: seq is needed")
+    if stamps is not None:
+        _dense(stamps, "stamps", torch.int32, (tokens,), device)
+    if q_out is None:
+        with _on(stream):
+            q_out = torch.empty((tokens, heads, dim), dtype=cache.dtype, device=device)
+    else:
+        _operand(q_out, "q_out", cache.dtype, (tokens, heads, dim), device)
+    qs, ks, vs, os = q.stride(), k.stride(), v.stride(), q_out.stride()
+    st = cache._lib.gemv_rope_append(
+        cache._at, elem, q.data_ptr(), _pair(qs[0], qs[1]), k.data_ptr(), _pair(ks[0], ks[1]), v.data_ptr(),
+        _pair(vs[0], vs[1]), q_out.data_ptr(), _pair(os[0], os[1]), tokens, heads, positions.data_ptr(),
+        positions.stride(0), rope.axes, slots.data_ptr(), None if seq is None else seq.data_ptr(),
+        None if stamps is None else stamps.data_ptr(), rope._turns_at, rope._axis_at, rope.rot_dim,
+        1 if rope.pairs else 0, _mbg._stream_ptr(stream))
+    if st:
+        _mbg._raise(st, "gemv_rope_append")
+    return q_out
+
+
+def _moves(cache, moves, counts):
+    torch = _mbg._torch()
+    if not isinstance(moves, torch.Tensor) or moves.dim() != 4:
+        raise ValueError("moves must be a tensor [batch, kv_heads, max_moves, 2]")
+    _dense(moves, "moves", torch.int32, (cache.batch, cache.kv_heads, moves.shape[2], 2), cache.device)
+    _dense(counts, "counts", torch.int32, (cache.batch, cache.kv_heads), cache.device)
+
+
+def gemv_kv_evict_plan(cache: PagedKV, lengths, keep: int, sinks: int = 0, recent: int = 0, moves=None, counts=None,
+                       stream=None):
+    """Which slots move so that ``keep`` of each sequence and cached head stay; returns (moves, counts).
+
+    Those that stay: slots whose stamp is below ``sinks`` or among the
+    ``recent`` newest numbers, then the larger score, then the lower slot.
+    moves: int32 [batch, kv_heads, max_moves, 2], the first counts[b, h] pairs
+    (from, to) are written; max_moves at least min(keep, capacity - keep).
+    Nothing in the cache changes."""
+    torch = _mbg._torch()
+    if cache.scores is None or cache.stamps is None:
+        raise ValueError("eviction needs a cache with scores and stamps")
+    if keep < 1 or sinks < 0 or recent < 0:
+        raise ValueError("keep must be at least 1, sinks and recent not negative")
+    _dense(lengths, "lengths", torch.int32, (cache.batch,), cache.device)
+    most = max(1, min(keep, cache.capacity - keep))
+    if moves is None or counts is None:
+        with _on(stream):
+            if moves is None:
+                moves = torch.empty((cache.batch, cache.kv_heads, most, 2), dtype=torch.int32, device=cache.device)
+            if counts is None:
+                counts = torch.empty((cache.batch, cache.kv_heads), dtype=torch.int32, device=cache.device)
+    _moves(cache, moves, counts)
+    if moves.shape[2] < most:
+        raise ValueError(f"moves has room for {moves.shape[2]}, at least {most} are needed")
+    st = cache._lib.gemv_kv_evict_plan(cache._at, lengths.data_ptr(), keep, sinks, recent, moves.data_ptr(),
+                                       moves.shape[2], counts.data_ptr(), _mbg._stream_ptr(stream))
+    if st:
+        _mbg._raise(st, "gemv_kv_evict_plan")
+    return moves, counts
+
+
+def gemv_kv_evict_apply(cache: PagedKV, moves, counts, lengths, keep: int, stream=None):
+    """Carries a plan out: keys, values, scores and stamps move, lengths is lowered to keep.
+
+    ``lengths`` may be None (left to the caller).  A plan may be carried out on
+    several caches that are filled alike."""
+    torch = _mbg._torch()
+    if keep < 1:
+        raise ValueError("keep must be at least 1")
+    _moves(cache, moves, counts)
+    if lengths is not None:
+        _dense(lengths, "lengths", torch.int32, (cache.batch,), cache.device)
+    st = cache._lib.gemv_kv_evict_apply(cache._at, moves.data_ptr(), moves.shape[2], counts.data_ptr(),
+                                        None if lengths is None else lengths.data_ptr(), keep,
+                                        _mbg._stream_ptr(stream))
+    if st:
+        _mbg._raise(st, "gemv_kv_evict_apply")
+
+
+def gemv_kv_evict(cache: PagedKV, lengths, keep: int, sinks: int = 0, recent: int = 0, moves=None, counts=None,
+                  stream=None):
+    """``gemv_kv_evict_plan`` and ``gemv_kv_evict_apply`` in turn; returns (moves, counts)."""
+    moves, counts = gemv_kv_evict_plan(cache, lengths, keep, sinks, recent, moves, counts, stream)
+    gemv_kv_evict_apply(cache, moves, counts, lengths, keep, stream)
+    return moves, counts
+
+
+_NORM = struct.Struct("PqiPqiPqiPqiPqiPqiPqiPqiqqffI0q")
+_NONE = (0, 0, 0)
+
+
+def _rows(t, name, rows, width, device, dtype=None):
+    """(address, row stride, type) of an operand [rows, width] or [width]."""
+    torch = _mbg._torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    elem = _elem(t.dtype)
+    if elem is None:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected float32, float16 or bfloat16")
+    if t.dim() == 1 and dtype is None:
+        _operand(t, name, t.dtype, (width,), device)
+        return t.data_ptr(), 0, elem
+    _operand(t, name, dtype or t.dtype, (rows, width), device)
+    return t.data_ptr(), t.stride(0), elem
+
+
+def gemv_norm_residual(y, x, post: bool = False, post_weight=None, gate=None, alpha: float = 1.0, pre_weight=None,
+                       pre_bias=None, kind: str = "rms", unit_offset: bool = False, eps: float = 1e-6, out=None,
+                       h=None, h_dtype=None, pre: bool = True, stream=None):
+    """The norms around a block with its gate and the residual; returns (out, h).
+
+        u = y;  u = norm(u) * post_weight (with post);  u = u * gate
+        out = x + alpha * u;  h = norm(out) * pre_weight + pre_bias
+
+    y (the block's output) and x (the residual): [rows, width], float32,
+    float16 or bfloat16 each.  post_weight, gate, pre_weight, pre_bias: [width],
+    or [rows, width] for values of each row; None leaves one out.
+    ``kind``: 'rms' or 'layer' for both norms.  ``unit_offset``: pre_weight
+    stands for 1 + pre_weight.  out: like x (may be x).  h: the next block's
+    input, [rows, width], ``h_dtype`` float16 by default; ``pre=False``: none
+    (h is None).  h is computed from the unrounded sum."""
+    torch = _mbg._torch()
+    if not isinstance(y, torch.Tensor) or y.dim() != 2:
+        raise ValueError("y must be a tensor [rows, width]")
+    if kind not in ("rms", "layer"):
+        raise ValueError("kind must be 'rms' or 'layer'")
+    if post_weight is not None and not post:
+        raise ValueError("post_weight goes with post=True")
+    if not pre and (pre_weight is not None or pre_bias is not None or h is not None):
+        raise ValueError("pre_weight, pre_bias and h go with pre=True")
+    rows, width = y.shape
+    dev = y.device
+    y_ = _rows(y, "y", rows, width, dev, y.dtype)
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    x_ = _rows(x, "x", rows, width, dev, x.dtype)
+    if out is None or (pre and h is None):
+        with _on(stream):
+            if out is None:
+                out = torch.empty((rows, width), dtype=x.dtype, device=dev)
+            if pre and h is None:
+                h = torch.empty((rows, width), dtype=h_dtype or torch.float16, device=dev)
+    flags = (NORM_LAYER if kind == "layer" else 0) | (NORM_POST if post else 0) | (NORM_UNIT_OFFSET if unit_offset else 0)
+    packed = _NORM.pack(
+        *y_, *x_, *(_rows(gate, "gate", rows, width, dev) if gate is not None else _NONE),
+        *(_rows(post_weight, "post_weight", rows, width, dev) if post_weight is not None else _NONE),
+        *(_rows(pre_weight, "pre_weight", rows, width, dev) if pre_weight is not None else _NONE),
+        *(_rows(pre_bias, "pre_bias", rows, width, dev) if pre_bias is not None else _NONE),
+        *_rows(out, "out", rows, width, dev, x.dtype),
+        *(_rows(h, "h", rows, width, dev, h_dtype or h.dtype) if pre else _NONE),
+        rows, width, alpha, eps, flags)
+    st = _mbg.lib().gemv_norm_residual(packed, _mbg._stream_ptr(stream))
+    if st:
+        _mbg._raise(st, "gemv_norm_residual")
+    return out, h
