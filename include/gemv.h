@@ -422,9 +422,11 @@ typedef struct {
  * kv->scores + the sum of p over the head's query heads, for the slots attended
  * to; the others are left alone.
  * workspace: device memory of gemv_attn_paged_workspace(...) bytes, 256-byte
- * aligned, zero-filled before its first use; a call leaves it fit for the
- * next on the same stream.  One workspace serves one call at a time.
+ * aligned, of which the first GEMV_ATTN_COUNTER_BYTES + 4 * batch * q_heads
+ * are zero before its first use; a call leaves it fit for the next on the same
+ * stream.  One workspace serves one call at a time.
  */
+#define GEMV_ATTN_COUNTER_BYTES 8192
 gemv_status_t gemv_attn_paged(const gemv_kv_t *kv, const void *q, const int64_t q_stride[2],
                               const int32_t *lengths, void *out, const int64_t out_stride[2],
                               int q_heads, float scale, int window, float *lse, float *scores_out,
@@ -432,6 +434,10 @@ gemv_status_t gemv_attn_paged(const gemv_kv_t *kv, const void *q, const int64_t 
 /* Bytes of workspace (0 where the arguments are not valid).  weights: whether
  * scores_out will be given; capacity-sized scratch comes with it. */
 size_t gemv_attn_paged_workspace(const gemv_kv_t *kv, int q_heads, int weights);
+/* Number of the CUDA graph capture that `stream` is in, 0 if none: calls of one
+ * capture on one stream follow each other and may share a workspace, which no
+ * call outside the graph may use. */
+uint64_t gemv_capture_id(void *stream);
 
 /*
  * Eviction by accumulated attention weight, one plan per sequence and cached

@@ -36,7 +36,7 @@
 // equal share of consecutive ones, whatever the lengths (they are read on the
 // device, so a captured graph serves any lengths).  A row inside one CTA's
 // share is written at once; otherwise each CTA leaves (O, m, l) in the
-// workspace and the last to arrive joins them, always in block order, so
+// workspace and the last to arrive joins them, always in the same order, so
 // results do not depend on the order of arrival.
 #pragma once
 
@@ -53,6 +53,8 @@ namespace attn {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr unsigned kFull = 0xFFFFFFFFu;
+// CTAs whose parts of a row are joined first, before the groups are.
+constexpr int kGroupCtas = 16;
 
 template <typename T>
 struct Mma;
@@ -191,11 +193,16 @@ struct Kernel {
     // registers it would not fit beside K, V and O
     static constexpr bool kQInSmem = NT * DC > 2;
 
+    // parts joined at once: a group, or the groups of a row
+    static constexpr int kMaxParts = kAttnMaxCtas / kGroupCtas;
+
     struct Shared {
         float o[kWarps][kRegs][32];
         float m[kWarps][kHeads];
         float l[kWarps][kHeads];
         uint32_t q[kQInSmem ? kQWords : 1][32];
+        float part_m[kMaxParts][kHeads];
+        float part_l[kMaxParts][kHeads];
         int scan[kWarps];
         int pick[2];
         int last;
@@ -511,7 +518,19 @@ struct Kernel {
         __syncthreads();
 
         const bool whole = k0 == 0 && k1 == span.blocks();
-        float *mine = a.part + (2 * static_cast<int64_t>(cta) + (k0 == 0 ? 1 : 0)) * a.part_stride;
+        const int slot = 2 * cta + (k0 == 0 ? 1 : 0);
+        finish(a, sh, r, whole ? -1 : slot, top, sum);
+        if (!whole) join(a, sh, span, r, unit0, units, ctas, cta);
+        __syncthreads();  // shared memory is free again
+    }
+
+    // Sums the warps' O in shared memory (relative to `top`) and writes the
+    // row's output (slot < 0) or a part.
+    static __device__ __forceinline__ void finish(const AttnArgs &a, const Shared &sh, const Row &r, int slot,
+                                                  const float (&top)[NT][2], const float (&sum)[NT][2])
+    {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        float *mine = a.part + slot * a.part_stride;
         for (int i4 = warp; i4 < kRegs / 4; i4 += kWarps) {
             const int nt = i4 / (DC * 4);
             float v[4];
@@ -521,7 +540,7 @@ struct Kernel {
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) v[e] += sh.o[w][i4 * 4 + e][lane];
             }
-            if (whole) {
+            if (slot < 0) {
                 float inv[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -533,13 +552,13 @@ struct Kernel {
                 *reinterpret_cast<float4 *>(mine + (i4 * 32 + lane) * 4) = make_float4(v[0], v[1], v[2], v[3]);
             }
         }
-        if (warp == 0 && g == 0) {
+        if (warp == 0 && lane < 4) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int head = nt * 8 + 2 * t + e;
-                    if (whole) {
+                    const int head = nt * 8 + 2 * lane + e;
+                    if (slot < 0) {
                         store_stats(a, r, head, top[nt][e], sum[nt][e]);
                     } else {
                         mine[kRegs * 32 + head] = top[nt][e];
@@ -547,8 +566,6 @@ struct Kernel {
                     }
                 }
         }
-        if (!whole) join(a, sh, span, r, unit0, units, ctas);
-        __syncthreads();  // shared memory is free again
     }
 
     // CTA whose share holds a block: the largest c with units * c / ctas <= u.
@@ -557,91 +574,101 @@ struct Kernel {
         return static_cast<int>(((u + 1) * ctas - 1) / units);
     }
 
-    // The last CTA of a row to arrive joins its parts.  unit0: number of the
-    // row's first block.
-    static __device__ void join(const AttnArgs &a, Shared &sh, const RowSpan &span, const Row &r, int64_t unit0,
-                                int64_t units, int ctas)
+    // Has every one of `expected` CTAs arrived at this counter?  True for the
+    // last, for which the others' parts are visible then.
+    static __device__ __forceinline__ bool last_of(Shared &sh, unsigned int *counter, int expected)
     {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 3;
-        const int c0 = cta_of(unit0, units, ctas), c1 = cta_of(unit0 + span.blocks() - 1, units, ctas);
-        const int64_t row = static_cast<int64_t>(r.b) * a.kv.kv_heads * a.head_tiles + r.hk;
         __threadfence();
         __syncthreads();
         if (threadIdx.x == 0) {
-            const unsigned seen = atomicAdd(a.arrived + row, 1u);
-            sh.last = seen == static_cast<unsigned>(c1 - c0);
-            if (sh.last) a.arrived[row] = 0;  // ready for the next call
+            sh.last = atomicAdd(counter, 1u) == static_cast<unsigned>(expected - 1);
+            if (sh.last) *counter = 0;  // ready for the next call
         }
         __syncthreads();
-        if (!sh.last) return;
+        if (!sh.last) return false;
         __threadfence();
-        // parts: c0's second slot, then the first slots of c0 + 1 .. c1
-        auto part = [&](int c) { return a.part + (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * a.part_stride; };
-        float mm[NT][2], ll[NT][2];
+        return true;
+    }
+
+    // Joins n parts, the i-th at slot_of(i), into the row's output (into < 0) or
+    // into a part's slot.  The warps take the parts in turn, several of each
+    // in flight; the order of the sums is fixed by n.
+    template <typename F>
+    static __device__ void combine(const AttnArgs &a, Shared &sh, const Row &r, int n, F slot_of, int into)
+    {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 3;
+        for (int i = threadIdx.x; i < n * 2 * kHeads; i += kThreads) {
+            const int p = i / (2 * kHeads), k = i - p * 2 * kHeads;
+            const float v = __ldcg(a.part + slot_of(p) * a.part_stride + kRegs * 32 + k);
+            if (k < kHeads)
+                sh.part_m[p][k] = v;
+            else
+                sh.part_l[p][k - kHeads] = v;
+        }
+        __syncthreads();
+        float top[NT][2], sum[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                mm[nt][e] = -INFINITY;
-                ll[nt][e] = 0.f;
+                const int head = nt * 8 + 2 * t + e;
+                float mm = -INFINITY, ll = 0.f;
+                for (int p = 0; p < n; ++p) mm = fmaxf(mm, sh.part_m[p][head]);
+                for (int p = 0; p < n; ++p) ll += sh.part_l[p][head] * exp2_from(sh.part_m[p][head], mm);
+                top[nt][e] = mm;
+                sum[nt][e] = ll;
             }
-        for (int c = c0; c <= c1; ++c) {
-            const float *p = part(c) + kRegs * 32;
+        float v[kRegs];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+        for (int i = 0; i < kRegs; ++i) v[i] = 0.f;
+#pragma unroll 2
+        for (int p = warp; p < n; p += kWarps) {
+            const float *part = a.part + slot_of(p) * a.part_stride;
+            float4 x[kRegs / 4];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) mm[nt][e] = fmaxf(mm[nt][e], __ldcg(p + nt * 8 + 2 * t + e));
-        }
-        constexpr int kMine = (kRegs / 4 + kWarps - 1) / kWarps;
-        float v[kMine][4];
+            for (int i = 0; i < kRegs / 4; ++i) x[i] = __ldcg(reinterpret_cast<const float4 *>(part + (i * 32 + lane) * 4));
 #pragma unroll
-        for (int k = 0; k < kMine; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[k][e] = 0.f;
-        for (int c = c0; c <= c1; ++c) {
-            const float *p = part(c);
-            float fix[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int head = nt * 8 + 2 * t + e;
-                    fix[nt][e] = exp2_from(__ldcg(p + kRegs * 32 + head), mm[nt][e]);
-                    ll[nt][e] += __ldcg(p + kRegs * 32 + kHeads + head) * fix[nt][e];
-                }
-#pragma unroll
-            for (int k = 0; k < kMine; ++k) {
-                const int i4 = k * kWarps + warp;
-                if (i4 >= kRegs / 4) continue;
-                const int nt = i4 / (DC * 4);
-                const float4 x = __ldcg(reinterpret_cast<const float4 *>(p + (i4 * 32 + lane) * 4));
-                const float f0 = NT == 1 || nt == 0 ? fix[0][0] : fix[NT - 1][0];
-                const float f1 = NT == 1 || nt == 0 ? fix[0][1] : fix[NT - 1][1];
-                v[k][0] += x.x * f0;
-                v[k][1] += x.y * f1;
-                v[k][2] += x.z * f0;
-                v[k][3] += x.w * f1;
+            for (int i = 0; i < kRegs / 4; ++i) {
+                const int nt = i / (DC * 4);
+                const float f0 = exp2_from(sh.part_m[p][nt * 8 + 2 * t], top[nt][0]);
+                const float f1 = exp2_from(sh.part_m[p][nt * 8 + 2 * t + 1], top[nt][1]);
+                v[4 * i] += x[i].x * f0;
+                v[4 * i + 1] += x[i].y * f1;
+                v[4 * i + 2] += x[i].z * f0;
+                v[4 * i + 3] += x[i].w * f1;
             }
         }
 #pragma unroll
-        for (int k = 0; k < kMine; ++k) {
-            const int i4 = k * kWarps + warp;
-            if (i4 >= kRegs / 4) continue;
-            const int nt = i4 / (DC * 4);
-            float inv[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float x = NT == 1 || nt == 0 ? ll[0][e] : ll[NT - 1][e];
-                inv[e] = x == 0.f ? 0.f : 1.f / x;
-            }
-            store_out(a, r, i4 * 4, v[k], lane, inv);
+        for (int i = 0; i < kRegs; ++i) sh.o[warp][i][lane] = v[i];
+        __syncthreads();
+        finish(a, sh, r, into, top, sum);
+    }
+
+    // A row that several CTAs share.  The last CTA of each group of kGroupCtas
+    // to arrive joins the group's parts, the last group to arrive joins the
+    // groups: one CTA joining all parts of a long row one after another took
+    // 20 us and more of latency, two levels take about 3.  unit0: number of the
+    // row's first block.
+    static __device__ void join(const AttnArgs &a, Shared &sh, const RowSpan &span, const Row &r, int64_t unit0,
+                                int64_t units, int ctas, int cta)
+    {
+        const int c0 = cta_of(unit0, units, ctas), n = cta_of(unit0 + span.blocks() - 1, units, ctas) - c0 + 1;
+        // a CTA's part that begins a row is its second slot, any other its first
+        auto slot = [&](int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); };
+        const int first = (cta - c0) / kGroupCtas * kGroupCtas, members = min(kGroupCtas, n - first);
+        const int groups = (n + kGroupCtas - 1) / kGroupCtas;
+        if (!last_of(sh, a.arrived_group + slot(first), members)) return;
+        if (groups == 1) {
+            combine(a, sh, r, n, slot, -1);
+            return;
         }
-        if (warp == 0 && lane < 4) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) store_stats(a, r, nt * 8 + 2 * t + e, mm[nt][e], ll[nt][e]);
+        if (members > 1) {
+            combine(a, sh, r, members, [&](int i) { return slot(first + i); }, slot(first));
+            __syncthreads();
         }
+        const int64_t row = static_cast<int64_t>(r.b) * a.kv.kv_heads * a.head_tiles + r.hk;
+        if (!last_of(sh, a.arrived + row, groups)) return;
+        combine(a, sh, r, groups, [&](int i) { return slot(i * kGroupCtas); }, -1);
     }
 
     // Sum over the block of one int per thread, and the thread's prefix.

@@ -50,6 +50,7 @@ struct AttnArgs {
     // workspace
     float *part;                // [2 * ctas][part_stride]: O in fragment order, then m and l per head
     int64_t part_stride;
+    unsigned int *arrived_group;  // [2 * kAttnMaxCtas], zero between calls
     unsigned int *arrived;      // [batch * kv_heads * head_tiles], zero between calls
     float *row_lse;             // same rows x 8 * NT heads: log2 of the softmax denominator
     float *logits;              // [rows][capacity][logit_heads], log2 units; weights only
@@ -75,7 +76,7 @@ struct EvictArgs {
     int64_t max_moves;
     unsigned int *err;
 };
-cudaError_t launch_evict_plan(const EvictArgs &a, int sm_count, cudaStream_t s);
+cudaError_t launch_evict_plan(const EvictArgs &a, cudaStream_t s);
 
 struct EvictApplyArgs {
     KvView kv;
@@ -121,6 +122,6 @@ struct NormArgs {
     int post, layer, unit_offset;
     float alpha, eps;
 };
-cudaError_t launch_norm(const NormArgs &a, bool vec, cudaStream_t s);
+cudaError_t launch_norm(const NormArgs &a, bool vec, int sm_count, cudaStream_t s);
 
 }  // namespace mbg

@@ -96,8 +96,8 @@ AttnPlan attn_plan(const KvView &v, int group, int nt, bool weights)
     p.logit_heads = group >= heads ? heads : (group + 1) / 2 * 2;
     p.part_stride = static_cast<int64_t>(nt) * dc * 16 * 32 + 2 * heads;
     p.rows = static_cast<int64_t>(v.batch) * v.kv_heads * p.head_tiles;
-    p.arrived = 0;
-    p.part = up(static_cast<size_t>(p.rows) * 4);
+    p.arrived = 2 * kAttnMaxCtas * 4;
+    p.part = p.arrived + up(static_cast<size_t>(p.rows) * 4);
     p.row_lse = p.part + up(static_cast<size_t>(2) * kAttnMaxCtas * p.part_stride * 4);
     p.logits = p.row_lse + (weights ? up(static_cast<size_t>(p.rows) * heads * 4) : 0);
     p.total = p.logits + (weights ? up(static_cast<size_t>(p.rows) * v.capacity * p.logit_heads * 4) : 0);
@@ -120,6 +120,17 @@ size_t gemv_attn_paged_workspace(const gemv_kv_t *kv, int q_heads, int weights)
     if (v.dim > 128 || group <= 8) return a.total;
     const AttnPlan b = attn_plan(v, group, 2, weights != 0);
     return a.total > b.total ? a.total : b.total;
+}
+
+uint64_t gemv_capture_id(void *stream)
+{
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    if (cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &status, &id) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    return status == cudaStreamCaptureStatusActive ? id : 0;
 }
 
 gemv_status_t gemv_attn_paged(const gemv_kv_t *kv, const void *q, const int64_t q_stride[2],
@@ -163,6 +174,7 @@ gemv_status_t gemv_attn_paged(const gemv_kv_t *kv, const void *q, const int64_t 
     a.scale_log2 = scale * 1.4426950408889634f;
     a.err = dev.status;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
+    a.arrived_group = reinterpret_cast<unsigned int *>(ws);
     a.arrived = reinterpret_cast<unsigned int *>(ws + p.arrived);
     a.part = reinterpret_cast<float *>(ws + p.part);
     a.part_stride = p.part_stride;
@@ -201,7 +213,7 @@ gemv_status_t gemv_kv_evict_plan(const gemv_kv_t *kv, const int32_t *lengths, in
     a.max_moves = max_moves;
     a.counts = counts;
     a.err = dev.status;
-    const cudaError_t e = launch_evict_plan(a, dev.sm_count, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_evict_plan(a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GEMV_OK : decode_cuda_fail(e, GEMV_ERR_LAUNCH);
 }
 
@@ -321,7 +333,9 @@ gemv_status_t gemv_norm_residual(const gemv_norm_t *n, void *stream)
     a.unit_offset = (n->flags & GEMV_NORM_UNIT_OFFSET) != 0;
     a.alpha = n->alpha;
     a.eps = n->eps;
-    const cudaError_t e = launch_norm(a, vec, static_cast<cudaStream_t>(stream));
+    DecodeDevice dev;
+    if (!decode_device(&dev)) return GEMV_ERR_CUDA;
+    const cudaError_t e = launch_norm(a, vec, dev.sm_count, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GEMV_OK : decode_cuda_fail(e, GEMV_ERR_LAUNCH);
 }
 

@@ -11,17 +11,31 @@
 //
 // The order's keep-th element is found by a radix select over the scores'
 // bits mapped to unsigned integers (larger score, larger integer), on the one
-// class (protected or not) that the budget cuts: four passes of 8 bits, then
-// one pass in slot order that ranks ties and writes the moves.
+// class (protected or not) that the budget cuts: three histograms of 11, 11
+// and 10 bits.  A row is read once, into registers; the passes, the ranking of
+// ties and the numbering of holes and movers run on those.  The bytes (8 per
+// slot) are few: what counts is the chain of dependent steps, so a long row
+// is spread over a cluster of blocks, which add their histograms through
+// distributed shared memory, and a row takes about a dozen barriers whatever
+// its length.
+#include <cooperative_groups.h>
 #include <stdint.h>
 
 #include "gemv_decode.h"
 #include "gemv_device.cuh"
 
+namespace cg = cooperative_groups;
+
 namespace mbg {
 namespace {
 
+constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanMaxCluster = 8;
+constexpr int kBins = 2048;
+// Slots per thread in registers: of short rows, and of the longest ones.
+constexpr int kPlanShort = 4, kPlanLong = 24;
 
 // Larger score, larger integer; NaN like -inf, -0 like 0.
 __device__ __forceinline__ uint32_t score_key(float s)
@@ -31,138 +45,295 @@ __device__ __forceinline__ uint32_t score_key(float s)
     return (u >> 31) ? ~u : u | 0x80000000u;
 }
 
-// Sum over the block, and the thread's exclusive prefix, of two counts packed
-// into one 64-bit word.
-__device__ uint64_t block_scan(uint64_t v, uint64_t *total, uint64_t *warp_sums)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint64_t s = v;
-#pragma unroll
-    for (int x = 1; x < 32; x *= 2) {
-        const uint64_t n = __shfl_up_sync(0xFFFFFFFFu, s, x);
-        if (lane >= x) s += n;
-    }
-    __syncthreads();
-    if (lane == 31) warp_sums[warp] = s;
-    __syncthreads();
-    uint64_t before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-        if (w < warp) before += warp_sums[w];
-        all += warp_sums[w];
-    }
-    *total = all;
-    return before + s - v;
-}
+// What the blocks of a cluster tell one another.  Every exchange has its own
+// fields, so that one cluster barrier is enough for each.
+struct PlanShared {
+    unsigned hist[4][kBins];
+    unsigned scan[4][kPlanWarps];   // block scans of the histograms
+    unsigned warp_ties[kPlanWarps], warp_holes[kPlanWarps], warp_movers[kPlanWarps];
+    int newest;                     // this block's newest stamp
+    unsigned in_class;              // this block's protected slots
+    unsigned ties, holes, movers;   // this block's sums
+    int got_i[kPlanMaxCluster];     // the blocks' values as read here
+    unsigned got[4][kPlanMaxCluster];
+    unsigned digit, left, count;    // a pass' result
+};
 
+// KPT slots of a row per thread in registers; KPT 0: a row of any length, read
+// again for each step.
+template <int KPT>
 __global__ void __launch_bounds__(kPlanThreads) mbg_evict_plan_kernel(const __grid_constant__ EvictArgs a)
 {
-    __shared__ unsigned hist[256];
-    __shared__ uint64_t warp_sums[kPlanThreads / 32];
-    __shared__ int s_newest, s_protected;
-    __shared__ unsigned s_prefix, s_left;
+    constexpr bool kReg = KPT > 0;
+    __shared__ PlanShared sh;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int blocks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t row = blockIdx.x / blocks;
     pdl_trigger();
+    for (int i = tid; i < 4 * kBins; i += kPlanThreads) (&sh.hist[0][0])[i] = 0;
+    if (tid == 0) {
+        sh.newest = INT32_MIN;
+        sh.in_class = 0;
+    }
     pdl_wait();
-    const int tid = threadIdx.x;
-    const int64_t row = blockIdx.x;
     const int b = static_cast<int>(row / a.kv.kv_heads);
     int n = __ldg(a.lengths + b);
     if (n < 0 || n > a.kv.capacity) {
         if (tid == 0) report_error(a.err, DEVERR_BAD_INDEX);
         n = n < 0 ? 0 : static_cast<int>(a.kv.capacity);
     }
-    if (n <= a.keep) {
-        if (tid == 0) a.counts[row] = 0;
+    if (n <= a.keep) {  // the whole cluster leaves here or none of it
+        if (tid == 0 && rank == 0) a.counts[row] = 0;
         return;
     }
     const float *scores = a.scores + row * a.kv.capacity;
     const int32_t *stamps = a.stamps + row * a.kv.capacity;
+    // each warp takes consecutive slots, 32 at a time
+    const int warps = blocks * kPlanWarps;
+    const int steps = ((n + warps - 1) / warps + 31) / 32;
+    const int64_t base = static_cast<int64_t>(rank * kPlanWarps + warp) * steps * 32 + lane;
+    constexpr int kHold = kReg ? KPT : 1;
+    auto sync_all = [&]() {
+        if (blocks > 1)
+            cluster.sync();
+        else
+            __syncthreads();
+    };
 
-    // newest stamp, and how many slots are protected
-    if (tid == 0) {
-        s_newest = INT32_MIN;
-        s_protected = 0;
-    }
-    __syncthreads();
+    uint32_t key[kHold];
     int newest = INT32_MIN;
-    for (int i = tid; i < n; i += kPlanThreads) newest = max(newest, __ldg(stamps + i));
-    newest = __reduce_max_sync(0xFFFFFFFFu, newest);
-    if ((tid & 31) == 0) atomicMax(&s_newest, newest);
+    // short rows keep the stamps too; for long ones they are read a second
+    // time, from L2
+    constexpr bool kHoldStamps = kReg && KPT <= 8;
+    int stamp[kHoldStamps ? KPT : 1];
+    if (kReg) {
+#pragma unroll
+        for (int j = 0; j < kHold; ++j) {
+            const int64_t i = base + 32 * j;
+            if (j < steps && i < n) {
+                const int st = __ldg(stamps + i);
+                key[j] = score_key(__ldg(scores + i));
+                newest = max(newest, st);
+                if (kHoldStamps) stamp[kHoldStamps ? j : 0] = st;
+            }
+        }
+    } else {
+        for (int j = 0; j < steps; ++j)
+            if (base + 32 * j < n) newest = max(newest, __ldg(stamps + base + 32 * j));
+    }
+    newest = __reduce_max_sync(kAll, newest);
     __syncthreads();
-    const int64_t recent_from = static_cast<int64_t>(s_newest) - a.recent;
-    auto is_protected = [&](int stamp) { return stamp < a.sinks || stamp > recent_from; };
-    int mine = 0;
-    for (int i = tid; i < n; i += kPlanThreads) mine += is_protected(__ldg(stamps + i));
-    mine = __reduce_add_sync(0xFFFFFFFFu, mine);
-    if ((tid & 31) == 0) atomicAdd(&s_protected, mine);
-    __syncthreads();
-    // the budget cuts one class; of it `left` slots stay
-    const bool cut_protected = s_protected >= a.keep;
-    unsigned left = cut_protected ? a.keep : a.keep - s_protected;
+    if (lane == 0) atomicMax(&sh.newest, newest);
+    sync_all();
+    if (blocks > 1) {
+        if (tid < blocks) sh.got_i[tid] = *cluster.map_shared_rank(&sh.newest, tid);
+        __syncthreads();
+        newest = sh.got_i[0];
+        for (int k = 1; k < blocks; ++k) newest = max(newest, sh.got_i[k]);
+    } else {
+        newest = sh.newest;
+    }
+    const int64_t recent_from = static_cast<int64_t>(newest) - a.recent;
+    auto is_protected = [&](int st) { return st < a.sinks || st > recent_from; };
+    uint32_t protected_bits = 0;
+    if (kReg) {
+#pragma unroll
+        for (int j = 0; j < kHold; ++j) {
+            const int64_t i = base + 32 * j;
+            if (j < steps && i < n && is_protected(kHoldStamps ? stamp[kHoldStamps ? j : 0] : __ldg(stamps + i)))
+                protected_bits |= 1u << j;
+        }
+    }
+    // calls f(step, exists, key, protected) for each of the thread's slots,
+    // in order and with the whole warp
+    auto each = [&](auto f) {
+        if (kReg) {
+#pragma unroll
+            for (int j = 0; j < kHold; ++j)
+                if (j < steps) f(j, base + 32 * j < n, key[j], ((protected_bits >> j) & 1u) != 0);
+        } else {
+            for (int j = 0; j < steps; ++j) {
+                const int64_t i = base + 32 * j;
+                const bool in = i < n;
+                f(j, in, in ? score_key(__ldg(scores + i)) : 0u, in && is_protected(__ldg(stamps + i)));
+            }
+        }
+    };
+    // adds a block value over the cluster (after sync_all)
+    auto total_of = [&](const unsigned *mine, int slot, unsigned *before) {
+        if (blocks == 1) {
+            *before = 0;
+            return *mine;
+        }
+        if (tid < blocks) sh.got[slot][tid] = *cluster.map_shared_rank(const_cast<unsigned *>(mine), tid);
+        __syncthreads();
+        unsigned sum = 0, pre = 0;
+        for (int k = 0; k < blocks; ++k) {
+            if (k < rank) pre += sh.got[slot][k];
+            sum += sh.got[slot][k];
+        }
+        *before = pre;
+        return sum;
+    };
+    // finds the digit that holds the left-th largest value of histogram h
+    auto pick = [&](int h, unsigned left) {
+        const int bin = kBins - 2 - 2 * tid;  // the thread's two bins, from the top
+        unsigned hi = 0, lo = 0;
+        if (blocks > 1) {
+            for (int k = 0; k < blocks; ++k) {
+                const uint2 c = *reinterpret_cast<const uint2 *>(cluster.map_shared_rank(&sh.hist[h][bin], k));
+                lo += c.x;
+                hi += c.y;
+            }
+        } else {
+            const uint2 c = *reinterpret_cast<const uint2 *>(&sh.hist[h][bin]);
+            lo = c.x;
+            hi = c.y;
+        }
+        unsigned s = hi + lo;
+#pragma unroll
+        for (int x = 1; x < 32; x *= 2) {
+            const unsigned up = __shfl_up_sync(kAll, s, x);
+            if (lane >= x) s += up;
+        }
+        if (lane == 31) sh.scan[h][warp] = s;
+        __syncthreads();
+        // sum over the warps before this one
+        unsigned ws = lane < warp ? sh.scan[h][lane] : 0;
+        ws = __reduce_add_sync(kAll, ws);
+        const unsigned above = ws + s - hi - lo;
+        if (above < left && left <= above + hi) {
+            sh.digit = bin + 1;
+            sh.left = left - above;
+            sh.count = hi;
+        } else if (above + hi < left && left <= above + hi + lo) {
+            sh.digit = bin;
+            sh.left = left - above - hi;
+            sh.count = lo;
+        }
+        __syncthreads();
+    };
+    static_assert(kBins == 2 * kPlanThreads, "two bins per thread");
 
-    // key of the left-th largest of that class
-    unsigned prefix = 0;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-        for (int i = tid; i < n; i += kPlanThreads) {
-            if (is_protected(__ldg(stamps + i)) != cut_protected) continue;
-            const uint32_t key = score_key(__ldg(scores + i));
-            if (shift < 24 && (key >> (shift + 8)) != prefix) continue;
-            atomicAdd(&hist[(key >> shift) & 255u], 1u);
-        }
-        __syncthreads();
-        if (tid == 0) {
-            unsigned rest = left;
-            int d = 255;
-            while (d > 0 && hist[d] < rest) rest -= hist[d--];
-            s_prefix = (prefix << 8) | static_cast<unsigned>(d);
-            s_left = rest;
-        }
-        __syncthreads();
-        prefix = s_prefix;
-        left = s_left;
+    // first digit, over the slots that are not protected; how many are
+    unsigned mine = 0, unused;
+    each([&](int, bool in, uint32_t k, bool prot) {
+        if (in && !prot) atomicAdd(&sh.hist[0][k >> 21], 1u);
+        mine += in && prot;
+    });
+    mine = __reduce_add_sync(kAll, mine);
+    if (lane == 0 && mine) atomicAdd(&sh.in_class, mine);
+    sync_all();
+    const unsigned protect = total_of(&sh.in_class, 0, &unused);
+    const bool cut = protect >= static_cast<unsigned>(a.keep);  // does the budget cut the protected class
+    unsigned left = cut ? a.keep : a.keep - protect;
+    if (cut) {  // rare: more protected slots than the budget
+        each([&](int, bool in, uint32_t k, bool prot) {
+            if (in && prot) atomicAdd(&sh.hist[1][k >> 21], 1u);
+        });
+        sync_all();
     }
+    pick(cut ? 1 : 0, left);
+    uint32_t limit = sh.digit;
+    left = sh.left;
+    each([&](int, bool in, uint32_t k, bool prot) {
+        if (in && prot == cut && (k >> 21) == limit) atomicAdd(&sh.hist[2][(k >> 10) & 2047u], 1u);
+    });
+    sync_all();
+    pick(2, left);
+    limit = (limit << 11) | sh.digit;
+    left = sh.left;
+    each([&](int, bool in, uint32_t k, bool prot) {
+        if (in && prot == cut && (k >> 10) == limit) atomicAdd(&sh.hist[3][k & 1023u], 1u);
+    });
+    sync_all();
+    pick(3, left);
+    limit = (limit << 10) | sh.digit;
+    left = sh.left;
     // `left` of the slots with exactly this key stay, the lowest first
-    const uint32_t limit = prefix;
-    int32_t *moves = a.moves + 2 * row * a.max_moves;
-    unsigned ties_before = 0, holes_before = 0, movers_before = 0;
-    for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
-        const int i = i0 + tid;
-        bool in = i < n, cls = false, tie = false, above = false;
-        if (in) {
-            cls = is_protected(__ldg(stamps + i)) == cut_protected;
-            const uint32_t key = score_key(__ldg(scores + i));
-            tie = cls && key == limit;
-            above = cls ? key > limit : !cut_protected;  // protected slots stay when the others are cut
+    const bool all_ties = left == sh.count;
+    const unsigned below = (1u << lane) - 1;
+    unsigned tie0 = 0;  // ties in front of this warp's slots
+    if (!all_ties) {
+        unsigned c = 0;
+        each([&](int, bool in, uint32_t k, bool prot) { c += in && prot == cut && k == limit; });
+        c = __reduce_add_sync(kAll, c);
+        if (lane == 0) sh.warp_ties[warp] = c;
+        __syncthreads();
+        if (warp == 0) {
+            const unsigned s = __reduce_add_sync(kAll, sh.warp_ties[lane]);
+            if (lane == 0) sh.ties = s;
         }
-        uint64_t all;
-        const uint64_t tie_rank = block_scan(tie, &all, warp_sums) + ties_before;
-        ties_before += static_cast<unsigned>(all);
-        const bool stays = in && (above || (tie && tie_rank < left));
-        const bool hole = in && !stays && i < a.keep, mover = stays && i >= a.keep;
-        const uint64_t pre = block_scan(static_cast<uint64_t>(hole) | (static_cast<uint64_t>(mover) << 32), &all,
-                                        warp_sums);
-        if (hole) {
-            const unsigned at = holes_before + static_cast<unsigned>(pre);
-            if (at < a.max_moves) moves[2 * static_cast<int64_t>(at) + 1] = i;
-        }
-        if (mover) {
-            const unsigned at = movers_before + static_cast<unsigned>(pre >> 32);
-            if (at < a.max_moves) moves[2 * static_cast<int64_t>(at)] = i;
-        }
-        holes_before += static_cast<unsigned>(all);
-        movers_before += static_cast<unsigned>(all >> 32);
+        sync_all();
+        total_of(&sh.ties, 1, &tie0);
+        tie0 += __reduce_add_sync(kAll, lane < warp ? sh.warp_ties[lane] : 0u);
     }
-    if (tid == 0) a.counts[row] = static_cast<int>(movers_before);
+    // calls f(slot, hole, mover) in slot order
+    auto decide = [&](auto f) {
+        unsigned ties = tie0;
+        each([&](int j, bool in, uint32_t k, bool prot) {
+            const bool tie = in && prot == cut && k == limit;
+            bool stays = in && (prot == cut ? k > limit : !cut);  // with the others cut, protected slots stay
+            if (all_ties) {
+                stays = stays || tie;
+            } else {
+                const unsigned m = __ballot_sync(kAll, tie);
+                stays = stays || (tie && ties + __popc(m & below) < left);
+                ties += __popc(m);
+            }
+            const int64_t i = base + 32 * j;
+            f(static_cast<int>(i), in && !stays && i < a.keep, stays && i >= a.keep);
+        });
+    };
+    unsigned nh = 0, nm = 0;
+    decide([&](int, bool hole, bool mover) {
+        nh += hole;
+        nm += mover;
+    });
+    nh = __reduce_add_sync(kAll, nh);
+    nm = __reduce_add_sync(kAll, nm);
+    if (lane == 0) {
+        sh.warp_holes[warp] = nh;
+        sh.warp_movers[warp] = nm;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const unsigned h = __reduce_add_sync(kAll, sh.warp_holes[lane]);
+        const unsigned m = __reduce_add_sync(kAll, sh.warp_movers[lane]);
+        if (lane == 0) {
+            sh.holes = h;
+            sh.movers = m;
+        }
+    }
+    sync_all();
+    unsigned hole_at, mover_at;
+    total_of(&sh.holes, 2, &hole_at);
+    const unsigned movers = total_of(&sh.movers, 3, &mover_at);
+    hole_at += __reduce_add_sync(kAll, lane < warp ? sh.warp_holes[lane] : 0u);
+    mover_at += __reduce_add_sync(kAll, lane < warp ? sh.warp_movers[lane] : 0u);
+    int32_t *moves = a.moves + 2 * row * a.max_moves;
+    decide([&](int i, bool hole, bool mover) {
+        const unsigned h = __ballot_sync(kAll, hole), m = __ballot_sync(kAll, mover);
+        const int64_t at = hole ? hole_at + __popc(h & below) : mover_at + __popc(m & below);
+        if ((hole || mover) && at < a.max_moves) moves[2 * at + (hole ? 1 : 0)] = i;
+        hole_at += __popc(h);
+        mover_at += __popc(m);
+    });
+    if (tid == 0 && rank == 0) a.counts[row] = static_cast<int>(movers);
+    // no block leaves while another may still read its shared memory
+    if (blocks > 1) cluster.sync();
 }
 
 // Moves.  Sources lie at or behind `keep` and targets before it, so nothing
 // is read that another thread writes and applying a plan twice changes
-// nothing.  Bound by the bytes moved; one warp takes one move, half of it for
-// K and half for V.
+// nothing.  Bound by the bytes moved, once enough of them are in flight: a
+// warp takes kApplyBatch moves at a time, its lanes look up their pages side by
+// side, then all their rows are requested before the first is written.
 constexpr int kApplyThreads = 256;
+constexpr int kApplyBatch = 8;
 
+// Page of a slot, and its place in the page; -1 where it has no valid one.
 __device__ __forceinline__ int64_t page_of(const KvView &kv, const int32_t *table, int slot, int *off)
 {
     const int idx = kv.page_shift >= 0 ? slot >> kv.page_shift : slot / kv.page_size;
@@ -176,8 +347,8 @@ __global__ void __launch_bounds__(kApplyThreads) mbg_evict_apply_kernel(const __
 {
     pdl_trigger();
     pdl_wait();
-    const int64_t row = blockIdx.y + static_cast<int64_t>(blockIdx.z) * gridDim.y;
     const int h = blockIdx.y, b = blockIdx.z;
+    const int64_t row = static_cast<int64_t>(b) * gridDim.y + h;
     const KvView &kv = a.kv;
     if (a.lengths && h == 0 && blockIdx.x == 0 && threadIdx.x == 0) {
         const int n = a.lengths[b];
@@ -189,65 +360,98 @@ __global__ void __launch_bounds__(kApplyThreads) mbg_evict_apply_kernel(const __
         count = count < 0 ? 0 : static_cast<int>(a.max_moves);
     }
     const int32_t *table = kv.table + b * kv.table_stride;
+    const int2 *moves = reinterpret_cast<const int2 *>(a.moves) + row * a.max_moves;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int warps = kApplyThreads / 32;
-    for (int i = blockIdx.x * warps + warp; i < count; i += gridDim.x * warps) {
-        const int2 mv = __ldg(reinterpret_cast<const int2 *>(a.moves) + row * a.max_moves + i);
-        if (mv.x < 0 || mv.x >= kv.capacity || mv.y < 0 || mv.y >= kv.capacity) {
-            if (lane == 0) report_error(a.err, DEVERR_BAD_INDEX);
-            continue;
+    const int stride = gridDim.x * (kApplyThreads / 32) * kApplyBatch;
+    // lanes 0..15 move K, the others V
+    const bool is_v = lane >= 16;
+    uint16_t *pool = static_cast<uint16_t *>(is_v ? kv.v : kv.k);
+    const int64_t ps = is_v ? kv.vs_page : kv.ks_page, ts = is_v ? kv.vs_tok : kv.ks_tok,
+                  hs = is_v ? kv.vs_head : kv.ks_head;
+    for (int i0 = (blockIdx.x * (kApplyThreads / 32) + warp) * kApplyBatch; i0 < count; i0 += stride) {
+        // lanes 0..7: a move each
+        int sp = -1, tp = -1, so = 0, to = 0;
+        if (lane < kApplyBatch && i0 + lane < count) {
+            const int2 mv = __ldg(moves + i0 + lane);
+            const bool in = mv.x >= 0 && mv.x < kv.capacity && mv.y >= 0 && mv.y < kv.capacity;
+            if (in) {
+                sp = static_cast<int>(page_of(kv, table, mv.x, &so));
+                tp = static_cast<int>(page_of(kv, table, mv.y, &to));
+            }
+            if (sp < 0 || tp < 0) {
+                report_error(a.err, DEVERR_BAD_INDEX);
+                sp = -1;
+            } else {
+                if (a.scores) {
+                    float *sc = a.scores + row * kv.capacity;
+                    sc[mv.y] = sc[mv.x];
+                }
+                if (a.stamps) {
+                    int32_t *st = a.stamps + row * kv.capacity;
+                    st[mv.y] = st[mv.x];
+                }
+            }
         }
-        int so, to;
-        const int64_t sp = page_of(kv, table, mv.x, &so), tp = page_of(kv, table, mv.y, &to);
-        if (sp < 0 || tp < 0) {
-            if (lane == 0) report_error(a.err, DEVERR_BAD_INDEX);
-            continue;
+        const uint16_t *src[kApplyBatch];
+        uint16_t *dst[kApplyBatch];
+#pragma unroll
+        for (int k = 0; k < kApplyBatch; ++k) {
+            const int s_page = __shfl_sync(kAll, sp, k), s_off = __shfl_sync(kAll, so, k);
+            const int t_page = __shfl_sync(kAll, tp, k), t_off = __shfl_sync(kAll, to, k);
+            src[k] = s_page < 0 ? nullptr : pool + s_page * ps + s_off * ts + h * hs;
+            dst[k] = pool + t_page * ps + t_off * ts + h * hs;
         }
-        const bool is_v = lane >= 16;
-        uint16_t *pool = static_cast<uint16_t *>(is_v ? kv.v : kv.k);
-        const int64_t ps = is_v ? kv.vs_page : kv.ks_page, ts = is_v ? kv.vs_tok : kv.ks_tok,
-                      hs = is_v ? kv.vs_head : kv.ks_head;
-        const uint16_t *src = pool + sp * ps + so * ts + h * hs;
-        uint16_t *dst = pool + tp * ps + to * ts + h * hs;
         if (VEC) {
-            for (int d = (lane & 15) * 8; d < kv.dim; d += 128)
-                *reinterpret_cast<uint4 *>(dst + d) = *reinterpret_cast<const uint4 *>(src + d);
+            for (int d = (lane & 15) * 8; d < kv.dim; d += 128) {
+                uint4 v[kApplyBatch];
+#pragma unroll
+                for (int k = 0; k < kApplyBatch; ++k)
+                    if (src[k]) v[k] = *reinterpret_cast<const uint4 *>(src[k] + d);
+#pragma unroll
+                for (int k = 0; k < kApplyBatch; ++k)
+                    if (src[k]) *reinterpret_cast<uint4 *>(dst[k] + d) = v[k];
+            }
         } else {
-            for (int d = lane & 15; d < kv.dim; d += 16) dst[d] = src[d];
-        }
-        if (lane == 0 && a.scores) {
-            float *sc = a.scores + row * kv.capacity;
-            sc[mv.y] = sc[mv.x];
-        }
-        if (lane == 16 && a.stamps) {
-            int32_t *st = a.stamps + row * kv.capacity;
-            st[mv.y] = st[mv.x];
+#pragma unroll
+            for (int k = 0; k < kApplyBatch; ++k)
+                if (src[k])
+                    for (int d = lane & 15; d < kv.dim; d += 16) dst[k][d] = src[k][d];
         }
     }
 }
 
-template <typename... Params, typename... Args>
-cudaError_t launch_pdl(void (*fn)(Params...), dim3 grid, int threads, cudaStream_t s, const Args &...args)
+template <typename Args>
+cudaError_t launch_pdl(void (*fn)(Args), dim3 grid, int threads, int cluster, cudaStream_t s, const Args &args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fn, args...);
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, fn, args);
 }
 
 }  // namespace
 
-cudaError_t launch_evict_plan(const EvictArgs &a, int sm_count, cudaStream_t s)
+cudaError_t launch_evict_plan(const EvictArgs &a, cudaStream_t s)
 {
-    (void)sm_count;
-    return launch_pdl(mbg_evict_plan_kernel, dim3(static_cast<unsigned>(a.kv.batch) * a.kv.kv_heads), kPlanThreads, s,
-                      a);
+    // the smallest cluster whose threads hold a row of the cache's capacity
+    // four slots each, then more slots per thread, then rows of any length
+    const int64_t slots = static_cast<int64_t>(kPlanThreads) * kPlanShort, cap = a.kv.capacity;
+    int cluster = 1;
+    while (cluster < kPlanMaxCluster && cap > cluster * slots) cluster *= 2;
+    const dim3 grid(static_cast<unsigned>(a.kv.batch) * a.kv.kv_heads * cluster);
+    auto fn = cap <= cluster * slots ? mbg_evict_plan_kernel<kPlanShort>
+              : cap <= static_cast<int64_t>(cluster) * kPlanThreads * kPlanLong ? mbg_evict_plan_kernel<kPlanLong>
+                                                                                : mbg_evict_plan_kernel<0>;
+    return launch_pdl(fn, grid, kPlanThreads, cluster, s, a);
 }
 
 cudaError_t launch_evict_apply(const EvictApplyArgs &a, bool vec, int sm_count, cudaStream_t s)
@@ -255,12 +459,13 @@ cudaError_t launch_evict_apply(const EvictApplyArgs &a, bool vec, int sm_count, 
     // enough blocks per row to fill the GPU a few times over, and no more
     // than the moves there can be
     const int64_t rows = static_cast<int64_t>(a.kv.batch) * a.kv.kv_heads;
+    const int64_t per_block = kApplyThreads / 32 * kApplyBatch;
     int64_t x = (16ll * sm_count + rows - 1) / rows;
-    const int64_t most = (a.max_moves + kApplyThreads / 32 - 1) / (kApplyThreads / 32);
+    const int64_t most = (a.max_moves + per_block - 1) / per_block;
     if (x > most) x = most;
     if (x < 1) x = 1;
     const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(a.kv.kv_heads), static_cast<unsigned>(a.kv.batch));
-    return launch_pdl(vec ? mbg_evict_apply_kernel<true> : mbg_evict_apply_kernel<false>, grid, kApplyThreads, s, a);
+    return launch_pdl(vec ? mbg_evict_apply_kernel<true> : mbg_evict_apply_kernel<false>, grid, kApplyThreads, 1, s, a);
 }
 
 }  // namespace mbg

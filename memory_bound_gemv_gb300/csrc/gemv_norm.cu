@@ -13,8 +13,9 @@
 //
 // Bound by the bytes: y, x and the row-wise gate, scale and shift are read
 // once, out and h written once.  One block takes one row and keeps it in
-// registers, eight neighbouring elements per thread and step, all loads of
-// the row requested before the first reduction.
+// registers, eight neighbouring elements per thread and step; y and x are
+// requested before the first reduction, and what the row alone has of the
+// other operands is prefetched into L2.
 #include <stdint.h>
 
 #include "gemv_decode.h"
@@ -137,7 +138,51 @@ __device__ __forceinline__ void normalise(float (&x)[K][8], const int (&cnt)[K],
         for (int e = 0; e < 8; ++e) x[k][e] *= r;
 }
 
-template <int K, int MAXT, bool VEC>
+// 16 bytes that are read once.  Not the read-only path: out may be x, h may
+// be y.
+__device__ __forceinline__ uint4 ld_once16(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
+// Types of y and x known at compile time (16 bits or FP32) halve the
+// registers that their loads wait in.
+template <bool VEC, bool WIDE>
+struct Stream {
+    Raw r;
+    __device__ __forceinline__ void load(const void *base, int elem, int64_t at, int n)
+    {
+        if (!VEC) {
+            r = raw_load<false>(base, elem, at, n);
+        } else if (n > 0) {
+            if (WIDE) {
+                const unsigned char *p = reinterpret_cast<const unsigned char *>(static_cast<const float *>(base) + at);
+                r.a = ld_once16(p);
+                r.b = ld_once16(p + 16);
+            } else {
+                r.a = ld_once16(static_cast<const uint16_t *>(base) + at);
+            }
+        } else {
+            r.a = r.b = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+    __device__ __forceinline__ void floats(int elem, float (&x)[8]) const
+    {
+        if (VEC && !WIDE) {
+            const Raw t = {r.a, make_uint4(0u, 0u, 0u, 0u)};
+            raw_floats(t, elem == GEMV_ELEM_F16 ? GEMV_ELEM_F16 : GEMV_ELEM_BF16, x);
+        } else {
+            raw_floats(r, VEC ? GEMV_ELEM_F32 : elem, x);
+        }
+    }
+};
+
+template <int K, int MAXT, bool VEC, bool Y32, bool X32>
 __global__ void __launch_bounds__(MAXT) mbg_norm_kernel(const __grid_constant__ NormArgs a)
 {
     __shared__ Sums sums;
@@ -145,22 +190,29 @@ __global__ void __launch_bounds__(MAXT) mbg_norm_kernel(const __grid_constant__ 
     pdl_wait();
     const int64_t row = blockIdx.x;
     int at[K], cnt[K];
-    Raw y[K], r[K], g[K];
+    Stream<VEC, Y32> y[K];
+    Stream<VEC, X32> r[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         at[k] = (threadIdx.x + k * blockDim.x) * 8;
         cnt[k] = min(8, a.width - at[k]);
-        y[k] = raw_load<VEC>(a.y, a.y_e, row * a.y_s + at[k], cnt[k]);
+        y[k].load(a.y, a.y_e, row * a.y_s + at[k], cnt[k]);
     }
 #pragma unroll
-    for (int k = 0; k < K; ++k) r[k] = raw_load<VEC>(a.r, a.r_e, row * a.r_s + at[k], cnt[k]);
-    if (a.gate) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) g[k] = raw_load<VEC>(a.gate, a.gate_e, row * a.gate_s + at[k], cnt[k]);
+    for (int k = 0; k < K; ++k) r[k].load(a.r, a.r_e, row * a.r_s + at[k], cnt[k]);
+    if (VEC && threadIdx.x == 0) {
+        // operands of this row alone that are needed late: into L2 meanwhile
+        auto early = [&](const void *p, int e, int64_t stride) {
+            const int size = e == GEMV_ELEM_F32 ? 4 : 2;
+            if (p && stride) prefetch_l2(static_cast<const unsigned char *>(p) + row * stride * size, a.width * size);
+        };
+        early(a.gate, a.gate_e, a.gate_s);
+        early(a.pre_w, a.pre_w_e, a.pre_w_s);
+        early(a.pre_b, a.pre_b_e, a.pre_b_s);
     }
     float x[K][8];
 #pragma unroll
-    for (int k = 0; k < K; ++k) raw_floats(y[k], a.y_e, x[k]);
+    for (int k = 0; k < K; ++k) y[k].floats(a.y_e, x[k]);
     if (a.post) {
         normalise<K>(x, cnt, a, sums, 0);
         if (a.post_w) {
@@ -177,37 +229,27 @@ __global__ void __launch_bounds__(MAXT) mbg_norm_kernel(const __grid_constant__ 
     for (int k = 0; k < K; ++k) {
         float t[8];
         if (a.gate) {
-            raw_floats(g[k], a.gate_e, t);
+            raw_floats(raw_load<VEC>(a.gate, a.gate_e, row * a.gate_s + at[k], cnt[k]), a.gate_e, t);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[k][e] *= t[e];
         }
-        raw_floats(r[k], a.r_e, t);
+        r[k].floats(a.r_e, t);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[k][e] = e < cnt[k] ? fmaf(a.alpha, x[k][e], t[e]) : 0.f;
         store_as<VEC>(a.out, a.r_e, row * a.out_s + at[k], cnt[k], x[k]);
     }
     if (!a.h) return;
-    // the next norm's weights are requested before its reductions
-    Raw w[K], b[K];
-    if (a.pre_w) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) w[k] = raw_load<VEC>(a.pre_w, a.pre_w_e, row * a.pre_w_s + at[k], cnt[k]);
-    }
-    if (a.pre_b) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) b[k] = raw_load<VEC>(a.pre_b, a.pre_b_e, row * a.pre_b_s + at[k], cnt[k]);
-    }
     normalise<K>(x, cnt, a, sums, 2);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         float t[8];
         if (a.pre_w) {
-            raw_floats(w[k], a.pre_w_e, t);
+            raw_floats(raw_load<VEC>(a.pre_w, a.pre_w_e, row * a.pre_w_s + at[k], cnt[k]), a.pre_w_e, t);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[k][e] *= a.unit_offset ? 1.f + t[e] : t[e];
         }
         if (a.pre_b) {
-            raw_floats(b[k], a.pre_b_e, t);
+            raw_floats(raw_load<VEC>(a.pre_b, a.pre_b_e, row * a.pre_b_s + at[k], cnt[k]), a.pre_b_e, t);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[k][e] += t[e];
         }
@@ -333,22 +375,29 @@ cudaError_t launch_rows(void (*fn)(NormArgs), const NormArgs &a, int threads, cu
     return cudaLaunchKernelEx(&cfg, fn, a);
 }
 
-template <bool VEC>
-cudaError_t launch(const NormArgs &a, cudaStream_t s)
+template <bool VEC, bool Y32, bool X32>
+cudaError_t launch(const NormArgs &a, int sm_count, cudaStream_t s)
 {
     const int chunks = (a.width + 7) / 8;
     auto threads = [&](int k) { return ((chunks + k - 1) / k + 31) / 32 * 32; };
-    if (chunks <= 512) return launch_rows(mbg_norm_kernel<1, 512, VEC>, a, threads(1), s);
-    if (chunks <= 1024) return launch_rows(mbg_norm_kernel<2, 512, VEC>, a, threads(2), s);
-    if (chunks <= 2048) return launch_rows(mbg_norm_kernel<4, 512, VEC>, a, threads(4), s);
+    // Few rows: a row's latency counts, and more threads shorten it.  Many
+    // rows: small blocks with four steps per thread, so that several rows are
+    // in different phases on one SM and loads are always under way.
+    const bool many = a.rows > 2 * sm_count;
+    if (chunks <= (many ? 128 : 512)) return launch_rows(mbg_norm_kernel<1, 512, VEC, Y32, X32>, a, threads(1), s);
+    if (chunks <= (many ? 256 : 1024)) return launch_rows(mbg_norm_kernel<2, 512, VEC, Y32, X32>, a, threads(2), s);
+    if (chunks <= 2048) return launch_rows(mbg_norm_kernel<4, 512, VEC, Y32, X32>, a, threads(4), s);
     return launch_rows(mbg_norm_long_kernel<VEC>, a, kLongThreads, s);
 }
 
 }  // namespace
 
-cudaError_t launch_norm(const NormArgs &a, bool vec, cudaStream_t s)
+cudaError_t launch_norm(const NormArgs &a, bool vec, int sm_count, cudaStream_t s)
 {
-    return vec ? launch<true>(a, s) : launch<false>(a, s);
+    if (!vec) return launch<false, true, true>(a, sm_count, s);
+    const bool y32 = a.y_e == GEMV_ELEM_F32, x32 = a.r_e == GEMV_ELEM_F32;
+    if (y32) return x32 ? launch<true, true, true>(a, sm_count, s) : launch<true, true, false>(a, sm_count, s);
+    return x32 ? launch<true, false, true>(a, sm_count, s) : launch<true, false, false>(a, sm_count, s);
 }
 
 }  // namespace mbg

@@ -17,11 +17,12 @@ from __future__ import annotations
 import ctypes
 import math
 import struct
-from typing import List, Optional, Sequence
+from typing import Optional, Sequence
 
 import memory_bound_gemv_gb300 as _mbg
 
 ELEM_F32, ELEM_F16, ELEM_BF16 = 0, 1, 5
+_ATTN_COUNTER_BYTES = 8192  # GEMV_ATTN_COUNTER_BYTES
 NORM_LAYER, NORM_POST, NORM_UNIT_OFFSET = 1, 2, 4
 
 _elems = None
@@ -61,6 +62,8 @@ def _declare(L):
         f.restype = st
     L.gemv_attn_paged_workspace.argtypes = [vp, i32, i32]
     L.gemv_attn_paged_workspace.restype = ctypes.c_size_t
+    L.gemv_capture_id.argtypes = [vp]
+    L.gemv_capture_id.restype = ctypes.c_uint64
     return L
 
 
@@ -121,8 +124,9 @@ class PagedKV:
 
     The tensors are kept; their contents may change, their storage not.  The
     handle keeps a workspace per stream for ``gemv_attn_paged``: calls on one
-    stream use it in turn, calls on different streams have one each, and a call
-    that is being captured into a CUDA graph gets its own.
+    stream use it in turn, calls on different streams have one each, and so has
+    each CUDA graph that calls are captured into (for as long as the handle
+    lives).
     """
 
     def __init__(self, k, v, page_table, scores=None, stamps=None):
@@ -152,28 +156,21 @@ class PagedKV:
             _elem(k.dtype), self.page_size, self.max_pages, self.batch, self.kv_heads, self.head_dim)
         self._at = ctypes.addressof(self._s)
         self._workspaces = {}
-        self._captured: List = []
         self._lib = _mbg.lib()
 
     def _workspace(self, q_heads, weights, ptr, stream):
         torch = _mbg._torch()
-        key = (ptr, q_heads, weights)
-        if not torch.cuda.is_current_stream_capturing():
-            got = self._workspaces.get(key)
-            if got is not None:
-                return got
-        with _on(stream):
-            capturing = torch.cuda.is_current_stream_capturing()
-            if not capturing and key in self._workspaces:
-                return self._workspaces[key]
+        capture = 0
+        if stream is not None or torch.cuda.is_current_stream_capturing():
+            capture = self._lib.gemv_capture_id(ptr)
+        key = (ptr, capture, q_heads, weights)
+        got = self._workspaces.get(key)
+        if got is None:
             n = self._lib.gemv_attn_paged_workspace(self._at, q_heads, 1 if weights else 0)
-            t = torch.empty(max(n, 256), dtype=torch.uint8, device=self.device)
-            t[:4 * self.batch * q_heads + 256].zero_()  # the counters of its first part
-            got = (t.data_ptr(), t.numel(), t)
-        if capturing:
-            self._captured.append(t)  # the graph's own, as long as the handle lives
-        else:
-            self._workspaces[key] = got
+            with _on(stream):
+                t = torch.empty(max(n, 256), dtype=torch.uint8, device=self.device)
+                t[:_ATTN_COUNTER_BYTES + 4 * self.batch * q_heads].zero_()
+            got = self._workspaces[key] = (t.data_ptr(), t.numel(), t)
         return got
 
 
