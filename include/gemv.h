@@ -379,9 +379,9 @@ gemv_status_t gemv_q8_rowscale_run_variant(int variant, const int8_t *A, const u
  * all arithmetic is FP32.  Lengths, slots and page numbers live on the device
  * and are checked there: one out of range is skipped and reported as
  * GEMV_ERR_BAD_INDEX by gemv_get_device_error, nothing is read or written
- * outside the given buffers.  16-byte aligned rows of a multiple of eight
- * elements take vector loads; any other layout gives the same results more
- * slowly.  Every kernel waits for the one before it on the stream, and may be
+ * outside the given buffers.  Rows of a multiple of eight elements, aligned
+ * to 16 bytes (FP32: 32), take vector loads; any other layout gives the same
+ * results more slowly.  Every kernel waits for the one before it on the stream, and may be
  * captured into a CUDA graph; grids do not depend on the lengths.  The pages
  * stop at the GEMV and the softmax; these calls have no counterpart there.
  */
@@ -427,10 +427,20 @@ typedef struct {
  * stream.  One workspace serves one call at a time.
  */
 #define GEMV_ATTN_COUNTER_BYTES 8192
-gemv_status_t gemv_attn_paged(const gemv_kv_t *kv, const void *q, const int64_t q_stride[2],
-                              const int32_t *lengths, void *out, const int64_t out_stride[2],
-                              int q_heads, float scale, int window, float *lse, float *scores_out,
-                              void *workspace, size_t workspace_bytes, void *stream);
+typedef struct {
+    void *data;
+    int64_t stride[2]; /* between tokens (or sequences) and between heads */
+} gemv_heads_t;
+typedef struct {
+    gemv_heads_t q, out;
+    const int32_t *lengths;
+    float *lse, *scores_out;
+    void *workspace;
+    size_t workspace_bytes;
+    int32_t q_heads, window;
+    float scale;
+} gemv_attn_t;
+gemv_status_t gemv_attn_paged(const gemv_kv_t *kv, const gemv_attn_t *args, void *stream);
 /* Bytes of workspace (0 where the arguments are not valid).  weights: whether
  * scores_out will be given; capacity-sized scratch comes with it. */
 size_t gemv_attn_paged_workspace(const gemv_kv_t *kv, int q_heads, int weights);
@@ -479,14 +489,16 @@ gemv_status_t gemv_kv_evict_apply(const gemv_kv_t *kv, const int32_t *moves, int
  * slot).  No two tokens of a call may share a slot.  axis: uint8 [rot / 2],
  * values below axes; rot even, at most head_dim.
  */
-gemv_status_t gemv_rope_append(const gemv_kv_t *kv, int src_elem, const void *q,
-                               const int64_t q_stride[2], const void *k, const int64_t k_stride[2],
-                               const void *v, const int64_t v_stride[2], void *q_out,
-                               const int64_t q_out_stride[2], int tokens, int q_heads,
-                               const int32_t *positions, int64_t pos_stride, int axes,
-                               const int32_t *slots, const int32_t *seq, const int32_t *stamps,
-                               const uint64_t *turns, const uint8_t *axis, int rot, int pairs,
-                               void *stream);
+typedef struct {
+    gemv_heads_t q, k, v, q_out;
+    const int32_t *positions;
+    int64_t pos_stride;
+    const int32_t *slots, *seq, *stamps;
+    const uint64_t *turns;
+    const uint8_t *axis;
+    int32_t src_elem, tokens, q_heads, axes, rot, pairs;
+} gemv_rope_t;
+gemv_status_t gemv_rope_append(const gemv_kv_t *kv, const gemv_rope_t *args, void *stream);
 
 /*
  * The norms around a block with its gate and the residual:

@@ -31,18 +31,21 @@
 // product run, and the next V after that: about 8 KB in flight per warp at a
 // head size of 128.
 //
-// Split over the length: the rows (sequence x cached head) are cut into blocks
-// of NW * 16 tokens; all blocks of the call are numbered and each CTA takes an
-// equal share of consecutive ones, whatever the lengths (they are read on the
-// device, so a captured graph serves any lengths).  A row inside one CTA's
-// share is written at once; otherwise each CTA leaves (O, m, l) in the
-// workspace and the last to arrive joins them, always in the same order, so
-// results do not depend on the order of arrival.
+// Split over the length: the rows (sequence x cached head) are cut into tiles
+// of 16 tokens; all tiles of the call are numbered and each CTA takes an equal
+// share of consecutive ones, whatever the lengths (they are read on the
+// device, so a captured graph serves any lengths).  A share's border that
+// falls close to a row's end moves there, so that short rows are not cut.  A
+// row inside one CTA's share is written at once; otherwise each CTA leaves
+// (O, m, l) in the workspace and the last to arrive joins them, always in the
+// same order, so results do not depend on the order of arrival.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "gemv_decode.h"
 #include "gemv_device.cuh"
@@ -50,11 +53,7 @@
 namespace mbg {
 namespace attn {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr unsigned kFull = 0xFFFFFFFFu;
-// CTAs whose parts of a row are joined first, before the groups are.
-constexpr int kGroupCtas = 16;
 
 template <typename T>
 struct Mma;
@@ -141,11 +140,10 @@ __device__ __forceinline__ uint4 load8(const uint16_t *p, int left)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// First tile of 16 tokens, number of tiles and of blocks of a sequence.
+// The tokens of a sequence that are attended to, and their tiles of 16.
 struct RowSpan {
     int first, len;         // tokens [first, len)
     int tile0, tiles;       // 16-token tiles, tile0 = first / 16
-    __device__ __forceinline__ int blocks() const { return (tiles + kWarps - 1) / kWarps; }
 };
 
 __device__ __forceinline__ RowSpan row_span(const AttnArgs &a, int b)
@@ -161,31 +159,40 @@ __device__ __forceinline__ RowSpan row_span(const AttnArgs &a, int b)
     return r;
 }
 
-// Page of one token, and its place in the page; page -1 where there is none.
-struct TokenPlace {
-    int page, off;
+// Where a tile's tokens are; page -1: nowhere.  WHOLE (pages of a multiple of
+// 16 tokens, so that a tile lies in one): the page, the place of its first
+// token there, and which of its 16 tokens count: lo <= r < hi.  Otherwise
+// lanes 0..15, and again 16..31, hold the page and place of one token each.
+struct TilePlace {
+    int page, off, lo, hi;
 };
 
-__device__ __forceinline__ TokenPlace place_of(const KvView &kv, const int32_t *table, int slot, bool wanted,
-                                               unsigned int *err)
+template <bool WHOLE>
+__device__ __forceinline__ TilePlace place_of(const KvView &kv, const int32_t *table, int tile, bool wanted, int first,
+                                              int len, unsigned int *err)
 {
-    TokenPlace p;
-    p.page = -1;
-    p.off = 0;
-    if (wanted) {
+    TilePlace p = {-1, 0, 0, 0};
+    const int slot = tile * 16 + (WHOLE ? 0 : threadIdx.x & 15);
+    if (wanted && (WHOLE || (slot >= first && slot < len))) {
         const int idx = kv.page_shift >= 0 ? slot >> kv.page_shift : slot / kv.page_size;
         p.off = slot - idx * kv.page_size;
-        const int page = __ldg(table + idx);
-        if (page >= 0 && page < kv.num_pages)
-            p.page = page;
-        else
+        p.page = __ldg(table + idx);
+        if (p.page < 0 || p.page >= kv.num_pages) {
+            p.page = -1;
             report_error(err, DEVERR_BAD_INDEX);
+        } else if (WHOLE) {
+            p.lo = first - slot;
+            p.hi = len - slot;
+        }
     }
     return p;
 }
 
-template <typename T, int DC, int NT, bool VEC>
+template <typename T, int DC, int NT, int NW, bool VEC, bool WHOLE>
 struct Kernel {
+    static constexpr int kWarps = NW, kThreads = NW * 32;
+    // CTAs whose parts of a row are joined first, before the groups are
+    static constexpr int kGroupCtas = 4 * NW;
     static constexpr int kHeads = 8 * NT;           // query heads of one tile
     static constexpr int kRegs = NT * DC * 16;      // O values per thread
     static constexpr int kQWords = NT * DC * 8;     // Q words per thread
@@ -194,7 +201,28 @@ struct Kernel {
     static constexpr bool kQInSmem = NT * DC > 2;
 
     // parts joined at once: a group, or the groups of a row
-    static constexpr int kMaxParts = kAttnMaxCtas / kGroupCtas;
+    static constexpr int kMaxParts = kAttnMaxCtas / kGroupCtas > kGroupCtas ? kAttnMaxCtas / kGroupCtas : kGroupCtas;
+
+    // This CTA's part of the call's work.  A row of n tiles counts `lead` + n:
+    // starting a row costs about that many tiles.  CTA c's share ends where CTA
+    // c + 1's begins, at total * c / ctas -- or at an end of the row there, if
+    // that is at most `near` tiles away.
+    struct Share {
+        int64_t total, x0, x1;
+        int ctas, cta, near, lead;
+    };
+    // The row that is looked at next; `before` counts what lies before its
+    // sequence, per cached head.
+    struct Cursor {
+        int64_t before;
+        int b, hk;
+    };
+    // Tiles [t0, t1) of a row; none are left when t0 = t1.
+    struct Segment {
+        int64_t r0;             // where the row begins
+        int b, hk, t0, t1;
+        int first, len, tile0, tiles;
+    };
 
     struct Shared {
         float o[kWarps][kRegs][32];
@@ -204,8 +232,10 @@ struct Kernel {
         float part_m[kMaxParts][kHeads];
         float part_l[kMaxParts][kHeads];
         int scan[kWarps];
-        int pick[2];
         int last;
+        Share share;
+        Cursor cursor;
+        Segment seg[3];   // the present one, the next, and the one being looked up
     };
 
     struct Row {
@@ -275,23 +305,63 @@ struct Kernel {
         }
     }
 
-    // Blocks [k0, k1) of a row.
-    static __device__ void segment(const AttnArgs &a, Shared &sh, const RowSpan &span, const Row &r, int k0, int k1,
-                                   int64_t unit0, int64_t units, int ctas, int cta)
+    static __device__ __forceinline__ int64_t border(const Share &w, int64_t x, int64_t r0, int64_t r1)
+    {
+        const int64_t d0 = x - r0 - w.lead, d1 = r1 - x;
+        if (d0 <= d1) return d0 <= w.near ? r0 : x;
+        return d1 <= w.near ? r1 : x;
+    }
+
+    // Looks up the CTA's next segment (one thread).
+    static __device__ void advance(const AttnArgs &a, const Share &w, Cursor &at, Segment &out)
+    {
+        const int hks = a.kv.kv_heads * a.head_tiles;
+        while (at.b < a.kv.batch) {  // (the last share ends with the last row)
+            const RowSpan span = row_span(a, at.b);
+            const int n = span.tiles, cost = n + w.lead;
+            if (n == 0) {
+                ++at.b;
+                continue;
+            }
+            const int hk = at.hk, b = at.b;
+            const int64_t r0 = at.before * hks + static_cast<int64_t>(hk) * cost, r1 = r0 + cost;
+            const int64_t from = w.x0 > r0 ? border(w, w.x0, r0, r1) : r0;
+            const int64_t to = w.x1 >= r1 ? r1 : border(w, w.x1, r0, r1);
+            if (++at.hk == hks) {
+                at.hk = 0;
+                ++at.b;
+                at.before += cost;
+            }
+            if (w.x1 <= r1) at.b = a.kv.batch;
+            if (from < to) {
+                out.r0 = r0;
+                out.b = b;
+                out.hk = hk;
+                out.t0 = from == r0 ? 0 : static_cast<int>(from - r0 - w.lead);
+                out.t1 = static_cast<int>(to - r0 - w.lead);
+                out.first = span.first;
+                out.len = span.len;
+                out.tile0 = span.tile0;
+                out.tiles = n;
+                if (out.t0 < out.t1) return;
+            }
+        }
+        out.b = out.hk = out.t0 = out.t1 = 0;
+    }
+
+    // The CTA's segments, one after another.  A warp requests the first tiles
+    // of its next segment before it joins the present one, so that the loads
+    // never pause between rows.
+    static __device__ void stream(const AttnArgs &a, Shared &sh)
     {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         const int g = lane >> 2, t = lane & 3;
         const KvView &kv = a.kv;
-        const int h = r.hk / a.head_tiles;
-        const uint16_t *kbase = static_cast<const uint16_t *>(kv.k) + h * kv.ks_head;
-        const uint16_t *vbase = static_cast<const uint16_t *>(kv.v) + h * kv.vs_head;
-        const int32_t *table = kv.table + r.b * kv.table_stride;
 
         uint4 q[kQInSmem ? 1 : NT][kQInSmem ? 1 : 2 * DC];
-        {
+        auto load_q = [&](const Row &r) {
             const uint16_t *qb = static_cast<const uint16_t *>(a.q) + r.b * a.q_sb;
             if (kQInSmem) {
-                __syncthreads();
                 for (int w = warp; w < NT * 2 * DC; w += kWarps) {
                     const int nt = w / (2 * DC), j = w - nt * 2 * DC;
                     const int head = nt * 8 + g, d = j * 32 + t * 8;
@@ -302,7 +372,6 @@ struct Kernel {
                     sh.q[4 * w + 2][lane] = v.z;
                     sh.q[4 * w + 3][lane] = v.w;
                 }
-                __syncthreads();
             } else {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -315,213 +384,251 @@ struct Kernel {
                                 : make_uint4(0, 0, 0, 0);
                     }
             }
-        }
-
-        float o[NT * DC * 4][4];
-        float m[NT][2], l[NT][2];
-#pragma unroll
-        for (int i = 0; i < NT * DC * 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            m[nt][0] = m[nt][1] = -INFINITY;
-            l[nt][0] = l[nt][1] = 0.f;
-        }
-
-        uint4 kx[2][2 * DC], vx[DC][4];
-        const int tile_end = min(span.tiles, k1 * kWarps);
-        // lanes 0..15 (and again 16..31) hold the places of the tile's tokens
-        auto place = [&](int tile) {
-            const int slot = (span.tile0 + tile) * 16 + (lane & 15);
-            return place_of(kv, table, slot, tile < tile_end && slot >= span.first && slot < span.len, a.err);
         };
-        auto load_k = [&](const TokenPlace &p) {
+        uint4 kx[2][2 * DC], vx[DC][4];
+        auto place = [&](const Segment &s, int tile) {
+            return place_of<WHOLE>(kv, kv.table + s.b * kv.table_stride, s.tile0 + tile, tile < s.t1, s.first, s.len,
+                                   a.err);
+        };
+        // does token r of a tile count, and its place relative to p's
+        auto token = [&](const TilePlace &p, int r, int *page, int *off) {
+            if (WHOLE) {
+                *page = p.page;
+                *off = p.off + r;
+                return r >= p.lo && r < p.hi;
+            }
+            *page = __shfl_sync(kFull, p.page, r);
+            *off = __shfl_sync(kFull, p.off, r);
+            return *page >= 0;
+        };
+        auto load_k = [&](const TilePlace &p, int h) {
+            const uint16_t *base = static_cast<const uint16_t *>(kv.k) + h * kv.ks_head;
+            if (WHOLE) base += p.page * kv.ks_page + p.off * kv.ks_tok;
 #pragma unroll
             for (int rr = 0; rr < 2; ++rr) {
-                const int page = __shfl_sync(kFull, p.page, g + 8 * rr);
-                const int off = __shfl_sync(kFull, p.off, g + 8 * rr);
-                const uint16_t *row = kbase + page * kv.ks_page + off * kv.ks_tok;
+                int page, off;
+                const bool live = token(p, g + 8 * rr, &page, &off);
+                const uint16_t *row = WHOLE ? base + (g + 8 * rr) * kv.ks_tok : base + page * kv.ks_page + off * kv.ks_tok;
 #pragma unroll
                 for (int j = 0; j < 2 * DC; ++j) {
                     const int d = j * 32 + t * 8;
-                    kx[rr][j] = (page >= 0 && d < kv.dim) ? load8<VEC>(row + d, kv.dim - d) : make_uint4(0, 0, 0, 0);
+                    kx[rr][j] = (live && d < kv.dim) ? load8<VEC>(row + d, kv.dim - d) : make_uint4(0, 0, 0, 0);
                 }
             }
         };
-        auto load_v = [&](const TokenPlace &p) {
+        auto load_v = [&](const TilePlace &p, int h) {
+            const uint16_t *base = static_cast<const uint16_t *>(kv.v) + h * kv.vs_head;
+            if (WHOLE) base += p.page * kv.vs_page + p.off * kv.vs_tok;
 #pragma unroll
             for (int rr = 0; rr < 4; ++rr) {
                 const int tok = 2 * t + (rr & 1) + 8 * (rr >> 1);
-                const int page = __shfl_sync(kFull, p.page, tok);
-                const int off = __shfl_sync(kFull, p.off, tok);
-                const uint16_t *row = vbase + page * kv.vs_page + off * kv.vs_tok;
+                int page, off;
+                const bool live = token(p, tok, &page, &off);
+                const uint16_t *row = WHOLE ? base + tok * kv.vs_tok : base + page * kv.vs_page + off * kv.vs_tok;
 #pragma unroll
                 for (int c = 0; c < DC; ++c) {
                     const int d = c * 64 + g * 8;
-                    vx[c][rr] = (page >= 0 && d < kv.dim) ? load8<VEC>(row + d, kv.dim - d) : make_uint4(0, 0, 0, 0);
+                    vx[c][rr] = (live && d < kv.dim) ? load8<VEC>(row + d, kv.dim - d) : make_uint4(0, 0, 0, 0);
                 }
             }
         };
 
-        int tile = k0 * kWarps + warp;
-        TokenPlace here = place(tile), next = place(tile + kWarps);
-        load_k(here);
-        load_v(here);
-        for (; tile < tile_end; tile += kWarps) {
-            // S^T = K Q^T
-            float s[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float odd[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
-#pragma unroll
-                for (int j = 0; j < 2 * DC; ++j) {
-                    uint4 b;
-                    if (kQInSmem) {
-                        const int w = 4 * (nt * 2 * DC + j);
-                        b = make_uint4(sh.q[kQInSmem ? w : 0][lane], sh.q[kQInSmem ? w + 1 : 0][lane],
-                                       sh.q[kQInSmem ? w + 2 : 0][lane], sh.q[kQInSmem ? w + 3 : 0][lane]);
-                    } else {
-                        b = q[kQInSmem ? 0 : nt][kQInSmem ? 0 : j];
-                    }
-                    Mma<T>::run(s[nt], kx[0][j].x, kx[1][j].x, kx[0][j].y, kx[1][j].y, b.x, b.y);
-                    Mma<T>::run(odd, kx[0][j].z, kx[1][j].z, kx[0][j].w, kx[1][j].w, b.z, b.w);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[nt][e] += odd[e];
+        TilePlace here = {-1, 0, 0, 0}, next = here;
+        bool first_segment = true;
+        bool primed = false;  // the present segment's first tiles are already requested
+        if (sh.seg[0].t0 < sh.seg[0].t1) load_q(row_of(a, sh.seg[0].b, sh.seg[0].hk));
+        for (int i = 0;; i = i == 2 ? 0 : i + 1) {
+            const Segment seg = sh.seg[i];
+            const Segment &after = sh.seg[i == 2 ? 0 : i + 1];
+            if (seg.t0 >= seg.t1) break;
+            const int h = seg.hk / a.head_tiles;
+            int tile = seg.t0 + warp;
+            if (!primed) {
+                here = place(seg, tile);
+                load_k(here, h);
+                load_v(here, h);
             }
-            const TokenPlace old = here;
-            here = next;
-            load_k(here);
-            next = place(tile + 2 * kWarps);
+            if (first_segment) {  // the second segment is looked up while the first loads are under way
+                if (threadIdx.x == 0) advance(a, sh.share, sh.cursor, sh.seg[1]);
+                __syncthreads();
+                first_segment = false;
+            }
+            if (threadIdx.x == 0) advance(a, sh.share, sh.cursor, sh.seg[i == 0 ? 2 : i - 1]);
+            // this warp's tiles of the segment
+            int left = (seg.t1 - tile + kWarps - 1) / kWarps;
+            if (!primed || left == 1) next = left > 1 ? place(seg, tile + kWarps) : place(after, after.t0 + warp);
+            primed = left > 0;
+            const int h_after = after.hk / a.head_tiles;
 
-            // scale, mask, running maximum
-            const bool live0 = __shfl_sync(kFull, old.page, g) >= 0;
-            const bool live1 = __shfl_sync(kFull, old.page, g + 8) >= 0;
+            float o[NT * DC * 4][4];
+            float m[NT][2], l[NT][2];
+#pragma unroll
+            for (int k = 0; k < NT * DC * 4; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[k][e] = 0.f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const bool live = e < 2 ? live0 : live1;
-                    s[nt][e] = live ? s[nt][e] * a.scale_log2 : -INFINITY;
-                }
+                m[nt][0] = m[nt][1] = -INFINITY;
+                l[nt][0] = l[nt][1] = 0.f;
             }
-            if (a.scores_out) {
-                const int64_t row = static_cast<int64_t>(r.b) * kv.kv_heads * a.head_tiles + r.hk;
-                const int slot = (span.tile0 + tile) * 16 + g;
+            for (; left > 0; --left, tile += kWarps) {
+                // S^T = K Q^T
+                float s[NT][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt) {
+                    float odd[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 2 * DC; ++j) {
+                        uint4 b;
+                        if (kQInSmem) {
+                            const int w = 4 * (nt * 2 * DC + j);
+                            b = make_uint4(sh.q[kQInSmem ? w : 0][lane], sh.q[kQInSmem ? w + 1 : 0][lane],
+                                           sh.q[kQInSmem ? w + 2 : 0][lane], sh.q[kQInSmem ? w + 3 : 0][lane]);
+                        } else {
+                            b = q[kQInSmem ? 0 : nt][kQInSmem ? 0 : j];
+                        }
+                        Mma<T>::run(s[nt], kx[0][j].x, kx[1][j].x, kx[0][j].y, kx[1][j].y, b.x, b.y);
+                        Mma<T>::run(odd, kx[0][j].z, kx[1][j].z, kx[0][j].w, kx[1][j].w, b.z, b.w);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[nt][e] += odd[e];
+                }
+                const TilePlace old = here;
+                here = next;
+                load_k(here, left > 1 ? h : h_after);
+                next = left > 2 ? place(seg, tile + 2 * kWarps) : place(after, after.t0 + warp + (2 - left) * kWarps);
+
+                // scale, mask, running maximum
+                int page, off;
+                const bool live0 = token(old, g, &page, &off), live1 = token(old, g + 8, &page, &off);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const bool live = e < 2 ? live0 : live1;
+                        s[nt][e] = live ? s[nt][e] * a.scale_log2 : -INFINITY;
+                    }
+                }
+                if (a.scores_out) {
+                    const int64_t row = static_cast<int64_t>(seg.b) * kv.kv_heads * a.head_tiles + seg.hk;
+                    const int slot = (seg.tile0 + tile) * 16 + g;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int rr = 0; rr < 2; ++rr) {
+                            const int head = nt * 8 + 2 * t, at = slot + 8 * rr;
+                            if (head < a.logit_heads && at < seg.len && at >= seg.first)
+                                *reinterpret_cast<float2 *>(a.logits + (row * kv.capacity + at) * a.logit_heads + head) =
+                                    make_float2(s[nt][2 * rr], s[nt][2 * rr + 1]);
+                        }
+                }
+                uint32_t phi[NT][2], plo[NT][2];
+                bool grew = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float top[2] = {fmaxf(s[nt][0], s[nt][2]), fmaxf(s[nt][1], s[nt][3])};
+#pragma unroll
+                    for (int x = 4; x < 32; x *= 2) {
+                        top[0] = fmaxf(top[0], __shfl_xor_sync(kFull, top[0], x));
+                        top[1] = fmaxf(top[1], __shfl_xor_sync(kFull, top[1], x));
+                    }
+                    float fix[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float m2 = fmaxf(m[nt][e], top[e]);
+                        grew = grew || m2 != m[nt][e];
+                        fix[e] = exp2_from(m[nt][e], m2);
+                        m[nt][e] = m2;
+                        const float p0 = exp2_from(s[nt][e], m2), p1 = exp2_from(s[nt][e + 2], m2);
+                        l[nt][e] = l[nt][e] * fix[e] + (p0 + p1);
+                        s[nt][e] = p0;
+                        s[nt][e + 2] = p1;
+                    }
+                    if (__any_sync(kFull, grew)) {
+#pragma unroll
+                        for (int i = 0; i < DC * 4; ++i)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[nt * DC * 4 + i][e] *= fix[e & 1];
+                    }
 #pragma unroll
                     for (int rr = 0; rr < 2; ++rr) {
-                        const int head = nt * 8 + 2 * t, at = slot + 8 * rr;
-                        if (head < a.logit_heads && at < span.len && at >= span.first)
-                            *reinterpret_cast<float2 *>(a.logits + (row * kv.capacity + at) * a.logit_heads + head) =
-                                make_float2(s[nt][2 * rr], s[nt][2 * rr + 1]);
+                        const uint32_t hi = Mma<T>::pack(s[nt][2 * rr], s[nt][2 * rr + 1]);
+                        const float2 back = Mma<T>::unpack(hi);
+                        const uint32_t lo = Mma<T>::pack(s[nt][2 * rr] - back.x, s[nt][2 * rr + 1] - back.y);
+                        phi[nt][rr] = transpose8x8(hi);
+                        plo[nt][rr] = transpose8x8(lo);
                     }
-            }
-            uint32_t phi[NT][2], plo[NT][2];
-            bool grew = false;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float top[2] = {fmaxf(s[nt][0], s[nt][2]), fmaxf(s[nt][1], s[nt][3])};
-#pragma unroll
-                for (int x = 4; x < 32; x *= 2) {
-                    top[0] = fmaxf(top[0], __shfl_xor_sync(kFull, top[0], x));
-                    top[1] = fmaxf(top[1], __shfl_xor_sync(kFull, top[1], x));
                 }
-                float fix[2];
+                // O^T += V^T P^T
+#pragma unroll
+                for (int c = 0; c < DC; ++c) {
+                    const uint32_t *w[4] = {reinterpret_cast<const uint32_t *>(&vx[c][0]),
+                                            reinterpret_cast<const uint32_t *>(&vx[c][1]),
+                                            reinterpret_cast<const uint32_t *>(&vx[c][2]),
+                                            reinterpret_cast<const uint32_t *>(&vx[c][3])};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t a0 = __byte_perm(w[0][i], w[1][i], 0x5410);
+                        const uint32_t a1 = __byte_perm(w[0][i], w[1][i], 0x7632);
+                        const uint32_t a2 = __byte_perm(w[2][i], w[3][i], 0x5410);
+                        const uint32_t a3 = __byte_perm(w[2][i], w[3][i], 0x7632);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            Mma<T>::run(o[(nt * DC + c) * 4 + i], a0, a1, a2, a3, phi[nt][0], phi[nt][1]);
+                            Mma<T>::run(o[(nt * DC + c) * 4 + i], a0, a1, a2, a3, plo[nt][0], plo[nt][1]);
+                        }
+                    }
+                }
+                load_v(here, left > 1 ? h : h_after);
+            }
+
+            if (!kQInSmem && after.t0 < after.t1) load_q(row_of(a, after.b, after.hk));
+
+            // join the warps
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float m2 = fmaxf(m[nt][e], top[e]);
-                    grew = grew || m2 != m[nt][e];
-                    fix[e] = exp2_from(m[nt][e], m2);
-                    m[nt][e] = m2;
-                    const float p0 = exp2_from(s[nt][e], m2), p1 = exp2_from(s[nt][e + 2], m2);
-                    l[nt][e] = l[nt][e] * fix[e] + (p0 + p1);
-                    s[nt][e] = p0;
-                    s[nt][e + 2] = p1;
-                }
-                if (__any_sync(kFull, grew)) {
 #pragma unroll
-                    for (int i = 0; i < DC * 4; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[nt * DC * 4 + i][e] *= fix[e & 1];
-                }
-#pragma unroll
-                for (int rr = 0; rr < 2; ++rr) {
-                    const uint32_t hi = Mma<T>::pack(s[nt][2 * rr], s[nt][2 * rr + 1]);
-                    const float2 back = Mma<T>::unpack(hi);
-                    const uint32_t lo = Mma<T>::pack(s[nt][2 * rr] - back.x, s[nt][2 * rr + 1] - back.y);
-                    phi[nt][rr] = transpose8x8(hi);
-                    plo[nt][rr] = transpose8x8(lo);
-                }
-            }
-            // O^T += V^T P^T
-#pragma unroll
-            for (int c = 0; c < DC; ++c) {
-                const uint32_t *w[4] = {reinterpret_cast<const uint32_t *>(&vx[c][0]),
-                                        reinterpret_cast<const uint32_t *>(&vx[c][1]),
-                                        reinterpret_cast<const uint32_t *>(&vx[c][2]),
-                                        reinterpret_cast<const uint32_t *>(&vx[c][3])};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t a0 = __byte_perm(w[0][i], w[1][i], 0x5410);
-                    const uint32_t a1 = __byte_perm(w[0][i], w[1][i], 0x7632);
-                    const uint32_t a2 = __byte_perm(w[2][i], w[3][i], 0x5410);
-                    const uint32_t a3 = __byte_perm(w[2][i], w[3][i], 0x7632);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        Mma<T>::run(o[(nt * DC + c) * 4 + i], a0, a1, a2, a3, phi[nt][0], phi[nt][1]);
-                        Mma<T>::run(o[(nt * DC + c) * 4 + i], a0, a1, a2, a3, plo[nt][0], plo[nt][1]);
+                    for (int x = 4; x < 32; x *= 2) l[nt][e] += __shfl_xor_sync(kFull, l[nt][e], x);
+                    if (g == 0) {
+                        sh.m[warp][nt * 8 + 2 * t + e] = m[nt][e];
+                        sh.l[warp][nt * 8 + 2 * t + e] = l[nt][e];
                     }
                 }
-            }
-            load_v(here);
+            __syncthreads();
+            float top[NT][2], sum[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int head = nt * 8 + 2 * t + e;
+                    float mm = -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sh.m[w][head]);
+                    float ll = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) ll += sh.l[w][head] * exp2_from(sh.m[w][head], mm);
+                    const float fix = exp2_from(m[nt][e], mm);
+#pragma unroll
+                    for (int i = 0; i < DC * 4; ++i) {
+                        sh.o[warp][(nt * DC * 4 + i) * 4 + e][lane] = o[nt * DC * 4 + i][e] * fix;
+                        sh.o[warp][(nt * DC * 4 + i) * 4 + e + 2][lane] = o[nt * DC * 4 + i][e + 2] * fix;
+                    }
+                    top[nt][e] = mm;
+                    sum[nt][e] = ll;
+                }
+            if (kQInSmem && after.t0 < after.t1) load_q(row_of(a, after.b, after.hk));
+            __syncthreads();
+
+            const bool whole = seg.t0 == 0 && seg.t1 == seg.tiles;
+            const Row r = row_of(a, seg.b, seg.hk);
+            finish(a, sh, r, whole ? -1 : 2 * sh.share.cta + (seg.t0 == 0 ? 1 : 0), top, sum);
+            if (!whole) join(a, sh, seg, r);
+            __syncthreads();  // shared memory is free again
         }
-
-        // join the warps
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                for (int x = 4; x < 32; x *= 2) l[nt][e] += __shfl_xor_sync(kFull, l[nt][e], x);
-                if (g == 0) {
-                    sh.m[warp][nt * 8 + 2 * t + e] = m[nt][e];
-                    sh.l[warp][nt * 8 + 2 * t + e] = l[nt][e];
-                }
-            }
-        __syncthreads();
-        float top[NT][2], sum[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int head = nt * 8 + 2 * t + e;
-                float mm = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sh.m[w][head]);
-                float ll = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) ll += sh.l[w][head] * exp2_from(sh.m[w][head], mm);
-                const float fix = exp2_from(m[nt][e], mm);
-#pragma unroll
-                for (int i = 0; i < DC * 4; ++i) {
-                    sh.o[warp][(nt * DC * 4 + i) * 4 + e][lane] = o[nt * DC * 4 + i][e] * fix;
-                    sh.o[warp][(nt * DC * 4 + i) * 4 + e + 2][lane] = o[nt * DC * 4 + i][e + 2] * fix;
-                }
-                top[nt][e] = mm;
-                sum[nt][e] = ll;
-            }
-        __syncthreads();
-
-        const bool whole = k0 == 0 && k1 == span.blocks();
-        const int slot = 2 * cta + (k0 == 0 ? 1 : 0);
-        finish(a, sh, r, whole ? -1 : slot, top, sum);
-        if (!whole) join(a, sh, span, r, unit0, units, ctas, cta);
-        __syncthreads();  // shared memory is free again
     }
 
     // Sums the warps' O in shared memory (relative to `top`) and writes the
@@ -568,26 +675,22 @@ struct Kernel {
         }
     }
 
-    // CTA whose share holds a block: the largest c with units * c / ctas <= u.
-    static __device__ __forceinline__ int cta_of(int64_t u, int64_t units, int ctas)
-    {
-        return static_cast<int>(((u + 1) * ctas - 1) / units);
-    }
-
     // Has every one of `expected` CTAs arrived at this counter?  True for the
     // last, for which the others' parts are visible then.
     static __device__ __forceinline__ bool last_of(Shared &sh, unsigned int *counter, int expected)
     {
-        __threadfence();
+        // the barrier orders the block's writes before thread 0's fence, which
+        // is cumulative
         __syncthreads();
         if (threadIdx.x == 0) {
-            sh.last = atomicAdd(counter, 1u) == static_cast<unsigned>(expected - 1);
-            if (sh.last) *counter = 0;  // ready for the next call
+            __threadfence();
+            const bool last = atomicAdd(counter, 1u) == static_cast<unsigned>(expected - 1);
+            if (last) *counter = 0;  // ready for the next call
+            __threadfence();
+            sh.last = last;
         }
         __syncthreads();
-        if (!sh.last) return false;
-        __threadfence();
-        return true;
+        return sh.last != 0;
     }
 
     // Joins n parts, the i-th at slot_of(i), into the row's output (into < 0) or
@@ -621,7 +724,6 @@ struct Kernel {
         float v[kRegs];
 #pragma unroll
         for (int i = 0; i < kRegs; ++i) v[i] = 0.f;
-#pragma unroll 2
         for (int p = warp; p < n; p += kWarps) {
             const float *part = a.part + slot_of(p) * a.part_stride;
             float4 x[kRegs / 4];
@@ -647,15 +749,23 @@ struct Kernel {
     // A row that several CTAs share.  The last CTA of each group of kGroupCtas
     // to arrive joins the group's parts, the last group to arrive joins the
     // groups: one CTA joining all parts of a long row one after another took
-    // 20 us and more of latency, two levels take about 3.  unit0: number of the
-    // row's first block.
-    static __device__ void join(const AttnArgs &a, Shared &sh, const RowSpan &span, const Row &r, int64_t unit0,
-                                int64_t units, int ctas, int cta)
+    // 20 us and more of latency.
+    static __device__ void join(const AttnArgs &a, Shared &sh, const Segment &seg, const Row &r)
     {
-        const int c0 = cta_of(unit0, units, ctas), n = cta_of(unit0 + span.blocks() - 1, units, ctas) - c0 + 1;
+        // borders inside the row: the first and the last CTA that begins in it
+        const Share &w = sh.share;
+        const int64_t tile0 = seg.r0 + w.lead, r1 = tile0 + seg.tiles;
+        const int first_in = static_cast<int>(((tile0 + w.near + 1) * w.ctas + w.total - 1) / w.total);
+        const int last_in = static_cast<int>(((r1 - w.near) * w.ctas - 1) / w.total);
+        const int c0 = first_in - 1, n = last_in - c0 + 1;
+        if (c0 < 0 || c0 > w.cta || last_in < w.cta || last_in >= w.ctas) {
+            // lengths that changed during the call: no part is where it should be
+            if (threadIdx.x == 0) report_error(a.err, DEVERR_BAD_INDEX);
+            return;
+        }
         // a CTA's part that begins a row is its second slot, any other its first
         auto slot = [&](int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); };
-        const int first = (cta - c0) / kGroupCtas * kGroupCtas, members = min(kGroupCtas, n - first);
+        const int first = (w.cta - c0) / kGroupCtas * kGroupCtas, members = min(kGroupCtas, n - first);
         const int groups = (n + kGroupCtas - 1) / kGroupCtas;
         if (!last_of(sh, a.arrived_group + slot(first), members)) return;
         if (groups == 1) {
@@ -700,90 +810,110 @@ struct Kernel {
         pdl_wait();
         empty_rows(a);
         const int hks = a.kv.kv_heads * a.head_tiles;
-        // blocks per cached head over all sequences
-        int64_t blocks = 0;
-        for (int b0 = 0; b0 < a.kv.batch; b0 += kThreads) {
-            const int b = b0 + threadIdx.x;
-            int all;
-            scan(sh, b < a.kv.batch ? row_span(a, b).blocks() : 0, &all);
-            blocks += all;
+        // up to 32 sequences: one per lane, every warp for itself
+        const bool few = a.kv.batch <= 32;
+        const int step = few ? 32 : kThreads, own = few ? threadIdx.x & 31 : threadIdx.x;
+        // tiles and rows per cached head over all sequences
+        int64_t tiles = 0, rows = 0;
+        for (int b0 = 0; b0 < a.kv.batch; b0 += step) {
+            const int n = b0 + own < a.kv.batch ? row_span(a, b0 + own).tiles : 0;
+            if (few) {
+                tiles = __reduce_add_sync(kFull, n);
+                rows = __popc(__ballot_sync(kFull, n > 0));
+            } else {
+                int all;
+                scan(sh, n, &all);
+                tiles += all;
+                rows += __syncthreads_count(n > 0);
+            }
         }
-        const int64_t units = blocks * hks;
-        if (units == 0) return;
-        // no CTA without a block, so that a row's CTAs are all that lie between
-        // its first and its last
-        const int ctas = static_cast<int>(min(units, static_cast<int64_t>(gridDim.x)));
-        const int cta = blockIdx.x;
-        if (cta >= ctas) return;
-        int64_t u = units * cta / ctas;
-        const int64_t u_end = units * (cta + 1) / ctas;
-        // the sequence that holds block u
+        // a row is not cut into shares of less than a.least rounds of a block's
+        // warps: a part more to join costs more than a round
+        const int64_t most = max(tiles * hks / (a.least * kWarps), rows * hks);
+        const int ctas = static_cast<int>(min(most, static_cast<int64_t>(gridDim.x))), cta = blockIdx.x;
+        if (tiles == 0 || cta >= ctas) return;
+        const int64_t total = (tiles + rows * a.lead) * hks;
+        const int64_t x0 = total * cta / ctas;
+        if (threadIdx.x == 0) {
+            sh.share.total = total;
+            sh.share.x0 = x0;
+            sh.share.x1 = total * (cta + 1) / ctas;
+            sh.share.ctas = ctas;
+            sh.share.cta = cta;
+            sh.share.near = a.near * kWarps;
+            sh.share.lead = a.lead;
+            sh.cursor.b = a.kv.batch;
+            sh.seg[0].t0 = sh.seg[0].t1 = 0;
+        }
+        __syncthreads();
+        // the sequence that holds x0
         int64_t before = 0;
-        int b = 0;
-        for (int b0 = 0; b0 < a.kv.batch; b0 += kThreads) {
-            const int mine = b0 + threadIdx.x;
-            const int n = mine < a.kv.batch ? row_span(a, mine).blocks() : 0;
-            int all;
-            const int pre = scan(sh, n, &all);
-            if (u < (before + all) * hks) {
-                if (n > 0 && (before + pre) * hks <= u && u < (before + pre + n) * hks) {
-                    sh.pick[0] = mine;
-                    sh.pick[1] = pre;
+        for (int b0 = 0; b0 < a.kv.batch && x0 >= before * hks; b0 += step) {
+            const int b = b0 + own, n = b < a.kv.batch ? row_span(a, b).tiles : 0, cost = n > 0 ? n + a.lead : 0;
+            int all, pre;
+            if (few) {
+                pre = cost;
+#pragma unroll
+                for (int x = 1; x < 32; x *= 2) {
+                    const int up = __shfl_up_sync(kFull, pre, x);
+                    if (own >= x) pre += up;
                 }
-                __syncthreads();
-                b = sh.pick[0];
-                before += sh.pick[1];
-                break;
+                pre -= cost;
+                all = 0;
+            } else {
+                pre = scan(sh, cost, &all);
+            }
+            const int64_t from = (before + pre) * hks;
+            if (n > 0 && from <= x0 && x0 < from + static_cast<int64_t>(cost) * hks && (!few || threadIdx.x < 32)) {
+                sh.cursor.before = before + pre;
+                sh.cursor.b = b;
+                sh.cursor.hk = static_cast<int>((x0 - from) / cost);
+                advance(a, sh.share, sh.cursor, sh.seg[0]);
             }
             before += all;
         }
-        while (u < u_end) {
-            const RowSpan span = row_span(a, b);
-            const int n = span.blocks();
-            if (n == 0) {
-                ++b;
-                continue;
-            }
-            const int64_t base = before * hks;
-            int64_t rem = u - base;
-            while (rem < static_cast<int64_t>(n) * hks && u < u_end) {
-                const int hk = static_cast<int>(rem / n), k0 = static_cast<int>(rem - static_cast<int64_t>(hk) * n);
-                const int k1 = static_cast<int>(min(static_cast<int64_t>(n), k0 + (u_end - u)));
-                segment(a, sh, span, row_of(a, b, hk), k0, k1, base + static_cast<int64_t>(hk) * n, units, ctas, cta);
-                u += k1 - k0;
-                rem += k1 - k0;
-            }
-            before += n;
-            ++b;
-        }
+        __syncthreads();
+        stream(a, sh);
     }
 };
 
+// Warps that fit on an SM by their registers (168 at a head size of 128), as
+// one block or as blocks of four.
 template <int DC, int NT>
-constexpr int ctas_per_sm()
+constexpr int warps_per_sm()
 {
-    return DC * NT <= 1 ? 4 : DC * NT <= 2 ? 3 : 2;
+    return DC * NT <= 1 ? 16 : DC * NT <= 2 ? 12 : 8;
 }
 
-template <typename T, int DC, int NT, bool VEC>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm<DC, NT>()) mbg_attn_kernel(const __grid_constant__ AttnArgs a)
+template <typename T, int DC, int NT, int NW, bool VEC, bool WHOLE>
+__global__ void __launch_bounds__(NW * 32, warps_per_sm<DC, NT>() / NW)
+    mbg_attn_kernel(const __grid_constant__ AttnArgs a)
 {
     extern __shared__ __align__(16) unsigned char raw[];
-    Kernel<T, DC, NT, VEC>::run(a, *reinterpret_cast<typename Kernel<T, DC, NT, VEC>::Shared *>(raw));
+    using K = Kernel<T, DC, NT, NW, VEC, WHOLE>;
+    K::run(a, *reinterpret_cast<typename K::Shared *>(raw));
 }
 
-template <typename T, int DC, int NT, bool VEC>
-cudaError_t launch_one(const AttnArgs &a, cudaStream_t s)
+template <typename T, int DC, int NT, int NW, bool VEC, bool WHOLE>
+cudaError_t launch_one(const AttnArgs &a, int sm_count, cudaStream_t s)
 {
-    constexpr int smem = sizeof(typename Kernel<T, DC, NT, VEC>::Shared);
-    auto fn = mbg_attn_kernel<T, DC, NT, VEC>;
+    constexpr int smem = sizeof(typename Kernel<T, DC, NT, NW, VEC, WHOLE>::Shared);
+    auto fn = mbg_attn_kernel<T, DC, NT, NW, VEC, WHOLE>;
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        static std::atomic<uint64_t> ready{0};  // a bit per device
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess && !(ready.load(std::memory_order_relaxed) >> (dev & 63) & 1)) {
+            e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e == cudaSuccess) ready.fetch_or(uint64_t{1} << (dev & 63), std::memory_order_relaxed);
+        }
         if (e != cudaSuccess) return e;
     }
+    int ctas = sm_count * (warps_per_sm<DC, NT>() / NW);
+    if (ctas > kAttnMaxCtas) ctas = kAttnMaxCtas;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.ctas));
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(NW * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -794,24 +924,36 @@ cudaError_t launch_one(const AttnArgs &a, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, fn, a);
 }
 
+// big: one block of all an SM's warps instead of blocks of four.
+template <typename T, int DC, int NT>
+cudaError_t launch_shape(const AttnArgs &a, bool big, int sm_count, cudaStream_t s)
+{
+    constexpr int kBig = warps_per_sm<DC, NT>();
+    if (a.kv.page_size % 16 == 0)
+        return big ? launch_one<T, DC, NT, kBig, true, true>(a, sm_count, s)
+                   : launch_one<T, DC, NT, 4, true, true>(a, sm_count, s);
+    return big ? launch_one<T, DC, NT, kBig, true, false>(a, sm_count, s)
+               : launch_one<T, DC, NT, 4, true, false>(a, sm_count, s);
+}
+
 template <typename T>
-cudaError_t launch(const AttnArgs &a, bool vec, int nt, cudaStream_t s)
+cudaError_t launch(const AttnArgs &a, bool vec, int nt, bool big, int sm_count, cudaStream_t s)
 {
     const int dc = (a.kv.dim + 63) / 64;
-    if (vec && nt == 2) return dc == 1 ? launch_one<T, 1, 2, true>(a, s) : launch_one<T, 2, 2, true>(a, s);
+    if (vec && nt == 2) return dc == 1 ? launch_shape<T, 1, 2>(a, big, sm_count, s) : launch_shape<T, 2, 2>(a, big, sm_count, s);
     if (vec) {
         switch (dc) {
-        case 1: return launch_one<T, 1, 1, true>(a, s);
-        case 2: return launch_one<T, 2, 1, true>(a, s);
-        case 3: return launch_one<T, 3, 1, true>(a, s);
-        default: return launch_one<T, 4, 1, true>(a, s);
+        case 1: return launch_shape<T, 1, 1>(a, big, sm_count, s);
+        case 2: return launch_shape<T, 2, 1>(a, big, sm_count, s);
+        case 3: return launch_shape<T, 3, 1>(a, big, sm_count, s);
+        default: return launch_shape<T, 4, 1>(a, big, sm_count, s);
         }
     }
     switch (dc) {
-    case 1: return launch_one<T, 1, 1, false>(a, s);
-    case 2: return launch_one<T, 2, 1, false>(a, s);
-    case 3: return launch_one<T, 3, 1, false>(a, s);
-    default: return launch_one<T, 4, 1, false>(a, s);
+    case 1: return launch_one<T, 1, 1, 4, false, false>(a, sm_count, s);
+    case 2: return launch_one<T, 2, 1, 4, false, false>(a, sm_count, s);
+    case 3: return launch_one<T, 3, 1, 4, false, false>(a, sm_count, s);
+    default: return launch_one<T, 4, 1, 4, false, false>(a, sm_count, s);
     }
 }
 

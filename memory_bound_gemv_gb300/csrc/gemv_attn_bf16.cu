@@ -3,9 +3,9 @@
 
 namespace mbg {
 
-cudaError_t launch_attn_bf16(const AttnArgs &a, bool vec, int nt, cudaStream_t s)
+cudaError_t launch_attn_bf16(const AttnArgs &a, bool vec, int nt, bool big, int sm_count, cudaStream_t s)
 {
-    return attn::launch<__nv_bfloat16>(a, vec, nt, s);
+    return attn::launch<__nv_bfloat16>(a, vec, nt, big, sm_count, s);
 }
 
 }  // namespace mbg

@@ -4,15 +4,9 @@
 
 namespace mbg {
 
-cudaError_t launch_attn_f16(const AttnArgs &a, bool vec, int nt, cudaStream_t s)
+cudaError_t launch_attn_f16(const AttnArgs &a, bool vec, int nt, bool big, int sm_count, cudaStream_t s)
 {
-    return attn::launch<__half>(a, vec, nt, s);
-}
-
-int attn_ctas_per_sm(int dim, int nt)
-{
-    const int dc = (dim + 63) / 64;
-    return dc * nt <= 1 ? 4 : dc * nt <= 2 ? 3 : 2;
+    return attn::launch<__half>(a, vec, nt, big, sm_count, s);
 }
 
 // scores_out[b, h, t] = scores_in[b, h, t] + sum over the group's query heads

@@ -55,14 +55,15 @@ struct AttnArgs {
     float *row_lse;             // same rows x 8 * NT heads: log2 of the softmax denominator
     float *logits;              // [rows][capacity][logit_heads], log2 units; weights only
     int logit_heads;
-    int ctas;
+    int near, least;            // rounds of a block's warps: see attn::Kernel
+    int lead;                   // tiles
 };
 
-// Launches for one cache type; vec: 16-byte loads are possible.
-cudaError_t launch_attn_f16(const AttnArgs &a, bool vec, int nt, cudaStream_t s);
-cudaError_t launch_attn_bf16(const AttnArgs &a, bool vec, int nt, cudaStream_t s);
+// Launches for one cache type; vec: 16-byte loads are possible; big: one block
+// per SM instead of several small ones.
+cudaError_t launch_attn_f16(const AttnArgs &a, bool vec, int nt, bool big, int sm_count, cudaStream_t s);
+cudaError_t launch_attn_bf16(const AttnArgs &a, bool vec, int nt, bool big, int sm_count, cudaStream_t s);
 cudaError_t launch_attn_weights(const AttnArgs &a, int nt, cudaStream_t s);
-int attn_ctas_per_sm(int dim, int nt);
 constexpr int kAttnMaxCtas = 1024;
 
 struct EvictArgs {

@@ -16,6 +16,8 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 bool is_elem(int e) { return e == GEMV_ELEM_F32 || e == GEMV_ELEM_F16 || e == GEMV_ELEM_BF16; }
 int elem_bytes(int e) { return e == GEMV_ELEM_F32 ? 4 : 2; }
+// Alignment of eight elements that are moved at once.
+int vec_bytes(int e) { return 8 * elem_bytes(e); }
 
 bool mult8(const int64_t *stride, int n)
 {
@@ -23,6 +25,8 @@ bool mult8(const int64_t *stride, int n)
         if (stride[i] % 8) return false;
     return true;
 }
+
+bool negative(const gemv_heads_t &h) { return h.stride[0] < 0 || h.stride[1] < 0; }
 
 // Checks a cache and fills the kernels' view of it.
 gemv_status_t view_of(const gemv_kv_t *kv, KvView *v, bool need_data = true)
@@ -133,47 +137,47 @@ uint64_t gemv_capture_id(void *stream)
     return status == cudaStreamCaptureStatusActive ? id : 0;
 }
 
-gemv_status_t gemv_attn_paged(const gemv_kv_t *kv, const void *q, const int64_t q_stride[2],
-                              const int32_t *lengths, void *out, const int64_t out_stride[2], int q_heads,
-                              float scale, int window, float *lse, float *scores_out, void *workspace,
-                              size_t workspace_bytes, void *stream)
+gemv_status_t gemv_attn_paged(const gemv_kv_t *kv, const gemv_attn_t *args, void *stream)
 {
     AttnArgs a{};
     gemv_status_t st = view_of(kv, &a.kv);
     if (st != GEMV_OK) return st;
-    if (!q_stride || !out_stride || q_heads < 1 || q_heads % a.kv.kv_heads || window < 0 || q_stride[0] < 0 ||
-        q_stride[1] < 0 || out_stride[0] < 0 || out_stride[1] < 0)
+    if (!args) return GEMV_ERR_INVALID_VALUE;
+    const gemv_heads_t &q = args->q, &out = args->out;
+    const int q_heads = args->q_heads;
+    if (q_heads < 1 || q_heads % a.kv.kv_heads || args->window < 0 || negative(q) || negative(out))
         return GEMV_ERR_INVALID_VALUE;
     if (a.kv.batch == 0) return GEMV_OK;
-    if (!q || !lengths || !out || !workspace || (scores_out && !kv->scores)) return GEMV_ERR_INVALID_VALUE;
-    if (!aligned(q, 2) || !aligned(out, 2) || !aligned(lengths, 4) || !aligned(lse, 4) || !aligned(scores_out, 4) ||
-        !aligned(workspace, 256))
+    if (!q.data || !args->lengths || !out.data || !args->workspace || (args->scores_out && !kv->scores))
+        return GEMV_ERR_INVALID_VALUE;
+    if (!aligned(q.data, 2) || !aligned(out.data, 2) || !aligned(args->lengths, 4) || !aligned(args->lse, 4) ||
+        !aligned(args->scores_out, 4) || !aligned(args->workspace, 256))
         return GEMV_ERR_MISALIGNED;
     const int group = q_heads / a.kv.kv_heads;
-    const bool vec = cache_vec(kv) && aligned(q, 16) && mult8(q_stride, 2);
+    const bool vec = cache_vec(kv) && aligned(q.data, 16) && mult8(q.stride, 2);
     const int nt = head_tile(a.kv.dim, group, vec);
-    const AttnPlan p = attn_plan(a.kv, group, nt, scores_out != nullptr);
+    const AttnPlan p = attn_plan(a.kv, group, nt, args->scores_out != nullptr);
     if (p.rows > INT_MAX) return GEMV_ERR_UNSUPPORTED;
-    if (workspace_bytes < p.total) return GEMV_ERR_INVALID_VALUE;
+    if (args->workspace_bytes < p.total) return GEMV_ERR_INVALID_VALUE;
     DecodeDevice dev;
     if (!decode_device(&dev)) return GEMV_ERR_CUDA;
-    a.q = q;
-    a.q_sb = q_stride[0];
-    a.q_sh = q_stride[1];
-    a.out = out;
-    a.o_sb = out_stride[0];
-    a.o_sh = out_stride[1];
-    a.lengths = lengths;
-    a.lse = lse;
+    a.q = q.data;
+    a.q_sb = q.stride[0];
+    a.q_sh = q.stride[1];
+    a.out = out.data;
+    a.o_sb = out.stride[0];
+    a.o_sh = out.stride[1];
+    a.lengths = args->lengths;
+    a.lse = args->lse;
     a.scores_in = kv->scores;
-    a.scores_out = scores_out;
+    a.scores_out = args->scores_out;
     a.q_heads = q_heads;
     a.group = group;
     a.head_tiles = p.head_tiles;
-    a.window = window;
-    a.scale_log2 = scale * 1.4426950408889634f;
+    a.window = args->window;
+    a.scale_log2 = args->scale * 1.4426950408889634f;
     a.err = dev.status;
-    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    unsigned char *ws = static_cast<unsigned char *>(args->workspace);
     a.arrived_group = reinterpret_cast<unsigned int *>(ws);
     a.arrived = reinterpret_cast<unsigned int *>(ws + p.arrived);
     a.part = reinterpret_cast<float *>(ws + p.part);
@@ -181,11 +185,22 @@ gemv_status_t gemv_attn_paged(const gemv_kv_t *kv, const void *q, const int64_t 
     a.row_lse = reinterpret_cast<float *>(ws + p.row_lse);
     a.logits = reinterpret_cast<float *>(ws + p.logits);
     a.logit_heads = p.logit_heads;
-    a.ctas = dev.sm_count * attn_ctas_per_sm(a.kv.dim, nt);
-    if (a.ctas > kAttnMaxCtas) a.ctas = kAttnMaxCtas;
+    // Few rows: one block of all an SM's warps, a third of the parts to join
+    // (8 rows of 131072 tokens of 128: 90.0 us, with blocks of four warps 93.2).
+    // Many rows: blocks of four warps, one joins while the others load (384
+    // rows of 1000 tokens: 42.7 us against 48.6).
+    const bool big = vec && p.rows <= dev.sm_count / 2;
+    // A cut costs a join of some 4 us, about as much as two rounds of a small
+    // block's four tiles: rows are not cut finer, nor that close to their
+    // ends (384 rows of 256 tokens: 15.9 us, one round for both 23.9).  A row's
+    // beginning counts like `lead` tiles (48 ragged sequences of up to 6000
+    // tokens: 123 us with 4, 134 us with none).
+    a.near = a.least = big ? 1 : 2;
+    a.lead = big ? 16 : 8;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = kv->elem == GEMV_ELEM_F16 ? launch_attn_f16(a, vec, nt, s) : launch_attn_bf16(a, vec, nt, s);
-    if (e == cudaSuccess && scores_out && a.kv.capacity > 0) e = launch_attn_weights(a, nt, s);
+    cudaError_t e = kv->elem == GEMV_ELEM_F16 ? launch_attn_f16(a, vec, nt, big, dev.sm_count, s)
+                                              : launch_attn_bf16(a, vec, nt, big, dev.sm_count, s);
+    if (e == cudaSuccess && a.scores_out && a.kv.capacity > 0) e = launch_attn_weights(a, nt, s);
     return e == cudaSuccess ? GEMV_OK : decode_cuda_fail(e, GEMV_ERR_LAUNCH);
 }
 
@@ -241,60 +256,51 @@ gemv_status_t gemv_kv_evict_apply(const gemv_kv_t *kv, const int32_t *moves, int
     return e == cudaSuccess ? GEMV_OK : decode_cuda_fail(e, GEMV_ERR_LAUNCH);
 }
 
-gemv_status_t gemv_rope_append(const gemv_kv_t *kv, int src_elem, const void *q, const int64_t q_stride[2],
-                               const void *k, const int64_t k_stride[2], const void *v, const int64_t v_stride[2],
-                               void *q_out, const int64_t q_out_stride[2], int tokens, int q_heads,
-                               const int32_t *positions, int64_t pos_stride, int axes, const int32_t *slots,
-                               const int32_t *seq, const int32_t *stamps, const uint64_t *turns, const uint8_t *axis,
-                               int rot, int pairs, void *stream)
+gemv_status_t gemv_rope_append(const gemv_kv_t *kv, const gemv_rope_t *r, void *stream)
 {
     RopeArgs a{};
     const gemv_status_t st = view_of(kv, &a.kv);
     if (st != GEMV_OK) return st;
-    if (!is_elem(src_elem) || !q_stride || !k_stride || !v_stride || !q_out_stride || tokens < 0 || q_heads < 0 ||
-        axes < 1 || rot < 0 || rot % 2 || rot > a.kv.dim || pos_stride < 0)
+    if (!r || !is_elem(r->src_elem) || r->tokens < 0 || r->q_heads < 0 || r->axes < 1 || r->rot < 0 || r->rot % 2 ||
+        r->rot > a.kv.dim || r->pos_stride < 0)
         return GEMV_ERR_INVALID_VALUE;
-    for (const int64_t *s : {q_stride, k_stride, v_stride, q_out_stride})
-        if (s[0] < 0 || s[1] < 0) return GEMV_ERR_INVALID_VALUE;
-    if (!seq && tokens > a.kv.batch) return GEMV_ERR_INVALID_VALUE;
-    if (tokens == 0) return GEMV_OK;
-    if ((q_heads > 0 && (!q || !q_out)) || !k || !v || !positions || !slots || (rot > 0 && (!turns || !axis)) ||
-        !kv->k || !kv->v)
+    if (negative(r->q) || negative(r->k) || negative(r->v) || negative(r->q_out)) return GEMV_ERR_INVALID_VALUE;
+    if (!r->seq && r->tokens > a.kv.batch) return GEMV_ERR_INVALID_VALUE;
+    if (r->tokens == 0) return GEMV_OK;
+    if ((r->q_heads > 0 && (!r->q.data || !r->q_out.data)) || !r->k.data || !r->v.data || !r->positions || !r->slots ||
+        (r->rot > 0 && (!r->turns || !r->axis)) || !kv->k || !kv->v)
         return GEMV_ERR_INVALID_VALUE;
-    const int eb = elem_bytes(src_elem);
-    if (!aligned(q, eb) || !aligned(k, eb) || !aligned(v, eb) || !aligned(q_out, 2) || !aligned(positions, 4) ||
-        !aligned(slots, 4) || !aligned(seq, 4) || !aligned(stamps, 4) || !aligned(turns, 8))
+    const int eb = elem_bytes(r->src_elem);
+    if (!aligned(r->q.data, eb) || !aligned(r->k.data, eb) || !aligned(r->v.data, eb) || !aligned(r->q_out.data, 2) ||
+        !aligned(r->positions, 4) || !aligned(r->slots, 4) || !aligned(r->seq, 4) || !aligned(r->stamps, 4) ||
+        !aligned(r->turns, 8))
         return GEMV_ERR_MISALIGNED;
     DecodeDevice dev;
     if (!decode_device(&dev)) return GEMV_ERR_CUDA;
-    a.q = q;
-    a.k = k;
-    a.v = v;
-    a.src_elem = src_elem;
+    a.q = r->q.data, a.q_st = r->q.stride[0], a.q_sh = r->q.stride[1];
+    a.k = r->k.data, a.k_st = r->k.stride[0], a.k_sh = r->k.stride[1];
+    a.v = r->v.data, a.v_st = r->v.stride[0], a.v_sh = r->v.stride[1];
+    a.q_out = r->q_out.data, a.qo_st = r->q_out.stride[0], a.qo_sh = r->q_out.stride[1];
+    a.src_elem = r->src_elem;
     a.dst_elem = kv->elem;
-    a.q_st = q_stride[0], a.q_sh = q_stride[1];
-    a.k_st = k_stride[0], a.k_sh = k_stride[1];
-    a.v_st = v_stride[0], a.v_sh = v_stride[1];
-    a.q_out = q_out;
-    a.qo_st = q_out_stride[0], a.qo_sh = q_out_stride[1];
-    a.positions = positions;
-    a.pos_stride = pos_stride;
-    a.slots = slots;
-    a.seq = seq;
-    a.stamps = stamps;
+    a.positions = r->positions;
+    a.pos_stride = r->pos_stride;
+    a.slots = r->slots;
+    a.seq = r->seq;
+    a.stamps = r->stamps;
     a.scores_cache = kv->scores;
     a.stamps_cache = kv->stamps;
-    a.turns = turns;
-    a.axis = axis;
-    a.tokens = tokens;
-    a.q_heads = q_heads;
-    a.rot = rot;
-    a.axes = axes;
-    a.pairs = pairs != 0;
+    a.turns = r->turns;
+    a.axis = r->axis;
+    a.tokens = r->tokens;
+    a.q_heads = r->q_heads;
+    a.rot = r->rot;
+    a.axes = r->axes;
+    a.pairs = r->pairs != 0;
     a.err = dev.status;
-    const bool vec = cache_vec(kv) && rot % (pairs ? 8 : 16) == 0 && aligned(q, 16) && aligned(k, 16) &&
-                     aligned(v, 16) && aligned(q_out, 16) && mult8(q_stride, 2) && mult8(k_stride, 2) &&
-                     mult8(v_stride, 2) && mult8(q_out_stride, 2);
+    bool vec = cache_vec(kv) && r->rot % 16 == 0;
+    for (const gemv_heads_t *h : {&r->q, &r->k, &r->v, &r->q_out})
+        vec = vec && aligned(h->data, h == &r->q_out ? 16 : vec_bytes(r->src_elem)) && mult8(h->stride, 2);
     const cudaError_t e = launch_rope(a, vec, dev.sm_count, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GEMV_OK : decode_cuda_fail(e, GEMV_ERR_LAUNCH);
 }
@@ -307,7 +313,7 @@ gemv_status_t gemv_norm_residual(const gemv_norm_t *n, void *stream)
         if (r->data && (!is_elem(r->elem) || r->row_stride < 0)) return GEMV_ERR_INVALID_VALUE;
     if (n->rows == 0 || n->width == 0) return GEMV_OK;
     if (!n->y.data || !n->x.data || !n->out.data || n->out.elem != n->x.elem) return GEMV_ERR_INVALID_VALUE;
-    if (n->width > (1 << 24) || n->rows > INT_MAX) return GEMV_ERR_UNSUPPORTED;
+    if (n->width > (1 << 24) || n->rows >= (1 << 28)) return GEMV_ERR_UNSUPPORTED;
     // rows that are written must not lie on one another
     if (n->rows > 1 && (n->out.row_stride < n->width || (n->h.data && n->h.row_stride < n->width)))
         return GEMV_ERR_INVALID_VALUE;
@@ -315,7 +321,7 @@ gemv_status_t gemv_norm_residual(const gemv_norm_t *n, void *stream)
     for (const gemv_rows_t *r : all) {
         if (!r->data) continue;
         if (!aligned(r->data, elem_bytes(r->elem))) return GEMV_ERR_MISALIGNED;
-        if (!aligned(r->data, 16) || r->row_stride % 8) vec = false;
+        if (!aligned(r->data, vec_bytes(r->elem)) || r->row_stride % 8) vec = false;
     }
     NormArgs a{};
     a.y = n->y.data, a.y_e = n->y.elem, a.y_s = n->y.row_stride;

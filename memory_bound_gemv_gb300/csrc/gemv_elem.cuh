@@ -10,6 +10,23 @@
 
 namespace mbg {
 
+// 32 bytes at once (32-byte aligned): eight FP32 values of a thread as one
+// whole sector; two 16-byte accesses would move every sector in two halves.
+__device__ __forceinline__ void ld_global32(const void *p, uint32_t (&w)[8])
+{
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p)
+                 : "memory");
+}
+
+__device__ __forceinline__ void st_global32(void *p, const float (&x)[8])
+{
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]),
+                 "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
+}
+
 // 32 bits holding two 16-bit elements -> two floats (bf16 is the upper half
 // of an FP32 value).
 template <int E>
@@ -48,8 +65,8 @@ __device__ __forceinline__ void elem_store1(void *base, int64_t at, float v)
 }
 
 // Elements [at, at + 8) of which the first n exist (the others read 0).  VEC:
-// `at` is a multiple of 8 from a 16-byte aligned base and n is 8 or less
-// than 1.
+// `at` is a multiple of 8 from a 16-byte aligned base (FP32: 32) and n is 8 or
+// less than 1.
 template <bool VEC, int E>
 __device__ __forceinline__ void elem_load8(const void *base, int64_t at, int n, float (&x)[8])
 {
@@ -58,10 +75,10 @@ __device__ __forceinline__ void elem_load8(const void *base, int64_t at, int n, 
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = 0.f;
         } else if (E == GEMV_ELEM_F32) {
-            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + at);
-            const float4 u = p[0], v = p[1];
-            x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
-            x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+            uint32_t w[8];
+            ld_global32(static_cast<const float *>(base) + at, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
         } else {
             const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + at);
             const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
@@ -84,9 +101,7 @@ __device__ __forceinline__ void elem_store8(void *base, int64_t at, int n, const
     if (VEC) {
         if (n < 8) return;
         if (E == GEMV_ELEM_F32) {
-            float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(base) + at);
-            p[0] = make_float4(x[0], x[1], x[2], x[3]);
-            p[1] = make_float4(x[4], x[5], x[6], x[7]);
+            st_global32(static_cast<float *>(base) + at, x);
         } else {
             *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + at) =
                 make_uint4(elem_pack2<E>(x[0], x[1]), elem_pack2<E>(x[2], x[3]), elem_pack2<E>(x[4], x[5]),

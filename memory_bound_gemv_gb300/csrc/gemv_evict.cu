@@ -34,8 +34,6 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanMaxCluster = 8;
 constexpr int kBins = 2048;
-// Slots per thread in registers: of short rows, and of the longest ones.
-constexpr int kPlanShort = 4, kPlanLong = 24;
 
 // Larger score, larger integer; NaN like -inf, -0 like 0.
 __device__ __forceinline__ uint32_t score_key(float s)
@@ -328,10 +326,10 @@ __global__ void __launch_bounds__(kPlanThreads) mbg_evict_plan_kernel(const __gr
 // Moves.  Sources lie at or behind `keep` and targets before it, so nothing
 // is read that another thread writes and applying a plan twice changes
 // nothing.  Bound by the bytes moved, once enough of them are in flight: a
-// warp takes kApplyBatch moves at a time, its lanes look up their pages side by
-// side, then all their rows are requested before the first is written.
+// warp's lanes look up the pages of kApplyLook moves side by side, then the
+// rows of kApplyBatch moves are requested before the first is written.
 constexpr int kApplyThreads = 256;
-constexpr int kApplyBatch = 8;
+constexpr int kApplyBatch = 8, kApplyLook = 16;
 
 // Page of a slot, and its place in the page; -1 where it has no valid one.
 __device__ __forceinline__ int64_t page_of(const KvView &kv, const int32_t *table, int slot, int *off)
@@ -362,16 +360,16 @@ __global__ void __launch_bounds__(kApplyThreads) mbg_evict_apply_kernel(const __
     const int32_t *table = kv.table + b * kv.table_stride;
     const int2 *moves = reinterpret_cast<const int2 *>(a.moves) + row * a.max_moves;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int stride = gridDim.x * (kApplyThreads / 32) * kApplyBatch;
+    const int stride = gridDim.x * (kApplyThreads / 32) * kApplyLook;
     // lanes 0..15 move K, the others V
     const bool is_v = lane >= 16;
-    uint16_t *pool = static_cast<uint16_t *>(is_v ? kv.v : kv.k);
     const int64_t ps = is_v ? kv.vs_page : kv.ks_page, ts = is_v ? kv.vs_tok : kv.ks_tok,
                   hs = is_v ? kv.vs_head : kv.ks_head;
-    for (int i0 = (blockIdx.x * (kApplyThreads / 32) + warp) * kApplyBatch; i0 < count; i0 += stride) {
-        // lanes 0..7: a move each
+    uint16_t *pool = static_cast<uint16_t *>(is_v ? kv.v : kv.k) + h * hs;
+    for (int i0 = (blockIdx.x * (kApplyThreads / 32) + warp) * kApplyLook; i0 < count; i0 += stride) {
+        // lanes 0..15: a move each
         int sp = -1, tp = -1, so = 0, to = 0;
-        if (lane < kApplyBatch && i0 + lane < count) {
+        if (lane < kApplyLook && i0 + lane < count) {
             const int2 mv = __ldg(moves + i0 + lane);
             const bool in = mv.x >= 0 && mv.x < kv.capacity && mv.y >= 0 && mv.y < kv.capacity;
             if (in) {
@@ -392,30 +390,33 @@ __global__ void __launch_bounds__(kApplyThreads) mbg_evict_apply_kernel(const __
                 }
             }
         }
-        const uint16_t *src[kApplyBatch];
-        uint16_t *dst[kApplyBatch];
-#pragma unroll
-        for (int k = 0; k < kApplyBatch; ++k) {
-            const int s_page = __shfl_sync(kAll, sp, k), s_off = __shfl_sync(kAll, so, k);
-            const int t_page = __shfl_sync(kAll, tp, k), t_off = __shfl_sync(kAll, to, k);
-            src[k] = s_page < 0 ? nullptr : pool + s_page * ps + s_off * ts + h * hs;
-            dst[k] = pool + t_page * ps + t_off * ts + h * hs;
-        }
-        if (VEC) {
-            for (int d = (lane & 15) * 8; d < kv.dim; d += 128) {
+        for (int k0 = 0; k0 < kApplyLook && i0 + k0 < count; k0 += kApplyBatch) {
+            for (int d = (lane & 15) * (VEC ? 8 : 1); d - (lane & 15) * (VEC ? 8 : 1) < kv.dim; d += VEC ? 128 : 16) {
                 uint4 v[kApplyBatch];
 #pragma unroll
-                for (int k = 0; k < kApplyBatch; ++k)
-                    if (src[k]) v[k] = *reinterpret_cast<const uint4 *>(src[k] + d);
+                for (int k = 0; k < kApplyBatch; ++k) {
+                    const int page = __shfl_sync(kAll, sp, k0 + k), off = __shfl_sync(kAll, so, k0 + k);
+                    const uint16_t *src = pool + page * ps + off * ts + d;
+                    if (page >= 0 && d < kv.dim) {
+                        if (VEC)
+                            v[k] = *reinterpret_cast<const uint4 *>(src);
+                        else
+                            v[k].x = *src;
+                    }
+                }
 #pragma unroll
-                for (int k = 0; k < kApplyBatch; ++k)
-                    if (src[k]) *reinterpret_cast<uint4 *>(dst[k] + d) = v[k];
+                for (int k = 0; k < kApplyBatch; ++k) {
+                    const int live = __shfl_sync(kAll, sp, k0 + k);
+                    const int page = __shfl_sync(kAll, tp, k0 + k), off = __shfl_sync(kAll, to, k0 + k);
+                    uint16_t *dst = pool + page * ps + off * ts + d;
+                    if (live >= 0 && d < kv.dim) {
+                        if (VEC)
+                            *reinterpret_cast<uint4 *>(dst) = v[k];
+                        else
+                            *dst = static_cast<uint16_t>(v[k].x);
+                    }
+                }
             }
-        } else {
-#pragma unroll
-            for (int k = 0; k < kApplyBatch; ++k)
-                if (src[k])
-                    for (int d = lane & 15; d < kv.dim; d += 16) dst[k][d] = src[k][d];
         }
     }
 }
@@ -443,14 +444,19 @@ cudaError_t launch_pdl(void (*fn)(Args), dim3 grid, int threads, int cluster, cu
 cudaError_t launch_evict_plan(const EvictArgs &a, cudaStream_t s)
 {
     // the smallest cluster whose threads hold a row of the cache's capacity
-    // four slots each, then more slots per thread, then rows of any length
-    const int64_t slots = static_cast<int64_t>(kPlanThreads) * kPlanShort, cap = a.kv.capacity;
+    // eight slots each (rows of 30000 slots, plan and moves: 40.7 us; with four
+    // slots and twice the blocks 59.6 us, with sixteen and half 46.8 us), then
+    // more slots per thread, then rows of any length
+    const int64_t cap = a.kv.capacity;
     int cluster = 1;
-    while (cluster < kPlanMaxCluster && cap > cluster * slots) cluster *= 2;
+    while (cluster < kPlanMaxCluster && cap > static_cast<int64_t>(cluster) * kPlanThreads * 8) cluster *= 2;
+    const int64_t each = (cap + cluster * kPlanThreads - 1) / (cluster * kPlanThreads);
+    auto fn = each <= 4    ? mbg_evict_plan_kernel<4>
+              : each <= 8  ? mbg_evict_plan_kernel<8>
+              : each <= 16 ? mbg_evict_plan_kernel<16>
+              : each <= 24 ? mbg_evict_plan_kernel<24>
+                           : mbg_evict_plan_kernel<0>;
     const dim3 grid(static_cast<unsigned>(a.kv.batch) * a.kv.kv_heads * cluster);
-    auto fn = cap <= cluster * slots ? mbg_evict_plan_kernel<kPlanShort>
-              : cap <= static_cast<int64_t>(cluster) * kPlanThreads * kPlanLong ? mbg_evict_plan_kernel<kPlanLong>
-                                                                                : mbg_evict_plan_kernel<0>;
     return launch_pdl(fn, grid, kPlanThreads, cluster, s, a);
 }
 
@@ -459,7 +465,7 @@ cudaError_t launch_evict_apply(const EvictApplyArgs &a, bool vec, int sm_count, 
     // enough blocks per row to fill the GPU a few times over, and no more
     // than the moves there can be
     const int64_t rows = static_cast<int64_t>(a.kv.batch) * a.kv.kv_heads;
-    const int64_t per_block = kApplyThreads / 32 * kApplyBatch;
+    const int64_t per_block = kApplyThreads / 32 * kApplyLook;
     int64_t x = (16ll * sm_count + rows - 1) / rows;
     const int64_t most = (a.max_moves + per_block - 1) / per_block;
     if (x > most) x = most;

@@ -13,10 +13,13 @@
 //
 // Bound by the bytes: y, x and the row-wise gate, scale and shift are read
 // once, out and h written once.  One block takes one row and keeps it in
-// registers, eight neighbouring elements per thread and step; y and x are
-// requested before the first reduction, and what the row alone has of the
-// other operands is prefetched into L2.
+// registers, eight neighbouring elements per thread and step.  Next to the
+// bytes it is the instructions that count, some twenty per element: types are
+// chosen outside the loops, addresses once per row and operand (8192 x 4096 in
+// bf16: 48.1 us; with both inside the loops 83 us).
 #include <stdint.h>
+
+#include <atomic>
 
 #include "gemv_decode.h"
 #include "gemv_device.cuh"
@@ -25,117 +28,27 @@
 namespace mbg {
 namespace {
 
-// Eight elements as loaded; converted after the loads of the whole row are
-// under way.
-struct Raw {
-    uint4 a, b;
+// f(type's constant) for a type known at run time: one branch around all of a
+// thread's steps.  (With the choice inside, the compiler converts every
+// element both ways and selects.)
+template <int E>
+struct ElemTag {
+    static constexpr int value = E;
 };
-
-template <bool VEC>
-__device__ __forceinline__ Raw raw_load(const void *base, int elem, int64_t at, int n)
-{
-    Raw r;
-    r.a = r.b = make_uint4(0u, 0u, 0u, 0u);
-    if (n <= 0) return r;
-    if (VEC) {
-        if (elem == GEMV_ELEM_F32) {
-            const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(base) + at);
-            r.a = p[0];
-            r.b = p[1];
-        } else {
-            r.a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + at);
-        }
-        return r;
-    }
-    uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (elem == GEMV_ELEM_F32) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) w[i] = static_cast<const uint32_t *>(base)[at + i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n)
-                w[i >> 1] |= static_cast<uint32_t>(static_cast<const uint16_t *>(base)[at + i]) << (16 * (i & 1));
-    }
-    r.a = make_uint4(w[0], w[1], w[2], w[3]);
-    r.b = make_uint4(w[4], w[5], w[6], w[7]);
-    return r;
-}
-
-__device__ __forceinline__ void raw_floats(const Raw &r, int elem, float (&x)[8])
-{
-    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
-    if (elem == GEMV_ELEM_F32) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = elem == GEMV_ELEM_F16 ? elem_unpack2<GEMV_ELEM_F16>(w[i]) : elem_unpack2<GEMV_ELEM_BF16>(w[i]);
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
-        }
-    }
-}
-
-template <bool VEC>
-__device__ __forceinline__ void store_as(void *base, int elem, int64_t at, int n, const float (&x)[8])
+template <typename F>
+__device__ __forceinline__ void by_elem(int elem, F f)
 {
     if (elem == GEMV_ELEM_F32)
-        elem_store8<VEC, GEMV_ELEM_F32>(base, at, n, x);
+        f(ElemTag<GEMV_ELEM_F32>());
     else if (elem == GEMV_ELEM_F16)
-        elem_store8<VEC, GEMV_ELEM_F16>(base, at, n, x);
+        f(ElemTag<GEMV_ELEM_F16>());
     else
-        elem_store8<VEC, GEMV_ELEM_BF16>(base, at, n, x);
+        f(ElemTag<GEMV_ELEM_BF16>());
 }
 
-// Sum over the block; `turn` numbers the reductions of a kernel so that one
-// barrier is enough for each.
-struct Sums {
-    float w[4][32];
-};
-
-__device__ __forceinline__ float block_sum(float v, Sums &s, int turn)
+__device__ __forceinline__ const unsigned char *row_of(const void *base, int elem, int64_t row, int64_t stride)
 {
-#pragma unroll
-    for (int x = 16; x > 0; x /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, x);
-    if ((threadIdx.x & 31) == 0) s.w[turn][threadIdx.x >> 5] = v;
-    __syncthreads();
-    const int warps = blockDim.x >> 5;
-    float t = 0.f;
-    for (int i = 0; i < warps; ++i) t += s.w[turn][i];
-    return t;
-}
-
-// x -> (x - mean) / sqrt(var + eps), or x / sqrt(mean of squares + eps), for
-// values held in registers; cnt[k] of the eight values of step k exist.
-template <int K>
-__device__ __forceinline__ void normalise(float (&x)[K][8], const int (&cnt)[K], const NormArgs &a, Sums &s, int turn)
-{
-    const float inv_n = 1.f / static_cast<float>(a.width);
-    if (a.layer) {
-        float t = 0.f;
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) t += x[k][e];  // elements that do not exist are 0
-        const float mean = block_sum(t, s, turn) * inv_n;
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[k][e] = e < cnt[k] ? x[k][e] - mean : 0.f;
-    }
-    float q = 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) q = fmaf(x[k][e], x[k][e], q);
-    const float r = 1.f / sqrtf(block_sum(q, s, turn + 1) * inv_n + a.eps);
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[k][e] *= r;
+    return static_cast<const unsigned char *>(base) + (row * stride << (elem == GEMV_ELEM_F32 ? 2 : 1));
 }
 
 // 16 bytes that are read once.  Not the read-only path: out may be x, h may
@@ -150,110 +63,219 @@ __device__ __forceinline__ uint4 ld_once16(const void *p)
     return v;
 }
 
-// Types of y and x known at compile time (16 bits or FP32) halve the
-// registers that their loads wait in.
+// Eight elements as loaded, converted after the row's loads are under way.
+// WIDE: FP32, else one of the 16-bit types.
 template <bool VEC, bool WIDE>
 struct Stream {
-    Raw r;
-    __device__ __forceinline__ void load(const void *base, int elem, int64_t at, int n)
+    uint4 a, b;  // b: FP32, or the element-wise path, which converts at once
+    __device__ __forceinline__ void load(const unsigned char *row, int elem, int at, int n)
     {
-        if (!VEC) {
-            r = raw_load<false>(base, elem, at, n);
-        } else if (n > 0) {
-            if (WIDE) {
-                const unsigned char *p = reinterpret_cast<const unsigned char *>(static_cast<const float *>(base) + at);
-                r.a = ld_once16(p);
-                r.b = ld_once16(p + 16);
-            } else {
-                r.a = ld_once16(static_cast<const uint16_t *>(base) + at);
+        if (VEC) {
+            a = b = make_uint4(0u, 0u, 0u, 0u);
+            if (n > 0) {
+                if (WIDE) {
+                    uint32_t w[8];
+                    ld_global32(row + at * 4, w);
+                    a = make_uint4(w[0], w[1], w[2], w[3]);
+                    b = make_uint4(w[4], w[5], w[6], w[7]);
+                } else {
+                    a = ld_once16(row + at * 2);
+                }
             }
         } else {
-            r.a = r.b = make_uint4(0u, 0u, 0u, 0u);
+            float x[8];
+            by_elem(elem, [&](auto e) { elem_load8<false, decltype(e)::value>(row, at, n, x); });
+            a = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+            b = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
         }
     }
-    __device__ __forceinline__ void floats(int elem, float (&x)[8]) const
+    template <int E>
+    __device__ __forceinline__ void floats(float (&x)[8]) const
     {
-        if (VEC && !WIDE) {
-            const Raw t = {r.a, make_uint4(0u, 0u, 0u, 0u)};
-            raw_floats(t, elem == GEMV_ELEM_F16 ? GEMV_ELEM_F16 : GEMV_ELEM_BF16, x);
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        if (!VEC || WIDE) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
         } else {
-            raw_floats(r, VEC ? GEMV_ELEM_F32 : elem, x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = elem_unpack2<E == GEMV_ELEM_F32 ? GEMV_ELEM_F16 : E>(w[i]);
+                x[2 * i] = f.x;
+                x[2 * i + 1] = f.y;
+            }
         }
     }
 };
 
-template <int K, int MAXT, bool VEC, bool Y32, bool X32>
+// The type of y or x where WIDE leaves only two.
+template <bool VEC, bool WIDE, typename F>
+__device__ __forceinline__ void by_stream(int elem, F f)
+{
+    if (VEC && WIDE)
+        f(ElemTag<GEMV_ELEM_F32>());
+    else if (VEC && elem == GEMV_ELEM_F16)
+        f(ElemTag<GEMV_ELEM_F16>());
+    else if (VEC)
+        f(ElemTag<GEMV_ELEM_BF16>());
+    else
+        by_elem(elem, f);
+}
+
+// Sum over the block.  `turn` numbers the reductions, so that one barrier is
+// enough for each; a block that goes through several rows alternates between
+// two sets of four.  (A row spread over a cluster of blocks, joined through
+// distributed shared memory, takes longer: 331 rows of 14336 in clusters of
+// two 21.5 us, in blocks 18.1 us.)
+struct Sums {
+    float w[8][32];
+};
+
+__device__ __forceinline__ float row_sum(float v, Sums &s, int turn)
+{
+#pragma unroll
+    for (int x = 16; x > 0; x /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, x);
+    if ((threadIdx.x & 31) == 0) s.w[turn][threadIdx.x >> 5] = v;
+    __syncthreads();
+    const int warps = blockDim.x >> 5;
+    float t = 0.f;
+    for (int i = 0; i < warps; ++i) t += s.w[turn][i];
+    return t;
+}
+
+// x -> (x - mean) / sqrt(var + eps), or x / sqrt(mean of squares + eps), for
+// values held in registers; cnt[k] of the eight values of step k exist.
+template <int K, bool VEC, bool FULL>
+__device__ __forceinline__ void normalise(float (&x)[K][8], const int (&cnt)[K], const NormArgs &a, Sums &s, int turn)
+{
+    const float inv_n = 1.f / static_cast<float>(a.width);
+    auto mask = [&](float shift) {  // elements that do not exist become 0
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                x[k][e] = FULL || (VEC ? cnt[k] > 0 : e < cnt[k]) ? x[k][e] - shift : 0.f;
+    };
+    if (!FULL) mask(0.f);
+    if (a.layer) {
+        float t = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t += x[k][e];
+        mask(row_sum(t, s, turn) * inv_n);
+    }
+    float q = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q = fmaf(x[k][e], x[k][e], q);
+    const float r = 1.f / sqrtf(row_sum(q, s, turn + 1) * inv_n + a.eps);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[k][e] *= r;
+}
+
+// A block goes through rows and requests the next row's y and x while it
+// works on the present one; what else differs from row to row is prefetched
+// into L2, what does not comes from L1.  FULL: every thread has all of its K
+// steps.
+template <int K, int MAXT, bool VEC, bool FULL, bool Y32, bool X32>
 __global__ void __launch_bounds__(MAXT) mbg_norm_kernel(const __grid_constant__ NormArgs a)
 {
     __shared__ Sums sums;
     pdl_trigger();
     pdl_wait();
-    const int64_t row = blockIdx.x;
+    int64_t row = blockIdx.x;
     int at[K], cnt[K];
     Stream<VEC, Y32> y[K];
     Stream<VEC, X32> r[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        at[k] = (threadIdx.x + k * blockDim.x) * 8;
-        cnt[k] = min(8, a.width - at[k]);
-        y[k].load(a.y, a.y_e, row * a.y_s + at[k], cnt[k]);
+        at[k] = (k * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * 8;
+        cnt[k] = FULL ? 8 : min(8, a.width - at[k]);
     }
-#pragma unroll
-    for (int k = 0; k < K; ++k) r[k].load(a.r, a.r_e, row * a.r_s + at[k], cnt[k]);
-    if (VEC && threadIdx.x == 0) {
-        // operands of this row alone that are needed late: into L2 meanwhile
-        auto early = [&](const void *p, int e, int64_t stride) {
-            const int size = e == GEMV_ELEM_F32 ? 4 : 2;
-            if (p && stride) prefetch_l2(static_cast<const unsigned char *>(p) + row * stride * size, a.width * size);
+    // operands of a row alone that are needed late
+    auto prefetch = [&](int64_t rw) {
+        if (!VEC || threadIdx.x != 0 || rw >= a.rows) return;
+        auto one = [&](const void *p, int e, int64_t stride) {
+            if (p && stride) prefetch_l2(row_of(p, e, rw, stride), a.width << (e == GEMV_ELEM_F32 ? 2 : 1));
         };
-        early(a.gate, a.gate_e, a.gate_s);
-        early(a.pre_w, a.pre_w_e, a.pre_w_s);
-        early(a.pre_b, a.pre_b_e, a.pre_b_s);
-    }
-    float x[K][8];
+        one(a.post_w, a.post_e, a.post_s);
+        one(a.gate, a.gate_e, a.gate_s);
+        one(a.pre_w, a.pre_w_e, a.pre_w_s);
+        one(a.pre_b, a.pre_b_e, a.pre_b_s);
+    };
+    auto request_y = [&](int64_t rw) {
+        const unsigned char *p = row_of(a.y, a.y_e, rw, a.y_s);
 #pragma unroll
-    for (int k = 0; k < K; ++k) y[k].floats(a.y_e, x[k]);
-    if (a.post) {
-        normalise<K>(x, cnt, a, sums, 0);
-        if (a.post_w) {
+        for (int k = 0; k < K; ++k) y[k].load(p, a.y_e, at[k], cnt[k]);
+    };
+    auto request_r = [&](int64_t rw) {
+        const unsigned char *p = row_of(a.r, a.r_e, rw, a.r_s);
+#pragma unroll
+        for (int k = 0; k < K; ++k) r[k].load(p, a.r_e, at[k], cnt[k]);
+    };
+    // x[k][i] = f(x[k][i], operand)
+    float x[K][8];
+    auto with = [&](const void *base, int elem, int64_t stride, auto f) {
+        const unsigned char *p = row_of(base, elem, row, stride);
+        by_elem(elem, [&](auto e) {
+            float t[K][8];
+#pragma unroll
+            for (int k = 0; k < K; ++k) elem_load8<VEC, decltype(e)::value>(p, at[k], cnt[k], t[k]);
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[k][i] = f(x[k][i], t[k][i]);
+        });
+    };
+    auto product = [](float v, float w) { return v * w; };
+    prefetch(row);
+    request_y(row);
+    request_r(row);
+    for (int turn = 0;; turn ^= 4) {
+        const int64_t next = row + gridDim.x;
+        prefetch(next);
+        by_stream<VEC, Y32>(a.y_e, [&](auto e) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) y[k].template floats<decltype(e)::value>(x[k]);
+        });
+        if (next < a.rows) request_y(next);
+        if (a.post) {
+            normalise<K, VEC, FULL>(x, cnt, a, sums, turn);
+            if (a.post_w) with(a.post_w, a.post_e, a.post_s, product);
+        }
+        if (a.gate) with(a.gate, a.gate_e, a.gate_s, product);
+        by_stream<VEC, X32>(a.r_e, [&](auto e) {
+            constexpr int E = decltype(e)::value;
+            unsigned char *p = const_cast<unsigned char *>(row_of(a.out, E, row, a.out_s));
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                float w[8];
-                raw_floats(raw_load<VEC>(a.post_w, a.post_e, row * a.post_s + at[k], cnt[k]), a.post_e, w);
+                float t[8];
+                r[k].template floats<E>(t);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[k][e] *= w[e];
+                for (int i = 0; i < 8; ++i) x[k][i] = fmaf(a.alpha, x[k][i], t[i]);
+                elem_store8<VEC, E>(p, at[k], cnt[k], x[k]);
             }
+        });
+        if (next < a.rows) request_r(next);
+        if (a.h) {
+            normalise<K, VEC, FULL>(x, cnt, a, sums, turn + 2);
+            if (a.pre_w) {
+                const float unit = a.unit_offset ? 1.f : 0.f;
+                with(a.pre_w, a.pre_w_e, a.pre_w_s, [&](float v, float w) { return v * (w + unit); });
+            }
+            if (a.pre_b) with(a.pre_b, a.pre_b_e, a.pre_b_s, [](float v, float w) { return v + w; });
+            by_elem(a.h_e, [&](auto e) {
+                constexpr int E = decltype(e)::value;
+                unsigned char *p = const_cast<unsigned char *>(row_of(a.h, E, row, a.h_s));
+#pragma unroll
+                for (int k = 0; k < K; ++k) elem_store8<VEC, E>(p, at[k], cnt[k], x[k]);
+            });
         }
-    }
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        float t[8];
-        if (a.gate) {
-            raw_floats(raw_load<VEC>(a.gate, a.gate_e, row * a.gate_s + at[k], cnt[k]), a.gate_e, t);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[k][e] *= t[e];
-        }
-        r[k].floats(a.r_e, t);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[k][e] = e < cnt[k] ? fmaf(a.alpha, x[k][e], t[e]) : 0.f;
-        store_as<VEC>(a.out, a.r_e, row * a.out_s + at[k], cnt[k], x[k]);
-    }
-    if (!a.h) return;
-    normalise<K>(x, cnt, a, sums, 2);
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        float t[8];
-        if (a.pre_w) {
-            raw_floats(raw_load<VEC>(a.pre_w, a.pre_w_e, row * a.pre_w_s + at[k], cnt[k]), a.pre_w_e, t);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[k][e] *= a.unit_offset ? 1.f + t[e] : t[e];
-        }
-        if (a.pre_b) {
-            raw_floats(raw_load<VEC>(a.pre_b, a.pre_b_e, row * a.pre_b_s + at[k], cnt[k]), a.pre_b_e, t);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[k][e] += t[e];
-        }
-        store_as<VEC>(a.h, a.h_e, row * a.h_s + at[k], cnt[k], x[k]);
+        if (next >= a.rows) break;
+        row = next;
     }
 }
 
@@ -271,8 +293,13 @@ __global__ void __launch_bounds__(kLongThreads) mbg_norm_long_kernel(const __gri
     const int64_t row = blockIdx.x;
     const float inv_n = 1.f / static_cast<float>(a.width);
     float mean_y = 0.f, r_y = 1.f, mean_x = 0.f;
-    auto load = [&](const void *p, int e, int64_t stride, int at, int n, float(&t)[8]) {
-        raw_floats(raw_load<VEC>(p, e, row * stride + at, n), e, t);
+    auto load = [&](const void *p, int elem, int64_t stride, int at, int n, float(&t)[8]) {
+        by_elem(elem, [&](auto e) { elem_load8<VEC, decltype(e)::value>(row_of(p, elem, row, stride), at, n, t); });
+    };
+    auto store = [&](void *p, int elem, int64_t stride, int at, int n, const float(&t)[8]) {
+        by_elem(elem, [&](auto e) {
+            elem_store8<VEC, decltype(e)::value>(const_cast<unsigned char *>(row_of(p, elem, row, stride)), at, n, t);
+        });
     };
     auto sum_y = [&](int at, int n, bool square) {
         float t[8], s = 0.f;
@@ -310,11 +337,11 @@ __global__ void __launch_bounds__(kLongThreads) mbg_norm_long_kernel(const __gri
         float s = 0.f;
         if (a.layer) {
             for (int at = first; at < a.width; at += step) s += sum_y(at, min(8, a.width - at), false);
-            mean_y = block_sum(s, sums, 0) * inv_n;
+            mean_y = row_sum(s, sums, 0) * inv_n;
             s = 0.f;
         }
         for (int at = first; at < a.width; at += step) s += sum_y(at, min(8, a.width - at), true);
-        r_y = 1.f / sqrtf(block_sum(s, sums, 1) * inv_n + a.eps);
+        r_y = 1.f / sqrtf(row_sum(s, sums, 1) * inv_n + a.eps);
     }
     float x[8], r_x = 1.f;
     if (a.h) {
@@ -325,7 +352,7 @@ __global__ void __launch_bounds__(kLongThreads) mbg_norm_long_kernel(const __gri
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s += x[e];
             }
-            mean_x = block_sum(s, sums, 2) * inv_n;
+            mean_x = row_sum(s, sums, 2) * inv_n;
             s = 0.f;
         }
         for (int at = first; at < a.width; at += step) {
@@ -337,13 +364,13 @@ __global__ void __launch_bounds__(kLongThreads) mbg_norm_long_kernel(const __gri
                 s = fmaf(d, d, s);
             }
         }
-        r_x = 1.f / sqrtf(block_sum(s, sums, 3) * inv_n + a.eps);
+        r_x = 1.f / sqrtf(row_sum(s, sums, 3) * inv_n + a.eps);
     }
     for (int at = first; at < a.width; at += step) {
         const int n = min(8, a.width - at);
         float t[8];
         stream(at, n, x);
-        store_as<VEC>(a.out, a.r_e, row * a.out_s + at, n, x);
+        store(a.out, a.r_e, a.out_s, at, n, x);
         if (!a.h) continue;
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = (x[e] - mean_x) * r_x;
@@ -357,14 +384,14 @@ __global__ void __launch_bounds__(kLongThreads) mbg_norm_long_kernel(const __gri
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] += t[e];
         }
-        store_as<VEC>(a.h, a.h_e, row * a.h_s + at, n, x);
+        store(a.h, a.h_e, a.h_s, at, n, x);
     }
 }
 
-cudaError_t launch_rows(void (*fn)(NormArgs), const NormArgs &a, int threads, cudaStream_t s)
+cudaError_t launch_rows(void (*fn)(NormArgs), const NormArgs &a, int64_t blocks, int threads, cudaStream_t s)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.rows));
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -375,19 +402,43 @@ cudaError_t launch_rows(void (*fn)(NormArgs), const NormArgs &a, int threads, cu
     return cudaLaunchKernelEx(&cfg, fn, a);
 }
 
+// Blocks that fit on the GPU at once, each going through rows.
+template <int K, bool VEC, bool FULL, bool Y32, bool X32>
+cudaError_t launch_fitting(const NormArgs &a, int threads, int sm_count, cudaStream_t s)
+{
+    auto fn = mbg_norm_kernel<K, 512, VEC, FULL, Y32, X32>;
+    static std::atomic<int> fit[512 / 32 + 1];  // blocks per SM, by warps (0: not asked yet)
+    int per_sm = fit[threads / 32].load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, threads, 0);
+        if (e != cudaSuccess) return e;
+        if (per_sm < 1) per_sm = 1;
+        fit[threads / 32].store(per_sm, std::memory_order_relaxed);
+    }
+    const int64_t most = static_cast<int64_t>(per_sm) * sm_count;
+    return launch_rows(fn, a, a.rows < most ? a.rows : most, threads, s);
+}
+
+template <int K, bool VEC, bool Y32, bool X32>
+cudaError_t launch_steps(const NormArgs &a, int sm_count, cudaStream_t s)
+{
+    const int chunks = (a.width + 7) / 8, threads = ((chunks + K - 1) / K + 31) / 32 * 32;
+    if (VEC && chunks == threads * K) return launch_fitting<K, VEC, true, Y32, X32>(a, threads, sm_count, s);
+    return launch_fitting<K, VEC, false, Y32, X32>(a, threads, sm_count, s);
+}
+
 template <bool VEC, bool Y32, bool X32>
 cudaError_t launch(const NormArgs &a, int sm_count, cudaStream_t s)
 {
     const int chunks = (a.width + 7) / 8;
-    auto threads = [&](int k) { return ((chunks + k - 1) / k + 31) / 32 * 32; };
+    if (chunks > 2048) return launch_rows(mbg_norm_long_kernel<VEC>, a, a.rows, kLongThreads, s);
     // Few rows: a row's latency counts, and more threads shorten it.  Many
-    // rows: small blocks with four steps per thread, so that several rows are
-    // in different phases on one SM and loads are always under way.
+    // rows: small blocks with several steps per thread, so that several rows
+    // are in different phases on one SM.
     const bool many = a.rows > 2 * sm_count;
-    if (chunks <= (many ? 128 : 512)) return launch_rows(mbg_norm_kernel<1, 512, VEC, Y32, X32>, a, threads(1), s);
-    if (chunks <= (many ? 256 : 1024)) return launch_rows(mbg_norm_kernel<2, 512, VEC, Y32, X32>, a, threads(2), s);
-    if (chunks <= 2048) return launch_rows(mbg_norm_kernel<4, 512, VEC, Y32, X32>, a, threads(4), s);
-    return launch_rows(mbg_norm_long_kernel<VEC>, a, kLongThreads, s);
+    if (chunks > 1024 || (many && !Y32 && !X32 && chunks > 256)) return launch_steps<4, VEC, Y32, X32>(a, sm_count, s);
+    if (chunks > (many ? 128 : 512)) return launch_steps<2, VEC, Y32, X32>(a, sm_count, s);
+    return launch_steps<1, VEC, Y32, X32>(a, sm_count, s);
 }
 
 }  // namespace

@@ -8,13 +8,16 @@
 // at most |pos| * 2^-65 turns from the table's rounding.  Its upper 32 bits
 // go to sincospif.
 //
-// Bound by the bytes of q, k and v read and written once.  A block takes one
-// token and some of its heads.  Each thread requests its first heads' part,
-// the block computes the token's sines and cosines into shared memory while
-// those are under way, then they are turned and written.
+// Bound by the bytes of q, k and v read and written once.  A thread keeps one
+// head and one unit of 16 of its elements, so that its addresses and its part
+// of the work are settled once, and goes through tokens: a block's loads of
+// the next tokens are under way while it turns the present one, whose sines
+// and cosines were computed into shared memory during the one before.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "gemv_decode.h"
 #include "gemv_device.cuh"
@@ -23,170 +26,284 @@
 namespace mbg {
 namespace {
 
-constexpr int kMaxThreads = 512;
+constexpr int kMaxThreads = 256;
 constexpr int kMaxPairs = 128;
 
-// A head is cut into units of 16 elements: two runs of eight, at d0 and d1, of
-// which n0 and n1 exist.  Turned units are eight pairs (style "halves":
-// elements i..i+7 and those rot / 2 behind them; "pairs": 16 consecutive
-// ones); the others are copied.
+// A head is cut into runs of eight elements, and a unit is two of them, at d0
+// and d1, of which n0 and n1 elements exist: runs u and u + (half of them), so
+// that neighbouring threads load neighbouring runs (two neighbouring runs in
+// one thread would fetch and write every 32-byte sector in two halves).  Turned
+// units are eight pairs: style "halves" elements i..i+7 and those rot / 2
+// behind them, "pairs" four pairs in each run.  The others are copied.
 struct Unit {
     int d0, d1, n0, n1;
+    int pair0, pair1;  // first pairs of the runs
     bool turned;
     __device__ __forceinline__ Unit(const RopeArgs &a, int u, bool is_v)
     {
         const int half = a.rot >> 1, dim = a.kv.dim, turn_units = (half + 7) >> 3;
         turned = !is_v && u < turn_units;
-        if (!turned) {
-            d0 = is_v ? u * 16 : a.rot + (u - turn_units) * 16;
-            d1 = d0 + 8;
-            n0 = min(8, dim - d0);
-            n1 = min(8, dim - d1);
-        } else if (a.pairs) {
-            d0 = u * 16;
-            d1 = d0 + 8;
-            n0 = min(8, a.rot - d0);
-            n1 = min(8, a.rot - d1);
-        } else {
+        pair0 = pair1 = 8 * u;
+        if (turned && !a.pairs) {
             d0 = u * 8;
             d1 = half + d0;
             n0 = n1 = min(8, half - d0);
+        } else {
+            const int from = is_v || turned ? 0 : a.rot, to = turned ? a.rot : dim, first = is_v || turned ? u : u - turn_units;
+            const int units = (to - from + 15) >> 4;
+            d0 = from + first * 8;
+            d1 = d0 + units * 8;
+            n0 = min(8, to - d0);
+            n1 = min(8, to - d1);
+            pair0 = 4 * u;
+            pair1 = 4 * (u + units);
+        }
+        if (u >= (is_v ? (dim + 15) >> 4 : turn_units + ((dim - a.rot + 15) >> 4))) n0 = n1 = 0;
+    }
+};
+
+// Eight elements as loaded.
+template <int E>
+struct Raw8 {
+    uint4 a, b;  // b: FP32 only
+    template <bool VEC>
+    __device__ __forceinline__ void load(const void *base, int64_t at, int n)
+    {
+        const int size = E == GEMV_ELEM_F32 ? 4 : 2;
+        if (VEC) {
+            if (n < 8) return;
+            const unsigned char *p = static_cast<const unsigned char *>(base) + at * size;
+            if (E == GEMV_ELEM_F32) {
+                uint32_t w[8];
+                ld_global32(p, w);
+                a = make_uint4(w[0], w[1], w[2], w[3]);
+                b = make_uint4(w[4], w[5], w[6], w[7]);
+            } else {
+                a = ld_stream16(p);
+            }
+        } else {
+            float x[8];
+            elem_load8<false, E>(base, at, n, x);
+            a = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+            b = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+        }
+    }
+    template <bool VEC>
+    __device__ __forceinline__ void floats(float (&x)[8]) const
+    {
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        if (!VEC || E == GEMV_ELEM_F32) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = elem_unpack2<E>(w[i]);
+                x[2 * i] = f.x;
+                x[2 * i + 1] = f.y;
+            }
         }
     }
 };
 
-// blockDim.x = units per head x heads that are worked on side by side.  A
-// thread keeps to one unit, so its sines and cosines stay in registers while
-// it goes through the heads, HEADS of them requested at once.
-template <bool VEC, int SRC, int DST, int HEADS>
-__global__ void __launch_bounds__(kMaxThreads)
+// What a block knows of a token before it turns it.
+struct Place {
+    int seq, slot, page, off;  // page -1: not written
+};
+
+// All warps but the last turn; the last one looks ahead: it computes the next
+// token's sines and cosines and its place in the cache.  (Both in every
+// thread took 100 registers and left room for 12 warps on an SM.)
+template <bool VEC, int SRC, int DST>
+__global__ void __launch_bounds__(kMaxThreads + 32, 3)
     mbg_rope_kernel(const __grid_constant__ RopeArgs a, int heads_per_block, int per_head)
 {
-    __shared__ __align__(16) float s_cos[kMaxPairs], s_sin[kMaxPairs];
+    __shared__ __align__(16) float s_cos[2][kMaxPairs], s_sin[2][kMaxPairs];
+    __shared__ Place s_place[2];
     pdl_trigger();
     pdl_wait();
     const KvView &kv = a.kv;
-    const int t = blockIdx.x, threads = blockDim.x;
-    const int half = a.rot >> 1;
-    const int side = threads / per_head, lane_head = threadIdx.x / per_head, u = threadIdx.x - lane_head * per_head;
-    const int head0 = blockIdx.y * heads_per_block;
-    const int head1 = min(head0 + heads_per_block, a.q_heads + 2 * kv.kv_heads);
-    const int first_v = a.q_heads + kv.kv_heads;
-    const Unit uqk(a, u, false), uv(a, u, true);
-    float x[HEADS][8], y[HEADS][8];
-    auto request = [&](int h0) {
+    const int tid = threadIdx.x, half = a.rot >> 1, step = gridDim.x;
+
+    if (tid >= static_cast<int>(blockDim.x) - 32) {
+        const int lane = tid & 31;
+        constexpr int kPairs = kMaxPairs / 32;
+        uint64_t turns[kPairs];
+        int ax[kPairs], pos[kPairs];
 #pragma unroll
-        for (int k = 0; k < HEADS; ++k) {
-            const int head = h0 + k * side;
-            if (head >= head1) continue;
-            const bool is_v = head >= first_v;
-            const void *src = head < a.q_heads ? a.q : is_v ? a.v : a.k;
-            const int h = head < a.q_heads ? head : is_v ? head - first_v : head - a.q_heads;
-            const int64_t st = head < a.q_heads ? a.q_st : is_v ? a.v_st : a.k_st;
-            const int64_t sh = head < a.q_heads ? a.q_sh : is_v ? a.v_sh : a.k_sh;
-            const int64_t at = t * st + h * sh;
-            elem_load8<VEC, SRC>(src, at + (is_v ? uv.d0 : uqk.d0), is_v ? uv.n0 : uqk.n0, x[k]);
-            elem_load8<VEC, SRC>(src, at + (is_v ? uv.d1 : uqk.d1), is_v ? uv.n1 : uqk.n1, y[k]);
+        for (int i = 0; i < kPairs; ++i) {
+            const int pair = lane + 32 * i;
+            turns[i] = pair < half ? __ldg(a.turns + pair) : 0;
+            ax[i] = pair < half ? __ldg(a.axis + pair) : 0;
+            if (ax[i] >= a.axes) {
+                report_error(a.err, DEVERR_BAD_INDEX);
+                ax[i] = 0;
+            }
+        }
+        auto positions = [&](int t) {
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i)
+                if (lane + 32 * i < half && t < a.tokens) pos[i] = __ldg(a.positions + ax[i] * a.pos_stride + t);
+        };
+        auto sines = [&](int buf) {
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) {
+                if (lane + 32 * i >= half) continue;
+                const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(pos[i])) * turns[i];
+                // the nearest 2^-32 turns, as half turns in [-1, 1)
+                const int32_t part = static_cast<int32_t>((turn + 0x80000000ull) >> 32);
+                sincospif(static_cast<float>(part) * 4.656612873077393e-10f, &s_sin[buf][lane + 32 * i],
+                          &s_cos[buf][lane + 32 * i]);
+            }
+        };
+        auto slot_of = [&](int t) {
+            Place p = {0, -1, -1, 0};
+            if (t < a.tokens) {
+                p.seq = a.seq ? __ldg(a.seq + t) : t;
+                p.slot = __ldg(a.slots + t);
+            }
+            return p;
+        };
+        auto page_of = [&](Place p) {
+            if (p.slot < 0) return p;  // a negative slot is padding: nothing is written
+            bool ok = p.seq >= 0 && p.seq < kv.batch && p.slot < kv.capacity;
+            if (ok) {
+                const int idx = kv.page_shift >= 0 ? p.slot >> kv.page_shift : p.slot / kv.page_size;
+                p.off = p.slot - idx * kv.page_size;
+                p.page = __ldg(kv.table + p.seq * kv.table_stride + idx);
+                ok = p.page >= 0 && p.page < kv.num_pages;
+            }
+            if (!ok) {
+                p.page = -1;
+                if (lane == 0) report_error(a.err, DEVERR_BAD_INDEX);
+            }
+            return p;
+        };
+        // each token's positions and slot are read a token before they are
+        // needed, its page after its slot
+        int t = blockIdx.x;
+        positions(t);
+        Place here = page_of(slot_of(t)), later = slot_of(t + step);
+        for (int buf = 0; t < a.tokens; t += step, buf ^= 1) {
+            sines(buf);
+            if (lane == 0) s_place[buf] = here;
+            __syncthreads();
+            if (blockIdx.y == 0 && here.page >= 0) {
+                for (int i = lane; i < kv.kv_heads; i += 32) {
+                    const int64_t at = (static_cast<int64_t>(here.seq) * kv.kv_heads + i) * kv.capacity + here.slot;
+                    if (a.scores_cache) a.scores_cache[at] = 0.f;
+                    if (a.stamps_cache) a.stamps_cache[at] = a.stamps ? __ldg(a.stamps + t) : here.slot;
+                }
+            }
+            positions(t + step);
+            here = page_of(later);
+            later = slot_of(t + 2 * step);
+        }
+        return;
+    }
+
+    // this thread's head and unit
+    const int lane_head = tid / per_head, u = tid - lane_head * per_head;
+    const int head = blockIdx.y * heads_per_block + lane_head, first_v = a.q_heads + kv.kv_heads;
+    const bool is_q = head < a.q_heads, is_v = head >= first_v;
+    const bool mine = lane_head < heads_per_block && head < first_v + kv.kv_heads;
+    const int h = is_q ? head : is_v ? head - first_v : head - a.q_heads;
+    const Unit un(a, u, is_v);
+    const int n0 = mine ? un.n0 : 0, n1 = mine ? un.n1 : 0;
+    constexpr int kSize = SRC == GEMV_ELEM_F32 ? 4 : 2;
+    const int64_t src_token = is_q ? a.q_st : is_v ? a.v_st : a.k_st;
+    const unsigned char *src = static_cast<const unsigned char *>(is_q ? a.q : is_v ? a.v : a.k) +
+                               (h * (is_q ? a.q_sh : is_v ? a.v_sh : a.k_sh) + blockIdx.x * src_token) * kSize;
+    const int64_t src_step = step * src_token * kSize;
+    uint16_t *dst = is_q ? static_cast<uint16_t *>(a.q_out) + h * a.qo_sh + blockIdx.x * a.qo_st
+                    : is_v ? static_cast<uint16_t *>(kv.v) + h * kv.vs_head
+                           : static_cast<uint16_t *>(kv.k) + h * kv.ks_head;
+    const int64_t d_page = is_v ? kv.vs_page : kv.ks_page, d_tok = is_v ? kv.vs_tok : kv.ks_tok;
+    constexpr int kAhead = SRC == GEMV_ELEM_F32 ? 1 : 2;  // tokens requested ahead
+    Raw8<SRC> x[kAhead], y[kAhead];
+    auto request = [&](int k, int t) {
+        if (t < a.tokens) {
+            x[k].template load<VEC>(src, un.d0, n0);
+            y[k].template load<VEC>(src, un.d1, n1);
+            src += src_step;
         }
     };
-    int head = head0 + lane_head;
-    if (lane_head >= side) head = head1;  // threads beyond the last whole head
-    request(head);
-    // where the token goes
-    const int seq = a.seq ? __ldg(a.seq + t) : t;
-    const int slot = __ldg(a.slots + t);
-    int64_t page = -1;
-    int off = 0;
-    if (slot >= 0) {  // a negative slot is padding: nothing is written
-        bool ok = seq >= 0 && seq < kv.batch && slot < kv.capacity;
-        if (ok) {
-            const int idx = kv.page_shift >= 0 ? slot >> kv.page_shift : slot / kv.page_size;
-            off = slot - idx * kv.page_size;
-            page = __ldg(kv.table + seq * kv.table_stride + idx);
-            ok = page >= 0 && page < kv.num_pages;
-        }
-        if (!ok) {
-            page = -1;
-            if (threadIdx.x == 0) report_error(a.err, DEVERR_BAD_INDEX);
-        }
-    }
-    for (int i = threadIdx.x; i < half; i += threads) {
-        int ax = __ldg(a.axis + i);
-        if (ax >= a.axes) {
-            if (t == 0) report_error(a.err, DEVERR_BAD_INDEX);
-            ax = 0;
-        }
-        const int pos = __ldg(a.positions + ax * a.pos_stride + t);
-        const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(pos)) * __ldg(a.turns + i);
-        // the nearest 2^-32 turns, as half turns in [-1, 1)
-        const int32_t part = static_cast<int32_t>((turn + 0x80000000ull) >> 32);
-        float sn, cs;
-        sincospif(static_cast<float>(part) * 4.656612873077393e-10f, &sn, &cs);
-        s_cos[i] = cs;
-        s_sin[i] = sn;
-    }
-    if (blockIdx.y == 0 && page >= 0) {
-        for (int h = threadIdx.x; h < kv.kv_heads; h += threads) {
-            const int64_t at = (static_cast<int64_t>(seq) * kv.kv_heads + h) * kv.capacity + slot;
-            if (a.scores_cache) a.scores_cache[at] = 0.f;
-            if (a.stamps_cache) a.stamps_cache[at] = a.stamps ? __ldg(a.stamps + t) : slot;
-        }
-    }
-    __syncthreads();
-    float c[8], s[8];
-    if (uqk.turned) {
+    int t = blockIdx.x;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {  // pairs past the last turn elements that do not exist
-            const int i = min(u * 8 + e, half - 1);
-            c[e] = s_cos[VEC ? u * 8 + e : i];
-            s[e] = s_sin[VEC ? u * 8 + e : i];
-        }
-    }
-    for (; head < head1;) {
+    for (int k = 0; k < kAhead; ++k) request(k, t + k * step);
+    for (int buf = 0; t < a.tokens;) {
 #pragma unroll
-        for (int k = 0; k < HEADS; ++k) {
-            const int hd = head + k * side;
-            const bool is_v = hd >= first_v;
-            if (hd >= head1 || (hd >= a.q_heads && page < 0)) continue;
-            if (uqk.turned && !is_v) {
+        for (int k = 0; k < kAhead; ++k) {
+            if (t >= a.tokens) break;
+            __syncthreads();
+            float v[8], w[8];
+            x[k].template floats<VEC>(v);
+            y[k].template floats<VEC>(w);
+            request(k, t + kAhead * step);
+            if (un.turned) {
+                // pairs past the last turn elements that do not exist
+                const int last = half - 1;
                 if (a.pairs) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float p = x[k][2 * e], q = x[k][2 * e + 1], v = y[k][2 * e], w = y[k][2 * e + 1];
-                        x[k][2 * e] = p * c[e] - q * s[e];
-                        x[k][2 * e + 1] = p * s[e] + q * c[e];
-                        y[k][2 * e] = v * c[e + 4] - w * s[e + 4];
-                        y[k][2 * e + 1] = v * s[e + 4] + w * c[e + 4];
+                        const int p0 = min(un.pair0 + e, last), p1 = min(un.pair1 + e, last);
+                        const float c0 = s_cos[buf][p0], s0 = s_sin[buf][p0], c1 = s_cos[buf][p1], s1 = s_sin[buf][p1];
+                        const float f = v[2 * e], g = v[2 * e + 1], i = w[2 * e], j = w[2 * e + 1];
+                        v[2 * e] = f * c0 - g * s0;
+                        v[2 * e + 1] = f * s0 + g * c0;
+                        w[2 * e] = i * c1 - j * s1;
+                        w[2 * e + 1] = i * s1 + j * c1;
                     }
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float p = x[k][e], q = y[k][e];
-                        x[k][e] = p * c[e] - q * s[e];
-                        y[k][e] = p * s[e] + q * c[e];
+                        const int i = min(un.pair0 + e, last);
+                        const float c = s_cos[buf][i], s = s_sin[buf][i], f = v[e], g = w[e];
+                        v[e] = f * c - g * s;
+                        w[e] = f * s + g * c;
                     }
                 }
             }
-            uint16_t *dst;
-            if (hd < a.q_heads)
-                dst = static_cast<uint16_t *>(a.q_out) + t * a.qo_st + hd * a.qo_sh;
-            else if (!is_v)
-                dst = static_cast<uint16_t *>(kv.k) + page * kv.ks_page + off * kv.ks_tok + (hd - a.q_heads) * kv.ks_head;
-            else
-                dst = static_cast<uint16_t *>(kv.v) + page * kv.vs_page + off * kv.vs_tok + (hd - first_v) * kv.vs_head;
-            elem_store8<VEC, DST>(dst, is_v ? uv.d0 : uqk.d0, is_v ? uv.n0 : uqk.n0, x[k]);
-            elem_store8<VEC, DST>(dst, is_v ? uv.d1 : uqk.d1, is_v ? uv.n1 : uqk.n1, y[k]);
+            const int page = s_place[buf].page, off = s_place[buf].off;
+            if (mine && (is_q || page >= 0)) {
+                uint16_t *to = is_q ? dst : dst + page * d_page + off * d_tok;
+                elem_store8<VEC, DST>(to, un.d0, n0, v);
+                elem_store8<VEC, DST>(to, un.d1, n1, w);
+            }
+            if (is_q) dst += step * a.qo_st;
+            t += step;
+            buf ^= 1;
         }
-        head += HEADS * side;
-        request(head);
     }
 }
 
-template <bool VEC, int SRC, int DST, int HEADS>
-cudaError_t launch_heads(const RopeArgs &a, dim3 grid, int threads, int per, int per_head, cudaStream_t s)
+template <bool VEC, int SRC, int DST>
+cudaError_t launch(const RopeArgs &a, int sm_count, cudaStream_t s)
 {
+    const int heads = a.q_heads + 2 * a.kv.kv_heads, half = a.rot / 2;
+    const int units = (half + 7) / 8 + (a.kv.dim - a.rot + 15) / 16, v_units = (a.kv.dim + 15) / 16;
+    const int per_head = units > v_units ? units : v_units;
+    // few tokens: spread the heads of one over several blocks, so that the
+    // call is as long as one block's few loads
+    int per = heads;
+    while (per * per_head > kMaxThreads || (per > 4 && static_cast<int64_t>(a.tokens) * ((heads + per - 1) / per) < sm_count))
+        per = (per + 1) / 2;
+    const int threads = (per * per_head + 31) / 32 * 32 + 32, groups = (heads + per - 1) / per;
+    // blocks that fit on the GPU at once go through the tokens
+    auto fn = mbg_rope_kernel<VEC, SRC, DST>;
+    static std::atomic<int> fit[kMaxThreads / 32 + 2];  // blocks per SM, by warps (0: not asked yet)
+    int per_sm = fit[threads / 32].load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, threads, 0);
+        if (e != cudaSuccess) return e;
+        if (per_sm < 1) per_sm = 1;
+        fit[threads / 32].store(per_sm, std::memory_order_relaxed);
+    }
+    int64_t blocks = static_cast<int64_t>(per_sm) * sm_count / groups;
+    if (blocks < 1) blocks = 1;
+    if (blocks > a.tokens) blocks = a.tokens;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(groups));
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -194,29 +311,7 @@ cudaError_t launch_heads(const RopeArgs &a, dim3 grid, int threads, int per, int
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mbg_rope_kernel<VEC, SRC, DST, HEADS>, a, per, per_head);
-}
-
-template <bool VEC, int SRC, int DST>
-cudaError_t launch(const RopeArgs &a, int sm_count, cudaStream_t s)
-{
-    // few tokens: spread the heads of one over several blocks, so that the
-    // call is as long as one block's few loads
-    const int heads = a.q_heads + 2 * a.kv.kv_heads;
-    int per = heads;
-    while (per > 4 && static_cast<int64_t>(a.tokens) * ((heads + per - 1) / per) < sm_count) per = (per + 1) / 2;
-    const int half = a.rot / 2;
-    const int units = (half + 7) / 8 + (a.kv.dim - a.rot + 15) / 16, v_units = (a.kv.dim + 15) / 16;
-    const int per_head = units > v_units ? units : v_units;
-    const dim3 grid(static_cast<unsigned>(a.tokens), static_cast<unsigned>((heads + per - 1) / per));
-    // many heads per block: each thread takes three or more, three requested
-    // at once
-    const bool deep = VEC && per >= 12;
-    int side = deep ? (per + 2) / 3 : per;
-    while (side > 1 && side * per_head > (deep ? 192 : kMaxThreads)) side = (side + 1) / 2;
-    const int threads = (side * per_head + 31) / 32 * 32;
-    if (deep) return launch_heads<VEC, SRC, DST, VEC ? 3 : 1>(a, grid, threads, per, per_head, s);
-    return launch_heads<VEC, SRC, DST, 1>(a, grid, threads, per, per_head, s);
+    return cudaLaunchKernelEx(&cfg, fn, a, per, per_head);
 }
 
 template <int SRC, int DST>

@@ -25,15 +25,17 @@ ELEM_F32, ELEM_F16, ELEM_BF16 = 0, 1, 5
 _ATTN_COUNTER_BYTES = 8192  # GEMV_ATTN_COUNTER_BYTES
 NORM_LAYER, NORM_POST, NORM_UNIT_OFFSET = 1, 2, 4
 
-_elems = None
+torch = _Tensor = None  # looked up by _need_torch: importing the package does not import torch
+_elems = {}
 
 
-def _elem(dtype) -> Optional[int]:
-    global _elems
-    if _elems is None:
-        torch = _mbg._torch()
-        _elems = {torch.float32: ELEM_F32, torch.float16: ELEM_F16, torch.bfloat16: ELEM_BF16}
-    return _elems.get(dtype)
+def _need_torch():
+    global torch, _Tensor
+    if torch is None:
+        import torch as module
+
+        _elems.update({module.float32: ELEM_F32, module.float16: ELEM_F16, module.bfloat16: ELEM_BF16})
+        torch, _Tensor = module, module.Tensor
 
 
 class _KvStruct(ctypes.Structure):
@@ -47,13 +49,11 @@ class _KvStruct(ctypes.Structure):
 
 def _declare(L):
     vp, i32, i64, st = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int
-    f32 = ctypes.c_float
     sig = {
-        "gemv_attn_paged": [vp, vp, vp, vp, vp, vp, i32, f32, i32, vp, vp, vp, ctypes.c_size_t, vp],
+        "gemv_attn_paged": [vp, vp, vp],
         "gemv_kv_evict_plan": [vp, vp, i32, i32, i32, vp, i64, vp, vp],
         "gemv_kv_evict_apply": [vp, vp, i64, vp, vp, i32, vp],
-        "gemv_rope_append": [vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, vp, i64, i32, vp, vp, vp, vp, vp,
-                             i32, i32, vp],
+        "gemv_rope_append": [vp, vp, vp],
         "gemv_norm_residual": [vp, vp],
     }
     for name, args in sig.items():
@@ -67,45 +67,45 @@ def _declare(L):
     return L
 
 
-_pairs = {}
+# The argument structures of include/gemv.h, packed in one go.
+_ATTN = struct.Struct("PqqPqqPPPPNiif0q")
+_ROPE = struct.Struct("PqqPqqPqqPqqPqPPPPPiiiiii0q")
+_NORM = struct.Struct("PqiPqiPqiPqiPqiPqiPqiPqiqqffI0q")
 
 
-def _pair(a: int, b: int):
-    """Two strides as a C array (kept: a program has few)."""
-    got = _pairs.get((a, b))
-    if got is None:
-        if len(_pairs) > 4096:
-            _pairs.clear()
-        got = _pairs[(a, b)] = (ctypes.c_int64 * 2)(a, b)
-    return got
+def _operand(t, name, dtype, shape, index):
+    """Strides of a tensor of this type and shape, on CUDA device `index`, whose last dimension is contiguous."""
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == index and t.shape == shape:
+        strides = t.stride()
+        if not strides or strides[-1] == 1 or shape[-1] <= 1:
+            return strides
+    _refuse(t, name, dtype, shape, index)
 
 
-def _operand(t, name, dtype, shape, device):
-    """A CUDA tensor of this type and shape whose last dimension is contiguous."""
-    torch = _mbg._torch()
-    if not isinstance(t, torch.Tensor):
+def _refuse(t, name, dtype, shape, index):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if shape and shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
+    raise ValueError(f"the last dimension of {name} must be contiguous")
 
 
-def _dense(t, name, dtype, shape, device):
-    _operand(t, name, dtype, shape, device)
+def _dense(t, name, dtype, shape, index):
+    """Address of a contiguous tensor."""
+    _operand(t, name, dtype, shape, index)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _on(stream):
     """Context in which tensors belong to the stream that a call runs on."""
-    torch = _mbg._torch()
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream)
     return torch.cuda.stream(stream)  # None: no change
@@ -130,36 +130,36 @@ class PagedKV:
     """
 
     def __init__(self, k, v, page_table, scores=None, stamps=None):
-        torch = _mbg._torch()
-        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        _need_torch()
+        if not isinstance(k, _Tensor) or k.dim() != 4:
             raise ValueError("k must be a tensor [pages, page_size, kv_heads, head_dim]")
         if k.dtype not in (torch.float16, torch.bfloat16):
             raise TypeError(f"k has dtype {k.dtype}, expected float16 or bfloat16")
-        _operand(k, "k", k.dtype, k.shape, k.device)
-        _operand(v, "v", k.dtype, k.shape, k.device)
-        if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        index = k.get_device()
+        _operand(k, "k", k.dtype, k.shape, max(index, 0))
+        _operand(v, "v", k.dtype, k.shape, index)
+        if not isinstance(page_table, _Tensor) or page_table.dim() != 2:
             raise ValueError("page_table must be a tensor [batch, max_pages]")
-        _operand(page_table, "page_table", torch.int32, page_table.shape, k.device)
+        _operand(page_table, "page_table", torch.int32, page_table.shape, index)
         pages, self.page_size, self.kv_heads, self.head_dim = k.shape
         self.batch, self.max_pages = page_table.shape
         self.capacity = self.max_pages * self.page_size
-        self.device, self.dtype = k.device, k.dtype
+        self.device, self.index, self.dtype = k.device, index, k.dtype
         per_slot = (self.batch, self.kv_heads, self.capacity)
         if scores is not None:
-            _dense(scores, "scores", torch.float32, per_slot, k.device)
+            _dense(scores, "scores", torch.float32, per_slot, index)
         if stamps is not None:
-            _dense(stamps, "stamps", torch.int32, per_slot, k.device)
+            _dense(stamps, "stamps", torch.int32, per_slot, index)
         self.k, self.v, self.page_table, self.scores, self.stamps = k, v, page_table, scores, stamps
         self._s = _KvStruct(
             k.data_ptr(), v.data_ptr(), k.stride()[:3], v.stride()[:3], page_table.data_ptr(), page_table.stride(0),
             pages, None if scores is None else scores.data_ptr(), None if stamps is None else stamps.data_ptr(),
-            _elem(k.dtype), self.page_size, self.max_pages, self.batch, self.kv_heads, self.head_dim)
+            _elems[k.dtype], self.page_size, self.max_pages, self.batch, self.kv_heads, self.head_dim)
         self._at = ctypes.addressof(self._s)
         self._workspaces = {}
         self._lib = _mbg.lib()
 
     def _workspace(self, q_heads, weights, ptr, stream):
-        torch = _mbg._torch()
         capture = 0
         if stream is not None or torch.cuda.is_current_stream_capturing():
             capture = self._lib.gemv_capture_id(ptr)
@@ -189,7 +189,7 @@ class RopeTable:
     def __init__(self, rot_dim: int, sections: Optional[Sequence[int]] = None, theta: float = 10000.0,
                  pairs: bool = False, per_axis: bool = False, frequencies: Optional[Sequence[float]] = None,
                  device="cuda"):
-        torch = _mbg._torch()
+        _need_torch()
         half = rot_dim // 2
         if rot_dim < 0 or rot_dim % 2:
             raise ValueError("rot_dim must be even and not negative")
@@ -214,6 +214,7 @@ class RopeTable:
         self.rot_dim, self.axes, self.pairs = rot_dim, len(sections), bool(pairs)
         self.turns = torch.tensor(turns, dtype=torch.int64).to(device)
         self.axis = torch.tensor([a for a, n in enumerate(sections) for _ in range(n)], dtype=torch.uint8).to(device)
+        self.index = self.turns.get_device()
         self._turns_at, self._axis_at = self.turns.data_ptr(), self.axis.data_ptr()
 
 
@@ -228,44 +229,41 @@ def gemv_attn_paged(cache: PagedKV, q, lengths, out=None, scale: Optional[float]
     ``accumulate``: adds the weights, summed over the query heads of a cached
     head, to cache.scores, or with ``scores_out`` writes the sums there.  A
     sequence of length 0 gives zeros (and lse -inf)."""
-    torch = _mbg._torch()
-    device = cache.device
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+    index = cache.index
+    if not isinstance(q, _Tensor) or q.dim() != 3:
         raise ValueError("q must be a tensor [batch, q_heads, head_dim]")
     heads = q.shape[1]
     shape = (cache.batch, heads, cache.head_dim)
-    _operand(q, "q", cache.dtype, shape, device)
+    qs = _operand(q, "q", cache.dtype, shape, index)
     if heads < 1 or heads % cache.kv_heads:
         raise ValueError(f"q has {heads} heads, expected a multiple of {cache.kv_heads}")
-    _dense(lengths, "lengths", torch.int32, (cache.batch,), device)
+    n_ptr = _dense(lengths, "lengths", torch.int32, (cache.batch,), index)
     if window < 0:
         raise ValueError("window must not be negative")
     if out is None:
         with _on(stream):
-            out = torch.empty(shape, dtype=cache.dtype, device=device)
+            out = torch.empty(shape, dtype=cache.dtype, device=cache.device)
+        os = out.stride()
     else:
-        _operand(out, "out", cache.dtype, shape, device)
-    if lse is not None:
-        _dense(lse, "lse", torch.float32, (cache.batch, heads), device)
-    s_ptr = None
+        os = _operand(out, "out", cache.dtype, shape, index)
+    l_ptr = 0 if lse is None else _dense(lse, "lse", torch.float32, (cache.batch, heads), index)
+    s_ptr = 0
     if accumulate:
         if cache.scores is None:
             raise ValueError("accumulate needs a cache with scores")
         if scores_out is None:
-            scores_out = cache.scores
+            s_ptr = cache.scores.data_ptr()
         else:
-            _dense(scores_out, "scores_out", torch.float32, cache.scores.shape, device)
-        s_ptr = scores_out.data_ptr()
+            s_ptr = _dense(scores_out, "scores_out", torch.float32, cache.scores.shape, index)
     elif scores_out is not None:
         raise ValueError("scores_out goes with accumulate=True")
     if scale is None:
         scale = cache.head_dim ** -0.5
     ptr = _mbg._stream_ptr(stream)
     ws = cache._workspace(heads, accumulate, ptr, stream)
-    qs, os = q.stride(), out.stride()
-    st = cache._lib.gemv_attn_paged(cache._at, q.data_ptr(), _pair(qs[0], qs[1]), lengths.data_ptr(), out.data_ptr(),
-                                    _pair(os[0], os[1]), heads, scale, window,
-                                    None if lse is None else lse.data_ptr(), s_ptr, ws[0], ws[1], ptr)
+    st = cache._lib.gemv_attn_paged(
+        cache._at, _ATTN.pack(q.data_ptr(), qs[0], qs[1], out.data_ptr(), os[0], os[1], n_ptr, l_ptr, s_ptr, ws[0],
+                              ws[1], heads, window, scale), ptr)
     if st:
         _mbg._raise(st, "gemv_attn_paged")
     return out
@@ -283,53 +281,54 @@ def gemv_rope_append(cache: PagedKV, q, k, v, positions, slots, rope: RopeTable,
     tokens' sequences (default: token t belongs to sequence t).  stamps: int32
     [tokens], the tokens' numbers (default: the slots) for a cache with stamps.
     q_out: [tokens, q_heads, head_dim] of the cache's type."""
-    torch = _mbg._torch()
-    device = cache.device
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+    index = cache.index
+    if not isinstance(q, _Tensor) or q.dim() != 3:
         raise ValueError("q must be a tensor [tokens, q_heads, head_dim]")
-    elem = _elem(q.dtype)
+    dtype = q.dtype
+    elem = _elems.get(dtype)
     if elem is None:
-        raise TypeError(f"q has dtype {q.dtype}, expected float32, float16 or bfloat16")
+        raise TypeError(f"q has dtype {dtype}, expected float32, float16 or bfloat16")
     tokens, heads, dim = q.shape
-    _operand(q, "q", q.dtype, (tokens, heads, cache.head_dim), device)
-    kv_shape = (tokens, cache.kv_heads, dim)
-    _operand(k, "k", q.dtype, kv_shape, device)
-    _operand(v, "v", q.dtype, kv_shape, device)
+    q_shape, kv_shape = (tokens, heads, cache.head_dim), (tokens, cache.kv_heads, dim)
+    qs = _operand(q, "q", dtype, q_shape, index)
+    ks = _operand(k, "k", dtype, kv_shape, index)
+    vs = _operand(v, "v", dtype, kv_shape, index)
     if rope.rot_dim > dim:
         raise ValueError(f"the rope turns {rope.rot_dim} elements, a head has {dim}")
-    if rope.turns.device != device:
-        raise ValueError(f"the rope table is on {rope.turns.device}, expected {device}")
-    _operand(positions, "positions", torch.int32, (rope.axes, tokens), device)
-    _dense(slots, "slots", torch.int32, (tokens,), device)
+    if rope.index != index:
+        raise ValueError(f"the rope table is on {rope.turns.device}, expected {cache.device}")
+    ps = _operand(positions, "positions", torch.int32, (rope.axes, tokens), index)
+    per_token = (tokens,)
+    s_ptr = _dense(slots, "slots", torch.int32, per_token, index)
+    b_ptr = t_ptr = 0
     if seq is not None:
-        _dense(seq, "seq", torch.int32, (tokens,), device)
+        b_ptr = _dense(seq, "seq", torch.int32, per_token, index)
     elif tokens > cache.batch:
         raise ValueError(f"{tokens} tokens for {cache.batch} sequences: seq is needed")
     if stamps is not None:
-        _dense(stamps, "stamps", torch.int32, (tokens,), device)
+        t_ptr = _dense(stamps, "stamps", torch.int32, per_token, index)
     if q_out is None:
         with _on(stream):
-            q_out = torch.empty((tokens, heads, dim), dtype=cache.dtype, device=device)
+            q_out = torch.empty(q_shape, dtype=cache.dtype, device=cache.device)
+        os = q_out.stride()
     else:
-        _operand(q_out, "q_out", cache.dtype, (tokens, heads, dim), device)
-    qs, ks, vs, os = q.stride(), k.stride(), v.stride(), q_out.stride()
+        os = _operand(q_out, "q_out", cache.dtype, q_shape, index)
     st = cache._lib.gemv_rope_append(
-        cache._at, elem, q.data_ptr(), _pair(qs[0], qs[1]), k.data_ptr(), _pair(ks[0], ks[1]), v.data_ptr(),
-        _pair(vs[0], vs[1]), q_out.data_ptr(), _pair(os[0], os[1]), tokens, heads, positions.data_ptr(),
-        positions.stride(0), rope.axes, slots.data_ptr(), None if seq is None else seq.data_ptr(),
-        None if stamps is None else stamps.data_ptr(), rope._turns_at, rope._axis_at, rope.rot_dim,
-        1 if rope.pairs else 0, _mbg._stream_ptr(stream))
+        cache._at, _ROPE.pack(q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+                              q_out.data_ptr(), os[0], os[1], positions.data_ptr(), ps[0], s_ptr, b_ptr, t_ptr,
+                              rope._turns_at, rope._axis_at, elem, tokens, heads, rope.axes, rope.rot_dim, rope.pairs),
+        _mbg._stream_ptr(stream))
     if st:
         _mbg._raise(st, "gemv_rope_append")
     return q_out
 
 
 def _moves(cache, moves, counts):
-    torch = _mbg._torch()
-    if not isinstance(moves, torch.Tensor) or moves.dim() != 4:
+    if not isinstance(moves, _Tensor) or moves.dim() != 4:
         raise ValueError("moves must be a tensor [batch, kv_heads, max_moves, 2]")
-    _dense(moves, "moves", torch.int32, (cache.batch, cache.kv_heads, moves.shape[2], 2), cache.device)
-    _dense(counts, "counts", torch.int32, (cache.batch, cache.kv_heads), cache.device)
+    room = moves.shape[2]
+    return (_dense(moves, "moves", torch.int32, (cache.batch, cache.kv_heads, room, 2), cache.index), room,
+            _dense(counts, "counts", torch.int32, (cache.batch, cache.kv_heads), cache.index))
 
 
 def gemv_kv_evict_plan(cache: PagedKV, lengths, keep: int, sinks: int = 0, recent: int = 0, moves=None, counts=None,
@@ -341,12 +340,11 @@ def gemv_kv_evict_plan(cache: PagedKV, lengths, keep: int, sinks: int = 0, recen
     moves: int32 [batch, kv_heads, max_moves, 2], the first counts[b, h] pairs
     (from, to) are written; max_moves at least min(keep, capacity - keep).
     Nothing in the cache changes."""
-    torch = _mbg._torch()
     if cache.scores is None or cache.stamps is None:
         raise ValueError("eviction needs a cache with scores and stamps")
     if keep < 1 or sinks < 0 or recent < 0:
         raise ValueError("keep must be at least 1, sinks and recent not negative")
-    _dense(lengths, "lengths", torch.int32, (cache.batch,), cache.device)
+    n_ptr = _dense(lengths, "lengths", torch.int32, (cache.batch,), cache.index)
     most = max(1, min(keep, cache.capacity - keep))
     if moves is None or counts is None:
         with _on(stream):
@@ -354,11 +352,11 @@ def gemv_kv_evict_plan(cache: PagedKV, lengths, keep: int, sinks: int = 0, recen
                 moves = torch.empty((cache.batch, cache.kv_heads, most, 2), dtype=torch.int32, device=cache.device)
             if counts is None:
                 counts = torch.empty((cache.batch, cache.kv_heads), dtype=torch.int32, device=cache.device)
-    _moves(cache, moves, counts)
-    if moves.shape[2] < most:
-        raise ValueError(f"moves has room for {moves.shape[2]}, at least {most} are needed")
-    st = cache._lib.gemv_kv_evict_plan(cache._at, lengths.data_ptr(), keep, sinks, recent, moves.data_ptr(),
-                                       moves.shape[2], counts.data_ptr(), _mbg._stream_ptr(stream))
+    m_ptr, room, c_ptr = _moves(cache, moves, counts)
+    if room < most:
+        raise ValueError(f"moves has room for {room}, at least {most} are needed")
+    st = cache._lib.gemv_kv_evict_plan(cache._at, n_ptr, keep, sinks, recent, m_ptr, room, c_ptr,
+                                       _mbg._stream_ptr(stream))
     if st:
         _mbg._raise(st, "gemv_kv_evict_plan")
     return moves, counts
@@ -369,15 +367,11 @@ def gemv_kv_evict_apply(cache: PagedKV, moves, counts, lengths, keep: int, strea
 
     ``lengths`` may be None (left to the caller).  A plan may be carried out on
     several caches that are filled alike."""
-    torch = _mbg._torch()
     if keep < 1:
         raise ValueError("keep must be at least 1")
-    _moves(cache, moves, counts)
-    if lengths is not None:
-        _dense(lengths, "lengths", torch.int32, (cache.batch,), cache.device)
-    st = cache._lib.gemv_kv_evict_apply(cache._at, moves.data_ptr(), moves.shape[2], counts.data_ptr(),
-                                        None if lengths is None else lengths.data_ptr(), keep,
-                                        _mbg._stream_ptr(stream))
+    m_ptr, room, c_ptr = _moves(cache, moves, counts)
+    n_ptr = None if lengths is None else _dense(lengths, "lengths", torch.int32, (cache.batch,), cache.index)
+    st = cache._lib.gemv_kv_evict_apply(cache._at, m_ptr, room, c_ptr, n_ptr, keep, _mbg._stream_ptr(stream))
     if st:
         _mbg._raise(st, "gemv_kv_evict_apply")
 
@@ -390,23 +384,23 @@ def gemv_kv_evict(cache: PagedKV, lengths, keep: int, sinks: int = 0, recent: in
     return moves, counts
 
 
-_NORM = struct.Struct("PqiPqiPqiPqiPqiPqiPqiPqiqqffI0q")
 _NONE = (0, 0, 0)
 
 
-def _rows(t, name, rows, width, device, dtype=None):
+def _rows(t, name, rows, width, index):
     """(address, row stride, type) of an operand [rows, width] or [width]."""
-    torch = _mbg._torch()
-    if not isinstance(t, torch.Tensor):
+    if t is None:
+        return _NONE
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    elem = _elem(t.dtype)
+    dtype = t.dtype
+    elem = _elems.get(dtype)
     if elem is None:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected float32, float16 or bfloat16")
-    if t.dim() == 1 and dtype is None:
-        _operand(t, name, t.dtype, (width,), device)
+        raise TypeError(f"{name} has dtype {dtype}, expected float32, float16 or bfloat16")
+    if t.dim() == 1:
+        _operand(t, name, dtype, (width,), index)
         return t.data_ptr(), 0, elem
-    _operand(t, name, dtype or t.dtype, (rows, width), device)
-    return t.data_ptr(), t.stride(0), elem
+    return t.data_ptr(), _operand(t, name, dtype, (rows, width), index)[0], elem
 
 
 def gemv_norm_residual(y, x, post: bool = False, post_weight=None, gate=None, alpha: float = 1.0, pre_weight=None,
@@ -424,37 +418,40 @@ def gemv_norm_residual(y, x, post: bool = False, post_weight=None, gate=None, al
     stands for 1 + pre_weight.  out: like x (may be x).  h: the next block's
     input, [rows, width], ``h_dtype`` float16 by default; ``pre=False``: none
     (h is None).  h is computed from the unrounded sum."""
-    torch = _mbg._torch()
-    if not isinstance(y, torch.Tensor) or y.dim() != 2:
+    if torch is None:
+        _need_torch()
+    if not isinstance(y, _Tensor) or y.dim() != 2:
         raise ValueError("y must be a tensor [rows, width]")
-    if kind not in ("rms", "layer"):
+    if not isinstance(x, _Tensor) or x.dim() != 2:
+        raise ValueError("x must be a tensor [rows, width]")
+    if kind != "rms" and kind != "layer":
         raise ValueError("kind must be 'rms' or 'layer'")
     if post_weight is not None and not post:
         raise ValueError("post_weight goes with post=True")
     if not pre and (pre_weight is not None or pre_bias is not None or h is not None):
         raise ValueError("pre_weight, pre_bias and h go with pre=True")
     rows, width = y.shape
-    dev = y.device
-    y_ = _rows(y, "y", rows, width, dev, y.dtype)
-    if not isinstance(x, torch.Tensor):
-        raise TypeError("x must be a torch.Tensor")
-    x_ = _rows(x, "x", rows, width, dev, x.dtype)
+    index = max(y.get_device(), 0)
+    y_, x_ = _rows(y, "y", rows, width, index), _rows(x, "x", rows, width, index)
     if out is None or (pre and h is None):
         with _on(stream):
             if out is None:
-                out = torch.empty((rows, width), dtype=x.dtype, device=dev)
+                out = torch.empty((rows, width), dtype=x.dtype, device=y.device)
             if pre and h is None:
-                h = torch.empty((rows, width), dtype=h_dtype or torch.float16, device=dev)
+                h = torch.empty((rows, width), dtype=h_dtype or torch.float16, device=y.device)
+    o_ = (out.data_ptr(), _operand(out, "out", x.dtype, (rows, width), index)[0], x_[2])
+    h_ = _NONE
+    if pre:
+        h_ = _rows(h, "h", rows, width, index)
+        if h.dim() != 2 or (h_dtype is not None and h.dtype is not h_dtype):
+            _refuse(h, "h", h_dtype or h.dtype, (rows, width), index)
     flags = (NORM_LAYER if kind == "layer" else 0) | (NORM_POST if post else 0) | (NORM_UNIT_OFFSET if unit_offset else 0)
-    packed = _NORM.pack(
-        *y_, *x_, *(_rows(gate, "gate", rows, width, dev) if gate is not None else _NONE),
-        *(_rows(post_weight, "post_weight", rows, width, dev) if post_weight is not None else _NONE),
-        *(_rows(pre_weight, "pre_weight", rows, width, dev) if pre_weight is not None else _NONE),
-        *(_rows(pre_bias, "pre_bias", rows, width, dev) if pre_bias is not None else _NONE),
-        *_rows(out, "out", rows, width, dev, x.dtype),
-        *(_rows(h, "h", rows, width, dev, h_dtype or h.dtype) if pre else _NONE),
-        rows, width, alpha, eps, flags)
-    st = _mbg.lib().gemv_norm_residual(packed, _mbg._stream_ptr(stream))
+    st = _mbg.lib().gemv_norm_residual(
+        _NORM.pack(*y_, *x_, *_rows(gate, "gate", rows, width, index),
+                   *_rows(post_weight, "post_weight", rows, width, index),
+                   *_rows(pre_weight, "pre_weight", rows, width, index),
+                   *_rows(pre_bias, "pre_bias", rows, width, index), *o_, *h_, rows, width, alpha, eps, flags),
+        _mbg._stream_ptr(stream))
     if st:
         _mbg._raise(st, "gemv_norm_residual")
     return out, h

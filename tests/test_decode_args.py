@@ -26,16 +26,21 @@ def at(s):
     return ctypes.addressof(s)
 
 
-TWO = (ctypes.c_int64 * 2)(128, 64)
-NEG = (ctypes.c_int64 * 2)(-1, 64)
+TWO = (128, 64)
+NEG = (-1, 64)
 
 
-def attn(s, **change):
-    a = dict(q=FAKE, qs=TWO, lengths=FAKE, out=FAKE, os=TWO, heads=8, scale=1.0, window=0, lse=None, sums=None,
-             ws=FAKE, n=1 << 40)
-    a.update(change)
-    return mbg.lib().gemv_attn_paged(at(s), a["q"], a["qs"], a["lengths"], a["out"], a["os"], a["heads"], a["scale"],
-                                     a["window"], a["lse"], a["sums"], a["ws"], a["n"], None)
+def attn(s, q=FAKE, qs=TWO, lengths=FAKE, out=FAKE, os=TWO, heads=8, scale=1.0, window=0, lse=0, sums=0, ws=FAKE,
+         n=1 << 40):
+    args = decode._ATTN.pack(q, *qs, out, *os, lengths, lse, sums, ws, n, heads, window, scale)
+    return mbg.lib().gemv_attn_paged(at(s), args, None)
+
+
+def rope(s=None, elem=0, q=FAKE, qs=TWO, k=FAKE, ks=TWO, v=FAKE, vs=TWO, out=FAKE, os=TWO, tokens=4, heads=8,
+         pos=FAKE, ps=4, axes=1, slots=FAKE, seq=0, stamps=0, turns=FAKE, axis=FAKE, rot=64, pairs=0):
+    args = decode._ROPE.pack(q, *qs, k, *ks, v, *vs, out, *os, pos, ps, slots, seq, stamps, turns, axis, elem, tokens,
+                             heads, axes, rot, pairs)
+    return mbg.lib().gemv_rope_append(at(s or kv()), args, None)
 
 
 BAD_CACHES = [(dict(elem=0), 1), (dict(elem=7), 1), (dict(batch=-1), 1), (dict(kv_heads=0), 1), (dict(head_dim=0), 1),
@@ -52,21 +57,21 @@ def test_every_call_checks_the_cache(change, status):
     assert attn(s) == status
     assert L.gemv_kv_evict_plan(at(s), FAKE, 64, 0, 0, FAKE, 64, FAKE, None) == status
     assert L.gemv_kv_evict_apply(at(s), FAKE, 64, FAKE, FAKE, 64, None) == status
-    assert L.gemv_rope_append(at(s), 0, FAKE, TWO, FAKE, TWO, FAKE, TWO, FAKE, TWO, 4, 8, FAKE, 4, 1, FAKE, None,
-                              None, FAKE, FAKE, 64, 0, None) == status
+    assert rope(s) == status
 
 
 def test_attn_refusals():
     s = kv()
-    for change in (dict(q=None), dict(lengths=None), dict(out=None), dict(ws=None), dict(heads=0), dict(heads=7),
-                   dict(window=-1), dict(qs=None), dict(os=None), dict(qs=NEG), dict(os=NEG), dict(n=16)):
+    for change in (dict(q=0), dict(lengths=0), dict(out=0), dict(ws=0), dict(heads=0), dict(heads=7),
+                   dict(window=-1), dict(qs=NEG), dict(os=NEG), dict(n=16)):
         assert attn(s, **change) == mbg.ERR_INVALID_VALUE, change
     for change in (dict(q=FAKE + 1), dict(out=FAKE + 1), dict(lengths=FAKE + 2), dict(lse=FAKE + 2),
                    dict(sums=FAKE + 1), dict(ws=FAKE + 16)):
         assert attn(s, **change) == mbg.ERR_MISALIGNED, change
     assert attn(kv(scores=None), sums=FAKE) == mbg.ERR_INVALID_VALUE
     assert attn(kv(batch=0)) == mbg.OK
-    assert mbg.lib().gemv_attn_paged(None, FAKE, TWO, FAKE, FAKE, TWO, 8, 1.0, 0, None, None, FAKE, 1 << 40, None) == 1
+    assert mbg.lib().gemv_attn_paged(at(kv()), None, None) == mbg.ERR_INVALID_VALUE
+    assert mbg.lib().gemv_attn_paged(None, bytes(decode._ATTN.size), None) == mbg.ERR_INVALID_VALUE
 
 
 def test_attn_workspace_sizes():
@@ -105,23 +110,16 @@ def test_evict_refusals():
 
 
 def test_rope_refusals():
-    L = mbg.lib()
-
-    def rope(s=None, elem=0, q=FAKE, qs=TWO, k=FAKE, ks=TWO, v=FAKE, vs=TWO, out=FAKE, os=TWO, tokens=4, heads=8,
-             pos=FAKE, ps=4, axes=1, slots=FAKE, seq=None, stamps=None, turns=FAKE, axis=FAKE, rot=64, pairs=0):
-        s = s or kv()
-        return L.gemv_rope_append(at(s), elem, q, qs, k, ks, v, vs, out, os, tokens, heads, pos, ps, axes, slots, seq,
-                                  stamps, turns, axis, rot, pairs, None)
-
-    for change in (dict(elem=2), dict(qs=None), dict(ks=NEG), dict(vs=None), dict(os=NEG), dict(tokens=-1),
+    for change in (dict(elem=2), dict(qs=NEG), dict(ks=NEG), dict(vs=NEG), dict(os=NEG), dict(tokens=-1),
                    dict(heads=-1), dict(axes=0), dict(rot=63), dict(rot=66), dict(rot=-2), dict(ps=-1), dict(tokens=5),
-                   dict(q=None), dict(k=None), dict(v=None), dict(out=None), dict(pos=None), dict(slots=None),
-                   dict(turns=None), dict(axis=None)):
+                   dict(q=0), dict(k=0), dict(v=0), dict(out=0), dict(pos=0), dict(slots=0), dict(turns=0),
+                   dict(axis=0)):
         assert rope(**change) == mbg.ERR_INVALID_VALUE, change
     for change in (dict(q=FAKE + 2), dict(k=FAKE + 1), dict(v=FAKE + 2), dict(out=FAKE + 1), dict(pos=FAKE + 2),
                    dict(slots=FAKE + 1), dict(seq=FAKE + 2), dict(stamps=FAKE + 1), dict(turns=FAKE + 4)):
         assert rope(**change) == mbg.ERR_MISALIGNED, change
     assert rope(tokens=0) == mbg.OK
+    assert mbg.lib().gemv_rope_append(at(kv()), None, None) == mbg.ERR_INVALID_VALUE
 
 
 def test_norm_refusals():
@@ -150,8 +148,10 @@ def test_norm_refusals():
 
 
 def test_struct_layouts_match():
-    """The packed norm arguments and the cache structure have C's size: 8 operands of 24 bytes, two sizes, three words."""
+    """The packed arguments and the cache structure have the sizes of C's structures on a 64-bit machine."""
     assert decode._NORM.size == 8 * 24 + 2 * 8 + 3 * 4 + 4
+    assert decode._ATTN.size == 2 * 24 + 5 * 8 + 3 * 4 + 4
+    assert decode._ROPE.size == 4 * 24 + 7 * 8 + 6 * 4
     assert ctypes.sizeof(decode._KvStruct) == 2 * 8 + 6 * 8 + 5 * 8 + 6 * 4
 
 
