@@ -638,3 +638,16 @@ def test_binding_refusals():
         mbg.gemv_kv_evict_plan(cache, lens, 4)  # no scores
     with pytest.raises(ValueError):
         mbg.PagedKV(cache.k, cache.v, cache.page_table, scores=torch.zeros(2, 2, 5, device="cuda"))
+
+
+@pytest.mark.parametrize("kind", ["normal", "equal", "few values"])
+@pytest.mark.parametrize("keep,sinks,recent", [(2000, 4, 100), (50, 0, 0), (50, 3, 60), (5000, 2, 5000), (4990, 0, 4992)])
+def test_evict_a_few_slots_over_the_budget(keep, sinks, recent, kind):
+    """One to six slots too many, as in decode steps; rows where every slot is protected among them."""
+    lengths = [keep + k for k in (1, 2, 3, 4, 5, 6, 0)]
+    cache = make_cache(57, lengths, 2, 8, 16, F16, history=True)
+    if kind == "equal":
+        cache.scores.fill_(2.0)
+    elif kind == "few values":
+        cache.scores.copy_(torch.randint(0, 3, cache.scores.shape, device="cuda").float())
+    check_evict(cache, lengths, keep, sinks, recent)
