@@ -5,7 +5,9 @@ Every translation unit under ``csrc/`` is compiled for sm_103a only
 one shared library with the CUDA runtime linked statically.  ``ptxas -v``
 output (registers, spills, shared memory per kernel) is kept in
 ``_build/ptxas.log``.  Rebuilds only when a source or header is newer than
-the library.
+the library.  Beside it the host compiler makes ``_build/_mbgbinding.so`` from
+``csrc/binding.cpp``, for the installed torch: the quick form of the
+decode-step calls' argument checks.
 """
 
 from __future__ import annotations
@@ -22,6 +24,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmbgemv.so")
+BINDING = os.path.join(BUILD, "_mbgbinding.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -43,15 +46,36 @@ def _sources():
 
 def _deps():
     return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh"))
-            + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+            + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cpp"))
+            + glob.glob(os.path.join(INCLUDE, "*.h"))
             + [os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _build_binding():
+    """csrc/binding.cpp against the installed torch's headers, with the host compiler."""
+    import sysconfig
+
+    import torch
+
+    top = os.path.join(os.path.dirname(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    includes = [os.path.join(top, "include"), os.path.join(top, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+           f'-DMBG_TORCH_VERSION="{torch.__version__}"', f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-I{p}" for p in includes], os.path.join(CSRC, "binding.cpp"), "-L" + os.path.join(top, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-o", f"{BINDING}.{os.getpid()}.tmp"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("compiling binding.cpp failed")
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -68,9 +92,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, r
 
-    workers = min(len(srcs), os.cpu_count() or 4)
+    workers = min(len(srcs) + 1, os.cpu_count() or 4)
     with concurrent.futures.ThreadPoolExecutor(max_workers=workers) as ex:
+        binding = ex.submit(_build_binding)
         results = list(ex.map(compile_one, srcs))
+        binding.result()
     log = []
     for src, obj, r in results:
         log.append(f"== {os.path.basename(src)}\n{r.stdout}{r.stderr}")
@@ -79,6 +105,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}")
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         f.write("\n".join(log))
+    os.replace(f"{BINDING}.{os.getpid()}.tmp", BINDING)
     tmp = f"{LIB}.{os.getpid()}.tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *[o for _, o, _ in results]]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -27,15 +27,37 @@ NORM_LAYER, NORM_POST, NORM_UNIT_OFFSET = 1, 2, 4
 
 torch = _Tensor = None  # looked up by _need_torch: importing the package does not import torch
 _elems = {}
+_quick = None  # csrc/binding.cpp
 
 
 def _need_torch():
-    global torch, _Tensor
+    global torch, _Tensor, _quick
     if torch is None:
         import torch as module
 
         _elems.update({module.float32: ELEM_F32, module.float16: ELEM_F16, module.bfloat16: ELEM_BF16})
+        _quick = _load_binding(module)
         torch, _Tensor = module, module.Tensor
+
+
+def _load_binding(module):
+    """The compiled form of the calls below for the installed torch; it answers -1 where a call is not of the
+    common kind, and the Python form then checks it and says why."""
+    import importlib.machinery
+    import importlib.util
+
+    from . import build
+
+    lib = _mbg.lib()
+    loader = importlib.machinery.ExtensionFileLoader("_mbgbinding", build.BINDING)
+    binding = importlib.util.module_from_spec(importlib.util.spec_from_loader("_mbgbinding", loader))
+    loader.exec_module(binding)
+    if binding.torch_version != module.__version__:
+        raise RuntimeError(f"the binding was built for torch {binding.torch_version}, this is {module.__version__}: "
+                           "run memory_bound_gemv_gb300.build")
+    binding.use(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+        "gemv_attn_paged", "gemv_rope_append", "gemv_kv_evict_plan", "gemv_kv_evict_apply", "gemv_norm_residual")))
+    return binding
 
 
 class _KvStruct(ctypes.Structure):
@@ -216,6 +238,7 @@ class RopeTable:
         self.axis = torch.tensor([a for a, n in enumerate(sections) for _ in range(n)], dtype=torch.uint8).to(device)
         self.index = self.turns.get_device()
         self._turns_at, self._axis_at = self.turns.data_ptr(), self.axis.data_ptr()
+        self._packed = struct.pack("QQiiii", self._turns_at, self._axis_at, self.index, self.axes, rot_dim, self.pairs)
 
 
 def gemv_attn_paged(cache: PagedKV, q, lengths, out=None, scale: Optional[float] = None, window: int = 0, lse=None,
@@ -230,9 +253,17 @@ def gemv_attn_paged(cache: PagedKV, q, lengths, out=None, scale: Optional[float]
     head, to cache.scores, or with ``scores_out`` writes the sums there.  A
     sequence of length 0 gives zeros (and lse -inf)."""
     index = cache.index
+    if scale is None:
+        scale = cache.head_dim ** -0.5
     if not isinstance(q, _Tensor) or q.dim() != 3:
         raise ValueError("q must be a tensor [batch, q_heads, head_dim]")
     heads = q.shape[1]
+    if out is not None and not accumulate and scores_out is None and heads:
+        ptr = _mbg._stream_ptr(stream)
+        ws = cache._workspace(heads, False, ptr, stream)
+        st = _quick.attn(cache._at, index, q, lengths, out, lse, 0, ws[0], ws[1], scale, window, ptr)
+        if st == 0:
+            return out
     shape = (cache.batch, heads, cache.head_dim)
     qs = _operand(q, "q", cache.dtype, shape, index)
     if heads < 1 or heads % cache.kv_heads:
@@ -257,8 +288,6 @@ def gemv_attn_paged(cache: PagedKV, q, lengths, out=None, scale: Optional[float]
             s_ptr = _dense(scores_out, "scores_out", torch.float32, cache.scores.shape, index)
     elif scores_out is not None:
         raise ValueError("scores_out goes with accumulate=True")
-    if scale is None:
-        scale = cache.head_dim ** -0.5
     ptr = _mbg._stream_ptr(stream)
     ws = cache._workspace(heads, accumulate, ptr, stream)
     st = cache._lib.gemv_attn_paged(
@@ -282,6 +311,9 @@ def gemv_rope_append(cache: PagedKV, q, k, v, positions, slots, rope: RopeTable,
     [tokens], the tokens' numbers (default: the slots) for a cache with stamps.
     q_out: [tokens, q_heads, head_dim] of the cache's type."""
     index = cache.index
+    if q_out is not None and _quick.rope(cache._at, index, rope._packed, q, k, v, positions, slots, seq, stamps, q_out,
+                                         stream if stream is None else _mbg._stream_ptr(stream)) == 0:
+        return q_out
     if not isinstance(q, _Tensor) or q.dim() != 3:
         raise ValueError("q must be a tensor [tokens, q_heads, head_dim]")
     dtype = q.dtype
@@ -340,6 +372,9 @@ def gemv_kv_evict_plan(cache: PagedKV, lengths, keep: int, sinks: int = 0, recen
     moves: int32 [batch, kv_heads, max_moves, 2], the first counts[b, h] pairs
     (from, to) are written; max_moves at least min(keep, capacity - keep).
     Nothing in the cache changes."""
+    if moves is not None and _quick.plan(cache._at, cache.index, lengths, keep, sinks, recent, moves, counts,
+                                         stream if stream is None else _mbg._stream_ptr(stream)) == 0:
+        return moves, counts
     if cache.scores is None or cache.stamps is None:
         raise ValueError("eviction needs a cache with scores and stamps")
     if keep < 1 or sinks < 0 or recent < 0:
@@ -367,6 +402,9 @@ def gemv_kv_evict_apply(cache: PagedKV, moves, counts, lengths, keep: int, strea
 
     ``lengths`` may be None (left to the caller).  A plan may be carried out on
     several caches that are filled alike."""
+    if _quick.apply(cache._at, cache.index, moves, counts, lengths, keep,
+                    stream if stream is None else _mbg._stream_ptr(stream)) == 0:
+        return
     if keep < 1:
         raise ValueError("keep must be at least 1")
     m_ptr, room, c_ptr = _moves(cache, moves, counts)
@@ -420,16 +458,21 @@ def gemv_norm_residual(y, x, post: bool = False, post_weight=None, gate=None, al
     (h is None).  h is computed from the unrounded sum."""
     if torch is None:
         _need_torch()
-    if not isinstance(y, _Tensor) or y.dim() != 2:
-        raise ValueError("y must be a tensor [rows, width]")
-    if not isinstance(x, _Tensor) or x.dim() != 2:
-        raise ValueError("x must be a tensor [rows, width]")
     if kind != "rms" and kind != "layer":
         raise ValueError("kind must be 'rms' or 'layer'")
     if post_weight is not None and not post:
         raise ValueError("post_weight goes with post=True")
     if not pre and (pre_weight is not None or pre_bias is not None or h is not None):
         raise ValueError("pre_weight, pre_bias and h go with pre=True")
+    flags = (NORM_LAYER if kind == "layer" else 0) | (NORM_POST if post else 0) | (NORM_UNIT_OFFSET if unit_offset else 0)
+    if out is not None and (h is not None or not pre) and h_dtype is None and _quick.norm(
+            y, x, gate, post_weight, pre_weight, pre_bias, out, h, alpha, eps, flags,
+            stream if stream is None else _mbg._stream_ptr(stream)) == 0:
+        return out, h
+    if not isinstance(y, _Tensor) or y.dim() != 2:
+        raise ValueError("y must be a tensor [rows, width]")
+    if not isinstance(x, _Tensor) or x.dim() != 2:
+        raise ValueError("x must be a tensor [rows, width]")
     rows, width = y.shape
     index = max(y.get_device(), 0)
     y_, x_ = _rows(y, "y", rows, width, index), _rows(x, "x", rows, width, index)
@@ -445,7 +488,6 @@ def gemv_norm_residual(y, x, post: bool = False, post_weight=None, gate=None, al
         h_ = _rows(h, "h", rows, width, index)
         if h.dim() != 2 or (h_dtype is not None and h.dtype is not h_dtype):
             _refuse(h, "h", h_dtype or h.dtype, (rows, width), index)
-    flags = (NORM_LAYER if kind == "layer" else 0) | (NORM_POST if post else 0) | (NORM_UNIT_OFFSET if unit_offset else 0)
     st = _mbg.lib().gemv_norm_residual(
         _NORM.pack(*y_, *x_, *_rows(gate, "gate", rows, width, index),
                    *_rows(post_weight, "post_weight", rows, width, index),

@@ -651,3 +651,36 @@ def test_evict_a_few_slots_over_the_budget(keep, sinks, recent, kind):
     elif kind == "few values":
         cache.scores.copy_(torch.randint(0, 3, cache.scores.shape, device="cuda").float())
     check_evict(cache, lengths, keep, sinks, recent)
+
+
+def test_the_compiled_checks_take_the_common_calls_and_leave_the_others():
+    from memory_bound_gemv_gb300 import decode
+
+    cache = make_cache(72, [20, 20], 2, 64, 16, F16, fill=0.0, history=True)
+    lens = torch.tensor([20, 20], dtype=torch.int32, device="cuda")
+    q, out = normal(1, (2, 4, 64), F16), torch.empty(2, 4, 64, dtype=F16, device="cuda")
+    ws = cache._workspace(4, False, mbg._stream_ptr(None), None)
+
+    def attn(q=q, lens=lens, out=out, lse=None, window=0):
+        return decode._quick.attn(cache._at, 0, q, lens, out, lse, 0, ws[0], ws[1], 0.125, window, None)
+
+    assert attn() == 0 and attn(q=normal(1, (2, 8, 64), F16)[:, ::2]) == 0
+    for bad in (dict(q=q.float()), dict(q=q[:1]), dict(q=q[:, :3]), dict(q=q[..., :32]), dict(q=q.cpu()), dict(q=3),
+                dict(lens=lens.long()), dict(lens=lens[:1]), dict(out=None), dict(out=out[0]), dict(window=-1),
+                dict(window=1 << 40), dict(window="2"), dict(lse=out), dict(lens=torch.stack((lens, lens), 1)[:, 0])):
+        assert attn(**bad) == -1, bad
+    y = normal(2, (3, 32))
+    assert decode._quick.norm(y, y, None, None, None, None, y.clone(), None, 1.0, 1e-6, 0, None) == 0
+    for bad in ((y, y, None, None, None, None, y.half(), None), (y, y[:2], None, None, None, None, y, None),
+                (y, y, y[0][:31], None, None, None, y, None), (y.int(), y, None, None, None, None, y, None),
+                (y, y, None, None, None, None, y, y[0]), (y, None, None, None, None, None, y, None)):
+        assert decode._quick.norm(*bad, 1.0, 1e-6, 0, None) == -1
+    with pytest.raises(mbg.GemvError):  # a refusal of the library comes through the Python form
+        mbg.gemv_norm_residual(y, y.clone(), out=torch.zeros(1, 32, device="cuda").expand(3, 32), pre=False)
+    moves = torch.empty(2, 2, 16, 2, dtype=torch.int32, device="cuda")
+    counts = torch.empty(2, 2, dtype=torch.int32, device="cuda")
+    assert decode._quick.plan(cache._at, 0, lens, 16, 0, 0, moves, counts, None) == 0
+    assert decode._quick.apply(cache._at, 0, moves, counts, None, 16, None) == 0
+    assert decode._quick.plan(cache._at, 0, lens, 0, 0, 0, moves, counts, None) == -1
+    assert decode._quick.plan(cache._at, 0, lens, 16, 0, 0, moves[:, :, :3], counts, None) == -1
+    assert decode._quick.apply(cache._at, 0, moves.float(), counts, None, 16, None) == -1
