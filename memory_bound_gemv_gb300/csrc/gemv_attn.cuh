@@ -32,7 +32,7 @@
 // head size of 128.
 //
 // Split over the length: the rows (sequence x cached head) are cut into tiles
-// of 16 tokens; all tiles of the call are numbered and each CTA takes an equal
+// of 16 or 32 tokens; all tiles of the call are numbered and each CTA takes an equal
 // share of consecutive ones, whatever the lengths (they are read on the
 // device, so a captured graph serves any lengths).  A share's border that
 // falls close to a row's end moves there, so that short rows are not cut.  A
@@ -125,11 +125,24 @@ __device__ __forceinline__ float exp2_from(float x, float m)
     return exp2_approx(x - (m == -INFINITY ? 0.f : m));
 }
 
+// 16 bytes of a cached row, read once.  (Asking L2 for the whole 256 bytes
+// around them brings other heads' rows along when a row is shorter: 16 x 32768
+// tokens of four heads of 64 take 118 us then, 96 us without, and rows of 256
+// bytes gain nothing from it.)
+__device__ __forceinline__ uint4 ld_row16(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
 // Eight consecutive 16-bit elements at p, of which the first `left` exist.
 template <bool VEC>
 __device__ __forceinline__ uint4 load8(const uint16_t *p, int left)
 {
-    if (VEC) return ld_stream16(p);
+    if (VEC) return ld_row16(p);
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -140,12 +153,13 @@ __device__ __forceinline__ uint4 load8(const uint16_t *p, int left)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The tokens of a sequence that are attended to, and their tiles of 16.
+// The tokens of a sequence that are attended to, and their tiles.
 struct RowSpan {
     int first, len;         // tokens [first, len)
-    int tile0, tiles;       // 16-token tiles, tile0 = first / 16
+    int tile0, tiles;       // tiles of TOKENS tokens, tile0 = first / TOKENS
 };
 
+template <int TOKENS>
 __device__ __forceinline__ RowSpan row_span(const AttnArgs &a, int b)
 {
     RowSpan r;
@@ -154,8 +168,8 @@ __device__ __forceinline__ RowSpan row_span(const AttnArgs &a, int b)
     if (len > a.kv.capacity) len = static_cast<int>(a.kv.capacity);
     r.len = len;
     r.first = (a.window > 0 && len > a.window) ? len - a.window : 0;
-    r.tile0 = r.first >> 4;
-    r.tiles = len > r.first ? ((len + 15) >> 4) - r.tile0 : 0;
+    r.tile0 = r.first / TOKENS;
+    r.tiles = len > r.first ? (len + TOKENS - 1) / TOKENS - r.tile0 : 0;
     return r;
 }
 
@@ -173,7 +187,7 @@ __device__ __forceinline__ TilePlace place_of(const KvView &kv, const int32_t *t
 {
     TilePlace p = {-1, 0, 0, 0};
     const int slot = tile * 16 + (WHOLE ? 0 : threadIdx.x & 15);
-    if (wanted && (WHOLE || (slot >= first && slot < len))) {
+    if (wanted && slot < len && slot + (WHOLE ? 15 : 0) >= first) {
         const int idx = kv.page_shift >= 0 ? slot >> kv.page_shift : slot / kv.page_size;
         p.off = slot - idx * kv.page_size;
         p.page = __ldg(table + idx);
@@ -188,9 +202,15 @@ __device__ __forceinline__ TilePlace place_of(const KvView &kv, const int32_t *t
     return p;
 }
 
+template <int DC, int NT>
+constexpr int kTilesAtOnce = DC * NT == 1 ? 2 : 1;
+
 template <typename T, int DC, int NT, int NW, bool VEC, bool WHOLE>
 struct Kernel {
     static constexpr int kWarps = NW, kThreads = NW * 32;
+    // tiles of 16 tokens that a warp takes at once: two of narrow heads, so that
+    // as many bytes are under way as with wide ones
+    static constexpr int MT = kTilesAtOnce<DC, NT>, kTokens = 16 * MT;
     // CTAs whose parts of a row are joined first, before the groups are
     static constexpr int kGroupCtas = 4 * NW;
     static constexpr int kHeads = 8 * NT;           // query heads of one tile
@@ -317,7 +337,7 @@ struct Kernel {
     {
         const int hks = a.kv.kv_heads * a.head_tiles;
         while (at.b < a.kv.batch) {  // (the last share ends with the last row)
-            const RowSpan span = row_span(a, at.b);
+            const RowSpan span = row_span<kTokens>(a, at.b);
             const int n = span.tiles, cost = n + w.lead;
             if (n == 0) {
                 ++at.b;
@@ -385,10 +405,17 @@ struct Kernel {
                     }
             }
         };
-        uint4 kx[2][2 * DC], vx[DC][4];
+        uint4 kx[MT][2][2 * DC], vx[MT][DC][4];
+        struct Places {
+            TilePlace t[MT];
+        };
         auto place = [&](const Segment &s, int tile) {
-            return place_of<WHOLE>(kv, kv.table + s.b * kv.table_stride, s.tile0 + tile, tile < s.t1, s.first, s.len,
-                                   a.err);
+            Places p;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                p.t[i] = place_of<WHOLE>(kv, kv.table + s.b * kv.table_stride, (s.tile0 + tile) * MT + i, tile < s.t1,
+                                         s.first, s.len, a.err);
+            return p;
         };
         // does token r of a tile count, and its place relative to p's
         auto token = [&](const TilePlace &p, int r, int *page, int *off) {
@@ -401,7 +428,7 @@ struct Kernel {
             *off = __shfl_sync(kFull, p.off, r);
             return *page >= 0;
         };
-        auto load_k = [&](const TilePlace &p, int h) {
+        auto load_k16 = [&](const TilePlace &p, int h, uint4(&x)[2][2 * DC]) {
             const uint16_t *base = static_cast<const uint16_t *>(kv.k) + h * kv.ks_head;
             if (WHOLE) base += p.page * kv.ks_page + p.off * kv.ks_tok;
 #pragma unroll
@@ -412,11 +439,11 @@ struct Kernel {
 #pragma unroll
                 for (int j = 0; j < 2 * DC; ++j) {
                     const int d = j * 32 + t * 8;
-                    kx[rr][j] = (live && d < kv.dim) ? load8<VEC>(row + d, kv.dim - d) : make_uint4(0, 0, 0, 0);
+                    x[rr][j] = (live && d < kv.dim) ? load8<VEC>(row + d, kv.dim - d) : make_uint4(0, 0, 0, 0);
                 }
             }
         };
-        auto load_v = [&](const TilePlace &p, int h) {
+        auto load_v16 = [&](const TilePlace &p, int h, uint4(&x)[DC][4]) {
             const uint16_t *base = static_cast<const uint16_t *>(kv.v) + h * kv.vs_head;
             if (WHOLE) base += p.page * kv.vs_page + p.off * kv.vs_tok;
 #pragma unroll
@@ -428,12 +455,23 @@ struct Kernel {
 #pragma unroll
                 for (int c = 0; c < DC; ++c) {
                     const int d = c * 64 + g * 8;
-                    vx[c][rr] = (live && d < kv.dim) ? load8<VEC>(row + d, kv.dim - d) : make_uint4(0, 0, 0, 0);
+                    x[c][rr] = (live && d < kv.dim) ? load8<VEC>(row + d, kv.dim - d) : make_uint4(0, 0, 0, 0);
                 }
             }
         };
 
-        TilePlace here = {-1, 0, 0, 0}, next = here;
+        auto load_k = [&](const Places &p, int h) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i) load_k16(p.t[i], h, kx[i]);
+        };
+        auto load_v = [&](const Places &p, int h) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i) load_v16(p.t[i], h, vx[i]);
+        };
+
+        Places here, next;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) here.t[i] = next.t[i] = {-1, 0, 0, 0};
         bool first_segment = true;
         bool primed = false;  // the present segment's first tiles are already requested
         if (sh.seg[0].t0 < sh.seg[0].t1) load_q(row_of(a, sh.seg[0].b, sh.seg[0].hk));
@@ -473,62 +511,70 @@ struct Kernel {
             }
             for (; left > 0; --left, tile += kWarps) {
                 // S^T = K Q^T
-                float s[NT][4];
+                float s[MT][NT][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float odd[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float odd[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int j = 0; j < 2 * DC; ++j) {
-                        uint4 b;
-                        if (kQInSmem) {
-                            const int w = 4 * (nt * 2 * DC + j);
-                            b = make_uint4(sh.q[kQInSmem ? w : 0][lane], sh.q[kQInSmem ? w + 1 : 0][lane],
-                                           sh.q[kQInSmem ? w + 2 : 0][lane], sh.q[kQInSmem ? w + 3 : 0][lane]);
-                        } else {
-                            b = q[kQInSmem ? 0 : nt][kQInSmem ? 0 : j];
+                        for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 2 * DC; ++j) {
+                            uint4 b;
+                            if (kQInSmem) {
+                                const int w = 4 * (nt * 2 * DC + j);
+                                b = make_uint4(sh.q[kQInSmem ? w : 0][lane], sh.q[kQInSmem ? w + 1 : 0][lane],
+                                               sh.q[kQInSmem ? w + 2 : 0][lane], sh.q[kQInSmem ? w + 3 : 0][lane]);
+                            } else {
+                                b = q[kQInSmem ? 0 : nt][kQInSmem ? 0 : j];
+                            }
+                            const uint4 k0 = kx[mt][0][j], k1 = kx[mt][1][j];
+                            Mma<T>::run(s[mt][nt], k0.x, k1.x, k0.y, k1.y, b.x, b.y);
+                            Mma<T>::run(odd, k0.z, k1.z, k0.w, k1.w, b.z, b.w);
                         }
-                        Mma<T>::run(s[nt], kx[0][j].x, kx[1][j].x, kx[0][j].y, kx[1][j].y, b.x, b.y);
-                        Mma<T>::run(odd, kx[0][j].z, kx[1][j].z, kx[0][j].w, kx[1][j].w, b.z, b.w);
-                    }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[nt][e] += odd[e];
-                }
-                const TilePlace old = here;
+                        for (int e = 0; e < 4; ++e) s[mt][nt][e] += odd[e];
+                    }
+                const Places old = here;
                 here = next;
                 load_k(here, left > 1 ? h : h_after);
                 next = left > 2 ? place(seg, tile + 2 * kWarps) : place(after, after.t0 + warp + (2 - left) * kWarps);
 
                 // scale, mask, running maximum
-                int page, off;
-                const bool live0 = token(old, g, &page, &off), live1 = token(old, g + 8, &page, &off);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const bool live = e < 2 ? live0 : live1;
-                        s[nt][e] = live ? s[nt][e] * a.scale_log2 : -INFINITY;
-                    }
-                }
-                if (a.scores_out) {
-                    const int64_t row = static_cast<int64_t>(seg.b) * kv.kv_heads * a.head_tiles + seg.hk;
-                    const int slot = (seg.tile0 + tile) * 16 + g;
+                for (int mt = 0; mt < MT; ++mt) {
+                    int page, off;
+                    const bool live0 = token(old.t[mt], g, &page, &off), live1 = token(old.t[mt], g + 8, &page, &off);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int rr = 0; rr < 2; ++rr) {
-                            const int head = nt * 8 + 2 * t, at = slot + 8 * rr;
-                            if (head < a.logit_heads && at < seg.len && at >= seg.first)
-                                *reinterpret_cast<float2 *>(a.logits + (row * kv.capacity + at) * a.logit_heads + head) =
-                                    make_float2(s[nt][2 * rr], s[nt][2 * rr + 1]);
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            s[mt][nt][e] = (e < 2 ? live0 : live1) ? s[mt][nt][e] * a.scale_log2 : -INFINITY;
                 }
-                uint32_t phi[NT][2], plo[NT][2];
+                if (a.scores_out) {
+                    const int64_t row = static_cast<int64_t>(seg.b) * kv.kv_heads * a.head_tiles + seg.hk;
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int rr = 0; rr < 2; ++rr) {
+                                const int head = nt * 8 + 2 * t, at = ((seg.tile0 + tile) * MT + mt) * 16 + g + 8 * rr;
+                                if (head < a.logit_heads && at < seg.len && at >= seg.first)
+                                    *reinterpret_cast<float2 *>(a.logits + (row * kv.capacity + at) * a.logit_heads + head) =
+                                        make_float2(s[mt][nt][2 * rr], s[mt][nt][2 * rr + 1]);
+                            }
+                }
+                uint32_t phi[MT][NT][2], plo[MT][NT][2];
                 bool grew = false;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float top[2] = {fmaxf(s[nt][0], s[nt][2]), fmaxf(s[nt][1], s[nt][3])};
+                    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) top[e & 1] = fmaxf(top[e & 1], s[mt][nt][e]);
 #pragma unroll
                     for (int x = 4; x < 32; x *= 2) {
                         top[0] = fmaxf(top[0], __shfl_xor_sync(kFull, top[0], x));
@@ -541,46 +587,55 @@ struct Kernel {
                         grew = grew || m2 != m[nt][e];
                         fix[e] = exp2_from(m[nt][e], m2);
                         m[nt][e] = m2;
-                        const float p0 = exp2_from(s[nt][e], m2), p1 = exp2_from(s[nt][e + 2], m2);
-                        l[nt][e] = l[nt][e] * fix[e] + (p0 + p1);
-                        s[nt][e] = p0;
-                        s[nt][e + 2] = p1;
+                        l[nt][e] *= fix[e];
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            const float p0 = exp2_from(s[mt][nt][e], m2), p1 = exp2_from(s[mt][nt][e + 2], m2);
+                            l[nt][e] += p0 + p1;
+                            s[mt][nt][e] = p0;
+                            s[mt][nt][e + 2] = p1;
+                        }
                     }
                     if (__any_sync(kFull, grew)) {
 #pragma unroll
-                        for (int i = 0; i < DC * 4; ++i)
+                        for (int k = 0; k < DC * 4; ++k)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) o[nt * DC * 4 + i][e] *= fix[e & 1];
+                            for (int e = 0; e < 4; ++e) o[nt * DC * 4 + k][e] *= fix[e & 1];
                     }
 #pragma unroll
-                    for (int rr = 0; rr < 2; ++rr) {
-                        const uint32_t hi = Mma<T>::pack(s[nt][2 * rr], s[nt][2 * rr + 1]);
-                        const float2 back = Mma<T>::unpack(hi);
-                        const uint32_t lo = Mma<T>::pack(s[nt][2 * rr] - back.x, s[nt][2 * rr + 1] - back.y);
-                        phi[nt][rr] = transpose8x8(hi);
-                        plo[nt][rr] = transpose8x8(lo);
-                    }
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int rr = 0; rr < 2; ++rr) {
+                            const float p0 = s[mt][nt][2 * rr], p1 = s[mt][nt][2 * rr + 1];
+                            const uint32_t hi = Mma<T>::pack(p0, p1);
+                            const float2 back = Mma<T>::unpack(hi);
+                            phi[mt][nt][rr] = transpose8x8(hi);
+                            plo[mt][nt][rr] = transpose8x8(Mma<T>::pack(p0 - back.x, p1 - back.y));
+                        }
                 }
                 // O^T += V^T P^T
 #pragma unroll
-                for (int c = 0; c < DC; ++c) {
-                    const uint32_t *w[4] = {reinterpret_cast<const uint32_t *>(&vx[c][0]),
-                                            reinterpret_cast<const uint32_t *>(&vx[c][1]),
-                                            reinterpret_cast<const uint32_t *>(&vx[c][2]),
-                                            reinterpret_cast<const uint32_t *>(&vx[c][3])};
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t a0 = __byte_perm(w[0][i], w[1][i], 0x5410);
-                        const uint32_t a1 = __byte_perm(w[0][i], w[1][i], 0x7632);
-                        const uint32_t a2 = __byte_perm(w[2][i], w[3][i], 0x5410);
-                        const uint32_t a3 = __byte_perm(w[2][i], w[3][i], 0x7632);
+                    for (int c = 0; c < DC; ++c) {
+                        const uint32_t *w[4] = {reinterpret_cast<const uint32_t *>(&vx[mt][c][0]),
+                                                reinterpret_cast<const uint32_t *>(&vx[mt][c][1]),
+                                                reinterpret_cast<const uint32_t *>(&vx[mt][c][2]),
+                                                reinterpret_cast<const uint32_t *>(&vx[mt][c][3])};
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            Mma<T>::run(o[(nt * DC + c) * 4 + i], a0, a1, a2, a3, phi[nt][0], phi[nt][1]);
-                            Mma<T>::run(o[(nt * DC + c) * 4 + i], a0, a1, a2, a3, plo[nt][0], plo[nt][1]);
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t a0 = __byte_perm(w[0][k], w[1][k], 0x5410);
+                            const uint32_t a1 = __byte_perm(w[0][k], w[1][k], 0x7632);
+                            const uint32_t a2 = __byte_perm(w[2][k], w[3][k], 0x5410);
+                            const uint32_t a3 = __byte_perm(w[2][k], w[3][k], 0x7632);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                float(&acc)[4] = o[(nt * DC + c) * 4 + k];
+                                Mma<T>::run(acc, a0, a1, a2, a3, phi[mt][nt][0], phi[mt][nt][1]);
+                                Mma<T>::run(acc, a0, a1, a2, a3, plo[mt][nt][0], plo[mt][nt][1]);
+                            }
                         }
                     }
-                }
                 load_v(here, left > 1 ? h : h_after);
             }
 
@@ -679,15 +734,15 @@ struct Kernel {
     // last, for which the others' parts are visible then.
     static __device__ __forceinline__ bool last_of(Shared &sh, unsigned int *counter, int expected)
     {
-        // the barrier orders the block's writes before thread 0's fence, which
-        // is cumulative
+        // the barrier orders the block's writes before thread 0's release, which
+        // is cumulative; its acquire orders the others' parts before what the
+        // block reads after the second barrier
         __syncthreads();
         if (threadIdx.x == 0) {
-            __threadfence();
-            const bool last = atomicAdd(counter, 1u) == static_cast<unsigned>(expected - 1);
-            if (last) *counter = 0;  // ready for the next call
-            __threadfence();
-            sh.last = last;
+            unsigned seen;
+            asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(seen) : "l"(counter) : "memory");
+            sh.last = seen == static_cast<unsigned>(expected - 1);
+            if (sh.last) *counter = 0;  // ready for the next call
         }
         __syncthreads();
         return sh.last != 0;
@@ -767,18 +822,20 @@ struct Kernel {
         auto slot = [&](int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); };
         const int first = (w.cta - c0) / kGroupCtas * kGroupCtas, members = min(kGroupCtas, n - first);
         const int groups = (n + kGroupCtas - 1) / kGroupCtas;
-        if (!last_of(sh, a.arrived_group + slot(first), members)) return;
-        if (groups == 1) {
-            combine(a, sh, r, n, slot, -1);
-            return;
-        }
-        if (members > 1) {
-            combine(a, sh, r, members, [&](int i) { return slot(first + i); }, slot(first));
-            __syncthreads();
-        }
         const int64_t row = static_cast<int64_t>(r.b) * a.kv.kv_heads * a.head_tiles + r.hk;
-        if (!last_of(sh, a.arrived + row, groups)) return;
-        combine(a, sh, r, groups, [&](int i) { return slot(i * kGroupCtas); }, -1);
+        // level 0: the members of the group; level 1: the groups
+        for (int level = 0; level < 2; ++level) {
+            const bool members_only = level == 0;
+            if (!last_of(sh, members_only ? a.arrived_group + slot(first) : a.arrived + row, members_only ? members : groups))
+                return;
+            const bool done = !members_only || groups == 1;
+            if (done || members > 1) {
+                combine(a, sh, r, members_only ? members : groups,
+                        [&](int i) { return slot(members_only ? first + i : i * kGroupCtas); }, done ? -1 : slot(first));
+                __syncthreads();
+            }
+            if (done) return;
+        }
     }
 
     // Sum over the block of one int per thread, and the thread's prefix.
@@ -816,7 +873,7 @@ struct Kernel {
         // tiles and rows per cached head over all sequences
         int64_t tiles = 0, rows = 0;
         for (int b0 = 0; b0 < a.kv.batch; b0 += step) {
-            const int n = b0 + own < a.kv.batch ? row_span(a, b0 + own).tiles : 0;
+            const int n = b0 + own < a.kv.batch ? row_span<kTokens>(a, b0 + own).tiles : 0;
             if (few) {
                 tiles = __reduce_add_sync(kFull, n);
                 rows = __popc(__ballot_sync(kFull, n > 0));
@@ -849,7 +906,7 @@ struct Kernel {
         // the sequence that holds x0
         int64_t before = 0;
         for (int b0 = 0; b0 < a.kv.batch && x0 >= before * hks; b0 += step) {
-            const int b = b0 + own, n = b < a.kv.batch ? row_span(a, b).tiles : 0, cost = n > 0 ? n + a.lead : 0;
+            const int b = b0 + own, n = b < a.kv.batch ? row_span<kTokens>(a, b).tiles : 0, cost = n > 0 ? n + a.lead : 0;
             int all, pre;
             if (few) {
                 pre = cost;
@@ -882,7 +939,7 @@ struct Kernel {
 template <int DC, int NT>
 constexpr int warps_per_sm()
 {
-    return DC * NT <= 1 ? 16 : DC * NT <= 2 ? 12 : 8;
+    return DC * NT <= 2 ? 12 : 8;
 }
 
 template <typename T, int DC, int NT, int NW, bool VEC, bool WHOLE>

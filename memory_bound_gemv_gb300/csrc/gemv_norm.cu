@@ -177,15 +177,16 @@ __device__ __forceinline__ void normalise(float (&x)[K][8], const int (&cnt)[K],
 }
 
 // A block goes through rows and requests the next row's y and x while it
-// works on the present one; what else differs from row to row is prefetched
-// into L2, what does not comes from L1.  FULL: every thread has all of its K
-// steps.
-template <int K, int MAXT, bool VEC, bool FULL, bool Y32, bool X32>
-__global__ void __launch_bounds__(MAXT) mbg_norm_kernel(const __grid_constant__ NormArgs a)
+// works on the present one (MINB 1), or takes one row (MINB blocks on an SM);
+// what else differs from row to row is prefetched into L2, what does not comes
+// from L1.  FULL: every thread has all of its K steps.
+template <int K, int MAXT, int MINB, bool VEC, bool FULL, bool Y32, bool X32>
+__global__ void __launch_bounds__(MAXT, MINB) mbg_norm_kernel(const __grid_constant__ NormArgs a)
 {
     __shared__ Sums sums;
     pdl_trigger();
     pdl_wait();
+    constexpr bool kNext = MINB == 1;  // rows ahead; otherwise a block for each row
     int64_t row = blockIdx.x;
     int at[K], cnt[K];
     Stream<VEC, Y32> y[K];
@@ -235,13 +236,13 @@ __global__ void __launch_bounds__(MAXT) mbg_norm_kernel(const __grid_constant__ 
     request_y(row);
     request_r(row);
     for (int turn = 0;; turn ^= 4) {
-        const int64_t next = row + gridDim.x;
-        prefetch(next);
+        const int64_t next = kNext ? row + gridDim.x : a.rows;
+        if (kNext) prefetch(next);
         by_stream<VEC, Y32>(a.y_e, [&](auto e) {
 #pragma unroll
             for (int k = 0; k < K; ++k) y[k].template floats<decltype(e)::value>(x[k]);
         });
-        if (next < a.rows) request_y(next);
+        if (kNext && next < a.rows) request_y(next);
         if (a.post) {
             normalise<K, VEC, FULL>(x, cnt, a, sums, turn);
             if (a.post_w) with(a.post_w, a.post_e, a.post_s, product);
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(MAXT) mbg_norm_kernel(const __grid_constant__ 
                 elem_store8<VEC, E>(p, at[k], cnt[k], x[k]);
             }
         });
-        if (next < a.rows) request_r(next);
+        if (kNext && next < a.rows) request_r(next);
         if (a.h) {
             normalise<K, VEC, FULL>(x, cnt, a, sums, turn + 2);
             if (a.pre_w) {
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(MAXT) mbg_norm_kernel(const __grid_constant__ 
                 for (int k = 0; k < K; ++k) elem_store8<VEC, E>(p, at[k], cnt[k], x[k]);
             });
         }
-        if (next >= a.rows) break;
+        if (!kNext || next >= a.rows) break;
         row = next;
     }
 }
@@ -406,7 +407,7 @@ cudaError_t launch_rows(void (*fn)(NormArgs), const NormArgs &a, int64_t blocks,
 template <int K, bool VEC, bool FULL, bool Y32, bool X32>
 cudaError_t launch_fitting(const NormArgs &a, int threads, int sm_count, cudaStream_t s)
 {
-    auto fn = mbg_norm_kernel<K, 512, VEC, FULL, Y32, X32>;
+    auto fn = mbg_norm_kernel<K, 512, 1, VEC, FULL, Y32, X32>;
     static std::atomic<int> fit[512 / 32 + 1];  // blocks per SM, by warps (0: not asked yet)
     int per_sm = fit[threads / 32].load(std::memory_order_relaxed);
     if (per_sm == 0) {
@@ -423,6 +424,16 @@ template <int K, bool VEC, bool Y32, bool X32>
 cudaError_t launch_steps(const NormArgs &a, int sm_count, cudaStream_t s)
 {
     const int chunks = (a.width + 7) / 8, threads = ((chunks + K - 1) / K + 31) / 32 * 32;
+    // Operands of each row: a block per row, two wide ones on an SM, hides the
+    // loads of those better than rows ahead do (331 x 14336 with gate, weight
+    // and bias of each row 15.6 us against 18.2, 2000 x 8192 38.3 against 42.7;
+    // with shared ones 28.1 against 26.7).  400 x 4096, all rows at once on the
+    // GPU, is faster without (5.4 us against 6.4).
+    const bool each = a.gate_s || a.pre_w_s || a.pre_b_s;
+    if (VEC && K == 4 && each && threads <= 448 && (threads > 256 || a.rows > 8 * sm_count))
+        return launch_rows(chunks == threads * K ? mbg_norm_kernel<4, 448, 2, VEC, VEC, Y32, X32>
+                                                 : mbg_norm_kernel<4, 448, 2, VEC, false, Y32, X32>,
+                           a, a.rows, threads, s);
     if (VEC && chunks == threads * K) return launch_fitting<K, VEC, true, Y32, X32>(a, threads, sm_count, s);
     return launch_fitting<K, VEC, false, Y32, X32>(a, threads, sm_count, s);
 }
