@@ -407,11 +407,13 @@ __global__ void __launch_bounds__(kPlanThreads) mbg_evict_plan_kernel(const __gr
 // nothing.  Bound by the bytes moved, once enough of them are in flight: a
 // warp's lanes look up the pages of kApplyLook moves side by side, then the
 // rows of kApplyBatch moves are requested before the first is written.  Rows
-// of 256 bytes from anywhere in the pool to anywhere: 74000 moves take 21 us,
-// half the rate of a plain copy; dealing all moves evenly to a fitting grid
-// with the next group's pages looked up ahead took as long.
+// of 256 bytes from anywhere in the pool to anywhere: 74000 moves take some
+// 20 us, half the rate of a plain copy.  Four rows in flight per warp and 32
+// warps on an SM (plan and moves 36.6 us) beat eight and 24 (38.1 us), sixteen
+// and 16 (45.3 us), and dealing all moves evenly to a fitting grid with the
+// next group's pages looked up ahead (41.1 us).
 constexpr int kApplyThreads = 256;
-constexpr int kApplyBatch = 8, kApplyLook = 16;
+constexpr int kApplyBatch = 4, kApplyLook = 8;
 
 // Page of a slot, and its place in the page; -1 where it has no valid one.
 __device__ __forceinline__ int64_t page_of(const KvView &kv, const int32_t *table, int slot, int *off)
@@ -423,7 +425,7 @@ __device__ __forceinline__ int64_t page_of(const KvView &kv, const int32_t *tabl
 }
 
 template <bool VEC>
-__global__ void __launch_bounds__(kApplyThreads) mbg_evict_apply_kernel(const __grid_constant__ EvictApplyArgs a)
+__global__ void __launch_bounds__(kApplyThreads, 4) mbg_evict_apply_kernel(const __grid_constant__ EvictApplyArgs a)
 {
     pdl_trigger();
     pdl_wait();
@@ -449,7 +451,7 @@ __global__ void __launch_bounds__(kApplyThreads) mbg_evict_apply_kernel(const __
                   hs = is_v ? kv.vs_head : kv.ks_head;
     uint16_t *pool = static_cast<uint16_t *>(is_v ? kv.v : kv.k) + h * hs;
     for (int i0 = (blockIdx.x * (kApplyThreads / 32) + warp) * kApplyLook; i0 < count; i0 += stride) {
-        // lanes 0..15: a move each
+        // lanes 0..7: a move each
         int sp = -1, tp = -1, so = 0, to = 0;
         if (lane < kApplyLook && i0 + lane < count) {
             const int2 mv = __ldg(moves + i0 + lane);
