@@ -63,37 +63,139 @@ __device__ __forceinline__ uint4 ld_once16(const void *p)
     return v;
 }
 
+// Rows that do not all begin at a 16-byte border (an odd width, say).  Their
+// steps of eight elements are counted from the border before the row's
+// beginning in out, which is where its beginning in the other tensors of the
+// same layout has one too: those are moved whole, and only the row's first and
+// last elements one by one.  What lies otherwise (weights shared by all rows)
+// is loaded in the aligned windows that hold it, and the first `skip` elements
+// are shifted out.  8192 x 4001 in bf16: 124.7 us, with loads and stores of
+// single elements 250.8 us.
+template <int E>
+struct Window {
+    static constexpr int kSize = E == GEMV_ELEM_F32 ? 4 : 2;
+    static constexpr int kWords = E == GEMV_ELEM_F32 ? 12 : 8, kWhole = E == GEMV_ELEM_F32 ? 8 : 4;
+    uint32_t w[kWords];
+    int skip;
+    // elements [at, at + 8) of a row of `width`; those outside it read 0
+    __device__ __forceinline__ void load(const unsigned char *row, int at, int width)
+    {
+        const unsigned char *p = row + static_cast<int64_t>(at) * kSize;
+        skip = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15) / kSize;
+        const uint4 *q = reinterpret_cast<const uint4 *>(p - skip * kSize);
+        if (skip == 0 && at >= 0 && at + 8 <= width) {
+#pragma unroll
+            for (int i = 0; i < kWhole / 4; ++i) set(i, q[i]);
+#pragma unroll
+            for (int i = kWhole; i < kWords; ++i) w[i] = 0u;
+        } else if (at >= skip && at - skip + kWords * 4 / kSize <= width) {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i) set(i, q[i]);
+        } else {
+            skip = 0;
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) w[i] = 0u;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (at + i < 0 || at + i >= width) continue;
+                if (E == GEMV_ELEM_F32)
+                    w[i] = reinterpret_cast<const uint32_t *>(p)[i];
+                else
+                    w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p)[i]) << (16 * (i & 1));
+            }
+        }
+    }
+    __device__ __forceinline__ void set(int i, const uint4 &v)
+    {
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+    __device__ __forceinline__ void floats(float (&x)[8]) const
+    {
+        uint32_t t[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) t[i] = w[i];
+        if (__any_sync(0xFFFFFFFFu, skip != 0)) {
+            const int words = E == GEMV_ELEM_F32 ? skip : skip >> 1;
+#pragma unroll
+            for (int d = 2; d > 0; d /= 2)
+#pragma unroll
+                for (int i = 0; i + d < kWords; ++i) t[i] = (words & d) ? t[i + d] : t[i];
+            if (E != GEMV_ELEM_F32) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) t[i] = (skip & 1) ? __funnelshift_r(t[i], t[i + 1], 16) : t[i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            if (E == GEMV_ELEM_F32) {
+                x[i] = __uint_as_float(t[i]), x[i + 1] = __uint_as_float(t[i + 1]);
+            } else {
+                const float2 f = elem_unpack2<E == GEMV_ELEM_F32 ? GEMV_ELEM_F16 : E>(t[i / 2]);
+                x[i] = f.x, x[i + 1] = f.y;
+            }
+        }
+    }
+};
+
+// Elements between the border before a row's beginning and that beginning.
+__device__ __forceinline__ int border_shift(const unsigned char *row, int elem)
+{
+    const uintptr_t p = reinterpret_cast<uintptr_t>(row);
+    return static_cast<int>(elem == GEMV_ELEM_F32 ? (p & 31) >> 2 : (p & 15) >> 1);
+}
+
+// A thread's eight elements [at, at + 8) of a row.  VEC: all there (n = 8) or
+// none, and aligned.
+template <bool VEC, int E>
+__device__ __forceinline__ void load_step(const unsigned char *row, int at, int n, int width, float (&x)[8])
+{
+    if (VEC) {
+        elem_load8<true, E>(row, at, n, x);
+    } else {
+        Window<E> v;
+        v.load(row, at, width);
+        v.floats(x);
+    }
+}
+
+template <bool VEC, int E>
+__device__ __forceinline__ void store_step(unsigned char *row, int at, int n, int width, const float (&x)[8])
+{
+    unsigned char *p = row + static_cast<int64_t>(at) * (E == GEMV_ELEM_F32 ? 4 : 2);
+    if (VEC) {
+        elem_store8<true, E>(row, at, n, x);
+    } else if (at >= 0 && at + 8 <= width && (reinterpret_cast<uintptr_t>(p) & (E == GEMV_ELEM_F32 ? 31 : 15)) == 0) {
+        elem_store8<true, E>(p, 0, 8, x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (at + i >= 0 && at + i < width) elem_store1<E>(p, i, x[i]);
+    }
+}
+
 // Eight elements as loaded, converted after the row's loads are under way.
 // WIDE: FP32, else one of the 16-bit types.
 template <bool VEC, bool WIDE>
 struct Stream {
-    uint4 a, b;  // b: FP32, or the element-wise path, which converts at once
-    __device__ __forceinline__ void load(const unsigned char *row, int elem, int at, int n)
+    uint4 a, b;  // b: FP32
+    __device__ __forceinline__ void load(const unsigned char *row, int at, int n, int)
     {
-        if (VEC) {
-            a = b = make_uint4(0u, 0u, 0u, 0u);
-            if (n > 0) {
-                if (WIDE) {
-                    uint32_t w[8];
-                    ld_global32(row + at * 4, w);
-                    a = make_uint4(w[0], w[1], w[2], w[3]);
-                    b = make_uint4(w[4], w[5], w[6], w[7]);
-                } else {
-                    a = ld_once16(row + at * 2);
-                }
-            }
+        a = b = make_uint4(0u, 0u, 0u, 0u);
+        if (n <= 0) return;
+        if (WIDE) {
+            uint32_t w[8];
+            ld_global32(row + static_cast<int64_t>(at) * 4, w);
+            a = make_uint4(w[0], w[1], w[2], w[3]);
+            b = make_uint4(w[4], w[5], w[6], w[7]);
         } else {
-            float x[8];
-            by_elem(elem, [&](auto e) { elem_load8<false, decltype(e)::value>(row, at, n, x); });
-            a = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-            b = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+            a = ld_once16(row + static_cast<int64_t>(at) * 2);
         }
     }
     template <int E>
     __device__ __forceinline__ void floats(float (&x)[8]) const
     {
         const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        if (!VEC || WIDE) {
+        if (WIDE) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
         } else {
@@ -107,18 +209,36 @@ struct Stream {
     }
 };
 
+// The same for rows that begin anywhere.
+template <bool WIDE>
+struct Stream<false, WIDE> {
+    Window<WIDE ? GEMV_ELEM_F32 : GEMV_ELEM_F16> v;
+    __device__ __forceinline__ void load(const unsigned char *row, int at, int, int width) { v.load(row, at, width); }
+    template <int E>
+    __device__ __forceinline__ void floats(float (&x)[8]) const
+    {
+        if (WIDE) {
+            v.floats(x);
+        } else {
+            Window<E == GEMV_ELEM_F32 ? GEMV_ELEM_F16 : E> t;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t.w[i] = v.w[i];
+            t.skip = v.skip;
+            t.floats(x);
+        }
+    }
+};
+
 // The type of y or x where WIDE leaves only two.
-template <bool VEC, bool WIDE, typename F>
+template <bool WIDE, typename F>
 __device__ __forceinline__ void by_stream(int elem, F f)
 {
-    if (VEC && WIDE)
+    if (WIDE)
         f(ElemTag<GEMV_ELEM_F32>());
-    else if (VEC && elem == GEMV_ELEM_F16)
+    else if (elem == GEMV_ELEM_F16)
         f(ElemTag<GEMV_ELEM_F16>());
-    else if (VEC)
-        f(ElemTag<GEMV_ELEM_BF16>());
     else
-        by_elem(elem, f);
+        f(ElemTag<GEMV_ELEM_BF16>());
 }
 
 // Sum over the block.  `turn` numbers the reductions, so that one barrier is
@@ -145,7 +265,8 @@ __device__ __forceinline__ float row_sum(float v, Sums &s, int turn)
 // x -> (x - mean) / sqrt(var + eps), or x / sqrt(mean of squares + eps), for
 // values held in registers; cnt[k] of the eight values of step k exist.
 template <int K, bool VEC, bool FULL>
-__device__ __forceinline__ void normalise(float (&x)[K][8], const int (&cnt)[K], const NormArgs &a, Sums &s, int turn)
+__device__ __forceinline__ void normalise(float (&x)[K][8], const int (&at)[K], int shift_by, const NormArgs &a, Sums &s,
+                                          int turn)
 {
     const float inv_n = 1.f / static_cast<float>(a.width);
     auto mask = [&](float shift) {  // elements that do not exist become 0
@@ -153,7 +274,9 @@ __device__ __forceinline__ void normalise(float (&x)[K][8], const int (&cnt)[K],
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                x[k][e] = FULL || (VEC ? cnt[k] > 0 : e < cnt[k]) ? x[k][e] - shift : 0.f;
+                x[k][e] = FULL || static_cast<unsigned>(at[k] - shift_by + (VEC ? 0 : e)) < static_cast<unsigned>(a.width)
+                              ? x[k][e] - shift
+                              : 0.f;
     };
     if (!FULL) mask(0.f);
     if (a.layer) {
@@ -194,7 +317,7 @@ __global__ void __launch_bounds__(MAXT, MINB) mbg_norm_kernel(const __grid_const
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         at[k] = (k * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * 8;
-        cnt[k] = FULL ? 8 : min(8, a.width - at[k]);
+        cnt[k] = FULL ? 8 : min(8, a.width - at[k]);  // VEC: 8 or none
     }
     // operands of a row alone that are needed late
     auto prefetch = [&](int64_t rw) {
@@ -207,24 +330,29 @@ __global__ void __launch_bounds__(MAXT, MINB) mbg_norm_kernel(const __grid_const
         one(a.pre_w, a.pre_w_e, a.pre_w_s);
         one(a.pre_b, a.pre_b_e, a.pre_b_s);
     };
+    // where the steps are counted from
+    auto shift_of = [&](int64_t rw) { return VEC ? 0 : border_shift(row_of(a.out, a.r_e, rw, a.out_s), a.r_e); };
     auto request_y = [&](int64_t rw) {
         const unsigned char *p = row_of(a.y, a.y_e, rw, a.y_s);
+        const int from = shift_of(rw);
 #pragma unroll
-        for (int k = 0; k < K; ++k) y[k].load(p, a.y_e, at[k], cnt[k]);
+        for (int k = 0; k < K; ++k) y[k].load(p, at[k] - from, cnt[k], a.width);
     };
     auto request_r = [&](int64_t rw) {
         const unsigned char *p = row_of(a.r, a.r_e, rw, a.r_s);
+        const int from = shift_of(rw);
 #pragma unroll
-        for (int k = 0; k < K; ++k) r[k].load(p, a.r_e, at[k], cnt[k]);
+        for (int k = 0; k < K; ++k) r[k].load(p, at[k] - from, cnt[k], a.width);
     };
     // x[k][i] = f(x[k][i], operand)
     float x[K][8];
+    int shift = 0;
     auto with = [&](const void *base, int elem, int64_t stride, auto f) {
         const unsigned char *p = row_of(base, elem, row, stride);
         by_elem(elem, [&](auto e) {
             float t[K][8];
 #pragma unroll
-            for (int k = 0; k < K; ++k) elem_load8<VEC, decltype(e)::value>(p, at[k], cnt[k], t[k]);
+            for (int k = 0; k < K; ++k) load_step<VEC, decltype(e)::value>(p, at[k] - shift, cnt[k], a.width, t[k]);
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -236,19 +364,20 @@ __global__ void __launch_bounds__(MAXT, MINB) mbg_norm_kernel(const __grid_const
     request_y(row);
     request_r(row);
     for (int turn = 0;; turn ^= 4) {
+        shift = shift_of(row);
         const int64_t next = kNext ? row + gridDim.x : a.rows;
         if (kNext) prefetch(next);
-        by_stream<VEC, Y32>(a.y_e, [&](auto e) {
+        by_stream<Y32>(a.y_e, [&](auto e) {
 #pragma unroll
             for (int k = 0; k < K; ++k) y[k].template floats<decltype(e)::value>(x[k]);
         });
         if (kNext && next < a.rows) request_y(next);
         if (a.post) {
-            normalise<K, VEC, FULL>(x, cnt, a, sums, turn);
+            normalise<K, VEC, FULL>(x, at, shift, a, sums, turn);
             if (a.post_w) with(a.post_w, a.post_e, a.post_s, product);
         }
         if (a.gate) with(a.gate, a.gate_e, a.gate_s, product);
-        by_stream<VEC, X32>(a.r_e, [&](auto e) {
+        by_stream<X32>(a.r_e, [&](auto e) {
             constexpr int E = decltype(e)::value;
             unsigned char *p = const_cast<unsigned char *>(row_of(a.out, E, row, a.out_s));
 #pragma unroll
@@ -257,12 +386,12 @@ __global__ void __launch_bounds__(MAXT, MINB) mbg_norm_kernel(const __grid_const
                 r[k].template floats<E>(t);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[k][i] = fmaf(a.alpha, x[k][i], t[i]);
-                elem_store8<VEC, E>(p, at[k], cnt[k], x[k]);
+                store_step<VEC, E>(p, at[k] - shift, cnt[k], a.width, x[k]);
             }
         });
         if (kNext && next < a.rows) request_r(next);
         if (a.h) {
-            normalise<K, VEC, FULL>(x, cnt, a, sums, turn + 2);
+            normalise<K, VEC, FULL>(x, at, shift, a, sums, turn + 2);
             if (a.pre_w) {
                 const float unit = a.unit_offset ? 1.f : 0.f;
                 with(a.pre_w, a.pre_w_e, a.pre_w_s, [&](float v, float w) { return v * (w + unit); });
@@ -272,7 +401,7 @@ __global__ void __launch_bounds__(MAXT, MINB) mbg_norm_kernel(const __grid_const
                 constexpr int E = decltype(e)::value;
                 unsigned char *p = const_cast<unsigned char *>(row_of(a.h, E, row, a.h_s));
 #pragma unroll
-                for (int k = 0; k < K; ++k) elem_store8<VEC, E>(p, at[k], cnt[k], x[k]);
+                for (int k = 0; k < K; ++k) store_step<VEC, E>(p, at[k] - shift, cnt[k], a.width, x[k]);
             });
         }
         if (!kNext || next >= a.rows) break;
@@ -294,12 +423,18 @@ __global__ void __launch_bounds__(kLongThreads) mbg_norm_long_kernel(const __gri
     const int64_t row = blockIdx.x;
     const float inv_n = 1.f / static_cast<float>(a.width);
     float mean_y = 0.f, r_y = 1.f, mean_x = 0.f;
+    const int shift = VEC ? 0 : border_shift(row_of(a.out, a.r_e, row, a.out_s), a.r_e);
+    const int steps = (a.width + shift + kLongThreads * 8 - 1) / (kLongThreads * 8);
+    auto step_at = [&](int step) { return (step * kLongThreads + static_cast<int>(threadIdx.x)) * 8 - shift; };
+    auto exists = [&](int at, int e) { return static_cast<unsigned>(at + e) < static_cast<unsigned>(a.width); };
     auto load = [&](const void *p, int elem, int64_t stride, int at, int n, float(&t)[8]) {
-        by_elem(elem, [&](auto e) { elem_load8<VEC, decltype(e)::value>(row_of(p, elem, row, stride), at, n, t); });
+        by_elem(elem, [&](auto e) {
+            load_step<VEC, decltype(e)::value>(row_of(p, elem, row, stride), at, n, a.width, t);
+        });
     };
     auto store = [&](void *p, int elem, int64_t stride, int at, int n, const float(&t)[8]) {
         by_elem(elem, [&](auto e) {
-            elem_store8<VEC, decltype(e)::value>(const_cast<unsigned char *>(row_of(p, elem, row, stride)), at, n, t);
+            store_step<VEC, decltype(e)::value>(const_cast<unsigned char *>(row_of(p, elem, row, stride)), at, n, a.width, t);
         });
     };
     auto sum_y = [&](int at, int n, bool square) {
@@ -307,7 +442,7 @@ __global__ void __launch_bounds__(kLongThreads) mbg_norm_long_kernel(const __gri
         load(a.y, a.y_e, a.y_s, at, n, t);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float d = e < n ? t[e] - mean_y : 0.f;
+            const float d = exists(at, e) ? t[e] - mean_y : 0.f;
             s += square ? d * d : d;
         }
         return s;
@@ -331,24 +466,24 @@ __global__ void __launch_bounds__(kLongThreads) mbg_norm_long_kernel(const __gri
         }
         load(a.r, a.r_e, a.r_s, at, n, t);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = e < n ? fmaf(a.alpha, x[e], t[e]) : 0.f;
+        for (int e = 0; e < 8; ++e) x[e] = exists(at, e) ? fmaf(a.alpha, x[e], t[e]) : 0.f;
     };
-    const int step = kLongThreads * 8, first = threadIdx.x * 8;
     if (a.post) {
         float s = 0.f;
         if (a.layer) {
-            for (int at = first; at < a.width; at += step) s += sum_y(at, min(8, a.width - at), false);
+            for (int c = 0; c < steps; ++c) s += sum_y(step_at(c), min(8, a.width - step_at(c)), false);
             mean_y = row_sum(s, sums, 0) * inv_n;
             s = 0.f;
         }
-        for (int at = first; at < a.width; at += step) s += sum_y(at, min(8, a.width - at), true);
+        for (int c = 0; c < steps; ++c) s += sum_y(step_at(c), min(8, a.width - step_at(c)), true);
         r_y = 1.f / sqrtf(row_sum(s, sums, 1) * inv_n + a.eps);
     }
     float x[8], r_x = 1.f;
     if (a.h) {
         float s = 0.f;
         if (a.layer) {
-            for (int at = first; at < a.width; at += step) {
+            for (int c = 0; c < steps; ++c) {
+                const int at = step_at(c);
                 stream(at, min(8, a.width - at), x);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s += x[e];
@@ -356,19 +491,19 @@ __global__ void __launch_bounds__(kLongThreads) mbg_norm_long_kernel(const __gri
             mean_x = row_sum(s, sums, 2) * inv_n;
             s = 0.f;
         }
-        for (int at = first; at < a.width; at += step) {
-            const int n = min(8, a.width - at);
+        for (int c = 0; c < steps; ++c) {
+            const int at = step_at(c), n = min(8, a.width - at);
             stream(at, n, x);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float d = e < n ? x[e] - mean_x : 0.f;
+                const float d = exists(at, e) ? x[e] - mean_x : 0.f;
                 s = fmaf(d, d, s);
             }
         }
         r_x = 1.f / sqrtf(row_sum(s, sums, 3) * inv_n + a.eps);
     }
-    for (int at = first; at < a.width; at += step) {
-        const int n = min(8, a.width - at);
+    for (int c = 0; c < steps; ++c) {
+        const int at = step_at(c), n = min(8, a.width - at);
         float t[8];
         stream(at, n, x);
         store(a.out, a.r_e, a.out_s, at, n, x);
@@ -423,31 +558,33 @@ cudaError_t launch_fitting(const NormArgs &a, int threads, int sm_count, cudaStr
 template <int K, bool VEC, bool Y32, bool X32>
 cudaError_t launch_steps(const NormArgs &a, int sm_count, cudaStream_t s)
 {
-    const int chunks = (a.width + 7) / 8, threads = ((chunks + K - 1) / K + 31) / 32 * 32;
+    const int chunks = (a.width + (VEC ? 7 : 14)) / 8, threads = ((chunks + K - 1) / K + 31) / 32 * 32;
     // Operands of each row: a block per row, two wide ones on an SM, hides the
     // loads of those better than rows ahead do (331 x 14336 with gate, weight
     // and bias of each row 15.6 us against 18.2, 2000 x 8192 38.3 against 42.7;
     // with shared ones 28.1 against 26.7).  400 x 4096, all rows at once on the
     // GPU, is faster without (5.4 us against 6.4).
     const bool each = a.gate_s || a.pre_w_s || a.pre_b_s;
-    if (VEC && K == 4 && each && threads <= 448 && (threads > 256 || a.rows > 8 * sm_count))
-        return launch_rows(chunks == threads * K ? mbg_norm_kernel<4, 448, 2, VEC, VEC, Y32, X32>
-                                                 : mbg_norm_kernel<4, 448, 2, VEC, false, Y32, X32>,
-                           a, a.rows, threads, s);
-    if (VEC && chunks == threads * K) return launch_fitting<K, VEC, true, Y32, X32>(a, threads, sm_count, s);
+    if constexpr (VEC && K == 4) {
+        if (each && threads <= 448 && (threads > 256 || a.rows > 8 * sm_count))
+            return launch_rows(chunks == threads * K ? mbg_norm_kernel<4, 448, 2, true, true, Y32, X32>
+                                                     : mbg_norm_kernel<4, 448, 2, true, false, Y32, X32>,
+                               a, a.rows, threads, s);
+    }
+    if (VEC && chunks == threads * K) return launch_fitting<K, VEC, VEC, Y32, X32>(a, threads, sm_count, s);
     return launch_fitting<K, VEC, false, Y32, X32>(a, threads, sm_count, s);
 }
 
 template <bool VEC, bool Y32, bool X32>
 cudaError_t launch(const NormArgs &a, int sm_count, cudaStream_t s)
 {
-    const int chunks = (a.width + 7) / 8;
+    const int chunks = (a.width + (VEC ? 7 : 14)) / 8;  // a row may begin up to seven elements into its first step
     if (chunks > 2048) return launch_rows(mbg_norm_long_kernel<VEC>, a, a.rows, kLongThreads, s);
     // Few rows: a row's latency counts, and more threads shorten it.  Many
     // rows: small blocks with several steps per thread, so that several rows
     // are in different phases on one SM.
     const bool many = a.rows > 2 * sm_count;
-    if (chunks > 1024 || (many && !Y32 && !X32 && chunks > 256)) return launch_steps<4, VEC, Y32, X32>(a, sm_count, s);
+    if (chunks > 1024 || (VEC && many && !Y32 && !X32 && chunks > 256)) return launch_steps<4, VEC, Y32, X32>(a, sm_count, s);
     if (chunks > (many ? 128 : 512)) return launch_steps<2, VEC, Y32, X32>(a, sm_count, s);
     return launch_steps<1, VEC, Y32, X32>(a, sm_count, s);
 }
@@ -456,10 +593,13 @@ cudaError_t launch(const NormArgs &a, int sm_count, cudaStream_t s)
 
 cudaError_t launch_norm(const NormArgs &a, bool vec, int sm_count, cudaStream_t s)
 {
-    if (!vec) return launch<false, true, true>(a, sm_count, s);
     const bool y32 = a.y_e == GEMV_ELEM_F32, x32 = a.r_e == GEMV_ELEM_F32;
-    if (y32) return x32 ? launch<true, true, true>(a, sm_count, s) : launch<true, true, false>(a, sm_count, s);
-    return x32 ? launch<true, false, true>(a, sm_count, s) : launch<true, false, false>(a, sm_count, s);
+    auto pick = [&](auto v) {
+        constexpr bool V = decltype(v)::value != 0;
+        if (y32) return x32 ? launch<V, true, true>(a, sm_count, s) : launch<V, true, false>(a, sm_count, s);
+        return x32 ? launch<V, false, true>(a, sm_count, s) : launch<V, false, false>(a, sm_count, s);
+    };
+    return vec ? pick(ElemTag<1>()) : pick(ElemTag<0>());
 }
 
 }  // namespace mbg

@@ -684,3 +684,23 @@ def test_the_compiled_checks_take_the_common_calls_and_leave_the_others():
     assert decode._quick.plan(cache._at, 0, lens, 0, 0, 0, moves, counts, None) == -1
     assert decode._quick.plan(cache._at, 0, lens, 16, 0, 0, moves[:, :, :3], counts, None) == -1
     assert decode._quick.apply(cache._at, 0, moves.float(), counts, None, 16, None) == -1
+
+
+@pytest.mark.parametrize("width", [2, 9, 17, 250, 1001, 4001, 8191, 16383, 20001])
+@pytest.mark.parametrize("yt,xt,ht", [(F32, F32, F16), (BF16, BF16, BF16), (F32, F16, F32)])
+def test_norm_rows_that_begin_anywhere(width, yt, xt, ht):
+    """Nine rows of an odd width begin at every place between two 16-byte borders."""
+    y, x = normal(81, (9, width), yt, 1.7), normal(82, (9, width), xt, 3.0)
+    args = dict(kind="layer", post=True, post_weight=normal(83, (width,), xt), gate=normal(84, (9, width), xt),
+                pre_weight=normal(85, (width,), F32), pre_bias=normal(86, (9, width), ht), alpha=0.5)
+    s, ds, rh, dh = norm_reference(y, x, args)
+    out, h = check_norm(y, x, ht, **args)
+    guard = torch.full((9 * width + 64,), -3.0, dtype=xt, device="cuda")  # in place, between guards
+    inside = guard[32:32 + 9 * width].view(9, width)
+    inside.copy_(x)
+    again, h2 = mbg.gemv_norm_residual(y, inside, out=inside, h_dtype=ht, **args)
+    assert torch.equal(inside, out) and torch.equal(h2, h)
+    assert (guard[:32] == -3).all() and (guard[32 + 9 * width:] == -3).all()
+    wide = torch.full((9, width + 5), -3.0, dtype=ht, device="cuda")  # rows of another stride than x's
+    _, h3 = mbg.gemv_norm_residual(y, x, out=torch.empty_like(x), h=wide[:, 3:3 + width], **args)
+    assert torch.equal(h3, h) and (wide[:, :3] == -3).all() and (wide[:, 3 + width:] == -3).all()
