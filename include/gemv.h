@@ -423,8 +423,9 @@ typedef struct {
  * to; the others are left alone.
  * workspace: device memory of gemv_attn_paged_workspace(...) bytes, 256-byte
  * aligned, of which the first GEMV_ATTN_COUNTER_BYTES + 4 * batch * q_heads
- * are zero before its first use; a call leaves it fit for the next on the same
- * stream.  One workspace serves one call at a time.
+ * are zero before its first use; a call leaves it fit for the next call with the
+ * same cache sizes and q_heads on the same stream.  One workspace serves one
+ * call at a time.
  */
 #define GEMV_ATTN_COUNTER_BYTES 8192
 typedef struct {

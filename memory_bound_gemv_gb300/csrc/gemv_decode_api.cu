@@ -100,8 +100,10 @@ AttnPlan attn_plan(const KvView &v, int group, int nt, bool weights)
     p.logit_heads = group >= heads ? heads : (group + 1) / 2 * 2;
     p.part_stride = static_cast<int64_t>(nt) * dc * 16 * 32 + 2 * heads;
     p.rows = static_cast<int64_t>(v.batch) * v.kv_heads * p.head_tiles;
+    // The counters stand ahead of all else, as many as the narrowest tiles need:
+    // calls whose q allows wide loads and calls whose q does not share a workspace.
     p.arrived = 2 * kAttnMaxCtas * 4;
-    p.part = p.arrived + up(static_cast<size_t>(p.rows) * 4);
+    p.part = p.arrived + up(static_cast<size_t>(v.batch) * v.kv_heads * ((group + 7) / 8) * 4);
     p.row_lse = p.part + up(static_cast<size_t>(2) * kAttnMaxCtas * p.part_stride * 4);
     p.logits = p.row_lse + (weights ? up(static_cast<size_t>(p.rows) * heads * 4) : 0);
     p.total = p.logits + (weights ? up(static_cast<size_t>(p.rows) * v.capacity * p.logit_heads * 4) : 0);

@@ -704,3 +704,20 @@ def test_norm_rows_that_begin_anywhere(width, yt, xt, ht):
     wide = torch.full((9, width + 5), -3.0, dtype=ht, device="cuda")  # rows of another stride than x's
     _, h3 = mbg.gemv_norm_residual(y, x, out=torch.empty_like(x), h=wide[:, 3:3 + width], **args)
     assert torch.equal(h3, h) and (wide[:, :3] == -3).all() and (wide[:, 3 + width:] == -3).all()
+
+
+def test_attn_calls_with_wide_and_narrow_loads_share_a_workspace():
+    # many rows, one tile of 16 query heads for the wide loads, two of eight for the narrow ones; long enough to be cut
+    lengths = [300 + 97 * (b % 31) for b in range(512)]
+    pools = [normal(3 + i, (4096, 16, 8, 64), F16) for i in range(2)]
+    per = -(-max(lengths) // 16)
+    table = torch.from_numpy(np.random.default_rng(9).integers(0, 4096, (512, per)).astype(np.int32)).cuda()
+    cache = mbg.PagedKV(*pools, table)
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    flat = normal(8, (512 * 128 * 64 + 1,), F16)
+    narrow, wide = flat[1:].view(512, 128, 64), flat[1:].clone().view(512, 128, 64)
+    first = mbg.gemv_attn_paged(cache, narrow, n, out=torch.full_like(wide, math.nan))
+    for _ in range(3):
+        mbg.gemv_attn_paged(cache, wide, n, out=torch.full_like(wide, math.nan))
+        again = mbg.gemv_attn_paged(cache, narrow, n, out=torch.full_like(wide, math.nan))
+        assert same_bits(first, again)
