@@ -528,9 +528,9 @@ cudaError_t launch_pdl(void (*fn)(Args), dim3 grid, int threads, int cluster, cu
 cudaError_t launch_evict_plan(const EvictArgs &a, cudaStream_t s)
 {
     // the smallest cluster whose threads hold a row of the cache's capacity
-    // eight slots each (rows of 30000 slots, plan and moves: 40.7 us; with four
-    // slots and twice the blocks 59.6 us, with sixteen and half 46.8 us), then
-    // more slots per thread, then rows of any length
+    // eight slots each (rows of 30000 slots: some 19 us; four slots and twice
+    // the blocks take 19 us more, sixteen and half of them 6 us more), then more
+    // slots per thread, then rows of any length
     const int64_t cap = a.kv.capacity;
     int cluster = 1;
     while (cluster < kPlanMaxCluster && cap > static_cast<int64_t>(cluster) * kPlanThreads * 8) cluster *= 2;

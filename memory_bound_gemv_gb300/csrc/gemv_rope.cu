@@ -113,8 +113,8 @@ struct Place {
 
 // All warps but the last turn; the last one looks ahead: it computes the next
 // token's sines and cosines and its place in the cache, whose indices it has
-// read for 32 tokens at a time.  7001 tokens of 48 heads of 128 in bf16: 30.3 us,
-// 5.7 TB/s; with these reads token by token 33.6 us, with the sines in every
+// read for 32 tokens at a time.  7001 tokens of 48 heads of 128 in bf16: 29.8 us,
+// 5.8 TB/s; with these reads token by token 33.6 us, with the sines in every
 // thread (100 registers, 12 warps on an SM) 62.8 us.
 template <bool VEC, int SRC, int DST>
 __global__ void __launch_bounds__(kMaxThreads + 32, 3)
