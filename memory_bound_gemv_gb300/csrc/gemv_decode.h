@@ -121,6 +121,7 @@ struct NormArgs {
     int64_t rows;
     int width;
     int post, layer, unit_offset;
+    int staged;  // bits 0..3: post_w, gate, pre_w, pre_b stand in shared memory
     float alpha, eps;
 };
 cudaError_t launch_norm(const NormArgs &a, bool vec, int sm_count, cudaStream_t s);

@@ -67,10 +67,11 @@ __device__ __forceinline__ uint4 ld_once16(const void *p)
 // steps of eight elements are counted from the border before the row's
 // beginning in out, which is where its beginning in the other tensors of the
 // same layout has one too: those are moved whole, and only the row's first and
-// last elements one by one.  What lies otherwise (weights shared by all rows)
-// is loaded in the aligned windows that hold it, and the first `skip` elements
-// are shifted out.  8192 x 4001 in bf16: 124.7 us, with loads and stores of
-// single elements 250.8 us.
+// last elements one by one.  Operands shared by all rows lie otherwise: a block
+// lays them out once in shared memory (Staged).  What does not fit there is
+// loaded in the aligned windows that hold it, and the first `skip` elements are
+// shifted out.  8192 x 4001 in bf16: 74.2 us; with windows for the shared
+// operands too 124.7 us, with loads and stores of single elements 250.8 us.
 template <int E>
 struct Window {
     static constexpr int kSize = E == GEMV_ELEM_F32 ? 4 : 2;
@@ -109,12 +110,15 @@ struct Window {
     {
         w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
     }
-    __device__ __forceinline__ void floats(float (&x)[8]) const
+    __device__ __forceinline__ void floats(float (&x)[8]) const { shifted(__any_sync(0xFFFFFFFFu, skip != 0), x); }
+    // the same where the warp's lanes are not all here
+    __device__ __forceinline__ void floats_one(float (&x)[8]) const { shifted(skip != 0, x); }
+    __device__ __forceinline__ void shifted(bool any, float (&x)[8]) const
     {
         uint32_t t[kWords];
 #pragma unroll
         for (int i = 0; i < kWords; ++i) t[i] = w[i];
-        if (__any_sync(0xFFFFFFFFu, skip != 0)) {
+        if (any) {
             const int words = E == GEMV_ELEM_F32 ? skip : skip >> 1;
 #pragma unroll
             for (int d = 2; d > 0; d /= 2)
@@ -209,25 +213,67 @@ struct Stream {
     }
 };
 
-// The same for rows that begin anywhere.
+// The same for rows that begin anywhere: whole pieces where they lie at a
+// border, single elements where not; those outside the row read 0.
 template <bool WIDE>
 struct Stream<false, WIDE> {
-    Window<WIDE ? GEMV_ELEM_F32 : GEMV_ELEM_F16> v;
-    __device__ __forceinline__ void load(const unsigned char *row, int at, int, int width) { v.load(row, at, width); }
+    static constexpr int kSize = WIDE ? 4 : 2, kWords = WIDE ? 8 : 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const unsigned char *row, int at, int, int width)
+    {
+        const unsigned char *p = row + static_cast<int64_t>(at) * kSize;
+        if (at >= 0 && at + 8 <= width && (reinterpret_cast<uintptr_t>(p) & (8 * kSize - 1)) == 0) {
+            if constexpr (WIDE) {
+                ld_global32(p, w);
+            } else {
+                const uint4 v = ld_once16(p);
+                w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (at + i < 0 || at + i >= width) continue;
+            if constexpr (WIDE)
+                w[i] = reinterpret_cast<const uint32_t *>(p)[i];
+            else
+                w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p)[i]) << (16 * (i & 1));
+        }
+    }
     template <int E>
     __device__ __forceinline__ void floats(float (&x)[8]) const
     {
-        if (WIDE) {
-            v.floats(x);
-        } else {
-            Window<E == GEMV_ELEM_F32 ? GEMV_ELEM_F16 : E> t;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) t.w[i] = v.w[i];
-            t.skip = v.skip;
-            t.floats(x);
+        for (int i = 0; i < 8; i += 2) {
+            if constexpr (WIDE) {
+                x[i] = __uint_as_float(w[i]), x[i + 1] = __uint_as_float(w[i + 1]);
+            } else {
+                const float2 f = elem_unpack2<E == GEMV_ELEM_F32 ? GEMV_ELEM_F16 : E>(w[i / 2]);
+                x[i] = f.x, x[i + 1] = f.y;
+            }
         }
     }
 };
+
+// An operand shared by all rows, in shared memory as FP32: element j stands in
+// line (j + 8) % 8, column (j + 8) / 8, zeros around the row.  Whatever the row's
+// shift, neighbouring threads then read neighbouring words, one element of each
+// thread's eight at a time, and no instruction goes into shifting.
+__device__ __forceinline__ void stage_operand(float *to, int columns, const void *from, int elem, int width)
+{
+    by_elem(elem, [&](auto e) {
+        for (int c = threadIdx.x; c < columns; c += blockDim.x) {
+            Window<decltype(e)::value> v;
+            float t[8];
+            v.load(static_cast<const unsigned char *>(from), 8 * c - 8, width);
+            v.floats_one(t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) to[i * columns + c] = t[i];
+        }
+    });
+}
 
 // The type of y or x where WIDE leaves only two.
 template <bool WIDE, typename F>
@@ -263,29 +309,27 @@ __device__ __forceinline__ float row_sum(float v, Sums &s, int turn)
 }
 
 // x -> (x - mean) / sqrt(var + eps), or x / sqrt(mean of squares + eps), for
-// values held in registers; cnt[k] of the eight values of step k exist.
+// values held in registers.  Elements that do not exist are 0 before and after
+// (every operand reads 0 there; where a factor is infinite or NaN, so is the row).
 template <int K, bool VEC, bool FULL>
 __device__ __forceinline__ void normalise(float (&x)[K][8], const int (&at)[K], int shift_by, const NormArgs &a, Sums &s,
                                           int turn)
 {
     const float inv_n = 1.f / static_cast<float>(a.width);
-    auto mask = [&](float shift) {  // elements that do not exist become 0
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                x[k][e] = FULL || static_cast<unsigned>(at[k] - shift_by + (VEC ? 0 : e)) < static_cast<unsigned>(a.width)
-                              ? x[k][e] - shift
-                              : 0.f;
-    };
-    if (!FULL) mask(0.f);
     if (a.layer) {
         float t = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int e = 0; e < 8; ++e) t += x[k][e];
-        mask(row_sum(t, s, turn) * inv_n);
+        const float mean = row_sum(t, s, turn) * inv_n;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                x[k][e] = FULL || static_cast<unsigned>(at[k] - shift_by + (VEC ? 0 : e)) < static_cast<unsigned>(a.width)
+                              ? x[k][e] - mean
+                              : 0.f;
     }
     float q = 0.f;
 #pragma unroll
@@ -344,10 +388,24 @@ __global__ void __launch_bounds__(MAXT, MINB) mbg_norm_kernel(const __grid_const
 #pragma unroll
         for (int k = 0; k < K; ++k) r[k].load(p, at[k] - from, cnt[k], a.width);
     };
+    // operands shared by all rows, where those begin anywhere
+    extern __shared__ float staged[];
+    const int columns = K * static_cast<int>(blockDim.x) + 1;
     // x[k][i] = f(x[k][i], operand)
     float x[K][8];
     int shift = 0;
-    auto with = [&](const void *base, int elem, int64_t stride, auto f) {
+    auto with = [&](int which, const void *base, int elem, int64_t stride, auto f) {
+        if (!VEC && ((a.staged >> which) & 1)) {
+            const float *lines = staged + __popc(a.staged & ((1 << which) - 1)) * 8 * columns;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int line = (i - shift) & 7, col = line > i ? 0 : 1;
+                const float *from = lines + line * columns + col + threadIdx.x;
+#pragma unroll
+                for (int k = 0; k < K; ++k) x[k][i] = f(x[k][i], from[k * blockDim.x]);
+            }
+            return;
+        }
         const unsigned char *p = row_of(base, elem, row, stride);
         by_elem(elem, [&](auto e) {
             float t[K][8];
@@ -363,6 +421,17 @@ __global__ void __launch_bounds__(MAXT, MINB) mbg_norm_kernel(const __grid_const
     prefetch(row);
     request_y(row);
     request_r(row);
+    if (!VEC) {
+        int n = 0;
+        auto stage = [&](int which, const void *from, int elem) {
+            if ((a.staged >> which) & 1) stage_operand(staged + n++ * 8 * columns, columns, from, elem, a.width);
+        };
+        stage(0, a.post_w, a.post_e);
+        stage(1, a.gate, a.gate_e);
+        stage(2, a.pre_w, a.pre_w_e);
+        stage(3, a.pre_b, a.pre_b_e);
+        __syncthreads();
+    }
     for (int turn = 0;; turn ^= 4) {
         shift = shift_of(row);
         const int64_t next = kNext ? row + gridDim.x : a.rows;
@@ -374,9 +443,9 @@ __global__ void __launch_bounds__(MAXT, MINB) mbg_norm_kernel(const __grid_const
         if (kNext && next < a.rows) request_y(next);
         if (a.post) {
             normalise<K, VEC, FULL>(x, at, shift, a, sums, turn);
-            if (a.post_w) with(a.post_w, a.post_e, a.post_s, product);
+            if (a.post_w) with(0, a.post_w, a.post_e, a.post_s, product);
         }
-        if (a.gate) with(a.gate, a.gate_e, a.gate_s, product);
+        if (a.gate) with(1, a.gate, a.gate_e, a.gate_s, product);
         by_stream<X32>(a.r_e, [&](auto e) {
             constexpr int E = decltype(e)::value;
             unsigned char *p = const_cast<unsigned char *>(row_of(a.out, E, row, a.out_s));
@@ -394,9 +463,9 @@ __global__ void __launch_bounds__(MAXT, MINB) mbg_norm_kernel(const __grid_const
             normalise<K, VEC, FULL>(x, at, shift, a, sums, turn + 2);
             if (a.pre_w) {
                 const float unit = a.unit_offset ? 1.f : 0.f;
-                with(a.pre_w, a.pre_w_e, a.pre_w_s, [&](float v, float w) { return v * (w + unit); });
+                with(2, a.pre_w, a.pre_w_e, a.pre_w_s, [&](float v, float w) { return v * (w + unit); });
             }
-            if (a.pre_b) with(a.pre_b, a.pre_b_e, a.pre_b_s, [](float v, float w) { return v + w; });
+            if (a.pre_b) with(3, a.pre_b, a.pre_b_e, a.pre_b_s, [](float v, float w) { return v + w; });
             by_elem(a.h_e, [&](auto e) {
                 constexpr int E = decltype(e)::value;
                 unsigned char *p = const_cast<unsigned char *>(row_of(a.h, E, row, a.h_s));
@@ -524,11 +593,13 @@ __global__ void __launch_bounds__(kLongThreads) mbg_norm_long_kernel(const __gri
     }
 }
 
-cudaError_t launch_rows(void (*fn)(NormArgs), const NormArgs &a, int64_t blocks, int threads, cudaStream_t s)
+cudaError_t launch_rows(void (*fn)(NormArgs), const NormArgs &a, int64_t blocks, int threads, cudaStream_t s,
+                        size_t smem = 0)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -538,21 +609,46 @@ cudaError_t launch_rows(void (*fn)(NormArgs), const NormArgs &a, int64_t blocks,
     return cudaLaunchKernelEx(&cfg, fn, a);
 }
 
+// Shared memory that staged operands may take.
+constexpr int kStageBytes = 224 * 1024;
+
 // Blocks that fit on the GPU at once, each going through rows.
 template <int K, bool VEC, bool FULL, bool Y32, bool X32>
-cudaError_t launch_fitting(const NormArgs &a, int threads, int sm_count, cudaStream_t s)
+cudaError_t launch_fitting(NormArgs a, int threads, int sm_count, cudaStream_t s)
 {
     auto fn = mbg_norm_kernel<K, 512, 1, VEC, FULL, Y32, X32>;
-    static std::atomic<int> fit[512 / 32 + 1];  // blocks per SM, by warps (0: not asked yet)
-    int per_sm = fit[threads / 32].load(std::memory_order_relaxed);
+    static std::atomic<int> fit[512 / 32 + 1][5];  // blocks per SM, by warps and staged operands (0: not asked yet)
+    const int each = 32 * (K * threads + 1);       // bytes of a staged operand
+    int count = 0;
+    a.staged = 0;
+    if (!VEC) {
+        const bool shared[4] = {a.post_w && !a.post_s, a.gate && !a.gate_s, a.pre_w && !a.pre_w_s, a.pre_b && !a.pre_b_s};
+        for (int i = 0; i < 4; ++i)
+            if (shared[i] && (count + 1) * each <= kStageBytes) {
+                a.staged |= 1 << i;
+                ++count;
+            }
+    }
+    const int smem = count * each;
+    if (smem > 0) {
+        static std::atomic<uint64_t> ready{0};  // a bit per device
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess && !(ready.load(std::memory_order_relaxed) >> (dev & 63) & 1)) {
+            e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageBytes);
+            if (e == cudaSuccess) ready.fetch_or(uint64_t{1} << (dev & 63), std::memory_order_relaxed);
+        }
+        if (e != cudaSuccess) return e;
+    }
+    int per_sm = fit[threads / 32][count].load(std::memory_order_relaxed);
     if (per_sm == 0) {
-        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, threads, 0);
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, threads, smem);
         if (e != cudaSuccess) return e;
         if (per_sm < 1) per_sm = 1;
-        fit[threads / 32].store(per_sm, std::memory_order_relaxed);
+        fit[threads / 32][count].store(per_sm, std::memory_order_relaxed);
     }
     const int64_t most = static_cast<int64_t>(per_sm) * sm_count;
-    return launch_rows(fn, a, a.rows < most ? a.rows : most, threads, s);
+    return launch_rows(fn, a, a.rows < most ? a.rows : most, threads, s, smem);
 }
 
 template <int K, bool VEC, bool Y32, bool X32>
@@ -584,7 +680,7 @@ cudaError_t launch(const NormArgs &a, int sm_count, cudaStream_t s)
     // rows: small blocks with several steps per thread, so that several rows
     // are in different phases on one SM.
     const bool many = a.rows > 2 * sm_count;
-    if (chunks > 1024 || (VEC && many && !Y32 && !X32 && chunks > 256)) return launch_steps<4, VEC, Y32, X32>(a, sm_count, s);
+    if (chunks > 1024 || (many && !Y32 && !X32 && chunks > 256)) return launch_steps<4, VEC, Y32, X32>(a, sm_count, s);
     if (chunks > (many ? 128 : 512)) return launch_steps<2, VEC, Y32, X32>(a, sm_count, s);
     return launch_steps<1, VEC, Y32, X32>(a, sm_count, s);
 }
