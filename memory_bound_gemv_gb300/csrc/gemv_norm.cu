@@ -70,8 +70,8 @@ __device__ __forceinline__ uint4 ld_once16(const void *p)
 // last elements one by one.  Operands shared by all rows lie otherwise: a block
 // lays them out once in shared memory (Staged).  What does not fit there is
 // loaded in the aligned windows that hold it, and the first `skip` elements are
-// shifted out.  8192 x 4001 in bf16: 74.2 us; with windows for the shared
-// operands too 124.7 us, with loads and stores of single elements 250.8 us.
+// shifted out.  8192 x 4001 in bf16: 73.9 us; with windows for the shared
+// operands too 93.0 us, with loads and stores of single elements 250.8 us.
 template <int E>
 struct Window {
     static constexpr int kSize = E == GEMV_ELEM_F32 ? 4 : 2;
@@ -344,7 +344,8 @@ __device__ __forceinline__ void normalise(float (&x)[K][8], const int (&at)[K], 
 }
 
 // A block goes through rows and requests the next row's y and x while it
-// works on the present one (MINB 1), or takes one row (MINB blocks on an SM);
+// works on the present one (MINB 1); or MINB blocks are on an SM, each with one
+// row, or with rows that begin anywhere several, one after another;
 // what else differs from row to row is prefetched into L2, what does not comes
 // from L1.  FULL: every thread has all of its K steps.
 template <int K, int MAXT, int MINB, bool VEC, bool FULL, bool Y32, bool X32>
@@ -353,7 +354,8 @@ __global__ void __launch_bounds__(MAXT, MINB) mbg_norm_kernel(const __grid_const
     __shared__ Sums sums;
     pdl_trigger();
     pdl_wait();
-    constexpr bool kNext = MINB == 1;  // rows ahead; otherwise a block for each row
+    constexpr bool kLoop = MINB == 1 || !VEC;  // otherwise a block for each row
+    constexpr bool kNext = MINB == 1;          // rows ahead
     int64_t row = blockIdx.x;
     int at[K], cnt[K];
     Stream<VEC, Y32> y[K];
@@ -430,11 +432,11 @@ __global__ void __launch_bounds__(MAXT, MINB) mbg_norm_kernel(const __grid_const
         stage(1, a.gate, a.gate_e);
         stage(2, a.pre_w, a.pre_w_e);
         stage(3, a.pre_b, a.pre_b_e);
-        __syncthreads();
+        if (n > 0) __syncthreads();
     }
     for (int turn = 0;; turn ^= 4) {
         shift = shift_of(row);
-        const int64_t next = kNext ? row + gridDim.x : a.rows;
+        const int64_t next = kLoop ? row + gridDim.x : a.rows;
         if (kNext) prefetch(next);
         by_stream<Y32>(a.y_e, [&](auto e) {
 #pragma unroll
@@ -473,8 +475,12 @@ __global__ void __launch_bounds__(MAXT, MINB) mbg_norm_kernel(const __grid_const
                 for (int k = 0; k < K; ++k) store_step<VEC, E>(p, at[k] - shift, cnt[k], a.width, x[k]);
             });
         }
-        if (!kNext || next >= a.rows) break;
+        if (!kLoop || next >= a.rows) break;
         row = next;
+        if (!kNext) {
+            request_y(row);
+            request_r(row);
+        }
     }
 }
 
@@ -609,45 +615,52 @@ cudaError_t launch_rows(void (*fn)(NormArgs), const NormArgs &a, int64_t blocks,
     return cudaLaunchKernelEx(&cfg, fn, a);
 }
 
-// Shared memory that staged operands may take.
+// Shared memory that an SM's staged operands may take.
 constexpr int kStageBytes = 224 * 1024;
 
 // Blocks that fit on the GPU at once, each going through rows.
-template <int K, bool VEC, bool FULL, bool Y32, bool X32>
+template <int K, int MAXT, int MINB, bool VEC, bool FULL, bool Y32, bool X32>
 cudaError_t launch_fitting(NormArgs a, int threads, int sm_count, cudaStream_t s)
 {
-    auto fn = mbg_norm_kernel<K, 512, 1, VEC, FULL, Y32, X32>;
-    static std::atomic<int> fit[512 / 32 + 1][5];  // blocks per SM, by warps and staged operands (0: not asked yet)
+    auto fn = mbg_norm_kernel<K, MAXT, MINB, VEC, FULL, Y32, X32>;
+    static std::atomic<int> fit[MAXT / 32 + 1][5];  // blocks per SM, by warps and staged operands (0: not asked yet)
     const int each = 32 * (K * threads + 1);       // bytes of a staged operand
-    int count = 0;
+    int count = 0, smem = 0;
+    auto blocks = [&](int64_t *n) {
+        int per_sm = fit[threads / 32][count].load(std::memory_order_relaxed);
+        if (per_sm == 0) {
+            const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, threads, smem);
+            if (e != cudaSuccess) return e;
+            if (per_sm < 1) per_sm = 1;
+            fit[threads / 32][count].store(per_sm, std::memory_order_relaxed);
+        }
+        *n = static_cast<int64_t>(per_sm) * sm_count;
+        return cudaSuccess;
+    };
+    int64_t most = 0;
+    cudaError_t e = blocks(&most);
     a.staged = 0;
-    if (!VEC) {
+    // Staging pays from the third row of a block on (1500 x 4001 in binary16,
+    // 2.5 rows a block: 19.0 us against 20.9; 600 rows, one a block: 8.8
+    // against 7.5; in FP32, two a block, 10.5 against 10.2).
+    if (!VEC && e == cudaSuccess && a.rows > 2 * most) {
         const bool shared[4] = {a.post_w && !a.post_s, a.gate && !a.gate_s, a.pre_w && !a.pre_w_s, a.pre_b && !a.pre_b_s};
         for (int i = 0; i < 4; ++i)
-            if (shared[i] && (count + 1) * each <= kStageBytes) {
+            if (shared[i] && (count + 1) * each <= kStageBytes / MINB) {
                 a.staged |= 1 << i;
                 ++count;
             }
-    }
-    const int smem = count * each;
-    if (smem > 0) {
+        smem = count * each;
         static std::atomic<uint64_t> ready{0};  // a bit per device
         int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e == cudaSuccess && !(ready.load(std::memory_order_relaxed) >> (dev & 63) & 1)) {
+        if (count > 0) e = cudaGetDevice(&dev);
+        if (count > 0 && e == cudaSuccess && !(ready.load(std::memory_order_relaxed) >> (dev & 63) & 1)) {
             e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageBytes);
             if (e == cudaSuccess) ready.fetch_or(uint64_t{1} << (dev & 63), std::memory_order_relaxed);
         }
-        if (e != cudaSuccess) return e;
+        if (count > 0 && e == cudaSuccess) e = blocks(&most);
     }
-    int per_sm = fit[threads / 32][count].load(std::memory_order_relaxed);
-    if (per_sm == 0) {
-        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, threads, smem);
-        if (e != cudaSuccess) return e;
-        if (per_sm < 1) per_sm = 1;
-        fit[threads / 32][count].store(per_sm, std::memory_order_relaxed);
-    }
-    const int64_t most = static_cast<int64_t>(per_sm) * sm_count;
+    if (e != cudaSuccess) return e;
     return launch_rows(fn, a, a.rows < most ? a.rows : most, threads, s, smem);
 }
 
@@ -655,20 +668,30 @@ template <int K, bool VEC, bool Y32, bool X32>
 cudaError_t launch_steps(const NormArgs &a, int sm_count, cudaStream_t s)
 {
     const int chunks = (a.width + (VEC ? 7 : 14)) / 8, threads = ((chunks + K - 1) / K + 31) / 32 * 32;
-    // Operands of each row: a block per row, two wide ones on an SM, hides the
-    // loads of those better than rows ahead do (331 x 14336 with gate, weight
-    // and bias of each row 15.6 us against 18.2, 2000 x 8192 38.3 against 42.7;
-    // with shared ones 28.1 against 26.7).  400 x 4096, all rows at once on the
-    // GPU, is faster without (5.4 us against 6.4).
+    // Rows of more than 256 threads: one such block at a time on an SM leaves it
+    // idle at every sum, so two of fewer registers each take turns.  A block
+    // per row, without rows ahead (2000 x 9216 in bf16 29.8 us against 37.3, 200
+    // rows 6.2 against 6.5; 100 rows 4.9 against 4.2: not with shared operands
+    // on fewer rows than SMs); where rows begin anywhere, blocks that keep their
+    // staged operands (2000 x 9001 50.6 us against 66.7), up to 320 threads,
+    // beyond which registers spill.  Operands of each row are loaded late in
+    // it, which blocks hide better than rows ahead do (2000 x 8192 with gate,
+    // weight and bias of each row 38.3 us against 42.7; with shared ones 28.1
+    // against 26.7).  400 x 4096, all rows at once on the GPU, is faster without
+    // (5.4 us against 6.4).
     const bool each = a.gate_s || a.pre_w_s || a.pre_b_s;
+    if constexpr (!VEC && K == 4) {
+        if (threads > 256 && threads <= 320 && a.rows > sm_count)
+            return launch_fitting<4, 320, 2, false, false, Y32, X32>(a, threads, sm_count, s);
+    }
     if constexpr (VEC && K == 4) {
-        if (each && threads <= 448 && (threads > 256 || a.rows > 8 * sm_count))
+        if (threads <= 448 && (threads > 256 ? each || a.rows > sm_count : each && a.rows > 8 * sm_count))
             return launch_rows(chunks == threads * K ? mbg_norm_kernel<4, 448, 2, true, true, Y32, X32>
                                                      : mbg_norm_kernel<4, 448, 2, true, false, Y32, X32>,
                                a, a.rows, threads, s);
     }
-    if (VEC && chunks == threads * K) return launch_fitting<K, VEC, VEC, Y32, X32>(a, threads, sm_count, s);
-    return launch_fitting<K, VEC, false, Y32, X32>(a, threads, sm_count, s);
+    if (VEC && chunks == threads * K) return launch_fitting<K, 512, 1, VEC, VEC, Y32, X32>(a, threads, sm_count, s);
+    return launch_fitting<K, 512, 1, VEC, false, Y32, X32>(a, threads, sm_count, s);
 }
 
 template <bool VEC, bool Y32, bool X32>
