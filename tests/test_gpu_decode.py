@@ -721,3 +721,27 @@ def test_attn_calls_with_wide_and_narrow_loads_share_a_workspace():
         mbg.gemv_attn_paged(cache, wide, n, out=torch.full_like(wide, math.nan))
         again = mbg.gemv_attn_paged(cache, narrow, n, out=torch.full_like(wide, math.nan))
         assert same_bits(first, again)
+
+
+@pytest.mark.parametrize("width,pad", [(333, 0), (1001, 0), (4001, 0), (777, 3), (9001, 0)])
+@pytest.mark.parametrize("yt,xt", [(BF16, BF16), (F32, F16), (F32, F32)])
+def test_norm_nan_stays_in_its_row_at_odd_widths(yt, xt, width, pad):
+    rows = 1400  # several rows per block, neighbours in other blocks
+    y = normal(1, (rows, width + pad), yt)[:, :width]
+    x = normal(2, (rows, width + pad), xt)[:, :width]
+    w, g = normal(3, (width,), F16), normal(4, (width,), BF16)
+    # rows laid out like x: where a row begins settles how its sums are grouped
+    call = dict(post=True, post_weight=w, gate=g, pre_weight=w, kind="layer", h_dtype=F16)
+    call["out"] = torch.empty(rows, width + pad, dtype=xt, device="cuda")[:, :width]
+    out, h = mbg.gemv_norm_residual(y, x, **call)
+    y[1::3] = math.nan
+    x[2::3] = math.inf
+    call["out"] = torch.empty_strided(out.shape, out.stride(), dtype=xt, device="cuda")
+    bad_out, bad_h = mbg.gemv_norm_residual(y, x, **call)
+    assert same_bits(out[::3].contiguous(), bad_out[::3].contiguous())
+    assert same_bits(h[::3].contiguous(), bad_h[::3].contiguous())
+    assert bad_out[1::3].isnan().all() and bad_h[1::3].isnan().all() and bad_h[2::3].isnan().all()
+    # in place: the neighbours' elements are being written meanwhile
+    y, x = normal(1, (rows, width + pad), yt)[:, :width], normal(2, (rows, width + pad), xt)[:, :width]
+    mbg.gemv_norm_residual(y, x, **{**call, "out": x, "h": y, "h_dtype": None})
+    assert same_bits(x.contiguous(), out.contiguous())
