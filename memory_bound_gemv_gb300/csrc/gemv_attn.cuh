@@ -35,8 +35,8 @@
 // of 16 or 32 tokens; all tiles of the call are numbered and each CTA takes an equal
 // share of consecutive ones, whatever the lengths (they are read on the
 // device, so a captured graph serves any lengths).  A share's border that
-// falls close to a row's end moves there, so that short rows are not cut.  A
-// row inside one CTA's share is written at once; otherwise each CTA leaves
+// falls close to a row's end moves there, so that short rows are not cut, nor
+// are others that spread evenly over the CTAs whole.  A row inside one CTA's share is written at once; otherwise each CTA leaves
 // (O, m, l) in the workspace and the last to arrive joins them, always in the
 // same order, so results do not depend on the order of arrival.
 #pragma once
@@ -226,10 +226,18 @@ struct Kernel {
     // This CTA's part of the call's work.  A row of n tiles counts `lead` + n:
     // starting a row costs about that many tiles.  CTA c's share ends where CTA
     // c + 1's begins, at total * c / ctas -- or at an end of the row there, if
-    // that is at most `near` tiles away.
+    // that is at most kNear tiles away (one round of the warps: 160 rows of 2000
+    // tokens of 128 36.0 us, two rounds 37.2; 128 of 500 16.2 and 17.6).  A cut
+    // costs as much as some kUncut tiles: rows of no more have none (384 rows of
+    // 256 tokens: 15.5 us, cut 23.4), nor has any row where the CTA with most to
+    // do would then have no more than that above the mean (384 rows of 400 tokens
+    // 20.3 us, cut 27.2; of 1000 38.8 and 42.1; but 512 of 1000 64.9 and 52.0,
+    // 800 ragged ones of up to 800 45.9 and 39.0).
+    static constexpr int kNear = kWarps, kUncut = 16;
     struct Share {
         int64_t total, x0, x1;
-        int ctas, cta, near, lead;
+        int ctas, cta, lead;
+        int uncut;  // rows of up to so many tiles are not cut
     };
     // The row that is looked at next; `before` counts what lies before its
     // sequence, per cached head.
@@ -328,8 +336,9 @@ struct Kernel {
     static __device__ __forceinline__ int64_t border(const Share &w, int64_t x, int64_t r0, int64_t r1)
     {
         const int64_t d0 = x - r0 - w.lead, d1 = r1 - x;
-        if (d0 <= d1) return d0 <= w.near ? r0 : x;
-        return d1 <= w.near ? r1 : x;
+        const int64_t tiles = r1 - r0 - w.lead, near = tiles <= w.uncut ? tiles : kNear;
+        if (d0 <= d1) return d0 <= near ? r0 : x;
+        return d1 <= near ? r1 : x;
     }
 
     // Looks up the CTA's next segment (one thread).
@@ -810,8 +819,8 @@ struct Kernel {
         // borders inside the row: the first and the last CTA that begins in it
         const Share &w = sh.share;
         const int64_t tile0 = seg.r0 + w.lead, r1 = tile0 + seg.tiles;
-        const int first_in = static_cast<int>(((tile0 + w.near + 1) * w.ctas + w.total - 1) / w.total);
-        const int last_in = static_cast<int>(((r1 - w.near) * w.ctas - 1) / w.total);
+        const int first_in = static_cast<int>(((tile0 + kNear + 1) * w.ctas + w.total - 1) / w.total);
+        const int last_in = static_cast<int>(((r1 - kNear) * w.ctas - 1) / w.total);
         const int c0 = first_in - 1, n = last_in - c0 + 1;
         if (c0 < 0 || c0 > w.cta || last_in < w.cta || last_in >= w.ctas) {
             // lengths that changed during the call: no part is where it should be
@@ -872,8 +881,10 @@ struct Kernel {
         const int step = few ? 32 : kThreads, own = few ? threadIdx.x & 31 : threadIdx.x;
         // tiles and rows per cached head over all sequences
         int64_t tiles = 0, rows = 0;
+        int longest = 0;
         for (int b0 = 0; b0 < a.kv.batch; b0 += step) {
             const int n = b0 + own < a.kv.batch ? row_span<kTokens>(a, b0 + own).tiles : 0;
+            longest = max(longest, n);
             if (few) {
                 tiles = __reduce_add_sync(kFull, n);
                 rows = __popc(__ballot_sync(kFull, n > 0));
@@ -884,9 +895,16 @@ struct Kernel {
                 rows += __syncthreads_count(n > 0);
             }
         }
-        // a row is not cut into shares of less than a.least rounds of a block's
-        // warps: a part more to join costs more than a round
-        const int64_t most = max(tiles * hks / (a.least * kWarps), rows * hks);
+        longest = __reduce_max_sync(kFull, longest);
+        if (!few) {
+            __syncthreads();
+            if ((threadIdx.x & 31) == 0) sh.scan[threadIdx.x >> 5] = longest;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) longest = max(longest, sh.scan[w]);
+        }
+        // shares of a round of the block's warps at least, but for short rows
+        const int64_t most = max(tiles * hks / kWarps, rows * hks);
         const int ctas = static_cast<int>(min(most, static_cast<int64_t>(gridDim.x))), cta = blockIdx.x;
         if (tiles == 0 || cta >= ctas) return;
         const int64_t total = (tiles + rows * a.lead) * hks;
@@ -897,8 +915,10 @@ struct Kernel {
             sh.share.x1 = total * (cta + 1) / ctas;
             sh.share.ctas = ctas;
             sh.share.cta = cta;
-            sh.share.near = a.near * kWarps;
             sh.share.lead = a.lead;
+            // uncut rows go to CTAs as evenly as their number allows
+            const int64_t each = (rows * hks + ctas - 1) / ctas;
+            sh.share.uncut = (each * longest - kUncut) * ctas <= tiles * hks ? INT32_MAX : kUncut;
             sh.cursor.b = a.kv.batch;
             sh.seg[0].t0 = sh.seg[0].t1 = 0;
         }

@@ -55,8 +55,7 @@ struct AttnArgs {
     float *row_lse;             // same rows x 8 * NT heads: log2 of the softmax denominator
     float *logits;              // [rows][capacity][logit_heads], log2 units; weights only
     int logit_heads;
-    int near, least;            // rounds of a block's warps: see attn::Kernel
-    int lead;                   // tiles
+    int lead;                   // tiles that a row's beginning counts like
 };
 
 // Launches for one cache type; vec: 16-byte loads are possible; big: one block

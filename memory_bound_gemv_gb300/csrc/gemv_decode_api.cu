@@ -190,14 +190,10 @@ gemv_status_t gemv_attn_paged(const gemv_kv_t *kv, const gemv_attn_t *args, void
     // Few rows: one block of all an SM's warps, a third of the parts to join
     // (8 rows of 131001 tokens of 128: 87.8 us, with blocks of four warps 92.8).
     // Many rows: blocks of four warps, one joins while the others load (384
-    // rows of 1000 tokens: 42.5 us against 47.1).
+    // rows of 1000 tokens: 38.8 us against 47.1).
     const bool big = vec && p.rows <= dev.sm_count / 2;
-    // A cut costs a join of some 4 us, about as much as two rounds of a small
-    // block's four tiles: rows are not cut finer, nor that close to their
-    // ends (384 rows of 256 tokens: 15.6 us, one round for both 23.5).  A row's
-    // beginning counts like `lead` tiles (48 ragged sequences of up to 6000
+    // A row's beginning counts like `lead` tiles (48 ragged sequences of up to 6000
     // tokens with their weights: 115 us, 123 us with none).
-    a.near = a.least = big ? 1 : 2;
     a.lead = big ? 16 : 8;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = kv->elem == GEMV_ELEM_F16 ? launch_attn_f16(a, vec, nt, big, dev.sm_count, s)
