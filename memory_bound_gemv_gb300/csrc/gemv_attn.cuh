@@ -36,9 +36,10 @@
 // share of consecutive ones, whatever the lengths (they are read on the
 // device, so a captured graph serves any lengths).  A share's border that
 // falls close to a row's end moves there, so that short rows are not cut, nor
-// are others that spread evenly over the CTAs whole.  A row inside one CTA's share is written at once; otherwise each CTA leaves
-// (O, m, l) in the workspace and the last to arrive joins them, always in the
-// same order, so results do not depend on the order of arrival.
+// are others that spread evenly over the CTAs whole.  A row inside one CTA's
+// share is written at once; otherwise each CTA leaves (O, m, l) in the workspace
+// and the last to arrive joins them, always in the same order, so results do
+// not depend on the order of arrival.
 #pragma once
 
 #include <cuda_bf16.h>

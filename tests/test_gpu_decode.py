@@ -745,3 +745,12 @@ def test_norm_nan_stays_in_its_row_at_odd_widths(yt, xt, width, pad):
     y, x = normal(1, (rows, width + pad), yt)[:, :width], normal(2, (rows, width + pad), xt)[:, :width]
     mbg.gemv_norm_residual(y, x, **{**call, "out": x, "h": y, "h_dtype": None})
     assert same_bits(x.contiguous(), out.contiguous())
+
+
+@pytest.mark.parametrize("batch,longest,spread,window", [
+    (57, 400, 0, 0), (57, 400, 3, 0), (57, 400, 60, 0), (24, 900, 0, 0), (24, 900, 17, 0), (48, 300, 200, 256), (64, 700, 1, 0)])
+def test_attn_rows_of_about_one_length(batch, longest, spread, window):
+    # uncut, cut and ragged rows, by lanes (up to 32 sequences) and by blocks
+    lengths = [longest - (7 * b) % (spread + 1) for b in range(batch)]
+    cache = make_cache(batch, lengths, 8, 64, 16, BF16)
+    check_attn(cache, normal(batch + 1, (batch, 16, 64), BF16), lengths, window=window)
