@@ -673,8 +673,11 @@ cudaError_t launch_steps(const NormArgs &a, int sm_count, cudaStream_t s)
     // per row, without rows ahead (2000 x 9216 in bf16 29.8 us against 37.3, 200
     // rows 6.2 against 6.5; 100 rows 4.9 against 4.2: not with shared operands
     // on fewer rows than SMs); where rows begin anywhere, blocks that keep their
-    // staged operands (2000 x 9001 50.6 us against 66.7), up to 320 threads,
-    // beyond which registers spill.  Operands of each row are loaded late in
+    // staged operands (2000 x 9001 50.6 us against 66.7), up to 320 threads.  Up
+    // to 384 registers spill and an SM has no room to stage three operands twice:
+    // faster where nothing is staged (200 x 11908 in bf16 9.5 us against 11.7, 600
+    // 21.9 against 23.5) or both streams are FP32 (2000 95.1 against 101), not for
+    // more rows of other types (69.0 against 71.2).  Operands of each row are loaded late in
     // it, which blocks hide better than rows ahead do (2000 x 8192 with gate,
     // weight and bias of each row 38.3 us against 42.7; with shared ones 28.1
     // against 26.7).  400 x 4096, all rows at once on the GPU, is faster without
@@ -683,6 +686,8 @@ cudaError_t launch_steps(const NormArgs &a, int sm_count, cudaStream_t s)
     if constexpr (!VEC && K == 4) {
         if (threads > 256 && threads <= 320 && a.rows > sm_count)
             return launch_fitting<4, 320, 2, false, false, Y32, X32>(a, threads, sm_count, s);
+        if (threads > 320 && threads <= 384 && a.rows > sm_count && (a.rows <= 4 * sm_count || (Y32 && X32)))
+            return launch_fitting<4, 384, 2, false, false, Y32, X32>(a, threads, sm_count, s);
     }
     if constexpr (VEC && K == 4) {
         if (threads <= 448 && (threads > 256 ? each || a.rows > sm_count : each && a.rows > 8 * sm_count))

@@ -723,7 +723,7 @@ def test_attn_calls_with_wide_and_narrow_loads_share_a_workspace():
         assert same_bits(first, again)
 
 
-@pytest.mark.parametrize("width,pad", [(333, 0), (1001, 0), (4001, 0), (777, 3), (9001, 0)])
+@pytest.mark.parametrize("width,pad", [(333, 0), (1001, 0), (4001, 0), (777, 3), (9001, 0), (11908, 0)])
 @pytest.mark.parametrize("yt,xt", [(BF16, BF16), (F32, F16), (F32, F32)])
 def test_norm_nan_stays_in_its_row_at_odd_widths(yt, xt, width, pad):
     rows = 1400  # several rows per block, neighbours in other blocks
