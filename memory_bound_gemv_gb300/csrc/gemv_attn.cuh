@@ -23,9 +23,12 @@
 //     consecutive d of tokens 2t, 2t + 1, 2t + 8, 2t + 9; byte permutes pair
 //     the tokens.  P comes out of S^T's registers by a transposing move
 //     (movmatrix).
-// P is split into two 16-bit parts (high and the rest), two MMAs per V tile:
-// a rounding of P to 8 (bf16) or 11 (f16) bits would be as large as that of
-// the output itself; with the rest added the error is 2^-16 or less.
+// P is split into 16-bit parts, an MMA per V tile each: a rounding of P to 8
+// (bf16) or 11 (f16) bits would be as large as that of the output itself.  In
+// bf16 three parts hold the 24 bits of FP32.  In f16 two parts hold 22 bits, off
+// by 2^-22 relative; as P is multiplied by 2^15 first, the smallest f16 steps lie
+// at 2^-39 of the warp's largest weight (unscaled they lie at 2^-24, where weights
+// behind a token that leads by 17 nats, a sink say, would vanish from O).
 //
 // The next tile's K is requested while the present tile's softmax and V
 // product run, and the next V after that: about 8 KB in flight per warp at a
@@ -69,15 +72,19 @@ struct Mma<__half> {
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     }
-    // Two values rounded to 16 bits, first one in the low half.
-    static __device__ __forceinline__ uint32_t pack(float lo, float hi)
+    // Two weights in parts, the first one in the low halves; kUnscale times the
+    // parts' sum are the weights.
+    static constexpr int kParts = 2;
+    static constexpr float kUnscale = 1.f / 32768.f;
+    static __device__ __forceinline__ void split(float p0, float p1, uint32_t (&w)[kParts])
     {
-        const __half2 h = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    }
-    static __device__ __forceinline__ float2 unpack(uint32_t w)
-    {
-        return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+        p0 *= 32768.f;
+        p1 *= 32768.f;
+        const __half2 high = __floats2half2_rn(p0, p1);
+        const float2 back = __half22float2(high);
+        const __half2 rest = __floats2half2_rn(p0 - back.x, p1 - back.y);
+        w[0] = *reinterpret_cast<const uint32_t *>(&high);
+        w[1] = *reinterpret_cast<const uint32_t *>(&rest);
     }
     static __device__ __forceinline__ uint16_t bits(float v) { return __half_as_ushort(__float2half_rn(v)); }
 };
@@ -92,14 +99,19 @@ struct Mma<__nv_bfloat16> {
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     }
-    static __device__ __forceinline__ uint32_t pack(float lo, float hi)
+    // Eight bits of the significand each: the upper halves of p, of what is left
+    // of it, and of what is left of that, which has no more than eight.
+    static constexpr int kParts = 3;
+    static constexpr float kUnscale = 1.f;
+    static __device__ __forceinline__ void split(float p0, float p1, uint32_t (&w)[kParts])
     {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    }
-    static __device__ __forceinline__ float2 unpack(uint32_t w)
-    {
-        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w));
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
+            w[i] = __byte_perm(b0, b1, 0x7632);
+            p0 -= __uint_as_float(b0 & 0xFFFF0000u);
+            p1 -= __uint_as_float(b1 & 0xFFFF0000u);
+        }
     }
     static __device__ __forceinline__ uint16_t bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 };
@@ -576,7 +588,7 @@ struct Kernel {
                                         make_float2(s[mt][nt][2 * rr], s[mt][nt][2 * rr + 1]);
                             }
                 }
-                uint32_t phi[MT][NT][2], plo[MT][NT][2];
+                uint32_t part[MT][NT][2][Mma<T>::kParts];
                 bool grew = false;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -616,11 +628,9 @@ struct Kernel {
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                         for (int rr = 0; rr < 2; ++rr) {
-                            const float p0 = s[mt][nt][2 * rr], p1 = s[mt][nt][2 * rr + 1];
-                            const uint32_t hi = Mma<T>::pack(p0, p1);
-                            const float2 back = Mma<T>::unpack(hi);
-                            phi[mt][nt][rr] = transpose8x8(hi);
-                            plo[mt][nt][rr] = transpose8x8(Mma<T>::pack(p0 - back.x, p1 - back.y));
+                            Mma<T>::split(s[mt][nt][2 * rr], s[mt][nt][2 * rr + 1], part[mt][nt][rr]);
+#pragma unroll
+                            for (int i = 0; i < Mma<T>::kParts; ++i) part[mt][nt][rr][i] = transpose8x8(part[mt][nt][rr][i]);
                         }
                 }
                 // O^T += V^T P^T
@@ -641,8 +651,9 @@ struct Kernel {
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
                                 float(&acc)[4] = o[(nt * DC + c) * 4 + k];
-                                Mma<T>::run(acc, a0, a1, a2, a3, phi[mt][nt][0], phi[mt][nt][1]);
-                                Mma<T>::run(acc, a0, a1, a2, a3, plo[mt][nt][0], plo[mt][nt][1]);
+#pragma unroll
+                                for (int i = 0; i < Mma<T>::kParts; ++i)
+                                    Mma<T>::run(acc, a0, a1, a2, a3, part[mt][nt][0][i], part[mt][nt][1][i]);
                             }
                         }
                     }
@@ -717,7 +728,7 @@ struct Kernel {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float ll = NT == 1 || nt == 0 ? sum[0][e] : sum[NT - 1][e];
-                    inv[e] = ll == 0.f ? 0.f : 1.f / ll;
+                    inv[e] = ll == 0.f ? 0.f : Mma<T>::kUnscale / ll;
                 }
                 store_out(a, r, i4 * 4, v, lane, inv);
             } else {
