@@ -25,10 +25,10 @@
 //     (movmatrix).
 // P is split into 16-bit parts, an MMA per V tile each: a rounding of P to 8
 // (bf16) or 11 (f16) bits would be as large as that of the output itself.  In
-// bf16 three parts hold the 24 bits of FP32.  In f16 two parts hold 22 bits, off
-// by 2^-22 relative; as P is multiplied by 2^15 first, the smallest f16 steps lie
-// at 2^-39 of the warp's largest weight (unscaled they lie at 2^-24, where weights
-// behind a token that leads by 17 nats, a sink say, would vanish from O).
+// bf16 three parts hold the 24 bits of FP32.  In f16 two parts are off by 2^-21
+// relative; P is multiplied by 2^15 first, so that the smallest f16 steps lie at
+// 2^-39 of the warp's largest weight (unscaled at 2^-24, where weights behind
+// a token that leads by 17 nats, a sink say, would vanish from O).
 //
 // The next tile's K is requested while the present tile's softmax and V
 // product run, and the next V after that: about 8 KB in flight per warp at a
@@ -73,17 +73,20 @@ struct Mma<__half> {
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     }
     // Two weights in parts, the first one in the low halves; kUnscale times the
-    // parts' sum are the weights.
+    // parts' sum are the weights.  Parts of a weight above 0 are above 0 (the high
+    // part is rounded down, the steps at the lower end are the least they can
+    // be): times an infinite value, a part of 0 would be NaN.
     static constexpr int kParts = 2;
     static constexpr float kUnscale = 1.f / 32768.f;
     static __device__ __forceinline__ void split(float p0, float p1, uint32_t (&w)[kParts])
     {
-        p0 *= 32768.f;
-        p1 *= 32768.f;
-        const __half2 high = __floats2half2_rn(p0, p1);
-        const float2 back = __half22float2(high);
-        const __half2 rest = __floats2half2_rn(p0 - back.x, p1 - back.y);
-        w[0] = *reinterpret_cast<const uint32_t *>(&high);
+        constexpr float kStep = 1.f / 16777216.f;
+        const float s0 = p0 > 0.f ? kStep : 0.f, s1 = p1 > 0.f ? kStep : 0.f;
+        p0 = fmaxf(p0 * 32768.f, s0);
+        p1 = fmaxf(p1 * 32768.f, s1);
+        asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(w[0]) : "f"(p1), "f"(p0));
+        const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&w[0]));
+        const __half2 rest = __floats2half2_rn(fmaxf(p0 - back.x, s0), fmaxf(p1 - back.y, s1));
         w[1] = *reinterpret_cast<const uint32_t *>(&rest);
     }
     static __device__ __forceinline__ uint16_t bits(float v) { return __half_as_ushort(__float2half_rn(v)); }
@@ -100,17 +103,19 @@ struct Mma<__nv_bfloat16> {
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     }
     // Eight bits of the significand each: the upper halves of p, of what is left
-    // of it, and of what is left of that, which has no more than eight.
+    // of it, and of what is left of that, which has no more than eight.  What
+    // is left of a weight above 0 (they are 2^-126 or more) counts as that much.
     static constexpr int kParts = 3;
     static constexpr float kUnscale = 1.f;
     static __device__ __forceinline__ void split(float p0, float p1, uint32_t (&w)[kParts])
     {
+        const float s0 = fminf(p0, 1.17549435e-38f), s1 = fminf(p1, 1.17549435e-38f);
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
             const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
             w[i] = __byte_perm(b0, b1, 0x7632);
-            p0 -= __uint_as_float(b0 & 0xFFFF0000u);
-            p1 -= __uint_as_float(b1 & 0xFFFF0000u);
+            p0 = fmaxf(p0 - __uint_as_float(b0 & 0xFFFF0000u), s0);
+            p1 = fmaxf(p1 - __uint_as_float(b1 & 0xFFFF0000u), s1);
         }
     }
     static __device__ __forceinline__ uint16_t bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
