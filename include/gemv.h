@@ -422,10 +422,10 @@ typedef struct {
  * kv->scores + the sum of p over the head's query heads, for the slots attended
  * to; the others are left alone.
  * workspace: device memory of gemv_attn_paged_workspace(...) bytes, 256-byte
- * aligned, of which the first GEMV_ATTN_COUNTER_BYTES + 4 * batch * q_heads
- * are zero before its first use; a call leaves it fit for the next call with the
- * same cache sizes and q_heads on the same stream.  One workspace serves one
- * call at a time.
+ * aligned, of which the first GEMV_ATTN_COUNTER_BYTES are zero before its first
+ * use; a call leaves it fit for the next call on the same stream that it is large
+ * enough for.  One workspace serves one call at a time.  Lengths that change
+ * while a call runs spoil that call's output, and no later call's.
  */
 #define GEMV_ATTN_COUNTER_BYTES 8192
 typedef struct {

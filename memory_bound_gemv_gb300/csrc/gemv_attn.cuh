@@ -279,6 +279,7 @@ struct Kernel {
         float part_l[kMaxParts][kHeads];
         int scan[kWarps];
         int last;
+        uint64_t call;    // the call's number, as counters carry it
         Share share;
         Cursor cursor;
         Segment seg[3];   // the present one, the next, and the one being looked up
@@ -399,7 +400,7 @@ struct Kernel {
     // The CTA's segments, one after another.  A warp requests the first tiles
     // of its next segment before it joins the present one, so that the loads
     // never pause between rows.
-    static __device__ void stream(const AttnArgs &a, Shared &sh)
+    static __device__ void stream(const AttnArgs &a, Shared &sh, uint64_t ticket)
     {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         const int g = lane >> 2, t = lane & 3;
@@ -515,6 +516,7 @@ struct Kernel {
             }
             if (first_segment) {  // the second segment is looked up while the first loads are under way
                 if (threadIdx.x == 0) advance(a, sh.share, sh.cursor, sh.seg[1]);
+                if (threadIdx.x == kTicketThread) sh.call = (ticket / kTickets + 1) << 2 * kCountBits;
                 __syncthreads();
                 first_segment = false;
             }
@@ -756,19 +758,40 @@ struct Kernel {
         }
     }
 
-    // Has every one of `expected` CTAs arrived at this counter?  True for the
-    // last, for which the others' parts are visible then.
-    static __device__ __forceinline__ bool last_of(Shared &sh, unsigned int *counter, int expected)
+    // A counter holds the number of the call that last used it and, in
+    // kCountBits each, two counts of that call.  What an earlier call has left there
+    // (one whose lengths changed meanwhile leaves arrivals that no one waited for)
+    // is below the present call's number and gives way to it.  The number comes from
+    // the tickets that every CTA of a call draws, kTickets in all; CTA 0 draws
+    // what the others leave.
+    static constexpr int kCountBits = 11;
+    static constexpr unsigned kTickets = 2 * kAttnMaxCtas, kTicketThread = 32;
+    static_assert(kAttnMaxCtas < 1 << kCountBits && kTicketThread < kThreads, "");
+
+    static __device__ __forceinline__ uint64_t draw_ticket(const AttnArgs &a)
+    {
+        // a part's slot 0 begins no group (join): its counter is free for the tickets
+        const unsigned long long n = blockIdx.x == 0 ? kTickets - (gridDim.x - 1) : 1;
+        return atomicAdd(reinterpret_cast<unsigned long long *>(a.arrived), n);
+    }
+
+    // Has every one of `expected` CTAs arrived at this counter's first or second
+    // count?  True for the last, for which the others' parts are visible then.
+    static __device__ __forceinline__ bool last_of(Shared &sh, uint64_t *counter, int which, int expected)
     {
         // the barrier orders the block's writes before thread 0's release, which
         // is cumulative; its acquire orders the others' parts before what the
         // block reads after the second barrier
         __syncthreads();
         if (threadIdx.x == 0) {
-            unsigned seen;
-            asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(seen) : "l"(counter) : "memory");
-            sh.last = seen == static_cast<unsigned>(expected - 1);
-            if (sh.last) *counter = 0;  // ready for the next call
+            const int shift = which * kCountBits;
+            uint64_t seen;
+            asm volatile("red.relaxed.gpu.global.max.u64 [%0], %1;" ::"l"(counter), "l"(sh.call) : "memory");
+            asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], %2;"
+                         : "=l"(seen)
+                         : "l"(counter), "l"(uint64_t{1} << shift)
+                         : "memory");
+            sh.last = static_cast<int>(seen >> shift & ((1 << kCountBits) - 1)) == expected - 1;
         }
         __syncthreads();
         return sh.last != 0;
@@ -848,12 +871,10 @@ struct Kernel {
         auto slot = [&](int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); };
         const int first = (w.cta - c0) / kGroupCtas * kGroupCtas, members = min(kGroupCtas, n - first);
         const int groups = (n + kGroupCtas - 1) / kGroupCtas;
-        const int64_t row = static_cast<int64_t>(r.b) * a.kv.kv_heads * a.head_tiles + r.hk;
-        // level 0: the members of the group; level 1: the groups
+        // level 0: the members of the group; level 1: the groups, counted beside the first one's members
         for (int level = 0; level < 2; ++level) {
             const bool members_only = level == 0;
-            if (!last_of(sh, members_only ? a.arrived_group + slot(first) : a.arrived + row, members_only ? members : groups))
-                return;
+            if (!last_of(sh, a.arrived + slot(members_only ? first : 0), level, members_only ? members : groups)) return;
             const bool done = !members_only || groups == 1;
             if (done || members > 1) {
                 combine(a, sh, r, members_only ? members : groups,
@@ -891,6 +912,8 @@ struct Kernel {
     {
         pdl_trigger();
         pdl_wait();
+        uint64_t ticket = 0;
+        if (threadIdx.x == kTicketThread) ticket = draw_ticket(a);  // needed late
         empty_rows(a);
         const int hks = a.kv.kv_heads * a.head_tiles;
         // up to 32 sequences: one per lane, every warp for itself
@@ -967,7 +990,7 @@ struct Kernel {
             before += all;
         }
         __syncthreads();
-        stream(a, sh);
+        stream(a, sh, ticket);
     }
 };
 

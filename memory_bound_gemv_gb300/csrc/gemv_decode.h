@@ -50,8 +50,7 @@ struct AttnArgs {
     // workspace
     float *part;                // [2 * ctas][part_stride]: O in fragment order, then m and l per head
     int64_t part_stride;
-    unsigned int *arrived_group;  // [2 * kAttnMaxCtas], zero between calls
-    unsigned int *arrived;      // [batch * kv_heads * head_tiles], zero between calls
+    uint64_t *arrived;          // [2 * kAttnMaxCtas], by a part's slot; zero before the first call
     float *row_lse;             // same rows x 8 * NT heads: log2 of the softmax denominator
     float *logits;              // [rows][capacity][logit_heads], log2 units; weights only
     int logit_heads;
@@ -63,7 +62,7 @@ struct AttnArgs {
 cudaError_t launch_attn_f16(const AttnArgs &a, bool vec, int nt, bool big, int sm_count, cudaStream_t s);
 cudaError_t launch_attn_bf16(const AttnArgs &a, bool vec, int nt, bool big, int sm_count, cudaStream_t s);
 cudaError_t launch_attn_weights(const AttnArgs &a, int nt, cudaStream_t s);
-constexpr int kAttnMaxCtas = 1024;
+constexpr int kAttnMaxCtas = 512;
 
 struct EvictArgs {
     KvView kv;

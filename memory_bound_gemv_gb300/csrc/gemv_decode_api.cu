@@ -86,7 +86,7 @@ int head_tile(int dim, int group, bool vec) { return vec && group > 8 && dim <= 
 struct AttnPlan {
     int nt, head_tiles, logit_heads;
     int64_t part_stride, rows;
-    size_t part, arrived, row_lse, logits, total;  // offsets and size in bytes
+    size_t part, row_lse, logits, total;  // offsets and size in bytes
 };
 
 // The element-wise kernel takes single tiles: sized for the larger need.
@@ -100,10 +100,10 @@ AttnPlan attn_plan(const KvView &v, int group, int nt, bool weights)
     p.logit_heads = group >= heads ? heads : (group + 1) / 2 * 2;
     p.part_stride = static_cast<int64_t>(nt) * dc * 16 * 32 + 2 * heads;
     p.rows = static_cast<int64_t>(v.batch) * v.kv_heads * p.head_tiles;
-    // The counters stand ahead of all else, as many as the narrowest tiles need:
-    // calls whose q allows wide loads and calls whose q does not share a workspace.
-    p.arrived = 2 * kAttnMaxCtas * 4;
-    p.part = p.arrived + up(static_cast<size_t>(v.batch) * v.kv_heads * ((group + 7) / 8) * 4);
+    // The counters stand ahead of all else, whatever the tiles: calls whose q
+    // allows wide loads and calls whose q does not share a workspace.
+    static_assert(2 * kAttnMaxCtas * sizeof(uint64_t) == GEMV_ATTN_COUNTER_BYTES, "");
+    p.part = GEMV_ATTN_COUNTER_BYTES;
     p.row_lse = p.part + up(static_cast<size_t>(2) * kAttnMaxCtas * p.part_stride * 4);
     p.logits = p.row_lse + (weights ? up(static_cast<size_t>(p.rows) * heads * 4) : 0);
     p.total = p.logits + (weights ? up(static_cast<size_t>(p.rows) * v.capacity * p.logit_heads * 4) : 0);
@@ -180,8 +180,7 @@ gemv_status_t gemv_attn_paged(const gemv_kv_t *kv, const gemv_attn_t *args, void
     a.scale_log2 = args->scale * 1.4426950408889634f;
     a.err = dev.status;
     unsigned char *ws = static_cast<unsigned char *>(args->workspace);
-    a.arrived_group = reinterpret_cast<unsigned int *>(ws);
-    a.arrived = reinterpret_cast<unsigned int *>(ws + p.arrived);
+    a.arrived = reinterpret_cast<uint64_t *>(ws);
     a.part = reinterpret_cast<float *>(ws + p.part);
     a.part_stride = p.part_stride;
     a.row_lse = reinterpret_cast<float *>(ws + p.row_lse);

@@ -191,7 +191,7 @@ class PagedKV:
             n = self._lib.gemv_attn_paged_workspace(self._at, q_heads, 1 if weights else 0)
             with _on(stream):
                 t = torch.empty(max(n, 256), dtype=torch.uint8, device=self.device)
-                t[:_ATTN_COUNTER_BYTES + 4 * self.batch * q_heads].zero_()
+                t[:_ATTN_COUNTER_BYTES].zero_()
             got = self._workspaces[key] = (t.data_ptr(), t.numel(), t)
         return got
 
