@@ -340,7 +340,7 @@ struct Kernel {
         for (int b = blockIdx.x; b < a.kv.batch; b += gridDim.x) {
             const int len = __ldg(a.lengths + b);
             if ((len < 0 || len > a.kv.capacity) && threadIdx.x == 0) report_error(a.err, DEVERR_BAD_INDEX);
-            if (len > 0) continue;
+            if (len > 0 && a.kv.capacity > 0) continue;
             uint16_t *out = static_cast<uint16_t *>(a.out) + b * a.o_sb;
             for (int i = threadIdx.x; i < a.q_heads * a.kv.dim; i += kThreads) {
                 const int h = i / a.kv.dim;

@@ -1,0 +1,27 @@
+"""Arguments at and beyond the limits of the decode-step calls: refused, or right."""
+
+import math
+
+import pytest
+
+import memory_bound_gemv_gb300 as mbg
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():  # pragma: no cover - CPU container
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+from test_gpu_decode import F16, make_cache, normal  # noqa: E402
+
+
+def test_attn_of_a_cache_without_slots():
+    """Lengths beyond a capacity of 0 are reported, and the row is an empty one like any other."""
+    k = torch.zeros(1, 16, 1, 64, dtype=F16, device="cuda")
+    cache = mbg.PagedKV(k, k.clone(), torch.zeros(2, 0, dtype=torch.int32, device="cuda"))
+    q, lse = normal(2, (2, 4, 64), F16), torch.zeros(2, 4, device="cuda")
+    for lengths, status in (([0, 0], mbg.OK), ([0, 5], mbg.ERR_BAD_INDEX)):
+        out = torch.full_like(q, 7.0)
+        mbg.gemv_attn_paged(cache, q, torch.tensor(lengths, dtype=torch.int32, device="cuda"), out=out, lse=lse.zero_())
+        assert mbg.gemv_get_device_error() == status
+        assert (out == 0).all() and (lse == -math.inf).all()
