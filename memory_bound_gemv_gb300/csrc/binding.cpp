@@ -132,7 +132,7 @@ PyObject *attn(PyObject *, PyObject *const *a, Py_ssize_t n)
         const at::Tensor &q = tensor(a[2], index);
         if (q.dim() != 3) throw Other();
         const int64_t count = q.size(1);
-        if (count < 1 || count % kv->kv_heads || count > INT32_MAX) throw Other();
+        if (count < 1 || kv->kv_heads < 1 || count % kv->kv_heads || count > INT32_MAX) throw Other();
         const at::ScalarType type = type_of(kv->elem);
         g.q = heads(operand(a[2], index, type, {kv->batch, count, kv->head_dim}));
         g.lengths = dense<int32_t>(a[3], index, {kv->batch});

@@ -157,6 +157,8 @@ class PagedKV:
             raise ValueError("k must be a tensor [pages, page_size, kv_heads, head_dim]")
         if k.dtype not in (torch.float16, torch.bfloat16):
             raise TypeError(f"k has dtype {k.dtype}, expected float16 or bfloat16")
+        if min(k.shape[1:]) < 1:
+            raise ValueError(f"k has shape {tuple(k.shape)}: pages need slots, heads and elements")
         index = k.get_device()
         _operand(k, "k", k.dtype, k.shape, max(index, 0))
         _operand(v, "v", k.dtype, k.shape, index)

@@ -15,6 +15,13 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU container
 from test_gpu_decode import F16, make_cache, normal  # noqa: E402
 
 
+def test_caches_without_heads_slots_or_elements_are_refused():
+    table = torch.zeros(2, 3, dtype=torch.int32, device="cuda")
+    for shape in ((4, 16, 0, 64), (4, 0, 2, 64), (4, 16, 2, 0)):
+        with pytest.raises(ValueError):
+            mbg.PagedKV(torch.zeros(shape, dtype=F16, device="cuda"), torch.zeros(shape, dtype=F16, device="cuda"), table)
+
+
 def test_attn_of_a_cache_without_slots():
     """Lengths beyond a capacity of 0 are reported, and the row is an empty one like any other."""
     k = torch.zeros(1, 16, 1, 64, dtype=F16, device="cuda")
