@@ -126,6 +126,12 @@ def _dense(t, name, dtype, shape, index):
     return t.data_ptr()
 
 
+def _count(value, name, least):
+    """Refuses counts that the library's 32-bit arguments cannot hold (ctypes would cut them off)."""
+    if not least <= value < 2 ** 31:
+        raise ValueError(f"{name} must be at least {least} and below 2^31")
+
+
 def _on(stream):
     """Context in which tensors belong to the stream that a call runs on."""
     if isinstance(stream, int):
@@ -271,8 +277,7 @@ def gemv_attn_paged(cache: PagedKV, q, lengths, out=None, scale: Optional[float]
     if heads < 1 or heads % cache.kv_heads:
         raise ValueError(f"q has {heads} heads, expected a multiple of {cache.kv_heads}")
     n_ptr = _dense(lengths, "lengths", torch.int32, (cache.batch,), index)
-    if window < 0:
-        raise ValueError("window must not be negative")
+    _count(window, "window", 0)
     if out is None:
         with _on(stream):
             out = torch.empty(shape, dtype=cache.dtype, device=cache.device)
@@ -379,8 +384,9 @@ def gemv_kv_evict_plan(cache: PagedKV, lengths, keep: int, sinks: int = 0, recen
         return moves, counts
     if cache.scores is None or cache.stamps is None:
         raise ValueError("eviction needs a cache with scores and stamps")
-    if keep < 1 or sinks < 0 or recent < 0:
-        raise ValueError("keep must be at least 1, sinks and recent not negative")
+    _count(keep, "keep", 1)
+    _count(sinks, "sinks", 0)
+    _count(recent, "recent", 0)
     n_ptr = _dense(lengths, "lengths", torch.int32, (cache.batch,), cache.index)
     most = max(1, min(keep, cache.capacity - keep))
     if moves is None or counts is None:
@@ -407,8 +413,7 @@ def gemv_kv_evict_apply(cache: PagedKV, moves, counts, lengths, keep: int, strea
     if _quick.apply(cache._at, cache.index, moves, counts, lengths, keep,
                     stream if stream is None else _mbg._stream_ptr(stream)) == 0:
         return
-    if keep < 1:
-        raise ValueError("keep must be at least 1")
+    _count(keep, "keep", 1)
     m_ptr, room, c_ptr = _moves(cache, moves, counts)
     n_ptr = None if lengths is None else _dense(lengths, "lengths", torch.int32, (cache.batch,), cache.index)
     st = cache._lib.gemv_kv_evict_apply(cache._at, m_ptr, room, c_ptr, n_ptr, keep, _mbg._stream_ptr(stream))

@@ -22,6 +22,23 @@ def test_caches_without_heads_slots_or_elements_are_refused():
             mbg.PagedKV(torch.zeros(shape, dtype=F16, device="cuda"), torch.zeros(shape, dtype=F16, device="cuda"), table)
 
 
+@pytest.mark.parametrize("many", [2 ** 31, 2 ** 32 + 5, 2 ** 40])
+def test_counts_beyond_32_bits_are_refused(many):
+    cache = make_cache(131, [40, 40], 2, 8, 16, F16, history=True)
+    n = torch.tensor([40, 40], dtype=torch.int32, device="cuda")
+    moves = torch.empty(2, 2, 64, 2, dtype=torch.int32, device="cuda")
+    counts = torch.zeros(2, 2, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        mbg.gemv_kv_evict_apply(cache, moves, counts, n, many)  # lengths would become 5
+    for bad in (dict(keep=many), dict(keep=8, sinks=many), dict(keep=8, recent=many)):
+        for room in (dict(), dict(moves=moves, counts=counts)):
+            with pytest.raises(ValueError):
+                mbg.gemv_kv_evict_plan(cache, n, **bad, **room)
+    with pytest.raises(ValueError):
+        mbg.gemv_attn_paged(cache, normal(1, (2, 4, 8), F16), n, window=many)
+    assert n.tolist() == [40, 40]
+
+
 def test_attn_of_a_cache_without_slots():
     """Lengths beyond a capacity of 0 are reported, and the row is an empty one like any other."""
     k = torch.zeros(1, 16, 1, 64, dtype=F16, device="cuda")
