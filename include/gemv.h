@@ -414,7 +414,7 @@ typedef struct {
  *   s_t = scale * q . k_t,  p = softmax(s),  out = sum_t p_t v_t
  * over the slots t in [max(0, n - window), n), n = lengths[b] (window 0: all).
  * q and out: [batch][q_heads][head_dim] of the cache's type, strides (sequence,
- * head) given; q_heads a multiple of kv_heads, query heads h * g .. h * g + g - 1
+ * head) given; q_heads a multiple of kv_heads (q_heads * head_dim below 2^31), query heads h * g .. h * g + g - 1
  * read cached head h (g = q_heads / kv_heads).  A sequence of length 0, or
  * whose scores are all -inf, gives zeros.  lse: NULL, or FP32 [batch][q_heads]
  * log(sum exp(s)) (-inf for such a row).
@@ -487,7 +487,8 @@ gemv_status_t gemv_kv_evict_apply(const gemv_kv_t *kv, const int32_t *moves, int
  * slot slots[token] of sequence seq[token] (seq NULL: the token's number); a
  * negative slot is padding (q_out is written, the cache is not).  Where kv has
  * scores and stamps the slot's become 0 and stamps[token] (stamps NULL: the
- * slot).  No two tokens of a call may share a slot.  axis: uint8 [rot / 2],
+ * slot).  No two tokens of a call may share a slot; a call takes up to 2^31 -
+ * 2^20 of them.  axis: uint8 [rot / 2],
  * values below axes; rot even, at most head_dim.
  */
 typedef struct {

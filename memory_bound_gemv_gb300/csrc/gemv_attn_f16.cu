@@ -26,7 +26,8 @@ __global__ void __launch_bounds__(256) mbg_attn_weights_kernel(const __grid_cons
     const attn::RowSpan span = attn::row_span<16>(a, b);
     const int64_t out_row = (static_cast<int64_t>(b) * a.kv.kv_heads + h) * a.kv.capacity;
     const int step = gridDim.x * 256 * kTokens;
-    for (int s0 = span.first + blockIdx.x * 256 * kTokens + threadIdx.x; s0 < span.len; s0 += step) {
+    // (a step behind the last slot may lie beyond 2^31)
+    for (int64_t s0 = span.first + blockIdx.x * 256 * kTokens + threadIdx.x; s0 < span.len; s0 += step) {
         float sum[kTokens], old[kTokens];
 #pragma unroll
         for (int k = 0; k < kTokens; ++k) {

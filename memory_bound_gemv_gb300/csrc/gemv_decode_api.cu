@@ -79,6 +79,12 @@ bool cache_vec(const gemv_kv_t *kv)
            mult8(kv->v_stride, 3);
 }
 
+// Heads that the kernels' 32-bit counts of heads and of their elements can hold.
+bool too_many_heads(int heads, int dim)
+{
+    return heads > 1 << 24 || static_cast<int64_t>(heads) * dim > INT_MAX;
+}
+
 // Query heads per tile: two MMA tiles of eight where a cached head has more
 // than eight and the accumulators of both fit in registers.
 int head_tile(int dim, int group, bool vec) { return vec && group > 8 && dim <= 128 ? 2 : 1; }
@@ -120,7 +126,8 @@ extern "C" {
 size_t gemv_attn_paged_workspace(const gemv_kv_t *kv, int q_heads, int weights)
 {
     KvView v;
-    if (view_of(kv, &v, false) != GEMV_OK || q_heads < 1 || q_heads % v.kv_heads) return 0;
+    if (view_of(kv, &v, false) != GEMV_OK || q_heads < 1 || q_heads % v.kv_heads || too_many_heads(q_heads, v.dim))
+        return 0;
     const int group = q_heads / v.kv_heads;
     const AttnPlan a = attn_plan(v, group, 1, weights != 0);
     if (v.dim > 128 || group <= 8) return a.total;
@@ -149,6 +156,7 @@ gemv_status_t gemv_attn_paged(const gemv_kv_t *kv, const gemv_attn_t *args, void
     const int q_heads = args->q_heads;
     if (q_heads < 1 || q_heads % a.kv.kv_heads || args->window < 0 || negative(q) || negative(out))
         return GEMV_ERR_INVALID_VALUE;
+    if (too_many_heads(q_heads, a.kv.dim)) return GEMV_ERR_UNSUPPORTED;
     if (a.kv.batch == 0) return GEMV_OK;
     if (!q.data || !args->lengths || !out.data || !args->workspace || (args->scores_out && !kv->scores))
         return GEMV_ERR_INVALID_VALUE;
@@ -263,6 +271,8 @@ gemv_status_t gemv_rope_append(const gemv_kv_t *kv, const gemv_rope_t *r, void *
         return GEMV_ERR_INVALID_VALUE;
     if (negative(r->q) || negative(r->k) || negative(r->v) || negative(r->q_out)) return GEMV_ERR_INVALID_VALUE;
     if (!r->seq && r->tokens > a.kv.batch) return GEMV_ERR_INVALID_VALUE;
+    // a block looks up to 64 steps of the grid ahead, in 32 bits
+    if (r->tokens > INT_MAX - (1 << 20) || too_many_heads(r->q_heads, a.kv.dim)) return GEMV_ERR_UNSUPPORTED;
     if (r->tokens == 0) return GEMV_OK;
     if ((r->q_heads > 0 && (!r->q.data || !r->q_out.data)) || !r->k.data || !r->v.data || !r->positions || !r->slots ||
         (r->rot > 0 && (!r->turns || !r->axis)) || !kv->k || !kv->v)

@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(kApplyThreads, 4) mbg_evict_apply_kernel(const
     const int64_t ps = is_v ? kv.vs_page : kv.ks_page, ts = is_v ? kv.vs_tok : kv.ks_tok,
                   hs = is_v ? kv.vs_head : kv.ks_head;
     uint16_t *pool = static_cast<uint16_t *>(is_v ? kv.v : kv.k) + h * hs;
-    for (int i0 = (blockIdx.x * (kApplyThreads / 32) + warp) * kApplyLook; i0 < count; i0 += stride) {
+    for (int64_t i0 = (blockIdx.x * (kApplyThreads / 32) + warp) * kApplyLook; i0 < count; i0 += stride) {
         // lanes 0..7: a move each
         int sp = -1, tp = -1, so = 0, to = 0;
         if (lane < kApplyLook && i0 + lane < count) {

@@ -49,3 +49,20 @@ def test_attn_of_a_cache_without_slots():
         mbg.gemv_attn_paged(cache, q, torch.tensor(lengths, dtype=torch.int32, device="cuda"), out=out, lse=lse.zero_())
         assert mbg.gemv_get_device_error() == status
         assert (out == 0).all() and (lse == -math.inf).all()
+
+
+def test_attn_weights_of_a_row_that_ends_close_to_2_to_the_31():
+    """One page stands for all: 2^31 slots of equal keys, weights of 1 / n each."""
+    page, pages = 65536, 32767
+    n = page * pages
+    k, v = torch.zeros(1, page, 1, 8, dtype=F16, device="cuda"), torch.ones(1, page, 1, 8, dtype=F16, device="cuda")
+    table = torch.zeros(1, pages, dtype=torch.int32, device="cuda")
+    cache = mbg.PagedKV(k, v, table, scores=torch.zeros(1, 1, n, device="cuda"))
+    q, lse = torch.ones(1, 1, 8, dtype=F16, device="cuda"), torch.zeros(1, 1, device="cuda")
+    out = mbg.gemv_attn_paged(cache, q, torch.tensor([n - 3], dtype=torch.int32, device="cuda"), lse=lse, accumulate=True)
+    # sums of some hundred parts in FP32
+    assert (out == 1).all() and abs(float(lse) - math.log(n - 3)) < 2.0 ** -14
+    got = cache.scores[0, 0]
+    low, high = float(got[:n - 3].min()), float(got[:n - 3].max())
+    assert (got[n - 3:] == 0).all()
+    assert abs(low * (n - 3) - 1) < 2.0 ** -14 and abs(high * (n - 3) - 1) < 2.0 ** -14
