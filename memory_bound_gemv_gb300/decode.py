@@ -17,6 +17,8 @@ from __future__ import annotations
 import ctypes
 import math
 import struct
+import threading
+import weakref
 from typing import Optional, Sequence
 
 import memory_bound_gemv_gb300 as _mbg
@@ -139,6 +141,21 @@ def _on(stream):
     return torch.cuda.stream(stream)  # None: no change
 
 
+class _Workspace:
+    """Scratch memory of ``gemv_attn_paged`` calls that follow each other: (address, bytes, tensor)."""
+
+    def __init__(self, tensor):
+        self._values = tensor.data_ptr(), tensor.numel(), tensor
+
+    def __getitem__(self, i):
+        return self._values[i]
+
+
+# Workspaces that some handle holds, by device, stream, capture and size.
+_shared = weakref.WeakValueDictionary()
+_shared_lock = threading.Lock()
+
+
 class PagedKV:
     """A paged key-value cache, described once.
 
@@ -150,11 +167,11 @@ class PagedKV:
     [batch, kv_heads, max_pages * page_size]: the attention weight each slot
     has gathered and the number of its token, for eviction.
 
-    The tensors are kept; their contents may change, their storage not.  The
-    handle keeps a workspace per stream for ``gemv_attn_paged``: calls on one
-    stream use it in turn, calls on different streams have one each, and so has
-    each CUDA graph that calls are captured into (for as long as the handle
-    lives).
+    The tensors are kept; their contents may change, their storage not.  For
+    ``gemv_attn_paged`` there is a workspace per stream, and one per stream of
+    each CUDA graph that calls are captured into.  Handles that need as much
+    (a model's layers) share them, as calls on one stream follow each other.  A
+    handle keeps what it has used until it is gone or ``release_workspaces`` is called.
     """
 
     def __init__(self, k, v, page_table, scores=None, stamps=None):
@@ -196,12 +213,24 @@ class PagedKV:
         key = (ptr, capture, q_heads, weights)
         got = self._workspaces.get(key)
         if got is None:
-            n = self._lib.gemv_attn_paged_workspace(self._at, q_heads, 1 if weights else 0)
-            with _on(stream):
-                t = torch.empty(max(n, 256), dtype=torch.uint8, device=self.device)
-                t[:_ATTN_COUNTER_BYTES].zero_()
-            got = self._workspaces[key] = (t.data_ptr(), t.numel(), t)
+            n = max(self._lib.gemv_attn_paged_workspace(self._at, q_heads, 1 if weights else 0), _ATTN_COUNTER_BYTES)
+            shared = (self.index, ptr, capture, n)
+            with _shared_lock:
+                got = _shared.get(shared)
+                if got is None:
+                    with _on(stream):
+                        t = torch.empty(n, dtype=torch.uint8, device=self.device)
+                        t[:_ATTN_COUNTER_BYTES].zero_()
+                    got = _shared[shared] = _Workspace(t)
+            self._workspaces[key] = got
         return got
+
+    def release_workspaces(self):
+        """Lets go of the workspaces that ``gemv_attn_paged`` has made: for handles that outlive CUDA graphs.
+
+        A graph that calls with this handle were captured into must not be
+        replayed afterwards.  Later calls make new ones."""
+        self._workspaces.clear()
 
 
 class RopeTable:

@@ -41,3 +41,64 @@ def test_attn_after_a_call_whose_lengths_changed(lengths):
         out = mbg.gemv_attn_paged(cache, q, n, out=torch.full_like(q, 7.0))
         assert torch.equal(out, good[step]), step
     assert mbg.gemv_get_device_error() == mbg.OK
+
+
+def test_attn_handles_of_one_size_share_a_workspace():
+    """A model's layers on one stream: one workspace, not one each, and every layer its own answer."""
+    lengths = [3000, 17, 900]
+    layers = [make(lengths, heads=2, seed=s, history=True, capacity=20000) for s in range(4)]
+    alone = []
+    for cache, n in layers:
+        alone.append(mbg.gemv_attn_paged(cache, query(cache, 8, 5), n, accumulate=True,
+                                         scores_out=torch.zeros_like(cache.scores)).clone())
+        cache.release_workspaces()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    outs = [mbg.gemv_attn_paged(cache, query(cache, 8, 5), n, accumulate=True) for cache, n in layers]
+    held = torch.cuda.memory_allocated() - before
+    need = max(w[1] for w in layers[0][0]._workspaces.values())
+    assert need <= held < 2 * need  # (the outputs are small beside it)
+    assert len({w[0] for cache, _ in layers for w in cache._workspaces.values()}) == 1
+    assert all(torch.equal(a, b) for a, b in zip(outs, alone))
+    del outs
+    for cache, _ in layers:
+        cache.release_workspaces()
+    assert torch.cuda.memory_allocated() <= before
+    small, n = make([50], heads=2)
+    assert small._workspace(8, False, mbg._stream_ptr(None), None)[1] < need
+    other = torch.cuda.Stream()
+    first = layers[0][0]
+    ptr = mbg._stream_ptr(None)
+    assert first._workspace(8, True, ptr, None)[0] != first._workspace(8, True, mbg._stream_ptr(other), other)[0]
+
+
+def test_attn_graphs_of_several_layers_and_their_release():
+    """Layers captured into one graph share its workspace; graphs that are gone leave nothing behind."""
+    lengths = [5000, 40]
+    layers = [make(lengths, heads=2, seed=s, history=True) for s in range(3)]
+    queries = [query(layers[0][0], 8, s) for s in range(3)]
+    want = [mbg.gemv_attn_paged(cache, q, n).clone() for (cache, n), q in zip(layers, queries)]
+    outs = [torch.empty_like(q) for q in queries]
+
+    def captured():
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for (cache, n), q, out in zip(layers, queries, outs):
+                mbg.gemv_attn_paged(cache, q, n, out=out)
+        return graph
+
+    sizes = []
+    for _ in range(4):
+        for cache, _ in layers:
+            cache.release_workspaces()
+        graph = captured()
+        assert len({w[0] for cache, _ in layers for w in cache._workspaces.values()}) == 1
+        for out in outs:
+            out.fill_(7.0)
+        for _ in range(3):
+            graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+        torch.cuda.synchronize()
+        sizes.append(torch.cuda.memory_allocated())
+        del graph
+    assert sizes[1:] == sizes[:-1]
