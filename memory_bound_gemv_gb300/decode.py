@@ -142,10 +142,13 @@ def _on(stream):
 
 
 class _Workspace:
-    """Scratch memory of ``gemv_attn_paged`` calls that follow each other: (address, bytes, tensor)."""
+    """Scratch memory of ``gemv_attn_paged`` calls that follow each other: (address, bytes, tensor).
+
+    A call with weights is two launches: ``lock`` keeps those of another thread from coming between them."""
 
     def __init__(self, tensor):
         self._values = tensor.data_ptr(), tensor.numel(), tensor
+        self.lock = threading.Lock()
 
     def __getitem__(self, i):
         return self._values[i]
@@ -326,9 +329,10 @@ def gemv_attn_paged(cache: PagedKV, q, lengths, out=None, scale: Optional[float]
         raise ValueError("scores_out goes with accumulate=True")
     ptr = _mbg._stream_ptr(stream)
     ws = cache._workspace(heads, accumulate, ptr, stream)
-    st = cache._lib.gemv_attn_paged(
-        cache._at, _ATTN.pack(q.data_ptr(), qs[0], qs[1], out.data_ptr(), os[0], os[1], n_ptr, l_ptr, s_ptr, ws[0],
-                              ws[1], heads, window, scale), ptr)
+    args = _ATTN.pack(q.data_ptr(), qs[0], qs[1], out.data_ptr(), os[0], os[1], n_ptr, l_ptr, s_ptr, ws[0], ws[1],
+                      heads, window, scale)
+    with ws.lock:
+        st = cache._lib.gemv_attn_paged(cache._at, args, ptr)
     if st:
         _mbg._raise(st, "gemv_attn_paged")
     return out

@@ -1,5 +1,8 @@
 """The attention's workspace: what calls that misuse it leave, who shares it."""
 
+import threading
+import time
+
 import pytest
 
 import memory_bound_gemv_gb300 as mbg
@@ -102,3 +105,94 @@ def test_attn_graphs_of_several_layers_and_their_release():
         sizes.append(torch.cuda.memory_allocated())
         del graph
     assert sizes[1:] == sizes[:-1]
+
+
+@pytest.mark.parametrize("form", ["compiled checks", "Python checks"])
+def test_attn_with_weights_from_several_threads(form, monkeypatch):
+    """Threads on one stream: the attention of one call and its weights are not parted by another call's."""
+    if form == "Python checks":
+        decode._need_torch()
+
+        class Absent:
+            def __getattr__(self, name):
+                return lambda *args: -1
+
+        monkeypatch.setattr(decode, "_quick", Absent())
+    cache, n = make([200, 100, 31, 77], heads=2, history=True)
+    queries = [query(cache, 8, s) for s in range(4)]
+
+    def call(i, out, sums):
+        mbg.gemv_attn_paged(cache, queries[i], n, out=out, accumulate=True, scores_out=sums)
+
+    want = []
+    for i in range(4):
+        want.append((torch.empty_like(queries[i]), torch.zeros_like(cache.scores)))
+        call(i, *want[i])
+    torch.cuda.synchronize()
+    calls = 3000
+    got = [[(torch.empty_like(queries[i]), torch.zeros_like(cache.scores)) for _ in range(calls)] for i in range(4)]
+    go = threading.Barrier(4)
+
+    def work(i):
+        go.wait()
+        for out, sums in got[i]:
+            call(i, out, sums)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    wrong = sum(not (torch.equal(out, want[i][0]) and torch.equal(sums, want[i][1])) for i in range(4) for out, sums in got[i])
+    assert wrong == 0
+
+
+def test_attn_with_weights_is_one_call_at_a_time_per_workspace(monkeypatch):
+    """What lets another thread's launches between a call's two: no two calls overlap on one workspace."""
+    cache, n = make([20, 31], heads=2, history=True)
+    other = mbg.PagedKV(cache.k, cache.v, cache.page_table, scores=torch.zeros_like(cache.scores))  # shares the workspace
+    q = query(cache, 8, 1)
+    for c in (cache, other):
+        mbg.gemv_attn_paged(c, q, n, accumulate=True)
+    state, guard = dict(inside=0, most=0, calls=0), threading.Lock()
+
+    class Watched:
+        """A library, or compiled checks, whose attention takes its time without holding the interpreter."""
+
+        def __init__(self, real, name):
+            self._real, self._name = real, name
+
+        def __getattr__(self, name):
+            f = getattr(self._real, name)
+            if name != self._name:
+                return f
+
+            def watched(*args):
+                with guard:
+                    state["inside"] += 1
+                    state["most"] = max(state["most"], state["inside"])
+                    state["calls"] += 1
+                time.sleep(0.002)
+                result = f(*args)
+                with guard:
+                    state["inside"] -= 1
+                return result
+
+            return watched
+
+    for c in (cache, other):
+        c._lib = Watched(c._lib, "gemv_attn_paged")
+    monkeypatch.setattr(decode, "_quick", Watched(decode._quick, "attn"))
+
+    def work(i):
+        for _ in range(10):
+            mbg.gemv_attn_paged((cache, other)[i % 2], q, n, accumulate=True)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert state["calls"] == 40 and state["most"] == 1
