@@ -298,12 +298,23 @@ def gemv_attn_paged(cache: PagedKV, q, lengths, out=None, scale: Optional[float]
     if not isinstance(q, _Tensor) or q.dim() != 3:
         raise ValueError("q must be a tensor [batch, q_heads, head_dim]")
     heads = q.shape[1]
-    if out is not None and not accumulate and scores_out is None and heads:
+    s_ptr = 0
+    if accumulate and cache.scores is not None:
+        if scores_out is None:
+            s_ptr = cache.scores.data_ptr()
+        else:
+            s_ptr = _dense(scores_out, "scores_out", torch.float32, cache.scores.shape, index)
+    if heads and (s_ptr if accumulate else scores_out is None):
         ptr = _mbg._stream_ptr(stream)
-        ws = cache._workspace(heads, False, ptr, stream)
-        st = _quick.attn(cache._at, index, q, lengths, out, lse, 0, ws[0], ws[1], scale, window, ptr)
+        ws = cache._workspace(heads, accumulate, ptr, stream)
+        result = out
+        if result is None:
+            with _on(stream):
+                result = torch.empty(q.shape, dtype=cache.dtype, device=cache.device)
+        with ws.lock:
+            st = _quick.attn(cache._at, index, q, lengths, result, lse, s_ptr, ws[0], ws[1], scale, window, ptr)
         if st == 0:
-            return out
+            return result
     shape = (cache.batch, heads, cache.head_dim)
     qs = _operand(q, "q", cache.dtype, shape, index)
     if heads < 1 or heads % cache.kv_heads:
@@ -317,15 +328,9 @@ def gemv_attn_paged(cache: PagedKV, q, lengths, out=None, scale: Optional[float]
     else:
         os = _operand(out, "out", cache.dtype, shape, index)
     l_ptr = 0 if lse is None else _dense(lse, "lse", torch.float32, (cache.batch, heads), index)
-    s_ptr = 0
-    if accumulate:
-        if cache.scores is None:
-            raise ValueError("accumulate needs a cache with scores")
-        if scores_out is None:
-            s_ptr = cache.scores.data_ptr()
-        else:
-            s_ptr = _dense(scores_out, "scores_out", torch.float32, cache.scores.shape, index)
-    elif scores_out is not None:
+    if accumulate and cache.scores is None:
+        raise ValueError("accumulate needs a cache with scores")
+    if scores_out is not None and not accumulate:
         raise ValueError("scores_out goes with accumulate=True")
     ptr = _mbg._stream_ptr(stream)
     ws = cache._workspace(heads, accumulate, ptr, stream)

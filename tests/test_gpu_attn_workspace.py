@@ -196,3 +196,27 @@ def test_attn_with_weights_is_one_call_at_a_time_per_workspace(monkeypatch):
         t.join()
     torch.cuda.synchronize()
     assert state["calls"] == 40 and state["most"] == 1
+
+
+def test_attn_calls_with_weights_or_a_new_output_take_the_compiled_checks(monkeypatch):
+    cache, n = make([40, 31], heads=2, history=True)
+    q, sums = query(cache, 8, 1), torch.zeros_like(cache.scores)
+    want = mbg.gemv_attn_paged(cache, q, n, out=torch.empty_like(q))
+
+    def refused(*args):
+        raise AssertionError("not through the Python form")
+
+    monkeypatch.setattr(decode, "_operand", refused)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    assert torch.equal(mbg.gemv_attn_paged(cache, q, n), want)
+    assert torch.equal(mbg.gemv_attn_paged(cache, q, n, accumulate=True), want)
+    assert torch.equal(mbg.gemv_attn_paged(cache, q, n, out=torch.empty_like(q), accumulate=True), want)
+    streamed = mbg.gemv_attn_paged(cache, q, n, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(streamed, want)
+    monkeypatch.undo()
+    assert torch.equal(mbg.gemv_attn_paged(cache, q, n, accumulate=True, scores_out=sums), want)
+    # two calls have added to the scores, and the third adds to a copy
+    close = (sums - 1.5 * cache.scores).abs() <= 2.0 ** -21 * sums
+    assert close.all() and (cache.scores[0, :, :40] > 0).all()
