@@ -7,7 +7,9 @@ output (registers, spills, shared memory per kernel) is kept in
 ``_build/ptxas.log``.  Rebuilds only when a source or header is newer than
 the library.  Beside it the host compiler makes ``_build/_mbgbinding.so`` from
 ``csrc/binding.cpp``, for the installed torch: the quick form of the
-decode-step calls' argument checks.
+decode-step calls' argument checks.  The library needs neither torch nor the
+host compiler for it: where the quick form cannot be built, a warning says so and
+the checks run in Python.
 """
 
 from __future__ import annotations
@@ -15,6 +17,7 @@ from __future__ import annotations
 import concurrent.futures
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -45,17 +48,46 @@ def _sources():
 
 
 def _deps():
-    return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh"))
-            + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cpp"))
-            + glob.glob(os.path.join(INCLUDE, "*.h"))
-            + [os.path.abspath(__file__)])
+    return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+            + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
+
+
+def _newer(made, deps) -> bool:
+    return os.path.exists(made) and all(os.path.getmtime(p) <= os.path.getmtime(made) for p in deps)
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    """Whether the library needs no build (``binding_up_to_date`` for the quick form of the checks)."""
+    return _newer(LIB, _deps())
+
+
+def _torch_version():
+    """Version of the installed torch, which is not imported for it; None where there is none."""
+    import importlib.util
+
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return None
+    try:
+        with open(os.path.join(os.path.dirname(spec.origin), "version.py")) as f:
+            found = re.search(r"^__version__\s*=\s*['\"]([^'\"]+)", f.read(), re.M)
+    except OSError:
+        return None
+    return found.group(1) if found else None
+
+
+def binding_up_to_date() -> bool:
+    """Whether the quick form is there, made for the installed torch, or none can be."""
+    version = _torch_version()
+    if version is None:
+        return True
+    try:
+        with open(BINDING + ".torch") as f:
+            made_for = f.read()
+    except OSError:
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    deps = [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "gemv.h"), os.path.abspath(__file__)]
+    return made_for == version and _newer(BINDING, deps)
 
 
 def _build_binding():
@@ -66,23 +98,47 @@ def _build_binding():
 
     top = os.path.join(os.path.dirname(torch.__file__))
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = f"{BINDING}.{os.getpid()}.tmp"
     includes = [os.path.join(top, "include"), os.path.join(top, "include", "torch", "csrc", "api", "include"),
                 sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
     cmd = [os.environ.get("CXX") or shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
            f'-DMBG_TORCH_VERSION="{torch.__version__}"', f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *[f"-I{p}" for p in includes], os.path.join(CSRC, "binding.cpp"), "-L" + os.path.join(top, "lib"),
-           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-o", f"{BINDING}.{os.getpid()}.tmp"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("compiling binding.cpp failed")
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-o", tmp]
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError("compiling binding.cpp failed")
+        os.replace(tmp, BINDING)
+    finally:
+        if os.path.exists(tmp):
+            os.remove(tmp)
+    with open(BINDING + ".torch", "w") as f:
+        f.write(torch.__version__)
+
+
+def _try_binding():
+    """Builds the quick form; what stands in its way is told, and stands in the library's way no more."""
+    try:
+        _build_binding()
+    except Exception as e:  # noqa: BLE001 - a broken torch, no compiler, no headers ...
+        sys.stderr.write(f"memory_bound_gemv_gb300: without the compiled argument checks ({e}); they run in Python\n")
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link the library if needed; returns its path."""
-    if not force and up_to_date():
-        return LIB
+    """Compile and link what is needed; returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
+    with concurrent.futures.ThreadPoolExecutor(max_workers=1) as ex:
+        binding = ex.submit(_try_binding) if force or not binding_up_to_date() else None
+        if force or not up_to_date():
+            _build_library(verbose)
+        if binding:
+            binding.result()
+    return LIB
+
+
+def _build_library(verbose):
     nvcc = _nvcc()
     srcs = _sources()
 
@@ -92,11 +148,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, r
 
-    workers = min(len(srcs) + 1, os.cpu_count() or 4)
+    workers = min(len(srcs), os.cpu_count() or 4)
     with concurrent.futures.ThreadPoolExecutor(max_workers=workers) as ex:
-        binding = ex.submit(_build_binding)
         results = list(ex.map(compile_one, srcs))
-        binding.result()
     log = []
     for src, obj, r in results:
         log.append(f"== {os.path.basename(src)}\n{r.stdout}{r.stderr}")
@@ -105,7 +159,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}")
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         f.write("\n".join(log))
-    os.replace(f"{BINDING}.{os.getpid()}.tmp", BINDING)
     tmp = f"{LIB}.{os.getpid()}.tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *[o for _, o, _ in results]]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -115,7 +168,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.replace(tmp, LIB)
     if verbose:
         print(f"built {LIB}")
-    return LIB
 
 
 if __name__ == "__main__":

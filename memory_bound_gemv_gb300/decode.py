@@ -18,6 +18,7 @@ import ctypes
 import math
 import struct
 import threading
+import warnings
 import weakref
 from typing import Optional, Sequence
 
@@ -42,21 +43,34 @@ def _need_torch():
         torch, _Tensor = module, module.Tensor
 
 
+class _NoBinding:
+    """Stands in for the compiled form: every call is left to the Python form."""
+
+    def __getattr__(self, name):
+        return lambda *args: -1
+
+
 def _load_binding(module):
     """The compiled form of the calls below for the installed torch; it answers -1 where a call is not of the
-    common kind, and the Python form then checks it and says why."""
+    common kind, and the Python form then checks it and says why.  One that is missing or was made for another
+    torch is built anew; where that cannot be, the Python form takes all calls, with a warning."""
     import importlib.machinery
     import importlib.util
 
     from . import build
 
     lib = _mbg.lib()
-    loader = importlib.machinery.ExtensionFileLoader("_mbgbinding", build.BINDING)
-    binding = importlib.util.module_from_spec(importlib.util.spec_from_loader("_mbgbinding", loader))
-    loader.exec_module(binding)
-    if binding.torch_version != module.__version__:
-        raise RuntimeError(f"the binding was built for torch {binding.torch_version}, this is {module.__version__}: "
-                           "run memory_bound_gemv_gb300.build")
+    try:
+        if not build.binding_up_to_date():
+            build.build()
+        loader = importlib.machinery.ExtensionFileLoader("_mbgbinding", build.BINDING)
+        binding = importlib.util.module_from_spec(importlib.util.spec_from_loader("_mbgbinding", loader))
+        loader.exec_module(binding)
+        if binding.torch_version != module.__version__:
+            raise ImportError(f"made for torch {binding.torch_version}, this is {module.__version__}")
+    except (ImportError, OSError, RuntimeError) as e:
+        warnings.warn(f"decode-step calls check their arguments in Python, a few microseconds slower each: {e}")
+        return _NoBinding()
     binding.use(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
         "gemv_attn_paged", "gemv_rope_append", "gemv_kv_evict_plan", "gemv_kv_evict_apply", "gemv_norm_residual")))
     return binding
