@@ -1,4 +1,4 @@
-"""A decode step of a small transformer on this library's kernels alone.
+"""A decode step of a small transformer on this library's kernels (the MLP's activation and the counters are torch's).
 
 Per layer: the QKV product (INT4 GEMV), rotary positions with three axes and
 the append to the paged cache, attention of the new token with its weights

@@ -376,7 +376,9 @@ gemv_status_t gemv_q8_rowscale_run_variant(int variant, const int8_t *A, const u
  *
  * Conventions as above, and: data is FP32, binary16 or bfloat16 as named by a
  * gemv_elem_t; strides are in elements, the last dimension is contiguous;
- * all arithmetic is FP32.  Lengths, slots and page numbers live on the device
+ * all arithmetic is FP32 (but for the attention's weights next to the values:
+ * 24 bits in parts for bfloat16, 21 or more for binary16, down to 2^-39 of the
+ * largest).  Lengths, slots and page numbers live on the device
  * and are checked there: one out of range is skipped and reported as
  * GEMV_ERR_BAD_INDEX by gemv_get_device_error, nothing is read or written
  * outside the given buffers.  Rows of a multiple of eight elements, aligned

@@ -155,7 +155,7 @@ __device__ __forceinline__ float exp2_from(float x, float m)
 
 // 16 bytes of a cached row, read once.  (Asking L2 for the whole 256 bytes
 // around them brings other heads' rows along when a row is shorter: 16 x 32768
-// tokens of four heads of 64 take 118 us then, 96 us without, and rows of 256
+// tokens of four heads of 64 take 115 us then, 92 us without, and rows of 256
 // bytes gain nothing from it.)
 __device__ __forceinline__ uint4 ld_row16(const void *p)
 {
@@ -255,12 +255,12 @@ struct Kernel {
     // starting a row costs about that many tiles.  CTA c's share ends where CTA
     // c + 1's begins, at total * c / ctas -- or at an end of the row there, if
     // that is at most kNear tiles away (one round of the warps: 160 rows of 2000
-    // tokens of 128 36.0 us, two rounds 37.2; 128 of 500 16.2 and 17.6).  A cut
+    // tokens of 128 35.8 us, two rounds 36.7; 128 of 500 17.2 and 18.4).  A cut
     // costs as much as some kUncut tiles: rows of no more have none (384 rows of
-    // 256 tokens: 15.5 us, cut 23.4), nor has any row where the CTA with most to
+    // 256 tokens: 16.0 us, cut 23.9), nor has any row where the CTA with most to
     // do would then have no more than that above the mean (384 rows of 400 tokens
-    // 20.3 us, cut 27.2; of 1000 38.8 and 42.1; but 512 of 1000 64.9 and 52.0,
-    // 800 ragged ones of up to 800 45.9 and 39.0).
+    // 20.7 us, cut 27.7; of 1000 39.8 and 43.4; but 512 of 1000 66.7 and 53.8,
+    // 800 ragged ones of up to 800 46.3 and 40.1).
     static constexpr int kNear = kWarps, kUncut = 16;
     struct Share {
         int64_t total, x0, x1;

@@ -195,12 +195,12 @@ gemv_status_t gemv_attn_paged(const gemv_kv_t *kv, const gemv_attn_t *args, void
     a.logits = reinterpret_cast<float *>(ws + p.logits);
     a.logit_heads = p.logit_heads;
     // Few rows: one block of all an SM's warps, a third of the parts to join
-    // (8 rows of 131001 tokens of 128: 87.8 us, with blocks of four warps 92.8).
+    // (8 rows of 131001 tokens of 128: 88.4 us, with blocks of four warps 94.1).
     // Many rows: blocks of four warps, one joins while the others load (384
-    // rows of 1000 tokens: 38.8 us against 47.1).
+    // rows of 1000 tokens: 39.8 us against 48.2).
     const bool big = vec && p.rows <= dev.sm_count / 2;
     // A row's beginning counts like `lead` tiles (48 ragged sequences of up to 6000
-    // tokens with their weights: 115 us, 123 us with none).
+    // tokens with their weights: 111.5 us, 120.4 us with none).
     a.lead = big ? 16 : 8;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = kv->elem == GEMV_ELEM_F16 ? launch_attn_f16(a, vec, nt, big, dev.sm_count, s)

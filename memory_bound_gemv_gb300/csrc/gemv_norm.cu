@@ -675,9 +675,11 @@ cudaError_t launch_steps(const NormArgs &a, int sm_count, cudaStream_t s)
     // on fewer rows than SMs); where rows begin anywhere, blocks that keep their
     // staged operands (2000 x 9001 50.6 us against 66.7), up to 320 threads.  Up
     // to 384 registers spill and an SM has no room to stage three operands twice:
-    // faster where nothing is staged (200 x 11908 in bf16 9.5 us against 11.7, 600
-    // 21.9 against 23.5) or both streams are FP32 (2000 95.1 against 101), not for
-    // more rows of other types (69.0 against 71.2).  Operands of each row are loaded late in
+    // two blocks where nothing is staged (11908 wide in bf16: 200 rows 8.2 us
+    // against 10.1, 608 19.6 against 21.9, though 400 17.2 against 16.3) or both
+    // streams are FP32 (2000 x 10501 71.8 against 90.6, 12281 90.3 against 97.7),
+    // one for more rows of other types (in bf16 1000 x 11908 35.2 against 37.5,
+    // 2000 65.3 against 63.1; FP32 and binary16 2000 x 12281 60.9 against 75.9).  Operands of each row are loaded late in
     // it, which blocks hide better than rows ahead do (2000 x 8192 with gate,
     // weight and bias of each row 38.3 us against 42.7; with shared ones 28.1
     // against 26.7).  400 x 4096, all rows at once on the GPU, is faster without
