@@ -444,6 +444,10 @@ typedef struct {
     float scale;
 } gemv_attn_t;
 gemv_status_t gemv_attn_paged(const gemv_kv_t *kv, const gemv_attn_t *args, void *stream);
+/* The same with first slots that stay visible behind the window: a sequence of n
+ * slots attends to t < sinks and n - window <= t < n (window 0: to all).  With
+ * scores_out the sums of both parts are written. */
+gemv_status_t gemv_attn_paged_sinks(const gemv_kv_t *kv, const gemv_attn_t *args, int sinks, void *stream);
 /* Bytes of workspace (0 where the arguments are not valid).  weights: whether
  * scores_out will be given; capacity-sized scratch comes with it. */
 size_t gemv_attn_paged_workspace(const gemv_kv_t *kv, int q_heads, int weights);
@@ -503,6 +507,57 @@ typedef struct {
     int32_t src_elem, tokens, q_heads, axes, rot, pairs;
 } gemv_rope_t;
 gemv_status_t gemv_rope_append(const gemv_kv_t *kv, const gemv_rope_t *args, void *stream);
+/*
+ * The same with a norm of every head of q and k before it is turned:
+ *   x / sqrt(mean(x^2) + eps) * weight
+ * over its head_dim elements.  q_weight, k_weight: head_dim values of types
+ * q_elem and k_elem, NULL for none; with unit_offset they stand for 1 + weight.  v
+ * is not normed.  The normed values are not rounded before they are turned.
+ */
+typedef struct {
+    const void *q_weight, *k_weight;
+    int32_t q_elem, k_elem; /* gemv_elem_t */
+    int32_t unit_offset;
+    float eps;
+} gemv_head_norm_t;
+gemv_status_t gemv_rope_append_norm(const gemv_kv_t *kv, const gemv_rope_t *args, const gemv_head_norm_t *norm,
+                                    void *stream);
+
+/*
+ * A step's pages and slots, from the lengths of the requests (sequences of
+ * kv): request b has lengths[b] slots in use and gets fresh[b] new tokens
+ * (negative: it is over).
+ *   - Requests that need pages take them, in their order, from the ring of free
+ *     pages: of its ring_size places, state[1] from place state[0] on hold free
+ *     pages (places are counted around its end).  They go into the
+ *     requests' rows of the page table behind those they have.
+ *   - A request whose pages are not there gets none, nor do those behind it
+ *     that need some; it waits: as if it had no new tokens.  So does a request
+ *     whose tokens do not fit in the slot map, and those behind it.
+ *   - The pages of requests that are over go behind the ring's end, in their
+ *     order, but for those of shared[b] first slots (whole pages; NULL:
+ *     none), which others have too.  Their rows stay as they are.
+ *   - starts [batch + 1]: where the tokens of each request begin in the slot
+ *     map; slots and seq [room]: each token's slot and request, as
+ *     gemv_rope_append takes them; behind the last token -1 and 0.
+ *   - lengths_out [batch]: the slots in use afterwards (0 where a request is
+ *     over); state_out [2]: the ring's state afterwards.  They may be lengths
+ *     and state.
+ * Of kv the page table, its sizes and num_pages are used.  A length, a page or a
+ * state out of range, new tokens beyond the capacity, and more pages returned than
+ * the ring has lent are reported as GEMV_ERR_BAD_INDEX; such a request gets nothing.
+ */
+typedef struct {
+    const int32_t *lengths, *fresh, *shared;
+    int32_t *lengths_out;
+    int32_t *ring;
+    int64_t ring_size;
+    const int32_t *state;
+    int32_t *state_out;
+    int32_t *starts, *slots, *seq;
+    int64_t room;
+} gemv_assign_t;
+gemv_status_t gemv_kv_assign(const gemv_kv_t *kv, const gemv_assign_t *args, void *stream);
 
 /*
  * The norms around a block with its gate and the residual:

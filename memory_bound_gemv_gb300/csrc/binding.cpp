@@ -19,8 +19,10 @@
 
 namespace {
 
-gemv_status_t (*p_attn)(const gemv_kv_t *, const gemv_attn_t *, void *);
+gemv_status_t (*p_attn)(const gemv_kv_t *, const gemv_attn_t *, int, void *);
 gemv_status_t (*p_rope)(const gemv_kv_t *, const gemv_rope_t *, void *);
+gemv_status_t (*p_rope_norm)(const gemv_kv_t *, const gemv_rope_t *, const gemv_head_norm_t *, void *);
+gemv_status_t (*p_assign)(const gemv_kv_t *, const gemv_assign_t *, void *);
 gemv_status_t (*p_plan)(const gemv_kv_t *, const int32_t *, int, int, int, int32_t *, int64_t, int32_t *, void *);
 gemv_status_t (*p_apply)(const gemv_kv_t *, const int32_t *, int64_t, const int32_t *, int32_t *, int, void *);
 gemv_status_t (*p_norm)(const gemv_norm_t *, void *);
@@ -121,10 +123,10 @@ PyObject *answer(Py_ssize_t n, Py_ssize_t wanted, F call)
     return PyLong_FromLong(status);
 }
 
-// (cache, device, q, lengths, out, lse, scores_out address, workspace address, its bytes, scale, window, stream)
+// (cache, device, q, lengths, out, lse, scores_out address, workspace address, its bytes, scale, window, stream), and sinks (0)
 PyObject *attn(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    return answer(n, 12, [&]() -> int {
+    return answer(n == 13 ? 12 : n, 12, [&]() -> int {
         const gemv_kv_t *kv = cache(a[0]);
         const int64_t index = integer(a[1]);
         gemv_attn_t g;
@@ -144,15 +146,27 @@ PyObject *attn(PyObject *, PyObject *const *a, Py_ssize_t n)
         g.q_heads = static_cast<int32_t>(count);
         g.scale = real(a[9]);
         g.window = integer32(a[10]);
-        if (g.window < 0) throw Other();
-        return p_attn(kv, &g, stream_of(a[11], index));
+        const int sinks = n == 13 ? integer32(a[12]) : 0;
+        if (g.window < 0 || sinks < 0) throw Other();
+        return p_attn(kv, &g, sinks, stream_of(a[11], index));
     });
 }
 
-// (cache, device, rope's packed fields, q, k, v, positions, slots, seq, stamps, q_out, stream)
+// A norm's weight [dim] of any type; None: NULL.
+const void *weight_of(PyObject *o, int64_t index, int64_t dim, int32_t *elem)
+{
+    *elem = GEMV_ELEM_F32;
+    if (o == Py_None) return nullptr;
+    const at::Tensor &t = tensor(o, index);
+    *elem = elem_of(t.scalar_type());
+    return operand(o, index, t.scalar_type(), {dim}).data_ptr();
+}
+
+// (cache, device, rope's packed fields, q, k, v, positions, slots, seq, stamps, q_out, stream), and for norms
+// (q_weight, k_weight, unit_offset, eps) behind them
 PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    return answer(n, 12, [&]() -> int {
+    return answer(n == 16 ? 12 : n, 12, [&]() -> int {
         const gemv_kv_t *kv = cache(a[0]);
         const int64_t index = integer(a[1]);
         gemv_rope_t g;
@@ -189,7 +203,13 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n)
         g.axes = r.axes;
         g.rot = r.rot;
         g.pairs = r.pairs;
-        return p_rope(kv, &g, stream_of(a[11], index));
+        if (n == 12) return p_rope(kv, &g, stream_of(a[11], index));
+        gemv_head_norm_t w;
+        w.q_weight = weight_of(a[12], index, kv->head_dim, &w.q_elem);
+        w.k_weight = weight_of(a[13], index, kv->head_dim, &w.k_elem);
+        w.unit_offset = integer(a[14]) != 0;
+        w.eps = real(a[15]);
+        return p_rope_norm(kv, &g, &w, stream_of(a[11], index));
     });
 }
 
@@ -236,6 +256,32 @@ PyObject *apply(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
+// (cache, device, ring, state, lengths, fresh, starts, slots, seq, shared, lengths_out, state_out, stream)
+PyObject *assign(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return answer(n, 13, [&]() -> int {
+        const gemv_kv_t *kv = cache(a[0]);
+        const int64_t index = integer(a[1]);
+        gemv_assign_t g;
+        std::memset(&g, 0, sizeof(g));
+        const at::Tensor &ring = tensor(a[2], index), &slots = tensor(a[7], index);
+        if (ring.dim() != 1 || slots.dim() != 1) throw Other();
+        g.ring_size = ring.size(0);
+        g.room = slots.size(0);
+        g.ring = dense<int32_t>(a[2], index, {g.ring_size});
+        g.state = dense<int32_t>(a[3], index, {2});
+        g.lengths = dense<int32_t>(a[4], index, {kv->batch});
+        g.fresh = dense<int32_t>(a[5], index, {kv->batch});
+        g.starts = dense<int32_t>(a[6], index, {kv->batch + 1});
+        g.slots = dense<int32_t>(a[7], index, {g.room});
+        g.seq = dense<int32_t>(a[8], index, {g.room});
+        if (a[9] != Py_None) g.shared = dense<int32_t>(a[9], index, {kv->batch});
+        g.lengths_out = a[10] == Py_None ? const_cast<int32_t *>(g.lengths) : dense<int32_t>(a[10], index, {kv->batch});
+        g.state_out = a[11] == Py_None ? const_cast<int32_t *>(g.state) : dense<int32_t>(a[11], index, {2});
+        return p_assign(kv, &g, stream_of(a[12], index));
+    });
+}
+
 gemv_rows_t rows_of(PyObject *o, int64_t index, int64_t rows, int64_t width, bool one_row)
 {
     if (o == Py_None) return {nullptr, 0, 0};
@@ -277,23 +323,25 @@ PyObject *norm(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
-// The library's entry points: (attn, rope, plan, apply, norm) as addresses.
+// The library's entry points: (attn, rope, plan, apply, norm, rope with norms, assign) as addresses.
 PyObject *use(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    long long at[5] = {0, 0, 0, 0, 0};
-    for (Py_ssize_t i = 0; i < 5 && i < n; ++i) at[i] = PyLong_AsLongLong(a[i]);
+    long long at[7] = {0, 0, 0, 0, 0, 0, 0};
+    for (Py_ssize_t i = 0; i < 7 && i < n; ++i) at[i] = PyLong_AsLongLong(a[i]);
     if (PyErr_Occurred()) return nullptr;
     p_attn = reinterpret_cast<decltype(p_attn)>(at[0]);
     p_rope = reinterpret_cast<decltype(p_rope)>(at[1]);
     p_plan = reinterpret_cast<decltype(p_plan)>(at[2]);
     p_apply = reinterpret_cast<decltype(p_apply)>(at[3]);
     p_norm = reinterpret_cast<decltype(p_norm)>(at[4]);
+    p_rope_norm = reinterpret_cast<decltype(p_rope_norm)>(at[5]);
+    p_assign = reinterpret_cast<decltype(p_assign)>(at[6]);
     Py_RETURN_NONE;
 }
 
 #define MBG_FUNCTION(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(f)), METH_FASTCALL, nullptr}
 PyMethodDef functions[] = {MBG_FUNCTION(attn), MBG_FUNCTION(rope), MBG_FUNCTION(plan), MBG_FUNCTION(apply),
-                           MBG_FUNCTION(norm), MBG_FUNCTION(use), {nullptr, nullptr, 0, nullptr}};
+                           MBG_FUNCTION(norm), MBG_FUNCTION(assign), MBG_FUNCTION(use), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mbgbinding", nullptr, -1, functions, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

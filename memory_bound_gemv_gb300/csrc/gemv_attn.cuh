@@ -2,8 +2,8 @@
 //
 //   s_t = scale * q . k_t,  p = softmax(s),  o = sum_t p_t v_t
 //
-// over the tokens t in [max(0, len - window), len) of a sequence, G query
-// heads sharing one cached head.  One pass over the cache: each warp keeps a
+// over the tokens t in [max(0, len - window), len) of a sequence, and with
+// sinks those in [0, sinks), G query heads sharing one cached head.  One pass over the cache: each warp keeps a
 // running maximum m, denominator l and output O of its own tokens and rescales
 // by 2^(m - m') when m grows (Milakov & Gimelshein's online softmax); the
 // warps, then the blocks, that share a row are joined by the same rule.
@@ -181,10 +181,16 @@ __device__ __forceinline__ uint4 load8(const uint16_t *p, int left)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The tokens of a sequence that are attended to, and their tiles.
+// The tokens of a sequence that are attended to, and their tiles of TOKENS
+// tokens.  Tile t of the sequence's tiles is tile t of the cache for t <
+// sink_tiles, of which the tokens before `sinks` count, and tile0 + t behind
+// them.  (Sinks and window may meet in one tile of the cache, which is then
+// gone through twice.)
 struct RowSpan {
     int first, len;         // tokens [first, len)
-    int tile0, tiles;       // tiles of TOKENS tokens, tile0 = first / TOKENS
+    int sinks;              // and [0, sinks), sinks < first; or 0
+    int sink_tiles;
+    int tile0, tiles;       // first / TOKENS - sink_tiles; the tiles' number
 };
 
 template <int TOKENS>
@@ -196,7 +202,10 @@ __device__ __forceinline__ RowSpan row_span(const AttnArgs &a, int b)
     if (len > a.kv.capacity) len = static_cast<int>(a.kv.capacity);
     r.len = len;
     r.first = (a.window > 0 && len > a.window) ? len - a.window : 0;
-    r.tile0 = r.first / TOKENS;
+    if (r.first <= a.sinks) r.first = 0;
+    r.sinks = r.first > 0 ? a.sinks : 0;
+    r.sink_tiles = (r.sinks + TOKENS - 1) / TOKENS;
+    r.tile0 = r.first / TOKENS - r.sink_tiles;
     r.tiles = len > r.first ? (len + TOKENS - 1) / TOKENS - r.tile0 : 0;
     return r;
 }
@@ -277,7 +286,7 @@ struct Kernel {
     struct Segment {
         int64_t r0;             // where the row begins
         int b, hk, t0, t1;
-        int first, len, tile0, tiles;
+        int first, len, sinks, sink_tiles, tile0, tiles;
     };
 
     struct Shared {
@@ -399,6 +408,8 @@ struct Kernel {
                 out.t1 = static_cast<int>(to - r0 - w.lead);
                 out.first = span.first;
                 out.len = span.len;
+                out.sinks = span.sinks;
+                out.sink_tiles = span.sink_tiles;
                 out.tile0 = span.tile0;
                 out.tiles = n;
                 if (out.t0 < out.t1) return;
@@ -449,10 +460,11 @@ struct Kernel {
         };
         auto place = [&](const Segment &s, int tile) {
             Places p;
+            const bool sink = tile < s.sink_tiles;
 #pragma unroll
             for (int i = 0; i < MT; ++i)
-                p.t[i] = place_of<WHOLE>(kv, kv.table + s.b * kv.table_stride, (s.tile0 + tile) * MT + i, tile < s.t1,
-                                         s.first, s.len, a.err);
+                p.t[i] = place_of<WHOLE>(kv, kv.table + s.b * kv.table_stride, (sink ? tile : s.tile0 + tile) * MT + i,
+                                         tile < s.t1, sink ? 0 : s.first, sink ? s.sinks : s.len, a.err);
             return p;
         };
         // does token r of a tile count, and its place relative to p's
@@ -593,14 +605,17 @@ struct Kernel {
                 }
                 if (a.scores_out) {
                     const int64_t row = static_cast<int64_t>(seg.b) * kv.kv_heads * a.head_tiles + seg.hk;
+                    const bool sink = tile < seg.sink_tiles;
+                    const int at0 = (sink ? tile : seg.tile0 + tile) * MT * 16 + g;
+                    const int first = sink ? 0 : seg.first, len = sink ? seg.sinks : seg.len;
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                             for (int rr = 0; rr < 2; ++rr) {
-                                const int head = nt * 8 + 2 * t, at = ((seg.tile0 + tile) * MT + mt) * 16 + g + 8 * rr;
-                                if (head < a.logit_heads && at < seg.len && at >= seg.first)
+                                const int head = nt * 8 + 2 * t, at = at0 + mt * 16 + 8 * rr;
+                                if (head < a.logit_heads && at < len && at >= first)
                                     *reinterpret_cast<float2 *>(a.logits + (row * kv.capacity + at) * a.logit_heads + head) =
                                         make_float2(s[mt][nt][2 * rr], s[mt][nt][2 * rr + 1]);
                             }

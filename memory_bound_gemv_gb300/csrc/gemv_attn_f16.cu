@@ -26,6 +26,17 @@ __global__ void __launch_bounds__(256) mbg_attn_weights_kernel(const __grid_cons
     const attn::RowSpan span = attn::row_span<16>(a, b);
     const int64_t out_row = (static_cast<int64_t>(b) * a.kv.kv_heads + h) * a.kv.capacity;
     const int step = gridDim.x * 256 * kTokens;
+    // the first blocks take the sinks, and then their share of the others
+    for (int s = blockIdx.x * 256 + threadIdx.x; s < span.sinks; s += gridDim.x * 256) {
+        float sum = a.scores_in[out_row + s];
+        for (int i = 0; i < a.group; ++i) {
+            const int64_t row = (static_cast<int64_t>(b) * a.kv.kv_heads + h) * a.head_tiles + i / tile_heads;
+            const int k = i % tile_heads;
+            sum += attn::exp2_approx(__ldcg(a.logits + (row * a.kv.capacity + s) * a.logit_heads + k) -
+                                     __ldg(a.row_lse + row * tile_heads + k));
+        }
+        a.scores_out[out_row + s] = sum;
+    }
     // (a step behind the last slot may lie beyond 2^31)
     for (int64_t s0 = span.first + blockIdx.x * 256 * kTokens + threadIdx.x; s0 < span.len; s0 += step) {
         float sum[kTokens], old[kTokens];

@@ -45,6 +45,7 @@ struct AttnArgs {
     int q_heads, group;         // query heads per cached head
     int head_tiles;             // tiles of 8 * NT query heads per cached head
     int window;                 // 0: none
+    int sinks;                  // first slots that stay visible behind a window
     float scale_log2;           // scale * log2(e)
     unsigned int *err;
     // workspace
@@ -107,9 +108,33 @@ struct RopeArgs {
     const uint64_t *turns;      // [rot / 2]: 2^64 * frequency / (2 pi)
     const uint8_t *axis;        // [rot / 2]
     int tokens, q_heads, rot, axes, pairs;
+    // norms of q's and k's heads before they are turned
+    int norm, unit_offset;
+    const void *q_weight, *k_weight;  // [dim] or NULL (1)
+    int q_weight_e, k_weight_e;
+    float eps;
     unsigned int *err;
 };
 cudaError_t launch_rope(const RopeArgs &a, bool vec, int sm_count, cudaStream_t s);
+
+struct AssignArgs {
+    int32_t *table;             // [batch][max_pages]
+    int64_t table_stride, capacity;
+    int64_t num_pages;
+    int batch, page_size;
+    const int32_t *lengths, *fresh;
+    const int32_t *shared;      // NULL: none
+    int32_t *lengths_out;       // may be lengths
+    int32_t *ring;              // free pages, from state[0] on, state[1] of them
+    int64_t ring_size;
+    const int32_t *state;
+    int32_t *state_out;         // may be state
+    int32_t *starts;            // [batch + 1]
+    int32_t *slots, *seq;       // [room]
+    int64_t room;
+    unsigned int *err;
+};
+cudaError_t launch_assign(const AssignArgs &a, cudaStream_t s);
 
 struct NormArgs {
     const void *y, *r, *gate, *post_w, *pre_w, *pre_b;

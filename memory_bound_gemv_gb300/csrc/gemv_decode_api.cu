@@ -116,6 +116,69 @@ AttnPlan attn_plan(const KvView &v, int group, int nt, bool weights)
     return p;
 }
 
+gemv_status_t rope_append(const gemv_kv_t *kv, const gemv_rope_t *r, const gemv_head_norm_t *norm, void *stream)
+{
+    RopeArgs a{};
+    const gemv_status_t st = view_of(kv, &a.kv);
+    if (st != GEMV_OK) return st;
+    if (!r || !is_elem(r->src_elem) || r->tokens < 0 || r->q_heads < 0 || r->axes < 1 || r->rot < 0 || r->rot % 2 ||
+        r->rot > a.kv.dim || r->pos_stride < 0)
+        return GEMV_ERR_INVALID_VALUE;
+    if (negative(r->q) || negative(r->k) || negative(r->v) || negative(r->q_out)) return GEMV_ERR_INVALID_VALUE;
+    if (!r->seq && r->tokens > a.kv.batch) return GEMV_ERR_INVALID_VALUE;
+    if (norm && ((norm->q_weight && !is_elem(norm->q_elem)) || (norm->k_weight && !is_elem(norm->k_elem))))
+        return GEMV_ERR_INVALID_VALUE;
+    // a block looks up to 64 steps of the grid ahead, in 32 bits
+    if (r->tokens > INT_MAX - (1 << 20) || too_many_heads(r->q_heads, a.kv.dim)) return GEMV_ERR_UNSUPPORTED;
+    if (r->tokens == 0) return GEMV_OK;
+    if ((r->q_heads > 0 && (!r->q.data || !r->q_out.data)) || !r->k.data || !r->v.data || !r->positions || !r->slots ||
+        (r->rot > 0 && (!r->turns || !r->axis)) || !kv->k || !kv->v)
+        return GEMV_ERR_INVALID_VALUE;
+    const int eb = elem_bytes(r->src_elem);
+    if (!aligned(r->q.data, eb) || !aligned(r->k.data, eb) || !aligned(r->v.data, eb) || !aligned(r->q_out.data, 2) ||
+        !aligned(r->positions, 4) || !aligned(r->slots, 4) || !aligned(r->seq, 4) || !aligned(r->stamps, 4) ||
+        !aligned(r->turns, 8))
+        return GEMV_ERR_MISALIGNED;
+    if (norm && ((norm->q_weight && !aligned(norm->q_weight, elem_bytes(norm->q_elem))) ||
+                 (norm->k_weight && !aligned(norm->k_weight, elem_bytes(norm->k_elem)))))
+        return GEMV_ERR_MISALIGNED;
+    DecodeDevice dev;
+    if (!decode_device(&dev)) return GEMV_ERR_CUDA;
+    if (norm) {
+        a.norm = 1;
+        a.unit_offset = norm->unit_offset != 0;
+        a.q_weight = norm->q_weight, a.q_weight_e = norm->q_elem;
+        a.k_weight = norm->k_weight, a.k_weight_e = norm->k_elem;
+        a.eps = norm->eps;
+    }
+    a.q = r->q.data, a.q_st = r->q.stride[0], a.q_sh = r->q.stride[1];
+    a.k = r->k.data, a.k_st = r->k.stride[0], a.k_sh = r->k.stride[1];
+    a.v = r->v.data, a.v_st = r->v.stride[0], a.v_sh = r->v.stride[1];
+    a.q_out = r->q_out.data, a.qo_st = r->q_out.stride[0], a.qo_sh = r->q_out.stride[1];
+    a.src_elem = r->src_elem;
+    a.dst_elem = kv->elem;
+    a.positions = r->positions;
+    a.pos_stride = r->pos_stride;
+    a.slots = r->slots;
+    a.seq = r->seq;
+    a.stamps = r->stamps;
+    a.scores_cache = kv->scores;
+    a.stamps_cache = kv->stamps;
+    a.turns = r->turns;
+    a.axis = r->axis;
+    a.tokens = r->tokens;
+    a.q_heads = r->q_heads;
+    a.rot = r->rot;
+    a.axes = r->axes;
+    a.pairs = r->pairs != 0;
+    a.err = dev.status;
+    bool vec = cache_vec(kv) && r->rot % 16 == 0;
+    for (const gemv_heads_t *h : {&r->q, &r->k, &r->v, &r->q_out})
+        vec = vec && aligned(h->data, h == &r->q_out ? 16 : vec_bytes(r->src_elem)) && mult8(h->stride, 2);
+    const cudaError_t e = launch_rope(a, vec, dev.sm_count, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GEMV_OK : decode_cuda_fail(e, GEMV_ERR_LAUNCH);
+}
+
 }  // namespace
 }  // namespace mbg
 
@@ -148,13 +211,18 @@ uint64_t gemv_capture_id(void *stream)
 
 gemv_status_t gemv_attn_paged(const gemv_kv_t *kv, const gemv_attn_t *args, void *stream)
 {
+    return gemv_attn_paged_sinks(kv, args, 0, stream);
+}
+
+gemv_status_t gemv_attn_paged_sinks(const gemv_kv_t *kv, const gemv_attn_t *args, int sinks, void *stream)
+{
     AttnArgs a{};
     gemv_status_t st = view_of(kv, &a.kv);
     if (st != GEMV_OK) return st;
     if (!args) return GEMV_ERR_INVALID_VALUE;
     const gemv_heads_t &q = args->q, &out = args->out;
     const int q_heads = args->q_heads;
-    if (q_heads < 1 || q_heads % a.kv.kv_heads || args->window < 0 || negative(q) || negative(out))
+    if (q_heads < 1 || q_heads % a.kv.kv_heads || args->window < 0 || sinks < 0 || negative(q) || negative(out))
         return GEMV_ERR_INVALID_VALUE;
     if (too_many_heads(q_heads, a.kv.dim)) return GEMV_ERR_UNSUPPORTED;
     if (a.kv.batch == 0) return GEMV_OK;
@@ -185,6 +253,7 @@ gemv_status_t gemv_attn_paged(const gemv_kv_t *kv, const gemv_attn_t *args, void
     a.group = group;
     a.head_tiles = p.head_tiles;
     a.window = args->window;
+    a.sinks = sinks;
     a.scale_log2 = args->scale * 1.4426950408889634f;
     a.err = dev.status;
     unsigned char *ws = static_cast<unsigned char *>(args->workspace);
@@ -263,52 +332,56 @@ gemv_status_t gemv_kv_evict_apply(const gemv_kv_t *kv, const int32_t *moves, int
 
 gemv_status_t gemv_rope_append(const gemv_kv_t *kv, const gemv_rope_t *r, void *stream)
 {
-    RopeArgs a{};
-    const gemv_status_t st = view_of(kv, &a.kv);
+    return rope_append(kv, r, nullptr, stream);
+}
+
+gemv_status_t gemv_rope_append_norm(const gemv_kv_t *kv, const gemv_rope_t *r, const gemv_head_norm_t *norm, void *stream)
+{
+    if (!norm) return GEMV_ERR_INVALID_VALUE;
+    return rope_append(kv, r, norm, stream);
+}
+
+gemv_status_t gemv_kv_assign(const gemv_kv_t *kv, const gemv_assign_t *g, void *stream)
+{
+    KvView v;
+    // the pools are not touched: they may be missing, not so the table
+    const gemv_status_t st = view_of(kv, &v, false);
     if (st != GEMV_OK) return st;
-    if (!r || !is_elem(r->src_elem) || r->tokens < 0 || r->q_heads < 0 || r->axes < 1 || r->rot < 0 || r->rot % 2 ||
-        r->rot > a.kv.dim || r->pos_stride < 0)
+    if (!g || g->room < 0 || g->ring_size < 0) return GEMV_ERR_INVALID_VALUE;
+    if (g->room > INT_MAX - (1 << 20) || g->ring_size > INT_MAX) return GEMV_ERR_UNSUPPORTED;
+    if (!g->state || !g->state_out || !g->starts || (g->ring_size > 0 && !g->ring) || (g->room > 0 && (!g->slots || !g->seq)) ||
+        (v.batch > 0 && (!g->lengths || !g->lengths_out || !g->fresh || (v.max_pages > 0 && !v.table))))
         return GEMV_ERR_INVALID_VALUE;
-    if (negative(r->q) || negative(r->k) || negative(r->v) || negative(r->q_out)) return GEMV_ERR_INVALID_VALUE;
-    if (!r->seq && r->tokens > a.kv.batch) return GEMV_ERR_INVALID_VALUE;
-    // a block looks up to 64 steps of the grid ahead, in 32 bits
-    if (r->tokens > INT_MAX - (1 << 20) || too_many_heads(r->q_heads, a.kv.dim)) return GEMV_ERR_UNSUPPORTED;
-    if (r->tokens == 0) return GEMV_OK;
-    if ((r->q_heads > 0 && (!r->q.data || !r->q_out.data)) || !r->k.data || !r->v.data || !r->positions || !r->slots ||
-        (r->rot > 0 && (!r->turns || !r->axis)) || !kv->k || !kv->v)
-        return GEMV_ERR_INVALID_VALUE;
-    const int eb = elem_bytes(r->src_elem);
-    if (!aligned(r->q.data, eb) || !aligned(r->k.data, eb) || !aligned(r->v.data, eb) || !aligned(r->q_out.data, 2) ||
-        !aligned(r->positions, 4) || !aligned(r->slots, 4) || !aligned(r->seq, 4) || !aligned(r->stamps, 4) ||
-        !aligned(r->turns, 8))
-        return GEMV_ERR_MISALIGNED;
+    if (v.batch > 1 && v.table_stride < v.max_pages) return GEMV_ERR_INVALID_VALUE;  // rows that are written must not lie on one another
+    for (const void *p : {static_cast<const void *>(v.table), static_cast<const void *>(g->ring), static_cast<const void *>(g->state),
+                          static_cast<const void *>(g->state_out), static_cast<const void *>(g->starts),
+                          static_cast<const void *>(g->slots), static_cast<const void *>(g->seq),
+                          static_cast<const void *>(g->lengths), static_cast<const void *>(g->lengths_out),
+                          static_cast<const void *>(g->fresh), static_cast<const void *>(g->shared)})
+        if (!aligned(p, 4)) return GEMV_ERR_MISALIGNED;
     DecodeDevice dev;
     if (!decode_device(&dev)) return GEMV_ERR_CUDA;
-    a.q = r->q.data, a.q_st = r->q.stride[0], a.q_sh = r->q.stride[1];
-    a.k = r->k.data, a.k_st = r->k.stride[0], a.k_sh = r->k.stride[1];
-    a.v = r->v.data, a.v_st = r->v.stride[0], a.v_sh = r->v.stride[1];
-    a.q_out = r->q_out.data, a.qo_st = r->q_out.stride[0], a.qo_sh = r->q_out.stride[1];
-    a.src_elem = r->src_elem;
-    a.dst_elem = kv->elem;
-    a.positions = r->positions;
-    a.pos_stride = r->pos_stride;
-    a.slots = r->slots;
-    a.seq = r->seq;
-    a.stamps = r->stamps;
-    a.scores_cache = kv->scores;
-    a.stamps_cache = kv->stamps;
-    a.turns = r->turns;
-    a.axis = r->axis;
-    a.tokens = r->tokens;
-    a.q_heads = r->q_heads;
-    a.rot = r->rot;
-    a.axes = r->axes;
-    a.pairs = r->pairs != 0;
+    AssignArgs a{};
+    a.table = const_cast<int32_t *>(v.table);
+    a.table_stride = v.table_stride;
+    a.capacity = v.capacity;
+    a.num_pages = v.num_pages;
+    a.batch = v.batch;
+    a.page_size = v.page_size;
+    a.lengths = g->lengths;
+    a.fresh = g->fresh;
+    a.shared = g->shared;
+    a.lengths_out = g->lengths_out;
+    a.ring = g->ring;
+    a.ring_size = g->ring_size;
+    a.state = g->state;
+    a.state_out = g->state_out;
+    a.starts = g->starts;
+    a.slots = g->slots;
+    a.seq = g->seq;
+    a.room = g->room;
     a.err = dev.status;
-    bool vec = cache_vec(kv) && r->rot % 16 == 0;
-    for (const gemv_heads_t *h : {&r->q, &r->k, &r->v, &r->q_out})
-        vec = vec && aligned(h->data, h == &r->q_out ? 16 : vec_bytes(r->src_elem)) && mult8(h->stride, 2);
-    const cudaError_t e = launch_rope(a, vec, dev.sm_count, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_assign(a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GEMV_OK : decode_cuda_fail(e, GEMV_ERR_LAUNCH);
 }
 

@@ -8,6 +8,11 @@
 // at most |pos| * 2^-65 turns from the table's rounding.  Its upper 32 bits
 // go to sincospif.
 //
+// With norms, each head of q and k is first divided by the root of its mean
+// square plus eps and multiplied by its weight: the threads that hold a head,
+// 2^n of them side by side, add their squares by shuffles, and the rest is the
+// same pass.
+//
 // Bound by the bytes of q, k and v read and written once.  A thread keeps one
 // head and one unit of 16 of its elements, so that its addresses and its part
 // of the work are settled once, and goes through tokens: a block's loads of
@@ -111,21 +116,39 @@ struct Place {
     int seq, slot, page, off;  // page -1: not written
 };
 
+// A norm's weight; none is 1.
+__device__ __forceinline__ float weight_at(const void *w, int elem, int d, int unit_offset)
+{
+    if (!w) return 1.f;
+    const float v = elem == GEMV_ELEM_F32   ? elem_load1<GEMV_ELEM_F32>(w, d)
+                    : elem == GEMV_ELEM_F16 ? elem_load1<GEMV_ELEM_F16>(w, d)
+                                            : elem_load1<GEMV_ELEM_BF16>(w, d);
+    return unit_offset ? v + 1.f : v;
+}
+
 // All warps but the last turn; the last one looks ahead: it computes the next
 // token's sines and cosines and its place in the cache, whose indices it has
 // read for 32 tokens at a time.  7001 tokens of 48 heads of 128 in bf16: 29.8 us,
 // 5.8 TB/s; with these reads token by token 33.6 us, with the sines in every
 // thread (100 registers, 12 warps on an SM) 62.8 us.
-template <bool VEC, int SRC, int DST>
+template <bool VEC, int SRC, int DST, bool NORM>
 __global__ void __launch_bounds__(kMaxThreads + 32, 3)
     mbg_rope_kernel(const __grid_constant__ RopeArgs a, int heads_per_block, int per_head)
 {
     __shared__ __align__(16) float s_cos[2][kMaxPairs], s_sin[2][kMaxPairs];
     __shared__ Place s_place[2];
+    __shared__ __align__(16) float s_weight[NORM ? 2 : 1][NORM ? 2 * kMaxPairs : 1];  // of q and k
     pdl_trigger();
     pdl_wait();
     const KvView &kv = a.kv;
     const int tid = threadIdx.x, half = a.rot >> 1, step = gridDim.x;
+    if (NORM) {  // read behind the first token's barrier
+        for (int i = tid; i < 2 * kv.dim; i += blockDim.x) {
+            const int k = i >= kv.dim, d = i - k * kv.dim;
+            const void *w = k ? a.k_weight : a.q_weight;
+            s_weight[k][d] = weight_at(w, k ? a.k_weight_e : a.q_weight_e, d, a.unit_offset);
+        }
+    }
 
     if (tid >= static_cast<int>(blockDim.x) - 32) {
         const int lane = tid & 31;
@@ -230,6 +253,10 @@ __global__ void __launch_bounds__(kMaxThreads + 32, 3)
     const int64_t d_page = is_v ? kv.vs_page : kv.ks_page, d_tok = is_v ? kv.vs_tok : kv.ks_tok;
     constexpr int kAhead = SRC == GEMV_ELEM_F32 ? 1 : 2;  // tokens requested ahead
     Raw8<SRC> x[kAhead], y[kAhead];
+    if (NORM) {  // elements that do not exist count as 0 in the squares' sum
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) x[k].a = x[k].b = y[k].a = y[k].b = make_uint4(0, 0, 0, 0);
+    }
     auto request = [&](int k, int t) {
         if (t < a.tokens) {
             x[k].template load<VEC>(src, un.d0, n0);
@@ -249,6 +276,23 @@ __global__ void __launch_bounds__(kMaxThreads + 32, 3)
             x[k].template floats<VEC>(v);
             y[k].template floats<VEC>(w);
             request(k, t + kAhead * step);
+            if (NORM) {
+                float sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum += v[e] * v[e];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum += w[e] * w[e];
+                for (int i = 1; i < per_head; i *= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, i);
+                if (!is_v) {
+                    const float f = rsqrtf(sum / kv.dim + a.eps);
+                    const float *weight = s_weight[is_q ? 0 : 1];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        if (e < n0) v[e] *= f * weight[un.d0 + e];
+                        if (e < n1) w[e] *= f * weight[un.d1 + e];
+                    }
+                }
+            }
             if (un.turned) {
                 // pairs past the last turn elements that do not exist
                 const int last = half - 1;
@@ -286,12 +330,17 @@ __global__ void __launch_bounds__(kMaxThreads + 32, 3)
     }
 }
 
-template <bool VEC, int SRC, int DST>
+template <bool VEC, int SRC, int DST, bool NORM>
 cudaError_t launch(const RopeArgs &a, int sm_count, cudaStream_t s)
 {
     const int heads = a.q_heads + 2 * a.kv.kv_heads, half = a.rot / 2;
     const int units = (half + 7) / 8 + (a.kv.dim - a.rot + 15) / 16, v_units = (a.kv.dim + 15) / 16;
-    const int per_head = units > v_units ? units : v_units;
+    int per_head = units > v_units ? units : v_units;
+    if (NORM) {  // a head's threads lie in one warp
+        int p = 1;
+        while (p < per_head) p *= 2;
+        per_head = p;
+    }
     // few tokens: spread the heads of one over several blocks, so that the
     // call is as long as one block's few loads
     int per = heads;
@@ -299,7 +348,7 @@ cudaError_t launch(const RopeArgs &a, int sm_count, cudaStream_t s)
         per = (per + 1) / 2;
     const int threads = (per * per_head + 31) / 32 * 32 + 32, groups = (heads + per - 1) / per;
     // blocks that fit on the GPU at once go through the tokens
-    auto fn = mbg_rope_kernel<VEC, SRC, DST>;
+    auto fn = mbg_rope_kernel<VEC, SRC, DST, NORM>;
     static std::atomic<int> fit[kMaxThreads / 32 + 2];  // blocks per SM, by warps (0: not asked yet)
     int per_sm = fit[threads / 32].load(std::memory_order_relaxed);
     if (per_sm == 0) {
@@ -326,7 +375,8 @@ cudaError_t launch(const RopeArgs &a, int sm_count, cudaStream_t s)
 template <int SRC, int DST>
 cudaError_t pick(const RopeArgs &a, bool vec, int sm_count, cudaStream_t s)
 {
-    return vec ? launch<true, SRC, DST>(a, sm_count, s) : launch<false, SRC, DST>(a, sm_count, s);
+    if (a.norm) return vec ? launch<true, SRC, DST, true>(a, sm_count, s) : launch<false, SRC, DST, true>(a, sm_count, s);
+    return vec ? launch<true, SRC, DST, false>(a, sm_count, s) : launch<false, SRC, DST, false>(a, sm_count, s);
 }
 
 }  // namespace

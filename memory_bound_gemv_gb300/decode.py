@@ -72,7 +72,8 @@ def _load_binding(module):
         warnings.warn(f"decode-step calls check their arguments in Python, a few microseconds slower each: {e}")
         return _NoBinding()
     binding.use(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
-        "gemv_attn_paged", "gemv_rope_append", "gemv_kv_evict_plan", "gemv_kv_evict_apply", "gemv_norm_residual")))
+        "gemv_attn_paged_sinks", "gemv_rope_append", "gemv_kv_evict_plan", "gemv_kv_evict_apply", "gemv_norm_residual",
+        "gemv_rope_append_norm", "gemv_kv_assign")))
     return binding
 
 
@@ -89,6 +90,9 @@ def _declare(L):
     vp, i32, i64, st = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int
     sig = {
         "gemv_attn_paged": [vp, vp, vp],
+        "gemv_attn_paged_sinks": [vp, vp, i32, vp],
+        "gemv_kv_assign": [vp, vp, vp],
+        "gemv_rope_append_norm": [vp, vp, vp, vp],
         "gemv_kv_evict_plan": [vp, vp, i32, i32, i32, vp, i64, vp, vp],
         "gemv_kv_evict_apply": [vp, vp, i64, vp, vp, i32, vp],
         "gemv_rope_append": [vp, vp, vp],
@@ -109,6 +113,8 @@ def _declare(L):
 _ATTN = struct.Struct("PqqPqqPPPPNiif0q")
 _ROPE = struct.Struct("PqqPqqPqqPqqPqPPPPPiiiiii0q")
 _NORM = struct.Struct("PqiPqiPqiPqiPqiPqiPqiPqiqqffI0q")
+_HEAD_NORM = struct.Struct("PPiiif0q")
+_ASSIGN = struct.Struct("PPPPPqPPPPPq")
 
 
 def _operand(t, name, dtype, shape, index):
@@ -296,12 +302,13 @@ class RopeTable:
 
 
 def gemv_attn_paged(cache: PagedKV, q, lengths, out=None, scale: Optional[float] = None, window: int = 0, lse=None,
-                    accumulate: bool = False, scores_out=None, stream=None):
+                    accumulate: bool = False, scores_out=None, stream=None, sinks: int = 0):
     """Attention of one new token per sequence over the cache; returns out.
 
     q: [batch, q_heads, head_dim] of the cache's type, any strides with a
     contiguous last dimension; lengths: int32 [batch], the slots in use (the
-    new token's among them).  ``window``: only the last so many slots (0: all).
+    new token's among them).  ``window``: only the last so many slots (0: all),
+    and with ``sinks`` the first so many, which stay visible behind it.
     ``lse``: float32 [batch, q_heads] that receives log(sum exp(score)).
     ``accumulate``: adds the weights, summed over the query heads of a cached
     head, to cache.scores, or with ``scores_out`` writes the sums there.  A
@@ -326,7 +333,7 @@ def gemv_attn_paged(cache: PagedKV, q, lengths, out=None, scale: Optional[float]
             with _on(stream):
                 result = torch.empty(q.shape, dtype=cache.dtype, device=cache.device)
         with ws.lock:
-            st = _quick.attn(cache._at, index, q, lengths, result, lse, s_ptr, ws[0], ws[1], scale, window, ptr)
+            st = _quick.attn(cache._at, index, q, lengths, result, lse, s_ptr, ws[0], ws[1], scale, window, ptr, sinks)
         if st == 0:
             return result
     shape = (cache.batch, heads, cache.head_dim)
@@ -335,6 +342,7 @@ def gemv_attn_paged(cache: PagedKV, q, lengths, out=None, scale: Optional[float]
         raise ValueError(f"q has {heads} heads, expected a multiple of {cache.kv_heads}")
     n_ptr = _dense(lengths, "lengths", torch.int32, (cache.batch,), index)
     _count(window, "window", 0)
+    _count(sinks, "sinks", 0)
     if out is None:
         with _on(stream):
             out = torch.empty(shape, dtype=cache.dtype, device=cache.device)
@@ -351,14 +359,15 @@ def gemv_attn_paged(cache: PagedKV, q, lengths, out=None, scale: Optional[float]
     args = _ATTN.pack(q.data_ptr(), qs[0], qs[1], out.data_ptr(), os[0], os[1], n_ptr, l_ptr, s_ptr, ws[0], ws[1],
                       heads, window, scale)
     with ws.lock:
-        st = cache._lib.gemv_attn_paged(cache._at, args, ptr)
+        st = cache._lib.gemv_attn_paged_sinks(cache._at, args, sinks, ptr)
     if st:
         _mbg._raise(st, "gemv_attn_paged")
     return out
 
 
 def gemv_rope_append(cache: PagedKV, q, k, v, positions, slots, rope: RopeTable, q_out=None, seq=None, stamps=None,
-                     stream=None):
+                     stream=None, norm: bool = False, q_weight=None, k_weight=None, unit_offset: bool = False,
+                     eps: float = 1e-6):
     """Turns q and k by their positions, writes k and v to the cache; returns q_out.
 
     q: [tokens, q_heads, head_dim], k and v: [tokens, kv_heads, head_dim], all
@@ -368,11 +377,22 @@ def gemv_rope_append(cache: PagedKV, q, k, v, positions, slots, rope: RopeTable,
     in its sequence (negative: padding, not written).  seq: int32 [tokens], the
     tokens' sequences (default: token t belongs to sequence t).  stamps: int32
     [tokens], the tokens' numbers (default: the slots) for a cache with stamps.
-    q_out: [tokens, q_heads, head_dim] of the cache's type."""
+    q_out: [tokens, q_heads, head_dim] of the cache's type.
+    ``norm``: every head of q and k is first divided by sqrt(mean(x^2) + eps) and
+    multiplied by ``q_weight`` or ``k_weight`` ([head_dim], float32, float16 or
+    bfloat16; None: 1), with ``unit_offset`` by 1 + weight; v is not."""
     index = cache.index
-    if q_out is not None and _quick.rope(cache._at, index, rope._packed, q, k, v, positions, slots, seq, stamps, q_out,
-                                         stream if stream is None else _mbg._stream_ptr(stream)) == 0:
-        return q_out
+    if not norm and (q_weight is not None or k_weight is not None or unit_offset):
+        raise ValueError("q_weight, k_weight and unit_offset go with norm=True")
+    if q_out is not None:
+        last = stream if stream is None else _mbg._stream_ptr(stream)
+        if norm:
+            st = _quick.rope(cache._at, index, rope._packed, q, k, v, positions, slots, seq, stamps, q_out, last,
+                             q_weight, k_weight, unit_offset, eps)
+        else:
+            st = _quick.rope(cache._at, index, rope._packed, q, k, v, positions, slots, seq, stamps, q_out, last)
+        if st == 0:
+            return q_out
     if not isinstance(q, _Tensor) or q.dim() != 3:
         raise ValueError("q must be a tensor [tokens, q_heads, head_dim]")
     dtype = q.dtype
@@ -398,20 +418,105 @@ def gemv_rope_append(cache: PagedKV, q, k, v, positions, slots, rope: RopeTable,
         raise ValueError(f"{tokens} tokens for {cache.batch} sequences: seq is needed")
     if stamps is not None:
         t_ptr = _dense(stamps, "stamps", torch.int32, per_token, index)
+    if norm:
+        qw, kw = _rows(q_weight, "q_weight", 1, dim, index), _rows(k_weight, "k_weight", 1, dim, index)
+        if (q_weight is not None and q_weight.dim() != 1) or (k_weight is not None and k_weight.dim() != 1):
+            raise ValueError("q_weight and k_weight must be tensors [head_dim]")
     if q_out is None:
         with _on(stream):
             q_out = torch.empty(q_shape, dtype=cache.dtype, device=cache.device)
         os = q_out.stride()
     else:
         os = _operand(q_out, "q_out", cache.dtype, q_shape, index)
-    st = cache._lib.gemv_rope_append(
-        cache._at, _ROPE.pack(q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
-                              q_out.data_ptr(), os[0], os[1], positions.data_ptr(), ps[0], s_ptr, b_ptr, t_ptr,
-                              rope._turns_at, rope._axis_at, elem, tokens, heads, rope.axes, rope.rot_dim, rope.pairs),
-        _mbg._stream_ptr(stream))
+    args = _ROPE.pack(q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+                      q_out.data_ptr(), os[0], os[1], positions.data_ptr(), ps[0], s_ptr, b_ptr, t_ptr,
+                      rope._turns_at, rope._axis_at, elem, tokens, heads, rope.axes, rope.rot_dim, rope.pairs)
+    if norm:
+        st = cache._lib.gemv_rope_append_norm(
+            cache._at, args, _HEAD_NORM.pack(qw[0], kw[0], qw[2], kw[2], bool(unit_offset), eps), _mbg._stream_ptr(stream))
+    else:
+        st = cache._lib.gemv_rope_append(cache._at, args, _mbg._stream_ptr(stream))
     if st:
         _mbg._raise(st, "gemv_rope_append")
     return q_out
+
+
+class PagePool:
+    """The free pages that sequences take their pages from: a ring and its state, kept on the device.
+
+    ``ring`` int32 [places] and ``state`` int32 [2]: state[1] places from place
+    state[0] on, counted around the ring's end, hold the numbers of free pages.
+    ``pages``: a new pool in which pages 0 .. pages - 1 are free.  One pool serves
+    all caches that share a page table (a model's layers).  A ring needs as many places
+    as there are pages to lend."""
+
+    def __init__(self, pages: Optional[int] = None, ring=None, state=None, device="cuda"):
+        _need_torch()
+        if (pages is None) == (ring is None) or (ring is None) != (state is None):
+            raise ValueError("either pages, or ring and state")
+        if pages is not None:
+            _count(pages, "pages", 0)
+            ring = torch.arange(pages, dtype=torch.int32).to(device)
+            state = torch.tensor([0, pages], dtype=torch.int32).to(device)
+        if not isinstance(ring, _Tensor) or ring.dim() != 1:
+            raise ValueError("ring must be a tensor [places]")
+        self.index = max(ring.get_device(), 0)
+        _dense(ring, "ring", torch.int32, ring.shape, self.index)
+        _dense(state, "state", torch.int32, (2,), self.index)
+        self.ring, self.state = ring, state
+
+
+def gemv_kv_assign(cache: PagedKV, pool: PagePool, lengths, fresh, starts=None, slots=None, seq=None, shared=None,
+                   lengths_out=None, state_out=None, tokens: Optional[int] = None, stream=None):
+    """A step's pages and slots from the lengths of its requests; returns (starts, slots, seq).
+
+    lengths: int32 [batch], the slots that each request has in use; fresh: int32
+    [batch], its new tokens in this step, negative for a request that is over.
+    Requests that need pages take them from the pool in their order, into the
+    cache's page table; one whose pages are not there waits, as do those behind it
+    that need some.  The pages of those that are over go back to the pool, but
+    for the whole pages of their first ``shared`` slots (int32 [batch]).
+    starts: int32 [batch + 1], where each request's tokens begin; slots and seq:
+    int32 [tokens], each token's slot and request, as ``gemv_rope_append`` takes
+    them, -1 and 0 behind the last one (``tokens`` sizes new ones).  lengths
+    becomes the slots in use afterwards, or with ``lengths_out`` these go there;
+    so does the pool's state with ``state_out``."""
+    if seq is not None and _quick.assign(cache._at, cache.index, pool.ring, pool.state, lengths, fresh, starts, slots, seq,
+                                         shared, lengths_out, state_out,
+                                         stream if stream is None else _mbg._stream_ptr(stream)) == 0:
+        return starts, slots, seq
+    index, batch = cache.index, (cache.batch,)
+    if pool.index != index:
+        raise ValueError(f"the pool is on {pool.ring.device}, expected {cache.device}")
+    n_ptr = _dense(lengths, "lengths", torch.int32, batch, index)
+    f_ptr = _dense(fresh, "fresh", torch.int32, batch, index)
+    h_ptr = 0 if shared is None else _dense(shared, "shared", torch.int32, batch, index)
+    no_ptr = n_ptr if lengths_out is None else _dense(lengths_out, "lengths_out", torch.int32, batch, index)
+    so_ptr = pool.state.data_ptr() if state_out is None else _dense(state_out, "state_out", torch.int32, (2,), index)
+    if slots is not None:
+        if not isinstance(slots, _Tensor) or slots.dim() != 1:
+            raise ValueError("slots must be a tensor [tokens]")
+        if tokens is not None and tokens != slots.shape[0]:
+            raise ValueError(f"slots has room for {slots.shape[0]} tokens, expected {tokens}")
+        tokens = slots.shape[0]
+    elif tokens is None:
+        raise ValueError("slots or tokens is needed")
+    _count(tokens, "tokens", 0)
+    with _on(stream):
+        if starts is None:
+            starts = torch.empty(cache.batch + 1, dtype=torch.int32, device=cache.device)
+        if slots is None:
+            slots = torch.empty(tokens, dtype=torch.int32, device=cache.device)
+        if seq is None:
+            seq = torch.empty(tokens, dtype=torch.int32, device=cache.device)
+    st = cache._lib.gemv_kv_assign(
+        cache._at, _ASSIGN.pack(n_ptr, f_ptr, h_ptr, no_ptr, pool.ring.data_ptr(), pool.ring.shape[0], pool.state.data_ptr(),
+                                so_ptr, _dense(starts, "starts", torch.int32, (cache.batch + 1,), index),
+                                _dense(slots, "slots", torch.int32, (tokens,), index),
+                                _dense(seq, "seq", torch.int32, (tokens,), index), tokens), _mbg._stream_ptr(stream))
+    if st:
+        _mbg._raise(st, "gemv_kv_assign")
+    return starts, slots, seq
 
 
 def _moves(cache, moves, counts):
