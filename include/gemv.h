@@ -457,6 +457,45 @@ size_t gemv_attn_paged_workspace(const gemv_kv_t *kv, int q_heads, int weights);
 uint64_t gemv_capture_id(void *stream);
 
 /*
+ * Attention of the new tokens of a batch: prompts, or parts of them behind what
+ * a sequence has cached already.  Sequence b's tokens are starts[b] ..
+ * starts[b + 1] - 1 of the `tokens` rows of q and out [tokens][q_heads][head_dim];
+ * they are the last of its lengths[b] slots (their keys and values are in the
+ * cache).  The i-th of m attends to the slots t < n with n = lengths[b] - m + i +
+ * 1, with a window to n - window <= t < n and t < sinks.  Rows without weights
+ * are zeros (lse, [tokens][q_heads]: -inf).  Rows of q that no sequence has are
+ * left as they are.  Starts that do not ascend from 0 to tokens, and more new tokens
+ * than slots, are reported as GEMV_ERR_BAD_INDEX; such tokens get zeros or are
+ * left alone.  workspace: gemv_attn_prompt_workspace(...) bytes, 256-byte
+ * aligned; one workspace serves one call at a time, and needs no preparation.
+ */
+typedef struct {
+    gemv_heads_t q, out;
+    const int32_t *starts, *lengths;
+    float *lse;
+    void *workspace;
+    size_t workspace_bytes;
+    int64_t tokens;
+    int32_t q_heads, window, sinks;
+    float scale;
+} gemv_prompt_t;
+gemv_status_t gemv_attn_prompt(const gemv_kv_t *kv, const gemv_prompt_t *args, void *stream);
+size_t gemv_attn_prompt_workspace(const gemv_kv_t *kv, int64_t tokens, int q_heads);
+
+/*
+ * gemv_attn_paged_sinks for a batch whose sequences share their first *prefix
+ * slots (a number on the device): their keys and values are read once for all, by
+ * the first row of the page table, which has to name their pages even where that
+ * sequence is empty.  A sequence shorter than the prefix attends to what it
+ * has of it.  scores_out has to be NULL.  A prefix below 0 or beyond the
+ * capacity is reported as GEMV_ERR_BAD_INDEX and cut off there.  workspace:
+ * gemv_attn_shared_workspace(...) bytes, otherwise as for gemv_attn_paged.
+ */
+gemv_status_t gemv_attn_shared(const gemv_kv_t *kv, const gemv_attn_t *args, const int32_t *prefix, int sinks,
+                               void *stream);
+size_t gemv_attn_shared_workspace(const gemv_kv_t *kv, int q_heads);
+
+/*
  * Eviction by accumulated attention weight, one plan per sequence and cached
  * head.  Of the n = lengths[b] slots the first `keep` (>= 1) stay in this
  * order: protected slots (stamp < sinks, or stamp > newest stamp - recent),

@@ -556,5 +556,6 @@ def build_info() -> str:
 
 
 from .decode import _declare as _declare_decode  # noqa: E402
-from .decode import (PagedKV, PagePool, RopeTable, gemv_attn_paged, gemv_kv_assign, gemv_kv_evict,  # noqa: E402,F401
-                     gemv_kv_evict_apply, gemv_kv_evict_plan, gemv_norm_residual, gemv_rope_append)
+from .decode import (PagedKV, PagePool, RopeTable, gemv_attn_paged, gemv_attn_prompt, gemv_attn_shared,  # noqa: E402,F401
+                     gemv_kv_assign, gemv_kv_evict, gemv_kv_evict_apply, gemv_kv_evict_plan, gemv_norm_residual,
+                     gemv_rope_append)

@@ -153,6 +153,9 @@ __device__ __forceinline__ float exp2_from(float x, float m)
     return exp2_approx(x - (m == -INFINITY ? 0.f : m));
 }
 
+// log2 of the sum of 2^s, -inf for a row without weights.
+__device__ __forceinline__ float lse2_of(float m, float l) { return l > 0.f || l != l ? m + log2f(l) : -INFINITY; }
+
 // 16 bytes of a cached row, read once.  (Asking L2 for the whole 256 bytes
 // around them brings other heads' rows along when a row is shorter: 16 x 32768
 // tokens of four heads of 64 take 115 us then, 92 us without, and rows of 256
@@ -182,13 +185,13 @@ __device__ __forceinline__ uint4 load8(const uint16_t *p, int left)
 }
 
 // The tokens of a sequence that are attended to, and their tiles of TOKENS
-// tokens.  Tile t of the sequence's tiles is tile t of the cache for t <
-// sink_tiles, of which the tokens before `sinks` count, and tile0 + t behind
-// them.  (Sinks and window may meet in one tile of the cache, which is then
-// gone through twice.)
+// tokens.  Tile t of the sequence's tiles is tile begin / TOKENS + t of the
+// cache for t < sink_tiles, of which the tokens before `sinks` count, and tile0
+// + t behind them.  (Sinks and window may meet in one tile of the cache,
+// which is then gone through twice.)
 struct RowSpan {
     int first, len;         // tokens [first, len)
-    int sinks;              // and [0, sinks), sinks < first; or 0
+    int begin, sinks;       // and [begin, sinks), sinks < first; none if sink_tiles is 0
     int sink_tiles;
     int tile0, tiles;       // first / TOKENS - sink_tiles; the tiles' number
 };
@@ -202,9 +205,11 @@ __device__ __forceinline__ RowSpan row_span(const AttnArgs &a, int b)
     if (len > a.kv.capacity) len = static_cast<int>(a.kv.capacity);
     r.len = len;
     r.first = (a.window > 0 && len > a.window) ? len - a.window : 0;
-    if (r.first <= a.sinks) r.first = 0;
-    r.sinks = r.first > 0 ? a.sinks : 0;
-    r.sink_tiles = (r.sinks + TOKENS - 1) / TOKENS;
+    r.begin = 0;
+    if (a.prefix) r.begin = min(max(__ldg(a.prefix), 0), len);
+    if (r.first <= max(a.sinks, r.begin)) r.first = r.begin;
+    r.sinks = r.first > r.begin && a.sinks > r.begin ? a.sinks : r.begin;
+    r.sink_tiles = r.sinks > r.begin ? (r.sinks + TOKENS - 1) / TOKENS - r.begin / TOKENS : 0;
     r.tile0 = r.first / TOKENS - r.sink_tiles;
     r.tiles = len > r.first ? (len + TOKENS - 1) / TOKENS - r.tile0 : 0;
     return r;
@@ -286,7 +291,7 @@ struct Kernel {
     struct Segment {
         int64_t r0;             // where the row begins
         int b, hk, t0, t1;
-        int first, len, sinks, sink_tiles, tile0, tiles;
+        int first, len, begin, sinks, sink_tiles, tile0, tiles;
     };
 
     struct Shared {
@@ -320,11 +325,33 @@ struct Kernel {
         return r;
     }
 
+    // The prefix's O, maximum and denominator of a row.
+    static __device__ __forceinline__ const float *prefix_of(const AttnArgs &a, const Row &r, int head)
+    {
+        return a.pre + (static_cast<int64_t>(r.b) * a.q_heads + r.head0 + head) * (a.kv.dim + 2);
+    }
+
+    // Joins a row's maximum and denominator with its prefix's; what the row's
+    // and the prefix's O are to be multiplied by.
+    static __device__ __forceinline__ void join_prefix(const AttnArgs &a, const Row &r, int head, float &m, float &l,
+                                                       float &own, float &other)
+    {
+        other = 0.f;
+        if (head < r.heads) {
+            const float *pre = prefix_of(a, r, head) + a.kv.dim;
+            const float m2 = __ldcg(pre), l2 = __ldcg(pre + 1), mm = fmaxf(m, m2);
+            own = exp2_from(m, mm);
+            other = exp2_from(m2, mm);
+            l = l * own + l2 * other;
+            m = mm;
+        }
+    }
+
     // Output value pair: fragment register idx of a lane is O[head][d].
     //   idx = ((nt * DC + c) * 4 + i) * 4 + e;  head = nt * 8 + 2t + (e & 1),
     //   d = c * 64 + 8g + 2i + (e >> 1)
     static __device__ void store_out(const AttnArgs &a, const Row &r, int idx0, const float (&o)[4], int lane,
-                                     const float (&inv)[2])
+                                     const float (&inv)[2], const float (&inv_pre)[2])
     {
         const int g = lane >> 2, t = lane & 3;
         const int i = (idx0 >> 2) & 3, c = (idx0 >> 4) % DC, nt = (idx0 >> 4) / DC;
@@ -335,8 +362,14 @@ struct Kernel {
             const int head = nt * 8 + 2 * t + e;
             if (head >= r.heads) continue;
             uint16_t *p = out + (r.head0 + head) * a.o_sh + d;
-            if (d < a.kv.dim) p[0] = Mma<T>::bits(o[e] * inv[e]);
-            if (d + 1 < a.kv.dim) p[1] = Mma<T>::bits(o[e + 2] * inv[e]);
+            float x = o[e] * inv[e], y = o[e + 2] * inv[e];
+            if (a.pre) {
+                const float *pre = prefix_of(a, r, head) + d;
+                if (d < a.kv.dim) x += __ldcg(pre) * inv_pre[e];
+                if (d + 1 < a.kv.dim) y += __ldcg(pre + 1) * inv_pre[e];
+            }
+            if (d < a.kv.dim) p[0] = Mma<T>::bits(x);
+            if (d + 1 < a.kv.dim) p[1] = Mma<T>::bits(y);
         }
     }
 
@@ -345,7 +378,7 @@ struct Kernel {
     // +inf for the weights (every weight is then 2^-inf = 0).
     static __device__ void store_stats(const AttnArgs &a, const Row &r, int head, float m, float l)
     {
-        const float lse2 = l > 0.f || l != l ? m + log2f(l) : -INFINITY;
+        const float lse2 = lse2_of(m, l);
         if (a.scores_out) {
             const int64_t row = static_cast<int64_t>(r.b) * a.kv.kv_heads * a.head_tiles + r.hk;
             a.row_lse[row * kHeads + head] = lse2 == -INFINITY ? INFINITY : lse2;
@@ -354,20 +387,34 @@ struct Kernel {
             a.lse[static_cast<int64_t>(r.b) * a.q_heads + r.head0 + head] = lse2 * 0.69314718055994531f;
     }
 
+    // Rows without tokens: zeros, or what the prefix has.
     static __device__ void empty_rows(const AttnArgs &a)
     {
         for (int b = blockIdx.x; b < a.kv.batch; b += gridDim.x) {
             const int len = __ldg(a.lengths + b);
             if ((len < 0 || len > a.kv.capacity) && threadIdx.x == 0) report_error(a.err, DEVERR_BAD_INDEX);
-            if (len > 0 && a.kv.capacity > 0) continue;
+            if (a.prefix ? row_span<kTokens>(a, b).tiles > 0 : len > 0 && a.kv.capacity > 0) continue;
             uint16_t *out = static_cast<uint16_t *>(a.out) + b * a.o_sb;
+            const float *pre = a.pre ? a.pre + static_cast<int64_t>(b) * a.q_heads * (a.kv.dim + 2) : nullptr;
             for (int i = threadIdx.x; i < a.q_heads * a.kv.dim; i += kThreads) {
-                const int h = i / a.kv.dim;
-                out[h * a.o_sh + (i - h * a.kv.dim)] = 0;
+                const int h = i / a.kv.dim, d = i - h * a.kv.dim;
+                uint16_t v = 0;
+                if (pre) {
+                    const float *p = pre + h * (a.kv.dim + 2);
+                    const float l = __ldcg(p + a.kv.dim + 1);
+                    if (l != 0.f) v = Mma<T>::bits(__ldcg(p + d) / l);
+                }
+                out[h * a.o_sh + d] = v;
             }
             if (a.lse)
-                for (int h = threadIdx.x; h < a.q_heads; h += kThreads)
-                    a.lse[static_cast<int64_t>(b) * a.q_heads + h] = -INFINITY;
+                for (int h = threadIdx.x; h < a.q_heads; h += kThreads) {
+                    float v = -INFINITY;
+                    if (pre) {
+                        const float m = __ldcg(pre + h * (a.kv.dim + 2) + a.kv.dim), l = __ldcg(pre + h * (a.kv.dim + 2) + a.kv.dim + 1);
+                        v = lse2_of(m, l) * 0.69314718055994531f;
+                    }
+                    a.lse[static_cast<int64_t>(b) * a.q_heads + h] = v;
+                }
         }
     }
 
@@ -408,6 +455,7 @@ struct Kernel {
                 out.t1 = static_cast<int>(to - r0 - w.lead);
                 out.first = span.first;
                 out.len = span.len;
+                out.begin = span.begin;
                 out.sinks = span.sinks;
                 out.sink_tiles = span.sink_tiles;
                 out.tile0 = span.tile0;
@@ -463,8 +511,9 @@ struct Kernel {
             const bool sink = tile < s.sink_tiles;
 #pragma unroll
             for (int i = 0; i < MT; ++i)
-                p.t[i] = place_of<WHOLE>(kv, kv.table + s.b * kv.table_stride, (sink ? tile : s.tile0 + tile) * MT + i,
-                                         tile < s.t1, sink ? 0 : s.first, sink ? s.sinks : s.len, a.err);
+                p.t[i] = place_of<WHOLE>(kv, kv.table + s.b * kv.table_stride,
+                                         ((sink ? s.begin / kTokens : s.tile0) + tile) * MT + i, tile < s.t1,
+                                         sink ? s.begin : s.first, sink ? s.sinks : s.len, a.err);
             return p;
         };
         // does token r of a tile count, and its place relative to p's
@@ -606,8 +655,8 @@ struct Kernel {
                 if (a.scores_out) {
                     const int64_t row = static_cast<int64_t>(seg.b) * kv.kv_heads * a.head_tiles + seg.hk;
                     const bool sink = tile < seg.sink_tiles;
-                    const int at0 = (sink ? tile : seg.tile0 + tile) * MT * 16 + g;
-                    const int first = sink ? 0 : seg.first, len = sink ? seg.sinks : seg.len;
+                    const int at0 = ((sink ? seg.begin / kTokens : seg.tile0) + tile) * MT * 16 + g;
+                    const int first = sink ? seg.begin : seg.first, len = sink ? seg.sinks : seg.len;
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -754,13 +803,18 @@ struct Kernel {
                 for (int w = 0; w < kWarps; ++w) v[e] += sh.o[w][i4 * 4 + e][lane];
             }
             if (slot < 0) {
-                float inv[2];
+                float inv[2], inv_pre[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float ll = NT == 1 || nt == 0 ? sum[0][e] : sum[NT - 1][e];
-                    inv[e] = ll == 0.f ? 0.f : Mma<T>::kUnscale / ll;
+                    float ll = NT == 1 || nt == 0 ? sum[0][e] : sum[NT - 1][e], own = 1.f;
+                    if (a.pre) {
+                        float m = NT == 1 || nt == 0 ? top[0][e] : top[NT - 1][e];
+                        join_prefix(a, r, nt * 8 + 2 * (lane & 3) + e, m, ll, own, inv_pre[e]);
+                        inv_pre[e] = ll == 0.f ? 0.f : inv_pre[e] / ll;
+                    }
+                    inv[e] = ll == 0.f ? 0.f : Mma<T>::kUnscale * own / ll;
                 }
-                store_out(a, r, i4 * 4, v, lane, inv);
+                store_out(a, r, i4 * 4, v, lane, inv, inv_pre);
             } else {
                 *reinterpret_cast<float4 *>(mine + (i4 * 32 + lane) * 4) = make_float4(v[0], v[1], v[2], v[3]);
             }
@@ -772,7 +826,9 @@ struct Kernel {
                 for (int e = 0; e < 2; ++e) {
                     const int head = nt * 8 + 2 * lane + e;
                     if (slot < 0) {
-                        store_stats(a, r, head, top[nt][e], sum[nt][e]);
+                        float m = top[nt][e], l = sum[nt][e], own, other;
+                        if (a.pre) join_prefix(a, r, head, m, l, own, other);
+                        store_stats(a, r, head, m, l);
                     } else {
                         mine[kRegs * 32 + head] = top[nt][e];
                         mine[kRegs * 32 + kHeads + head] = sum[nt][e];

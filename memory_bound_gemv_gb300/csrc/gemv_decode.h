@@ -56,6 +56,9 @@ struct AttnArgs {
     float *logits;              // [rows][capacity][logit_heads], log2 units; weights only
     int logit_heads;
     int lead;                   // tiles that a row's beginning counts like
+    // a prefix whose attention is joined to the rows': only slots from *prefix on are read here
+    const int32_t *prefix;      // NULL: none
+    const float *pre;           // [batch * q_heads][dim + 2]: O, the maximum (log2 units) and the denominator
 };
 
 // Launches for one cache type; vec: 16-byte loads are possible; big: one block
@@ -64,6 +67,28 @@ cudaError_t launch_attn_f16(const AttnArgs &a, bool vec, int nt, bool big, int s
 cudaError_t launch_attn_bf16(const AttnArgs &a, bool vec, int nt, bool big, int sm_count, cudaStream_t s);
 cudaError_t launch_attn_weights(const AttnArgs &a, int nt, cudaStream_t s);
 constexpr int kAttnMaxCtas = 512;
+
+// Attention of many tokens over one table row's slots: of the new tokens of
+// each sequence (starts), or of a batch's tokens over the prefix that its
+// sequences share (prefix).
+struct SpanArgs {
+    KvView kv;
+    const void *q;
+    int64_t q_st, q_sh;
+    void *out;
+    int64_t o_st, o_sh;
+    float *lse;                 // [tokens][q_heads] natural log, or NULL
+    float *pre;                 // prefix: [tokens * q_heads][dim + 2], instead of out
+    const int32_t *starts;      // [batch + 1]; NULL: prefix
+    const int32_t *lengths;     // [batch]
+    const int32_t *prefix;
+    int tokens;
+    int q_heads, group;
+    int window, sinks;
+    float scale_log2;
+    unsigned int *err;
+};
+cudaError_t launch_span(const SpanArgs &a, bool vec, int elem, int sm_count, cudaStream_t s);
 
 struct EvictArgs {
     KvView kv;

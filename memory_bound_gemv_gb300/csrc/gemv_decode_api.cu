@@ -116,6 +116,110 @@ AttnPlan attn_plan(const KvView &v, int group, int nt, bool weights)
     return p;
 }
 
+// Workspace of the attention of many tokens.
+struct SpanPlan {
+    size_t pre, total;
+};
+
+SpanPlan span_plan(const KvView &v, int64_t tokens, int q_heads, bool prefix)
+{
+    SpanPlan p;
+    p.pre = 0;
+    p.total = 256;
+    if (prefix) p.total += (static_cast<size_t>(tokens) * q_heads * (v.dim + 2) * 4 + 255) / 256 * 256;
+    return p;
+}
+
+bool too_many_rows(int64_t tokens, int q_heads) { return tokens > INT_MAX / 64 || tokens * q_heads > INT_MAX; }
+
+// prefix: the slots before *prefix are attended to by a launch of their own, whose
+// results stand behind the workspace of the others.
+gemv_status_t attn_paged(const gemv_kv_t *kv, const gemv_attn_t *args, const int32_t *prefix, int sinks, void *stream)
+{
+    AttnArgs a{};
+    gemv_status_t st = view_of(kv, &a.kv);
+    if (st != GEMV_OK) return st;
+    if (!args) return GEMV_ERR_INVALID_VALUE;
+    const gemv_heads_t &q = args->q, &out = args->out;
+    const int q_heads = args->q_heads;
+    if (q_heads < 1 || q_heads % a.kv.kv_heads || args->window < 0 || sinks < 0 || negative(q) || negative(out))
+        return GEMV_ERR_INVALID_VALUE;
+    if (too_many_heads(q_heads, a.kv.dim)) return GEMV_ERR_UNSUPPORTED;
+    if (a.kv.batch == 0) return GEMV_OK;
+    if (!q.data || !args->lengths || !out.data || !args->workspace || (args->scores_out && !kv->scores))
+        return GEMV_ERR_INVALID_VALUE;
+    if (!aligned(q.data, 2) || !aligned(out.data, 2) || !aligned(args->lengths, 4) || !aligned(args->lse, 4) ||
+        !aligned(args->scores_out, 4) || !aligned(args->workspace, 256))
+        return GEMV_ERR_MISALIGNED;
+    const int group = q_heads / a.kv.kv_heads;
+    const bool vec = cache_vec(kv) && aligned(q.data, 16) && mult8(q.stride, 2);
+    const int nt = head_tile(a.kv.dim, group, vec);
+    const AttnPlan p = attn_plan(a.kv, group, nt, args->scores_out != nullptr);
+    if (p.rows > INT_MAX || (prefix && too_many_rows(a.kv.batch, q_heads))) return GEMV_ERR_UNSUPPORTED;
+    const size_t total = prefix ? gemv_attn_shared_workspace(kv, q_heads) : p.total;
+    if (args->workspace_bytes < total || total == 0) return GEMV_ERR_INVALID_VALUE;
+    DecodeDevice dev;
+    if (!decode_device(&dev)) return GEMV_ERR_CUDA;
+    a.q = q.data;
+    a.q_sb = q.stride[0];
+    a.q_sh = q.stride[1];
+    a.out = out.data;
+    a.o_sb = out.stride[0];
+    a.o_sh = out.stride[1];
+    a.lengths = args->lengths;
+    a.lse = args->lse;
+    a.scores_in = kv->scores;
+    a.scores_out = args->scores_out;
+    a.q_heads = q_heads;
+    a.group = group;
+    a.head_tiles = p.head_tiles;
+    a.window = args->window;
+    a.sinks = sinks;
+    a.scale_log2 = args->scale * 1.4426950408889634f;
+    a.err = dev.status;
+    unsigned char *ws = static_cast<unsigned char *>(args->workspace);
+    a.arrived = reinterpret_cast<uint64_t *>(ws);
+    a.part = reinterpret_cast<float *>(ws + p.part);
+    a.part_stride = p.part_stride;
+    a.row_lse = reinterpret_cast<float *>(ws + p.row_lse);
+    a.logits = reinterpret_cast<float *>(ws + p.logits);
+    a.logit_heads = p.logit_heads;
+    // Few rows: one block of all an SM's warps, a third of the parts to join
+    // (8 rows of 131001 tokens of 128: 88.4 us, with blocks of four warps 94.1).
+    // Many rows: blocks of four warps, one joins while the others load (384
+    // rows of 1000 tokens: 39.8 us against 48.2).
+    const bool big = vec && p.rows <= dev.sm_count / 2;
+    // A row's beginning counts like `lead` tiles (48 ragged sequences of up to 6000
+    // tokens with their weights: 111.5 us, 120.4 us with none).
+    a.lead = big ? 16 : 8;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (prefix) {
+        SpanArgs g{};
+        const SpanPlan sp = span_plan(a.kv, a.kv.batch, q_heads, true);
+        unsigned char *mine = ws + (total - sp.total);
+        g.kv = a.kv;
+        g.q = a.q, g.q_st = a.q_sb, g.q_sh = a.q_sh;
+        g.pre = reinterpret_cast<float *>(mine + sp.pre);
+        g.lengths = a.lengths;
+        g.prefix = prefix;
+        g.tokens = a.kv.batch;
+        g.q_heads = q_heads;
+        g.group = group;
+        g.window = args->window;
+        g.sinks = sinks;
+        g.scale_log2 = a.scale_log2;
+        g.err = a.err;
+        const cudaError_t e = launch_span(g, vec, kv->elem, dev.sm_count, s);
+        if (e != cudaSuccess) return decode_cuda_fail(e, GEMV_ERR_LAUNCH);
+        a.prefix = prefix;
+        a.pre = g.pre;
+    }
+    cudaError_t e = kv->elem == GEMV_ELEM_F16 ? launch_attn_f16(a, vec, nt, big, dev.sm_count, s)
+                                              : launch_attn_bf16(a, vec, nt, big, dev.sm_count, s);
+    if (e == cudaSuccess && a.scores_out && a.kv.capacity > 0) e = launch_attn_weights(a, nt, s);
+    return e == cudaSuccess ? GEMV_OK : decode_cuda_fail(e, GEMV_ERR_LAUNCH);
+}
+
 gemv_status_t rope_append(const gemv_kv_t *kv, const gemv_rope_t *r, const gemv_head_norm_t *norm, void *stream)
 {
     RopeArgs a{};
@@ -216,65 +320,65 @@ gemv_status_t gemv_attn_paged(const gemv_kv_t *kv, const gemv_attn_t *args, void
 
 gemv_status_t gemv_attn_paged_sinks(const gemv_kv_t *kv, const gemv_attn_t *args, int sinks, void *stream)
 {
-    AttnArgs a{};
-    gemv_status_t st = view_of(kv, &a.kv);
+    return attn_paged(kv, args, nullptr, sinks, stream);
+}
+
+size_t gemv_attn_shared_workspace(const gemv_kv_t *kv, int q_heads)
+{
+    const size_t own = gemv_attn_paged_workspace(kv, q_heads, 0);
+    KvView v;
+    if (own == 0 || view_of(kv, &v, false) != GEMV_OK || too_many_rows(v.batch, q_heads)) return 0;
+    return own + span_plan(v, v.batch, q_heads, true).total;
+}
+
+gemv_status_t gemv_attn_shared(const gemv_kv_t *kv, const gemv_attn_t *args, const int32_t *prefix, int sinks, void *stream)
+{
+    if (!args || !prefix || args->scores_out) return GEMV_ERR_INVALID_VALUE;
+    if (!aligned(prefix, 4)) return GEMV_ERR_MISALIGNED;
+    return attn_paged(kv, args, prefix, sinks, stream);
+}
+
+size_t gemv_attn_prompt_workspace(const gemv_kv_t *kv, int64_t tokens, int q_heads)
+{
+    KvView v;
+    if (view_of(kv, &v, false) != GEMV_OK || q_heads < 1 || q_heads % v.kv_heads || too_many_heads(q_heads, v.dim) ||
+        tokens < 0 || too_many_rows(tokens, q_heads))
+        return 0;
+    return span_plan(v, tokens, q_heads, false).total;
+}
+
+gemv_status_t gemv_attn_prompt(const gemv_kv_t *kv, const gemv_prompt_t *g, void *stream)
+{
+    SpanArgs a{};
+    const gemv_status_t st = view_of(kv, &a.kv);
     if (st != GEMV_OK) return st;
-    if (!args) return GEMV_ERR_INVALID_VALUE;
-    const gemv_heads_t &q = args->q, &out = args->out;
-    const int q_heads = args->q_heads;
-    if (q_heads < 1 || q_heads % a.kv.kv_heads || args->window < 0 || sinks < 0 || negative(q) || negative(out))
+    if (!g || g->q_heads < 1 || g->q_heads % a.kv.kv_heads || g->tokens < 0 || g->window < 0 || g->sinks < 0 ||
+        negative(g->q) || negative(g->out))
         return GEMV_ERR_INVALID_VALUE;
-    if (too_many_heads(q_heads, a.kv.dim)) return GEMV_ERR_UNSUPPORTED;
-    if (a.kv.batch == 0) return GEMV_OK;
-    if (!q.data || !args->lengths || !out.data || !args->workspace || (args->scores_out && !kv->scores))
-        return GEMV_ERR_INVALID_VALUE;
-    if (!aligned(q.data, 2) || !aligned(out.data, 2) || !aligned(args->lengths, 4) || !aligned(args->lse, 4) ||
-        !aligned(args->scores_out, 4) || !aligned(args->workspace, 256))
+    if (too_many_heads(g->q_heads, a.kv.dim) || too_many_rows(g->tokens, g->q_heads)) return GEMV_ERR_UNSUPPORTED;
+    if (a.kv.batch == 0 || g->tokens == 0) return GEMV_OK;
+    if (!g->q.data || !g->out.data || !g->starts || !g->lengths || !g->workspace) return GEMV_ERR_INVALID_VALUE;
+    if (!aligned(g->q.data, 2) || !aligned(g->out.data, 2) || !aligned(g->starts, 4) || !aligned(g->lengths, 4) ||
+        !aligned(g->lse, 4) || !aligned(g->workspace, 256))
         return GEMV_ERR_MISALIGNED;
-    const int group = q_heads / a.kv.kv_heads;
-    const bool vec = cache_vec(kv) && aligned(q.data, 16) && mult8(q.stride, 2);
-    const int nt = head_tile(a.kv.dim, group, vec);
-    const AttnPlan p = attn_plan(a.kv, group, nt, args->scores_out != nullptr);
-    if (p.rows > INT_MAX) return GEMV_ERR_UNSUPPORTED;
-    if (args->workspace_bytes < p.total) return GEMV_ERR_INVALID_VALUE;
+    const SpanPlan p = span_plan(a.kv, g->tokens, g->q_heads, false);
+    if (g->workspace_bytes < p.total) return GEMV_ERR_INVALID_VALUE;
     DecodeDevice dev;
     if (!decode_device(&dev)) return GEMV_ERR_CUDA;
-    a.q = q.data;
-    a.q_sb = q.stride[0];
-    a.q_sh = q.stride[1];
-    a.out = out.data;
-    a.o_sb = out.stride[0];
-    a.o_sh = out.stride[1];
-    a.lengths = args->lengths;
-    a.lse = args->lse;
-    a.scores_in = kv->scores;
-    a.scores_out = args->scores_out;
-    a.q_heads = q_heads;
-    a.group = group;
-    a.head_tiles = p.head_tiles;
-    a.window = args->window;
-    a.sinks = sinks;
-    a.scale_log2 = args->scale * 1.4426950408889634f;
+    a.q = g->q.data, a.q_st = g->q.stride[0], a.q_sh = g->q.stride[1];
+    a.out = g->out.data, a.o_st = g->out.stride[0], a.o_sh = g->out.stride[1];
+    a.lse = g->lse;
+    a.starts = g->starts;
+    a.lengths = g->lengths;
+    a.tokens = static_cast<int>(g->tokens);
+    a.q_heads = g->q_heads;
+    a.group = g->q_heads / a.kv.kv_heads;
+    a.window = g->window;
+    a.sinks = g->sinks;
+    a.scale_log2 = g->scale * 1.4426950408889634f;
     a.err = dev.status;
-    unsigned char *ws = static_cast<unsigned char *>(args->workspace);
-    a.arrived = reinterpret_cast<uint64_t *>(ws);
-    a.part = reinterpret_cast<float *>(ws + p.part);
-    a.part_stride = p.part_stride;
-    a.row_lse = reinterpret_cast<float *>(ws + p.row_lse);
-    a.logits = reinterpret_cast<float *>(ws + p.logits);
-    a.logit_heads = p.logit_heads;
-    // Few rows: one block of all an SM's warps, a third of the parts to join
-    // (8 rows of 131001 tokens of 128: 88.4 us, with blocks of four warps 94.1).
-    // Many rows: blocks of four warps, one joins while the others load (384
-    // rows of 1000 tokens: 39.8 us against 48.2).
-    const bool big = vec && p.rows <= dev.sm_count / 2;
-    // A row's beginning counts like `lead` tiles (48 ragged sequences of up to 6000
-    // tokens with their weights: 111.5 us, 120.4 us with none).
-    a.lead = big ? 16 : 8;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = kv->elem == GEMV_ELEM_F16 ? launch_attn_f16(a, vec, nt, big, dev.sm_count, s)
-                                              : launch_attn_bf16(a, vec, nt, big, dev.sm_count, s);
-    if (e == cudaSuccess && a.scores_out && a.kv.capacity > 0) e = launch_attn_weights(a, nt, s);
+    const bool vec = cache_vec(kv) && aligned(g->q.data, 16) && mult8(g->q.stride, 2);
+    const cudaError_t e = launch_span(a, vec, kv->elem, dev.sm_count, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GEMV_OK : decode_cuda_fail(e, GEMV_ERR_LAUNCH);
 }
 

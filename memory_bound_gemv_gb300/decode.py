@@ -91,6 +91,8 @@ def _declare(L):
     sig = {
         "gemv_attn_paged": [vp, vp, vp],
         "gemv_attn_paged_sinks": [vp, vp, i32, vp],
+        "gemv_attn_prompt": [vp, vp, vp],
+        "gemv_attn_shared": [vp, vp, vp, i32, vp],
         "gemv_kv_assign": [vp, vp, vp],
         "gemv_rope_append_norm": [vp, vp, vp, vp],
         "gemv_kv_evict_plan": [vp, vp, i32, i32, i32, vp, i64, vp, vp],
@@ -102,8 +104,11 @@ def _declare(L):
         f = getattr(L, name)
         f.argtypes = args
         f.restype = st
-    L.gemv_attn_paged_workspace.argtypes = [vp, i32, i32]
-    L.gemv_attn_paged_workspace.restype = ctypes.c_size_t
+    for name, args in (("gemv_attn_paged_workspace", [vp, i32, i32]), ("gemv_attn_shared_workspace", [vp, i32]),
+                       ("gemv_attn_prompt_workspace", [vp, i64, i32])):
+        f = getattr(L, name)
+        f.argtypes = args
+        f.restype = ctypes.c_size_t
     L.gemv_capture_id.argtypes = [vp]
     L.gemv_capture_id.restype = ctypes.c_uint64
     return L
@@ -113,6 +118,7 @@ def _declare(L):
 _ATTN = struct.Struct("PqqPqqPPPPNiif0q")
 _ROPE = struct.Struct("PqqPqqPqqPqqPqPPPPPiiiiii0q")
 _NORM = struct.Struct("PqiPqiPqiPqiPqiPqiPqiPqiqqffI0q")
+_PROMPT = struct.Struct("PqqPqqPPPPNqiiif0q")
 _HEAD_NORM = struct.Struct("PPiiif0q")
 _ASSIGN = struct.Struct("PPPPPqPPPPPq")
 
@@ -229,22 +235,24 @@ class PagedKV:
         self._workspaces = {}
         self._lib = _mbg.lib()
 
-    def _workspace(self, q_heads, weights, ptr, stream):
+    def _workspace(self, q_heads, weights, ptr, stream, shared=False):
         capture = 0
         if stream is not None or torch.cuda.is_current_stream_capturing():
             capture = self._lib.gemv_capture_id(ptr)
-        key = (ptr, capture, q_heads, weights)
+        key = (ptr, capture, q_heads, weights, shared)
         got = self._workspaces.get(key)
         if got is None:
-            n = max(self._lib.gemv_attn_paged_workspace(self._at, q_heads, 1 if weights else 0), _ATTN_COUNTER_BYTES)
-            shared = (self.index, ptr, capture, n)
+            n = (self._lib.gemv_attn_shared_workspace(self._at, q_heads) if shared else
+                 self._lib.gemv_attn_paged_workspace(self._at, q_heads, 1 if weights else 0))
+            n = max(n, _ATTN_COUNTER_BYTES)
+            same = (self.index, ptr, capture, n)
             with _shared_lock:
-                got = _shared.get(shared)
+                got = _shared.get(same)
                 if got is None:
                     with _on(stream):
                         t = torch.empty(n, dtype=torch.uint8, device=self.device)
                         t[:_ATTN_COUNTER_BYTES].zero_()
-                    got = _shared[shared] = _Workspace(t)
+                    got = _shared[same] = _Workspace(t)
             self._workspaces[key] = got
         return got
 
@@ -362,6 +370,89 @@ def gemv_attn_paged(cache: PagedKV, q, lengths, out=None, scale: Optional[float]
         st = cache._lib.gemv_attn_paged_sinks(cache._at, args, sinks, ptr)
     if st:
         _mbg._raise(st, "gemv_attn_paged")
+    return out
+
+
+def _scale_of(cache, scale):
+    return cache.head_dim ** -0.5 if scale is None else scale
+
+
+def gemv_attn_shared(cache: PagedKV, q, lengths, prefix, out=None, scale: Optional[float] = None, window: int = 0,
+                     sinks: int = 0, lse=None, stream=None):
+    """``gemv_attn_paged`` for sequences that share their first slots, whose keys and values are read once for
+    all; returns out.
+
+    prefix: int32 [1], the number of those slots.  They are looked up by the first row of the page table, which
+    has to name their pages even where its sequence is empty; a sequence shorter than
+    the prefix attends to what it has of it.  The other arguments are those of ``gemv_attn_paged``."""
+    index = cache.index
+    if not isinstance(q, _Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor [batch, q_heads, head_dim]")
+    heads = q.shape[1]
+    shape = (cache.batch, heads, cache.head_dim)
+    qs = _operand(q, "q", cache.dtype, shape, index)
+    if heads < 1 or heads % cache.kv_heads:
+        raise ValueError(f"q has {heads} heads, expected a multiple of {cache.kv_heads}")
+    n_ptr = _dense(lengths, "lengths", torch.int32, (cache.batch,), index)
+    p_ptr = _dense(prefix, "prefix", torch.int32, (1,), index)
+    _count(window, "window", 0)
+    _count(sinks, "sinks", 0)
+    if out is None:
+        with _on(stream):
+            out = torch.empty(shape, dtype=cache.dtype, device=cache.device)
+        os = out.stride()
+    else:
+        os = _operand(out, "out", cache.dtype, shape, index)
+    l_ptr = 0 if lse is None else _dense(lse, "lse", torch.float32, (cache.batch, heads), index)
+    ptr = _mbg._stream_ptr(stream)
+    ws = cache._workspace(heads, False, ptr, stream, shared=True)
+    args = _ATTN.pack(q.data_ptr(), qs[0], qs[1], out.data_ptr(), os[0], os[1], n_ptr, l_ptr, 0, ws[0], ws[1], heads, window,
+                      _scale_of(cache, scale))
+    with ws.lock:
+        st = cache._lib.gemv_attn_shared(cache._at, args, p_ptr, sinks, ptr)
+    if st:
+        _mbg._raise(st, "gemv_attn_shared")
+    return out
+
+
+def gemv_attn_prompt(cache: PagedKV, q, starts, lengths, out=None, scale: Optional[float] = None, window: int = 0,
+                     sinks: int = 0, lse=None, stream=None):
+    """Attention of the new tokens of each sequence, prompts or parts of them, over the cache; returns out.
+
+    q: [tokens, q_heads, head_dim] of the cache's type, any strides with a
+    contiguous last dimension.  starts: int32 [batch + 1]: sequence b's tokens are
+    starts[b] to starts[b + 1] - 1, the last of its lengths[b] slots (int32
+    [batch]; the new tokens' keys and values are in the cache).  Each attends to
+    the slots up to its own, with ``window`` to the last so many of them (0: all)
+    and the first ``sinks``.  ``lse``: float32 [tokens, q_heads] that receives
+    log(sum exp(score)).  Tokens that no sequence has (padding behind the last one)
+    are left as they are in out."""
+    index = cache.index
+    if not isinstance(q, _Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor [tokens, q_heads, head_dim]")
+    tokens, heads = q.shape[:2]
+    shape = (tokens, heads, cache.head_dim)
+    qs = _operand(q, "q", cache.dtype, shape, index)
+    if heads < 1 or heads % cache.kv_heads:
+        raise ValueError(f"q has {heads} heads, expected a multiple of {cache.kv_heads}")
+    s_ptr = _dense(starts, "starts", torch.int32, (cache.batch + 1,), index)
+    n_ptr = _dense(lengths, "lengths", torch.int32, (cache.batch,), index)
+    _count(window, "window", 0)
+    _count(sinks, "sinks", 0)
+    l_ptr = 0 if lse is None else _dense(lse, "lse", torch.float32, (tokens, heads), index)
+    n = cache._lib.gemv_attn_prompt_workspace(cache._at, tokens, heads)
+    with _on(stream):
+        if out is None:
+            out = torch.empty(shape, dtype=cache.dtype, device=cache.device)
+        os = _operand(out, "out", cache.dtype, shape, index)
+        # freed behind the launch, which the stream orders before its next use
+        ws = torch.empty(max(n, 256), dtype=torch.uint8, device=cache.device)
+    st = cache._lib.gemv_attn_prompt(
+        cache._at, _PROMPT.pack(q.data_ptr(), qs[0], qs[1], out.data_ptr(), os[0], os[1], s_ptr, n_ptr, l_ptr,
+                                ws.data_ptr(), ws.numel(), tokens, heads, window, sinks, _scale_of(cache, scale)),
+        _mbg._stream_ptr(stream))
+    if st:
+        _mbg._raise(st, "gemv_attn_prompt")
     return out
 
 

@@ -81,3 +81,54 @@ def test_page_pool():
             mbg.PagePool(device="cpu", **bad)
     with pytest.raises(ValueError, match="CUDA"):
         mbg.PagePool(4, device="cpu")
+
+
+TWO, NEG = (128, 64), (-1, 64)
+
+
+def prompt(at, q=FAKE, qs=TWO, out=FAKE, os=TWO, starts=FAKE, lengths=FAKE, lse=0, ws=FAKE, n=1 << 40, tokens=9, heads=8,
+           window=0, sinks=0):
+    return mbg.lib().gemv_attn_prompt(at, decode._PROMPT.pack(q, *qs, out, *os, starts, lengths, lse, ws, n, tokens, heads,
+                                                              window, sinks, 1.0), None)
+
+
+def test_prompt_refusals(kv):
+    need = mbg.lib().gemv_attn_prompt_workspace(kv(), 9, 8)
+    assert need > 0 and need % 256 == 0
+    for change in (dict(q=0), dict(out=0), dict(starts=0), dict(lengths=0), dict(ws=0), dict(heads=0), dict(heads=7),
+                   dict(window=-1), dict(sinks=-1), dict(tokens=-1), dict(qs=NEG), dict(os=NEG), dict(n=need - 1)):
+        assert prompt(kv(), **change) == mbg.ERR_INVALID_VALUE, change
+    for change in (dict(q=FAKE + 1), dict(out=FAKE + 1), dict(starts=FAKE + 2), dict(lengths=FAKE + 2), dict(lse=FAKE + 2),
+                   dict(ws=FAKE + 16)):
+        assert prompt(kv(), **change) == mbg.ERR_MISALIGNED, change
+    for change in (dict(tokens=2 ** 31), dict(tokens=2 ** 24, heads=2 ** 8), dict(heads=2 ** 25)):
+        assert prompt(kv(), **change) == mbg.ERR_UNSUPPORTED, change
+        assert mbg.lib().gemv_attn_prompt_workspace(kv(), change.get("tokens", 9), change.get("heads", 8)) == 0
+    assert prompt(kv(batch=0)) == prompt(kv(), tokens=0) == mbg.OK
+    assert prompt(kv(elem=0)) == prompt(kv(k=None)) == mbg.ERR_INVALID_VALUE
+    assert prompt(None) == mbg.lib().gemv_attn_prompt(kv(), None, None) == mbg.ERR_INVALID_VALUE
+    assert mbg.lib().gemv_attn_prompt_workspace(None, 9, 8) == mbg.lib().gemv_attn_prompt_workspace(kv(), -1, 8) == 0
+
+
+def shared(at, prefix=FAKE, sinks=0, q=FAKE, lengths=FAKE, heads=8, window=0, sums=0, ws=FAKE, n=1 << 40):
+    args = decode._ATTN.pack(q, *TWO, FAKE, *TWO, lengths, 0, sums, ws, n, heads, window, 1.0)
+    return mbg.lib().gemv_attn_shared(at, args, prefix, sinks, None)
+
+
+def test_shared_refusals(kv):
+    L = mbg.lib()
+    need = L.gemv_attn_shared_workspace(kv(), 8)
+    assert need > L.gemv_attn_paged_workspace(kv(), 8, 0)
+    for change in (dict(prefix=None), dict(sinks=-1), dict(window=-1), dict(heads=7), dict(heads=0), dict(q=0),
+                   dict(lengths=0), dict(ws=0), dict(sums=FAKE), dict(n=need - 1)):
+        assert shared(kv(), **change) == mbg.ERR_INVALID_VALUE, change
+    for change in (dict(prefix=FAKE + 2), dict(q=FAKE + 1), dict(ws=FAKE + 128)):
+        assert shared(kv(), **change) == mbg.ERR_MISALIGNED, change
+    assert shared(kv(batch=0)) == mbg.OK
+    assert shared(kv(batch=65535), heads=2 ** 17) == mbg.ERR_UNSUPPORTED
+    assert L.gemv_attn_shared_workspace(kv(batch=65535), 2 ** 17) == L.gemv_attn_shared_workspace(kv(), 7) == 0
+    assert L.gemv_attn_shared(kv(), None, FAKE, 0, None) == mbg.ERR_INVALID_VALUE
+
+
+def test_prompt_layout_matches():
+    assert decode._PROMPT.size == 2 * 24 + 3 * 8 + 2 * 8 + 8 + 4 * 4
