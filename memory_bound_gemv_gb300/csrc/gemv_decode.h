@@ -68,6 +68,12 @@ cudaError_t launch_attn_bf16(const AttnArgs &a, bool vec, int nt, bool big, int 
 cudaError_t launch_attn_weights(const AttnArgs &a, int nt, cudaStream_t s);
 constexpr int kAttnMaxCtas = 512;
 
+// A part of a block of rows that several CTAs share (tiles 0: none).
+struct SpanInfo {
+    int b, h, row0, t0, t1, tiles;
+};
+constexpr int kSpanMaxCtas = 160;
+
 // Attention of many tokens over one table row's slots: of the new tokens of
 // each sequence (starts), or of a batch's tokens over the prefix that its
 // sequences share (prefix).
@@ -86,8 +92,21 @@ struct SpanArgs {
     int q_heads, group;
     int window, sinks;
     float scale_log2;
+    int out_vec;                // out takes 16-byte stores
     unsigned int *err;
+    // workspace
+    float *part;                // [2 * ctas][part_stride]: per tile of rows O [dim / 4][row][4], m and l [row]
+    int64_t part_stride;
+    SpanInfo *info;             // [2 * ctas]
+    uint8_t *redo;              // [tokens * q_heads]: rows to be computed one by one
 };
+// Rows of a tile of query rows, and how many tiles a block of them has.
+constexpr int kSpanRows = 128;
+constexpr int span_streams(int dim) { return dim <= 128 ? 2 : 1; }
+// Floats of a part.
+constexpr int64_t span_part(int dim) { return static_cast<int64_t>(span_streams(dim)) * kSpanRows * ((dim + 15) / 16 * 16 + 2); }
+cudaError_t launch_tile_f16(const SpanArgs &a, bool vec, int ctas, cudaStream_t s);
+cudaError_t launch_tile_bf16(const SpanArgs &a, bool vec, int ctas, cudaStream_t s);
 cudaError_t launch_span(const SpanArgs &a, bool vec, int elem, int sm_count, cudaStream_t s);
 
 struct EvictArgs {

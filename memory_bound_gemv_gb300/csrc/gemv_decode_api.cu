@@ -116,18 +116,30 @@ AttnPlan attn_plan(const KvView &v, int group, int nt, bool weights)
     return p;
 }
 
-// Workspace of the attention of many tokens.
+// Workspace of the attention of many tokens: offsets and size in bytes.
 struct SpanPlan {
-    size_t pre, total;
+    size_t info, redo, pre, total;
 };
 
 SpanPlan span_plan(const KvView &v, int64_t tokens, int q_heads, bool prefix)
 {
     SpanPlan p;
-    p.pre = 0;
-    p.total = 256;
-    if (prefix) p.total += (static_cast<size_t>(tokens) * q_heads * (v.dim + 2) * 4 + 255) / 256 * 256;
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    const size_t rows = static_cast<size_t>(tokens) * q_heads;
+    p.info = up(static_cast<size_t>(2) * kSpanMaxCtas * span_part(v.dim) * 4);
+    p.redo = p.info + up(2 * kSpanMaxCtas * sizeof(SpanInfo));
+    p.pre = p.redo + up(rows);
+    p.total = p.pre + (prefix ? up(rows * (v.dim + 2) * 4) : 0);
     return p;
+}
+
+void place_span(SpanArgs *a, const SpanPlan &p, void *workspace)
+{
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    a->part = reinterpret_cast<float *>(ws);
+    a->part_stride = span_part(a->kv.dim);
+    a->info = reinterpret_cast<SpanInfo *>(ws + p.info);
+    a->redo = ws + p.redo;
 }
 
 bool too_many_rows(int64_t tokens, int q_heads) { return tokens > INT_MAX / 64 || tokens * q_heads > INT_MAX; }
@@ -198,6 +210,7 @@ gemv_status_t attn_paged(const gemv_kv_t *kv, const gemv_attn_t *args, const int
         const SpanPlan sp = span_plan(a.kv, a.kv.batch, q_heads, true);
         unsigned char *mine = ws + (total - sp.total);
         g.kv = a.kv;
+        place_span(&g, sp, mine);
         g.q = a.q, g.q_st = a.q_sb, g.q_sh = a.q_sh;
         g.pre = reinterpret_cast<float *>(mine + sp.pre);
         g.lengths = a.lengths;
@@ -377,6 +390,8 @@ gemv_status_t gemv_attn_prompt(const gemv_kv_t *kv, const gemv_prompt_t *g, void
     a.sinks = g->sinks;
     a.scale_log2 = g->scale * 1.4426950408889634f;
     a.err = dev.status;
+    a.out_vec = aligned(g->out.data, 16) && mult8(g->out.stride, 2);
+    place_span(&a, p, g->workspace);
     const bool vec = cache_vec(kv) && aligned(g->q.data, 16) && mult8(g->q.stride, 2);
     const cudaError_t e = launch_span(a, vec, kv->elem, dev.sm_count, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GEMV_OK : decode_cuda_fail(e, GEMV_ERR_LAUNCH);

@@ -1,0 +1,933 @@
+// Attention of many tokens on the tensor cores: the new tokens of prompts, and a
+// batch's tokens over the prefix that its sequences share.
+//
+//   S = Q K^T,  P = softmax(scale S),  O = P V
+//
+// for the rows of a cached head: the group's query heads of all tokens of a
+// sequence (or of all sequences, over the prefix), 128 rows to a tile.  A row
+// of 128 slots and head size 128 takes 65536 flop for S and O each and 256 bytes
+// of K and V per slot, which all rows of a block share: from some 250 rows on the
+// products bound it, with fewer the cache's bytes.
+//
+// One pass over the slots: each row keeps a running maximum m and sum l, and O
+// is multiplied by 2^(m - m') when m grows (Milakov & Gimelshein's online
+// softmax) -- here only when it grows by more than kLazy powers of two, so
+// that most tiles leave O alone; P then exceeds 1 by at most that.
+//
+// Work of a block's warps:
+//   warps 0-3, 4-7  two streams of softmax, a thread per row: S from tensor
+//                   memory, P back over it, at the end O;
+//   warps 8-11      K and V, 16 bytes at a time (cp.async) from their pages into
+//                   swizzled shared memory, so that pages of any size, strides and
+//                   unaligned pools take one path;
+//   warp 12         one thread issues the products;
+//   warp 13         looks up what the block does next.
+// While one stream's softmax runs, the other's products do.  The streams are two
+// tiles of rows over the same slots, or with up to 128 rows one tile of
+// rows over even and odd tiles of slots, joined at the end.  (Head sizes above
+// 128: one stream, O takes half of tensor memory.)
+//
+// P enters the value product in two 16-bit parts, 16 bits (bf16) or 22 (f16) of
+// FP32's 24: one part would add an error as large as the output's own rounding,
+// and costs half of the value product's time.  In f16 P is multiplied by
+// 2^11, so that what is small beside the largest weight is kept down to 2^-35 of it.
+//
+// Blocks of rows are cut between the CTAs: all tiles of a call are numbered and
+// each CTA takes an equal share of consecutive ones, whatever the lengths (read
+// on the device).  A block inside one share is written at once, others
+// leave (O, m, l) in the workspace for a second launch, in a fixed order.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include <atomic>
+#include <type_traits>
+
+#include "gemv_decode.h"
+#include "gemv_device.cuh"
+#include "gemv_span.cuh"
+#include "gemv_tcgen05.cuh"
+
+namespace mbg {
+namespace tile {
+
+constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr int kThreads = 512, kRows = 128;
+constexpr uint64_t kWaitNs = 1000000000ull;
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// DC: head sizes up to 64 DC.
+template <int DC>
+struct Shape {
+    static constexpr int kStreams = DC <= 2 ? 2 : 1;
+    static constexpr int kTok = DC <= 2 ? 128 : 64;  // slots of a tile
+    static constexpr int kQBytes = kRows * DC * 128; // a tile of rows
+    static constexpr int kKvBytes = kTok * DC * 128;
+    static constexpr int kStages = DC == 1 ? 4 : DC == 3 ? 3 : 2;  // tiles of K, and of V, in shared memory
+    static constexpr int kBlock = kStreams * kRows;  // rows of a block
+    static constexpr int kOColumn = 256;
+};
+
+// A block of rows and its tiles of slots: tile j is tile j of the sequence for
+// j < sink_tiles, and tile j + skip behind them.
+struct Block {
+    int tiles, sink_tiles, skip;
+    int lo, hi, sinks;  // some row sees [lo, hi) and, before hi, [0, sinks)
+    int rows;
+};
+
+// What a CTA does next: tiles [t0, t1) of a block.
+struct Segment {
+    span::Seq seq;
+    Block block;
+    int h, row0;      // cached head, first row among its sequence's
+    int t0, t1;
+    int slot;         // of the part; -1: the whole block
+    int stop;         // nothing is left
+};
+
+struct Limits {
+    int shortest, longest;  // prefix: lengths of the batch
+};
+
+template <int DC>
+__device__ __forceinline__ Block block_of(const SpanArgs &a, const span::Seq &s, int row0, const Limits &lim)
+{
+    constexpr int T = Shape<DC>::kTok;
+    Block k;
+    k.rows = min(Shape<DC>::kBlock, s.m * a.group - row0);
+    if (a.prefix) {
+        k.lo = a.window > 0 && lim.shortest > a.window ? lim.shortest - a.window : 0;
+        k.hi = min(s.n, lim.longest);
+    } else {
+        k.lo = span::seen_by(a, s, row0 / a.group).lo;
+        k.hi = span::seen_by(a, s, (row0 + k.rows - 1) / a.group).hi;
+    }
+    k.sinks = min(a.sinks, k.hi);
+    if (k.lo <= k.sinks) k.lo = k.sinks = 0;
+    k.sink_tiles = (k.sinks + T - 1) / T;
+    const int first = k.lo / T, last = (k.hi + T - 1) / T;
+    if (k.lo >= k.hi) {
+        k.tiles = k.sink_tiles;
+        k.skip = 0;
+    } else if (first < k.sink_tiles) {  // they meet in a tile
+        k.tiles = last;
+        k.sink_tiles = k.skip = 0;
+    } else {
+        k.tiles = k.sink_tiles + last - first;
+        k.skip = first - k.sink_tiles;
+    }
+    return k;
+}
+
+// Costs: a tile of slots takes one unit per tile of rows, a block's beginning
+// and end about kLead.
+constexpr int kLead = 3;
+template <int DC>
+__device__ __forceinline__ int per_tile(const Block &k) { return k.rows > kRows ? 2 : 1; }
+template <int DC>
+__device__ __forceinline__ int cost_of(const Block &k) { return kLead + k.tiles * per_tile<DC>(k); }
+
+template <int DC>
+struct Shared {
+    alignas(8) uint64_t kfull[Shape<DC>::kStages], kempty[Shape<DC>::kStages], vfull[Shape<DC>::kStages], vempty[Shape<DC>::kStages];
+    alignas(8) uint64_t sready[2], pready[2], odone[2], qready, meet, last, segfull[2], segempty[2];
+    uint32_t tmem;
+    int abort;
+    Segment seg[2];
+    Limits lim;
+    // the look-up of the CTA's first block
+    int64_t total;
+    int64_t before;   // cost of what lies before the cursor's block, per cached head
+    int b, row0, found;
+    int64_t warp_sum[16];
+    int ends[kThreads];
+    float join_m[kRows], join_l[kRows];
+};
+
+// One share: [x0, x1) of the call's total.
+struct Share {
+    int64_t x0, x1;
+    int near;  // cuts that leave so few tiles of a block move to its end
+};
+
+template <typename T, int DC, bool VEC>
+struct Kernel {
+    using S = Shape<DC>;
+    static constexpr bool kBf16 = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value;
+    static constexpr int kTok = S::kTok;
+    // P is at most 2^kLazy times kUp: in f16 below 2^16
+    static constexpr float kLazy = kBf16 ? 8.f : 4.f, kUp = kBf16 ? 0.f : 11.f;
+
+    static __device__ __forceinline__ bool wait(Shared<DC> &sh, uint64_t &bar, uint32_t parity, const SpanArgs &a)
+    {
+        if (mbar_wait_bounded(smem_addr(&bar), parity, kWaitNs)) return true;
+        report_error(a.err, DEVERR_TIMEOUT);
+        sh.abort = 1;
+        return false;
+    }
+
+    // Sum over the block up to and with this thread's value.
+    static __device__ int64_t scan(Shared<DC> &sh, int64_t v, int64_t *all)
+    {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+        for (int x = 1; x < 32; x *= 2) {
+            const int64_t u = __shfl_up_sync(kFull, v, x);
+            if (lane >= x) v += u;
+        }
+        __syncthreads();
+        if (lane == 31) sh.warp_sum[warp] = v;
+        __syncthreads();
+        int64_t before = 0, sum = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += sh.warp_sum[w];
+            sum += sh.warp_sum[w];
+        }
+        *all = sum;
+        return before + v;
+    }
+
+    // All blocks of rows in order, kThreads at a time: f(sequence, first row,
+    // block, cost of the blocks before) is called by one thread for each.
+    // Returns their cost together.
+    template <typename F>
+    static __device__ int64_t for_blocks(const SpanArgs &a, Shared<DC> &sh, F f)
+    {
+        const int batch = a.prefix ? 1 : a.kv.batch, tid = threadIdx.x;
+        int64_t before = 0;
+        for (int b0 = 0; b0 < batch; b0 += kThreads) {
+            int64_t blocks = 0, all = 0;
+            if (b0 + tid < batch) blocks = (static_cast<int64_t>(span::seq_of(a, b0 + tid, false).m) * a.group + S::kBlock - 1) / S::kBlock;
+            const int64_t end = scan(sh, blocks, &all);
+            sh.ends[tid] = static_cast<int>(end);
+            __syncthreads();
+            for (int64_t i0 = 0; i0 < all; i0 += kThreads) {
+                const int64_t i = i0 + tid;
+                int cost = 0;
+                span::Seq s;
+                Block k;
+                int row0 = 0;
+                if (i < all) {
+                    int lo = 0, hi = kThreads - 1;  // the first whose end lies above i
+                    while (lo < hi) {
+                        const int mid = (lo + hi) >> 1;
+                        if (sh.ends[mid] > i)
+                            hi = mid;
+                        else
+                            lo = mid + 1;
+                    }
+                    row0 = static_cast<int>(i - (lo ? sh.ends[lo - 1] : 0)) * S::kBlock;
+                    s = span::seq_of(a, b0 + lo, false);
+                    k = block_of<DC>(a, s, row0, sh.lim);
+                    cost = cost_of<DC>(k);
+                }
+                int64_t sum;
+                const int64_t to = scan(sh, cost, &sum);
+                if (i < all) f(s, row0, k, before + to - cost);
+                before += sum;
+            }
+            __syncthreads();
+        }
+        return before;
+    }
+
+    // The tile before which a block that begins at r0 is cut at x.
+    static __device__ __forceinline__ int cut(const Block &k, int64_t r0, int64_t x, int near)
+    {
+        if (x <= r0) return 0;
+        const int64_t t = (x - r0 - kLead) / per_tile<DC>(k);
+        if (t <= near) return x >= r0 + cost_of<DC>(k) ? k.tiles : 0;
+        return k.tiles - t <= near ? k.tiles : static_cast<int>(t);
+    }
+
+    // Looks up the CTA's next segment (one thread).
+    static __device__ void advance(const SpanArgs &a, const Shared<DC> &sh, const Share &w, int64_t &before, int &b, int &row0,
+                                   int &h, Segment &out)
+    {
+        const int batch = a.prefix ? 1 : a.kv.batch;
+        while (b < batch) {
+            const span::Seq s = span::seq_of(a, b, false);
+            if (row0 >= s.m * a.group) {
+                ++b;
+                row0 = h = 0;
+                continue;
+            }
+            const Block k = block_of<DC>(a, s, row0, sh.lim);
+            const int cost = cost_of<DC>(k);
+            const int64_t r0 = before * a.kv.kv_heads + static_cast<int64_t>(h) * cost;
+            if (r0 >= w.x1) break;
+            const int t0 = cut(k, r0, w.x0, w.near), t1 = cut(k, r0, w.x1, w.near);
+            out.seq = s;
+            out.block = k;
+            out.h = h;
+            out.row0 = row0;
+            out.t0 = t0;
+            out.t1 = t1;
+            if (++h == a.kv.kv_heads) {
+                h = 0;
+                row0 += S::kBlock;
+                before += cost;
+            }
+            // (a block without slots is its beginning's)
+            if (t0 < t1 || (k.tiles == 0 && r0 >= w.x0)) {
+                out.slot = t0 == 0 && t1 == k.tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (t0 == 0 ? 1 : 0);
+                out.stop = 0;
+                return;
+            }
+        }
+        b = batch;
+        out.stop = 1;
+    }
+
+    // ---------------------------------------------------------------- loading
+
+    static __device__ __forceinline__ uint32_t swizzled(int rows, int row, int chunk)
+    {
+        return static_cast<uint32_t>((chunk >> 3) * rows * 128 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+    }
+
+    static __device__ __forceinline__ uint4 load8(const uint16_t *p, int left)
+    {
+        if (VEC) return left > 0 ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0);
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = 2 * i < left ? p[2 * i] : 0, hi = 2 * i + 1 < left ? p[2 * i + 1] : 0;
+            w[i] = lo | hi << 16;
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+
+    static __device__ __forceinline__ void st_shared(uint32_t addr, uint4 v)
+    {
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+    }
+
+    // One tile of K or V: this warp's quarter of its slots, whose rows begin at
+    // `row` (a lane each; -1: zeros).
+    static __device__ __forceinline__ void load_tile(uint32_t dst, const uint16_t *base, int64_t row, int dim, int warp, int lane)
+    {
+        constexpr int kOwn = kTok / 4;                            // slots of a warp
+        constexpr int kLanes = DC == 1 ? 8 : DC == 2 ? 16 : 32;   // of a slot
+        constexpr int kAtOnce = 32 / kLanes;
+        const int chunk = lane % kLanes, sub = lane / kLanes;
+#pragma unroll 4
+        for (int i = 0; i < kOwn; i += kAtOnce) {
+            const int own = i + sub;
+            const int64_t at = __shfl_sync(kFull, row, own);
+            if (chunk >= DC * 8) continue;
+            const int left = at >= 0 ? dim - chunk * 8 : 0;
+            const uint32_t to = dst + swizzled(kTok, warp * kOwn + own, chunk);
+            const uint16_t *from = base + (left > 0 ? at + chunk * 8 : 0);
+            if (VEC) {
+                asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(left > 0 ? 16 : 0)
+                             : "memory");
+            } else {
+                st_shared(to, left > 0 ? load8(from, left) : make_uint4(0, 0, 0, 0));
+            }
+        }
+    }
+
+    static __device__ void loader(const SpanArgs &a, Shared<DC> &sh, uint32_t ks, uint32_t vs)
+    {
+        const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 8;
+        const KvView &kv = a.kv;
+        constexpr int kOwn = kTok / 4;
+        // loads not yet announced: the barriers of the last two
+        uint64_t *pending[2] = {nullptr, nullptr};
+        auto announce = [&](uint64_t *bar) {
+            tc::fence_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(bar));
+        };
+        auto drain = [&]() {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            for (int i = 0; i < 2; ++i) {
+                if (pending[i]) announce(pending[i]);
+                pending[i] = nullptr;
+            }
+        };
+        auto issued = [&](uint64_t *bar) {
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (pending[0]) {
+                asm volatile("cp.async.wait_group 2;" ::: "memory");
+                announce(pending[0]);
+            }
+            pending[0] = pending[1];
+            pending[1] = bar;
+        };
+        // A place of the ring is free; what is pending goes out before a wait.
+        auto free_place = [&](uint64_t &bar, uint32_t parity) {
+            uint32_t done;
+            asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                         : "=r"(done)
+                         : "r"(smem_addr(&bar)), "r"(parity)
+                         : "memory");
+            if (__all_sync(kFull, done)) return true;
+            drain();
+            return static_cast<bool>(__all_sync(kFull, wait(sh, bar, parity, a)));
+        };
+        uint32_t nk = 0, nv = 0;
+        for (uint32_t n = 0;; ++n) {
+            drain_if_idle(sh, n, drain);
+            if (!__all_sync(kFull, wait(sh, sh.segfull[n & 1], n >> 1 & 1, a))) break;
+            const Segment &g = sh.seg[n & 1];
+            if (g.stop) break;
+            const int32_t *table = kv.table + g.seq.b * kv.table_stride;
+            const int t0 = g.t0, t1 = g.t1, sink_tiles = g.block.sink_tiles, skip = g.block.skip;
+            const int lo = g.block.lo, hi = g.block.hi, sinks = g.block.sinks;
+            const uint16_t *kb = static_cast<const uint16_t *>(kv.k) + g.h * kv.ks_head;
+            const uint16_t *vb = static_cast<const uint16_t *>(kv.v) + g.h * kv.vs_head;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.segempty[n & 1]));
+            bool ok = true;
+            // this lane's slot of a tile: its page (-1: none) and place there
+            auto look_up = [&](int j, int &off) {
+                const int slot = (j < sink_tiles ? j : j + skip) * kTok + warp * kOwn + lane;
+                int page = -1;
+                off = 0;
+                if (j < t1 && lane < kOwn && slot < hi && (slot >= lo || slot < sinks)) {
+                    const int idx = kv.page_shift >= 0 ? slot >> kv.page_shift : slot / kv.page_size;
+                    off = slot - idx * kv.page_size;
+                    page = __ldg(table + idx);
+                }
+                return page;
+            };
+            auto checked = [&](int page) {
+                if (page < -1 || page >= kv.num_pages) page = -1;
+                return page;
+            };
+            auto report = [&](int j, int page, int off) {
+                const int slot = (j < sink_tiles ? j : j + skip) * kTok + warp * kOwn + lane;
+                if (j < t1 && lane < kOwn && slot < hi && (slot >= lo || slot < sinks) && (page < 0 || page >= kv.num_pages))
+                    report_error(a.err, DEVERR_BAD_INDEX);
+            };
+            int off_k = 0, off_v = 0, page_v = -1;
+            int page_k = look_up(t0, off_k);
+            report(t0, page_k, off_k);
+            page_k = checked(page_k);
+            for (int j = t0; j <= t1 && ok; ++j) {  // K of tile j, then V of tile j - 1
+                int off_next = 0, page_next = -1;
+                if (j < t1) {
+                    page_next = look_up(j + 1, off_next);
+                    const int st = nk % S::kStages;
+                    ok = free_place(sh.kempty[st], (nk / S::kStages & 1) ^ 1);
+                    if (!ok) break;
+                    load_tile(ks + st * S::kKvBytes, kb, page_k < 0 ? -1 : page_k * kv.ks_page + off_k * kv.ks_tok, kv.dim, warp, lane);
+                    issued(&sh.kfull[st]);
+                    ++nk;
+                }
+                if (j > t0) {
+                    const int st = nv % S::kStages;
+                    ok = free_place(sh.vempty[st], (nv / S::kStages & 1) ^ 1);
+                    if (!ok) break;
+                    load_tile(vs + st * S::kKvBytes, vb, page_v < 0 ? -1 : page_v * kv.vs_page + off_v * kv.vs_tok, kv.dim, warp, lane);
+                    issued(&sh.vfull[st]);
+                    ++nv;
+                }
+                page_v = page_k;
+                off_v = off_k;
+                report(j + 1, page_next, off_next);
+                page_k = checked(page_next);
+                off_k = off_next;
+            }
+            if (!ok) break;
+        }
+        drain();
+    }
+
+    // Before the first wait for a segment nothing is pending; later, what is
+    // pending goes out unless the next segment is there already.
+    template <typename F>
+    static __device__ __forceinline__ void drain_if_idle(Shared<DC> &sh, uint32_t n, F drain)
+    {
+        uint32_t done;
+        asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                     : "=r"(done)
+                     : "r"(smem_addr(&sh.segfull[n & 1])), "r"(n >> 1 & 1)
+                     : "memory");
+        if (!__all_sync(kFull, done)) drain();
+    }
+
+    // --------------------------------------------------------------- products
+
+    // One thread issues all products; none is under way when it leaves.
+    static __device__ void products(const SpanArgs &a, Shared<DC> &sh, uint32_t qs, uint32_t ks, uint32_t vs)
+    {
+        issue(a, sh, qs, ks, vs);
+        tc::commit(smem_addr(&sh.last));
+        wait(sh, sh.last, 0, a);
+    }
+
+    static __device__ void issue(const SpanArgs &a, Shared<DC> &sh, uint32_t qs, uint32_t ks, uint32_t vs)
+    {
+        const uint32_t tmem = sh.tmem;
+        const int k16 = (a.kv.dim + 15) / 16;
+        const uint32_t s_instr = tc::instruction<kBf16>(kTok, false), o_instr = tc::instruction<kBf16>(k16 * 16, true);
+        uint32_t nk = 0, nv = 0, nq = 0, np[2] = {0, 0};
+        for (uint32_t n = 0;; ++n) {
+            if (!wait(sh, sh.segfull[n & 1], n >> 1 & 1, a)) return;
+            const Segment &g = sh.seg[n & 1];
+            if (g.stop) return;
+            const int tiles = g.t1 - g.t0;
+            const bool both = g.block.rows > kRows;
+            mbar_arrive(smem_addr(&sh.segempty[n & 1]));
+            if (tiles == 0) continue;
+            if (!wait(sh, sh.qready, nq++ & 1, a)) return;
+            tc::fence_after();
+            const int steps = both ? 2 * tiles : tiles;
+            auto scores = [&](int s) {
+                const int w = s % S::kStreams, st = nk % S::kStages;
+                if ((!both || w == 0) && !wait(sh, sh.kfull[st], nk / S::kStages & 1, a)) return false;
+                tc::fence_after();
+                const uint32_t q = qs + (both ? w * S::kQBytes : 0), k = ks + st * S::kKvBytes;
+                for (int i = 0; i < k16; ++i) {
+                    const uint32_t in = (i & 3) * 32;
+                    tc::mma_ss(tmem + w * kTok, tc::descriptor(q + (i >> 2) * (kRows * 128) + in, 16),
+                               tc::descriptor(k + (i >> 2) * (kTok * 128) + in, 16), s_instr, i > 0);
+                }
+                tc::commit(smem_addr(&sh.sready[w]));
+                if (!both || w == 1) {
+                    tc::commit(smem_addr(&sh.kempty[st]));
+                    ++nk;
+                }
+                return true;
+            };
+            bool ok = true;
+            for (int s = 0; s < S::kStreams && s < steps && ok; ++s) ok = scores(s);
+            for (int s = 0; s < steps && ok; ++s) {
+                const int w = s % S::kStreams, st = nv % S::kStages;
+                ok = wait(sh, sh.pready[w], np[w]++ & 1, a);
+                if (ok && (!both || w == 0)) ok = wait(sh, sh.vfull[st], nv / S::kStages & 1, a);
+                if (!ok) break;
+                tc::fence_after();
+                const uint32_t v = vs + st * S::kKvBytes, p = tmem + w * kTok, o = tmem + S::kOColumn + w * (DC * 64);
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+                    for (int i = 0; i < kTok / 16; ++i)
+                        tc::mma_ts(o, p + part * (kTok / 2) + i * 8, tc::descriptor(v + i * 2048, kTok * 128), o_instr,
+                                   s >= S::kStreams || part > 0 || i > 0);
+                if (s + S::kStreams >= steps) tc::commit(smem_addr(&sh.odone[w]));
+                if (!both || w == 1) {
+                    tc::commit(smem_addr(&sh.vempty[st]));
+                    ++nv;
+                }
+                if (s + S::kStreams < steps) ok = scores(s + S::kStreams);
+            }
+            if (!ok) return;
+        }
+    }
+
+    // ---------------------------------------------------------------- softmax
+
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi)
+    {
+        uint32_t r;
+        if (kBf16)
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+        else
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+        return r;
+    }
+
+    // Two weights as 16-bit parts whose sum they are, but for the last part's rounding.
+    static __device__ __forceinline__ void split(float p0, float p1, uint32_t &hi, uint32_t &lo)
+    {
+        if (kBf16) {
+            hi = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+            lo = pack(p0 - __uint_as_float(__float_as_uint(p0) & 0xFFFF0000u), p1 - __uint_as_float(__float_as_uint(p1) & 0xFFFF0000u));
+        } else {
+            hi = pack(p0, p1);
+            const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+            lo = pack(p0 - back.x, p1 - back.y);
+        }
+    }
+
+    // Multiplies this warp's rows of O by f.
+    static __device__ __forceinline__ void scale_o(uint32_t o, float f, int dim)
+    {
+        for (int c = 0; c < dim; c += 16) {
+            float x[16];
+            tc::load16(o + c, x);
+            tc::wait_ld();
+            uint32_t y[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(x[i] * f);
+            tc::store16(o + c, y);
+        }
+        tc::wait_st();
+    }
+
+    // The streams' threads meet.
+    static __device__ __forceinline__ bool all_softmax(const SpanArgs &a, Shared<DC> &sh, uint32_t &count)
+    {
+        mbar_arrive(smem_addr(&sh.meet));
+        return __all_sync(kFull, wait(sh, sh.meet, count++ & 1, a));
+    }
+
+    static __device__ void softmax(const SpanArgs &a, Shared<DC> &sh, uint32_t qs, unsigned char *q_generic)
+    {
+        const int stream = threadIdx.x >> 7, row = threadIdx.x & 127, lane = threadIdx.x & 31;
+        const uint32_t tmem = sh.tmem + (static_cast<uint32_t>(row & 96) << 16);
+        const uint32_t s_at = tmem + stream * kTok, o_at = tmem + S::kOColumn + stream * (DC * 64);
+        const KvView &kv = a.kv;
+        uint32_t ns = 0, no = 0, nm = 0;
+        if (stream >= S::kStreams) return;
+        for (uint32_t n = 0;; ++n) {
+            // neither stream runs ahead: Q is one barrier's business
+            if (S::kStreams == 2 && !all_softmax(a, sh, nm)) return;
+            if (!__all_sync(kFull, wait(sh, sh.segfull[n & 1], n >> 1 & 1, a))) return;
+            if (sh.seg[n & 1].stop) return;
+            const Segment g = sh.seg[n & 1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.segempty[n & 1]));
+            const int tiles = g.t1 - g.t0;
+            const bool both = g.block.rows > kRows;
+            // this thread's row: a query head of a token
+            const int r = g.row0 + (both ? stream * kRows : 0) + row;
+            const bool live = r < g.row0 + g.block.rows;
+            const int token = live ? r / a.group : 0, head = g.h * a.group + (live ? r - token * a.group : 0);
+            const uint16_t *q = static_cast<const uint16_t *>(a.q) + (g.seq.q0 + token) * a.q_st + head * a.q_sh;
+            if (tiles > 0 && (both || stream == 0)) {
+                const uint32_t dst = qs + (both ? stream * S::kQBytes : 0), flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+#pragma unroll 4
+                for (int c = 0; c < DC * 8; ++c) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (live && c * 8 < kv.dim) v = load8(q + c * 8, kv.dim - c * 8);
+                    v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+                    st_shared(dst + swizzled(kRows, row, c), v);
+                }
+                tc::fence_smem();
+            }
+            if (tiles > 0) mbar_arrive(smem_addr(&sh.qready));
+            // rows that do not exist see everything, of which nothing is kept
+            span::Seen seen = {0, INT32_MAX};
+            if (live) seen = span::seen_by(a, g.seq, token);
+            const float scale = fabsf(a.scale_log2);
+            float m = -INFINITY, l = 0.f;  // m: what P is relative to, less kUp
+            const int first = both || S::kStreams == 1 ? 0 : stream, step = both || S::kStreams == 1 ? 1 : 2;
+            for (int j = first; j < tiles; j += step) {
+                if (!__all_sync(kFull, wait(sh, sh.sready[stream], ns++ & 1, a))) return;
+                tc::fence_after();
+                float s[kTok];
+#pragma unroll
+                for (int c = 0; c < kTok; c += 32) tc::load32(s_at + c, s + c);
+                tc::wait_ld();
+                const int jj = g.t0 + j, t0 = (jj < g.block.sink_tiles ? jj : jj + g.block.skip) * kTok;
+                const bool clear = t0 + kTok <= seen.hi && (t0 >= seen.lo || t0 + kTok <= a.sinks);
+                if (!__all_sync(kFull, clear)) {
+#pragma unroll
+                    for (int i = 0; i < kTok; ++i)
+                        if (t0 + i >= seen.hi || (t0 + i < seen.lo && t0 + i >= a.sinks)) s[i] = -INFINITY;
+                }
+                float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int i = 4; i < kTok; ++i) top[i & 3] = fmaxf(top[i & 3], s[i]);
+                const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale - kUp;
+                const bool grow = high > m + kLazy || (m == -INFINITY && high != m);
+                if (__any_sync(kFull, grow)) {
+                    const float to = grow ? high : m;
+                    const float f = grow ? exp2_approx(m - (to == -INFINITY ? 0.f : to)) : 1.f;
+                    if (j != first) scale_o(o_at, f, kv.dim);
+                    l *= f;
+                    m = to;
+                }
+                const float ref = m == -INFINITY ? 0.f : m;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < kTok; c += 32) {
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float p0 = exp2_approx(fmaf(s[c + 2 * i], scale, -ref)), p1 = exp2_approx(fmaf(s[c + 2 * i + 1], scale, -ref));
+                        sum[2 * i & 3] += p0;
+                        sum[(2 * i & 3) + 1] += p1;
+                        split(p0, p1, hi[i], lo[i]);
+                    }
+                    tc::store16(s_at + c / 2, hi);
+                    tc::store16(s_at + kTok / 2 + c / 2, lo);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tc::wait_st();
+                tc::fence_before();
+                mbar_arrive(smem_addr(&sh.pready[stream]));
+            }
+            const bool any = first < tiles;
+            if (any && !__all_sync(kFull, wait(sh, sh.odone[stream], no++ & 1, a))) return;
+            tc::fence_after();
+            float own = 1.f, other = 0.f;  // factors of this stream's O and the other's
+            const bool join = !both && S::kStreams == 2 && tiles > 1;
+            float *buf = reinterpret_cast<float *>(q_generic);  // [dim][rows]
+            if (join) {
+                if (!all_softmax(a, sh, nm)) return;  // both streams are done with Q
+                if (stream == 1) {
+                    sh.join_m[row] = m;
+                    sh.join_l[row] = l;
+                    for (int c = 0; c < kv.dim; c += 16) {
+                        float x[16];
+                        tc::load16(o_at + c, x);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (c + i < kv.dim) buf[(c + i) * kRows + row] = x[i];
+                    }
+                }
+                if (!all_softmax(a, sh, nm)) return;
+                if (stream == 0) {
+                    const float m2 = sh.join_m[row], mm = fmaxf(m, m2), base = mm == -INFINITY ? 0.f : mm;
+                    own = exp2_approx(m - base);
+                    other = exp2_approx(m2 - base);
+                    l = l * own + sh.join_l[row] * other;
+                    m = mm;
+                }
+            }
+            if (both || stream == 0) finish(a, g, o_at, any, stream, row, live, token, head, m, l, own, other, join ? buf : nullptr);
+            tc::fence_before();
+            // (the buffer is Q's again once the streams have met for the next segment)
+        }
+    }
+
+    // Writes a row: its output, its part of the prefix, or a part of a cut block.
+    static __device__ __forceinline__ void finish(const SpanArgs &a, const Segment &g, uint32_t o_at, bool any, int stream, int row, bool live,
+                                                  int token, int head, float m, float l, float own, float other, const float *buf)
+    {
+        const int dim = a.kv.dim;
+        const int64_t t = g.seq.q0 + token, index = t * a.q_heads + head;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        float *part = a.part + g.slot * a.part_stride + stream * (a.part_stride / S::kStreams);
+        bool nan = false;
+        for (int c = 0; c < dim; c += 16) {
+            float x[16];
+            __syncwarp();
+            if (any) {
+                tc::load16(o_at + c, x);
+                tc::wait_ld();
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = 0.f;
+            }
+            if (buf) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (c + i < dim) x[i] = x[i] * own + buf[(c + i) * kRows + row] * other;
+            }
+            if (live) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) nan = nan || (c + i < dim && x[i] != x[i]);
+            if (g.slot >= 0) {
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+                    *reinterpret_cast<float4 *>(part + ((c + i) / 4 * kRows + row) * 4) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+            } else if (a.pre) {
+                float *p = a.pre + index * (dim + 2) + c;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (c + i < dim) p[i] = x[i];
+            } else {
+                uint16_t *p = static_cast<uint16_t *>(a.out) + t * a.o_st + head * a.o_sh + c;
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = pack(x[2 * i] * inv, x[2 * i + 1] * inv);
+                if (a.out_vec && c + 16 <= dim) {
+                    reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                    reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (c + i < dim) p[i] = static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16));
+                }
+            }
+            }
+        }
+        __syncwarp();
+        if (!live) return;
+        if (g.slot >= 0) {
+            float *stat = part + (dim + 15) / 16 * 16 * kRows;
+            stat[row] = m;
+            stat[kRows + row] = l;
+            a.redo[index] = 0;  // the join's business
+            return;
+        }
+        // a value that another row of the block sees may be infinite where this row's
+        // weight is 0: such rows are computed again, one by one
+        a.redo[index] = nan && l == l;
+        if (a.pre) {
+            a.pre[index * (dim + 2) + dim] = m;
+            a.pre[index * (dim + 2) + dim + 1] = l;
+        } else if (a.lse) {
+            a.lse[index] = l > 0.f || l != l ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        }
+    }
+
+    static __device__ void run(const SpanArgs &a, unsigned char *raw)
+    {
+        unsigned char *base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+        unsigned char *kgen = base + S::kStreams * S::kQBytes;
+        Shared<DC> &sh = *reinterpret_cast<Shared<DC> *>(kgen + 2 * S::kStages * S::kKvBytes);
+        const uint32_t qs = smem_addr(base), ks = smem_addr(kgen), vs = ks + S::kStages * S::kKvBytes;
+        const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+        if (tid == 0) {
+            for (int i = 0; i < S::kStages; ++i) {
+                mbar_init(smem_addr(&sh.kfull[i]), 4);
+                mbar_init(smem_addr(&sh.vfull[i]), 4);
+                mbar_init(smem_addr(&sh.kempty[i]), 1);
+                mbar_init(smem_addr(&sh.vempty[i]), 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(smem_addr(&sh.sready[i]), 1);
+                mbar_init(smem_addr(&sh.pready[i]), kRows);
+                mbar_init(smem_addr(&sh.odone[i]), 1);
+                mbar_init(smem_addr(&sh.segfull[i]), 1);
+                mbar_init(smem_addr(&sh.segempty[i]), 4 + 1 + 4 * S::kStreams);
+            }
+            mbar_init(smem_addr(&sh.qready), kRows * S::kStreams);
+            mbar_init(smem_addr(&sh.meet), kRows * S::kStreams);
+            mbar_init(smem_addr(&sh.last), 1);
+            sh.abort = 0;
+            sh.lim.shortest = INT32_MAX;
+            sh.lim.longest = 0;
+            sh.found = 0;
+        }
+        if (warp == 0) tc::alloc(smem_addr(&sh.tmem), 512);
+        pdl_trigger();
+        pdl_wait();
+        tc::fence_before();
+        __syncthreads();
+        tc::fence_after();
+        const int batch = a.prefix ? 1 : a.kv.batch;
+        if (blockIdx.x == 0)
+            for (int b = tid; b < batch; b += kThreads) span::seq_of(a, b, true);
+        if (a.prefix) {
+            int lo = INT32_MAX, hi = 0;
+            for (int b = tid; b < a.tokens; b += kThreads) {
+                const int n = min(max(__ldg(a.lengths + b), 0), static_cast<int>(a.kv.capacity));
+                if (n > 0) lo = min(lo, n);  // (an empty sequence sees nothing)
+                hi = max(hi, n);
+            }
+            atomicMin(&sh.lim.shortest, __reduce_min_sync(kFull, lo));
+            atomicMax(&sh.lim.longest, __reduce_max_sync(kFull, hi));
+            __syncthreads();
+        }
+        // the call's work, and where this CTA's share of it begins
+        const int64_t total = for_blocks(a, sh, [](const span::Seq &, int, const Block &, int64_t) {}) * a.kv.kv_heads;
+        const int ctas = gridDim.x, cta = blockIdx.x;
+        Share w;
+        w.x0 = total * cta / ctas;
+        w.x1 = total * (cta + 1) / ctas;
+        const int64_t near = total / ctas / 16;
+        w.near = near > 2 ? 2 : static_cast<int>(near);
+        for_blocks(a, sh, [&](const span::Seq &s, int row0, const Block &k, int64_t before) {
+            const int64_t r0 = before * a.kv.kv_heads, r1 = r0 + static_cast<int64_t>(cost_of<DC>(k)) * a.kv.kv_heads;
+            if (r0 <= w.x0 && w.x0 < r1) {
+                sh.before = before;
+                sh.b = s.b;
+                sh.row0 = row0;
+                sh.found = 1 + static_cast<int>((w.x0 - r0) / cost_of<DC>(k));
+            }
+        });
+        if (tid < 2) a.info[2 * cta + tid].tiles = 0;  // no parts yet
+        __syncthreads();
+        if (warp < 8) {
+            tc::set_registers_up<200>();
+            softmax(a, sh, qs, base);
+        } else if (warp < 12) {
+            tc::set_registers_down<72>();
+            loader(a, sh, ks, vs);
+        } else {
+            tc::set_registers_down<40>();
+            if (warp == 12 && lane == 0) products(a, sh, qs, ks, vs);
+            if (warp == 13 && lane == 0) schedule(a, sh, w);
+        }
+        __syncwarp();
+        tc::fence_before();
+        __syncthreads();
+        tc::fence_after();
+        if (warp == 0) tc::dealloc(sh.tmem, 512);
+    }
+
+    static __device__ void schedule(const SpanArgs &a, Shared<DC> &sh, const Share &w)
+    {
+        int64_t before = sh.before;
+        int b = sh.found && w.x0 < w.x1 ? sh.b : INT32_MAX, row0 = sh.row0, h = sh.found - 1;
+        for (uint32_t n = 0;; ++n) {
+            if (n >= 2 && !wait(sh, sh.segempty[n & 1], (n >> 1 & 1) ^ 1, a)) {
+                sh.seg[n & 1].stop = 1;
+                mbar_arrive(smem_addr(&sh.segfull[n & 1]));
+                return;
+            }
+            Segment &g = sh.seg[n & 1];
+            advance(a, sh, w, before, b, row0, h, g);
+            if (sh.abort) g.stop = 1;
+            if (!g.stop && g.slot >= 0) {
+                SpanInfo &i = a.info[g.slot];
+                i.b = g.seq.b;
+                i.h = g.h;
+                i.row0 = g.row0;
+                i.t0 = g.t0;
+                i.t1 = g.t1;
+                i.tiles = g.block.tiles;
+            }
+            mbar_arrive(smem_addr(&sh.segfull[n & 1]));
+            if (g.stop) return;
+        }
+    }
+};
+
+template <typename T, int DC, bool VEC>
+__global__ void __launch_bounds__(kThreads, 1) mbg_tile_kernel(const __grid_constant__ SpanArgs a)
+{
+    extern __shared__ __align__(1024) unsigned char raw[];
+    Kernel<T, DC, VEC>::run(a, raw);
+}
+
+template <typename T, int DC, bool VEC>
+cudaError_t launch_one(const SpanArgs &a, int ctas, cudaStream_t s)
+{
+    using S = Shape<DC>;
+    constexpr int smem = 1024 + S::kStreams * S::kQBytes + 2 * S::kStages * S::kKvBytes + sizeof(Shared<DC>);
+    static_assert(smem <= 227 * 1024, "");
+    auto fn = mbg_tile_kernel<T, DC, VEC>;
+    static std::atomic<uint64_t> ready{0};  // a bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && !(ready.load(std::memory_order_relaxed) >> (dev & 63) & 1)) {
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess) ready.fetch_or(uint64_t{1} << (dev & 63), std::memory_order_relaxed);
+    }
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, a);
+}
+
+template <typename T>
+cudaError_t launch(const SpanArgs &a, bool vec, int ctas, cudaStream_t s)
+{
+    switch ((a.kv.dim + 63) / 64) {
+    case 1: return vec ? launch_one<T, 1, true>(a, ctas, s) : launch_one<T, 1, false>(a, ctas, s);
+    case 2: return vec ? launch_one<T, 2, true>(a, ctas, s) : launch_one<T, 2, false>(a, ctas, s);
+    case 3: return vec ? launch_one<T, 3, true>(a, ctas, s) : launch_one<T, 3, false>(a, ctas, s);
+    default: return vec ? launch_one<T, 4, true>(a, ctas, s) : launch_one<T, 4, false>(a, ctas, s);
+    }
+}
+
+}  // namespace tile
+}  // namespace mbg

@@ -187,12 +187,17 @@ def test_prompt_scores_that_keep_growing(dtype):
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_prompt_hidden_infinities_leave_no_trace(dtype, dim):
-    """What lies in a token's future or behind its window may be infinite or NaN; what it sees is as in the formula."""
+    """What lies in a token's future or behind its window may be infinite or NaN; what it sees is as in the formula.
+
+    Rows that share a tile with such a value are computed again, each for itself, so that the sums behind their outputs are
+    made in another order: they need not have the bits of the call without it, but both calls are held to the
+    same distance from the formula over what the row sees (the definition has no term for the rest)."""
     fresh, lengths = [200, 40], [260, 1000]
     cache = make_cache(59, lengths, 2, dim, 16, dtype)
     q = normal(60, (240, 4, dim), dtype, 1.0)
     starts, n = ints([0, 200, 240]), ints(lengths)
-    clean = mbg.gemv_attn_prompt(cache, q, starts, n, window=150, sinks=4)
+    ref, tol, _, _ = prompt_reference(cache, q, [0, 200, 240], lengths, dim ** -0.5, 150, 4)
+    close(mbg.gemv_attn_prompt(cache, q, starts, n, window=150, sinks=4), ref, tol)
 
     def place(b, t):
         return int(cache.page_table[b, t // 16]), t % 16
@@ -201,14 +206,16 @@ def test_prompt_hidden_infinities_leave_no_trace(dtype, dim):
         p, o = place(b, t)
         cache.k[p, o], cache.v[p, o] = math.nan if b else 2.0, what
     got = mbg.gemv_attn_prompt(cache, q, starts, n, window=150, sinks=4)
-    assert torch.equal(got[:195], clean[:195])          # slot 255 is token 195's own
+    close(got[:195], ref[:195], tol[:195])               # slot 255 is token 195's own
     assert (got[195:200] == math.inf).all()
-    assert torch.equal(got[200:239], clean[200:239]) and got[239].isnan().all()
+    close(got[200:239], ref[200:239], tol[200:239])
+    assert got[239].isnan().all()
     p, o = place(0, 255)                                 # infinities of both signs: NaN where both are seen
     p2, o2 = place(0, 257)
     cache.v[p, o, :, 3], cache.v[p2, o2, :, 3] = math.inf, -math.inf
     got = mbg.gemv_attn_prompt(cache, q, starts, n, window=150, sinks=4)
-    assert torch.equal(got[:195], clean[:195]) and (got[195:197] == math.inf).all()
+    close(got[:195], ref[:195], tol[:195])
+    assert (got[195:197] == math.inf).all()
     assert got[197:200, :, 3].isnan().all()
     keep = [d for d in range(dim) if d != 3]
     assert (got[197:200][..., keep] == math.inf).all()
@@ -403,16 +410,19 @@ def test_shared_infinities_stay_where_they_are_seen():
     lengths, prefix = [100, 300, 129], 256
     cache = shared_cache(77, lengths, prefix, 1, 128, 16, BF16)
     q, n, pre = normal(8, (3, 4, 128), BF16), ints(lengths), ints([prefix])
-    clean = mbg.gemv_attn_shared(cache, q, n, pre)
+    k, v = rows_of(cache, 0, list(range(100)))
+    ref, tol, _, _ = attend(q[:1], k, v, hidden_of([100], 100, 0, 0), 128 ** -0.5, BF16)
     p = int(cache.page_table[0, 128 // 16])
     cache.v[p, 0] = math.inf  # slot 128: sequences 1 and 2 see it
     got = mbg.gemv_attn_shared(cache, q, n, pre)
-    assert torch.equal(got[0], clean[0]) and (got[1:] == math.inf).all()
+    close(got[:1], ref, tol)  # computed again without the tile: as near to the formula, not the same bits
+    assert (got[1:] == math.inf).all()
     own = int(cache.page_table[1, 290 // 16])
     cache.v[p, 0] = 0.0
     cache.k[own, 290 % 16] = math.nan
     got = mbg.gemv_attn_shared(cache, q, n, pre)
-    assert got[1].isnan().all() and got[2].isfinite().all() and torch.equal(got[0], clean[0])
+    assert got[1].isnan().all() and got[2].isfinite().all()
+    close(got[:1], ref, tol)
 
 
 def test_shared_out_of_range_is_reported():
