@@ -94,6 +94,14 @@ struct Segment {
     int stop;         // nothing is left
 };
 
+// The block, and the cached head, that is looked at next.
+struct Cursor {
+    int64_t before;   // cost of what lies before the block, per cached head
+    int b, row0, h;
+    span::Seq seq;
+    Block block;
+};
+
 struct Limits {
     int shortest, longest;  // prefix: lengths of the batch
 };
@@ -144,11 +152,9 @@ struct Shared {
     int abort;
     Segment seg[2];
     Limits lim;
-    // the look-up of the CTA's first block
-    int64_t total;
-    int64_t before;   // cost of what lies before the cursor's block, per cached head
-    int b, row0, found;
-    int64_t warp_sum[16];
+    Cursor first;     // where the CTA's share begins
+    int found;
+    int64_t warp_sum[2][kThreads / 32];
     int ends[kThreads];
     float join_m[kRows], join_l[kRows];
 };
@@ -175,42 +181,51 @@ struct Kernel {
         return false;
     }
 
-    // Sum over the block up to and with this thread's value.
-    static __device__ int64_t scan(Shared<DC> &sh, int64_t v, int64_t *all)
+    // Sum over the block up to and with this thread's value; one barrier.
+    static __device__ int64_t scan(Shared<DC> &sh, int &turn, int64_t v, int64_t *all)
     {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        int64_t *sums = sh.warp_sum[turn];
+        turn ^= 1;
 #pragma unroll
         for (int x = 1; x < 32; x *= 2) {
             const int64_t u = __shfl_up_sync(kFull, v, x);
             if (lane >= x) v += u;
         }
+        if (lane == 31) sums[warp] = v;
         __syncthreads();
-        if (lane == 31) sh.warp_sum[warp] = v;
-        __syncthreads();
-        int64_t before = 0, sum = 0;
+        int64_t t = lane < kThreads / 32 ? sums[lane] : 0;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += sh.warp_sum[w];
-            sum += sh.warp_sum[w];
+        for (int x = 1; x < kThreads / 32; x *= 2) {
+            const int64_t u = __shfl_up_sync(kFull, t, x);
+            if (lane >= x) t += u;
         }
-        *all = sum;
-        return before + v;
+        *all = __shfl_sync(kFull, t, kThreads / 32 - 1);
+        const int64_t before = __shfl_sync(kFull, t, warp ? warp - 1 : 0);
+        return warp ? before + v : v;
     }
 
     // All blocks of rows in order, kThreads at a time: f(sequence, first row,
     // block, cost of the blocks before) is called by one thread for each.
-    // Returns their cost together.
+    // Returns their cost together; *once: no thread had more than one.
     template <typename F>
-    static __device__ int64_t for_blocks(const SpanArgs &a, Shared<DC> &sh, F f)
+    static __device__ int64_t for_blocks(const SpanArgs &a, Shared<DC> &sh, F f, bool *once)
     {
         const int batch = a.prefix ? 1 : a.kv.batch, tid = threadIdx.x;
         int64_t before = 0;
+        int turn = 0;
+        *once = batch <= kThreads;
         for (int b0 = 0; b0 < batch; b0 += kThreads) {
             int64_t blocks = 0, all = 0;
-            if (b0 + tid < batch) blocks = (static_cast<int64_t>(span::seq_of(a, b0 + tid, false).m) * a.group + S::kBlock - 1) / S::kBlock;
-            const int64_t end = scan(sh, blocks, &all);
+            span::Seq own = {0, 0, 0, 0};
+            if (b0 + tid < batch) {
+                own = span::seq_of(a, b0 + tid, blockIdx.x == 0);
+                blocks = (static_cast<int64_t>(own.m) * a.group + S::kBlock - 1) / S::kBlock;
+            }
+            const int64_t end = scan(sh, turn, blocks, &all);
             sh.ends[tid] = static_cast<int>(end);
             __syncthreads();
+            if (all > kThreads) *once = false;
             for (int64_t i0 = 0; i0 < all; i0 += kThreads) {
                 const int64_t i = i0 + tid;
                 int cost = 0;
@@ -218,7 +233,7 @@ struct Kernel {
                 Block k;
                 int row0 = 0;
                 if (i < all) {
-                    int lo = 0, hi = kThreads - 1;  // the first whose end lies above i
+                    int lo = 0, hi = min(kThreads, batch - b0) - 1;  // the first whose end lies above i
                     while (lo < hi) {
                         const int mid = (lo + hi) >> 1;
                         if (sh.ends[mid] > i)
@@ -232,7 +247,7 @@ struct Kernel {
                     cost = cost_of<DC>(k);
                 }
                 int64_t sum;
-                const int64_t to = scan(sh, cost, &sum);
+                const int64_t to = scan(sh, turn, cost, &sum);
                 if (i < all) f(s, row0, k, before + to - cost);
                 before += sum;
             }
@@ -245,47 +260,46 @@ struct Kernel {
     static __device__ __forceinline__ int cut(const Block &k, int64_t r0, int64_t x, int near)
     {
         if (x <= r0) return 0;
-        const int64_t t = (x - r0 - kLead) / per_tile<DC>(k);
-        if (t <= near) return x >= r0 + cost_of<DC>(k) ? k.tiles : 0;
-        return k.tiles - t <= near ? k.tiles : static_cast<int>(t);
+        if (x >= r0 + cost_of<DC>(k)) return k.tiles;
+        const int t = (static_cast<int>(x - r0) - kLead) >> (per_tile<DC>(k) - 1);
+        return t <= near ? 0 : k.tiles - t <= near ? k.tiles : t;
     }
 
     // Looks up the CTA's next segment (one thread).
-    static __device__ void advance(const SpanArgs &a, const Shared<DC> &sh, const Share &w, int64_t &before, int &b, int &row0,
-                                   int &h, Segment &out)
+    static __device__ void advance(const SpanArgs &a, const Shared<DC> &sh, const Share &w, Cursor &at, Segment &out)
     {
         const int batch = a.prefix ? 1 : a.kv.batch;
-        while (b < batch) {
-            const span::Seq s = span::seq_of(a, b, false);
-            if (row0 >= s.m * a.group) {
-                ++b;
-                row0 = h = 0;
-                continue;
+        while (at.b < batch) {
+            if (at.h == a.kv.kv_heads) {  // the next block
+                at.before += cost_of<DC>(at.block);
+                at.row0 += S::kBlock;
+                at.h = 0;
+                while (at.row0 >= at.seq.m * a.group) {
+                    at.row0 = 0;
+                    if (++at.b >= batch) break;
+                    at.seq = span::seq_of(a, at.b, false);
+                }
+                if (at.b >= batch) break;
+                at.block = block_of<DC>(a, at.seq, at.row0, sh.lim);
             }
-            const Block k = block_of<DC>(a, s, row0, sh.lim);
-            const int cost = cost_of<DC>(k);
-            const int64_t r0 = before * a.kv.kv_heads + static_cast<int64_t>(h) * cost;
+            const Block &k = at.block;
+            const int64_t r0 = at.before * a.kv.kv_heads + static_cast<int64_t>(at.h) * cost_of<DC>(k);
             if (r0 >= w.x1) break;
-            const int t0 = cut(k, r0, w.x0, w.near), t1 = cut(k, r0, w.x1, w.near);
-            out.seq = s;
-            out.block = k;
-            out.h = h;
-            out.row0 = row0;
-            out.t0 = t0;
-            out.t1 = t1;
-            if (++h == a.kv.kv_heads) {
-                h = 0;
-                row0 += S::kBlock;
-                before += cost;
-            }
+            const int t0 = cut(k, r0, w.x0, w.near), t1 = cut(k, r0, w.x1, w.near), h = at.h++;
             // (a block without slots is its beginning's)
             if (t0 < t1 || (k.tiles == 0 && r0 >= w.x0)) {
+                out.seq = at.seq;
+                out.block = k;
+                out.h = h;
+                out.row0 = at.row0;
+                out.t0 = t0;
+                out.t1 = t1;
                 out.slot = t0 == 0 && t1 == k.tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (t0 == 0 ? 1 : 0);
                 out.stop = 0;
                 return;
             }
         }
-        b = batch;
+        at.b = batch;
         out.stop = 1;
     }
 
@@ -343,43 +357,17 @@ struct Kernel {
         const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 8;
         const KvView &kv = a.kv;
         constexpr int kOwn = kTok / 4;
-        // loads not yet announced: the barriers of the last two
-        uint64_t *pending[2] = {nullptr, nullptr};
-        auto announce = [&](uint64_t *bar) {
-            tc::fence_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(bar));
-        };
-        auto drain = [&]() {
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            for (int i = 0; i < 2; ++i) {
-                if (pending[i]) announce(pending[i]);
-                pending[i] = nullptr;
+        // arrives when this thread's copies so far have landed
+        auto issued = [&](uint64_t &bar) {
+            if (VEC) {
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&bar)) : "memory");
+            } else {
+                mbar_arrive(smem_addr(&bar));
             }
         };
-        auto issued = [&](uint64_t *bar) {
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            if (pending[0]) {
-                asm volatile("cp.async.wait_group 2;" ::: "memory");
-                announce(pending[0]);
-            }
-            pending[0] = pending[1];
-            pending[1] = bar;
-        };
-        // A place of the ring is free; what is pending goes out before a wait.
-        auto free_place = [&](uint64_t &bar, uint32_t parity) {
-            uint32_t done;
-            asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-                         : "=r"(done)
-                         : "r"(smem_addr(&bar)), "r"(parity)
-                         : "memory");
-            if (__all_sync(kFull, done)) return true;
-            drain();
-            return static_cast<bool>(__all_sync(kFull, wait(sh, bar, parity, a)));
-        };
+        auto free_place = [&](uint64_t &bar, uint32_t parity) { return static_cast<bool>(__all_sync(kFull, wait(sh, bar, parity, a))); };
         uint32_t nk = 0, nv = 0;
         for (uint32_t n = 0;; ++n) {
-            drain_if_idle(sh, n, drain);
             if (!__all_sync(kFull, wait(sh, sh.segfull[n & 1], n >> 1 & 1, a))) break;
             const Segment &g = sh.seg[n & 1];
             if (g.stop) break;
@@ -424,7 +412,7 @@ struct Kernel {
                     ok = free_place(sh.kempty[st], (nk / S::kStages & 1) ^ 1);
                     if (!ok) break;
                     load_tile(ks + st * S::kKvBytes, kb, page_k < 0 ? -1 : page_k * kv.ks_page + off_k * kv.ks_tok, kv.dim, warp, lane);
-                    issued(&sh.kfull[st]);
+                    issued(sh.kfull[st]);
                     ++nk;
                 }
                 if (j > t0) {
@@ -432,7 +420,7 @@ struct Kernel {
                     ok = free_place(sh.vempty[st], (nv / S::kStages & 1) ^ 1);
                     if (!ok) break;
                     load_tile(vs + st * S::kKvBytes, vb, page_v < 0 ? -1 : page_v * kv.vs_page + off_v * kv.vs_tok, kv.dim, warp, lane);
-                    issued(&sh.vfull[st]);
+                    issued(sh.vfull[st]);
                     ++nv;
                 }
                 page_v = page_k;
@@ -443,20 +431,7 @@ struct Kernel {
             }
             if (!ok) break;
         }
-        drain();
-    }
-
-    // Before the first wait for a segment nothing is pending; later, what is
-    // pending goes out unless the next segment is there already.
-    template <typename F>
-    static __device__ __forceinline__ void drain_if_idle(Shared<DC> &sh, uint32_t n, F drain)
-    {
-        uint32_t done;
-        asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-                     : "=r"(done)
-                     : "r"(smem_addr(&sh.segfull[n & 1])), "r"(n >> 1 & 1)
-                     : "memory");
-        if (!__all_sync(kFull, done)) drain();
+        asm volatile("cp.async.wait_all;" ::: "memory");
     }
 
     // --------------------------------------------------------------- products
@@ -488,7 +463,10 @@ struct Kernel {
             const int steps = both ? 2 * tiles : tiles;
             auto scores = [&](int s) {
                 const int w = s % S::kStreams, st = nk % S::kStages;
-                if ((!both || w == 0) && !wait(sh, sh.kfull[st], nk / S::kStages & 1, a)) return false;
+                if (!both || w == 0) {
+                    if (!wait(sh, sh.kfull[st], nk / S::kStages & 1, a)) return false;
+                    tc::fence_smem();  // what the loaders wrote, for the tensor core
+                }
                 tc::fence_after();
                 const uint32_t q = qs + (both ? w * S::kQBytes : 0), k = ks + st * S::kKvBytes;
                 for (int i = 0; i < k16; ++i) {
@@ -508,7 +486,10 @@ struct Kernel {
             for (int s = 0; s < steps && ok; ++s) {
                 const int w = s % S::kStreams, st = nv % S::kStages;
                 ok = wait(sh, sh.pready[w], np[w]++ & 1, a);
-                if (ok && (!both || w == 0)) ok = wait(sh, sh.vfull[st], nv / S::kStages & 1, a);
+                if (ok && (!both || w == 0)) {
+                    ok = wait(sh, sh.vfull[st], nv / S::kStages & 1, a);
+                    tc::fence_smem();
+                }
                 if (!ok) break;
                 tc::fence_after();
                 const uint32_t v = vs + st * S::kKvBytes, p = tmem + w * kTok, o = tmem + S::kOColumn + w * (DC * 64);
@@ -545,12 +526,43 @@ struct Kernel {
     {
         if (kBf16) {
             hi = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
-            lo = pack(p0 - __uint_as_float(__float_as_uint(p0) & 0xFFFF0000u), p1 - __uint_as_float(__float_as_uint(p1) & 0xFFFF0000u));
+            const float2 rest = apart(add2(two(p0, p1), two(__uint_as_float((__float_as_uint(p0) & 0xFFFF0000u) ^ 0x80000000u),
+                                                            __uint_as_float((__float_as_uint(p1) & 0xFFFF0000u) ^ 0x80000000u))));
+            lo = pack(rest.x, rest.y);
         } else {
             hi = pack(p0, p1);
             const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
             lo = pack(p0 - back.x, p1 - back.y);
         }
+    }
+
+    // The lowest n bits of 32.
+    static __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
+    // Two FP32 operations in one instruction.
+    static __device__ __forceinline__ uint64_t two(float a, float b)
+    {
+        uint64_t r;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+        return r;
+    }
+    static __device__ __forceinline__ float2 apart(uint64_t v)
+    {
+        float2 r;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+        return r;
+    }
+    static __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+    {
+        uint64_t r;
+        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+        return r;
+    }
+    static __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+    {
+        uint64_t r;
+        asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+        return r;
     }
 
     // Multiplies this warp's rows of O by f.
@@ -600,12 +612,20 @@ struct Kernel {
             const uint16_t *q = static_cast<const uint16_t *>(a.q) + (g.seq.q0 + token) * a.q_st + head * a.q_sh;
             if (tiles > 0 && (both || stream == 0)) {
                 const uint32_t dst = qs + (both ? stream * S::kQBytes : 0), flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-#pragma unroll 4
-                for (int c = 0; c < DC * 8; ++c) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (live && c * 8 < kv.dim) v = load8(q + c * 8, kv.dim - c * 8);
-                    v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-                    st_shared(dst + swizzled(kRows, row, c), v);
+                constexpr int kAtOnce = DC % 2 ? 8 : 16;
+#pragma unroll 1
+                for (int c0 = 0; c0 < DC * 8; c0 += kAtOnce) {
+                    uint4 v[kAtOnce];
+#pragma unroll
+                    for (int i = 0; i < kAtOnce; ++i) {
+                        const int c = c0 + i;
+                        v[i] = live && c * 8 < kv.dim ? load8(q + c * 8, kv.dim - c * 8) : make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kAtOnce; ++i) {
+                        v[i].x ^= flip, v[i].y ^= flip, v[i].z ^= flip, v[i].w ^= flip;
+                        st_shared(dst + swizzled(kRows, row, c0 + i), v[i]);
+                    }
                 }
                 tc::fence_smem();
             }
@@ -627,8 +647,12 @@ struct Kernel {
                 const bool clear = t0 + kTok <= seen.hi && (t0 >= seen.lo || t0 + kTok <= a.sinks);
                 if (!__all_sync(kFull, clear)) {
 #pragma unroll
-                    for (int i = 0; i < kTok; ++i)
-                        if (t0 + i >= seen.hi || (t0 + i < seen.lo && t0 + i >= a.sinks)) s[i] = -INFINITY;
+                    for (int c = 0; c < kTok; c += 32) {
+                        const int at = t0 + c;
+                        const uint32_t see = below(seen.hi - at) & (~below(seen.lo - at) | below(a.sinks - at));
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) s[c + i] = see & 1u << i ? s[c + i] : -INFINITY;
+                    }
                 }
                 float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -643,21 +667,23 @@ struct Kernel {
                     m = to;
                 }
                 const float ref = m == -INFINITY ? 0.f : m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t scale2 = two(scale, scale), ref2 = two(-ref, -ref);
+                uint64_t sum[2] = {0, 0};
 #pragma unroll
                 for (int c = 0; c < kTok; c += 32) {
                     uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const float p0 = exp2_approx(fmaf(s[c + 2 * i], scale, -ref)), p1 = exp2_approx(fmaf(s[c + 2 * i + 1], scale, -ref));
-                        sum[2 * i & 3] += p0;
-                        sum[(2 * i & 3) + 1] += p1;
+                        const float2 x = apart(fma2(two(s[c + 2 * i], s[c + 2 * i + 1]), scale2, ref2));
+                        const float p0 = exp2_approx(x.x), p1 = exp2_approx(x.y);
+                        sum[i & 1] = add2(sum[i & 1], two(p0, p1));
                         split(p0, p1, hi[i], lo[i]);
                     }
                     tc::store16(s_at + c / 2, hi);
                     tc::store16(s_at + kTok / 2 + c / 2, lo);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                const float2 sums = apart(add2(sum[0], sum[1]));
+                l += sums.x + sums.y;
                 tc::wait_st();
                 tc::fence_before();
                 mbar_arrive(smem_addr(&sh.pready[stream]));
@@ -778,8 +804,8 @@ struct Kernel {
         const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
         if (tid == 0) {
             for (int i = 0; i < S::kStages; ++i) {
-                mbar_init(smem_addr(&sh.kfull[i]), 4);
-                mbar_init(smem_addr(&sh.vfull[i]), 4);
+                mbar_init(smem_addr(&sh.kfull[i]), 128);
+                mbar_init(smem_addr(&sh.vfull[i]), 128);
                 mbar_init(smem_addr(&sh.kempty[i]), 1);
                 mbar_init(smem_addr(&sh.vempty[i]), 1);
             }
@@ -804,9 +830,6 @@ struct Kernel {
         tc::fence_before();
         __syncthreads();
         tc::fence_after();
-        const int batch = a.prefix ? 1 : a.kv.batch;
-        if (blockIdx.x == 0)
-            for (int b = tid; b < batch; b += kThreads) span::seq_of(a, b, true);
         if (a.prefix) {
             int lo = INT32_MAX, hi = 0;
             for (int b = tid; b < a.tokens; b += kThreads) {
@@ -819,22 +842,41 @@ struct Kernel {
             __syncthreads();
         }
         // the call's work, and where this CTA's share of it begins
-        const int64_t total = for_blocks(a, sh, [](const span::Seq &, int, const Block &, int64_t) {}) * a.kv.kv_heads;
+        Cursor mine;
+        mine.before = -1;
+        auto take = [&](const span::Seq &q, int row0, const Block &k, int64_t before) {
+            mine.before = before;
+            mine.b = q.b;
+            mine.row0 = row0;
+            mine.seq = q;
+            mine.block = k;
+        };
+        bool once, again;
+        const int64_t total = for_blocks(a, sh, take, &once) * a.kv.kv_heads;
         const int ctas = gridDim.x, cta = blockIdx.x;
         Share w;
         w.x0 = total * cta / ctas;
         w.x1 = total * (cta + 1) / ctas;
         const int64_t near = total / ctas / 16;
         w.near = near > 2 ? 2 : static_cast<int>(near);
-        for_blocks(a, sh, [&](const span::Seq &s, int row0, const Block &k, int64_t before) {
-            const int64_t r0 = before * a.kv.kv_heads, r1 = r0 + static_cast<int64_t>(cost_of<DC>(k)) * a.kv.kv_heads;
-            if (r0 <= w.x0 && w.x0 < r1) {
-                sh.before = before;
-                sh.b = s.b;
-                sh.row0 = row0;
-                sh.found = 1 + static_cast<int>((w.x0 - r0) / cost_of<DC>(k));
+        auto find = [&]() {
+            if (mine.before < 0) return;
+            const int64_t r0 = mine.before * a.kv.kv_heads;
+            const int cost = cost_of<DC>(mine.block);
+            if (r0 <= w.x0 && w.x0 < r0 + static_cast<int64_t>(cost) * a.kv.kv_heads) {
+                mine.h = static_cast<int>((w.x0 - r0) / cost);
+                sh.first = mine;
+                sh.found = 1;
             }
-        });
+        };
+        if (once) {
+            find();
+        } else {
+            for_blocks(a, sh, [&](const span::Seq &q, int row0, const Block &k, int64_t before) {
+                take(q, row0, k, before);
+                find();
+            }, &again);
+        }
         if (tid < 2) a.info[2 * cta + tid].tiles = 0;  // no parts yet
         __syncthreads();
         if (warp < 8) {
@@ -857,8 +899,8 @@ struct Kernel {
 
     static __device__ void schedule(const SpanArgs &a, Shared<DC> &sh, const Share &w)
     {
-        int64_t before = sh.before;
-        int b = sh.found && w.x0 < w.x1 ? sh.b : INT32_MAX, row0 = sh.row0, h = sh.found - 1;
+        Cursor at = sh.first;
+        if (!sh.found || w.x0 >= w.x1) at.b = INT32_MAX;
         for (uint32_t n = 0;; ++n) {
             if (n >= 2 && !wait(sh, sh.segempty[n & 1], (n >> 1 & 1) ^ 1, a)) {
                 sh.seg[n & 1].stop = 1;
@@ -866,7 +908,7 @@ struct Kernel {
                 return;
             }
             Segment &g = sh.seg[n & 1];
-            advance(a, sh, w, before, b, row0, h, g);
+            advance(a, sh, w, at, g);
             if (sh.abort) g.stop = 1;
             if (!g.stop && g.slot >= 0) {
                 SpanInfo &i = a.info[g.slot];
