@@ -42,6 +42,20 @@ __device__ __forceinline__ uint64_t descriptor(uint32_t smem, uint32_t chunk)
            static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
 }
 
+// The same operand `bytes` further on (within shared memory: no carry leaves the address).
+__device__ __forceinline__ uint64_t further(uint64_t d, uint32_t bytes)
+{
+    return (d & 0xFFFFFFFF00000000ull) | (static_cast<uint32_t>(d) + (bytes >> 4));
+}
+
+// One thread of a converged warp.
+__device__ __forceinline__ bool elect()
+{
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
+}
+
 // kind::f16 with FP32 accumulators: M = 128 rows, N columns.
 template <bool BF16>
 __device__ __forceinline__ uint32_t instruction(int n, bool b_along_n)

@@ -436,73 +436,85 @@ struct Kernel {
 
     // --------------------------------------------------------------- products
 
-    // One thread issues all products; none is under way when it leaves.
+    // One warp issues all products; none is under way when it leaves.
     static __device__ void products(const SpanArgs &a, Shared<DC> &sh, uint32_t qs, uint32_t ks, uint32_t vs)
     {
         issue(a, sh, qs, ks, vs);
-        tc::commit(smem_addr(&sh.last));
+        __syncwarp();
+        if (tc::elect()) tc::commit(smem_addr(&sh.last));
         wait(sh, sh.last, 0, a);
     }
 
+    static __device__ __forceinline__ bool warp_wait(Shared<DC> &sh, uint64_t &bar, uint32_t parity, const SpanArgs &a)
+    {
+        return __all_sync(kFull, wait(sh, bar, parity, a));
+    }
+
+    // The operands' descriptors differ by constants within a tile, the loops are
+    // unrolled: an instruction of 64 cycles has to be issued in less.
     static __device__ void issue(const SpanArgs &a, Shared<DC> &sh, uint32_t qs, uint32_t ks, uint32_t vs)
     {
         const uint32_t tmem = sh.tmem;
         const int k16 = (a.kv.dim + 15) / 16;
         const uint32_t s_instr = tc::instruction<kBf16>(kTok, false), o_instr = tc::instruction<kBf16>(k16 * 16, true);
+        const bool one = tc::elect();
         uint32_t nk = 0, nv = 0, nq = 0, np[2] = {0, 0};
         for (uint32_t n = 0;; ++n) {
-            if (!wait(sh, sh.segfull[n & 1], n >> 1 & 1, a)) return;
+            if (!warp_wait(sh, sh.segfull[n & 1], n >> 1 & 1, a)) return;
             const Segment &g = sh.seg[n & 1];
             if (g.stop) return;
             const int tiles = g.t1 - g.t0;
             const bool both = g.block.rows > kRows;
-            mbar_arrive(smem_addr(&sh.segempty[n & 1]));
+            __syncwarp();
+            if (one) mbar_arrive(smem_addr(&sh.segempty[n & 1]));
             if (tiles == 0) continue;
-            if (!wait(sh, sh.qready, nq++ & 1, a)) return;
+            if (!warp_wait(sh, sh.qready, nq++ & 1, a)) return;
             tc::fence_after();
             const int steps = both ? 2 * tiles : tiles;
             auto scores = [&](int s) {
                 const int w = s % S::kStreams, st = nk % S::kStages;
                 if (!both || w == 0) {
-                    if (!wait(sh, sh.kfull[st], nk / S::kStages & 1, a)) return false;
+                    if (!warp_wait(sh, sh.kfull[st], nk / S::kStages & 1, a)) return false;
                     tc::fence_smem();  // what the loaders wrote, for the tensor core
                 }
                 tc::fence_after();
-                const uint32_t q = qs + (both ? w * S::kQBytes : 0), k = ks + st * S::kKvBytes;
-                for (int i = 0; i < k16; ++i) {
-                    const uint32_t in = (i & 3) * 32;
-                    tc::mma_ss(tmem + w * kTok, tc::descriptor(q + (i >> 2) * (kRows * 128) + in, 16),
-                               tc::descriptor(k + (i >> 2) * (kTok * 128) + in, 16), s_instr, i > 0);
+                const uint64_t q = tc::descriptor(qs + (both ? w * S::kQBytes : 0), 16), k = tc::descriptor(ks + st * S::kKvBytes, 16);
+                if (one) {
+#pragma unroll
+                    for (int i = 0; i < DC * 4; ++i)
+                        if (i < k16)
+                            tc::mma_ss(tmem + w * kTok, tc::further(q, (i >> 2) * (kRows * 128) + (i & 3) * 32),
+                                       tc::further(k, (i >> 2) * (kTok * 128) + (i & 3) * 32), s_instr, i > 0);
+                    tc::commit(smem_addr(&sh.sready[w]));
+                    if (!both || w == 1) tc::commit(smem_addr(&sh.kempty[st]));
                 }
-                tc::commit(smem_addr(&sh.sready[w]));
-                if (!both || w == 1) {
-                    tc::commit(smem_addr(&sh.kempty[st]));
-                    ++nk;
-                }
+                if (!both || w == 1) ++nk;
                 return true;
             };
             bool ok = true;
             for (int s = 0; s < S::kStreams && s < steps && ok; ++s) ok = scores(s);
             for (int s = 0; s < steps && ok; ++s) {
                 const int w = s % S::kStreams, st = nv % S::kStages;
-                ok = wait(sh, sh.pready[w], np[w]++ & 1, a);
+                ok = warp_wait(sh, sh.pready[w], np[w]++ & 1, a);
                 if (ok && (!both || w == 0)) {
-                    ok = wait(sh, sh.vfull[st], nv / S::kStages & 1, a);
+                    ok = warp_wait(sh, sh.vfull[st], nv / S::kStages & 1, a);
                     tc::fence_smem();
                 }
                 if (!ok) break;
                 tc::fence_after();
-                const uint32_t v = vs + st * S::kKvBytes, p = tmem + w * kTok, o = tmem + S::kOColumn + w * (DC * 64);
+                const uint64_t v = tc::descriptor(vs + st * S::kKvBytes, kTok * 128);
+                const uint32_t p = tmem + w * kTok, o = tmem + S::kOColumn + w * (DC * 64);
+                if (one) {
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
-                    for (int i = 0; i < kTok / 16; ++i)
-                        tc::mma_ts(o, p + part * (kTok / 2) + i * 8, tc::descriptor(v + i * 2048, kTok * 128), o_instr,
-                                   s >= S::kStreams || part > 0 || i > 0);
-                if (s + S::kStreams >= steps) tc::commit(smem_addr(&sh.odone[w]));
-                if (!both || w == 1) {
-                    tc::commit(smem_addr(&sh.vempty[st]));
-                    ++nv;
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int i = 0; i < kTok / 16; ++i)
+                            tc::mma_ts(o, p + part * (kTok / 2) + i * 8, tc::further(v, i * 2048), o_instr,
+                                       s >= S::kStreams || part > 0 || i > 0);
+                    if (s + S::kStreams >= steps) tc::commit(smem_addr(&sh.odone[w]));
+                    if (!both || w == 1) tc::commit(smem_addr(&sh.vempty[st]));
                 }
+                if (!both || w == 1) ++nv;
                 if (s + S::kStreams < steps) ok = scores(s + S::kStreams);
             }
             if (!ok) return;
@@ -887,7 +899,7 @@ struct Kernel {
             loader(a, sh, ks, vs);
         } else {
             tc::set_registers_down<40>();
-            if (warp == 12 && lane == 0) products(a, sh, qs, ks, vs);
+            if (warp == 12) products(a, sh, qs, ks, vs);
             if (warp == 13 && lane == 0) schedule(a, sh, w);
         }
         __syncwarp();
