@@ -325,33 +325,17 @@ struct Kernel {
         return r;
     }
 
-    // The prefix's O, maximum and denominator of a row.
-    static __device__ __forceinline__ const float *prefix_of(const AttnArgs &a, const Row &r, int head)
+    // Where a row's O, maximum and denominator go that are to be joined with its prefix's.
+    static __device__ __forceinline__ float *own_of(const AttnArgs &a, const Row &r, int head)
     {
-        return a.pre + (static_cast<int64_t>(r.b) * a.q_heads + r.head0 + head) * (a.kv.dim + 2);
-    }
-
-    // Joins a row's maximum and denominator with its prefix's; what the row's
-    // and the prefix's O are to be multiplied by.
-    static __device__ __forceinline__ void join_prefix(const AttnArgs &a, const Row &r, int head, float &m, float &l,
-                                                       float &own, float &other)
-    {
-        other = 0.f;
-        if (head < r.heads) {
-            const float *pre = prefix_of(a, r, head) + a.kv.dim;
-            const float m2 = __ldcg(pre), l2 = __ldcg(pre + 1), mm = fmaxf(m, m2);
-            own = exp2_from(m, mm);
-            other = exp2_from(m2, mm);
-            l = l * own + l2 * other;
-            m = mm;
-        }
+        return a.own + (static_cast<int64_t>(r.b) * a.q_heads + r.head0 + head) * span_row(a.kv.dim);
     }
 
     // Output value pair: fragment register idx of a lane is O[head][d].
     //   idx = ((nt * DC + c) * 4 + i) * 4 + e;  head = nt * 8 + 2t + (e & 1),
     //   d = c * 64 + 8g + 2i + (e >> 1)
     static __device__ void store_out(const AttnArgs &a, const Row &r, int idx0, const float (&o)[4], int lane,
-                                     const float (&inv)[2], const float (&inv_pre)[2])
+                                     const float (&inv)[2])
     {
         const int g = lane >> 2, t = lane & 3;
         const int i = (idx0 >> 2) & 3, c = (idx0 >> 4) % DC, nt = (idx0 >> 4) / DC;
@@ -361,15 +345,14 @@ struct Kernel {
         for (int e = 0; e < 2; ++e) {
             const int head = nt * 8 + 2 * t + e;
             if (head >= r.heads) continue;
-            uint16_t *p = out + (r.head0 + head) * a.o_sh + d;
-            float x = o[e] * inv[e], y = o[e + 2] * inv[e];
-            if (a.pre) {
-                const float *pre = prefix_of(a, r, head) + d;
-                if (d < a.kv.dim) x += __ldcg(pre) * inv_pre[e];
-                if (d + 1 < a.kv.dim) y += __ldcg(pre + 1) * inv_pre[e];
+            if (a.own) {  // (d is even, and a row there a multiple of four)
+                if (d < a.kv.dim)
+                    *reinterpret_cast<float2 *>(own_of(a, r, head) + d) = make_float2(o[e] * inv[e], o[e + 2] * inv[e]);
+                continue;
             }
-            if (d < a.kv.dim) p[0] = Mma<T>::bits(x);
-            if (d + 1 < a.kv.dim) p[1] = Mma<T>::bits(y);
+            uint16_t *p = out + (r.head0 + head) * a.o_sh + d;
+            if (d < a.kv.dim) p[0] = Mma<T>::bits(o[e] * inv[e]);
+            if (d + 1 < a.kv.dim) p[1] = Mma<T>::bits(o[e + 2] * inv[e]);
         }
     }
 
@@ -387,34 +370,29 @@ struct Kernel {
             a.lse[static_cast<int64_t>(r.b) * a.q_heads + r.head0 + head] = lse2 * 0.69314718055994531f;
     }
 
-    // Rows without tokens: zeros, or what the prefix has.
     static __device__ void empty_rows(const AttnArgs &a)
     {
         for (int b = blockIdx.x; b < a.kv.batch; b += gridDim.x) {
             const int len = __ldg(a.lengths + b);
             if ((len < 0 || len > a.kv.capacity) && threadIdx.x == 0) report_error(a.err, DEVERR_BAD_INDEX);
-            if (a.prefix ? row_span<kTokens>(a, b).tiles > 0 : len > 0 && a.kv.capacity > 0) continue;
-            uint16_t *out = static_cast<uint16_t *>(a.out) + b * a.o_sb;
-            const float *pre = a.pre ? a.pre + static_cast<int64_t>(b) * a.q_heads * (a.kv.dim + 2) : nullptr;
-            for (int i = threadIdx.x; i < a.q_heads * a.kv.dim; i += kThreads) {
-                const int h = i / a.kv.dim, d = i - h * a.kv.dim;
-                uint16_t v = 0;
-                if (pre) {
-                    const float *p = pre + h * (a.kv.dim + 2);
-                    const float l = __ldcg(p + a.kv.dim + 1);
-                    if (l != 0.f) v = Mma<T>::bits(__ldcg(p + d) / l);
+            if (a.own) {
+                if (row_span<kTokens>(a, b).tiles > 0) continue;
+                for (int h = threadIdx.x; h < a.q_heads; h += kThreads) {
+                    float *stat = a.own + (static_cast<int64_t>(b) * a.q_heads + h) * span_row(a.kv.dim) + span_row(a.kv.dim) - 4;
+                    stat[0] = -INFINITY;
+                    stat[1] = 0.f;
                 }
-                out[h * a.o_sh + d] = v;
+                continue;
+            }
+            if (len > 0 && a.kv.capacity > 0) continue;
+            uint16_t *out = static_cast<uint16_t *>(a.out) + b * a.o_sb;
+            for (int i = threadIdx.x; i < a.q_heads * a.kv.dim; i += kThreads) {
+                const int h = i / a.kv.dim;
+                out[h * a.o_sh + (i - h * a.kv.dim)] = 0;
             }
             if (a.lse)
-                for (int h = threadIdx.x; h < a.q_heads; h += kThreads) {
-                    float v = -INFINITY;
-                    if (pre) {
-                        const float m = __ldcg(pre + h * (a.kv.dim + 2) + a.kv.dim), l = __ldcg(pre + h * (a.kv.dim + 2) + a.kv.dim + 1);
-                        v = lse2_of(m, l) * 0.69314718055994531f;
-                    }
-                    a.lse[static_cast<int64_t>(b) * a.q_heads + h] = v;
-                }
+                for (int h = threadIdx.x; h < a.q_heads; h += kThreads)
+                    a.lse[static_cast<int64_t>(b) * a.q_heads + h] = -INFINITY;
         }
     }
 
@@ -803,18 +781,13 @@ struct Kernel {
                 for (int w = 0; w < kWarps; ++w) v[e] += sh.o[w][i4 * 4 + e][lane];
             }
             if (slot < 0) {
-                float inv[2], inv_pre[2];
+                float inv[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float ll = NT == 1 || nt == 0 ? sum[0][e] : sum[NT - 1][e], own = 1.f;
-                    if (a.pre) {
-                        float m = NT == 1 || nt == 0 ? top[0][e] : top[NT - 1][e];
-                        join_prefix(a, r, nt * 8 + 2 * (lane & 3) + e, m, ll, own, inv_pre[e]);
-                        inv_pre[e] = ll == 0.f ? 0.f : inv_pre[e] / ll;
-                    }
-                    inv[e] = ll == 0.f ? 0.f : Mma<T>::kUnscale * own / ll;
+                    const float ll = NT == 1 || nt == 0 ? sum[0][e] : sum[NT - 1][e];
+                    inv[e] = a.own ? Mma<T>::kUnscale : ll == 0.f ? 0.f : Mma<T>::kUnscale / ll;
                 }
-                store_out(a, r, i4 * 4, v, lane, inv, inv_pre);
+                store_out(a, r, i4 * 4, v, lane, inv);
             } else {
                 *reinterpret_cast<float4 *>(mine + (i4 * 32 + lane) * 4) = make_float4(v[0], v[1], v[2], v[3]);
             }
@@ -826,9 +799,13 @@ struct Kernel {
                 for (int e = 0; e < 2; ++e) {
                     const int head = nt * 8 + 2 * lane + e;
                     if (slot < 0) {
-                        float m = top[nt][e], l = sum[nt][e], own, other;
-                        if (a.pre) join_prefix(a, r, head, m, l, own, other);
-                        store_stats(a, r, head, m, l);
+                        if (!a.own) {
+                            store_stats(a, r, head, top[nt][e], sum[nt][e]);
+                        } else if (head < r.heads) {
+                            float *stat = own_of(a, r, head) + span_row(a.kv.dim) - 4;
+                            stat[0] = top[nt][e];
+                            stat[1] = sum[nt][e];
+                        }
                     } else {
                         mine[kRegs * 32 + head] = top[nt][e];
                         mine[kRegs * 32 + kHeads + head] = sum[nt][e];
@@ -990,7 +967,7 @@ struct Kernel {
     static __device__ void run(const AttnArgs &a, Shared &sh)
     {
         pdl_trigger();
-        pdl_wait();
+        if (!a.own) pdl_wait();
         uint64_t ticket = 0;
         if (threadIdx.x == kTicketThread) ticket = draw_ticket(a);  // needed late
         empty_rows(a);
@@ -1088,6 +1065,10 @@ __global__ void __launch_bounds__(NW * 32, warps_per_sm<DC, NT>() / NW)
     extern __shared__ __align__(16) unsigned char raw[];
     using K = Kernel<T, DC, NT, NW, VEC, WHOLE>;
     K::run(a, *reinterpret_cast<typename K::Shared *>(raw));
+    // The launch before it attends to the prefix, which nothing here depends on;
+    // it starts others only when all before itself are done.  Who waits for this
+    // launch waits for both.
+    if (a.own) pdl_wait();
 }
 
 template <typename T, int DC, int NT, int NW, bool VEC, bool WHOLE>

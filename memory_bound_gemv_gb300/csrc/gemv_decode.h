@@ -56,10 +56,13 @@ struct AttnArgs {
     float *logits;              // [rows][capacity][logit_heads], log2 units; weights only
     int logit_heads;
     int lead;                   // tiles that a row's beginning counts like
-    // a prefix whose attention is joined to the rows': only slots from *prefix on are read here
+    // a prefix that is attended to elsewhere: only slots from *prefix on are read
     const int32_t *prefix;      // NULL: none
-    const float *pre;           // [batch * q_heads][dim + 2]: O, the maximum (log2 units) and the denominator
+    float *own;                 // instead of out, [batch * q_heads][span_row(dim)]
 };
+// A row of FP32 results: O, and from the last four on the maximum (log2 units)
+// and the denominator that it is relative to.
+__host__ __device__ constexpr int span_row(int dim) { return (dim + 3) / 4 * 4 + 4; }
 
 // Launches for one cache type; vec: 16-byte loads are possible; big: one block
 // per SM instead of several small ones.
@@ -84,7 +87,8 @@ struct SpanArgs {
     void *out;
     int64_t o_st, o_sh;
     float *lse;                 // [tokens][q_heads] natural log, or NULL
-    float *pre;                 // prefix: [tokens * q_heads][dim + 2], instead of out
+    float *pre;                 // prefix: blocks that are not cut, [tokens * q_heads][span_row(dim)]
+    const float *own;           // prefix: what the slots behind it give, alike
     const int32_t *starts;      // [batch + 1]; NULL: prefix
     const int32_t *lengths;     // [batch]
     const int32_t *prefix;
@@ -102,12 +106,15 @@ struct SpanArgs {
 };
 // Rows of a tile of query rows, and how many tiles a block of them has.
 constexpr int kSpanRows = 128;
-constexpr int span_streams(int dim) { return dim <= 128 ? 2 : 1; }
+__host__ __device__ constexpr int span_streams(int dim) { return dim <= 128 ? 2 : 1; }
 // Floats of a part.
-constexpr int64_t span_part(int dim) { return static_cast<int64_t>(span_streams(dim)) * kSpanRows * ((dim + 15) / 16 * 16 + 2); }
+__host__ __device__ constexpr int64_t span_part(int dim) { return static_cast<int64_t>(span_streams(dim)) * kSpanRows * ((dim + 15) / 16 * 16 + 2); }
 cudaError_t launch_tile_f16(const SpanArgs &a, bool vec, int ctas, cudaStream_t s);
 cudaError_t launch_tile_bf16(const SpanArgs &a, bool vec, int ctas, cudaStream_t s);
+// The tiles, and what follows them (and for a prefix the attention behind it):
+// joins, and rows computed one by one.
 cudaError_t launch_span(const SpanArgs &a, bool vec, int elem, int sm_count, cudaStream_t s);
+cudaError_t launch_span_finish(const SpanArgs &a, int elem, int sm_count, cudaStream_t s);
 
 struct EvictArgs {
     KvView kv;

@@ -118,7 +118,7 @@ AttnPlan attn_plan(const KvView &v, int group, int nt, bool weights)
 
 // Workspace of the attention of many tokens: offsets and size in bytes.
 struct SpanPlan {
-    size_t info, redo, pre, total;
+    size_t info, redo, pre, own, total;
 };
 
 SpanPlan span_plan(const KvView &v, int64_t tokens, int q_heads, bool prefix)
@@ -129,7 +129,8 @@ SpanPlan span_plan(const KvView &v, int64_t tokens, int q_heads, bool prefix)
     p.info = up(static_cast<size_t>(2) * kSpanMaxCtas * span_part(v.dim) * 4);
     p.redo = p.info + up(2 * kSpanMaxCtas * sizeof(SpanInfo));
     p.pre = p.redo + up(rows);
-    p.total = p.pre + (prefix ? up(rows * (v.dim + 2) * 4) : 0);
+    p.own = p.pre + (prefix ? up(rows * span_row(v.dim) * 4) : 0);
+    p.total = p.own + (p.own - p.pre);
     return p;
 }
 
@@ -205,16 +206,20 @@ gemv_status_t attn_paged(const gemv_kv_t *kv, const gemv_attn_t *args, const int
     // tokens with their weights: 111.5 us, 120.4 us with none).
     a.lead = big ? 16 : 8;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    SpanArgs g{};
     if (prefix) {
-        SpanArgs g{};
         const SpanPlan sp = span_plan(a.kv, a.kv.batch, q_heads, true);
         unsigned char *mine = ws + (total - sp.total);
         g.kv = a.kv;
         place_span(&g, sp, mine);
         g.q = a.q, g.q_st = a.q_sb, g.q_sh = a.q_sh;
+        g.out = a.out, g.o_st = a.o_sb, g.o_sh = a.o_sh;
+        g.out_vec = aligned(out.data, 16) && mult8(out.stride, 2);
+        g.lse = a.lse;
         g.pre = reinterpret_cast<float *>(mine + sp.pre);
+        g.own = a.own = reinterpret_cast<float *>(mine + sp.own);
         g.lengths = a.lengths;
-        g.prefix = prefix;
+        g.prefix = a.prefix = prefix;
         g.tokens = a.kv.batch;
         g.q_heads = q_heads;
         g.group = group;
@@ -224,12 +229,11 @@ gemv_status_t attn_paged(const gemv_kv_t *kv, const gemv_attn_t *args, const int
         g.err = a.err;
         const cudaError_t e = launch_span(g, vec, kv->elem, dev.sm_count, s);
         if (e != cudaSuccess) return decode_cuda_fail(e, GEMV_ERR_LAUNCH);
-        a.prefix = prefix;
-        a.pre = g.pre;
     }
     cudaError_t e = kv->elem == GEMV_ELEM_F16 ? launch_attn_f16(a, vec, nt, big, dev.sm_count, s)
                                               : launch_attn_bf16(a, vec, nt, big, dev.sm_count, s);
     if (e == cudaSuccess && a.scores_out && a.kv.capacity > 0) e = launch_attn_weights(a, nt, s);
+    if (e == cudaSuccess && prefix) e = launch_span_finish(g, kv->elem, dev.sm_count, s);
     return e == cudaSuccess ? GEMV_OK : decode_cuda_fail(e, GEMV_ERR_LAUNCH);
 }
 
@@ -393,7 +397,8 @@ gemv_status_t gemv_attn_prompt(const gemv_kv_t *kv, const gemv_prompt_t *g, void
     a.out_vec = aligned(g->out.data, 16) && mult8(g->out.stride, 2);
     place_span(&a, p, g->workspace);
     const bool vec = cache_vec(kv) && aligned(g->q.data, 16) && mult8(g->q.stride, 2);
-    const cudaError_t e = launch_span(a, vec, kv->elem, dev.sm_count, static_cast<cudaStream_t>(stream));
+    cudaError_t e = launch_span(a, vec, kv->elem, dev.sm_count, static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) e = launch_span_finish(a, kv->elem, dev.sm_count, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GEMV_OK : decode_cuda_fail(e, GEMV_ERR_LAUNCH);
 }
 

@@ -22,7 +22,7 @@
 namespace mbg {
 namespace {
 
-constexpr int kWarps = 4, kThreads = kWarps * 32, kMaxDim = 256, kOwn = kMaxDim / 32;
+constexpr int kWarps = 8, kThreads = kWarps * 32, kMaxDim = 256, kOwn = kMaxDim / 32;
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
 struct Shared {
@@ -130,14 +130,14 @@ __device__ void one_row(const SpanArgs &a, Shared &sh, int token, int head)
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) v += sh.o[w][d];
         if (a.pre)
-            a.pre[row * (dim + 2) + d] = v;
+            a.pre[row * span_row(dim) + d] = v;
         else
             elem_store1<E>(a.out, token * a.o_st + head * a.o_sh + d, sum == 0.f ? 0.f : v / sum);
     }
     if (threadIdx.x == 0) {
         if (a.pre) {
-            a.pre[row * (dim + 2) + dim] = top;
-            a.pre[row * (dim + 2) + dim + 1] = sum;
+            a.pre[(row + 1) * span_row(dim) - 4] = top;
+            a.pre[(row + 1) * span_row(dim) - 3] = sum;
         } else if (a.lse) {
             a.lse[row] = sum > 0.f || sum != sum ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
         }
@@ -145,112 +145,195 @@ __device__ void one_row(const SpanArgs &a, Shared &sh, int token, int head)
     __syncthreads();
 }
 
-// Sixteen rows of a block that was cut: thread (g, r) = (t / 16, t % 16) sums
-// every eighth run of four elements of row r.
-constexpr int kJoinRows = 16, kJoinGroups = kThreads / kJoinRows;
+// Sixteen rows of a block: thread (lane, row) = (t / 16, t % 16) takes every
+// sixteenth run of four elements of its row, so that half a warp reads 256
+// bytes of a part.
+constexpr int kJoinRows = 16, kJoinLanes = kThreads / kJoinRows;
+constexpr int kMaxParts = kSpanMaxCtas + 1;
 
 struct JoinShared {
-    int slot[kSpanMaxCtas + 1];
+    int slot[kMaxParts];
     int count[kWarps];
-    float m[kSpanMaxCtas + 1][kJoinRows];
+    float m[kMaxParts][kJoinRows], l[kMaxParts][kJoinRows];
     int bad[kJoinRows];
 };
 
-template <int E>
-__device__ void join_rows(const SpanArgs &a, Shared &sh, JoinShared &js, int ctas, int c0, int stream, int r16)
+// The numbers i < n for which f(i), in order, in list (no more than `most`).
+template <typename F>
+__device__ int collect(int n, int *list, int most, int *count, F f)
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, dim = a.kv.dim;
-    const SpanInfo first = a.info[2 * c0 + 1];
-    if (first.tiles == 0) return;
-    const span::Seq s = span::seq_of(a, first.b, false);
-    const int row0 = first.row0 + stream * kSpanRows + r16 * kJoinRows;
-    const int rows = s.m * a.group;
-    if (row0 >= rows || (stream > 0 && row0 >= first.row0 + span_streams(dim) * kSpanRows)) return;
-    // the parts behind the first: those of later CTAs that begin with this block
-    int parts = 1;
-    if (tid == 0) js.slot[0] = 2 * c0 + 1;
-    for (int c = c0 + 1; c < ctas; c += kThreads) {
-        bool mine = false;
-        if (c + tid < ctas) {
-            const SpanInfo i = a.info[2 * (c + tid)];
-            mine = i.tiles > 0 && i.b == first.b && i.h == first.h && i.row0 == first.row0;
-        }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int have = 0;
+    for (int i0 = 0; i0 < n; i0 += kThreads) {
+        const int i = i0 + threadIdx.x;
+        const bool mine = i < n && f(i);
         const unsigned vote = __ballot_sync(kFull, mine);
         __syncthreads();
-        if (lane == 0) js.count[warp] = __popc(vote);
+        if (lane == 0) count[warp] = __popc(vote);
         __syncthreads();
-        int at = parts;
+        int at = have;
         for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) at += js.count[w];
-            parts += js.count[w];
+            if (w < warp) at += count[w];
+            have += count[w];
         }
-        if (mine) js.slot[at + __popc(vote & ((1u << lane) - 1))] = 2 * (c + tid);
-    }
-    if (tid < kJoinRows) js.bad[tid] = 0;
-    __syncthreads();
-    const int64_t half = a.part_stride / span_streams(dim);
-    const int stat = (dim + 15) / 16 * 16 * kSpanRows, in = r16 * kJoinRows;
-    for (int i = tid; i < parts * kJoinRows; i += kThreads) {
-        const int p = i / kJoinRows, r = i - p * kJoinRows;
-        js.m[p][r] = __ldcg(a.part + js.slot[p] * a.part_stride + stream * half + stat + in + r);
+        at += __popc(vote & ((1u << lane) - 1));
+        if (mine && at < most) list[at] = i;
     }
     __syncthreads();
-    const int r = tid % kJoinRows, g = tid / kJoinRows, row = row0 + r;
-    float top = -INFINITY, sum = 0.f;
-    for (int p = 0; p < parts; ++p) top = fmaxf(top, js.m[p][r]);
-    for (int p = 0; p < parts; ++p)
-        sum += exp2_from(js.m[p][r], top) * __ldcg(a.part + js.slot[p] * a.part_stride + stream * half + stat + kSpanRows + in + r);
+    return min(have, most);
+}
+
+__device__ __forceinline__ float lse_of(float m, float l)
+{
+    return l > 0.f || l != l ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// Four elements of a row's output from d on.
+template <int E>
+__device__ __forceinline__ void store4(const SpanArgs &a, int token, int head, int d, const float (&v)[4])
+{
+    const int64_t at = token * a.o_st + head * a.o_sh + d;
+    if (a.out_vec && d + 4 <= a.kv.dim) {
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) = make_uint2(elem_pack2<E>(v[0], v[1]), elem_pack2<E>(v[2], v[3]));
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (d + k < a.kv.dim) elem_store1<E>(a.out, at + k, v[k]);
+    }
+}
+
+// What a prefix and the slots behind it give together: factors of their O.
+struct Both {
+    float pre, own, m, l;
+};
+__device__ __forceinline__ Both both_of(const SpanArgs &a, int64_t index, float m, float l)
+{
+    const float *stat = a.own + (index + 1) * span_row(a.kv.dim) - 4;
+    const float m2 = __ldcg(stat), l2 = __ldcg(stat + 1);
+    Both r;
+    r.m = fmaxf(m, m2);
+    r.pre = exp2_from(m, r.m);
+    r.own = l2 == 0.f ? 0.f : exp2_from(m2, r.m);  // (its O may not be there)
+    r.l = l * r.pre + (l2 == 0.f ? 0.f : l2 * r.own);
+    const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
+    r.pre *= inv;
+    r.own = l2 == 0.f ? 0.f : r.own * inv;
+    return r;
+}
+
+// Rows [row0 + 16 group, + 16) of the block of cached head h that begins at
+// row0 of sequence b's rows.
+template <int E>
+__device__ void join_rows(const SpanArgs &a, unsigned char *raw, int ctas, int b, int h, int row0, int group)
+{
+    JoinShared &js = *reinterpret_cast<JoinShared *>(raw);
+    const int tid = threadIdx.x, dim = a.kv.dim;
+    const span::Seq s = span::seq_of(a, b, false);
+    const int rows = s.m * a.group, first = row0 + group * kJoinRows;
+    if (first >= rows) return;
+    const int parts = collect(2 * ctas, js.slot, kMaxParts, js.count, [&](int i) {
+        const SpanInfo p = a.info[i];
+        return p.tiles > 0 && p.b == b && p.h == h && p.row0 == row0;
+    });
+    const int r = tid % kJoinRows, lane = tid / kJoinRows, row = first + r;
     const bool live = row < rows;
-    const int token = s.q0 + (live ? row / a.group : 0), head = first.h * a.group + (live ? row % a.group : 0);
+    const int token = s.q0 + (live ? row / a.group : 0), head = h * a.group + (live ? row % a.group : 0);
     const int64_t index = static_cast<int64_t>(token) * a.q_heads + head;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    for (int d = 4 * g; d < dim; d += 4 * kJoinGroups) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int p = 0; p < parts; ++p) {
-            const float4 x = __ldcg(reinterpret_cast<const float4 *>(
-                a.part + js.slot[p] * a.part_stride + stream * half + (static_cast<int64_t>(d / 4) * kSpanRows + in + r) * 4));
-            const float f = exp2_from(js.m[p][r], top);
-            v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
+    if (tid < kJoinRows) js.bad[tid] = parts == 0 && ctas > 0 && live && __ldcg(a.redo + index) == 1;
+    // the rows' places in a part
+    const int stream = group * kJoinRows / kSpanRows, in = group * kJoinRows % kSpanRows;
+    const int64_t half = stream * (a.part_stride / span_streams(dim));
+    const int stat = (dim + 15) / 16 * 16 * kSpanRows;
+    for (int p = lane; p < parts; p += kJoinLanes) {
+        const float *from = a.part + js.slot[p] * a.part_stride + half + stat + in + r;
+        js.m[p][r] = __ldcg(from);
+        js.l[p][r] = __ldcg(from + kSpanRows);
+    }
+    __syncthreads();
+    float top = -INFINITY, sum = 0.f;
+    if (parts > 0) {
+        for (int p = 0; p < parts; ++p) top = fmaxf(top, js.m[p][r]);
+        for (int p = 0; p < parts; ++p) sum += exp2_from(js.m[p][r], top) * js.l[p][r];
+    } else if (live) {
+        top = __ldcg(a.pre + (index + 1) * span_row(dim) - 4);
+        sum = __ldcg(a.pre + (index + 1) * span_row(dim) - 3);
+    }
+    Both f = {sum == 0.f ? 0.f : 1.f / sum, 0.f, top, sum};
+    if (a.own && live) f = both_of(a, index, top, sum);
+    for (int d = 4 * lane; d < dim; d += 4 * kJoinLanes) {
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (parts > 0) {
+            const float *from = a.part + half + (static_cast<int64_t>(d / 4) * kSpanRows + in + r) * 4;
+#pragma unroll 8
+            for (int p = 0; p < parts; ++p) {
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(from + js.slot[p] * a.part_stride));
+                const float w = exp2_from(js.m[p][r], top);
+                v[0] += x.x * w, v[1] += x.y * w, v[2] += x.z * w, v[3] += x.w * w;
+            }
+        } else if (live) {
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(a.pre + index * span_row(dim) + d));
+            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
         }
-        const float w[4] = {v.x, v.y, v.z, v.w};
         if (!live) continue;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            if (d + k >= dim) continue;
-            if (w[k] != w[k] && sum == sum) js.bad[r] = 1;
-            if (a.pre)
-                a.pre[index * (dim + 2) + d + k] = w[k];
-            else
-                elem_store1<E>(a.out, token * a.o_st + head * a.o_sh + d + k, w[k] * inv);
+            if (d + k < dim && v[k] != v[k] && sum == sum) js.bad[r] = 1;
+            v[k] *= f.pre;
         }
-    }
-    if (live && g == 0) {
-        if (a.pre) {
-            a.pre[index * (dim + 2) + dim] = top;
-            a.pre[index * (dim + 2) + dim + 1] = sum;
-        } else if (a.lse) {
-            a.lse[index] = sum > 0.f || sum != sum ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+        if (f.own != 0.f) {
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(a.own + index * span_row(dim) + d));
+            v[0] += x.x * f.own, v[1] += x.y * f.own, v[2] += x.z * f.own, v[3] += x.w * f.own;
         }
+        store4<E>(a, token, head, d, v);
     }
+    if (live && lane == 0 && a.lse) a.lse[index] = lse_of(f.m, f.l);
     __syncthreads();
-    for (int i = 0; i < kJoinRows; ++i)
-        if (js.bad[i]) one_row<E>(a, sh, s.q0 + (row0 + i) / a.group, first.h * a.group + (row0 + i) % a.group);
+    unsigned bad = 0;
+    for (int i = 0; i < kJoinRows; ++i) bad |= js.bad[i] ? 1u << i : 0u;
     __syncthreads();
+    for (int i = 0; i < kJoinRows; ++i) {
+        if (!(bad >> i & 1)) continue;
+        const int t = s.q0 + (first + i) / a.group, hd = h * a.group + (first + i) % a.group;
+        one_row<E>(a, *reinterpret_cast<Shared *>(raw), t, hd);
+        if (!a.own) continue;
+        const int64_t at = static_cast<int64_t>(t) * a.q_heads + hd;
+        const float *pre = a.pre + at * span_row(dim);
+        const Both g = both_of(a, at, pre[span_row(dim) - 4], pre[span_row(dim) - 3]);
+        for (int d = tid; d < dim; d += kThreads)
+            elem_store1<E>(a.out, t * a.o_st + hd * a.o_sh + d,
+                           pre[d] * g.pre + (g.own != 0.f ? __ldcg(a.own + at * span_row(dim) + d) * g.own : 0.f));
+        if (tid == 0 && a.lse) a.lse[at] = lse_of(g.m, g.l);
+        __syncthreads();
+    }
 }
 
-// The joins of all cut blocks, then the rows to be computed one by one.
+// Prompts: the joins of all blocks that were cut, then the rows to be computed
+// one by one.  Prefix: every row, joined with the slots behind it.
 template <int E>
 __global__ void __launch_bounds__(kThreads) mbg_span_finish_kernel(const __grid_constant__ SpanArgs a, int ctas)
 {
-    __shared__ Shared sh;
-    __shared__ JoinShared js;
+    __shared__ __align__(16) unsigned char raw[sizeof(JoinShared) > sizeof(Shared) ? sizeof(JoinShared) : sizeof(Shared)];
+    __shared__ int cuts[kSpanMaxCtas], count[kWarps];
     pdl_trigger();
     pdl_wait();
-    constexpr int kGroups = kSpanRows / kJoinRows;
-    const int streams = span_streams(a.kv.dim), tasks = ctas * streams * kGroups;
-    for (int i = blockIdx.x; i < tasks; i += gridDim.x)
-        join_rows<E>(a, sh, js, ctas, i / (streams * kGroups), i / kGroups % streams, i % kGroups);
+    const int block = span_streams(a.kv.dim) * kSpanRows, groups = block / kJoinRows;
+    if (a.prefix) {
+        const int blocks = static_cast<int>((static_cast<int64_t>(a.tokens) * a.group + block - 1) / block);
+        const int64_t tasks = static_cast<int64_t>(blocks) * a.kv.kv_heads * groups;
+        for (int64_t i = blockIdx.x; i < tasks; i += gridDim.x) {
+            const int g = static_cast<int>(i % groups), h = static_cast<int>(i / groups % a.kv.kv_heads);
+            join_rows<E>(a, raw, ctas, 0, h, static_cast<int>(i / groups / a.kv.kv_heads) * block, g);
+            __syncthreads();
+        }
+        return;
+    }
+    // blocks whose beginning is a part
+    const int n = collect(ctas, cuts, kSpanMaxCtas, count, [&](int c) { return a.info[2 * c + 1].tiles > 0; });
+    for (int i = blockIdx.x; i < n * groups; i += gridDim.x) {
+        const SpanInfo p = a.info[2 * cuts[i / groups] + 1];
+        join_rows<E>(a, raw, ctas, p.b, p.h, p.row0, i % groups);
+        __syncthreads();
+    }
     const int64_t rows = static_cast<int64_t>(a.tokens) * a.q_heads;
     for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kThreads; r0 < rows; r0 += static_cast<int64_t>(gridDim.x) * kThreads) {
         const bool again = r0 + threadIdx.x < rows && __ldcg(a.redo + r0 + threadIdx.x) == 1;
@@ -258,15 +341,15 @@ __global__ void __launch_bounds__(kThreads) mbg_span_finish_kernel(const __grid_
         for (int w = 0; w < kWarps; ++w) {
             if (threadIdx.x / 32 == w) {
                 const unsigned vote = __ballot_sync(kFull, again);
-                if (threadIdx.x % 32 == 0) js.count[0] = static_cast<int>(vote);
+                if (threadIdx.x % 32 == 0) count[0] = static_cast<int>(vote);
             }
             __syncthreads();
-            const unsigned vote = static_cast<unsigned>(js.count[0]);
+            const unsigned vote = static_cast<unsigned>(count[0]);
             __syncthreads();
             for (int i = 0; i < 32; ++i)
                 if (vote >> i & 1) {
                     const int64_t r = r0 + w * 32 + i;
-                    one_row<E>(a, sh, static_cast<int>(r / a.q_heads), static_cast<int>(r % a.q_heads));
+                    one_row<E>(a, *reinterpret_cast<Shared *>(raw), static_cast<int>(r / a.q_heads), static_cast<int>(r % a.q_heads));
                 }
         }
     }
@@ -276,8 +359,8 @@ template <int E>
 __global__ void __launch_bounds__(kThreads) mbg_span_rows_kernel(const __grid_constant__ SpanArgs a)
 {
     __shared__ Shared sh;
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();  // as the tiles: what follows may go by this launch's wait
     if (blockIdx.x == 0)
         for (int b = threadIdx.x; b < (a.prefix ? 1 : a.kv.batch); b += kThreads) span::seq_of(a, b, true);
     const int64_t rows = static_cast<int64_t>(a.tokens) * a.q_heads;
@@ -302,18 +385,29 @@ static cudaError_t launch_blocks(F fn, int64_t blocks, cudaStream_t s, Args... a
     return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
+// A scale of 0 (or none) leaves the tiles no maximum to go by.
+static bool tiled(const SpanArgs &a) { return fabsf(a.scale_log2) > 0.f && fabsf(a.scale_log2) < INFINITY; }
+static int ctas_of(int sm_count) { return sm_count < kSpanMaxCtas ? sm_count : kSpanMaxCtas; }
+
 cudaError_t launch_span(const SpanArgs &a, bool vec, int elem, int sm_count, cudaStream_t s)
 {
     const bool f16 = elem == GEMV_ELEM_F16;
-    const int64_t rows = static_cast<int64_t>(a.tokens) * a.q_heads, most = static_cast<int64_t>(sm_count) * 16;
-    // a scale of 0 (or none) leaves the tiles no maximum to go by
-    if (!(fabsf(a.scale_log2) > 0.f && fabsf(a.scale_log2) < INFINITY))
-        return launch_blocks(f16 ? mbg_span_rows_kernel<GEMV_ELEM_F16> : mbg_span_rows_kernel<GEMV_ELEM_BF16>, rows < most ? rows : most, s, a);
-    const int ctas = sm_count < kSpanMaxCtas ? sm_count : kSpanMaxCtas;
-    const cudaError_t e = f16 ? launch_tile_f16(a, vec, ctas, s) : launch_tile_bf16(a, vec, ctas, s);
-    if (e != cudaSuccess) return e;
-    const int64_t tasks = static_cast<int64_t>(ctas) * span_streams(a.kv.dim) * (kSpanRows / kJoinRows);
-    return launch_blocks(f16 ? mbg_span_finish_kernel<GEMV_ELEM_F16> : mbg_span_finish_kernel<GEMV_ELEM_BF16>, tasks, s, a, ctas);
+    if (tiled(a)) return f16 ? launch_tile_f16(a, vec, ctas_of(sm_count), s) : launch_tile_bf16(a, vec, ctas_of(sm_count), s);
+    const int64_t rows = static_cast<int64_t>(a.tokens) * a.q_heads, most = static_cast<int64_t>(sm_count) * 8;
+    return launch_blocks(f16 ? mbg_span_rows_kernel<GEMV_ELEM_F16> : mbg_span_rows_kernel<GEMV_ELEM_BF16>, rows < most ? rows : most, s, a);
+}
+
+cudaError_t launch_span_finish(const SpanArgs &a, int elem, int sm_count, cudaStream_t s)
+{
+    if (!tiled(a) && !a.prefix) return cudaSuccess;
+    const int64_t block = span_streams(a.kv.dim) * kSpanRows, rows = static_cast<int64_t>(a.tokens) * a.group;
+    int64_t blocks = static_cast<int64_t>(sm_count) * 4;
+    if (a.prefix) {
+        const int64_t tasks = (rows + block - 1) / block * a.kv.kv_heads * (block / kJoinRows);
+        if (tasks < blocks) blocks = tasks;
+    }
+    return launch_blocks(elem == GEMV_ELEM_F16 ? mbg_span_finish_kernel<GEMV_ELEM_F16> : mbg_span_finish_kernel<GEMV_ELEM_BF16>, blocks, s, a,
+                         tiled(a) ? ctas_of(sm_count) : 0);
 }
 
 }  // namespace mbg

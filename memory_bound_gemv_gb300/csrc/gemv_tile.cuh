@@ -147,7 +147,7 @@ __device__ __forceinline__ int cost_of(const Block &k) { return kLead + k.tiles 
 template <int DC>
 struct Shared {
     alignas(8) uint64_t kfull[Shape<DC>::kStages], kempty[Shape<DC>::kStages], vfull[Shape<DC>::kStages], vempty[Shape<DC>::kStages];
-    alignas(8) uint64_t sready[2], pready[2], odone[2], qready, meet, last, segfull[2], segempty[2];
+    alignas(8) uint64_t sready[2], pready[2][2], odone[2], qready, meet, last, segfull[2], segempty[2];
     uint32_t tmem;
     int abort;
     Segment seg[2];
@@ -173,9 +173,25 @@ struct Kernel {
     // P is at most 2^kLazy times kUp: in f16 below 2^16
     static constexpr float kLazy = kBf16 ? 8.f : 4.f, kUp = kBf16 ? 0.f : 11.f;
 
+    // Gives up after kWaitNs.  The clock is read once in 256 tries: a tile takes
+    // some ten waits one behind the other, and each reading some 0.5 us.
     static __device__ __forceinline__ bool wait(Shared<DC> &sh, uint64_t &bar, uint32_t parity, const SpanArgs &a)
     {
-        if (mbar_wait_bounded(smem_addr(&bar), parity, kWaitNs)) return true;
+        uint64_t since = 0;
+        for (uint32_t i = 0;; ++i) {
+            uint32_t done;
+            asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                         : "=r"(done)
+                         : "r"(smem_addr(&bar)), "r"(parity)
+                         : "memory");
+            if (done) return true;
+            if ((i & 255) != 255) continue;
+            const uint64_t now = global_timer_ns();
+            if (since == 0)
+                since = now;
+            else if (now - since > kWaitNs)
+                break;
+        }
         report_error(a.err, DEVERR_TIMEOUT);
         sh.abort = 1;
         return false;
@@ -471,13 +487,16 @@ struct Kernel {
             if (!warp_wait(sh, sh.qready, nq++ & 1, a)) return;
             tc::fence_after();
             const int steps = both ? 2 * tiles : tiles;
+            // K of the next scores is there
+            auto k_ready = [&](int s) {
+                if (both && s % S::kStreams == 1) return true;
+                const int st = nk % S::kStages;
+                if (!warp_wait(sh, sh.kfull[st], nk / S::kStages & 1, a)) return false;
+                tc::fence_smem();  // what the loaders wrote, for the tensor core
+                return true;
+            };
             auto scores = [&](int s) {
                 const int w = s % S::kStreams, st = nk % S::kStages;
-                if (!both || w == 0) {
-                    if (!warp_wait(sh, sh.kfull[st], nk / S::kStages & 1, a)) return false;
-                    tc::fence_smem();  // what the loaders wrote, for the tensor core
-                }
-                tc::fence_after();
                 const uint64_t q = tc::descriptor(qs + (both ? w * S::kQBytes : 0), 16), k = tc::descriptor(ks + st * S::kKvBytes, 16);
                 if (one) {
 #pragma unroll
@@ -489,33 +508,46 @@ struct Kernel {
                     if (!both || w == 1) tc::commit(smem_addr(&sh.kempty[st]));
                 }
                 if (!both || w == 1) ++nk;
-                return true;
             };
             bool ok = true;
-            for (int s = 0; s < S::kStreams && s < steps && ok; ++s) ok = scores(s);
+            for (int s = 0; s < S::kStreams && s < steps && ok; ++s) {
+                ok = k_ready(s);
+                if (ok) scores(s);
+            }
             for (int s = 0; s < steps && ok; ++s) {
                 const int w = s % S::kStreams, st = nv % S::kStages;
-                ok = warp_wait(sh, sh.pready[w], np[w]++ & 1, a);
-                if (ok && (!both || w == 0)) {
+                // V, and K of the stream's next tile, are waited for ahead of P
+                if (!both || w == 0) {
                     ok = warp_wait(sh, sh.vfull[st], nv / S::kStages & 1, a);
                     tc::fence_smem();
                 }
-                if (!ok) break;
-                tc::fence_after();
+                if (ok && s + S::kStreams < steps) ok = k_ready(s + S::kStreams);
                 const uint64_t v = tc::descriptor(vs + st * S::kKvBytes, kTok * 128);
                 const uint32_t p = tmem + w * kTok, o = tmem + S::kOColumn + w * (DC * 64);
+                // P comes in two halves of the tile's slots
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (ok) ok = warp_wait(sh, sh.pready[w][half], np[w] & 1, a);
+                    tc::fence_after();
+                    if (ok && one) {
+#pragma unroll
+                        for (int part = 0; part < 2; ++part)
+#pragma unroll
+                            for (int k = 0; k < kTok / 32; ++k) {
+                                const int i = half * (kTok / 32) + k;
+                                tc::mma_ts(o, p + part * (kTok / 2) + i * 8, tc::further(v, i * 2048), o_instr,
+                                           s >= S::kStreams || half > 0 || part > 0 || k > 0);
+                            }
+                    }
+                }
+                if (!ok) break;
+                ++np[w];
                 if (one) {
-#pragma unroll
-                    for (int part = 0; part < 2; ++part)
-#pragma unroll
-                        for (int i = 0; i < kTok / 16; ++i)
-                            tc::mma_ts(o, p + part * (kTok / 2) + i * 8, tc::further(v, i * 2048), o_instr,
-                                       s >= S::kStreams || part > 0 || i > 0);
                     if (s + S::kStreams >= steps) tc::commit(smem_addr(&sh.odone[w]));
                     if (!both || w == 1) tc::commit(smem_addr(&sh.vempty[st]));
                 }
                 if (!both || w == 1) ++nv;
-                if (s + S::kStreams < steps) ok = scores(s + S::kStreams);
+                if (s + S::kStreams < steps) scores(s + S::kStreams);
             }
             if (!ok) return;
         }
@@ -577,6 +609,28 @@ struct Kernel {
         return r;
     }
 
+    // A warp's 32 rows of Q, whose first elements are `at` (a lane each; -1:
+    // zeros), into shared memory; `flip` changes the sign.
+    static __device__ __forceinline__ void load_q(const uint16_t *q, int64_t at, uint32_t dst, int dim, int row0, int lane, uint32_t flip)
+    {
+        constexpr int kLanes = DC == 1 ? 8 : DC == 2 ? 16 : 32, kAtOnce = 32 / kLanes, kBatch = 8;
+        const int chunk = lane % kLanes, sub = lane / kLanes;
+#pragma unroll 1
+        for (int i0 = 0; i0 < 32; i0 += kBatch * kAtOnce) {
+            uint4 v[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int64_t from = __shfl_sync(kFull, at, (i0 + k * kAtOnce + sub) & 31);
+                v[k] = from >= 0 && chunk * 8 < dim ? load8(q + from + chunk * 8, dim - chunk * 8) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                v[k].x ^= flip, v[k].y ^= flip, v[k].z ^= flip, v[k].w ^= flip;
+                if (chunk < DC * 8) st_shared(dst + swizzled(kRows, row0 + i0 + k * kAtOnce + sub, chunk), v[k]);
+            }
+        }
+    }
+
     // Multiplies this warp's rows of O by f.
     static __device__ __forceinline__ void scale_o(uint32_t o, float f, int dim)
     {
@@ -621,24 +675,10 @@ struct Kernel {
             const int r = g.row0 + (both ? stream * kRows : 0) + row;
             const bool live = r < g.row0 + g.block.rows;
             const int token = live ? r / a.group : 0, head = g.h * a.group + (live ? r - token * a.group : 0);
-            const uint16_t *q = static_cast<const uint16_t *>(a.q) + (g.seq.q0 + token) * a.q_st + head * a.q_sh;
             if (tiles > 0 && (both || stream == 0)) {
-                const uint32_t dst = qs + (both ? stream * S::kQBytes : 0), flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-                constexpr int kAtOnce = DC % 2 ? 8 : 16;
-#pragma unroll 1
-                for (int c0 = 0; c0 < DC * 8; c0 += kAtOnce) {
-                    uint4 v[kAtOnce];
-#pragma unroll
-                    for (int i = 0; i < kAtOnce; ++i) {
-                        const int c = c0 + i;
-                        v[i] = live && c * 8 < kv.dim ? load8(q + c * 8, kv.dim - c * 8) : make_uint4(0, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int i = 0; i < kAtOnce; ++i) {
-                        v[i].x ^= flip, v[i].y ^= flip, v[i].z ^= flip, v[i].w ^= flip;
-                        st_shared(dst + swizzled(kRows, row, c0 + i), v[i]);
-                    }
-                }
+                const int64_t at = live ? (g.seq.q0 + token) * a.q_st + head * a.q_sh : -1;
+                load_q(static_cast<const uint16_t *>(a.q), at, qs + (both ? stream * S::kQBytes : 0), kv.dim, row & 96, lane,
+                       a.scale_log2 < 0.f ? 0x80008000u : 0u);
                 tc::fence_smem();
             }
             if (tiles > 0) mbar_arrive(smem_addr(&sh.qready));
@@ -693,12 +733,14 @@ struct Kernel {
                     }
                     tc::store16(s_at + c / 2, hi);
                     tc::store16(s_at + kTok / 2 + c / 2, lo);
+                    if (c + 32 == kTok / 2 || c + 32 == kTok) {  // half of P is there
+                        tc::wait_st();
+                        tc::fence_before();
+                        mbar_arrive(smem_addr(&sh.pready[stream][c + 32 == kTok]));
+                    }
                 }
                 const float2 sums = apart(add2(sum[0], sum[1]));
                 l += sums.x + sums.y;
-                tc::wait_st();
-                tc::fence_before();
-                mbar_arrive(smem_addr(&sh.pready[stream]));
             }
             const bool any = first < tiles;
             if (any && !__all_sync(kFull, wait(sh, sh.odone[stream], no++ & 1, a))) return;
@@ -767,7 +809,7 @@ struct Kernel {
                 for (int i = 0; i < 16; i += 4)
                     *reinterpret_cast<float4 *>(part + ((c + i) / 4 * kRows + row) * 4) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
             } else if (a.pre) {
-                float *p = a.pre + index * (dim + 2) + c;
+                float *p = a.pre + index * span_row(dim) + c;
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     if (c + i < dim) p[i] = x[i];
@@ -800,8 +842,9 @@ struct Kernel {
         // weight is 0: such rows are computed again, one by one
         a.redo[index] = nan && l == l;
         if (a.pre) {
-            a.pre[index * (dim + 2) + dim] = m;
-            a.pre[index * (dim + 2) + dim + 1] = l;
+            float *stat = a.pre + (index + 1) * span_row(dim) - 4;
+            stat[0] = m;
+            stat[1] = l;
         } else if (a.lse) {
             a.lse[index] = l > 0.f || l != l ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
         }
@@ -823,7 +866,8 @@ struct Kernel {
             }
             for (int i = 0; i < 2; ++i) {
                 mbar_init(smem_addr(&sh.sready[i]), 1);
-                mbar_init(smem_addr(&sh.pready[i]), kRows);
+                mbar_init(smem_addr(&sh.pready[i][0]), kRows);
+                mbar_init(smem_addr(&sh.pready[i][1]), kRows);
                 mbar_init(smem_addr(&sh.odone[i]), 1);
                 mbar_init(smem_addr(&sh.segfull[i]), 1);
                 mbar_init(smem_addr(&sh.segempty[i]), 4 + 1 + 4 * S::kStreams);
@@ -837,8 +881,10 @@ struct Kernel {
             sh.found = 0;
         }
         if (warp == 0) tc::alloc(smem_addr(&sh.tmem), 512);
-        pdl_trigger();
+        // the next launch may start once this one's wait is over: then nothing
+        // before this launch is under way any more
         pdl_wait();
+        pdl_trigger();
         tc::fence_before();
         __syncthreads();
         tc::fence_after();
