@@ -68,10 +68,10 @@ __device__ __forceinline__ float exp2_approx(float x)
 template <int DC>
 struct Shape {
     static constexpr int kStreams = DC <= 2 ? 2 : 1;
-    static constexpr int kTok = DC <= 2 ? 128 : 64;  // slots of a tile
+    static constexpr int kTok = 64;                  // slots of a tile
     static constexpr int kQBytes = kRows * DC * 128; // a tile of rows
     static constexpr int kKvBytes = kTok * DC * 128;
-    static constexpr int kStages = DC == 1 ? 4 : DC == 3 ? 3 : 2;  // tiles of K, and of V, in shared memory
+    static constexpr int kStages = DC == 1 ? 8 : DC == 2 ? 4 : DC == 3 ? 3 : 2;  // tiles of K, and of V, in shared memory
     static constexpr int kBlock = kStreams * kRows;  // rows of a block
     static constexpr int kOColumn = 256;
 };
@@ -138,7 +138,7 @@ __device__ __forceinline__ Block block_of(const SpanArgs &a, const span::Seq &s,
 
 // Costs: a tile of slots takes one unit per tile of rows, a block's beginning
 // and end about kLead.
-constexpr int kLead = 3;
+constexpr int kLead = 8;
 template <int DC>
 __device__ __forceinline__ int per_tile(const Block &k) { return k.rows > kRows ? 2 : 1; }
 template <int DC>
@@ -147,7 +147,7 @@ __device__ __forceinline__ int cost_of(const Block &k) { return kLead + k.tiles 
 template <int DC>
 struct Shared {
     alignas(8) uint64_t kfull[Shape<DC>::kStages], kempty[Shape<DC>::kStages], vfull[Shape<DC>::kStages], vempty[Shape<DC>::kStages];
-    alignas(8) uint64_t sready[2], pready[2][2], odone[2], qready, meet, last, segfull[2], segempty[2];
+    alignas(8) uint64_t sready[2][2], pready[2][2], vdone[2], qready, meet, last, segfull[2], segempty[2];
     uint32_t tmem;
     int abort;
     Segment seg[2];
@@ -474,7 +474,7 @@ struct Kernel {
         const int k16 = (a.kv.dim + 15) / 16;
         const uint32_t s_instr = tc::instruction<kBf16>(kTok, false), o_instr = tc::instruction<kBf16>(k16 * 16, true);
         const bool one = tc::elect();
-        uint32_t nk = 0, nv = 0, nq = 0, np[2] = {0, 0};
+        uint32_t nk = 0, nv = 0, nq = 0, np = 0;  // np: a bit per buffer of P, the phase of the next wait
         for (uint32_t n = 0;; ++n) {
             if (!warp_wait(sh, sh.segfull[n & 1], n >> 1 & 1, a)) return;
             const Segment &g = sh.seg[n & 1];
@@ -486,8 +486,9 @@ struct Kernel {
             if (tiles == 0) continue;
             if (!warp_wait(sh, sh.qready, nq++ & 1, a)) return;
             tc::fence_after();
+            // step s: stream s % kStreams, whose tiles alternate between two buffers
             const int steps = both ? 2 * tiles : tiles;
-            // K of the next scores is there
+            // K of a step's scores is there
             auto k_ready = [&](int s) {
                 if (both && s % S::kStreams == 1) return true;
                 const int st = nk % S::kStages;
@@ -496,58 +497,51 @@ struct Kernel {
                 return true;
             };
             auto scores = [&](int s) {
-                const int w = s % S::kStreams, st = nk % S::kStages;
+                const int w = s % S::kStreams, buf = s / S::kStreams & 1, st = nk % S::kStages;
                 const uint64_t q = tc::descriptor(qs + (both ? w * S::kQBytes : 0), 16), k = tc::descriptor(ks + st * S::kKvBytes, 16);
                 if (one) {
 #pragma unroll
                     for (int i = 0; i < DC * 4; ++i)
                         if (i < k16)
-                            tc::mma_ss(tmem + w * kTok, tc::further(q, (i >> 2) * (kRows * 128) + (i & 3) * 32),
+                            tc::mma_ss(tmem + (2 * w + buf) * kTok, tc::further(q, (i >> 2) * (kRows * 128) + (i & 3) * 32),
                                        tc::further(k, (i >> 2) * (kTok * 128) + (i & 3) * 32), s_instr, i > 0);
-                    tc::commit(smem_addr(&sh.sready[w]));
+                    tc::commit(smem_addr(&sh.sready[w][buf]));
                     if (!both || w == 1) tc::commit(smem_addr(&sh.kempty[st]));
                 }
                 if (!both || w == 1) ++nk;
             };
+            constexpr int kAhead = 2 * S::kStreams;
             bool ok = true;
-            for (int s = 0; s < S::kStreams && s < steps && ok; ++s) {
+            for (int s = 0; s < kAhead && s < steps && ok; ++s) {
                 ok = k_ready(s);
                 if (ok) scores(s);
             }
             for (int s = 0; s < steps && ok; ++s) {
-                const int w = s % S::kStreams, st = nv % S::kStages;
-                // V, and K of the stream's next tile, are waited for ahead of P
+                const int w = s % S::kStreams, buf = s / S::kStreams & 1, st = nv % S::kStages;
+                // V, and K of the buffer's next tile, are waited for ahead of P
                 if (!both || w == 0) {
                     ok = warp_wait(sh, sh.vfull[st], nv / S::kStages & 1, a);
                     tc::fence_smem();
                 }
-                if (ok && s + S::kStreams < steps) ok = k_ready(s + S::kStreams);
+                if (ok && s + kAhead < steps) ok = k_ready(s + kAhead);
                 const uint64_t v = tc::descriptor(vs + st * S::kKvBytes, kTok * 128);
-                const uint32_t p = tmem + w * kTok, o = tmem + S::kOColumn + w * (DC * 64);
-                // P comes in two halves of the tile's slots
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (ok) ok = warp_wait(sh, sh.pready[w][half], np[w] & 1, a);
-                    tc::fence_after();
-                    if (ok && one) {
-#pragma unroll
-                        for (int part = 0; part < 2; ++part)
-#pragma unroll
-                            for (int k = 0; k < kTok / 32; ++k) {
-                                const int i = half * (kTok / 32) + k;
-                                tc::mma_ts(o, p + part * (kTok / 2) + i * 8, tc::further(v, i * 2048), o_instr,
-                                           s >= S::kStreams || half > 0 || part > 0 || k > 0);
-                            }
-                    }
-                }
+                const uint32_t p = tmem + (2 * w + buf) * kTok, o = tmem + S::kOColumn + w * (DC * 64);
+                if (ok) ok = warp_wait(sh, sh.pready[w][buf], np >> (2 * w + buf) & 1, a);
+                np ^= 1u << (2 * w + buf);
                 if (!ok) break;
-                ++np[w];
+                tc::fence_after();
                 if (one) {
-                    if (s + S::kStreams >= steps) tc::commit(smem_addr(&sh.odone[w]));
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int i = 0; i < kTok / 16; ++i)
+                            tc::mma_ts(o, p + part * (kTok / 2) + i * 8, tc::further(v, i * 2048), o_instr,
+                                       s >= S::kStreams || part > 0 || i > 0);
+                    tc::commit(smem_addr(&sh.vdone[w]));
                     if (!both || w == 1) tc::commit(smem_addr(&sh.vempty[st]));
                 }
                 if (!both || w == 1) ++nv;
-                if (s + S::kStreams < steps) scores(s + S::kStreams);
+                if (s + kAhead < steps) scores(s + kAhead);
             }
             if (!ok) return;
         }
@@ -657,9 +651,11 @@ struct Kernel {
     {
         const int stream = threadIdx.x >> 7, row = threadIdx.x & 127, lane = threadIdx.x & 31;
         const uint32_t tmem = sh.tmem + (static_cast<uint32_t>(row & 96) << 16);
-        const uint32_t s_at = tmem + stream * kTok, o_at = tmem + S::kOColumn + stream * (DC * 64);
+        const uint32_t o_at = tmem + S::kOColumn + stream * (DC * 64);
         const KvView &kv = a.kv;
-        uint32_t ns = 0, no = 0, nm = 0;
+        // phases: of the buffers of S (a bit each), of the products with V, of the
+        // streams' meetings
+        uint32_t ns = 0, nv = 0, nm = 0;
         if (stream >= S::kStreams) return;
         for (uint32_t n = 0;; ++n) {
             // neither stream runs ahead: Q is one barrier's business
@@ -688,9 +684,12 @@ struct Kernel {
             const float scale = fabsf(a.scale_log2);
             float m = -INFINITY, l = 0.f;  // m: what P is relative to, less kUp
             const int first = both || S::kStreams == 1 ? 0 : stream, step = both || S::kStreams == 1 ? 1 : 2;
-            for (int j = first; j < tiles; j += step) {
-                if (!__all_sync(kFull, wait(sh, sh.sready[stream], ns++ & 1, a))) return;
+            int buf = 0;
+            for (int j = first; j < tiles; j += step, buf ^= 1) {
+                if (!__all_sync(kFull, wait(sh, sh.sready[stream][buf], ns >> buf & 1, a))) return;
+                ns ^= 1u << buf;
                 tc::fence_after();
+                const uint32_t s_at = tmem + (2 * stream + buf) * kTok;
                 float s[kTok];
 #pragma unroll
                 for (int c = 0; c < kTok; c += 32) tc::load32(s_at + c, s + c);
@@ -711,7 +710,15 @@ struct Kernel {
                 for (int i = 4; i < kTok; ++i) top[i & 3] = fmaxf(top[i & 3], s[i]);
                 const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale - kUp;
                 const bool grow = high > m + kLazy || (m == -INFINITY && high != m);
-                if (__any_sync(kFull, grow)) {
+                // The product before the last is done (these scores were issued behind
+                // it), the last one may be under way: it is waited for where O is
+                // changed, and ahead of the last P, so that no phase is missed.
+                const bool changes = __any_sync(kFull, grow);
+                if (j != first && (changes || j + step >= tiles) &&
+                    !__all_sync(kFull, wait(sh, sh.vdone[stream], (nv & 1) ^ 1, a)))
+                    return;
+                if (changes) {
+                    tc::fence_after();
                     const float to = grow ? high : m;
                     const float f = grow ? exp2_approx(m - (to == -INFINITY ? 0.f : to)) : 1.f;
                     if (j != first) scale_o(o_at, f, kv.dim);
@@ -733,21 +740,20 @@ struct Kernel {
                     }
                     tc::store16(s_at + c / 2, hi);
                     tc::store16(s_at + kTok / 2 + c / 2, lo);
-                    if (c + 32 == kTok / 2 || c + 32 == kTok) {  // half of P is there
-                        tc::wait_st();
-                        tc::fence_before();
-                        mbar_arrive(smem_addr(&sh.pready[stream][c + 32 == kTok]));
-                    }
                 }
+                tc::wait_st();
+                tc::fence_before();
+                mbar_arrive(smem_addr(&sh.pready[stream][buf]));
+                ++nv;
                 const float2 sums = apart(add2(sum[0], sum[1]));
                 l += sums.x + sums.y;
             }
             const bool any = first < tiles;
-            if (any && !__all_sync(kFull, wait(sh, sh.odone[stream], no++ & 1, a))) return;
+            if (any && !__all_sync(kFull, wait(sh, sh.vdone[stream], (nv & 1) ^ 1, a))) return;
             tc::fence_after();
             float own = 1.f, other = 0.f;  // factors of this stream's O and the other's
             const bool join = !both && S::kStreams == 2 && tiles > 1;
-            float *buf = reinterpret_cast<float *>(q_generic);  // [dim][rows]
+            float *shared_o = reinterpret_cast<float *>(q_generic);  // [dim][rows]
             if (join) {
                 if (!all_softmax(a, sh, nm)) return;  // both streams are done with Q
                 if (stream == 1) {
@@ -759,7 +765,7 @@ struct Kernel {
                         tc::wait_ld();
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            if (c + i < kv.dim) buf[(c + i) * kRows + row] = x[i];
+                            if (c + i < kv.dim) shared_o[(c + i) * kRows + row] = x[i];
                     }
                 }
                 if (!all_softmax(a, sh, nm)) return;
@@ -771,7 +777,7 @@ struct Kernel {
                     m = mm;
                 }
             }
-            if (both || stream == 0) finish(a, g, o_at, any, stream, row, live, token, head, m, l, own, other, join ? buf : nullptr);
+            if (both || stream == 0) finish(a, g, o_at, any, stream, row, live, token, head, m, l, own, other, join ? shared_o : nullptr);
             tc::fence_before();
             // (the buffer is Q's again once the streams have met for the next segment)
         }
@@ -865,10 +871,11 @@ struct Kernel {
                 mbar_init(smem_addr(&sh.vempty[i]), 1);
             }
             for (int i = 0; i < 2; ++i) {
-                mbar_init(smem_addr(&sh.sready[i]), 1);
-                mbar_init(smem_addr(&sh.pready[i][0]), kRows);
-                mbar_init(smem_addr(&sh.pready[i][1]), kRows);
-                mbar_init(smem_addr(&sh.odone[i]), 1);
+                for (int k = 0; k < 2; ++k) {
+                    mbar_init(smem_addr(&sh.sready[i][k]), 1);
+                    mbar_init(smem_addr(&sh.pready[i][k]), kRows);
+                }
+                mbar_init(smem_addr(&sh.vdone[i]), 1);
                 mbar_init(smem_addr(&sh.segfull[i]), 1);
                 mbar_init(smem_addr(&sh.segempty[i]), 4 + 1 + 4 * S::kStreams);
             }
