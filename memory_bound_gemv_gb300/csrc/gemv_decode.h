@@ -96,7 +96,7 @@ struct SpanArgs {
     int q_heads, group;
     int window, sinks;
     float scale_log2;
-    int out_vec;                // out takes 16-byte stores
+    int out_vec;                // out takes stores of 16 bytes (1), of 32 (2)
     unsigned int *err;
     // workspace
     float *part;                // [2 * ctas][part_stride]: per tile of rows O [dim / 4][row][4], m and l [row]

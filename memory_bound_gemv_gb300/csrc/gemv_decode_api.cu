@@ -143,6 +143,13 @@ void place_span(SpanArgs *a, const SpanPlan &p, void *workspace)
     a->redo = ws + p.redo;
 }
 
+// Stores of how many 16 bytes at once an output's rows take.
+int out_vec(const gemv_heads_t &h)
+{
+    if (!aligned(h.data, 16) || !mult8(h.stride, 2)) return 0;
+    return aligned(h.data, 32) && h.stride[0] % 16 == 0 && h.stride[1] % 16 == 0 ? 2 : 1;
+}
+
 bool too_many_rows(int64_t tokens, int q_heads) { return tokens > INT_MAX / 64 || tokens * q_heads > INT_MAX; }
 
 // prefix: the slots before *prefix are attended to by a launch of their own, whose
@@ -214,7 +221,7 @@ gemv_status_t attn_paged(const gemv_kv_t *kv, const gemv_attn_t *args, const int
         place_span(&g, sp, mine);
         g.q = a.q, g.q_st = a.q_sb, g.q_sh = a.q_sh;
         g.out = a.out, g.o_st = a.o_sb, g.o_sh = a.o_sh;
-        g.out_vec = aligned(out.data, 16) && mult8(out.stride, 2);
+        g.out_vec = out_vec(out);
         g.lse = a.lse;
         g.pre = reinterpret_cast<float *>(mine + sp.pre);
         g.own = a.own = reinterpret_cast<float *>(mine + sp.own);
@@ -394,7 +401,7 @@ gemv_status_t gemv_attn_prompt(const gemv_kv_t *kv, const gemv_prompt_t *g, void
     a.sinks = g->sinks;
     a.scale_log2 = g->scale * 1.4426950408889634f;
     a.err = dev.status;
-    a.out_vec = aligned(g->out.data, 16) && mult8(g->out.stride, 2);
+    a.out_vec = out_vec(g->out);
     place_span(&a, p, g->workspace);
     const bool vec = cache_vec(kv) && aligned(g->q.data, 16) && mult8(g->q.stride, 2);
     cudaError_t e = launch_span(a, vec, kv->elem, dev.sm_count, static_cast<cudaStream_t>(stream));

@@ -56,12 +56,15 @@ __device__ __forceinline__ bool elect()
     return p != 0;
 }
 
-// kind::f16 with FP32 accumulators: M = 128 rows, N columns.
+// A value that all lanes of a warp have, which the compiler then keeps once per warp.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
+// kind::f16 with FP32 accumulators: M = 128 rows, N columns; with `minus` -A B.
 template <bool BF16>
-__device__ __forceinline__ uint32_t instruction(int n, bool b_along_n)
+__device__ __forceinline__ uint32_t instruction(int n, bool b_along_n, bool minus)
 {
     const uint32_t type = BF16 ? 1u : 0u;
-    return 1u << 4 | type << 7 | type << 10 | (b_along_n ? 1u << 16 : 0u) | static_cast<uint32_t>(n >> 3) << 17 |
+    return 1u << 4 | type << 7 | type << 10 | (minus ? 1u << 13 : 0u) | (b_along_n ? 1u << 16 : 0u) | static_cast<uint32_t>(n >> 3) << 17 |
            static_cast<uint32_t>(128 >> 4) << 24;
 }
 

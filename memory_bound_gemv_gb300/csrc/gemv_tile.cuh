@@ -21,7 +21,9 @@
 //                   swizzled shared memory, so that pages of any size, strides and
 //                   unaligned pools take one path;
 //   warp 12         one thread issues the products;
-//   warp 13         looks up what the block does next.
+//   warp 13         looks up what the block does next;
+//   warps 14, 15    make the copied K and V visible to the tensor core (a fence of
+//                   some 0.2 us, during which the products would pause).
 // While one stream's softmax runs, the other's products do.  The streams are two
 // tiles of rows over the same slots, or with up to 128 rows one tile of
 // rows over even and odd tiles of slots, joined at the end.  (Head sizes above
@@ -55,6 +57,7 @@ namespace tile {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kThreads = 512, kRows = 128;
+constexpr uint32_t kSegs = 4;  // segments looked up ahead
 constexpr uint64_t kWaitNs = 1000000000ull;
 
 __device__ __forceinline__ float exp2_approx(float x)
@@ -68,10 +71,11 @@ __device__ __forceinline__ float exp2_approx(float x)
 template <int DC>
 struct Shape {
     static constexpr int kStreams = DC <= 2 ? 2 : 1;
-    static constexpr int kTok = 64;                  // slots of a tile
+    static constexpr int kTok = DC <= 2 ? 128 : 64;  // slots of a tile
+    static constexpr int kBufs = DC <= 2 ? 1 : 2;    // tiles of S or P that a stream has in tensor memory
     static constexpr int kQBytes = kRows * DC * 128; // a tile of rows
     static constexpr int kKvBytes = kTok * DC * 128;
-    static constexpr int kStages = DC == 1 ? 8 : DC == 2 ? 4 : DC == 3 ? 3 : 2;  // tiles of K, and of V, in shared memory
+    static constexpr int kStages = DC == 1 ? 4 : DC == 3 ? 3 : 2;  // tiles of K, and of V, in shared memory
     static constexpr int kBlock = kStreams * kRows;  // rows of a block
     static constexpr int kOColumn = 256;
 };
@@ -136,21 +140,23 @@ __device__ __forceinline__ Block block_of(const SpanArgs &a, const span::Seq &s,
     return k;
 }
 
-// Costs: a tile of slots takes one unit per tile of rows, a block's beginning
-// and end about kLead.
-constexpr int kLead = 8;
+// Costs, in units of some 0.5 us: a tile of slots for two tiles of rows, for
+// one, and a block's beginning and end.
+constexpr int kLead = 12;
 template <int DC>
-__device__ __forceinline__ int per_tile(const Block &k) { return k.rows > kRows ? 2 : 1; }
+__device__ __forceinline__ int per_tile(const Block &k) { return k.rows > kRows ? 5 : 4; }
 template <int DC>
 __device__ __forceinline__ int cost_of(const Block &k) { return kLead + k.tiles * per_tile<DC>(k); }
 
 template <int DC>
 struct Shared {
-    alignas(8) uint64_t kfull[Shape<DC>::kStages], kempty[Shape<DC>::kStages], vfull[Shape<DC>::kStages], vempty[Shape<DC>::kStages];
-    alignas(8) uint64_t sready[2][2], pready[2][2], vdone[2], qready, meet, last, segfull[2], segempty[2];
+    // of each place in the rings of K and V: copied; visible to the tensor core; free
+    alignas(8) uint64_t kthere[Shape<DC>::kStages], kfull[Shape<DC>::kStages], kempty[Shape<DC>::kStages];
+    alignas(8) uint64_t vthere[Shape<DC>::kStages], vfull[Shape<DC>::kStages], vempty[Shape<DC>::kStages];
+    alignas(8) uint64_t sready[2][2], pready[2][2], vdone[2], qready, meet, last, segfull[kSegs], segempty[kSegs];
     uint32_t tmem;
     int abort;
-    Segment seg[2];
+    Segment seg[kSegs];
     Limits lim;
     Cursor first;     // where the CTA's share begins
     int found;
@@ -173,25 +179,9 @@ struct Kernel {
     // P is at most 2^kLazy times kUp: in f16 below 2^16
     static constexpr float kLazy = kBf16 ? 8.f : 4.f, kUp = kBf16 ? 0.f : 11.f;
 
-    // Gives up after kWaitNs.  The clock is read once in 256 tries: a tile takes
-    // some ten waits one behind the other, and each reading some 0.5 us.
     static __device__ __forceinline__ bool wait(Shared<DC> &sh, uint64_t &bar, uint32_t parity, const SpanArgs &a)
     {
-        uint64_t since = 0;
-        for (uint32_t i = 0;; ++i) {
-            uint32_t done;
-            asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-                         : "=r"(done)
-                         : "r"(smem_addr(&bar)), "r"(parity)
-                         : "memory");
-            if (done) return true;
-            if ((i & 255) != 255) continue;
-            const uint64_t now = global_timer_ns();
-            if (since == 0)
-                since = now;
-            else if (now - since > kWaitNs)
-                break;
-        }
+        if (mbar_wait_bounded(smem_addr(&bar), parity, kWaitNs)) return true;
         report_error(a.err, DEVERR_TIMEOUT);
         sh.abort = 1;
         return false;
@@ -277,7 +267,7 @@ struct Kernel {
     {
         if (x <= r0) return 0;
         if (x >= r0 + cost_of<DC>(k)) return k.tiles;
-        const int t = (static_cast<int>(x - r0) - kLead) >> (per_tile<DC>(k) - 1);
+        const int t = max(0, static_cast<int>(x - r0) - kLead) / per_tile<DC>(k);
         return t <= near ? 0 : k.tiles - t <= near ? k.tiles : t;
     }
 
@@ -343,27 +333,27 @@ struct Kernel {
         asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
     }
 
-    // One tile of K or V: this warp's quarter of its slots, whose rows begin at
-    // `row` (a lane each; -1: zeros).
-    static __device__ __forceinline__ void load_tile(uint32_t dst, const uint16_t *base, int64_t row, int dim, int warp, int lane)
+    // OWN of ROWS rows in shared memory, from row0 on: those that begin at `at`
+    // (a lane each; -1: zeros).
+    template <int OWN, int ROWS>
+    static __device__ __forceinline__ void load_rows(uint32_t dst, const uint16_t *base, int64_t at, int dim, int row0, int lane)
     {
-        constexpr int kOwn = kTok / 4;                            // slots of a warp
-        constexpr int kLanes = DC == 1 ? 8 : DC == 2 ? 16 : 32;   // of a slot
+        constexpr int kLanes = DC == 1 ? 8 : DC == 2 ? 16 : 32;   // of a row
         constexpr int kAtOnce = 32 / kLanes;
         const int chunk = lane % kLanes, sub = lane / kLanes;
 #pragma unroll 4
-        for (int i = 0; i < kOwn; i += kAtOnce) {
+        for (int i = 0; i < OWN; i += kAtOnce) {
             const int own = i + sub;
-            const int64_t at = __shfl_sync(kFull, row, own);
+            const int64_t from = __shfl_sync(kFull, at, own);
             if (chunk >= DC * 8) continue;
-            const int left = at >= 0 ? dim - chunk * 8 : 0;
-            const uint32_t to = dst + swizzled(kTok, warp * kOwn + own, chunk);
-            const uint16_t *from = base + (left > 0 ? at + chunk * 8 : 0);
+            const int left = from >= 0 ? dim - chunk * 8 : 0;
+            const uint32_t to = dst + swizzled(ROWS, row0 + own, chunk);
+            const uint16_t *p = base + (left > 0 ? from + chunk * 8 : 0);
             if (VEC) {
-                asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(left > 0 ? 16 : 0)
+                asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(p), "r"(left > 0 ? 16 : 0)
                              : "memory");
             } else {
-                st_shared(to, left > 0 ? load8(from, left) : make_uint4(0, 0, 0, 0));
+                st_shared(to, left > 0 ? load8(p, left) : make_uint4(0, 0, 0, 0));
             }
         }
     }
@@ -384,8 +374,8 @@ struct Kernel {
         auto free_place = [&](uint64_t &bar, uint32_t parity) { return static_cast<bool>(__all_sync(kFull, wait(sh, bar, parity, a))); };
         uint32_t nk = 0, nv = 0;
         for (uint32_t n = 0;; ++n) {
-            if (!__all_sync(kFull, wait(sh, sh.segfull[n & 1], n >> 1 & 1, a))) break;
-            const Segment &g = sh.seg[n & 1];
+            if (!__all_sync(kFull, wait(sh, sh.segfull[n % kSegs], n / kSegs & 1, a))) break;
+            const Segment &g = sh.seg[n % kSegs];
             if (g.stop) break;
             const int32_t *table = kv.table + g.seq.b * kv.table_stride;
             const int t0 = g.t0, t1 = g.t1, sink_tiles = g.block.sink_tiles, skip = g.block.skip;
@@ -393,7 +383,7 @@ struct Kernel {
             const uint16_t *kb = static_cast<const uint16_t *>(kv.k) + g.h * kv.ks_head;
             const uint16_t *vb = static_cast<const uint16_t *>(kv.v) + g.h * kv.vs_head;
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sh.segempty[n & 1]));
+            if (lane == 0) mbar_arrive(smem_addr(&sh.segempty[n % kSegs]));
             bool ok = true;
             // this lane's slot of a tile: its page (-1: none) and place there
             auto look_up = [&](int j, int &off) {
@@ -427,16 +417,18 @@ struct Kernel {
                     const int st = nk % S::kStages;
                     ok = free_place(sh.kempty[st], (nk / S::kStages & 1) ^ 1);
                     if (!ok) break;
-                    load_tile(ks + st * S::kKvBytes, kb, page_k < 0 ? -1 : page_k * kv.ks_page + off_k * kv.ks_tok, kv.dim, warp, lane);
-                    issued(sh.kfull[st]);
+                    load_rows<kOwn, kTok>(ks + st * S::kKvBytes, kb, page_k < 0 ? -1 : page_k * kv.ks_page + off_k * kv.ks_tok, kv.dim,
+                                          warp * kOwn, lane);
+                    issued(sh.kthere[st]);
                     ++nk;
                 }
                 if (j > t0) {
                     const int st = nv % S::kStages;
                     ok = free_place(sh.vempty[st], (nv / S::kStages & 1) ^ 1);
                     if (!ok) break;
-                    load_tile(vs + st * S::kKvBytes, vb, page_v < 0 ? -1 : page_v * kv.vs_page + off_v * kv.vs_tok, kv.dim, warp, lane);
-                    issued(sh.vfull[st]);
+                    load_rows<kOwn, kTok>(vs + st * S::kKvBytes, vb, page_v < 0 ? -1 : page_v * kv.vs_page + off_v * kv.vs_tok, kv.dim,
+                                          warp * kOwn, lane);
+                    issued(sh.vthere[st]);
                     ++nv;
                 }
                 page_v = page_k;
@@ -452,6 +444,23 @@ struct Kernel {
 
     // --------------------------------------------------------------- products
 
+    // Tiles that have been copied (to `there`) are made visible to the tensor core.
+    static __device__ void pass_on(const SpanArgs &a, Shared<DC> &sh, uint64_t *there, uint64_t *full)
+    {
+        uint32_t n = 0;
+        for (uint32_t k = 0;; ++k) {
+            if (!wait(sh, sh.segfull[k % kSegs], k / kSegs & 1, a)) return;
+            if (sh.seg[k % kSegs].stop) return;
+            const int tiles = sh.seg[k % kSegs].t1 - sh.seg[k % kSegs].t0;
+            mbar_arrive(smem_addr(&sh.segempty[k % kSegs]));
+            for (int j = 0; j < tiles; ++j, ++n) {
+                if (!wait(sh, there[n % S::kStages], n / S::kStages & 1, a)) return;
+                tc::fence_smem();
+                mbar_arrive(smem_addr(&full[n % S::kStages]));
+            }
+        }
+    }
+
     // One warp issues all products; none is under way when it leaves.
     static __device__ void products(const SpanArgs &a, Shared<DC> &sh, uint32_t qs, uint32_t ks, uint32_t vs)
     {
@@ -466,81 +475,81 @@ struct Kernel {
         return __all_sync(kFull, wait(sh, bar, parity, a));
     }
 
-    // The operands' descriptors differ by constants within a tile, the loops are
-    // unrolled: an instruction of 64 cycles has to be issued in less.
+    // The whole warp goes through this with the same values, so that operands and
+    // descriptors are kept once per warp, as the instruction takes them; they
+    // differ by constants within a tile, and the loops are unrolled.  An
+    // instruction of 64 cycles has to be issued in less: by one thread of
+    // a diverged warp it takes 90.
     static __device__ void issue(const SpanArgs &a, Shared<DC> &sh, uint32_t qs, uint32_t ks, uint32_t vs)
     {
-        const uint32_t tmem = sh.tmem;
+        const int lane = threadIdx.x & 31;
+        const uint32_t tmem = tc::uniform(sh.tmem);
+        qs = tc::uniform(qs), ks = tc::uniform(ks), vs = tc::uniform(vs);
         const int k16 = (a.kv.dim + 15) / 16;
-        const uint32_t s_instr = tc::instruction<kBf16>(kTok, false), o_instr = tc::instruction<kBf16>(k16 * 16, true);
-        const bool one = tc::elect();
+        // (a negative scale: the scores' signs change, the softmax goes by its size)
+        const uint32_t s_instr = tc::instruction<kBf16>(kTok, false, a.scale_log2 < 0.f);
+        const uint32_t o_instr = tc::instruction<kBf16>(k16 * 16, true, false);
         uint32_t nk = 0, nv = 0, nq = 0, np = 0;  // np: a bit per buffer of P, the phase of the next wait
         for (uint32_t n = 0;; ++n) {
-            if (!warp_wait(sh, sh.segfull[n & 1], n >> 1 & 1, a)) return;
-            const Segment &g = sh.seg[n & 1];
-            if (g.stop) return;
-            const int tiles = g.t1 - g.t0;
-            const bool both = g.block.rows > kRows;
-            __syncwarp();
-            if (one) mbar_arrive(smem_addr(&sh.segempty[n & 1]));
+            if (!warp_wait(sh, sh.segfull[n % kSegs], n / kSegs & 1, a)) return;
+            const Segment &g = sh.seg[n % kSegs];
+            if (tc::uniform(g.stop)) return;
+            const int tiles = tc::uniform(g.t1 - g.t0);
+            const bool both = tc::uniform(g.block.rows > kRows);
+            if (tc::elect()) mbar_arrive(smem_addr(&sh.segempty[n % kSegs]));
             if (tiles == 0) continue;
             if (!warp_wait(sh, sh.qready, nq++ & 1, a)) return;
             tc::fence_after();
-            // step s: stream s % kStreams, whose tiles alternate between two buffers
+            // step s: stream s % kStreams, whose tiles go through its buffers in turn
             const int steps = both ? 2 * tiles : tiles;
-            // K of a step's scores is there
-            auto k_ready = [&](int s) {
-                if (both && s % S::kStreams == 1) return true;
-                const int st = nk % S::kStages;
-                if (!warp_wait(sh, sh.kfull[st], nk / S::kStages & 1, a)) return false;
-                tc::fence_smem();  // what the loaders wrote, for the tensor core
-                return true;
-            };
             auto scores = [&](int s) {
-                const int w = s % S::kStreams, buf = s / S::kStreams & 1, st = nk % S::kStages;
+                const int w = s % S::kStreams, buf = s / S::kStreams % S::kBufs, st = nk % S::kStages;
                 const uint64_t q = tc::descriptor(qs + (both ? w * S::kQBytes : 0), 16), k = tc::descriptor(ks + st * S::kKvBytes, 16);
-                if (one) {
+                const uint32_t d = tmem + (w * S::kBufs + buf) * kTok;
+                const bool last = !both || w == 1;  // of those that read this tile
+                if (tc::elect()) {
 #pragma unroll
                     for (int i = 0; i < DC * 4; ++i)
                         if (i < k16)
-                            tc::mma_ss(tmem + (2 * w + buf) * kTok, tc::further(q, (i >> 2) * (kRows * 128) + (i & 3) * 32),
+                            tc::mma_ss(d, tc::further(q, (i >> 2) * (kRows * 128) + (i & 3) * 32),
                                        tc::further(k, (i >> 2) * (kTok * 128) + (i & 3) * 32), s_instr, i > 0);
                     tc::commit(smem_addr(&sh.sready[w][buf]));
-                    if (!both || w == 1) tc::commit(smem_addr(&sh.kempty[st]));
+                    if (last) tc::commit(smem_addr(&sh.kempty[st]));
                 }
-                if (!both || w == 1) ++nk;
+                if (last) ++nk;
             };
-            constexpr int kAhead = 2 * S::kStreams;
+            constexpr int kAhead = S::kBufs * S::kStreams;
             bool ok = true;
             for (int s = 0; s < kAhead && s < steps && ok; ++s) {
-                ok = k_ready(s);
+                if (!both || s % S::kStreams == 0) ok = warp_wait(sh, sh.kfull[nk % S::kStages], nk / S::kStages & 1, a);
                 if (ok) scores(s);
             }
             for (int s = 0; s < steps && ok; ++s) {
-                const int w = s % S::kStreams, buf = s / S::kStreams & 1, st = nv % S::kStages;
-                // V, and K of the buffer's next tile, are waited for ahead of P
-                if (!both || w == 0) {
-                    ok = warp_wait(sh, sh.vfull[st], nv / S::kStages & 1, a);
-                    tc::fence_smem();
-                }
-                if (ok && s + kAhead < steps) ok = k_ready(s + kAhead);
-                const uint64_t v = tc::descriptor(vs + st * S::kKvBytes, kTok * 128);
-                const uint32_t p = tmem + (2 * w + buf) * kTok, o = tmem + S::kOColumn + w * (DC * 64);
-                if (ok) ok = warp_wait(sh, sh.pready[w][buf], np >> (2 * w + buf) & 1, a);
-                np ^= 1u << (2 * w + buf);
+                const int w = s % S::kStreams, buf = s / S::kStreams % S::kBufs, st = nv % S::kStages, b = w * S::kBufs + buf;
+                // P, V and K of the buffer's next tile are waited for at once, a lane each
+                const bool begins = !both || w == 0;  // of the steps that read these tiles
+                uint64_t *bar = &sh.pready[w][buf];
+                uint32_t parity = np >> b & 1;
+                if (lane == 1 && begins) bar = &sh.vfull[st], parity = nv / S::kStages & 1;
+                if (lane == 2 && begins && s + kAhead < steps) bar = &sh.kfull[nk % S::kStages], parity = nk / S::kStages & 1;
+                ok = warp_wait(sh, *bar, parity, a);
+                np ^= 1u << b;
                 if (!ok) break;
                 tc::fence_after();
-                if (one) {
+                const uint64_t v = tc::descriptor(vs + st * S::kKvBytes, kTok * 128);
+                const uint32_t p = tmem + b * kTok, o = tmem + S::kOColumn + w * (DC * 64);
+                const bool add = s >= S::kStreams, last = !both || w == 1;
+                if (tc::elect()) {
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
 #pragma unroll
                         for (int i = 0; i < kTok / 16; ++i)
-                            tc::mma_ts(o, p + part * (kTok / 2) + i * 8, tc::further(v, i * 2048), o_instr,
-                                       s >= S::kStreams || part > 0 || i > 0);
+                            tc::mma_ts(o, p + i / 2 * 32 + part * 16 + i % 2 * 8, tc::further(v, i * 2048), o_instr,
+                                       add || part > 0 || i > 0);
                     tc::commit(smem_addr(&sh.vdone[w]));
-                    if (!both || w == 1) tc::commit(smem_addr(&sh.vempty[st]));
+                    if (last) tc::commit(smem_addr(&sh.vempty[st]));
                 }
-                if (!both || w == 1) ++nv;
+                if (last) ++nv;
                 if (s + kAhead < steps) scores(s + kAhead);
             }
             if (!ok) return;
@@ -603,26 +612,28 @@ struct Kernel {
         return r;
     }
 
-    // A warp's 32 rows of Q, whose first elements are `at` (a lane each; -1:
-    // zeros), into shared memory; `flip` changes the sign.
-    static __device__ __forceinline__ void load_q(const uint16_t *q, int64_t at, uint32_t dst, int dim, int row0, int lane, uint32_t flip)
+    // This thread's row of a segment: a query head of a token.
+    struct Row {
+        bool live;
+        int token, head;
+    };
+    static __device__ __forceinline__ Row row_of(const SpanArgs &a, const Segment &g, int stream, int row)
     {
-        constexpr int kLanes = DC == 1 ? 8 : DC == 2 ? 16 : 32, kAtOnce = 32 / kLanes, kBatch = 8;
-        const int chunk = lane % kLanes, sub = lane / kLanes;
-#pragma unroll 1
-        for (int i0 = 0; i0 < 32; i0 += kBatch * kAtOnce) {
-            uint4 v[kBatch];
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int64_t from = __shfl_sync(kFull, at, (i0 + k * kAtOnce + sub) & 31);
-                v[k] = from >= 0 && chunk * 8 < dim ? load8(q + from + chunk * 8, dim - chunk * 8) : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                v[k].x ^= flip, v[k].y ^= flip, v[k].z ^= flip, v[k].w ^= flip;
-                if (chunk < DC * 8) st_shared(dst + swizzled(kRows, row0 + i0 + k * kAtOnce + sub, chunk), v[k]);
-            }
-        }
+        Row r;
+        const int i = g.row0 + (g.block.rows > kRows ? stream * kRows : 0) + row;
+        r.live = i < g.row0 + g.block.rows;
+        r.token = r.live ? i / a.group : 0;
+        r.head = g.h * a.group + (r.live ? i - r.token * a.group : 0);
+        return r;
+    }
+
+    // Requests a warp's 32 rows of Q (those of stream 1 only where it has rows of its own).
+    static __device__ __forceinline__ void load_q(const SpanArgs &a, const Segment &g, const Row &r, uint32_t qs, int stream, int row, int lane)
+    {
+        const bool both = g.block.rows > kRows;
+        if (g.t0 == g.t1 || (!both && stream == 1)) return;
+        const int64_t at = r.live ? (g.seq.q0 + r.token) * a.q_st + r.head * a.q_sh : -1;
+        load_rows<32, kRows>(qs + (both ? stream * S::kQBytes : 0), static_cast<const uint16_t *>(a.q), at, a.kv.dim, row & 96, lane);
     }
 
     // Multiplies this warp's rows of O by f.
@@ -657,44 +668,38 @@ struct Kernel {
         // streams' meetings
         uint32_t ns = 0, nv = 0, nm = 0;
         if (stream >= S::kStreams) return;
-        for (uint32_t n = 0;; ++n) {
+        if (!next_segment(a, sh, 0, stream, row, lane, qs)) return;
+        for (uint32_t n = 0; !sh.seg[n % kSegs].stop; ++n) {
+            // (what a loop over the tiles does not need is looked up again behind it:
+            // 128 scores leave few registers)
+            const Segment &g = sh.seg[n % kSegs];
+            const int tiles = g.t1 - g.t0, from = g.t0, sink_tiles = g.block.sink_tiles, skip = g.block.skip;
+            const bool both = g.block.rows > kRows;
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            tc::fence_smem();
             // neither stream runs ahead: Q is one barrier's business
             if (S::kStreams == 2 && !all_softmax(a, sh, nm)) return;
-            if (!__all_sync(kFull, wait(sh, sh.segfull[n & 1], n >> 1 & 1, a))) return;
-            if (sh.seg[n & 1].stop) return;
-            const Segment g = sh.seg[n & 1];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sh.segempty[n & 1]));
-            const int tiles = g.t1 - g.t0;
-            const bool both = g.block.rows > kRows;
-            // this thread's row: a query head of a token
-            const int r = g.row0 + (both ? stream * kRows : 0) + row;
-            const bool live = r < g.row0 + g.block.rows;
-            const int token = live ? r / a.group : 0, head = g.h * a.group + (live ? r - token * a.group : 0);
-            if (tiles > 0 && (both || stream == 0)) {
-                const int64_t at = live ? (g.seq.q0 + token) * a.q_st + head * a.q_sh : -1;
-                load_q(static_cast<const uint16_t *>(a.q), at, qs + (both ? stream * S::kQBytes : 0), kv.dim, row & 96, lane,
-                       a.scale_log2 < 0.f ? 0x80008000u : 0u);
-                tc::fence_smem();
-            }
             if (tiles > 0) mbar_arrive(smem_addr(&sh.qready));
             // rows that do not exist see everything, of which nothing is kept
             span::Seen seen = {0, INT32_MAX};
-            if (live) seen = span::seen_by(a, g.seq, token);
+            {
+                const Row r = row_of(a, g, stream, row);
+                if (r.live) seen = span::seen_by(a, g.seq, r.token);
+            }
             const float scale = fabsf(a.scale_log2);
             float m = -INFINITY, l = 0.f;  // m: what P is relative to, less kUp
             const int first = both || S::kStreams == 1 ? 0 : stream, step = both || S::kStreams == 1 ? 1 : 2;
             int buf = 0;
-            for (int j = first; j < tiles; j += step, buf ^= 1) {
+            for (int j = first; j < tiles; j += step, buf = S::kBufs - 1 - buf) {
                 if (!__all_sync(kFull, wait(sh, sh.sready[stream][buf], ns >> buf & 1, a))) return;
                 ns ^= 1u << buf;
                 tc::fence_after();
-                const uint32_t s_at = tmem + (2 * stream + buf) * kTok;
+                const uint32_t s_at = tmem + (S::kBufs * stream + buf) * kTok;
                 float s[kTok];
 #pragma unroll
                 for (int c = 0; c < kTok; c += 32) tc::load32(s_at + c, s + c);
                 tc::wait_ld();
-                const int jj = g.t0 + j, t0 = (jj < g.block.sink_tiles ? jj : jj + g.block.skip) * kTok;
+                const int jj = from + j, t0 = (jj < sink_tiles ? jj : jj + skip) * kTok;
                 const bool clear = t0 + kTok <= seen.hi && (t0 >= seen.lo || t0 + kTok <= a.sinks);
                 if (!__all_sync(kFull, clear)) {
 #pragma unroll
@@ -711,7 +716,7 @@ struct Kernel {
                 const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale - kUp;
                 const bool grow = high > m + kLazy || (m == -INFINITY && high != m);
                 // The product before the last is done (these scores were issued behind
-                // it), the last one may be under way: it is waited for where O is
+                // it), with two buffers the last one may be under way: it is waited for where O is
                 // changed, and ahead of the last P, so that no phase is missed.
                 const bool changes = __any_sync(kFull, grow);
                 if (j != first && (changes || j + step >= tiles) &&
@@ -728,6 +733,8 @@ struct Kernel {
                 const float ref = m == -INFINITY ? 0.f : m;
                 const uint64_t scale2 = two(scale, scale), ref2 = two(-ref, -ref);
                 uint64_t sum[2] = {0, 0};
+                // the P of 32 scores takes their place: 16 columns of first parts, 16 of
+                // second ones
 #pragma unroll
                 for (int c = 0; c < kTok; c += 32) {
                     uint32_t hi[16], lo[16];
@@ -738,8 +745,8 @@ struct Kernel {
                         sum[i & 1] = add2(sum[i & 1], two(p0, p1));
                         split(p0, p1, hi[i], lo[i]);
                     }
-                    tc::store16(s_at + c / 2, hi);
-                    tc::store16(s_at + kTok / 2 + c / 2, lo);
+                    tc::store16(s_at + c, hi);
+                    tc::store16(s_at + c + 16, lo);
                 }
                 tc::wait_st();
                 tc::fence_before();
@@ -777,10 +784,30 @@ struct Kernel {
                     m = mm;
                 }
             }
-            if (both || stream == 0) finish(a, g, o_at, any, stream, row, live, token, head, m, l, own, other, join ? shared_o : nullptr);
+            // The next segment's Q is requested before the present rows are
+            // written; the streams' joint buffer lies where it goes.
+            if (!join && !next_segment(a, sh, n + 1, stream, row, lane, qs)) return;
+            if (both || stream == 0) {
+                const Row r = row_of(a, g, stream, row);
+                finish(a, g, o_at, any, stream, row, r.live, r.token, r.head, m, l, own, other, join ? shared_o : nullptr);
+            }
             tc::fence_before();
-            // (the buffer is Q's again once the streams have met for the next segment)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.segempty[n % kSegs]));
+            if (join) {
+                if (!all_softmax(a, sh, nm)) return;
+                if (!next_segment(a, sh, n + 1, stream, row, lane, qs)) return;
+            }
         }
+    }
+
+    // Waits for a segment and requests its Q.
+    static __device__ __forceinline__ bool next_segment(const SpanArgs &a, Shared<DC> &sh, uint32_t n, int stream, int row, int lane, uint32_t qs)
+    {
+        if (!__all_sync(kFull, wait(sh, sh.segfull[n % kSegs], n / kSegs & 1, a))) return false;
+        const Segment &g = sh.seg[n % kSegs];
+        if (!g.stop) load_q(a, g, row_of(a, g, stream, row), qs, stream, row, lane);
+        return true;
     }
 
     // Writes a row: its output, its part of the prefix, or a part of a cut block.
@@ -809,30 +836,34 @@ struct Kernel {
             }
             if (live) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) nan = nan || (c + i < dim && x[i] != x[i]);
-            if (g.slot >= 0) {
+                for (int i = 0; i < 16; ++i) nan = nan || (c + i < dim && x[i] != x[i]);
+                if (g.slot >= 0) {
 #pragma unroll
-                for (int i = 0; i < 16; i += 4)
-                    *reinterpret_cast<float4 *>(part + ((c + i) / 4 * kRows + row) * 4) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-            } else if (a.pre) {
-                float *p = a.pre + index * span_row(dim) + c;
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (c + i < dim) p[i] = x[i];
-            } else {
-                uint16_t *p = static_cast<uint16_t *>(a.out) + t * a.o_st + head * a.o_sh + c;
-                uint32_t w[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = pack(x[2 * i] * inv, x[2 * i + 1] * inv);
-                if (a.out_vec && c + 16 <= dim) {
-                    reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                    reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                } else {
+                    for (int i = 0; i < 16; i += 4)
+                        *reinterpret_cast<float4 *>(part + ((c + i) / 4 * kRows + row) * 4) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                } else if (a.pre) {
+                    float *p = a.pre + index * span_row(dim) + c;
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        if (c + i < dim) p[i] = static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16));
+                        if (c + i < dim) p[i] = x[i];
+                } else {
+                    uint16_t *p = static_cast<uint16_t *>(a.out) + t * a.o_st + head * a.o_sh + c;
+                    uint32_t w[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) w[i] = pack(x[2 * i] * inv, x[2 * i + 1] * inv);
+                    if (a.out_vec == 2 && c + 16 <= dim) {  // a whole sector
+                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                                     : "memory");
+                    } else if (a.out_vec && c + 16 <= dim) {
+                        reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                        reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (c + i < dim) p[i] = static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16));
+                    }
                 }
-            }
             }
         }
         __syncwarp();
@@ -862,11 +893,13 @@ struct Kernel {
         unsigned char *kgen = base + S::kStreams * S::kQBytes;
         Shared<DC> &sh = *reinterpret_cast<Shared<DC> *>(kgen + 2 * S::kStages * S::kKvBytes);
         const uint32_t qs = smem_addr(base), ks = smem_addr(kgen), vs = ks + S::kStages * S::kKvBytes;
-        const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+        const int tid = threadIdx.x, warp = tc::uniform(tid >> 5), lane = tid & 31;
         if (tid == 0) {
             for (int i = 0; i < S::kStages; ++i) {
-                mbar_init(smem_addr(&sh.kfull[i]), 128);
-                mbar_init(smem_addr(&sh.vfull[i]), 128);
+                mbar_init(smem_addr(&sh.kthere[i]), 128);
+                mbar_init(smem_addr(&sh.vthere[i]), 128);
+                mbar_init(smem_addr(&sh.kfull[i]), 1);
+                mbar_init(smem_addr(&sh.vfull[i]), 1);
                 mbar_init(smem_addr(&sh.kempty[i]), 1);
                 mbar_init(smem_addr(&sh.vempty[i]), 1);
             }
@@ -876,8 +909,10 @@ struct Kernel {
                     mbar_init(smem_addr(&sh.pready[i][k]), kRows);
                 }
                 mbar_init(smem_addr(&sh.vdone[i]), 1);
+            }
+            for (int i = 0; i < kSegs; ++i) {
                 mbar_init(smem_addr(&sh.segfull[i]), 1);
-                mbar_init(smem_addr(&sh.segempty[i]), 4 + 1 + 4 * S::kStreams);
+                mbar_init(smem_addr(&sh.segempty[i]), 4 + 2 + 1 + 4 * S::kStreams);
             }
             mbar_init(smem_addr(&sh.qready), kRows * S::kStreams);
             mbar_init(smem_addr(&sh.meet), kRows * S::kStreams);
@@ -922,7 +957,7 @@ struct Kernel {
         Share w;
         w.x0 = total * cta / ctas;
         w.x1 = total * (cta + 1) / ctas;
-        const int64_t near = total / ctas / 16;
+        const int64_t near = total / ctas / 40;
         w.near = near > 2 ? 2 : static_cast<int>(near);
         auto find = [&]() {
             if (mine.before < 0) return;
@@ -945,15 +980,17 @@ struct Kernel {
         if (tid < 2) a.info[2 * cta + tid].tiles = 0;  // no parts yet
         __syncthreads();
         if (warp < 8) {
-            tc::set_registers_up<200>();
+            tc::set_registers_up<208>();
             softmax(a, sh, qs, base);
         } else if (warp < 12) {
-            tc::set_registers_down<72>();
+            tc::set_registers_down<56>();
             loader(a, sh, ks, vs);
         } else {
             tc::set_registers_down<40>();
             if (warp == 12) products(a, sh, qs, ks, vs);
             if (warp == 13 && lane == 0) schedule(a, sh, w);
+            if (warp == 14 && lane == 0) pass_on(a, sh, sh.kthere, sh.kfull);
+            if (warp == 15 && lane == 0) pass_on(a, sh, sh.vthere, sh.vfull);
         }
         __syncwarp();
         tc::fence_before();
@@ -967,12 +1004,12 @@ struct Kernel {
         Cursor at = sh.first;
         if (!sh.found || w.x0 >= w.x1) at.b = INT32_MAX;
         for (uint32_t n = 0;; ++n) {
-            if (n >= 2 && !wait(sh, sh.segempty[n & 1], (n >> 1 & 1) ^ 1, a)) {
-                sh.seg[n & 1].stop = 1;
-                mbar_arrive(smem_addr(&sh.segfull[n & 1]));
+            if (n >= kSegs && !wait(sh, sh.segempty[n % kSegs], (n / kSegs & 1) ^ 1, a)) {
+                sh.seg[n % kSegs].stop = 1;
+                mbar_arrive(smem_addr(&sh.segfull[n % kSegs]));
                 return;
             }
-            Segment &g = sh.seg[n & 1];
+            Segment &g = sh.seg[n % kSegs];
             advance(a, sh, w, at, g);
             if (sh.abort) g.stop = 1;
             if (!g.stop && g.slot >= 0) {
@@ -984,7 +1021,7 @@ struct Kernel {
                 i.t1 = g.t1;
                 i.tiles = g.block.tiles;
             }
-            mbar_arrive(smem_addr(&sh.segfull[n & 1]));
+            mbar_arrive(smem_addr(&sh.segfull[n % kSegs]));
             if (g.stop) return;
         }
     }
