@@ -2,6 +2,7 @@
 // eviction, rotary append, residual norms).  Not part of the public interface.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -103,10 +104,16 @@ struct SpanArgs {
     int64_t part_stride;
     SpanInfo *info;             // [2 * ctas]
     uint8_t *redo;              // [tokens * q_heads]: rows to be computed one by one
+    // K and V as tensors (element, token of a page, head, page) for bulk copies of
+    // `box` tokens of a page at a time; box 0: copied piece by piece
+    int box;
+    alignas(64) CUtensorMap k_map, v_map;
 };
 // Rows of a tile of query rows, and how many tiles a block of them has.
 constexpr int kSpanRows = 128;
 __host__ __device__ constexpr int span_streams(int dim) { return dim <= 128 ? 2 : 1; }
+// Slots of a tile.
+__host__ __device__ constexpr int span_tile(int dim) { return dim <= 128 ? 128 : 64; }
 // Floats of a part.
 __host__ __device__ constexpr int64_t span_part(int dim) { return static_cast<int64_t>(span_streams(dim)) * kSpanRows * ((dim + 15) / 16 * 16 + 2); }
 cudaError_t launch_tile_f16(const SpanArgs &a, bool vec, int ctas, cudaStream_t s);

@@ -10,9 +10,13 @@
 // the score of one slot, the warp keeps a running maximum and sum, and adds the
 // values weighted; the warps are joined at the end.  Nothing that a row does
 // not see is read, so that infinities and NaN there leave no trace.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "gemv_decode.h"
 #include "gemv_device.cuh"
@@ -389,10 +393,59 @@ static cudaError_t launch_blocks(F fn, int64_t blocks, cudaStream_t s, Args... a
 static bool tiled(const SpanArgs &a) { return fabsf(a.scale_log2) > 0.f && fabsf(a.scale_log2) < INFINITY; }
 static int ctas_of(int sm_count) { return sm_count < kSpanMaxCtas ? sm_count : kSpanMaxCtas; }
 
-cudaError_t launch_span(const SpanArgs &a, bool vec, int elem, int sm_count, cudaStream_t s)
+// The driver's encoder of tensor maps; NULL where there is none.
+static PFN_cuTensorMapEncodeTiled_v12000 encoder()
+{
+    static std::atomic<void *> found{nullptr};
+    void *f = found.load(std::memory_order_relaxed);
+    if (!f) {
+        cudaDriverEntryPointQueryResult result;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &result) != cudaSuccess ||
+            result != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            return nullptr;
+        }
+        found.store(f, std::memory_order_relaxed);
+    }
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+}
+
+// A pool as a tensor of boxes of 64 elements x `box` tokens, rows of 128 bytes
+// swizzled as the tensor core reads them.
+static bool map_pool(CUtensorMap *map, const KvView &kv, void *pool, int64_t page, int64_t token, int64_t head, int elem, int box)
+{
+    const auto encode = encoder();
+    if (!encode || kv.num_pages < 1) return false;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(kv.dim), static_cast<cuuint64_t>(kv.page_size), static_cast<cuuint64_t>(kv.kv_heads),
+                                static_cast<cuuint64_t>(kv.num_pages)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(token) * 2, static_cast<cuuint64_t>(head) * 2, static_cast<cuuint64_t>(page) * 2};
+    const cuuint32_t boxes[4] = {64, static_cast<cuuint32_t>(box), 1, 1}, steps[4] = {1, 1, 1, 1};
+    return encode(map, elem == GEMV_ELEM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pool, dims, strides, boxes,
+                  steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Bulk copies go by boxes of 8 tokens or more that divide both a page and a
+// tile; other pages, and pools that the maps cannot describe, are copied piece by piece.
+static void map_pools(SpanArgs *a, bool vec, int elem)
+{
+    a->box = 0;
+    int box = span_tile(a->kv.dim);
+    while (box >= 8 && a->kv.page_size % box) box /= 2;
+    if (!vec || box < 8 || a->kv.dim < 64) return;
+    if (map_pool(&a->k_map, a->kv, a->kv.k, a->kv.ks_page, a->kv.ks_tok, a->kv.ks_head, elem, box) &&
+        map_pool(&a->v_map, a->kv, a->kv.v, a->kv.vs_page, a->kv.vs_tok, a->kv.vs_head, elem, box))
+        a->box = box;
+}
+
+cudaError_t launch_span(const SpanArgs &args, bool vec, int elem, int sm_count, cudaStream_t s)
 {
     const bool f16 = elem == GEMV_ELEM_F16;
-    if (tiled(a)) return f16 ? launch_tile_f16(a, vec, ctas_of(sm_count), s) : launch_tile_bf16(a, vec, ctas_of(sm_count), s);
+    SpanArgs a = args;
+    if (tiled(a)) {
+        map_pools(&a, vec, elem);
+        return f16 ? launch_tile_f16(a, vec, ctas_of(sm_count), s) : launch_tile_bf16(a, vec, ctas_of(sm_count), s);
+    }
     const int64_t rows = static_cast<int64_t>(a.tokens) * a.q_heads, most = static_cast<int64_t>(sm_count) * 8;
     return launch_blocks(f16 ? mbg_span_rows_kernel<GEMV_ELEM_F16> : mbg_span_rows_kernel<GEMV_ELEM_BF16>, rows < most ? rows : most, s, a);
 }

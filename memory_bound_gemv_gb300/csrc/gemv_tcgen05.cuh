@@ -117,6 +117,15 @@ __device__ __forceinline__ void store16(uint32_t addr, const uint32_t *r)
                  : "memory");
 }
 
+// A box of a 4-dimensional tensor into shared memory; what lies outside the
+// tensor is zeros, and the box's bytes count at `bar` all the same.
+__device__ __forceinline__ void load_box(uint32_t dst, const void *map, int c0, int c1, int c2, int c3, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+                 "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+                 : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void set_registers_up()
 {

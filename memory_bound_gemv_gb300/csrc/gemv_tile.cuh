@@ -17,13 +17,17 @@
 // Work of a block's warps:
 //   warps 0-3, 4-7  two streams of softmax, a thread per row: S from tensor
 //                   memory, P back over it, at the end O;
-//   warps 8-11      K and V, 16 bytes at a time (cp.async) from their pages into
-//                   swizzled shared memory, so that pages of any size, strides and
-//                   unaligned pools take one path;
+//   warps 8-11      K and V from their pages into swizzled shared memory: by bulk
+//                   tensor copies (TMA) of the tokens of a page, a warp each, or,
+//                   where pages are not of a multiple of 8 tokens, 16 bytes at a time
+//                   (cp.async), and unaligned pools element by element;
 //   warp 12         one thread issues the products;
 //   warp 13         looks up what the block does next;
-//   warps 14, 15    make the copied K and V visible to the tensor core (a fence of
-//                   some 0.2 us, during which the products would pause).
+//   warps 14, 15    make what is copied piece by piece visible to the tensor core (a
+//                   fence of some 0.2 us, during which the products would pause).
+// Bulk copies: parts of prompts 835 us -> see below; a place in the ring is free for
+// the shorter, and pieces take 0.65 us to issue per tile and more to arrive than the
+// products take.
 // While one stream's softmax runs, the other's products do.  The streams are two
 // tiles of rows over the same slots, or with up to 128 rows one tile of
 // rows over even and odd tiles of slots, joined at the end.  (Head sizes above
@@ -440,6 +444,111 @@ struct Kernel {
             if (!ok) break;
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+
+    // Bulk copies, K's and V's by a warp each.  A lane takes one box: `box` tokens
+    // of a page x 64 elements.  Boxes that no row sees, and pages that do not
+    // exist, are asked for outside the pool, which gives zeros.  They arrive by
+    // themselves at `full`; a tile of V in which a sequence ends inside a box goes
+    // by `there` and zero_v.
+    static __device__ void bulk_loader(const SpanArgs &a, Shared<DC> &sh, uint32_t dst, bool is_v)
+    {
+        const int lane = threadIdx.x & 31, box = a.box, boxes = kTok / box;  // of 64 elements of a tile
+        const KvView &kv = a.kv;
+        uint64_t *full = is_v ? sh.vfull : sh.kfull, *empty = is_v ? sh.vempty : sh.kempty;
+        const CUtensorMap *map = is_v ? &a.v_map : &a.k_map;
+        const int group = lane % boxes, chunk = lane / boxes;
+        uint32_t count = 0, edges = 0;  // edges: the places whose last tile went by `there`, and the phases of those
+        uint32_t phases = 0;
+        bool ok = true;
+        for (uint32_t n = 0; ok; ++n) {
+            ok = __all_sync(kFull, wait(sh, sh.segfull[n % kSegs], n / kSegs & 1, a));
+            if (!ok) break;
+            const Segment &g = sh.seg[n % kSegs];
+            if (g.stop) return;
+            const int32_t *table = kv.table + g.seq.b * kv.table_stride;
+            const int t0 = g.t0, t1 = g.t1, h = g.h;
+            const int length = g.seq.n;
+            const Block k = g.block;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.segempty[n % kSegs]));
+            // this lane's box of a tile: its page (num_pages: none) and place there
+            auto look_up = [&](int j, int &off) {
+                const int slot = slot_of(k, j) + group * box;
+                int page = -1;
+                off = 0;
+                if (j < t1 && (max(slot, k.lo) < min(slot + box, k.hi) || slot < min(k.sinks, k.hi))) {
+                    const int idx = kv.page_shift >= 0 ? slot >> kv.page_shift : slot / kv.page_size;
+                    off = slot - idx * kv.page_size;
+                    page = __ldg(table + idx);
+                    if (page < 0 || page >= kv.num_pages) {
+                        if (!is_v && chunk == 0) report_error(a.err, DEVERR_BAD_INDEX);
+                        page = -1;
+                    }
+                }
+                return page < 0 ? static_cast<int>(kv.num_pages) : page;
+            };
+            int off = 0, page = look_up(t0, off);
+            for (int j = t0; j < t1; ++j, ++count) {
+                const int st = count % S::kStages;
+                ok = __all_sync(kFull, wait(sh, empty[st], (count / S::kStages & 1) ^ 1, a));
+                if (!ok) break;
+                const bool edge = is_v && ends_in(slot_of(k, j), length, box);
+                uint64_t *bar = edge ? &sh.vthere[st] : &full[st];
+                edges = (edges & ~(1u << st)) | static_cast<uint32_t>(edge) << st;
+                if (edge) phases ^= 1u << st;
+                if (lane == 0) mbar_arrive_expect_tx(smem_addr(bar), S::kKvBytes);
+                __syncwarp();
+                if (lane < boxes * DC)
+                    tc::load_box(dst + st * S::kKvBytes + chunk * (kTok * 128) + group * box * 128, map, chunk * 64, off, h, page,
+                                 smem_addr(bar));
+                page = look_up(j + 1, off);
+            }
+        }
+        // given up: no copy is left under way
+        for (uint32_t i = count > S::kStages ? count - S::kStages : 0; i < count; ++i) {
+            const int st = i % S::kStages;
+            const bool edge = edges >> st & 1;
+            const bool done = wait(sh, edge ? sh.vthere[st] : full[st], edge ? (phases >> st & 1) ^ 1 : i / S::kStages & 1, a);
+            if (!__all_sync(kFull, done) && lane == 0) report_error(a.err, DEVERR_UNDRAINED);
+        }
+    }
+
+    static __device__ __forceinline__ int slot_of(const Block &k, int j) { return (j < k.sink_tiles ? j : j + k.skip) * kTok; }
+
+    // Does a sequence of so many slots end inside a box of this tile?
+    static __device__ __forceinline__ bool ends_in(int slot, int length, int box)
+    {
+        return length > slot && length < slot + kTok && length % box != 0;
+    }
+
+    // What lies in the box behind a sequence's last slot was perhaps never written:
+    // it becomes zeros.  (Other slots that a row does not see hold values, whose
+    // weights are 0.)
+    static __device__ void zero_v(const SpanArgs &a, Shared<DC> &sh, uint32_t vs)
+    {
+        const int lane = threadIdx.x & 31, box = a.box;
+        uint32_t count = 0, phases = 0;
+        for (uint32_t n = 0;; ++n) {
+            if (!__all_sync(kFull, wait(sh, sh.segfull[n % kSegs], n / kSegs & 1, a))) return;
+            const Segment &g = sh.seg[n % kSegs];
+            if (g.stop) return;
+            const int t0 = g.t0, t1 = g.t1, length = g.seq.n;
+            const Block k = g.block;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.segempty[n % kSegs]));
+            for (int j = t0; j < t1; ++j, ++count) {
+                const int st = count % S::kStages, first = slot_of(k, j);
+                if (!ends_in(first, length, box)) continue;
+                if (!__all_sync(kFull, wait(sh, sh.vthere[st], phases >> st & 1, a))) return;
+                phases ^= 1u << st;
+                for (int r = length - first; r % box != 0; ++r)
+                    if (lane < DC * 8) st_shared(vs + st * S::kKvBytes + swizzled(kTok, r, lane), make_uint4(0, 0, 0, 0));
+                tc::fence_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sh.vfull[st]));
+            }
+        }
     }
 
     // --------------------------------------------------------------- products
@@ -894,10 +1003,11 @@ struct Kernel {
         Shared<DC> &sh = *reinterpret_cast<Shared<DC> *>(kgen + 2 * S::kStages * S::kKvBytes);
         const uint32_t qs = smem_addr(base), ks = smem_addr(kgen), vs = ks + S::kStages * S::kKvBytes;
         const int tid = threadIdx.x, warp = tc::uniform(tid >> 5), lane = tid & 31;
+        const bool bulk = VEC && a.box > 0;
         if (tid == 0) {
             for (int i = 0; i < S::kStages; ++i) {
                 mbar_init(smem_addr(&sh.kthere[i]), 128);
-                mbar_init(smem_addr(&sh.vthere[i]), 128);
+                mbar_init(smem_addr(&sh.vthere[i]), bulk ? 1 : 128);
                 mbar_init(smem_addr(&sh.kfull[i]), 1);
                 mbar_init(smem_addr(&sh.vfull[i]), 1);
                 mbar_init(smem_addr(&sh.kempty[i]), 1);
@@ -912,7 +1022,7 @@ struct Kernel {
             }
             for (int i = 0; i < kSegs; ++i) {
                 mbar_init(smem_addr(&sh.segfull[i]), 1);
-                mbar_init(smem_addr(&sh.segempty[i]), 4 + 2 + 1 + 4 * S::kStreams);
+                mbar_init(smem_addr(&sh.segempty[i]), (bulk ? 3 : 6) + 1 + 4 * S::kStreams);
             }
             mbar_init(smem_addr(&sh.qready), kRows * S::kStreams);
             mbar_init(smem_addr(&sh.meet), kRows * S::kStreams);
@@ -984,13 +1094,17 @@ struct Kernel {
             softmax(a, sh, qs, base);
         } else if (warp < 12) {
             tc::set_registers_down<56>();
-            loader(a, sh, ks, vs);
+            if (!bulk)
+                loader(a, sh, ks, vs);
+            else if (warp < 10)
+                bulk_loader(a, sh, warp == 9 ? vs : ks, warp == 9);
         } else {
             tc::set_registers_down<40>();
             if (warp == 12) products(a, sh, qs, ks, vs);
             if (warp == 13 && lane == 0) schedule(a, sh, w);
-            if (warp == 14 && lane == 0) pass_on(a, sh, sh.kthere, sh.kfull);
-            if (warp == 15 && lane == 0) pass_on(a, sh, sh.vthere, sh.vfull);
+            if (warp == 14 && lane == 0 && !bulk) pass_on(a, sh, sh.kthere, sh.kfull);
+            if (warp == 15 && lane == 0 && !bulk) pass_on(a, sh, sh.vthere, sh.vfull);
+            if (warp == 15 && bulk) zero_v(a, sh, vs);
         }
         __syncwarp();
         tc::fence_before();
