@@ -190,6 +190,7 @@ struct AssignArgs {
     int32_t *starts;            // [batch + 1]
     int32_t *slots, *seq;       // [room]
     int64_t room;
+    int wide;                   // both take 16-byte stores
     unsigned int *err;
 };
 cudaError_t launch_assign(const AssignArgs &a, cudaStream_t s);

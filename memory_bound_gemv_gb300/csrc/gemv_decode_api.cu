@@ -511,6 +511,7 @@ gemv_status_t gemv_kv_assign(const gemv_kv_t *kv, const gemv_assign_t *g, void *
     a.slots = g->slots;
     a.seq = g->seq;
     a.room = g->room;
+    a.wide = aligned(g->slots, 16) && aligned(g->seq, 16);
     a.err = dev.status;
     const cudaError_t e = launch_assign(a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GEMV_OK : decode_cuda_fail(e, GEMV_ERR_LAUNCH);

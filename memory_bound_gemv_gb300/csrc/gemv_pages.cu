@@ -70,6 +70,12 @@ __device__ __forceinline__ int find(const int64_t *ends, int n, int64_t i)
     return lo;
 }
 
+// Pages of n slots (below 2^31).
+__device__ __forceinline__ int pages_of(int64_t n, int page_size)
+{
+    return n > 0 ? static_cast<int>((static_cast<uint32_t>(n) - 1) / static_cast<uint32_t>(page_size) + 1) : 0;
+}
+
 __global__ void __launch_bounds__(kThreads, 1) mbg_assign_kernel(const __grid_constant__ AssignArgs a)
 {
     __shared__ Sums sums[2];
@@ -87,6 +93,13 @@ __global__ void __launch_bounds__(kThreads, 1) mbg_assign_kernel(const __grid_co
     const int64_t behind = broken ? 0 : a.ring_size - count;  // places in the ring that hold no free page
     const int page_size = a.page_size, batch = a.batch;
     const int64_t capacity = a.capacity;
+    // the page that this thread hands out first, whoever it goes to
+    int ahead = -1;
+    if (rank * kThreads + tid < count) {
+        int64_t place = at + rank * kThreads + tid;
+        if (place >= a.ring_size) place -= a.ring_size;
+        ahead = a.ring[place];
+    }
     int64_t needed = 0, wanted = 0, taken = 0, gone = 0, tokens = 0;  // sums of the chunks before
     int after = 0;  // this thread's request of the last chunk: slots in use afterwards
     for (int b0 = 0; b0 < batch; b0 += kThreads) {
@@ -96,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1) mbg_assign_kernel(const __grid_co
         if (b < batch) {
             n = a.lengths[b];
             f = a.fresh[b];
-            if (a.shared) keep = max(0, a.shared[b]) / page_size;
+            if (a.shared) keep = static_cast<int>(static_cast<uint32_t>(max(0, a.shared[b])) / static_cast<uint32_t>(page_size));
         }
         if (n < 0 || n > capacity || n + f > capacity) {
             if (rank == 0) report_error(a.err, DEVERR_BAD_INDEX);
@@ -105,8 +118,8 @@ __global__ void __launch_bounds__(kThreads, 1) mbg_assign_kernel(const __grid_co
         }
         const bool over = f < 0;
         if (over) f = 0;
-        const int have = static_cast<int>((n + page_size - 1) / page_size);
-        int64_t need = (n + f + page_size - 1) / page_size - have, back = over && have > keep ? have - keep : 0;
+        const int have = pages_of(n, page_size);
+        int64_t need = pages_of(n + f, page_size) - have, back = over && have > keep ? have - keep : 0;
         // first sums: pages needed, pages returned
         int64_t need_sum = need, back_sum = back, need_all, back_all;
         scan2(sums[0], need_sum, back_sum, need_all, back_all);
@@ -136,16 +149,34 @@ __global__ void __launch_bounds__(kThreads, 1) mbg_assign_kernel(const __grid_co
         if (tid >= fit) tok_end[tid] = tok_last, page_end[tid] = page_last;
         __syncthreads();
         const int step = kThreads * blocks, me = rank * kThreads + tid;
-        for (int64_t i = tokens + me; i < tok_last; i += step) {
-            const int r = find(tok_end, n_chunk, i);
-            a.slots[i] = from_slot[r] + static_cast<int>(i - (r ? tok_end[r - 1] : tokens));
-            a.seq[i] = b0 + r;
+        // four tokens side by side to a thread
+        for (int64_t i0 = tokens / 4 * 4 + 4 * me; i0 < tok_last; i0 += 4 * step) {
+            int r = find(tok_end, n_chunk, i0 < tokens ? tokens : i0), slot[4], seq[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t i = i0 + k;
+                if (i < tokens || i >= tok_last) continue;
+                while (tok_end[r] <= i) ++r;
+                slot[k] = from_slot[r] + static_cast<int>(i - (r ? tok_end[r - 1] : tokens));
+                seq[k] = b0 + r;
+            }
+            if (a.wide && i0 >= tokens && i0 + 4 <= tok_last) {
+                *reinterpret_cast<int4 *>(a.slots + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+                *reinterpret_cast<int4 *>(a.seq + i0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (i0 + k >= tokens && i0 + k < tok_last) a.slots[i0 + k] = slot[k], a.seq[i0 + k] = seq[k];
+            }
         }
         for (int64_t i = taken + me; i < page_last; i += step) {
             const int r = find(page_end, n_chunk, i);
-            int64_t place = at + i;
-            if (place >= a.ring_size) place -= a.ring_size;
-            int page = a.ring[place];
+            int page = ahead;
+            if (i != me) {
+                int64_t place = at + i;
+                if (place >= a.ring_size) place -= a.ring_size;
+                page = a.ring[place];
+            }
             if (page < 0 || page >= a.num_pages) {
                 report_error(a.err, DEVERR_BAD_INDEX);
                 page = -1;

@@ -40,6 +40,30 @@ __device__ __forceinline__ float exp2_from(float x, float m)
     return exp2f(x - (m == -INFINITY ? 0.f : m));
 }
 
+__device__ __forceinline__ float lse_of(float m, float l)
+{
+    return l > 0.f || l != l ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// What a prefix and the slots behind it give together: factors of their O.
+struct Both {
+    float pre, own, m, l;
+};
+__device__ __forceinline__ Both both_of(const SpanArgs &a, int64_t index, float m, float l)
+{
+    const float *stat = a.own + (index + 1) * span_row(a.kv.dim) - 4;
+    const float m2 = __ldcg(stat), l2 = __ldcg(stat + 1);
+    Both r;
+    r.m = fmaxf(m, m2);
+    r.pre = exp2_from(m, r.m);
+    r.own = l2 == 0.f ? 0.f : exp2_from(m2, r.m);  // (its O may not be there)
+    r.l = l * r.pre + (l2 == 0.f ? 0.f : l2 * r.own);
+    const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
+    r.pre *= inv;
+    r.own = l2 == 0.f ? 0.f : r.own * inv;
+    return r;
+}
+
 // The sequence that token t belongs to; -1: none.
 __device__ int seq_of_token(const SpanArgs &a, int t)
 {
@@ -56,7 +80,7 @@ __device__ int seq_of_token(const SpanArgs &a, int t)
 }
 
 template <int E>
-__device__ void one_row(const SpanArgs &a, Shared &sh, int token, int head)
+__device__ void one_row(const SpanArgs &a, Shared &sh, int token, int head, int d0, int d1)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dim = a.kv.dim;
     if (a.kv.batch == 0) return;
@@ -129,38 +153,63 @@ __device__ void one_row(const SpanArgs &a, Shared &sh, int token, int head)
         if (lane + 32 * j < dim) sh.o[warp][lane + 32 * j] = o[j] * fix;
     __syncthreads();
     const int64_t row = static_cast<int64_t>(token) * a.q_heads + head;
-    for (int d = threadIdx.x; d < dim; d += kThreads) {
+    // (the prefix of all rows: left for the joins; of a row that a join has sent here:
+    // joined at once)
+    const bool all = d0 == 0 && d1 == dim;
+    Both f = {sum == 0.f ? 0.f : 1.f / sum, 0.f, top, sum};
+    if (a.own && !all) f = both_of(a, row, top, sum);
+    for (int d = d0 + threadIdx.x; d < d1; d += kThreads) {
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) v += sh.o[w][d];
-        if (a.pre)
+        if (a.pre && all) {
             a.pre[row * span_row(dim) + d] = v;
-        else
-            elem_store1<E>(a.out, token * a.o_st + head * a.o_sh + d, sum == 0.f ? 0.f : v / sum);
+            continue;
+        }
+        v *= f.pre;
+        if (f.own != 0.f) v += __ldcg(a.own + row * span_row(dim) + d) * f.own;
+        elem_store1<E>(a.out, token * a.o_st + head * a.o_sh + d, v);
     }
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && all) {
         if (a.pre) {
             a.pre[(row + 1) * span_row(dim) - 4] = top;
             a.pre[(row + 1) * span_row(dim) - 3] = sum;
         } else if (a.lse) {
-            a.lse[row] = sum > 0.f || sum != sum ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+            a.lse[row] = lse_of(top, sum);
         }
     }
     __syncthreads();
 }
 
-// Sixteen rows of a block: thread (lane, row) = (t / 16, t % 16) takes every
-// sixteenth run of four elements of its row, so that half a warp reads 256
-// bytes of a part.
-constexpr int kJoinRows = 16, kJoinLanes = kThreads / kJoinRows;
+// A task joins 16 elements (a run) of all rows of a block, a thread per row: a
+// warp reads 512 bytes of a part at a time, and has those of four parts under way.
+constexpr int kRun = 16, kAtOnce = 4;
 constexpr int kMaxParts = kSpanMaxCtas + 1;
 
 struct JoinShared {
     int slot[kMaxParts];
     int count[kWarps];
-    float m[kMaxParts][kJoinRows], l[kMaxParts][kJoinRows];
-    int bad[kJoinRows];
+    unsigned bad[kWarps];
 };
+
+// What the tiles have left of their parts, read once per block.
+struct Parts {
+    SpanInfo info[2 * kSpanMaxCtas];
+    __device__ void read(const SpanArgs &a, int ctas)
+    {
+        constexpr int kMost = (2 * kSpanMaxCtas * sizeof(SpanInfo) / 16 + kThreads - 1) / kThreads;
+        const int words = 2 * ctas * static_cast<int>(sizeof(SpanInfo)) / 16;
+        uint4 w[kMost];
+#pragma unroll
+        for (int k = 0; k < kMost; ++k)
+            if (threadIdx.x + k * kThreads < words) w[k] = __ldcg(reinterpret_cast<const uint4 *>(a.info) + threadIdx.x + k * kThreads);
+#pragma unroll
+        for (int k = 0; k < kMost; ++k)
+            if (threadIdx.x + k * kThreads < words) reinterpret_cast<uint4 *>(info)[threadIdx.x + k * kThreads] = w[k];
+        __syncthreads();
+    }
+};
+static_assert(sizeof(SpanInfo) * 2 % 16 == 0, "");
 
 // The numbers i < n for which f(i), in order, in list (no more than `most`).
 template <typename F>
@@ -187,127 +236,116 @@ __device__ int collect(int n, int *list, int most, int *count, F f)
     return min(have, most);
 }
 
-__device__ __forceinline__ float lse_of(float m, float l)
-{
-    return l > 0.f || l != l ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-}
-
-// Four elements of a row's output from d on.
+// A run of a row's output, from d on.
 template <int E>
-__device__ __forceinline__ void store4(const SpanArgs &a, int token, int head, int d, const float (&v)[4])
+__device__ __forceinline__ void store_run(const SpanArgs &a, int token, int head, int d, const float (&v)[kRun])
 {
-    const int64_t at = token * a.o_st + head * a.o_sh + d;
-    if (a.out_vec && d + 4 <= a.kv.dim) {
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) = make_uint2(elem_pack2<E>(v[0], v[1]), elem_pack2<E>(v[2], v[3]));
+    uint16_t *to = static_cast<uint16_t *>(a.out) + token * a.o_st + head * a.o_sh + d;
+    if (a.out_vec && d + kRun <= a.kv.dim) {
+        uint32_t w[kRun / 2];
+#pragma unroll
+        for (int k = 0; k < kRun / 2; ++k) w[k] = elem_pack2<E>(v[2 * k], v[2 * k + 1]);
+        reinterpret_cast<uint4 *>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4 *>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
     } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (d + k < a.kv.dim) elem_store1<E>(a.out, at + k, v[k]);
+        for (int k = 0; k < kRun; ++k)
+            if (d + k < a.kv.dim) elem_store1<E>(to, k, v[k]);
     }
 }
 
-// What a prefix and the slots behind it give together: factors of their O.
-struct Both {
-    float pre, own, m, l;
-};
-__device__ __forceinline__ Both both_of(const SpanArgs &a, int64_t index, float m, float l)
-{
-    const float *stat = a.own + (index + 1) * span_row(a.kv.dim) - 4;
-    const float m2 = __ldcg(stat), l2 = __ldcg(stat + 1);
-    Both r;
-    r.m = fmaxf(m, m2);
-    r.pre = exp2_from(m, r.m);
-    r.own = l2 == 0.f ? 0.f : exp2_from(m2, r.m);  // (its O may not be there)
-    r.l = l * r.pre + (l2 == 0.f ? 0.f : l2 * r.own);
-    const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
-    r.pre *= inv;
-    r.own = l2 == 0.f ? 0.f : r.own * inv;
-    return r;
-}
-
-// Rows [row0 + 16 group, + 16) of the block of cached head h that begins at
-// row0 of sequence b's rows.
+// Run `run` of the rows of the block of cached head h that begins at row0 of
+// sequence b's rows.
 template <int E>
-__device__ void join_rows(const SpanArgs &a, unsigned char *raw, int ctas, int b, int h, int row0, int group)
+__device__ void join_run(const SpanArgs &a, unsigned char *raw, const Parts &left, int ctas, int b, int h, int row0, int run)
 {
     JoinShared &js = *reinterpret_cast<JoinShared *>(raw);
-    const int tid = threadIdx.x, dim = a.kv.dim;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, dim = a.kv.dim, d = run * kRun;
     const span::Seq s = span::seq_of(a, b, false);
-    const int rows = s.m * a.group, first = row0 + group * kJoinRows;
-    if (first >= rows) return;
     const int parts = collect(2 * ctas, js.slot, kMaxParts, js.count, [&](int i) {
-        const SpanInfo p = a.info[i];
+        const SpanInfo &p = left.info[i];
         return p.tiles > 0 && p.b == b && p.h == h && p.row0 == row0;
     });
-    const int r = tid % kJoinRows, lane = tid / kJoinRows, row = first + r;
-    const bool live = row < rows;
-    const int token = s.q0 + (live ? row / a.group : 0), head = h * a.group + (live ? row % a.group : 0);
+    const bool live = tid < span_streams(dim) * kSpanRows && row0 + tid < s.m * a.group;
+    const int row = live ? row0 + tid : row0;
+    const int token = s.q0 + row / a.group, head = h * a.group + row % a.group;
     const int64_t index = static_cast<int64_t>(token) * a.q_heads + head;
-    if (tid < kJoinRows) js.bad[tid] = parts == 0 && ctas > 0 && live && __ldcg(a.redo + index) == 1;
-    // the rows' places in a part
-    const int stream = group * kJoinRows / kSpanRows, in = group * kJoinRows % kSpanRows;
-    const int64_t half = stream * (a.part_stride / span_streams(dim));
-    const int stat = (dim + 15) / 16 * 16 * kSpanRows;
-    for (int p = lane; p < parts; p += kJoinLanes) {
-        const float *from = a.part + js.slot[p] * a.part_stride + half + stat + in + r;
-        js.m[p][r] = __ldcg(from);
-        js.l[p][r] = __ldcg(from + kSpanRows);
-    }
-    __syncthreads();
-    float top = -INFINITY, sum = 0.f;
-    if (parts > 0) {
-        for (int p = 0; p < parts; ++p) top = fmaxf(top, js.m[p][r]);
-        for (int p = 0; p < parts; ++p) sum += exp2_from(js.m[p][r], top) * js.l[p][r];
-    } else if (live) {
-        top = __ldcg(a.pre + (index + 1) * span_row(dim) - 4);
-        sum = __ldcg(a.pre + (index + 1) * span_row(dim) - 3);
-    }
-    Both f = {sum == 0.f ? 0.f : 1.f / sum, 0.f, top, sum};
-    if (a.own && live) f = both_of(a, index, top, sum);
-    for (int d = 4 * lane; d < dim; d += 4 * kJoinLanes) {
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        if (parts > 0) {
-            const float *from = a.part + half + (static_cast<int64_t>(d / 4) * kSpanRows + in + r) * 4;
-#pragma unroll 8
-            for (int p = 0; p < parts; ++p) {
-                const float4 x = __ldcg(reinterpret_cast<const float4 *>(from + js.slot[p] * a.part_stride));
-                const float w = exp2_from(js.m[p][r], top);
-                v[0] += x.x * w, v[1] += x.y * w, v[2] += x.z * w, v[3] += x.w * w;
-            }
-        } else if (live) {
-            const float4 x = __ldcg(reinterpret_cast<const float4 *>(a.pre + index * span_row(dim) + d));
-            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-        }
-        if (!live) continue;
+    bool bad = false;
+    if (live) {
+        // the row's place in a part
+        const int stream = tid / kSpanRows, in = tid % kSpanRows;
+        const float *part = a.part + stream * (a.part_stride / span_streams(dim));
+        const float *stat = part + (dim + 15) / 16 * 16 * kSpanRows + in;
+        const float *from = part + (static_cast<int64_t>(d / 4) * kSpanRows + in) * 4;
+        float top = -INFINITY, sum = 0.f, v[kRun];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (d + k < dim && v[k] != v[k] && sum == sum) js.bad[r] = 1;
+        for (int k = 0; k < kRun; ++k) v[k] = 0.f;
+        for (int p0 = 0; p0 < parts; p0 += kAtOnce) {
+            float m[kAtOnce], l[kAtOnce];
+            float4 x[kAtOnce][kRun / 4];
+#pragma unroll
+            for (int p = 0; p < kAtOnce; ++p) {
+                m[p] = -INFINITY, l[p] = 0.f;
+#pragma unroll
+                for (int k = 0; k < kRun / 4; ++k) x[p][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (p0 + p >= parts) continue;
+                const int64_t at = js.slot[p0 + p] * a.part_stride;
+                m[p] = __ldcg(stat + at), l[p] = __ldcg(stat + at + kSpanRows);
+#pragma unroll
+                for (int k = 0; k < kRun / 4; ++k) x[p][k] = __ldcg(reinterpret_cast<const float4 *>(from + at + k * kSpanRows * 4));
+            }
+            float high = top;
+#pragma unroll
+            for (int p = 0; p < kAtOnce; ++p) high = fmaxf(high, m[p]);
+            const float fix = exp2_from(top, high);
+            sum *= fix;
+#pragma unroll
+            for (int k = 0; k < kRun; ++k) v[k] *= fix;
+            top = high;
+#pragma unroll
+            for (int p = 0; p < kAtOnce; ++p) {
+                const float w = exp2_from(m[p], top);
+                sum += l[p] * w;
+#pragma unroll
+                for (int k = 0; k < kRun / 4; ++k) {
+                    v[4 * k] += x[p][k].x * w, v[4 * k + 1] += x[p][k].y * w;
+                    v[4 * k + 2] += x[p][k].z * w, v[4 * k + 3] += x[p][k].w * w;
+                }
+            }
+        }
+        if (parts == 0) {
+            const float *pre = a.pre + index * span_row(dim);
+            top = __ldcg(pre + span_row(dim) - 4);
+            sum = __ldcg(pre + span_row(dim) - 3);
+#pragma unroll
+            for (int k = 0; k < kRun; ++k)
+                if (d + k < dim) v[k] = __ldcg(pre + d + k);
+            bad = ctas > 0 && __ldcg(a.redo + index) == 1;
+        }
+        Both f = {sum == 0.f ? 0.f : 1.f / sum, 0.f, top, sum};
+        if (a.own) f = both_of(a, index, top, sum);
+        const float *own = a.own + index * span_row(dim) + d;
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) {
+            bad = bad || (d + k < dim && v[k] != v[k] && sum == sum);
             v[k] *= f.pre;
+            if (f.own != 0.f && d + k < dim) v[k] += __ldcg(own + k) * f.own;
         }
-        if (f.own != 0.f) {
-            const float4 x = __ldcg(reinterpret_cast<const float4 *>(a.own + index * span_row(dim) + d));
-            v[0] += x.x * f.own, v[1] += x.y * f.own, v[2] += x.z * f.own, v[3] += x.w * f.own;
-        }
-        store4<E>(a, token, head, d, v);
+        store_run<E>(a, token, head, d, v);
+        if (run == 0 && a.lse) a.lse[index] = lse_of(f.m, f.l);
     }
-    if (live && lane == 0 && a.lse) a.lse[index] = lse_of(f.m, f.l);
+    // rows that need it, one by one: this run of them
+    const unsigned vote = __ballot_sync(kFull, bad);
+    if (lane == 0) js.bad[warp] = vote;
+    if (!__syncthreads_or(bad)) return;
+    unsigned again[kWarps];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) again[w] = js.bad[w];
     __syncthreads();
-    unsigned bad = 0;
-    for (int i = 0; i < kJoinRows; ++i) bad |= js.bad[i] ? 1u << i : 0u;
-    __syncthreads();
-    for (int i = 0; i < kJoinRows; ++i) {
-        if (!(bad >> i & 1)) continue;
-        const int t = s.q0 + (first + i) / a.group, hd = h * a.group + (first + i) % a.group;
-        one_row<E>(a, *reinterpret_cast<Shared *>(raw), t, hd);
-        if (!a.own) continue;
-        const int64_t at = static_cast<int64_t>(t) * a.q_heads + hd;
-        const float *pre = a.pre + at * span_row(dim);
-        const Both g = both_of(a, at, pre[span_row(dim) - 4], pre[span_row(dim) - 3]);
-        for (int d = tid; d < dim; d += kThreads)
-            elem_store1<E>(a.out, t * a.o_st + hd * a.o_sh + d,
-                           pre[d] * g.pre + (g.own != 0.f ? __ldcg(a.own + at * span_row(dim) + d) * g.own : 0.f));
-        if (tid == 0 && a.lse) a.lse[at] = lse_of(g.m, g.l);
-        __syncthreads();
+    for (int i = 0; i < kThreads; ++i) {
+        if (!(again[i / 32] >> i % 32 & 1)) continue;
+        const int t = s.q0 + (row0 + i) / a.group, hd = h * a.group + (row0 + i) % a.group;
+        one_row<E>(a, *reinterpret_cast<Shared *>(raw), t, hd, d, min(dim, d + kRun));
     }
 }
 
@@ -318,24 +356,26 @@ __global__ void __launch_bounds__(kThreads) mbg_span_finish_kernel(const __grid_
 {
     __shared__ __align__(16) unsigned char raw[sizeof(JoinShared) > sizeof(Shared) ? sizeof(JoinShared) : sizeof(Shared)];
     __shared__ int cuts[kSpanMaxCtas], count[kWarps];
+    __shared__ __align__(16) Parts left;
     pdl_trigger();
     pdl_wait();
-    const int block = span_streams(a.kv.dim) * kSpanRows, groups = block / kJoinRows;
+    const int block = span_streams(a.kv.dim) * kSpanRows, groups = (a.kv.dim + kRun - 1) / kRun;
+    left.read(a, ctas);
     if (a.prefix) {
         const int blocks = static_cast<int>((static_cast<int64_t>(a.tokens) * a.group + block - 1) / block);
         const int64_t tasks = static_cast<int64_t>(blocks) * a.kv.kv_heads * groups;
         for (int64_t i = blockIdx.x; i < tasks; i += gridDim.x) {
             const int g = static_cast<int>(i % groups), h = static_cast<int>(i / groups % a.kv.kv_heads);
-            join_rows<E>(a, raw, ctas, 0, h, static_cast<int>(i / groups / a.kv.kv_heads) * block, g);
+            join_run<E>(a, raw, left, ctas, 0, h, static_cast<int>(i / groups / a.kv.kv_heads) * block, g);
             __syncthreads();
         }
         return;
     }
     // blocks whose beginning is a part
-    const int n = collect(ctas, cuts, kSpanMaxCtas, count, [&](int c) { return a.info[2 * c + 1].tiles > 0; });
+    const int n = collect(ctas, cuts, kSpanMaxCtas, count, [&](int c) { return left.info[2 * c + 1].tiles > 0; });
     for (int i = blockIdx.x; i < n * groups; i += gridDim.x) {
-        const SpanInfo p = a.info[2 * cuts[i / groups] + 1];
-        join_rows<E>(a, raw, ctas, p.b, p.h, p.row0, i % groups);
+        const SpanInfo &p = left.info[2 * cuts[i / groups] + 1];
+        join_run<E>(a, raw, left, ctas, p.b, p.h, p.row0, i % groups);
         __syncthreads();
     }
     const int64_t rows = static_cast<int64_t>(a.tokens) * a.q_heads;
@@ -353,7 +393,7 @@ __global__ void __launch_bounds__(kThreads) mbg_span_finish_kernel(const __grid_
             for (int i = 0; i < 32; ++i)
                 if (vote >> i & 1) {
                     const int64_t r = r0 + w * 32 + i;
-                    one_row<E>(a, *reinterpret_cast<Shared *>(raw), static_cast<int>(r / a.q_heads), static_cast<int>(r % a.q_heads));
+                    one_row<E>(a, *reinterpret_cast<Shared *>(raw), static_cast<int>(r / a.q_heads), static_cast<int>(r % a.q_heads), 0, a.kv.dim);
                 }
         }
     }
@@ -369,7 +409,7 @@ __global__ void __launch_bounds__(kThreads) mbg_span_rows_kernel(const __grid_co
         for (int b = threadIdx.x; b < (a.prefix ? 1 : a.kv.batch); b += kThreads) span::seq_of(a, b, true);
     const int64_t rows = static_cast<int64_t>(a.tokens) * a.q_heads;
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-        one_row<E>(a, sh, static_cast<int>(r / a.q_heads), static_cast<int>(r % a.q_heads));
+        one_row<E>(a, sh, static_cast<int>(r / a.q_heads), static_cast<int>(r % a.q_heads), 0, a.kv.dim);
 }
 
 }  // namespace
@@ -454,9 +494,9 @@ cudaError_t launch_span_finish(const SpanArgs &a, int elem, int sm_count, cudaSt
 {
     if (!tiled(a) && !a.prefix) return cudaSuccess;
     const int64_t block = span_streams(a.kv.dim) * kSpanRows, rows = static_cast<int64_t>(a.tokens) * a.group;
-    int64_t blocks = static_cast<int64_t>(sm_count) * 4;
+    int64_t blocks = static_cast<int64_t>(sm_count) * 6;
     if (a.prefix) {
-        const int64_t tasks = (rows + block - 1) / block * a.kv.kv_heads * (block / kJoinRows);
+        const int64_t tasks = (rows + block - 1) / block * a.kv.kv_heads * ((a.kv.dim + kRun - 1) / kRun);
         if (tasks < blocks) blocks = tasks;
     }
     return launch_blocks(elem == GEMV_ELEM_F16 ? mbg_span_finish_kernel<GEMV_ELEM_F16> : mbg_span_finish_kernel<GEMV_ELEM_BF16>, blocks, s, a,

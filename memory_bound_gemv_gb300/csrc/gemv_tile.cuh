@@ -163,7 +163,6 @@ struct Shared {
     Segment seg[kSegs];
     Limits lim;
     Cursor first;     // where the CTA's share begins
-    int found;
     int64_t warp_sum[2][kThreads / 32];
     int ends[kThreads];
     float join_m[kRows], join_l[kRows];
@@ -1030,7 +1029,7 @@ struct Kernel {
             sh.abort = 0;
             sh.lim.shortest = INT32_MAX;
             sh.lim.longest = 0;
-            sh.found = 0;
+            sh.seg[0].stop = 1;
         }
         if (warp == 0) tc::alloc(smem_addr(&sh.tmem), 512);
         // the next launch may start once this one's wait is over: then nothing
@@ -1073,10 +1072,10 @@ struct Kernel {
             if (mine.before < 0) return;
             const int64_t r0 = mine.before * a.kv.kv_heads;
             const int cost = cost_of<DC>(mine.block);
-            if (r0 <= w.x0 && w.x0 < r0 + static_cast<int64_t>(cost) * a.kv.kv_heads) {
+            if (w.x0 < w.x1 && r0 <= w.x0 && w.x0 < r0 + static_cast<int64_t>(cost) * a.kv.kv_heads) {
                 mine.h = static_cast<int>((w.x0 - r0) / cost);
+                advance(a, sh, w, mine, sh.seg[0]);
                 sh.first = mine;
-                sh.found = 1;
             }
         };
         if (once) {
@@ -1116,7 +1115,6 @@ struct Kernel {
     static __device__ void schedule(const SpanArgs &a, Shared<DC> &sh, const Share &w)
     {
         Cursor at = sh.first;
-        if (!sh.found || w.x0 >= w.x1) at.b = INT32_MAX;
         for (uint32_t n = 0;; ++n) {
             if (n >= kSegs && !wait(sh, sh.segempty[n % kSegs], (n / kSegs & 1) ^ 1, a)) {
                 sh.seg[n % kSegs].stop = 1;
@@ -1124,7 +1122,7 @@ struct Kernel {
                 return;
             }
             Segment &g = sh.seg[n % kSegs];
-            advance(a, sh, w, at, g);
+            if (n > 0) advance(a, sh, w, at, g);  // (the first is there)
             if (sh.abort) g.stop = 1;
             if (!g.stop && g.slot >= 0) {
                 SpanInfo &i = a.info[g.slot];
