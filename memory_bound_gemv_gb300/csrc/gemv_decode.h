@@ -107,7 +107,7 @@ struct SpanArgs {
     // K and V as tensors (element, token of a page, head, page) for bulk copies of
     // `box` tokens of a page at a time; box 0: copied piece by piece
     int box;
-    alignas(64) CUtensorMap k_map, v_map;
+    CUtensorMap k_map, v_map;
 };
 // Rows of a tile of query rows, and how many tiles a block of them has.
 constexpr int kSpanRows = 128;

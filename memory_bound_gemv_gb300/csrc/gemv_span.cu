@@ -80,7 +80,7 @@ __device__ int seq_of_token(const SpanArgs &a, int t)
 }
 
 template <int E>
-__device__ void one_row(const SpanArgs &a, Shared &sh, int token, int head, int d0, int d1)
+__device__ void one_row(const SpanArgs &a, Shared &sh, int token, int head, int d0, int d1, bool joined)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dim = a.kv.dim;
     if (a.kv.batch == 0) return;
@@ -155,14 +155,13 @@ __device__ void one_row(const SpanArgs &a, Shared &sh, int token, int head, int 
     const int64_t row = static_cast<int64_t>(token) * a.q_heads + head;
     // (the prefix of all rows: left for the joins; of a row that a join has sent here:
     // joined at once)
-    const bool all = d0 == 0 && d1 == dim;
     Both f = {sum == 0.f ? 0.f : 1.f / sum, 0.f, top, sum};
-    if (a.own && !all) f = both_of(a, row, top, sum);
+    if (a.own && joined) f = both_of(a, row, top, sum);
     for (int d = d0 + threadIdx.x; d < d1; d += kThreads) {
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) v += sh.o[w][d];
-        if (a.pre && all) {
+        if (a.pre && !joined) {
             a.pre[row * span_row(dim) + d] = v;
             continue;
         }
@@ -170,7 +169,7 @@ __device__ void one_row(const SpanArgs &a, Shared &sh, int token, int head, int 
         if (f.own != 0.f) v += __ldcg(a.own + row * span_row(dim) + d) * f.own;
         elem_store1<E>(a.out, token * a.o_st + head * a.o_sh + d, v);
     }
-    if (threadIdx.x == 0 && all) {
+    if (threadIdx.x == 0 && !joined) {
         if (a.pre) {
             a.pre[(row + 1) * span_row(dim) - 4] = top;
             a.pre[(row + 1) * span_row(dim) - 3] = sum;
@@ -181,9 +180,11 @@ __device__ void one_row(const SpanArgs &a, Shared &sh, int token, int head, int 
     __syncthreads();
 }
 
-// A task joins 16 elements (a run) of all rows of a block, a thread per row: a
-// warp reads 512 bytes of a part at a time, and has those of four parts under way.
-constexpr int kRun = 16, kAtOnce = 4;
+// A task joins a run of elements of all rows of a block, a thread per row: a warp
+// reads 512 bytes of a part at a time, and has those of several parts under
+// way.  Cut prompts: 16 elements of some two parts each; prefix: few blocks in many
+// parts, four elements of eight parts at once.
+constexpr int kPromptRun = 16, kPrefixRun = 4;
 constexpr int kMaxParts = kSpanMaxCtas + 1;
 
 struct JoinShared {
@@ -237,7 +238,7 @@ __device__ int collect(int n, int *list, int most, int *count, F f)
 }
 
 // A run of a row's output, from d on.
-template <int E>
+template <int E, int kRun>
 __device__ __forceinline__ void store_run(const SpanArgs &a, int token, int head, int d, const float (&v)[kRun])
 {
     uint16_t *to = static_cast<uint16_t *>(a.out) + token * a.o_st + head * a.o_sh + d;
@@ -245,8 +246,8 @@ __device__ __forceinline__ void store_run(const SpanArgs &a, int token, int head
         uint32_t w[kRun / 2];
 #pragma unroll
         for (int k = 0; k < kRun / 2; ++k) w[k] = elem_pack2<E>(v[2 * k], v[2 * k + 1]);
-        reinterpret_cast<uint4 *>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4 *>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+        for (int k = 0; k < kRun / 4; ++k) reinterpret_cast<uint2 *>(to)[k] = make_uint2(w[2 * k], w[2 * k + 1]);
     } else {
 #pragma unroll
         for (int k = 0; k < kRun; ++k)
@@ -256,7 +257,7 @@ __device__ __forceinline__ void store_run(const SpanArgs &a, int token, int head
 
 // Run `run` of the rows of the block of cached head h that begins at row0 of
 // sequence b's rows.
-template <int E>
+template <int E, int kRun, int kAtOnce>
 __device__ void join_run(const SpanArgs &a, unsigned char *raw, const Parts &left, int ctas, int b, int h, int row0, int run)
 {
     JoinShared &js = *reinterpret_cast<JoinShared *>(raw);
@@ -331,7 +332,7 @@ __device__ void join_run(const SpanArgs &a, unsigned char *raw, const Parts &lef
             v[k] *= f.pre;
             if (f.own != 0.f && d + k < dim) v[k] += __ldcg(own + k) * f.own;
         }
-        store_run<E>(a, token, head, d, v);
+        store_run<E, kRun>(a, token, head, d, v);
         if (run == 0 && a.lse) a.lse[index] = lse_of(f.m, f.l);
     }
     // rows that need it, one by one: this run of them
@@ -345,7 +346,7 @@ __device__ void join_run(const SpanArgs &a, unsigned char *raw, const Parts &lef
     for (int i = 0; i < kThreads; ++i) {
         if (!(again[i / 32] >> i % 32 & 1)) continue;
         const int t = s.q0 + (row0 + i) / a.group, hd = h * a.group + (row0 + i) % a.group;
-        one_row<E>(a, *reinterpret_cast<Shared *>(raw), t, hd, d, min(dim, d + kRun));
+        one_row<E>(a, *reinterpret_cast<Shared *>(raw), t, hd, d, min(dim, d + kRun), true);
     }
 }
 
@@ -359,14 +360,14 @@ __global__ void __launch_bounds__(kThreads) mbg_span_finish_kernel(const __grid_
     __shared__ __align__(16) Parts left;
     pdl_trigger();
     pdl_wait();
-    const int block = span_streams(a.kv.dim) * kSpanRows, groups = (a.kv.dim + kRun - 1) / kRun;
+    const int block = span_streams(a.kv.dim) * kSpanRows, run = a.prefix ? kPrefixRun : kPromptRun, groups = (a.kv.dim + run - 1) / run;
     left.read(a, ctas);
     if (a.prefix) {
         const int blocks = static_cast<int>((static_cast<int64_t>(a.tokens) * a.group + block - 1) / block);
         const int64_t tasks = static_cast<int64_t>(blocks) * a.kv.kv_heads * groups;
         for (int64_t i = blockIdx.x; i < tasks; i += gridDim.x) {
             const int g = static_cast<int>(i % groups), h = static_cast<int>(i / groups % a.kv.kv_heads);
-            join_run<E>(a, raw, left, ctas, 0, h, static_cast<int>(i / groups / a.kv.kv_heads) * block, g);
+            join_run<E, kPrefixRun, 8>(a, raw, left, ctas, 0, h, static_cast<int>(i / groups / a.kv.kv_heads) * block, g);
             __syncthreads();
         }
         return;
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(kThreads) mbg_span_finish_kernel(const __grid_
     const int n = collect(ctas, cuts, kSpanMaxCtas, count, [&](int c) { return left.info[2 * c + 1].tiles > 0; });
     for (int i = blockIdx.x; i < n * groups; i += gridDim.x) {
         const SpanInfo &p = left.info[2 * cuts[i / groups] + 1];
-        join_run<E>(a, raw, left, ctas, p.b, p.h, p.row0, i % groups);
+        join_run<E, kPromptRun, 4>(a, raw, left, ctas, p.b, p.h, p.row0, i % groups);
         __syncthreads();
     }
     const int64_t rows = static_cast<int64_t>(a.tokens) * a.q_heads;
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(kThreads) mbg_span_finish_kernel(const __grid_
             for (int i = 0; i < 32; ++i)
                 if (vote >> i & 1) {
                     const int64_t r = r0 + w * 32 + i;
-                    one_row<E>(a, *reinterpret_cast<Shared *>(raw), static_cast<int>(r / a.q_heads), static_cast<int>(r % a.q_heads), 0, a.kv.dim);
+                    one_row<E>(a, *reinterpret_cast<Shared *>(raw), static_cast<int>(r / a.q_heads), static_cast<int>(r % a.q_heads), 0, a.kv.dim, false);
                 }
         }
     }
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(kThreads) mbg_span_rows_kernel(const __grid_co
         for (int b = threadIdx.x; b < (a.prefix ? 1 : a.kv.batch); b += kThreads) span::seq_of(a, b, true);
     const int64_t rows = static_cast<int64_t>(a.tokens) * a.q_heads;
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-        one_row<E>(a, sh, static_cast<int>(r / a.q_heads), static_cast<int>(r % a.q_heads), 0, a.kv.dim);
+        one_row<E>(a, sh, static_cast<int>(r / a.q_heads), static_cast<int>(r % a.q_heads), 0, a.kv.dim, false);
 }
 
 }  // namespace
@@ -496,7 +497,7 @@ cudaError_t launch_span_finish(const SpanArgs &a, int elem, int sm_count, cudaSt
     const int64_t block = span_streams(a.kv.dim) * kSpanRows, rows = static_cast<int64_t>(a.tokens) * a.group;
     int64_t blocks = static_cast<int64_t>(sm_count) * 6;
     if (a.prefix) {
-        const int64_t tasks = (rows + block - 1) / block * a.kv.kv_heads * ((a.kv.dim + kRun - 1) / kRun);
+        const int64_t tasks = (rows + block - 1) / block * a.kv.kv_heads * ((a.kv.dim + kPrefixRun - 1) / kPrefixRun);
         if (tasks < blocks) blocks = tasks;
     }
     return launch_blocks(elem == GEMV_ELEM_F16 ? mbg_span_finish_kernel<GEMV_ELEM_F16> : mbg_span_finish_kernel<GEMV_ELEM_BF16>, blocks, s, a,

@@ -1060,8 +1060,19 @@ struct Kernel {
             mine.seq = q;
             mine.block = k;
         };
-        bool once, again;
-        const int64_t total = for_blocks(a, sh, take, &once) * a.kv.kv_heads;
+        bool once = true, again;
+        int64_t total;
+        span::Seq all;
+        int blocks = 0;
+        if (a.prefix) {  // one sequence, whose blocks but for the last are alike
+            all = span::seq_of(a, 0, blockIdx.x == 0 && tid == 0);
+            blocks = (all.m * a.group + S::kBlock - 1) / S::kBlock;
+            const int first = blocks > 1 ? cost_of<DC>(block_of<DC>(a, all, 0, sh.lim)) : 0;
+            total = (static_cast<int64_t>(first) * (blocks - 1) + cost_of<DC>(block_of<DC>(a, all, (blocks - 1) * S::kBlock, sh.lim))) * a.kv.kv_heads;
+            if (tid == 0) mine.before = first;
+        } else {
+            total = for_blocks(a, sh, take, &once) * a.kv.kv_heads;
+        }
         const int ctas = gridDim.x, cta = blockIdx.x;
         Share w;
         w.x0 = total * cta / ctas;
@@ -1078,7 +1089,14 @@ struct Kernel {
                 sh.first = mine;
             }
         };
-        if (once) {
+        if (a.prefix) {
+            if (tid == 0) {
+                const int64_t each = mine.before, per = each * a.kv.kv_heads;
+                const int i = per > 0 ? static_cast<int>(min(w.x0 / per, static_cast<int64_t>(blocks - 1))) : 0;
+                take(all, i * S::kBlock, block_of<DC>(a, all, i * S::kBlock, sh.lim), i * each);
+                find();
+            }
+        } else if (once) {
             find();
         } else {
             for_blocks(a, sh, [&](const span::Seq &q, int row0, const Block &k, int64_t before) {
@@ -1088,6 +1106,7 @@ struct Kernel {
         }
         if (tid < 2) a.info[2 * cta + tid].tiles = 0;  // no parts yet
         __syncthreads();
+        if (tid == 0) mbar_arrive(smem_addr(&sh.segfull[0]));  // the first segment is there
         if (warp < 8) {
             tc::set_registers_up<208>();
             softmax(a, sh, qs, base);
@@ -1123,7 +1142,7 @@ struct Kernel {
             }
             Segment &g = sh.seg[n % kSegs];
             if (n > 0) advance(a, sh, w, at, g);  // (the first is there)
-            if (sh.abort) g.stop = 1;
+            if (sh.abort && n > 0) g.stop = 1;
             if (!g.stop && g.slot >= 0) {
                 SpanInfo &i = a.info[g.slot];
                 i.b = g.seq.b;
@@ -1133,7 +1152,7 @@ struct Kernel {
                 i.t1 = g.t1;
                 i.tiles = g.block.tiles;
             }
-            mbar_arrive(smem_addr(&sh.segfull[n % kSegs]));
+            if (n > 0) mbar_arrive(smem_addr(&sh.segfull[n % kSegs]));
             if (g.stop) return;
         }
     }
