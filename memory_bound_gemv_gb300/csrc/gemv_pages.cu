@@ -149,24 +149,33 @@ __global__ void __launch_bounds__(kThreads, 1) mbg_assign_kernel(const __grid_co
         if (tid >= fit) tok_end[tid] = tok_last, page_end[tid] = page_last;
         __syncthreads();
         const int step = kThreads * blocks, me = rank * kThreads + tid;
-        // four tokens side by side to a thread
-        for (int64_t i0 = tokens / 4 * 4 + 4 * me; i0 < tok_last; i0 += 4 * step) {
-            int r = find(tok_end, n_chunk, i0 < tokens ? tokens : i0), slot[4], seq[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int64_t i = i0 + k;
-                if (i < tokens || i >= tok_last) continue;
-                while (tok_end[r] <= i) ++r;
-                slot[k] = from_slot[r] + static_cast<int>(i - (r ? tok_end[r - 1] : tokens));
-                seq[k] = b0 + r;
+        // a token to a thread, or four side by side where there are more
+        if (tok_last - tokens <= step) {
+            const int64_t i = tokens + me;
+            if (i < tok_last) {
+                const int r = find(tok_end, n_chunk, i);
+                a.slots[i] = from_slot[r] + static_cast<int>(i - (r ? tok_end[r - 1] : tokens));
+                a.seq[i] = b0 + r;
             }
-            if (a.wide && i0 >= tokens && i0 + 4 <= tok_last) {
-                *reinterpret_cast<int4 *>(a.slots + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-                *reinterpret_cast<int4 *>(a.seq + i0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
-            } else {
+        } else {
+            for (int64_t i0 = tokens / 4 * 4 + 4 * me; i0 < tok_last; i0 += 4 * step) {
+                int r = find(tok_end, n_chunk, i0 < tokens ? tokens : i0), slot[4], seq[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (i0 + k >= tokens && i0 + k < tok_last) a.slots[i0 + k] = slot[k], a.seq[i0 + k] = seq[k];
+                for (int k = 0; k < 4; ++k) {
+                    const int64_t i = i0 + k;
+                    if (i < tokens || i >= tok_last) continue;
+                    while (tok_end[r] <= i) ++r;
+                    slot[k] = from_slot[r] + static_cast<int>(i - (r ? tok_end[r - 1] : tokens));
+                    seq[k] = b0 + r;
+                }
+                if (a.wide && i0 >= tokens && i0 + 4 <= tok_last) {
+                    *reinterpret_cast<int4 *>(a.slots + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+                    *reinterpret_cast<int4 *>(a.seq + i0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (i0 + k >= tokens && i0 + k < tok_last) a.slots[i0 + k] = slot[k], a.seq[i0 + k] = seq[k];
+                }
             }
         }
         for (int64_t i = taken + me; i < page_last; i += step) {

@@ -441,3 +441,69 @@ def test_shared_out_of_range_is_reported():
         mbg.gemv_attn_shared(cache, q, ints(lengths), ints([3, 4]))
     with pytest.raises(ValueError):
         mbg.gemv_attn_shared(cache, q[:, :, :32], ints(lengths), ints([3]))
+
+
+@pytest.mark.parametrize("dim", [8, 16, 128])
+def test_infinities_next_to_cut_blocks(dim):
+    """Rows that are joined from parts, and rows of a prefix, are computed again where a hidden value is infinite."""
+    n, m = 3000, 200
+    cache = make_cache(81, [n], 1, dim, 16, BF16)
+    q = normal(82, (m, 4, dim), BF16)
+    starts, lens = ints([0, m]), ints([n])
+    ref, tol, _, _ = prompt_reference(cache, q, [0, m], [n], dim ** -0.5, 0, 0)
+    last = int(cache.page_table[0, (n - 1) // 16])
+    cache.v[last, (n - 1) % 16] = math.inf  # the last token's own
+    got = mbg.gemv_attn_prompt(cache, q, starts, lens)
+    close(got[:-1], ref[:-1], tol[:-1])
+    assert (got[-1] == math.inf).all()
+    lengths = [2600, 2990, 3000]
+    shared = mbg.PagedKV(cache.k, cache.v, cache.page_table.expand(3, -1).contiguous())
+    got = mbg.gemv_attn_shared(shared, q[:3], ints(lengths), ints([3000]))
+    for b in (0, 1):
+        k, v = rows_of(cache, 0, list(range(lengths[b])))
+        ref, tol, _, _ = attend(q[b:b + 1], k, v, hidden_of([lengths[b]], lengths[b], 0, 0), dim ** -0.5, BF16)
+        close(got[b:b + 1], ref, tol, f"sequence {b}")
+    assert (got[2] == math.inf).all()
+
+
+def test_prompt_arguments_are_checked():
+    cache = make_cache(83, [20, 20], 2, 64, 16, F16, fill=0.0)
+    q, starts, n = normal(1, (9, 4, 64), F16), ints([0, 4, 9]), ints([20, 20])
+    for bad in (dict(q=q[:, :3]), dict(q=q[..., :32]), dict(q=q[0]), dict(starts=ints([0, 9])), dict(lengths=ints([20])),
+                dict(window=-1), dict(sinks=2 ** 31), dict(out=q[:5]), dict(lse=torch.zeros(9, 3, device="cuda")),
+                dict(starts=starts.cpu()), dict(q=q.transpose(1, 2))):
+        args = dict(q=q, starts=starts, lengths=n)
+        args.update(bad)
+        with pytest.raises(ValueError):
+            mbg.gemv_attn_prompt(cache, args.pop("q"), args.pop("starts"), args.pop("lengths"), **args)
+    for bad in (q.float(), q.bfloat16()):
+        with pytest.raises(TypeError):
+            mbg.gemv_attn_prompt(cache, bad, starts, n)
+    with pytest.raises(TypeError):
+        mbg.gemv_attn_shared(cache, q[:2], n, torch.zeros(1, device="cuda"))
+    empty = mbg.gemv_attn_prompt(cache, q[:0], ints([0, 0, 0]), n)
+    assert empty.shape == (0, 4, 64)
+
+
+def test_two_threads_share_a_prefix_call_by_call():
+    """Calls of two threads on one stream do not mix: a call is three launches over one workspace."""
+    import threading
+
+    lengths = [700, 640, 900]
+    caches = [shared_cache(84 + i, lengths, 640, 2, 128, 16, F16) for i in range(2)]
+    q, n, pre = normal(86, (3, 8, 128), F16), ints(lengths), ints([640])
+    want = [mbg.gemv_attn_shared(c, q, n, pre) for c in caches]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        outs = [mbg.gemv_attn_shared(caches[i], q, n, pre) for _ in range(50)]
+        torch.cuda.synchronize()
+        bad.extend(i for o in outs if not torch.equal(o, want[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
