@@ -1,7 +1,10 @@
 // Attention of many tokens: what follows the tiles (gemv_tile.cuh).
 //
 // Blocks of rows that several CTAs shared are joined from their parts, in the
-// order of their slots.  And rows are computed one by one where a tile cannot:
+// order of their slots; rows behind a shared prefix with what their own slots
+// give.  Bound by round trips: what parts there are, the rows' maxima and sums
+// and their O, requested together for several parts; 11 us behind the tiles of a
+// prompt of 9001 tokens, whose 150 cut blocks have 40 MB of parts.  And rows are computed one by one where a tile cannot:
 // in the value product a weight of 0 meets the values that other rows of the tile
 // see and this one does not, and 0 times an infinite value is NaN.  Rows with a
 // NaN are therefore computed again, each for itself, slot by slot, in FP32.
@@ -456,7 +459,8 @@ static PFN_cuTensorMapEncodeTiled_v12000 encoder()
 static bool map_pool(CUtensorMap *map, const KvView &kv, void *pool, int64_t page, int64_t token, int64_t head, int elem, int box)
 {
     const auto encode = encoder();
-    if (!encode || kv.num_pages < 1) return false;
+    // (a stride of 0, a pool broadcast along an axis, is not a map's)
+    if (!encode || kv.num_pages < 1 || token < 1 || head < 1 || page < 1) return false;
     const cuuint64_t dims[4] = {static_cast<cuuint64_t>(kv.dim), static_cast<cuuint64_t>(kv.page_size), static_cast<cuuint64_t>(kv.kv_heads),
                                 static_cast<cuuint64_t>(kv.num_pages)};
     const cuuint64_t strides[3] = {static_cast<cuuint64_t>(token) * 2, static_cast<cuuint64_t>(head) * 2, static_cast<cuuint64_t>(page) * 2};

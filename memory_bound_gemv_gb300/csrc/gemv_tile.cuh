@@ -18,25 +18,37 @@
 //   warps 0-3, 4-7  two streams of softmax, a thread per row: S from tensor
 //                   memory, P back over it, at the end O;
 //   warps 8-11      K and V from their pages into swizzled shared memory: by bulk
-//                   tensor copies (TMA) of the tokens of a page, a warp each, or,
-//                   where pages are not of a multiple of 8 tokens, 16 bytes at a time
-//                   (cp.async), and unaligned pools element by element;
-//   warp 12         one thread issues the products;
+//                   tensor copies (TMA) of the tokens of a page, a warp each for
+//                   K and V, or, where pages are not of a multiple of 8 tokens or
+//                   heads are narrower than 64, 16 bytes at a time (cp.async), and
+//                   unaligned pools element by element;
+//   warp 12         issues the products;
 //   warp 13         looks up what the block does next;
 //   warps 14, 15    make what is copied piece by piece visible to the tensor core (a
 //                   fence of some 0.2 us, during which the products would pause).
-// Bulk copies: parts of prompts 835 us -> see below; a place in the ring is free for
-// the shorter, and pieces take 0.65 us to issue per tile and more to arrive than the
-// products take.
 // While one stream's softmax runs, the other's products do.  The streams are two
 // tiles of rows over the same slots, or with up to 128 rows one tile of
 // rows over even and odd tiles of slots, joined at the end.  (Head sizes above
-// 128: one stream, O takes half of tensor memory.)
+// 128: one stream with two buffers of S, O takes half of tensor memory.)
+//
+// What it measured: a tile of 128 slots for both streams takes 2.3 us (head size
+// 128), of which the tensor core works 1.9 (48 instructions of 64 cycles; 0.93 us
+// per stream are some 75 cycles each); the softmax of a stream takes 0.9 and its
+// hand-overs 0.5.  2000 new tokens behind up to 12000 cached ones, six
+// sequences: 581 us, 890 TFLOP/s counted without P's second part; with copies
+// piece by piece 835 us (a place of the ring is free for shorter than they
+// need to be issued, 0.65 us, and to arrive).  Tiles of 64 slots with two
+// buffers of S: 990 us -- the products' scores are read at half the width and their
+// waits come twice as often.
 //
 // P enters the value product in two 16-bit parts, 16 bits (bf16) or 22 (f16) of
-// FP32's 24: one part would add an error as large as the output's own rounding,
-// and costs half of the value product's time.  In f16 P is multiplied by
+// FP32's 24: one part would add an error as large as the output's own rounding.
+// The second one is a third of the products.  In f16 P is multiplied by
 // 2^11, so that what is small beside the largest weight is kept down to 2^-35 of it.
+//
+// A weight of 0 times an infinite value is NaN, and a tile's values meet the rows
+// that do not see them too: rows with a NaN are computed once more, alone
+// (gemv_span.cu).
 //
 // Blocks of rows are cut between the CTAs: all tiles of a call are numbered and
 // each CTA takes an equal share of consecutive ones, whatever the lengths (read
@@ -81,6 +93,7 @@ struct Shape {
     static constexpr int kKvBytes = kTok * DC * 128;
     static constexpr int kStages = DC == 1 ? 4 : DC == 3 ? 3 : 2;  // tiles of K, and of V, in shared memory
     static constexpr int kBlock = kStreams * kRows;  // rows of a block
+    static constexpr int kMost = 32768 / kTok;       // tiles of a segment
     static constexpr int kOColumn = 256;
 };
 
@@ -92,13 +105,20 @@ struct Block {
     int rows;
 };
 
-// What a CTA does next: tiles [t0, t1) of a block.
+// What a CTA does next: tiles [t0, t1) of a block.  Not more than 32768 slots at
+// a time: the tensor core adds products to O with the bits that O leaves
+// them, cut off, so that a long sum comes out too small (equal weights, positive
+// values, binary16: by 0.1 of 2^-12 after 32768 slots, by 2.3 after 131072, by 27
+// after 2^20).  What has been summed up is put aside and joined in FP32.  (And
+// no wait of another warp lasts longer than a few segments.)
 struct Segment {
     span::Seq seq;
     Block block;
     int h, row0;      // cached head, first row among its sequence's
     int t0, t1;
     int slot;         // of the part; -1: the whole block
+    int aside;        // where sums are put aside
+    int more, merge;  // some tiles follow; others came before
     int stop;         // nothing is left
 };
 
@@ -106,6 +126,7 @@ struct Segment {
 struct Cursor {
     int64_t before;   // cost of what lies before the block, per cached head
     int b, row0, h;
+    int done;         // tiles of this CTA's share of it that are behind
     span::Seq seq;
     Block block;
 };
@@ -294,19 +315,26 @@ struct Kernel {
             const Block &k = at.block;
             const int64_t r0 = at.before * a.kv.kv_heads + static_cast<int64_t>(at.h) * cost_of<DC>(k);
             if (r0 >= w.x1) break;
-            const int t0 = cut(k, r0, w.x0, w.near), t1 = cut(k, r0, w.x1, w.near), h = at.h++;
+            const int t0 = cut(k, r0, w.x0, w.near), t1 = cut(k, r0, w.x1, w.near);
             // (a block without slots is its beginning's)
             if (t0 < t1 || (k.tiles == 0 && r0 >= w.x0)) {
+                const int mine = 2 * static_cast<int>(blockIdx.x);
                 out.seq = at.seq;
                 out.block = k;
-                out.h = h;
+                out.h = at.h;
                 out.row0 = at.row0;
-                out.t0 = t0;
-                out.t1 = t1;
-                out.slot = t0 == 0 && t1 == k.tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (t0 == 0 ? 1 : 0);
+                out.t0 = t0 + at.done;
+                out.t1 = min(t1, out.t0 + S::kMost);
+                out.slot = t0 == 0 && t1 == k.tiles ? -1 : mine + (t0 == 0 ? 1 : 0);
+                out.aside = out.slot >= 0 ? out.slot : mine + 1;  // (a part there would be the CTA's last)
+                out.merge = at.done > 0;
+                out.more = out.t1 < t1;
                 out.stop = 0;
+                at.done = out.more ? out.t1 - t0 : 0;
+                if (!out.more) ++at.h;
                 return;
             }
+            ++at.h;
         }
         at.b = batch;
         out.stop = 1;
@@ -464,7 +492,7 @@ struct Kernel {
             ok = __all_sync(kFull, wait(sh, sh.segfull[n % kSegs], n / kSegs & 1, a));
             if (!ok) break;
             const Segment &g = sh.seg[n % kSegs];
-            if (g.stop) return;
+            if (g.stop) break;
             const int32_t *table = kv.table + g.seq.b * kv.table_stride;
             const int t0 = g.t0, t1 = g.t1, h = g.h;
             const int length = g.seq.n;
@@ -504,7 +532,7 @@ struct Kernel {
                 page = look_up(j + 1, off);
             }
         }
-        // given up: no copy is left under way
+        // no copy is left under way, had others given up too
         for (uint32_t i = count > S::kStages ? count - S::kStages : 0; i < count; ++i) {
             const int st = i % S::kStages;
             const bool edge = edges >> st & 1;
@@ -924,8 +952,18 @@ struct Kernel {
     {
         const int dim = a.kv.dim;
         const int64_t t = g.seq.q0 + token, index = t * a.q_heads + head;
+        float *part = a.part + g.aside * a.part_stride + stream * (a.part_stride / S::kStreams);
+        float *part_stat = part + (dim + 15) / 16 * 16 * kRows;
+        const bool aside = g.more || g.slot >= 0, merge = g.merge;
+        float now = 1.f, then = 0.f;  // factors of this segment's O and of what this thread put aside
+        if (merge && live) {
+            const float m1 = part_stat[row], l1 = part_stat[kRows + row], mm = fmaxf(m, m1), base = mm == -INFINITY ? 0.f : mm;
+            now = exp2_approx(m - base);
+            then = exp2_approx(m1 - base);
+            l = l * now + l1 * then;
+            m = mm;
+        }
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        float *part = a.part + g.slot * a.part_stride + stream * (a.part_stride / S::kStreams);
         bool nan = false;
         for (int c = 0; c < dim; c += 16) {
             float x[16];
@@ -943,9 +981,17 @@ struct Kernel {
                     if (c + i < dim) x[i] = x[i] * own + buf[(c + i) * kRows + row] * other;
             }
             if (live) {
+                if (merge) {
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 y = *reinterpret_cast<const float4 *>(part + ((c + i) / 4 * kRows + row) * 4);
+                        x[i] = x[i] * now + y.x * then, x[i + 1] = x[i + 1] * now + y.y * then;
+                        x[i + 2] = x[i + 2] * now + y.z * then, x[i + 3] = x[i + 3] * now + y.w * then;
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) nan = nan || (c + i < dim && x[i] != x[i]);
-                if (g.slot >= 0) {
+                if (aside) {
 #pragma unroll
                     for (int i = 0; i < 16; i += 4)
                         *reinterpret_cast<float4 *>(part + ((c + i) / 4 * kRows + row) * 4) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
@@ -976,10 +1022,9 @@ struct Kernel {
         }
         __syncwarp();
         if (!live) return;
-        if (g.slot >= 0) {
-            float *stat = part + (dim + 15) / 16 * 16 * kRows;
-            stat[row] = m;
-            stat[kRows + row] = l;
+        if (aside) {
+            part_stat[row] = m;
+            part_stat[kRows + row] = l;
             a.redo[index] = 0;  // the join's business
             return;
         }
@@ -1054,6 +1099,7 @@ struct Kernel {
         Cursor mine;
         mine.before = -1;
         auto take = [&](const span::Seq &q, int row0, const Block &k, int64_t before) {
+            mine.done = 0;
             mine.before = before;
             mine.b = q.b;
             mine.row0 = row0;
@@ -1110,6 +1156,7 @@ struct Kernel {
         if (warp < 8) {
             tc::set_registers_up<208>();
             softmax(a, sh, qs, base);
+            asm volatile("cp.async.wait_all;" ::: "memory");  // (given up: Q may be under way)
         } else if (warp < 12) {
             tc::set_registers_down<56>();
             if (!bulk)

@@ -507,3 +507,53 @@ def test_two_threads_share_a_prefix_call_by_call():
     for t in threads:
         t.join()
     assert not bad
+
+
+def test_prompt_blocks_that_take_seconds():
+    """A call's waits are bounded, not its length: 2^28 - 5 slots (one page, named again and again) for each of
+    152 heads.  Keys of 0 weigh every slot alike and the values are powers of two, so that sums of a tile's weights
+    and of 32768 slots' values are exact; the last ones' rounding is 2^-24 of them."""
+    page, pages, hk, dim = 512, 2 ** 19, 152, 64
+    n = page * pages - 5
+    v = torch.tensor([2.0 ** (d % 4) * (1 - d % 2 * 2) for d in range(dim)], dtype=BF16, device="cuda")
+    cache = mbg.PagedKV(torch.zeros(1, page, hk, dim, dtype=BF16, device="cuda"), v.expand(1, page, hk, dim).contiguous(),
+                        torch.zeros(1, pages, dtype=torch.int32, device="cuda"))
+    lse = torch.empty(1, hk, dtype=torch.float32, device="cuda")
+    got = mbg.gemv_attn_prompt(cache, normal(91, (1, hk, dim), BF16), ints([0, 1]), ints([n]), lse=lse)
+    torch.cuda.synchronize()
+    assert torch.equal(got, v.expand(1, hk, dim))
+    assert (lse.double() - math.log(n)).abs().max() <= 2.0 ** -18  # half a step of 19.4, of its 13.4 / ln 2 and of log2
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("dim,m", [(64, 1), (128, 1), (128, 70), (192, 1)])
+def test_prompt_and_prefix_sums_of_many_slots(dtype, dim, m):
+    """2^20 slots of like weights and positive values (two pages named again and again), 200 heads, so that some
+    blocks of rows are whole and some are cut.  A sum that keeps 24 bits loses up to 2^-23 of itself with each
+    product, half of that on average, and is half of the whole on average: 2^-25 N = 2^-10 of N = 2^15 slots, which the
+    kernel does not exceed; what joins the sums is FP32's rounding, far below."""
+    page, hk, n = 256, 200, 2 ** 20
+    torch.manual_seed(94)
+    v = (0.5 + torch.rand(2, page, hk, dim, device="cuda") / 2).to(dtype)
+    table = torch.arange(n // page, dtype=torch.int32, device="cuda")[None] % 2
+    cache = mbg.PagedKV(torch.zeros_like(v), v, table)
+    want = v.double().mean((0, 1))[None, :, None]  # the last tokens' missing slots: m / n of it
+    q = normal(95, (m, 4 * hk, dim), dtype)
+    got = mbg.gemv_attn_prompt(cache, q, ints([0, m]), ints([n])).view(m, hk, 4, dim)
+    tol = (2.0 ** -10 + HALF_STEP[dtype] + m / n) * want
+    assert ((got.double() - want).abs() <= tol).all()
+    both = mbg.PagedKV(cache.k, v, table.expand(m, -1).contiguous())
+    got = mbg.gemv_attn_shared(both, q, ints([n] * m), ints([n - 7])).view(m, hk, 4, dim)
+    assert ((got.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("axis", [1, 2])
+def test_prompt_and_prefix_over_broadcast_pools(axis):
+    """Pools that are broadcast along their tokens or heads (a stride of 0)."""
+    base = make_cache(92, [100, 77], 4, 64, 16, F16)
+    k, v = (x.narrow(axis, 1, 1).expand_as(x) for x in (base.k, base.v))
+    cache, dense = mbg.PagedKV(k, v, base.page_table), mbg.PagedKV(k.contiguous(), v.contiguous(), base.page_table)
+    q, starts, lens = normal(93, (60, 8, 64), F16), ints([0, 40, 60]), ints([100, 77])
+    assert torch.equal(mbg.gemv_attn_prompt(cache, q, starts, lens), mbg.gemv_attn_prompt(dense, q, starts, lens))
+    a, b = (mbg.PagedKV(c.k, c.v, c.page_table[:1].expand(2, -1).contiguous()) for c in (cache, dense))
+    assert torch.equal(mbg.gemv_attn_shared(a, q[:2], lens, ints([64])), mbg.gemv_attn_shared(b, q[:2], lens, ints([64])))
