@@ -10,7 +10,8 @@ Function names match the C entry points: ``gemv_f32``, ``gemv_f16``,
 ``gemv_q8``, ``gemv_q4``, ``gemv_f16_xf32``, ``gemv_q8_rowscale``, ``gemv_probe_read``, ``gemv_dequant_q8``,
 ``gemv_dequant_q4``, ``gemv_run_variant`` ...  ``lib()`` returns the raw
 ctypes handle for callers that want to pass pointers themselves.  The
-decode-step operators (``PagedKV``, ``gemv_attn_paged`` ...) are in ``decode``.
+decode-step and serving operators (``PagedKV``, ``gemv_attn_paged``, ``gemv_attn_prompt`` ...)
+are in ``decode``.
 """
 
 from __future__ import annotations

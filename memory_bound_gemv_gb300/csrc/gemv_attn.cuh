@@ -3,7 +3,9 @@
 //   s_t = scale * q . k_t,  p = softmax(s),  o = sum_t p_t v_t
 //
 // over the tokens t in [max(0, len - window), len) of a sequence, and with
-// sinks those in [0, sinks), G query heads sharing one cached head.  One pass over the cache: each warp keeps a
+// sinks those in [0, sinks), G query heads sharing one cached head.  Behind a
+// prefix that is attended to elsewhere only the tokens from its end on are
+// read, and O, m and l are left in FP32 for the join (gemv_span.cu).  One pass over the cache: each warp keeps a
 // running maximum m, denominator l and output O of its own tokens and rescales
 // by 2^(m - m') when m grows (Milakov & Gimelshein's online softmax); the
 // warps, then the blocks, that share a row are joined by the same rule.

