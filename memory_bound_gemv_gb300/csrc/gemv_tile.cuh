@@ -35,7 +35,7 @@
 // 128), of which the tensor core works 1.9 (48 instructions of 64 cycles; 0.93 us
 // per stream are some 75 cycles each); the softmax of a stream takes 0.9 and its
 // hand-overs 0.5.  2000 new tokens behind up to 12000 cached ones, six
-// sequences: 581 us, 890 TFLOP/s counted without P's second part; with copies
+// sequences: 580 us, 888 TFLOP/s counted without P's second part; with copies
 // piece by piece 835 us (a place of the ring is free for shorter than they
 // need to be issued, 0.65 us, and to arrive).  Tiles of 64 slots with two
 // buffers of S: 990 us -- the products' scores are read at half the width and their
@@ -925,7 +925,10 @@ struct Kernel {
             if (!join && !next_segment(a, sh, n + 1, stream, row, lane, qs)) return;
             if (both || stream == 0) {
                 const Row r = row_of(a, g, stream, row);
-                finish(a, g, o_at, any, stream, row, r.live, r.token, r.head, m, l, own, other, join ? shared_o : nullptr);
+                if (g.merge)
+                    finish<true>(a, g, o_at, any, stream, row, r.live, r.token, r.head, m, l, own, other, join ? shared_o : nullptr);
+                else
+                    finish<false>(a, g, o_at, any, stream, row, r.live, r.token, r.head, m, l, own, other, join ? shared_o : nullptr);
             }
             tc::fence_before();
             __syncwarp();
@@ -947,6 +950,7 @@ struct Kernel {
     }
 
     // Writes a row: its output, its part of the prefix, or a part of a cut block.
+    template <bool MERGE>
     static __device__ __forceinline__ void finish(const SpanArgs &a, const Segment &g, uint32_t o_at, bool any, int stream, int row, bool live,
                                                   int token, int head, float m, float l, float own, float other, const float *buf)
     {
@@ -954,9 +958,9 @@ struct Kernel {
         const int64_t t = g.seq.q0 + token, index = t * a.q_heads + head;
         float *part = a.part + g.aside * a.part_stride + stream * (a.part_stride / S::kStreams);
         float *part_stat = part + (dim + 15) / 16 * 16 * kRows;
-        const bool aside = g.more || g.slot >= 0, merge = g.merge;
+        const bool aside = g.more || g.slot >= 0;
         float now = 1.f, then = 0.f;  // factors of this segment's O and of what this thread put aside
-        if (merge && live) {
+        if (MERGE && live) {
             const float m1 = part_stat[row], l1 = part_stat[kRows + row], mm = fmaxf(m, m1), base = mm == -INFINITY ? 0.f : mm;
             now = exp2_approx(m - base);
             then = exp2_approx(m1 - base);
@@ -981,7 +985,7 @@ struct Kernel {
                     if (c + i < dim) x[i] = x[i] * own + buf[(c + i) * kRows + row] * other;
             }
             if (live) {
-                if (merge) {
+                if (MERGE) {
 #pragma unroll
                     for (int i = 0; i < 16; i += 4) {
                         const float4 y = *reinterpret_cast<const float4 *>(part + ((c + i) / 4 * kRows + row) * 4);
