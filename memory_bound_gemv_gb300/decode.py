@@ -575,9 +575,9 @@ def gemv_kv_assign(cache: PagedKV, pool: PagePool, lengths, fresh, starts=None, 
     them, -1 and 0 behind the last one (``tokens`` sizes new ones).  lengths
     becomes the slots in use afterwards, or with ``lengths_out`` these go there;
     so does the pool's state with ``state_out``."""
-    if seq is not None and _quick.assign(cache._at, cache.index, pool.ring, pool.state, lengths, fresh, starts, slots, seq,
-                                         shared, lengths_out, state_out,
-                                         stream if stream is None else _mbg._stream_ptr(stream)) == 0:
+    if seq is not None and tokens is None and _quick.assign(
+            cache._at, cache.index, pool.ring, pool.state, lengths, fresh, starts, slots, seq, shared, lengths_out,
+            state_out, stream if stream is None else _mbg._stream_ptr(stream)) == 0:
         return starts, slots, seq
     index, batch = cache.index, (cache.batch,)
     if pool.index != index:

@@ -265,6 +265,24 @@ def test_norm_rope_checks_its_arguments():
         mbg.gemv_rope_append(*args, norm=True, q_weight=torch.ones(64, dtype=torch.float64, device="cuda"))
 
 
+def test_assign_checks_its_arguments():
+    cache = make_cache(5, [4, 4], 2, 64, 16, F16, fill=0.0)
+    pool, n, fresh = mbg.PagePool(6), ints([4, 4]), ints([1, 1])
+    held = dict(starts=ints([0] * 3), slots=ints([0] * 9), seq=ints([0] * 9))
+    for bad in (dict(tokens=5), dict(seq=held["seq"][:8]), dict(starts=ints([0, 0])), dict(slots=held["slots"][:, None]),
+                dict(shared=ints([0])), dict(lengths_out=ints([0])), dict(state_out=ints([0])), dict(seq=held["seq"].cpu()),
+                dict(slots=torch.zeros(18, dtype=torch.int32, device="cuda")[::2])):
+        with pytest.raises(ValueError):
+            mbg.gemv_kv_assign(cache, pool, n, fresh, **{**held, **bad})
+    with pytest.raises(TypeError):
+        mbg.gemv_kv_assign(cache, pool, n, fresh.long(), **held)
+    with pytest.raises(ValueError):
+        mbg.gemv_kv_assign(cache, pool, n, fresh)  # neither slots nor tokens
+    assert n.tolist() == [4, 4] and pool.state.tolist() == [0, 6]  # nothing ran
+    mbg.gemv_kv_assign(cache, pool, n, fresh, tokens=9, **held)
+    assert n.tolist() == [5, 5] and held["slots"].tolist() == [4, 4] + [-1] * 7
+
+
 # --------------------------------------------------------------------------- single tokens with sinks
 
 def sinks_reference(cache, q, lengths, scale, window, sinks):
