@@ -584,7 +584,8 @@ gemv_status_t gemv_rope_append_norm(const gemv_kv_t *kv, const gemv_rope_t *args
  *     and state.
  * Of kv the page table, its sizes and num_pages are used.  A length, a page or a
  * state out of range, new tokens beyond the capacity, and more pages returned than
- * the ring has lent are reported as GEMV_ERR_BAD_INDEX; such a request gets nothing.
+ * the ring has lent are reported as GEMV_ERR_BAD_INDEX; such a request gets nothing,
+ * and where its length is out of range and it is over, returns nothing.
  */
 typedef struct {
     const int32_t *lengths, *fresh, *shared;

@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1) mbg_assign_kernel(const __grid_co
         const int b = b0 + tid, n_chunk = min(kThreads, batch - b0);
         int64_t n = 0, f = 0;
         int keep = 0;
+        bool wrong = false;  // a length out of range: what its row holds is not known to be its own
         if (b < batch) {
             n = a.lengths[b];
             f = a.fresh[b];
@@ -114,13 +115,14 @@ __global__ void __launch_bounds__(kThreads, 1) mbg_assign_kernel(const __grid_co
         }
         if (n < 0 || n > capacity || n + f > capacity) {
             if (rank == 0) report_error(a.err, DEVERR_BAD_INDEX);
+            wrong = n < 0 || n > capacity;
             n = n < 0 ? 0 : n > capacity ? capacity : n;
             f = f < 0 ? f : 0;
         }
         const bool over = f < 0;
         if (over) f = 0;
         const int have = pages_of(n, page_size);
-        int64_t need = pages_of(n + f, page_size) - have, back = over && have > keep ? have - keep : 0;
+        int64_t need = pages_of(n + f, page_size) - have, back = over && !wrong && have > keep ? have - keep : 0;
         // first sums: pages needed, pages returned
         int64_t need_sum = need, back_sum = back, need_all, back_all;
         scan2(sums[0], need_sum, back_sum, need_all, back_all);
