@@ -582,10 +582,13 @@ gemv_status_t gemv_rope_append_norm(const gemv_kv_t *kv, const gemv_rope_t *args
  *   - lengths_out [batch]: the slots in use afterwards (0 where a request is
  *     over); state_out [2]: the ring's state afterwards.  They may be lengths
  *     and state.
- * Of kv the page table, its sizes and num_pages are used.  A length, a page or a
- * state out of range, new tokens beyond the capacity, and more pages returned than
- * the ring has lent are reported as GEMV_ERR_BAD_INDEX; such a request gets nothing,
- * and where its length is out of range and it is over, returns nothing.
+ * Of kv the page table, its sizes and num_pages are used.  What follows is
+ * reported as GEMV_ERR_BAD_INDEX.  A length out of range, and new tokens beyond the
+ * capacity: such a request gets nothing, and with that length returns nothing
+ * where it is over.  A state out of range: no page is taken or put back.  A page in
+ * the ring that does not exist: whoever takes it gets -1 in its row of the page table,
+ * and its other pages and tokens as ever.  Pages that come back and do not
+ * exist, and more than the ring has lent: those are dropped.
  */
 typedef struct {
     const int32_t *lengths, *fresh, *shared;

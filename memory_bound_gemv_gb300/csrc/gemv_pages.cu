@@ -77,14 +77,47 @@ __device__ __forceinline__ int pages_of(int64_t n, int page_size)
     return n > 0 ? static_cast<int>((static_cast<uint32_t>(n) - 1) / static_cast<uint32_t>(page_size) + 1) : 0;
 }
 
+// Puts the pages that come back behind the ring's end, at `end`, once more and
+// one request at a time, without those that do not exist; returns how many.  No more
+// than `most` have a place.
+__device__ __noinline__ int64_t put_back(const AssignArgs &a, Sums &s, int64_t end, int64_t most)
+{
+    int64_t put = 0;
+    if (threadIdx.x == 0) report_error(a.err, DEVERR_BAD_INDEX);
+    for (int b = 0; b < a.batch; ++b) {
+        const int64_t n = a.lengths[b];
+        if (a.fresh[b] >= 0 || n < 0 || n > a.capacity) continue;
+        const int keep = a.shared ? max(0, a.shared[b]) / a.page_size : 0, have = pages_of(n, a.page_size);
+        for (int i0 = keep; i0 < have; i0 += kThreads) {
+            const int i = i0 + threadIdx.x;
+            const int page = i < have ? a.table[b * a.table_stride + i] : -1;
+            const bool there = page >= 0 && page < a.num_pages;
+            int64_t sum = there, none = 0, all, none_all;
+            scan2(s, sum, none, all, none_all);
+            __syncthreads();
+            if (there && put + sum <= most) {
+                int64_t place = end + put + sum - 1;
+                while (place >= a.ring_size) place -= a.ring_size;
+                a.ring[place] = page;
+            }
+            put += all;
+        }
+    }
+    return put < most ? put : most;
+}
+
 __global__ void __launch_bounds__(kThreads, 1) mbg_assign_kernel(const __grid_constant__ AssignArgs a)
 {
     __shared__ Sums sums[2];
     __shared__ int64_t tok_end[kThreads], page_end[kThreads], gone_end[kThreads];
     __shared__ int from_slot[kThreads], from_page[kThreads];
+    __shared__ int strays;  // (the first block's) of the pages that come back some do not exist
+    const int tid = threadIdx.x, rank = blockIdx.x, blocks = gridDim.x;
+    auto cluster = cooperative_groups::this_cluster();
+    if (tid == 0) strays = 0;
+    if (blocks > 1) cluster.barrier_arrive();  // waited for ahead of the first write to another block's memory
     pdl_trigger();
     pdl_wait();
-    const int tid = threadIdx.x, rank = blockIdx.x, blocks = gridDim.x;
     const int64_t at = a.state[0], count0 = a.state[1];
     // a state that cannot be: nothing is taken, nothing is put back
     const bool broken = at < 0 || count0 < 0 || count0 > a.ring_size || (at >= a.ring_size && a.ring_size > 0) ||
@@ -102,6 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1) mbg_assign_kernel(const __grid_co
         ahead = a.ring[place];
     }
     int64_t needed = 0, wanted = 0, taken = 0, gone = 0, tokens = 0;  // sums of the chunks before
+    bool stray = false;
     int after = 0;  // this thread's request of the last chunk: slots in use afterwards
     for (int b0 = 0; b0 < batch; b0 += kThreads) {
         const int b = b0 + tid, n_chunk = min(kThreads, batch - b0);
@@ -203,7 +237,9 @@ __global__ void __launch_bounds__(kThreads, 1) mbg_assign_kernel(const __grid_co
             const int r = find(gone_end, n_chunk, i);
             int64_t place = at + count + i;
             if (place >= a.ring_size) place -= a.ring_size;
-            a.ring[place] = a.table[(b0 + r) * a.table_stride + from_page[r] + (i - (r ? gone_end[r - 1] : gone))];
+            const int page = a.table[(b0 + r) * a.table_stride + from_page[r] + (i - (r ? gone_end[r - 1] : gone))];
+            if (page < 0 || page >= a.num_pages) stray = true;
+            a.ring[place] = page;
         }
         if (rank == 0 && b < batch) {
             a.starts[b + 1] = static_cast<int>(tok_end[tid]);
@@ -223,8 +259,16 @@ __global__ void __launch_bounds__(kThreads, 1) mbg_assign_kernel(const __grid_co
         a.seq[i] = 0;
     }
     // lengths and state may be written where they were read
-    if (blocks > 1) cooperative_groups::this_cluster().sync();
+    if (blocks > 1) {
+        cluster.barrier_wait();
+        if (stray) *cluster.map_shared_rank(&strays, 0) = 1;
+        cluster.sync();
+    } else {
+        if (stray) strays = 1;
+        __syncthreads();
+    }
     if (rank != 0) return;
+    if (strays) gone = put_back(a, sums[0], at + count, behind);
     if (batch <= kThreads) {
         if (tid < batch) a.lengths_out[tid] = after;
     } else {
