@@ -466,7 +466,7 @@ uint64_t gemv_capture_id(void *stream);
  * are zeros (lse, [tokens][q_heads]: -inf).  Rows of q that no sequence has are
  * left as they are.  Starts that do not ascend from 0 to tokens, and more new tokens
  * than slots, are reported as GEMV_ERR_BAD_INDEX; such tokens get zeros or are
- * left alone.  workspace: gemv_attn_prompt_workspace(...) bytes, 256-byte
+ * left alone.  So are pages that do not exist; their slots are left out.  workspace: gemv_attn_prompt_workspace(...) bytes, 256-byte
  * aligned; one workspace serves one call at a time, and needs no preparation.
  */
 typedef struct {

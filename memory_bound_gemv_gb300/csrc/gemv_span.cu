@@ -7,7 +7,8 @@
 // prompt of 9001 tokens, whose 150 cut blocks have 40 MB of parts.  And rows are computed one by one where a tile cannot:
 // in the value product a weight of 0 meets the values that other rows of the tile
 // see and this one does not, and 0 times an infinite value is NaN.  Rows with a
-// NaN are therefore computed again, each for itself, slot by slot, in FP32.
+// NaN are therefore computed again, each for itself, slot by slot, in FP32.  So are
+// rows that saw a page that does not exist.
 //
 // A block takes such a row.  Its warps share the slots 32 at a time: a lane forms
 // the score of one slot, the warp keeps a running maximum and sum, and adds the
@@ -172,7 +173,9 @@ __device__ void one_row(const SpanArgs &a, Shared &sh, int token, int head, int 
         if (f.own != 0.f) v += __ldcg(a.own + row * span_row(dim) + d) * f.own;
         elem_store1<E>(a.out, token * a.o_st + head * a.o_sh + d, v);
     }
-    if (threadIdx.x == 0 && !joined) {
+    if (threadIdx.x == 0 && joined) {  // the sums may differ from those of the tiles (a page that does not exist)
+        if (d0 == 0 && a.lse) a.lse[row] = lse_of(f.m, f.l);
+    } else if (threadIdx.x == 0) {
         if (a.pre) {
             a.pre[(row + 1) * span_row(dim) - 4] = top;
             a.pre[(row + 1) * span_row(dim) - 3] = sum;

@@ -48,7 +48,10 @@
 //
 // A weight of 0 times an infinite value is NaN, and a tile's values meet the rows
 // that do not see them too: rows with a NaN are computed once more, alone
-// (gemv_span.cu).
+// (gemv_span.cu).  So are the rows of a segment in which a page does not exist: its
+// slots are copied as zeros, and the rows become NaN on purpose.  (Scores of such slots
+// set to -inf tile by tile, by bits beside K, keep the tiles' speed there and cost
+// it everywhere else: a prompt of 9001 tokens 439 -> 485 us, so 461.)
 //
 // Blocks of rows are cut between the CTAs: all tiles of a call are numbered and
 // each CTA takes an equal share of consecutive ones, whatever the lengths (read
@@ -120,6 +123,7 @@ struct Segment {
     int aside;        // where sums are put aside
     int more, merge;  // some tiles follow; others came before
     int stop;         // nothing is left
+    int missing;      // rows see a slot whose page does not exist
 };
 
 // The block, and the cached head, that is looked at next.
@@ -329,7 +333,7 @@ struct Kernel {
                 out.aside = out.slot >= 0 ? out.slot : mine + 1;  // (a part there would be the CTA's last)
                 out.merge = at.done > 0;
                 out.more = out.t1 < t1;
-                out.stop = 0;
+                out.stop = out.missing = 0;
                 at.done = out.more ? out.t1 - t0 : 0;
                 if (!out.more) ++at.h;
                 return;
@@ -434,8 +438,10 @@ struct Kernel {
             };
             auto report = [&](int j, int page, int off) {
                 const int slot = (j < sink_tiles ? j : j + skip) * kTok + warp * kOwn + lane;
-                if (j < t1 && lane < kOwn && slot < hi && (slot >= lo || slot < sinks) && (page < 0 || page >= kv.num_pages))
+                if (j < t1 && lane < kOwn && slot < hi && (slot >= lo || slot < sinks) && (page < 0 || page >= kv.num_pages)) {
                     report_error(a.err, DEVERR_BAD_INDEX);
+                    sh.seg[n % kSegs].missing = 1;  // (the softmax keeps the segment until its rows are written)
+                }
             };
             int off_k = 0, off_v = 0, page_v = -1;
             int page_k = look_up(t0, off_k);
@@ -509,7 +515,10 @@ struct Kernel {
                     off = slot - idx * kv.page_size;
                     page = __ldg(table + idx);
                     if (page < 0 || page >= kv.num_pages) {
-                        if (!is_v && chunk == 0) report_error(a.err, DEVERR_BAD_INDEX);
+                        if (!is_v && chunk == 0) {
+                            report_error(a.err, DEVERR_BAD_INDEX);
+                            sh.seg[n % kSegs].missing = 1;  // (the softmax keeps the segment until its rows are written)
+                        }
                         page = -1;
                     }
                 }
@@ -967,6 +976,9 @@ struct Kernel {
             l = l * now + l1 * then;
             m = mm;
         }
+        // (a thread of the copies has written it ahead of the tile's K)
+        const bool missing = *const_cast<const volatile int *>(&g.missing) != 0;
+        if (missing) l = 1.f;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         bool nan = false;
         for (int c = 0; c < dim; c += 16) {
@@ -983,6 +995,10 @@ struct Kernel {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     if (c + i < dim) x[i] = x[i] * own + buf[(c + i) * kRows + row] * other;
+            }
+            if (missing) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = __int_as_float(0x7FFFFFFF);
             }
             if (live) {
                 if (MERGE) {
