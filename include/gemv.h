@@ -464,9 +464,12 @@ uint64_t gemv_capture_id(void *stream);
  * cache).  The i-th of m attends to the slots t < n with n = lengths[b] - m + i +
  * 1, with a window to n - window <= t < n and t < sinks.  Rows without weights
  * are zeros (lse, [tokens][q_heads]: -inf).  Rows of q that no sequence has are
- * left as they are.  Starts that do not ascend from 0 to tokens, and more new tokens
- * than slots, are reported as GEMV_ERR_BAD_INDEX; such tokens get zeros or are
- * left alone.  So are pages that do not exist; their slots are left out.  workspace: gemv_attn_prompt_workspace(...) bytes, 256-byte
+ * left as they are.  starts begin at 0 or above, ascend, and end at tokens or
+ * below; those that do not, and more new tokens than slots, are reported as
+ * GEMV_ERR_BAD_INDEX.  Tokens of a sequence that ends below its start, that lies
+ * outside the rows or that begins below the start of one before it are left alone,
+ * those without a slot get zeros.  Pages that do not exist are reported too; their
+ * slots are left out.  workspace: gemv_attn_prompt_workspace(...) bytes, 256-byte
  * aligned; one workspace serves one call at a time, and needs no preparation.
  */
 typedef struct {

@@ -37,6 +37,7 @@ struct Shared {
     float q[kMaxDim];
     float o[kWarps][kMaxDim];
     float m[kWarps], l[kWarps];
+    int first[kWarps];
 };
 
 __device__ __forceinline__ float exp2_from(float x, float m)
@@ -68,27 +69,53 @@ __device__ __forceinline__ Both both_of(const SpanArgs &a, int64_t index, float 
     return r;
 }
 
-// The sequence that token t belongs to; -1: none.
-__device__ int seq_of_token(const SpanArgs &a, int t)
+// Whether the starts ascend (the whole block asks).
+__device__ bool ascending(const SpanArgs &a)
 {
-    if (a.prefix) return 0;
-    int lo = 0, hi = a.kv.batch;  // the last b with starts[b] <= t
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (mid < a.kv.batch && __ldg(a.starts + mid) <= t)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    return lo;
+    bool falls = false;
+    for (int b = threadIdx.x; b < a.kv.batch; b += kThreads) falls = falls || __ldg(a.starts + b + 1) < __ldg(a.starts + b);
+    return !__syncthreads_or(falls);
 }
 
+// The sequence that token t belongs to, if any does; -1: none does (the whole
+// block asks).
+__device__ int seq_of_token(const SpanArgs &a, Shared &sh, int t, bool ascend)
+{
+    if (a.prefix) return 0;
+    const int batch = a.kv.batch, tid = threadIdx.x;
+    if (ascend) {
+        int lo = 0, hi = batch;  // the last b with starts[b] <= t
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (mid < batch && __ldg(a.starts + mid) <= t)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        return lo;
+    }
+    // The first start or end above t is the sequence's end, and no start before the
+    // sequence's lies above its own (span::seq_behind).
+    int first = batch + 1;
+    for (int i = tid; i <= batch && first > batch; i += kThreads)
+        if (__ldg(a.starts + i) > t) first = i;
+    first = __reduce_min_sync(kFull, first);
+    __syncthreads();
+    if (tid % 32 == 0) sh.first[tid / 32] = first;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) first = min(first, sh.first[w]);
+    const int b = first > batch ? -1 : first - 1;
+    bool above = false;
+    for (int i = tid; i < b; i += kThreads) above = above || __ldg(a.starts + i) > __ldg(a.starts + b);
+    return __syncthreads_or(above) ? -1 : b;
+}
+
+// (the whole block)
 template <int E>
-__device__ void one_row(const SpanArgs &a, Shared &sh, int token, int head, int d0, int d1, bool joined)
+__device__ void one_row(const SpanArgs &a, Shared &sh, const span::Seq &s, int token, int head, int d0, int d1, bool joined)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dim = a.kv.dim;
-    if (a.kv.batch == 0) return;
-    const span::Seq s = span::seq_of(a, seq_of_token(a, token), false);
     if (token < s.q0 || token >= s.q0 + s.m) return;
     const span::Seen seen = span::seen_by(a, s, token - s.q0);
     const KvView &kv = a.kv;
@@ -352,7 +379,7 @@ __device__ void join_run(const SpanArgs &a, unsigned char *raw, const Parts &lef
     for (int i = 0; i < kThreads; ++i) {
         if (!(again[i / 32] >> i % 32 & 1)) continue;
         const int t = s.q0 + (row0 + i) / a.group, hd = h * a.group + (row0 + i) % a.group;
-        one_row<E>(a, *reinterpret_cast<Shared *>(raw), t, hd, d, min(dim, d + kRun), true);
+        one_row<E>(a, *reinterpret_cast<Shared *>(raw), s, t, hd, d, min(dim, d + kRun), true);
     }
 }
 
@@ -389,6 +416,7 @@ __global__ void __launch_bounds__(kThreads) mbg_span_finish_kernel(const __grid_
     for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kThreads; r0 < rows; r0 += static_cast<int64_t>(gridDim.x) * kThreads) {
         const bool again = r0 + threadIdx.x < rows && __ldcg(a.redo + r0 + threadIdx.x) == 1;
         if (!__syncthreads_or(again)) continue;
+        const bool ascend = ascending(a);
         for (int w = 0; w < kWarps; ++w) {
             if (threadIdx.x / 32 == w) {
                 const unsigned vote = __ballot_sync(kFull, again);
@@ -400,7 +428,10 @@ __global__ void __launch_bounds__(kThreads) mbg_span_finish_kernel(const __grid_
             for (int i = 0; i < 32; ++i)
                 if (vote >> i & 1) {
                     const int64_t r = r0 + w * 32 + i;
-                    one_row<E>(a, *reinterpret_cast<Shared *>(raw), static_cast<int>(r / a.q_heads), static_cast<int>(r % a.q_heads), 0, a.kv.dim, false);
+                    const int t = static_cast<int>(r / a.q_heads);
+                    Shared &sh = *reinterpret_cast<Shared *>(raw);
+                    const int b = seq_of_token(a, sh, t, ascend);
+                    if (b >= 0) one_row<E>(a, sh, span::seq_of(a, b, false), t, static_cast<int>(r % a.q_heads), 0, a.kv.dim, false);
                 }
         }
     }
@@ -414,9 +445,12 @@ __global__ void __launch_bounds__(kThreads) mbg_span_rows_kernel(const __grid_co
     pdl_trigger();  // as the tiles: what follows may go by this launch's wait
     if (blockIdx.x == 0)
         for (int b = threadIdx.x; b < (a.prefix ? 1 : a.kv.batch); b += kThreads) span::seq_of(a, b, true);
+    const bool ascend = a.prefix || ascending(a);
     const int64_t rows = static_cast<int64_t>(a.tokens) * a.q_heads;
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-        one_row<E>(a, sh, static_cast<int>(r / a.q_heads), static_cast<int>(r % a.q_heads), 0, a.kv.dim, false);
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const int t = static_cast<int>(r / a.q_heads), b = seq_of_token(a, sh, t, ascend);
+        if (b >= 0) one_row<E>(a, sh, span::seq_of(a, b, false), t, static_cast<int>(r % a.q_heads), 0, a.kv.dim, false);
+    }
 }
 
 }  // namespace

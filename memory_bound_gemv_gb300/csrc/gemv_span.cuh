@@ -32,16 +32,25 @@ __device__ __forceinline__ Seq seq_of(const SpanArgs &a, int b, bool report)
         bad = s.n != p;
     } else {
         const int s0 = __ldg(a.starts + b), s1 = __ldg(a.starts + b + 1), n = __ldg(a.lengths + b);
-        s.q0 = s0;
-        s.m = s1 - s0;
-        if (s0 < 0 || s1 < s0 || s1 > a.tokens) {
-            s.q0 = s.m = 0;
-            bad = true;
-        }
+        bad = s0 < 0 || s1 < s0 || s1 > a.tokens;
+        s.q0 = bad ? 0 : s0;
+        s.m = bad ? 0 : s1 - s0;
         s.n = min(max(n, 0), static_cast<int>(a.kv.capacity));
         bad = bad || s.n != n || s.m > s.n;  // tokens without a slot see nothing
     }
     if (bad && report) report_error(a.err, DEVERR_BAD_INDEX);
+    return s;
+}
+
+// Starts that do not ascend: a sequence that begins below the start of one before
+// it, the largest of which is `top`, has no tokens, so that no two sequences have
+// the same.
+__device__ __forceinline__ Seq seq_behind(const SpanArgs &a, int b, int &top)
+{
+    Seq s = seq_of(a, b, false);
+    const int from = __ldg(a.starts + b);
+    if (from < top) s.q0 = s.m = 0;
+    top = max(top, from);
     return s;
 }
 

@@ -131,6 +131,7 @@ struct Cursor {
     int64_t before;   // cost of what lies before the block, per cached head
     int b, row0, h;
     int done;         // tiles of this CTA's share of it that are behind
+    int top;          // the largest start of a sequence so far
     span::Seq seq;
     Block block;
 };
@@ -247,14 +248,33 @@ struct Kernel {
     {
         const int batch = a.prefix ? 1 : a.kv.batch, tid = threadIdx.x;
         int64_t before = 0;
-        int turn = 0;
+        int turn = 0, top = 0;
+        bool ascend = true;
         *once = batch <= kThreads;
         for (int b0 = 0; b0 < batch; b0 += kThreads) {
             int64_t blocks = 0, all = 0;
             span::Seq own = {0, 0, 0, 0};
+            int from = 0;
+            bool falls = false;
             if (b0 + tid < batch) {
                 own = span::seq_of(a, b0 + tid, blockIdx.x == 0);
                 blocks = (static_cast<int64_t>(own.m) * a.group + S::kBlock - 1) / S::kBlock;
+                from = __ldg(a.starts + b0 + tid);
+                falls = __ldg(a.starts + b0 + tid + 1) < from;
+            }
+            ascend = !__syncthreads_or(falls) && ascend;
+            if (!ascend) {  // sequences that begin below an earlier one's start have no tokens
+                sh.ends[tid] = from;
+                __syncthreads();
+                int high = top;
+                for (int i = 0; i < min(kThreads, batch - b0); ++i) {
+                    if (i == tid && from < high) blocks = 0;
+                    high = max(high, sh.ends[i]);
+                }
+                top = high;
+                __syncthreads();
+            } else {
+                top = max(top, __ldg(a.starts + min(b0 + kThreads, batch)));
             }
             const int64_t end = scan(sh, turn, blocks, &all);
             sh.ends[tid] = static_cast<int>(end);
@@ -311,7 +331,7 @@ struct Kernel {
                 while (at.row0 >= at.seq.m * a.group) {
                     at.row0 = 0;
                     if (++at.b >= batch) break;
-                    at.seq = span::seq_of(a, at.b, false);
+                    at.seq = span::seq_behind(a, at.b, at.top);
                 }
                 if (at.b >= batch) break;
                 at.block = block_of<DC>(a, at.seq, at.row0, sh.lim);
@@ -1123,6 +1143,7 @@ struct Kernel {
             mine.before = before;
             mine.b = q.b;
             mine.row0 = row0;
+            mine.top = q.q0;  // (one that has tokens starts at or above all before it)
             mine.seq = q;
             mine.block = k;
         };
