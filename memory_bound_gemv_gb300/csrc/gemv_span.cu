@@ -31,6 +31,7 @@ namespace mbg {
 namespace {
 
 constexpr int kWarps = 8, kThreads = kWarps * 32, kMaxDim = 256, kOwn = kMaxDim / 32;
+constexpr int kPiece = 1024;  // slots of a warp that are summed up before they join the others
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
 struct Shared {
@@ -123,9 +124,12 @@ __device__ void one_row(const SpanArgs &a, Shared &sh, const span::Seq &s, int t
     for (int d = threadIdx.x; d < dim; d += kThreads)
         sh.q[d] = elem_load1<E>(a.q, token * a.q_st + head * a.q_sh + d);
     __syncthreads();
-    float m = -INFINITY, l = 0.f, o[kOwn];
+    // l and o: of the last kPiece slots that the warp has had at most; before: of those
+    // ahead of them.  FP32 sums of 2^17 like values are off by far more than a step
+    // of the output; of kPiece, and of so many pieces, they are not.
+    float m = -INFINITY, l = 0.f, l_before = 0.f, o[kOwn], before[kOwn];
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i) o[i] = 0.f;
+    for (int i = 0; i < kOwn; ++i) o[i] = before[i] = 0.f;
     const int sinks = min(a.sinks, min(seen.lo, seen.hi));
     const int64_t count = static_cast<int64_t>(sinks) + max(0, seen.hi - seen.lo);
     const int32_t *table = kv.table + s.b * kv.table_stride;
@@ -156,10 +160,11 @@ __device__ void one_row(const SpanArgs &a, Shared &sh, const span::Seq &s, int t
         float sum = p;
 #pragma unroll
         for (int k = 1; k < 32; k *= 2) sum += __shfl_xor_sync(kFull, sum, k);
+        l_before *= fix;
         l = l * fix + sum;
         m = mm;
 #pragma unroll
-        for (int k = 0; k < kOwn; ++k) o[k] *= fix;
+        for (int k = 0; k < kOwn; ++k) o[k] *= fix, before[k] *= fix;
         const int n = static_cast<int>(min(static_cast<int64_t>(32), count - i0));
         for (int k = 0; k < n; ++k) {
             const int pg = __shfl_sync(kFull, page, k), of = __shfl_sync(kFull, off, k);
@@ -170,7 +175,19 @@ __device__ void one_row(const SpanArgs &a, Shared &sh, const span::Seq &s, int t
             for (int j = 0; j < kOwn; ++j)
                 if (lane + 32 * j < dim) o[j] += w * elem_load1<E>(kv.v, at + lane + 32 * j);
         }
+        if ((i0 / kThreads + 1) % (kPiece / 32) == 0) {
+            l_before += l;
+            l = 0.f;
+#pragma unroll
+            for (int k = 0; k < kOwn; ++k) {
+                before[k] += o[k];
+                o[k] = 0.f;
+            }
+        }
     }
+    l += l_before;
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) o[k] += before[k];
     if (lane == 0) sh.m[warp] = m, sh.l[warp] = l;
     __syncthreads();
     float top = -INFINITY, sum = 0.f;
