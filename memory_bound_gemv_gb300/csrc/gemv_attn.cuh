@@ -198,7 +198,7 @@ struct RowSpan {
     int tile0, tiles;       // first / TOKENS - sink_tiles; the tiles' number
 };
 
-template <int TOKENS>
+template <int TOKENS, bool OWN = false>
 __device__ __forceinline__ RowSpan row_span(const AttnArgs &a, int b)
 {
     RowSpan r;
@@ -208,7 +208,7 @@ __device__ __forceinline__ RowSpan row_span(const AttnArgs &a, int b)
     r.len = len;
     r.first = (a.window > 0 && len > a.window) ? len - a.window : 0;
     r.begin = 0;
-    if (a.prefix) r.begin = min(max(__ldg(a.prefix), 0), len);
+    if (OWN) r.begin = min(max(__ldg(a.prefix), 0), len);
     if (r.first <= max(a.sinks, r.begin)) r.first = r.begin;
     r.sinks = r.first > r.begin && a.sinks > r.begin ? a.sinks : r.begin;
     r.sink_tiles = r.sinks > r.begin ? (r.sinks + TOKENS - 1) / TOKENS - r.begin / TOKENS : 0;
@@ -249,7 +249,7 @@ __device__ __forceinline__ TilePlace place_of(const KvView &kv, const int32_t *t
 template <int DC, int NT>
 constexpr int kTilesAtOnce = DC * NT == 1 ? 2 : 1;
 
-template <typename T, int DC, int NT, int NW, bool VEC, bool WHOLE>
+template <typename T, int DC, int NT, int NW, bool VEC, bool WHOLE, bool OWN>
 struct Kernel {
     static constexpr int kWarps = NW, kThreads = NW * 32;
     // tiles of 16 tokens that a warp takes at once: two of narrow heads, so that
@@ -347,7 +347,7 @@ struct Kernel {
         for (int e = 0; e < 2; ++e) {
             const int head = nt * 8 + 2 * t + e;
             if (head >= r.heads) continue;
-            if (a.own) {  // (d is even, and a row there a multiple of four)
+            if (OWN) {  // (d is even, and a row there a multiple of four)
                 if (d < a.kv.dim)
                     *reinterpret_cast<float2 *>(own_of(a, r, head) + d) = make_float2(o[e] * inv[e], o[e + 2] * inv[e]);
                 continue;
@@ -377,8 +377,8 @@ struct Kernel {
         for (int b = blockIdx.x; b < a.kv.batch; b += gridDim.x) {
             const int len = __ldg(a.lengths + b);
             if ((len < 0 || len > a.kv.capacity) && threadIdx.x == 0) report_error(a.err, DEVERR_BAD_INDEX);
-            if (a.own) {
-                if (row_span<kTokens>(a, b).tiles > 0) continue;
+            if (OWN) {
+                if (row_span<kTokens, OWN>(a, b).tiles > 0) continue;
                 for (int h = threadIdx.x; h < a.q_heads; h += kThreads) {
                     float *stat = a.own + (static_cast<int64_t>(b) * a.q_heads + h) * span_row(a.kv.dim) + span_row(a.kv.dim) - 4;
                     stat[0] = -INFINITY;
@@ -411,7 +411,7 @@ struct Kernel {
     {
         const int hks = a.kv.kv_heads * a.head_tiles;
         while (at.b < a.kv.batch) {  // (the last share ends with the last row)
-            const RowSpan span = row_span<kTokens>(a, at.b);
+            const RowSpan span = row_span<kTokens, OWN>(a, at.b);
             const int n = span.tiles, cost = n + w.lead;
             if (n == 0) {
                 ++at.b;
@@ -787,7 +787,7 @@ struct Kernel {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float ll = NT == 1 || nt == 0 ? sum[0][e] : sum[NT - 1][e];
-                    inv[e] = a.own ? Mma<T>::kUnscale : ll == 0.f ? 0.f : Mma<T>::kUnscale / ll;
+                    inv[e] = OWN ? Mma<T>::kUnscale : ll == 0.f ? 0.f : Mma<T>::kUnscale / ll;
                 }
                 store_out(a, r, i4 * 4, v, lane, inv);
             } else {
@@ -801,7 +801,7 @@ struct Kernel {
                 for (int e = 0; e < 2; ++e) {
                     const int head = nt * 8 + 2 * lane + e;
                     if (slot < 0) {
-                        if (!a.own) {
+                        if (!OWN) {
                             store_stats(a, r, head, top[nt][e], sum[nt][e]);
                         } else if (head < r.heads) {
                             float *stat = own_of(a, r, head) + span_row(a.kv.dim) - 4;
@@ -969,7 +969,7 @@ struct Kernel {
     static __device__ void run(const AttnArgs &a, Shared &sh)
     {
         pdl_trigger();
-        if (!a.own) pdl_wait();
+        if (!OWN) pdl_wait();
         uint64_t ticket = 0;
         if (threadIdx.x == kTicketThread) ticket = draw_ticket(a);  // needed late
         empty_rows(a);
@@ -981,7 +981,7 @@ struct Kernel {
         int64_t tiles = 0, rows = 0;
         int longest = 0;
         for (int b0 = 0; b0 < a.kv.batch; b0 += step) {
-            const int n = b0 + own < a.kv.batch ? row_span<kTokens>(a, b0 + own).tiles : 0;
+            const int n = b0 + own < a.kv.batch ? row_span<kTokens, OWN>(a, b0 + own).tiles : 0;
             longest = max(longest, n);
             if (few) {
                 tiles = __reduce_add_sync(kFull, n);
@@ -1024,7 +1024,7 @@ struct Kernel {
         // the sequence that holds x0
         int64_t before = 0;
         for (int b0 = 0; b0 < a.kv.batch && x0 >= before * hks; b0 += step) {
-            const int b = b0 + own, n = b < a.kv.batch ? row_span<kTokens>(a, b).tiles : 0, cost = n > 0 ? n + a.lead : 0;
+            const int b = b0 + own, n = b < a.kv.batch ? row_span<kTokens, OWN>(a, b).tiles : 0, cost = n > 0 ? n + a.lead : 0;
             int all, pre;
             if (few) {
                 pre = cost;
@@ -1060,24 +1060,24 @@ constexpr int warps_per_sm()
     return DC * NT <= 2 ? 12 : 8;
 }
 
-template <typename T, int DC, int NT, int NW, bool VEC, bool WHOLE>
+template <typename T, int DC, int NT, int NW, bool VEC, bool WHOLE, bool OWN>
 __global__ void __launch_bounds__(NW * 32, warps_per_sm<DC, NT>() / NW)
     mbg_attn_kernel(const __grid_constant__ AttnArgs a)
 {
     extern __shared__ __align__(16) unsigned char raw[];
-    using K = Kernel<T, DC, NT, NW, VEC, WHOLE>;
+    using K = Kernel<T, DC, NT, NW, VEC, WHOLE, OWN>;
     K::run(a, *reinterpret_cast<typename K::Shared *>(raw));
     // The launch before it attends to the prefix, which nothing here depends on;
     // it starts others only when all before itself are done.  Who waits for this
     // launch waits for both.
-    if (a.own) pdl_wait();
+    if (OWN) pdl_wait();
 }
 
-template <typename T, int DC, int NT, int NW, bool VEC, bool WHOLE>
+template <typename T, int DC, int NT, int NW, bool VEC, bool WHOLE, bool OWN>
 cudaError_t launch_one(const AttnArgs &a, int sm_count, cudaStream_t s)
 {
-    constexpr int smem = sizeof(typename Kernel<T, DC, NT, NW, VEC, WHOLE>::Shared);
-    auto fn = mbg_attn_kernel<T, DC, NT, NW, VEC, WHOLE>;
+    constexpr int smem = sizeof(typename Kernel<T, DC, NT, NW, VEC, WHOLE, OWN>::Shared);
+    auto fn = mbg_attn_kernel<T, DC, NT, NW, VEC, WHOLE, OWN>;
     if (smem > 48 * 1024) {
         static std::atomic<uint64_t> ready{0};  // a bit per device
         int dev = 0;
@@ -1104,35 +1104,36 @@ cudaError_t launch_one(const AttnArgs &a, int sm_count, cudaStream_t s)
 }
 
 // big: one block of all an SM's warps instead of blocks of four.
-template <typename T, int DC, int NT>
+template <typename T, int DC, int NT, bool OWN>
 cudaError_t launch_shape(const AttnArgs &a, bool big, int sm_count, cudaStream_t s)
 {
     constexpr int kBig = warps_per_sm<DC, NT>();
     if (a.kv.page_size % 16 == 0)
-        return big ? launch_one<T, DC, NT, kBig, true, true>(a, sm_count, s)
-                   : launch_one<T, DC, NT, 4, true, true>(a, sm_count, s);
-    return big ? launch_one<T, DC, NT, kBig, true, false>(a, sm_count, s)
-               : launch_one<T, DC, NT, 4, true, false>(a, sm_count, s);
+        return big ? launch_one<T, DC, NT, kBig, true, true, OWN>(a, sm_count, s)
+                   : launch_one<T, DC, NT, 4, true, true, OWN>(a, sm_count, s);
+    return big ? launch_one<T, DC, NT, kBig, true, false, OWN>(a, sm_count, s)
+               : launch_one<T, DC, NT, 4, true, false, OWN>(a, sm_count, s);
 }
 
-template <typename T>
+// OWN: the slots behind a prefix.
+template <typename T, bool OWN>
 cudaError_t launch(const AttnArgs &a, bool vec, int nt, bool big, int sm_count, cudaStream_t s)
 {
     const int dc = (a.kv.dim + 63) / 64;
-    if (vec && nt == 2) return dc == 1 ? launch_shape<T, 1, 2>(a, big, sm_count, s) : launch_shape<T, 2, 2>(a, big, sm_count, s);
+    if (vec && nt == 2) return dc == 1 ? launch_shape<T, 1, 2, OWN>(a, big, sm_count, s) : launch_shape<T, 2, 2, OWN>(a, big, sm_count, s);
     if (vec) {
         switch (dc) {
-        case 1: return launch_shape<T, 1, 1>(a, big, sm_count, s);
-        case 2: return launch_shape<T, 2, 1>(a, big, sm_count, s);
-        case 3: return launch_shape<T, 3, 1>(a, big, sm_count, s);
-        default: return launch_shape<T, 4, 1>(a, big, sm_count, s);
+        case 1: return launch_shape<T, 1, 1, OWN>(a, big, sm_count, s);
+        case 2: return launch_shape<T, 2, 1, OWN>(a, big, sm_count, s);
+        case 3: return launch_shape<T, 3, 1, OWN>(a, big, sm_count, s);
+        default: return launch_shape<T, 4, 1, OWN>(a, big, sm_count, s);
         }
     }
     switch (dc) {
-    case 1: return launch_one<T, 1, 1, 4, false, false>(a, sm_count, s);
-    case 2: return launch_one<T, 2, 1, 4, false, false>(a, sm_count, s);
-    case 3: return launch_one<T, 3, 1, 4, false, false>(a, sm_count, s);
-    default: return launch_one<T, 4, 1, 4, false, false>(a, sm_count, s);
+    case 1: return launch_one<T, 1, 1, 4, false, false, OWN>(a, sm_count, s);
+    case 2: return launch_one<T, 2, 1, 4, false, false, OWN>(a, sm_count, s);
+    case 3: return launch_one<T, 3, 1, 4, false, false, OWN>(a, sm_count, s);
+    default: return launch_one<T, 4, 1, 4, false, false, OWN>(a, sm_count, s);
     }
 }
 

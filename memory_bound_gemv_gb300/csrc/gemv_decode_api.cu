@@ -237,8 +237,9 @@ gemv_status_t attn_paged(const gemv_kv_t *kv, const gemv_attn_t *args, const int
         const cudaError_t e = launch_span(g, vec, kv->elem, dev.sm_count, s);
         if (e != cudaSuccess) return decode_cuda_fail(e, GEMV_ERR_LAUNCH);
     }
-    cudaError_t e = kv->elem == GEMV_ELEM_F16 ? launch_attn_f16(a, vec, nt, big, dev.sm_count, s)
-                                              : launch_attn_bf16(a, vec, nt, big, dev.sm_count, s);
+    const bool f16 = kv->elem == GEMV_ELEM_F16;
+    const auto attend = prefix ? f16 ? launch_attn_own_f16 : launch_attn_own_bf16 : f16 ? launch_attn_f16 : launch_attn_bf16;
+    cudaError_t e = attend(a, vec, nt, big, dev.sm_count, s);
     if (e == cudaSuccess && a.scores_out && a.kv.capacity > 0) e = launch_attn_weights(a, nt, s);
     if (e == cudaSuccess && prefix) e = launch_span_finish(g, kv->elem, dev.sm_count, s);
     return e == cudaSuccess ? GEMV_OK : decode_cuda_fail(e, GEMV_ERR_LAUNCH);
