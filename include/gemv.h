@@ -654,12 +654,15 @@ gemv_status_t gemv_get_device_error(void *stream);
  *   GEMV_DEBUG_SKIP_STAGE    the first weight stage of every bulk-pipeline block;
  *   GEMV_DEBUG_SKIP_SEGMENT  the first row segment of every softmax block that
  *                            stages rows by bulk copies;
- *   GEMV_DEBUG_SKIP_PROBE    the first chunk of every bulk-copy probe block.
+ *   GEMV_DEBUG_SKIP_PROBE    the first chunk of every bulk-copy probe block;
+ *   GEMV_DEBUG_SKIP_TILE     the third tile of K of every block of gemv_attn_prompt
+ *                            and of gemv_attn_shared's prefix.
  * gemv_debug_skip_x_copy(on) sets or clears GEMV_DEBUG_SKIP_X alone. */
 #define GEMV_DEBUG_SKIP_X 1u
 #define GEMV_DEBUG_SKIP_STAGE 2u
 #define GEMV_DEBUG_SKIP_SEGMENT 4u
 #define GEMV_DEBUG_SKIP_PROBE 8u
+#define GEMV_DEBUG_SKIP_TILE 16u
 void gemv_debug_set_wait_limit_ns(uint64_t ns);
 void gemv_debug_skip_x_copy(int on);
 void gemv_debug_skip_copies(unsigned int mask);

@@ -32,7 +32,7 @@ STATUS = {0: "GEMV_OK", 1: "GEMV_ERR_INVALID_VALUE", 2: "GEMV_ERR_MISALIGNED",
  ERR_TIMEOUT_UNDRAINED, ERR_BAD_INDEX) = range(9)
 
 # test hooks (gemv_debug_skip_copies)
-SKIP_X, SKIP_STAGE, SKIP_SEGMENT, SKIP_PROBE = 1, 2, 4, 8
+SKIP_X, SKIP_STAGE, SKIP_SEGMENT, SKIP_PROBE, SKIP_TILE = 1, 2, 4, 8, 16
 
 XMODES = {0: "bulk", 1: "vec", 2: "l1", 3: "elem", 4: "reg"}
 

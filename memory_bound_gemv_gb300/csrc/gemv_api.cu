@@ -437,6 +437,8 @@ bool decode_device(DecodeDevice *out)
     if (!d) return false;
     out->status = d->status;
     out->sm_count = d->sm_count;
+    out->wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+    out->skip_copies = g_skip_copies.load(std::memory_order_relaxed);
     return true;
 }
 
@@ -801,7 +803,7 @@ gemv_status_t gemv_debug_late_fill(void *dst, size_t bytes, uint32_t word, uint6
 
 void gemv_debug_skip_copies(unsigned int mask)
 {
-    g_skip_copies.store(mask & (SKIP_X | SKIP_STAGE | SKIP_SEGMENT | SKIP_PROBE), std::memory_order_relaxed);
+    g_skip_copies.store(mask & (SKIP_X | SKIP_STAGE | SKIP_SEGMENT | SKIP_PROBE | SKIP_TILE), std::memory_order_relaxed);
 }
 
 const char *gemv_status_string(gemv_status_t status)

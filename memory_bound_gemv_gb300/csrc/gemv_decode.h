@@ -15,6 +15,8 @@ namespace mbg {
 struct DecodeDevice {
     unsigned int *status;  // device status word
     int sm_count;
+    uint64_t wait_limit_ns;    // bound of every device-side wait
+    unsigned int skip_copies;  // test hook (SKIP_*)
 };
 bool decode_device(DecodeDevice *d);
 gemv_status_t decode_cuda_fail(cudaError_t e, gemv_status_t code);
@@ -112,6 +114,8 @@ struct SpanArgs {
     // K and V as tensors (element, token of a page, head, page) for bulk copies of
     // `box` tokens of a page at a time; box 0: copied piece by piece
     int box;
+    uint64_t wait_limit_ns;     // bound of every wait
+    int skip_tile;              // test hook (SKIP_TILE)
     CUtensorMap k_map, v_map;
 };
 // Rows of a tile of query rows, and how many tiles a block of them has.

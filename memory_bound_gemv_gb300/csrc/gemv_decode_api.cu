@@ -234,6 +234,8 @@ gemv_status_t attn_paged(const gemv_kv_t *kv, const gemv_attn_t *args, const int
         g.sinks = sinks;
         g.scale_log2 = a.scale_log2;
         g.err = a.err;
+        g.wait_limit_ns = dev.wait_limit_ns;
+        g.skip_tile = (dev.skip_copies & SKIP_TILE) != 0;
         const cudaError_t e = launch_span(g, vec, kv->elem, dev.sm_count, s);
         if (e != cudaSuccess) return decode_cuda_fail(e, GEMV_ERR_LAUNCH);
     }
@@ -403,6 +405,8 @@ gemv_status_t gemv_attn_prompt(const gemv_kv_t *kv, const gemv_prompt_t *g, void
     a.scale_log2 = g->scale * 1.4426950408889634f;
     a.err = dev.status;
     a.out_vec = out_vec(g->out);
+    a.wait_limit_ns = dev.wait_limit_ns;
+    a.skip_tile = (dev.skip_copies & SKIP_TILE) != 0;
     place_span(&a, p, g->workspace);
     const bool vec = cache_vec(kv) && aligned(g->q.data, 16) && mult8(g->q.stride, 2);
     cudaError_t e = launch_span(a, vec, kv->elem, dev.sm_count, static_cast<cudaStream_t>(stream));

@@ -38,8 +38,9 @@ enum : unsigned int { DEVERR_TIMEOUT = 1u, DEVERR_UNDRAINED = 2u, DEVERR_BAD_IND
 // faults).  SKIP_X: the bulk copy of x; SKIP_STAGE: the first weight stage
 // of every bulk-pipeline block; SKIP_SEGMENT: the first row segment of every
 // softmax block that stages rows by bulk copies; SKIP_PROBE: the first chunk
-// of every bulk-copy probe block.
-enum : unsigned int { SKIP_X = 1u, SKIP_STAGE = 2u, SKIP_SEGMENT = 4u, SKIP_PROBE = 8u };
+// of every bulk-copy probe block; SKIP_TILE: the third tile of K of every block
+// of the attention of many tokens (what comes before it is under way by then).
+enum : unsigned int { SKIP_X = 1u, SKIP_STAGE = 2u, SKIP_SEGMENT = 4u, SKIP_PROBE = 8u, SKIP_TILE = 16u };
 
 // Columns per FP16 scale in the quantised formats.
 constexpr int kGroup = 128;

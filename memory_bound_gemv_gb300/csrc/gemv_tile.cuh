@@ -77,7 +77,7 @@ namespace tile {
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kThreads = 512, kRows = 128;
 constexpr uint32_t kSegs = 4;  // segments looked up ahead
-constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr uint32_t kSkipped = 2;  // the tile of K that the test hook withholds
 
 __device__ __forceinline__ float exp2_approx(float x)
 {
@@ -210,7 +210,7 @@ struct Kernel {
 
     static __device__ __forceinline__ bool wait(Shared<DC> &sh, uint64_t &bar, uint32_t parity, const SpanArgs &a)
     {
-        if (mbar_wait_bounded(smem_addr(&bar), parity, kWaitNs)) return true;
+        if (mbar_wait_bounded(smem_addr(&bar), parity, a.wait_limit_ns)) return true;
         report_error(a.err, DEVERR_TIMEOUT);
         sh.abort = 1;
         return false;
@@ -472,6 +472,10 @@ struct Kernel {
                 if (j < t1) {
                     page_next = look_up(j + 1, off_next);
                     const int st = nk % S::kStages;
+                    if (a.skip_tile && nk == kSkipped) {
+                        ok = false;
+                        break;
+                    }
                     ok = free_place(sh.kempty[st], (nk / S::kStages & 1) ^ 1);
                     if (!ok) break;
                     load_rows<kOwn, kTok>(ks + st * S::kKvBytes, kb, page_k < 0 ? -1 : page_k * kv.ks_page + off_k * kv.ks_tok, kv.dim,
@@ -547,6 +551,10 @@ struct Kernel {
             int off = 0, page = look_up(t0, off);
             for (int j = t0; j < t1; ++j, ++count) {
                 const int st = count % S::kStages;
+                if (a.skip_tile && !is_v && count == kSkipped) {
+                    ok = false;
+                    break;
+                }
                 ok = __all_sync(kFull, wait(sh, empty[st], (count / S::kStages & 1) ^ 1, a));
                 if (!ok) break;
                 const bool edge = is_v && ends_in(slot_of(k, j), length, box);
