@@ -150,7 +150,9 @@ int out_vec(const gemv_heads_t &h)
     return aligned(h.data, 32) && h.stride[0] % 16 == 0 && h.stride[1] % 16 == 0 ? 2 : 1;
 }
 
-bool too_many_rows(int64_t tokens, int q_heads) { return tokens > INT_MAX / 64 || tokens * q_heads > INT_MAX; }
+// Rows that the kernels' 32-bit counts can hold: they are rounded up to blocks of
+// at most 256, and the row behind the last block is formed too.
+bool too_many_rows(int64_t tokens, int q_heads) { return tokens > INT_MAX / 64 || tokens * q_heads > INT_MAX - 1024; }
 
 // prefix: the slots before *prefix are attended to by a launch of their own, whose
 // results stand behind the workspace of the others.
