@@ -489,11 +489,12 @@ struct Kernel {
         auto place = [&](const Segment &s, int tile) {
             Places p;
             const bool sink = tile < s.sink_tiles;
+            const int begin = OWN ? s.begin : 0;
 #pragma unroll
             for (int i = 0; i < MT; ++i)
                 p.t[i] = place_of<WHOLE>(kv, kv.table + s.b * kv.table_stride,
-                                         ((sink ? s.begin / kTokens : s.tile0) + tile) * MT + i, tile < s.t1,
-                                         sink ? s.begin : s.first, sink ? s.sinks : s.len, a.err);
+                                         ((sink ? begin / kTokens : s.tile0) + tile) * MT + i, tile < s.t1,
+                                         sink ? begin : s.first, sink ? s.sinks : s.len, a.err);
             return p;
         };
         // does token r of a tile count, and its place relative to p's
@@ -635,8 +636,9 @@ struct Kernel {
                 if (a.scores_out) {
                     const int64_t row = static_cast<int64_t>(seg.b) * kv.kv_heads * a.head_tiles + seg.hk;
                     const bool sink = tile < seg.sink_tiles;
-                    const int at0 = ((sink ? seg.begin / kTokens : seg.tile0) + tile) * MT * 16 + g;
-                    const int first = sink ? seg.begin : seg.first, len = sink ? seg.sinks : seg.len;
+                    const int begin = OWN ? seg.begin : 0;
+                    const int at0 = ((sink ? begin / kTokens : seg.tile0) + tile) * MT * 16 + g;
+                    const int first = sink ? begin : seg.first, len = sink ? seg.sinks : seg.len;
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
