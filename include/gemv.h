@@ -469,7 +469,12 @@ uint64_t gemv_capture_id(void *stream);
  * GEMV_ERR_BAD_INDEX.  Tokens of a sequence that ends below its start, that lies
  * outside the rows or that begins below the start of one before it are left alone,
  * those without a slot get zeros.  Pages that do not exist are reported too; their
- * slots are left out.  workspace: gemv_attn_prompt_workspace(...) bytes, 256-byte
+ * slots are left out.  Weights enter the product with V with 16 bits (bfloat16) or
+ * 22 (binary16), where gemv_attn_paged keeps 24, and sums of up to 32768 slots go
+ * through the tensor core, which cuts them off at 24 bits.  Rows that meet a page that does
+ * not exist, or an infinite or NaN value that other rows of their block see, are computed
+ * one by one, some hundred times slower.  workspace: gemv_attn_prompt_workspace(...)
+ * bytes (at a head size of 128 43 MB whatever the call, and a byte per row), 256-byte
  * aligned; one workspace serves one call at a time, and needs no preparation.
  */
 typedef struct {
@@ -491,7 +496,8 @@ size_t gemv_attn_prompt_workspace(const gemv_kv_t *kv, int64_t tokens, int q_hea
  * the first row of the page table, which has to name their pages even where that
  * sequence is empty.  A sequence shorter than the prefix attends to what it
  * has of it.  scores_out has to be NULL.  A prefix below 0 or beyond the
- * capacity is reported as GEMV_ERR_BAD_INDEX and cut off there.  workspace:
+ * capacity is reported as GEMV_ERR_BAD_INDEX and cut off there.  The prefix is
+ * computed as by gemv_attn_prompt, with its bits.  workspace:
  * gemv_attn_shared_workspace(...) bytes, otherwise as for gemv_attn_paged.
  */
 gemv_status_t gemv_attn_shared(const gemv_kv_t *kv, const gemv_attn_t *args, const int32_t *prefix, int sinks,

@@ -1069,9 +1069,11 @@ __global__ void __launch_bounds__(NW * 32, warps_per_sm<DC, NT>() / NW)
     extern __shared__ __align__(16) unsigned char raw[];
     using K = Kernel<T, DC, NT, NW, VEC, WHOLE, OWN>;
     K::run(a, *reinterpret_cast<typename K::Shared *>(raw));
-    // The launch before it attends to the prefix, which nothing here depends on;
-    // it starts others only when all before itself are done.  Who waits for this
-    // launch waits for both.
+    // The launch before it attends to the prefix, which nothing here depends on.  Each
+    // of its blocks lets others start only behind its own wait, when what was launched
+    // before it is done and its writes (lengths, table, K, V, the last call's use of the
+    // workspace) are visible on the device; no block of this launch runs
+    // earlier.  Who waits for this launch waits for both.
     if (OWN) pdl_wait();
 }
 

@@ -6,8 +6,8 @@
 // map, and where the pages of those that are over go.
 //
 // Bound by latency: a few kilobytes behind a chain of reads (lengths, sums,
-// ring) and one launch: 64 requests of a token each 6.2 us, 307 of which many
-// bring prompts, 28272 tokens, 8.5 us.  Every block of one cluster makes the sums over all
+// ring) and one launch: 64 requests of a token each 6.3 us, 307 of which many
+// bring prompts, 28272 tokens, 8.7 us.  Every block of one cluster makes the sums over all
 // requests for itself, 1024 at a time, which costs less than handing them
 // on, and then writes its share of the tokens and pages, for each of which a
 // binary search among the chunk's sums finds the request.  What other blocks

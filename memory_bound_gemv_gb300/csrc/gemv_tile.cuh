@@ -4,10 +4,10 @@
 //   S = Q K^T,  P = softmax(scale S),  O = P V
 //
 // for the rows of a cached head: the group's query heads of all tokens of a
-// sequence (or of all sequences, over the prefix), 128 rows to a tile.  A row
-// of 128 slots and head size 128 takes 65536 flop for S and O each and 256 bytes
-// of K and V per slot, which all rows of a block share: from some 250 rows on the
-// products bound it, with fewer the cache's bytes.
+// sequence (or of all sequences, over the prefix), 128 rows to a tile.  At a
+// head size of 128 a row and 128 slots take 32768 flop for S and as many for O, and a
+// slot 256 bytes of K and 256 of V, which all rows of a block share: from some 280
+// rows on the products bound it, with fewer the cache's bytes.
 //
 // One pass over the slots: each row keeps a running maximum m and sum l, and O
 // is multiplied by 2^(m - m') when m grows (Milakov & Gimelshein's online
@@ -33,9 +33,9 @@
 //
 // What it measured: a tile of 128 slots for both streams takes 2.3 us (head size
 // 128), of which the tensor core works 1.9 (48 instructions of 64 cycles; 0.93 us
-// per stream are some 75 cycles each); the softmax of a stream takes 0.9 and its
-// hand-overs 0.5.  2000 new tokens behind up to 12000 cached ones, six
-// sequences: 580 us, 888 TFLOP/s counted without P's second part; with copies
+// per stream are some 75 cycles each).  A stream's own chain is as long: S 0.31, the
+// softmax 0.9, hand-overs 0.5, P V 0.62.  2000 new tokens behind up to 12000 cached ones, six
+// sequences: 593 us, 869 TFLOP/s counted without P's second part; with copies
 // piece by piece 835 us (a place of the ring is free for shorter than they
 // need to be issued, 0.65 us, and to arrive).  Tiles of 64 slots with two
 // buffers of S: 990 us -- the products' scores are read at half the width and their

@@ -200,7 +200,7 @@ class PagedKV:
     has gathered and the number of its token, for eviction.
 
     The tensors are kept; their contents may change, their storage not.  For
-    ``gemv_attn_paged`` there is a workspace per stream, and one per stream of
+    ``gemv_attn_paged`` and ``gemv_attn_shared`` there is a workspace per stream, and one per stream of
     each CUDA graph that calls are captured into.  Handles that need as much
     (a model's layers) share them, as calls on one stream follow each other.  A
     handle keeps what it has used until it is gone or ``release_workspaces`` is called.
@@ -260,7 +260,7 @@ class PagedKV:
         return got
 
     def release_workspaces(self):
-        """Lets go of the workspaces that ``gemv_attn_paged`` has made: for handles that outlive CUDA graphs.
+        """Lets go of the workspaces that ``gemv_attn_paged`` and ``gemv_attn_shared`` have made: for handles that outlive CUDA graphs.
 
         A graph that calls with this handle were captured into must not be
         replayed afterwards.  Later calls make new ones."""
@@ -387,7 +387,9 @@ def gemv_attn_shared(cache: PagedKV, q, lengths, prefix, out=None, scale: Option
 
     prefix: int32 [1], the number of those slots.  They are looked up by the first row of the page table, which
     has to name their pages even where its sequence is empty; a sequence shorter than
-    the prefix attends to what it has of it.  The other arguments are those of ``gemv_attn_paged``."""
+    the prefix attends to what it has of it.  The other arguments are those of ``gemv_attn_paged``.  The
+    prefix's weights enter the product with v as in ``gemv_attn_prompt``.  The call's workspace (some 45 MB at a head
+    size of 128) is kept as that of ``gemv_attn_paged``."""
     index = cache.index
     if not isinstance(q, _Tensor) or q.dim() != 3:
         raise ValueError("q must be a tensor [batch, q_heads, head_dim]")
@@ -428,8 +430,10 @@ def gemv_attn_prompt(cache: PagedKV, q, starts, lengths, out=None, scale: Option
     [batch]; the new tokens' keys and values are in the cache).  Each attends to
     the slots up to its own, with ``window`` to the last so many of them (0: all)
     and the first ``sinks``.  ``lse``: float32 [tokens, q_heads] that receives
-    log(sum exp(score)).  Tokens that no sequence has (padding behind the last one)
-    are left as they are in out."""
+    log(sum exp(score)).  Tokens that no sequence has (padding before the first one or
+    behind the last) are left as they are in out.  Weights enter the product with v with 16 bits
+    (bfloat16) or 22 (float16), where ``gemv_attn_paged`` keeps 24.  A call takes some
+    43 MB of workspace (head size 128) from the allocator, and gives it back."""
     index = cache.index
     if not isinstance(q, _Tensor) or q.dim() != 3:
         raise ValueError("q must be a tensor [tokens, q_heads, head_dim]")
