@@ -198,7 +198,7 @@ struct RowSpan {
     int tile0, tiles;       // first / TOKENS - sink_tiles; the tiles' number
 };
 
-template <int TOKENS, bool OWN = false>
+template <int TOKENS, bool SINKS = true, bool OWN = false>
 __device__ __forceinline__ RowSpan row_span(const AttnArgs &a, int b)
 {
     RowSpan r;
@@ -209,8 +209,8 @@ __device__ __forceinline__ RowSpan row_span(const AttnArgs &a, int b)
     r.first = (a.window > 0 && len > a.window) ? len - a.window : 0;
     r.begin = 0;
     if (OWN) r.begin = min(max(__ldg(a.prefix), 0), len);
-    if (r.first <= max(a.sinks, r.begin)) r.first = r.begin;
-    r.sinks = r.first > r.begin && a.sinks > r.begin ? a.sinks : r.begin;
+    if (SINKS && r.first <= max(a.sinks, r.begin)) r.first = r.begin;
+    r.sinks = SINKS && r.first > r.begin && a.sinks > r.begin ? a.sinks : r.begin;
     r.sink_tiles = r.sinks > r.begin ? (r.sinks + TOKENS - 1) / TOKENS - r.begin / TOKENS : 0;
     r.tile0 = r.first / TOKENS - r.sink_tiles;
     r.tiles = len > r.first ? (len + TOKENS - 1) / TOKENS - r.tile0 : 0;
@@ -249,7 +249,7 @@ __device__ __forceinline__ TilePlace place_of(const KvView &kv, const int32_t *t
 template <int DC, int NT>
 constexpr int kTilesAtOnce = DC * NT == 1 ? 2 : 1;
 
-template <typename T, int DC, int NT, int NW, bool VEC, bool WHOLE, bool OWN>
+template <typename T, int DC, int NT, int NW, bool VEC, bool WHOLE, bool SINKS, bool OWN>
 struct Kernel {
     static constexpr int kWarps = NW, kThreads = NW * 32;
     // tiles of 16 tokens that a warp takes at once: two of narrow heads, so that
@@ -378,7 +378,7 @@ struct Kernel {
             const int len = __ldg(a.lengths + b);
             if ((len < 0 || len > a.kv.capacity) && threadIdx.x == 0) report_error(a.err, DEVERR_BAD_INDEX);
             if (OWN) {
-                if (row_span<kTokens, OWN>(a, b).tiles > 0) continue;
+                if (row_span<kTokens, SINKS, OWN>(a, b).tiles > 0) continue;
                 for (int h = threadIdx.x; h < a.q_heads; h += kThreads) {
                     float *stat = a.own + (static_cast<int64_t>(b) * a.q_heads + h) * span_row(a.kv.dim) + span_row(a.kv.dim) - 4;
                     stat[0] = -INFINITY;
@@ -411,7 +411,7 @@ struct Kernel {
     {
         const int hks = a.kv.kv_heads * a.head_tiles;
         while (at.b < a.kv.batch) {  // (the last share ends with the last row)
-            const RowSpan span = row_span<kTokens, OWN>(a, at.b);
+            const RowSpan span = row_span<kTokens, SINKS, OWN>(a, at.b);
             const int n = span.tiles, cost = n + w.lead;
             if (n == 0) {
                 ++at.b;
@@ -488,7 +488,7 @@ struct Kernel {
         };
         auto place = [&](const Segment &s, int tile) {
             Places p;
-            const bool sink = tile < s.sink_tiles;
+            const bool sink = SINKS && tile < s.sink_tiles;
             const int begin = OWN ? s.begin : 0;
 #pragma unroll
             for (int i = 0; i < MT; ++i)
@@ -635,7 +635,7 @@ struct Kernel {
                 }
                 if (a.scores_out) {
                     const int64_t row = static_cast<int64_t>(seg.b) * kv.kv_heads * a.head_tiles + seg.hk;
-                    const bool sink = tile < seg.sink_tiles;
+                    const bool sink = SINKS && tile < seg.sink_tiles;
                     const int begin = OWN ? seg.begin : 0;
                     const int at0 = ((sink ? begin / kTokens : seg.tile0) + tile) * MT * 16 + g;
                     const int first = sink ? begin : seg.first, len = sink ? seg.sinks : seg.len;
@@ -983,7 +983,7 @@ struct Kernel {
         int64_t tiles = 0, rows = 0;
         int longest = 0;
         for (int b0 = 0; b0 < a.kv.batch; b0 += step) {
-            const int n = b0 + own < a.kv.batch ? row_span<kTokens, OWN>(a, b0 + own).tiles : 0;
+            const int n = b0 + own < a.kv.batch ? row_span<kTokens, SINKS, OWN>(a, b0 + own).tiles : 0;
             longest = max(longest, n);
             if (few) {
                 tiles = __reduce_add_sync(kFull, n);
@@ -1026,7 +1026,7 @@ struct Kernel {
         // the sequence that holds x0
         int64_t before = 0;
         for (int b0 = 0; b0 < a.kv.batch && x0 >= before * hks; b0 += step) {
-            const int b = b0 + own, n = b < a.kv.batch ? row_span<kTokens, OWN>(a, b).tiles : 0, cost = n > 0 ? n + a.lead : 0;
+            const int b = b0 + own, n = b < a.kv.batch ? row_span<kTokens, SINKS, OWN>(a, b).tiles : 0, cost = n > 0 ? n + a.lead : 0;
             int all, pre;
             if (few) {
                 pre = cost;
@@ -1062,12 +1062,12 @@ constexpr int warps_per_sm()
     return DC * NT <= 2 ? 12 : 8;
 }
 
-template <typename T, int DC, int NT, int NW, bool VEC, bool WHOLE, bool OWN>
+template <typename T, int DC, int NT, int NW, bool VEC, bool WHOLE, bool SINKS, bool OWN>
 __global__ void __launch_bounds__(NW * 32, warps_per_sm<DC, NT>() / NW)
     mbg_attn_kernel(const __grid_constant__ AttnArgs a)
 {
     extern __shared__ __align__(16) unsigned char raw[];
-    using K = Kernel<T, DC, NT, NW, VEC, WHOLE, OWN>;
+    using K = Kernel<T, DC, NT, NW, VEC, WHOLE, SINKS, OWN>;
     K::run(a, *reinterpret_cast<typename K::Shared *>(raw));
     // The launch before it attends to the prefix, which nothing here depends on.  Each
     // of its blocks lets others start only behind its own wait, when what was launched
@@ -1077,11 +1077,11 @@ __global__ void __launch_bounds__(NW * 32, warps_per_sm<DC, NT>() / NW)
     if (OWN) pdl_wait();
 }
 
-template <typename T, int DC, int NT, int NW, bool VEC, bool WHOLE, bool OWN>
+template <typename T, int DC, int NT, int NW, bool VEC, bool WHOLE, bool SINKS, bool OWN>
 cudaError_t launch_one(const AttnArgs &a, int sm_count, cudaStream_t s)
 {
-    constexpr int smem = sizeof(typename Kernel<T, DC, NT, NW, VEC, WHOLE, OWN>::Shared);
-    auto fn = mbg_attn_kernel<T, DC, NT, NW, VEC, WHOLE, OWN>;
+    constexpr int smem = sizeof(typename Kernel<T, DC, NT, NW, VEC, WHOLE, SINKS, OWN>::Shared);
+    auto fn = mbg_attn_kernel<T, DC, NT, NW, VEC, WHOLE, SINKS, OWN>;
     if (smem > 48 * 1024) {
         static std::atomic<uint64_t> ready{0};  // a bit per device
         int dev = 0;
@@ -1108,36 +1108,36 @@ cudaError_t launch_one(const AttnArgs &a, int sm_count, cudaStream_t s)
 }
 
 // big: one block of all an SM's warps instead of blocks of four.
-template <typename T, int DC, int NT, bool OWN>
+template <typename T, int DC, int NT, bool SINKS, bool OWN>
 cudaError_t launch_shape(const AttnArgs &a, bool big, int sm_count, cudaStream_t s)
 {
     constexpr int kBig = warps_per_sm<DC, NT>();
     if (a.kv.page_size % 16 == 0)
-        return big ? launch_one<T, DC, NT, kBig, true, true, OWN>(a, sm_count, s)
-                   : launch_one<T, DC, NT, 4, true, true, OWN>(a, sm_count, s);
-    return big ? launch_one<T, DC, NT, kBig, true, false, OWN>(a, sm_count, s)
-               : launch_one<T, DC, NT, 4, true, false, OWN>(a, sm_count, s);
+        return big ? launch_one<T, DC, NT, kBig, true, true, SINKS, OWN>(a, sm_count, s)
+                   : launch_one<T, DC, NT, 4, true, true, SINKS, OWN>(a, sm_count, s);
+    return big ? launch_one<T, DC, NT, kBig, true, false, SINKS, OWN>(a, sm_count, s)
+               : launch_one<T, DC, NT, 4, true, false, SINKS, OWN>(a, sm_count, s);
 }
 
-// OWN: the slots behind a prefix.
-template <typename T, bool OWN>
+// SINKS: with first slots that stay visible; OWN: the slots behind a prefix.
+template <typename T, bool SINKS, bool OWN>
 cudaError_t launch(const AttnArgs &a, bool vec, int nt, bool big, int sm_count, cudaStream_t s)
 {
     const int dc = (a.kv.dim + 63) / 64;
-    if (vec && nt == 2) return dc == 1 ? launch_shape<T, 1, 2, OWN>(a, big, sm_count, s) : launch_shape<T, 2, 2, OWN>(a, big, sm_count, s);
+    if (vec && nt == 2) return dc == 1 ? launch_shape<T, 1, 2, SINKS, OWN>(a, big, sm_count, s) : launch_shape<T, 2, 2, SINKS, OWN>(a, big, sm_count, s);
     if (vec) {
         switch (dc) {
-        case 1: return launch_shape<T, 1, 1, OWN>(a, big, sm_count, s);
-        case 2: return launch_shape<T, 2, 1, OWN>(a, big, sm_count, s);
-        case 3: return launch_shape<T, 3, 1, OWN>(a, big, sm_count, s);
-        default: return launch_shape<T, 4, 1, OWN>(a, big, sm_count, s);
+        case 1: return launch_shape<T, 1, 1, SINKS, OWN>(a, big, sm_count, s);
+        case 2: return launch_shape<T, 2, 1, SINKS, OWN>(a, big, sm_count, s);
+        case 3: return launch_shape<T, 3, 1, SINKS, OWN>(a, big, sm_count, s);
+        default: return launch_shape<T, 4, 1, SINKS, OWN>(a, big, sm_count, s);
         }
     }
     switch (dc) {
-    case 1: return launch_one<T, 1, 1, 4, false, false, OWN>(a, sm_count, s);
-    case 2: return launch_one<T, 2, 1, 4, false, false, OWN>(a, sm_count, s);
-    case 3: return launch_one<T, 3, 1, 4, false, false, OWN>(a, sm_count, s);
-    default: return launch_one<T, 4, 1, 4, false, false, OWN>(a, sm_count, s);
+    case 1: return launch_one<T, 1, 1, 4, false, false, SINKS, OWN>(a, sm_count, s);
+    case 2: return launch_one<T, 2, 1, 4, false, false, SINKS, OWN>(a, sm_count, s);
+    case 3: return launch_one<T, 3, 1, 4, false, false, SINKS, OWN>(a, sm_count, s);
+    default: return launch_one<T, 4, 1, 4, false, false, SINKS, OWN>(a, sm_count, s);
     }
 }
 

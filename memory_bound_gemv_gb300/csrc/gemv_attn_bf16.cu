@@ -5,7 +5,7 @@ namespace mbg {
 
 cudaError_t launch_attn_bf16(const AttnArgs &a, bool vec, int nt, bool big, int sm_count, cudaStream_t s)
 {
-    return attn::launch<__nv_bfloat16, false>(a, vec, nt, big, sm_count, s);
+    return attn::launch<__nv_bfloat16, false, false>(a, vec, nt, big, sm_count, s);
 }
 
 }  // namespace mbg

@@ -6,7 +6,7 @@ namespace mbg {
 
 cudaError_t launch_attn_f16(const AttnArgs &a, bool vec, int nt, bool big, int sm_count, cudaStream_t s)
 {
-    return attn::launch<__half, false>(a, vec, nt, big, sm_count, s);
+    return attn::launch<__half, false, false>(a, vec, nt, big, sm_count, s);
 }
 
 // scores_out[b, h, t] = scores_in[b, h, t] + sum over the group's query heads

@@ -6,7 +6,7 @@ namespace mbg {
 
 cudaError_t launch_attn_own_f16(const AttnArgs &a, bool vec, int nt, bool big, int sm_count, cudaStream_t s)
 {
-    return attn::launch<__half, true>(a, vec, nt, big, sm_count, s);
+    return attn::launch<__half, true, true>(a, vec, nt, big, sm_count, s);
 }
 
 }  // namespace mbg

@@ -71,9 +71,12 @@ __host__ __device__ constexpr int span_row(int dim) { return (dim + 3) / 4 * 4 +
 // per SM instead of several small ones.
 cudaError_t launch_attn_f16(const AttnArgs &a, bool vec, int nt, bool big, int sm_count, cudaStream_t s);
 cudaError_t launch_attn_bf16(const AttnArgs &a, bool vec, int nt, bool big, int sm_count, cudaStream_t s);
-// The same for the slots behind a.prefix, into a.own.  Kernels of their own: with the
-// two forms in one, chosen at run time, the plain one spilled registers (bf16, 128:
-// 88 bytes) and 24 sequences of heads of 256 took 121.5 us, not 113.3.
+// The same with a.sinks, and for the slots behind a.prefix, into a.own.  Kernels of
+// their own: with all forms in one, chosen at run time, the plain one spilled registers
+// (bf16, 128: 88 bytes) and 24 sequences of heads of 256 took 121.5 us, not 114.7; with
+// sinks in it 119.7.
+cudaError_t launch_attn_sinks_f16(const AttnArgs &a, bool vec, int nt, bool big, int sm_count, cudaStream_t s);
+cudaError_t launch_attn_sinks_bf16(const AttnArgs &a, bool vec, int nt, bool big, int sm_count, cudaStream_t s);
 cudaError_t launch_attn_own_f16(const AttnArgs &a, bool vec, int nt, bool big, int sm_count, cudaStream_t s);
 cudaError_t launch_attn_own_bf16(const AttnArgs &a, bool vec, int nt, bool big, int sm_count, cudaStream_t s);
 cudaError_t launch_attn_weights(const AttnArgs &a, int nt, cudaStream_t s);

@@ -242,7 +242,10 @@ gemv_status_t attn_paged(const gemv_kv_t *kv, const gemv_attn_t *args, const int
         if (e != cudaSuccess) return decode_cuda_fail(e, GEMV_ERR_LAUNCH);
     }
     const bool f16 = kv->elem == GEMV_ELEM_F16;
-    const auto attend = prefix ? f16 ? launch_attn_own_f16 : launch_attn_own_bf16 : f16 ? launch_attn_f16 : launch_attn_bf16;
+    const auto attend = prefix                         ? f16 ? launch_attn_own_f16 : launch_attn_own_bf16
+                        : a.sinks > 0 && a.window > 0 ? f16 ? launch_attn_sinks_f16 : launch_attn_sinks_bf16
+                        : f16                          ? launch_attn_f16
+                                                       : launch_attn_bf16;
     cudaError_t e = attend(a, vec, nt, big, dev.sm_count, s);
     if (e == cudaSuccess && a.scores_out && a.kv.capacity > 0) e = launch_attn_weights(a, nt, s);
     if (e == cudaSuccess && prefix) e = launch_span_finish(g, kv->elem, dev.sm_count, s);
